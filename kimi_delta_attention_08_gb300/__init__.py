@@ -16,6 +16,21 @@ __all__ = ["KdaError", "kda_fwd", "kda_bwd", "kda_fwd_transition", "kda_compose_
            "make_bwd_workspace", "make_chunk_states", "kda_get_chunk_states_size",
            "status_string", "CP_MODES", "PATHS"]
 
+# Operators around the recurrence (layer.py), bound on first use: importing them needs torch.
+_LAYER = ("kda_conv_fwd", "kda_conv_bwd", "make_conv_bwd_workspace", "kda_scan_fwd", "kda_scan_bwd",
+          "make_scan_states", "make_scan_workspace", "kda_prenorm_fwd", "kda_prenorm_bwd",
+          "kda_postnorm_fwd", "kda_postnorm_bwd", "make_norm_bwd_workspace")
+__all__ += list(_LAYER)
+
+
+def __getattr__(name):
+    if name not in _LAYER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import layer
+    globals()[name] = getattr(layer, name)
+    return globals()[name]
+
+
 KDA_OK = 0
 CP_MODES = {"auto": 0, "off": 1, "force": 2, None: 0, True: 2, False: 1}
 # kernel choice: chunked (WY) form, or the token-by-token recurrence for short inputs

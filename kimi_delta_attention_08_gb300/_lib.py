@@ -8,11 +8,16 @@ import os
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libkda.so")
 
-# Public symbols of include/kda.h.
+# Public symbols of include/kda.h and include/kda_layer.h.
 EXPORTS = ("kda_status_string", "kda_get_workspace_size", "kda_fwd", "kda_get_device_status",
            "kda_fwd_static_scratch", "kda_static_scratch_device_status",
            "kda_fwd_transition", "kda_compose_states", "kda_bwd_get_workspace_size", "kda_bwd",
-           "kda_get_chunk_states_size")
+           "kda_get_chunk_states_size",
+           "kda_conv_fwd", "kda_conv_bwd", "kda_conv_bwd_get_workspace_size",
+           "kda_scan_fwd", "kda_scan_bwd", "kda_scan_get_states_size",
+           "kda_scan_get_workspace_size", "kda_scan_bwd_get_workspace_size",
+           "kda_prenorm_fwd", "kda_prenorm_bwd", "kda_postnorm_fwd", "kda_postnorm_bwd",
+           "kda_norm_bwd_get_workspace_size")
 
 _lib = None
 
@@ -23,6 +28,16 @@ class kda_options(ctypes.Structure):
                 ("g_dtype", ctypes.c_int32), ("debug_stall", ctypes.c_int32),
                 ("reserved", ctypes.c_int32 * 2), ("chunk_states", ctypes.c_void_p),
                 ("chunk_states_bytes", ctypes.c_size_t)]
+
+
+class kda_scan_problem(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "dt", "z", "B", "C")] +
+                [(n + "_stride", ctypes.c_int64) for n in ("x", "dt", "z", "B", "C")] +
+                [(n, ctypes.c_void_p) for n in ("A_log", "D", "dt_bias", "initial_state",
+                                                "cu_seqlens")] +
+                [("batch", ctypes.c_int64), ("T", ctypes.c_int64)] +
+                [(n, ctypes.c_int32) for n in ("N", "dim", "state", "groups", "dtype",
+                                               "state_dtype")])
 
 
 def load():
@@ -62,5 +77,26 @@ def load():
     lib.kda_compose_states.argtypes = [P, P, I32, I64, P, P, P]
     lib.kda_static_scratch_device_status.restype = ctypes.c_int
     lib.kda_static_scratch_device_status.argtypes = [ctypes.POINTER(ctypes.c_int), P]
+    S, Z = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+    Q = ctypes.POINTER(kda_scan_problem)
+    for name, args in (
+            ("kda_conv_fwd", [P, I64, P, P, P, P, I32, P, P, P, I64, I64, I32, I32, I32, I32, I32, P,
+                              S, P]),
+            ("kda_conv_bwd_get_workspace_size", [I64, I32, I32, Z]),
+            ("kda_conv_bwd", [P, I64, P, P, P, P, I32, I32, P, P, P, P, P, P, P, I64, I64, I32, I32,
+                              I32, I32, I32, P, S, P]),
+            ("kda_scan_get_states_size", [I64, I32, I32, I32, Z]),
+            ("kda_scan_get_workspace_size", [Q, Z]),
+            ("kda_scan_bwd_get_workspace_size", [Q, I32, Z]),
+            ("kda_scan_fwd", [Q, P, P, P, S, P, S, P]),
+            ("kda_scan_bwd", [Q, P, P, P, S] + [P] * 10 + [S, P]),
+            ("kda_prenorm_fwd", [P, P, P, P, F, F, P, P, I64, I32, I32, I32, P]),
+            ("kda_norm_bwd_get_workspace_size", [I64, I32, Z]),
+            ("kda_prenorm_bwd", [P, P, P, P, P, P, F, F, P, P, P, P, I64, I32, I32, I32, P, S, P]),
+            ("kda_postnorm_fwd", [P, P, P, I64, I32, P, P, F, F, I32, P, I64, I32, I32, P]),
+            ("kda_postnorm_bwd", [P, P, P, P, I64, I32, P, F, F, I32, P, P, P, P, I64, I32, I32, P,
+                                  S, P])):
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = args
     _lib = lib
     return lib

@@ -17,8 +17,9 @@ LIB = os.path.join(BUILD, "libkda.so")
 ROOT = os.path.dirname(HERE)
 
 SOURCES = ["kda_api.cu", "kda_chunk_fwd.cu", "kda_plan.cu", "kda_noalloc.cu", "kda_recurrent.cu",
-           "kda_bwd.cu", "kda_bwd_chunk.cu"]
-HEADERS = ["kda_internal.h", "kda_ptx.cuh"]
+           "kda_bwd.cu", "kda_bwd_chunk.cu", "kda_norm.cu", "kda_conv.cu", "kda_scan_fwd.cu",
+           "kda_scan_bwd.cu"]
+HEADERS = ["kda_internal.h", "kda_ptx.cuh", "kda_inverse.cuh", "kda_rows.cuh", "kda_scan.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler",
               "-fvisibility=hidden", "-I", os.path.join(ROOT, "include")]
@@ -38,7 +39,8 @@ def _stale(target: str, deps) -> bool:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", "kda.h")]
+    hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", h)
+                                                          for h in ("kda.h", "kda_layer.h")]
     objs, jobs = [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)

@@ -10,6 +10,10 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+}  // namespace
+
+namespace kda {
+
 // Compute capability check, cached per device ordinal.
 kda_status check_device() {
   int dev = -1;
@@ -41,10 +45,6 @@ kda_status sm_count(int* out) {
   *out = n;
   return KDA_OK;
 }
-
-}  // namespace
-
-namespace kda {
 
 kda_status validate_fwd(const void* q, const void* k, const void* v, const void* g,
                         const void* beta, float scale, const void* out, const float* A_log,
@@ -154,12 +154,12 @@ kda_status kda_fwd(const void* q, const void* k, const void* v, const void* g, c
     if (st != KDA_OK) return st;
     if (opts->chunk_states_bytes < cs) return KDA_ERR_WORKSPACE_TOO_SMALL;
   }
-  st = check_device();
+  st = kda::check_device();
   if (st != KDA_OK) return st;
 
   if (cu_seqlens && (int64_t)N > total + 1) return KDA_ERR_INVALID_SHAPE;  // workspace bound
   int num_sms = 0;
-  if (sm_count(&num_sms) != KDA_OK) return KDA_ERR_CUDA;
+  if (kda::sm_count(&num_sms) != KDA_OK) return KDA_ERR_CUDA;
   const int cp_mode = opts ? opts->cp_mode : KDA_CP_AUTO;
   const int seg_chunks = opts ? opts->seg_chunks : 0;
   const bool gate_f32 = opts && opts->g_dtype == KDA_GATE_FP32;
@@ -322,7 +322,7 @@ kda_status kda_fwd_transition(const void* q, const void* k, const void* v, const
   st = kda_get_workspace_size(total, HV, &need);
   if (st != KDA_OK) return st;
   if (workspace_bytes < need) return KDA_ERR_WORKSPACE_TOO_SMALL;
-  st = check_device();
+  st = kda::check_device();
   if (st != KDA_OK) return st;
   const bool gate_f32 = opts && opts->g_dtype == KDA_GATE_FP32;
   kda::WsHeader* hdr = reinterpret_cast<kda::WsHeader*>(workspace);
@@ -361,7 +361,7 @@ kda_status kda_compose_states(const float* M, const float* B, int32_t R, int64_t
   if (!aligned(S_out, 16) || (M && !aligned(M, 16)) || (B && !aligned(B, 16)) ||
       (S_in && !aligned(S_in, 16)))
     return KDA_ERR_MISALIGNED;
-  const kda_status st = check_device();
+  const kda_status st = kda::check_device();
   if (st != KDA_OK) return st;
   kda::ComposeParams cp;
   cp.M = M;
@@ -501,10 +501,10 @@ kda_status kda_bwd(const void* q, const void* k, const void* v, const void* g, c
     if (cst != KDA_OK) return cst;
     if (opts->chunk_states_bytes < cs) return KDA_ERR_WORKSPACE_TOO_SMALL;
   }
-  kda_status st = check_device();
+  kda_status st = kda::check_device();
   if (st != KDA_OK) return st;
   int num_sms = 0;
-  if (sm_count(&num_sms) != KDA_OK) return KDA_ERR_CUDA;
+  if (kda::sm_count(&num_sms) != KDA_OK) return KDA_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   kda::WsHeader* hdr = reinterpret_cast<kda::WsHeader*>(ws);
   if (cudaMemsetAsync(hdr, 0, sizeof(kda::WsHeader), stream) != cudaSuccess) return KDA_ERR_CUDA;

@@ -237,6 +237,11 @@ inline cudaError_t ensure_smem_attr(const void* func, int bytes, bool (&done)[64
   return e;
 }
 
+// Whether the current device is an sm_103 GPU, and its multiprocessor count (both
+// cached per device ordinal).
+kda_status check_device();
+kda_status sm_count(int* out);
+
 // Host-side argument checks of kda_fwd, in its order (everything but the workspace
 // size and the device): returns the status kda_fwd would return for them, and on
 // success the value-head count in *HV_out and, for batched input, N = B in *N.

@@ -1,0 +1,625 @@
+// kda_norm.cu -- the norms before and after a block, forward and backward.
+//
+// Per row of D values: unit(h) = h rstd(h), rstd = (mean(h^2) + eps)^(-1/2).
+//   before a block: h = residual + s x,  out = unit(h) w            (h is kept as well)
+//   after a block:  out = residual + s (unit(x) w fn(gate))
+// and backwards, with du = the gradient of unit(h) per value,
+//   dh = rstd (du - unit(h) mean(du unit(h))),
+// which needs the two row sums S1 = sum h^2 and S2 = sum du h in one reduction, since
+// mean(du unit(h)) = rstd S2 / D.
+//
+// All of it is bound by HBM: each row is read once and written once, so a row stays in
+// the registers of the threads that read it, between the reduction and the output.  Rows
+// of up to 64 vectors belong to 16 or 32 lanes (no barrier, several rows per
+// warp's loads in flight); longer ones to a block with one barrier per row.  Weight
+// gradients are summed over a block's rows in registers, then over the blocks by a
+// second launch, in a fixed order.
+#include "kda_internal.h"
+#include "kda_rows.cuh"
+#include "../../include/kda_layer.h"
+
+#include <cmath>
+
+namespace kda {
+namespace {
+
+using namespace rows;
+
+struct NormParams {
+  const void *a, *b, *c, *d;  // row inputs (see the kernels)
+  void *o0, *o1;              // row outputs
+  const float *weight, *scale;
+  float scale_value, eps;
+  int64_t n_rows, gate_stride;
+  int heads, dim, fn;
+  int f32, stream_f32;        // types of the rows and of the residual stream
+  float* part;                // [blocks][1 or 2][dim] partial dweight (, dscale)
+  int want_scale;
+};
+
+// Position of a thread's vector i within its row: V = 8 consecutive values (16 bytes of
+// bf16, 32 of fp32) or single ones (V = 1, rows that are not 16-byte aligned).
+template <int V>
+__device__ __forceinline__ void load_vec(float (&f)[V], const void* p, int64_t at, int f32) {
+  if constexpr (V == 1) {
+    f[0] = f32 ? static_cast<const float*>(p)[at] : to_f(static_cast<const bf16*>(p)[at]);
+  } else if (f32) {
+    Raw<float, V> r;
+    load_words<true>(r.w, static_cast<const float*>(p) + at);
+    unpack(r, f);
+  } else {
+    Raw<bf16, V> r;
+    load_words<true>(r.w, static_cast<const bf16*>(p) + at);
+    unpack(r, f);
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_vec(void* p, int64_t at, const float (&f)[V], int f32) {
+  if constexpr (V == 1) {
+    if (f32) static_cast<float*>(p)[at] = f[0];
+    else static_cast<bf16*>(p)[at] = from_f<bf16>(f[0]);
+  } else if (f32) {
+    Raw<float, V> r;
+    pack(r, f);
+    store_words(static_cast<float*>(p) + at, r.w);
+  } else {
+    Raw<bf16, V> r;
+    pack(r, f);
+    store_words(static_cast<bf16*>(p) + at, r.w);
+  }
+}
+
+// Sum over the G threads of a row (G = 16, 32: lanes; G = 0: the whole block, one
+// barrier, `red` alternates between two halves so that no second one is needed).
+template <int G>
+__device__ __forceinline__ float2 row_sum(float2 v, float2* red, int turn) {
+  constexpr int W = G == 16 ? 16 : 32;
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  }
+  if constexpr (G != 0) return v;
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  float2* r = red + (turn & 1) * 32;
+  if (lane == 0) r[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < warps ? r[lane] : make_float2(0.f, 0.f);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  }
+  return v;
+}
+
+__device__ __forceinline__ float gate_fn(float p, int fn, float& d) {
+  const float s = sigmoid(p);
+  if (fn == KDA_FN_SILU) {
+    d = s * (1.f + p * (1.f - s));
+    return p * s;
+  }
+  d = s * (1.f - s);
+  return s;
+}
+
+// The rows of a block: group `grp` of the block's rows_per_block takes row
+// blockIdx * rpb + grp, then every grid * rpb further.  Lanes of a warp run the same
+// number of turns (the reductions are warp-wide); `live` masks the rows past the end.
+#define KDA_NORM_ROWS(G)                                                                 \
+  const int gsz = (G) ? (G) : (int)blockDim.x;                                           \
+  const int rpb = (G) ? (int)blockDim.x / (G) : 1;                                       \
+  const int g = (G) ? (int)threadIdx.x % (G) : (int)threadIdx.x;                         \
+  const int grp = (G) ? (int)threadIdx.x / (G) : 0;                                      \
+  __shared__ float2 red[64];                                                             \
+  int turn = 0;                                                                          \
+  const int D = p.dim, nv = (D + V - 1) / V;                                             \
+  const float inv_d = 1.0f / (float)D;                                                   \
+  const int64_t stride = (int64_t)gridDim.x * rpb;                                       \
+  float w[E][V] = {}, sc[E][V];                                                          \
+  _Pragma("unroll") for (int i = 0; i < E; ++i) {                                        \
+    const int vi = i * gsz + g;                                                          \
+    _Pragma("unroll") for (int k = 0; k < V; ++k) sc[i][k] = p.scale_value;              \
+    if (vi < nv) load_vec<V>(w[i], p.weight, (int64_t)vi * V, 1);                        \
+    if (vi < nv && p.scale) load_vec<V>(sc[i], p.scale, (int64_t)vi * V, 1);             \
+  }
+
+template <int G, int E, int V>
+__global__ void __launch_bounds__(G ? 256 : E * V >= 8 && V == 1 ? 1024 : 512) prenorm_fwd_kernel(const NormParams p) {
+  KDA_NORM_ROWS(G)
+  for (int64_t base = (int64_t)blockIdx.x * rpb; base < p.n_rows; base += stride, ++turn) {
+    const int64_t row = base + grp;
+    const bool live = row < p.n_rows;
+    float h[E][V];
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int vi = i * gsz + g;
+      const bool ok = live && vi < nv;
+      const int64_t at = row * D + (int64_t)vi * V;
+      float x[V] = {}, r[V] = {};
+      if (ok) load_vec<V>(x, p.a, at, p.f32);
+      if (ok && p.b) load_vec<V>(r, p.b, at, p.stream_f32);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        h[i][k] = fmaf(sc[i][k], x[k], r[k]);
+        s.x = fmaf(h[i][k], h[i][k], s.x);
+      }
+    }
+    s = row_sum<G>(s, red, turn);
+    const float rstd = rsqrtf(s.x * inv_d + p.eps);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int vi = i * gsz + g;
+      if (!live || vi >= nv) continue;
+      const int64_t at = row * D + (int64_t)vi * V;
+      if (p.o1) store_vec<V>(p.o1, at, h[i], p.stream_f32);
+      float y[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) y[k] = h[i][k] * rstd * w[i][k];
+      store_vec<V>(p.o0, at, y, p.f32);
+    }
+  }
+}
+
+template <int G, int E, int V>
+__global__ void __launch_bounds__(G ? 256 : E * V >= 8 && V == 1 ? 1024 : 512) postnorm_fwd_kernel(const NormParams p) {
+  KDA_NORM_ROWS(G)
+  for (int64_t base = (int64_t)blockIdx.x * rpb; base < p.n_rows; base += stride, ++turn) {
+    const int64_t row = base + grp;
+    const bool live = row < p.n_rows;
+    const int64_t grow = (row / p.heads) * p.gate_stride + (row % p.heads) * (int64_t)D;
+    float x[E][V], gt[E][V];
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int vi = i * gsz + g;
+      const bool ok = live && vi < nv;
+#pragma unroll
+      for (int k = 0; k < V; ++k) x[i][k] = gt[i][k] = 0.f;
+      if (ok) load_vec<V>(x[i], p.a, row * D + (int64_t)vi * V, p.f32);
+      if (ok && p.b) load_vec<V>(gt[i], p.b, grow + (int64_t)vi * V, p.f32);
+#pragma unroll
+      for (int k = 0; k < V; ++k) s.x = fmaf(x[i][k], x[i][k], s.x);
+    }
+    s = row_sum<G>(s, red, turn);
+    const float rstd = rsqrtf(s.x * inv_d + p.eps);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int vi = i * gsz + g;
+      if (!live || vi >= nv) continue;
+      const int64_t at = row * D + (int64_t)vi * V;
+      float y[V], r[V] = {};
+      if (p.c) load_vec<V>(r, p.c, at, p.f32);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        float n = x[i][k] * rstd * w[i][k], d;
+        if (p.b) n *= gate_fn(gt[i][k], p.fn, d);
+        y[k] = fmaf(sc[i][k], n, r[k]);
+      }
+      store_vec<V>(p.o0, at, y, p.f32);
+    }
+  }
+}
+
+// Adds the block's row groups' dweight and dscale in the groups' order and writes the
+// block's partial row.
+template <int G, int E, int V>
+__device__ __forceinline__ void write_partials(const NormParams& p, const float (&dw)[E][V],
+                                               const float (&ds)[E][V], int g, int grp, int gsz,
+                                               int rpb, int nv) {
+  extern __shared__ float acc[];  // [2][dim] when several rows share a block
+  const int pitch = (p.want_scale ? 2 : 1) * p.dim;
+  float* out = p.part + (int64_t)blockIdx.x * pitch;
+  if constexpr (G == 0) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int vi = i * gsz + g;
+      if (vi >= nv) continue;
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        out[vi * V + k] = dw[i][k];
+        if (p.want_scale) out[p.dim + vi * V + k] = ds[i][k];
+      }
+    }
+  } else {
+    for (int r = 0; r < rpb; ++r) {
+      if (grp == r) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const int vi = i * gsz + g;
+          if (vi >= nv) continue;
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            const int e = vi * V + k;
+            acc[e] = r ? acc[e] + dw[i][k] : dw[i][k];
+            if (p.want_scale) acc[p.dim + e] = r ? acc[p.dim + e] + ds[i][k] : ds[i][k];
+          }
+        }
+      }
+      __syncthreads();
+    }
+    for (int e = threadIdx.x; e < pitch; e += blockDim.x) out[e] = acc[e];
+  }
+}
+
+// a = dout, b = dresidual_out or null, c = h, d = x or null (dscale)
+template <int G, int E, int V>
+__global__ void __launch_bounds__(G ? 256 : E * V >= 8 && V == 1 ? 1024 : 512) prenorm_bwd_kernel(const NormParams p) {
+  KDA_NORM_ROWS(G)
+  float dw[E][V] = {}, ds[E][V] = {};
+  for (int64_t base = (int64_t)blockIdx.x * rpb; base < p.n_rows; base += stride, ++turn) {
+    const int64_t row = base + grp;
+    const bool live = row < p.n_rows;
+    float h[E][V], dy[E][V];
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int vi = i * gsz + g;
+      const bool ok = live && vi < nv;
+      const int64_t at = row * D + (int64_t)vi * V;
+#pragma unroll
+      for (int k = 0; k < V; ++k) h[i][k] = dy[i][k] = 0.f;
+      if (ok) load_vec<V>(h[i], p.c, at, p.stream_f32);
+      if (ok) load_vec<V>(dy[i], p.a, at, p.f32);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        s.x = fmaf(h[i][k], h[i][k], s.x);
+        s.y = fmaf(dy[i][k] * w[i][k], h[i][k], s.y);
+      }
+    }
+    s = row_sum<G>(s, red, turn);
+    const float rstd = rsqrtf(s.x * inv_d + p.eps);
+    const float c = s.y * inv_d * rstd * rstd * rstd;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int vi = i * gsz + g;
+      if (!live || vi >= nv) continue;
+      const int64_t at = row * D + (int64_t)vi * V;
+      float dh[V] = {}, x[V] = {};
+      if (p.b) load_vec<V>(dh, p.b, at, p.stream_f32);
+      if (p.want_scale) load_vec<V>(x, p.d, at, p.f32);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        dh[k] += rstd * dy[i][k] * w[i][k] - c * h[i][k];
+        dw[i][k] = fmaf(dy[i][k] * rstd, h[i][k], dw[i][k]);
+        ds[i][k] = fmaf(dh[k], x[k], ds[i][k]);
+      }
+      if (p.o1) store_vec<V>(p.o1, at, dh, p.stream_f32);
+      if (p.o0) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) dh[k] *= sc[i][k];
+        store_vec<V>(p.o0, at, dh, p.f32);
+      }
+    }
+  }
+  write_partials<G, E, V>(p, dw, ds, g, grp, gsz, rpb, nv);
+}
+
+// a = dout, b = gate or null, c = x; o0 = dx, o1 = dgate
+template <int G, int E, int V>
+__global__ void __launch_bounds__(G ? 256 : E * V >= 8 && V == 1 ? 1024 : 512) postnorm_bwd_kernel(const NormParams p) {
+  KDA_NORM_ROWS(G)
+  float dw[E][V] = {}, ds[E][V] = {};
+  for (int64_t base = (int64_t)blockIdx.x * rpb; base < p.n_rows; base += stride, ++turn) {
+    const int64_t row = base + grp;
+    const bool live = row < p.n_rows;
+    const int64_t grow = (row / p.heads) * p.gate_stride + (row % p.heads) * (int64_t)D;
+    float x[E][V], dy[E][V], gt[E][V];
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int vi = i * gsz + g;
+      const bool ok = live && vi < nv;
+      const int64_t at = row * D + (int64_t)vi * V;
+#pragma unroll
+      for (int k = 0; k < V; ++k) x[i][k] = dy[i][k] = gt[i][k] = 0.f;
+      if (ok) load_vec<V>(x[i], p.c, at, p.f32);
+      if (ok) load_vec<V>(dy[i], p.a, at, p.f32);
+      if (ok && p.b) load_vec<V>(gt[i], p.b, grow + (int64_t)vi * V, p.f32);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        float d, act = 1.f;
+        if (p.b) act = gate_fn(gt[i][k], p.fn, d);
+        s.x = fmaf(x[i][k], x[i][k], s.x);
+        s.y = fmaf(dy[i][k] * sc[i][k] * act * w[i][k], x[i][k], s.y);
+      }
+    }
+    s = row_sum<G>(s, red, turn);
+    const float rstd = rsqrtf(s.x * inv_d + p.eps);
+    const float c = s.y * inv_d * rstd * rstd * rstd;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int vi = i * gsz + g;
+      if (!live || vi >= nv) continue;
+      const int64_t at = row * D + (int64_t)vi * V;
+      float dx[V], dg[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        float d = 0.f, act = 1.f;
+        if (p.b) act = gate_fn(gt[i][k], p.fn, d);
+        const float u = x[i][k] * rstd, dn = dy[i][k] * sc[i][k];
+        dx[k] = rstd * dn * act * w[i][k] - c * x[i][k];
+        dg[k] = dn * u * w[i][k] * d;
+        dw[i][k] = fmaf(dn * act, u, dw[i][k]);
+        ds[i][k] = fmaf(dy[i][k], u * w[i][k] * act, ds[i][k]);
+      }
+      store_vec<V>(p.o0, at, dx, p.f32);
+      if (p.o1) store_vec<V>(p.o1, at, dg, p.f32);
+    }
+  }
+  write_partials<G, E, V>(p, dw, ds, g, grp, gsz, rpb, nv);
+}
+
+// A block per 32 columns: 32 row groups add every 32nd row, then their sums are added
+// in order.
+__global__ void column_sums_kernel(const float* part, int64_t rows, int64_t cols, int64_t n0,
+                                   int64_t n1, float* out0, float* out1, float* out2) {
+  __shared__ float sums[32][33];
+  const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+  const int64_t e = (int64_t)blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (e < cols) {
+#pragma unroll 4
+    for (int64_t r = grp; r < rows; r += 32) s += part[r * cols + e];
+  }
+  sums[grp][lane] = s;
+  __syncthreads();
+  s = sums[lane][grp];  // lane: row group, grp: column
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int64_t c = (int64_t)blockIdx.x * 32 + grp;
+  if (lane == 0 && c < cols) {
+    float* const out = c < n0 ? out0 : c < n0 + n1 ? out1 : out2;
+    if (out) out[c < n0 ? c : c < n0 + n1 ? c - n0 : c - n0 - n1] = s;
+  }
+}
+
+// How a row is divided: G lanes (0: a block of `threads`), E vectors of V values each.
+struct NormPlan {
+  int G, E, V, threads, rpb;
+};
+
+NormPlan norm_plan(int dim, bool vec) {
+  NormPlan n;
+  n.V = vec ? 8 : 1;
+  const int nv = (dim + n.V - 1) / n.V;
+  n.threads = 256;
+  if (nv <= 16) {
+    n.G = 16, n.E = 1;
+  } else if (nv <= 64) {
+    n.G = 32, n.E = nv <= 32 ? 1 : 2;
+  } else {
+    n.G = 0;
+    n.E = vec ? (nv <= 512 ? 1 : 2) : (nv <= 2048 ? 4 : 8);
+    n.threads = ((nv + n.E - 1) / n.E + 31) / 32 * 32;
+  }
+  n.rpb = n.G ? n.threads / n.G : 1;
+  return n;
+}
+
+constexpr int kMaxBlocks = 1216;  // 8 blocks on each of 152 SMs: partial rows of the sums
+
+int64_t norm_grid(const NormPlan& n, int64_t rows, int num_sms, int per_sm) {
+  const int64_t need = (rows + n.rpb - 1) / n.rpb;
+  const int64_t most = (int64_t)num_sms * per_sm;
+  return need < most ? need : most;
+}
+
+#define KDA_NORM_CASE(KERNEL, G_, E_, V_) \
+  if (n.G == G_ && n.E == E_ && n.V == V_) return KERNEL<G_, E_, V_>;
+#define KDA_NORM_PICK(NAME, KERNEL)             \
+  void (*NAME(const NormPlan& n))(NormParams) { \
+    KDA_NORM_CASE(KERNEL, 16, 1, 8)             \
+    KDA_NORM_CASE(KERNEL, 32, 1, 8)             \
+    KDA_NORM_CASE(KERNEL, 32, 2, 8)             \
+    KDA_NORM_CASE(KERNEL, 0, 1, 8)              \
+    KDA_NORM_CASE(KERNEL, 0, 2, 8)              \
+    KDA_NORM_CASE(KERNEL, 16, 1, 1)             \
+    KDA_NORM_CASE(KERNEL, 32, 1, 1)             \
+    KDA_NORM_CASE(KERNEL, 32, 2, 1)             \
+    KDA_NORM_CASE(KERNEL, 0, 4, 1)              \
+    KDA_NORM_CASE(KERNEL, 0, 8, 1)              \
+    return nullptr;                             \
+  }
+KDA_NORM_PICK(pick_prenorm_fwd, prenorm_fwd_kernel)
+KDA_NORM_PICK(pick_postnorm_fwd, postnorm_fwd_kernel)
+KDA_NORM_PICK(pick_prenorm_bwd, prenorm_bwd_kernel)
+KDA_NORM_PICK(pick_postnorm_bwd, postnorm_bwd_kernel)
+
+bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool al_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+kda_status check_norm(int64_t rows, int32_t dim, int32_t dtype, int32_t stream_dtype, float eps,
+                      const float* scale, float scale_value) {
+  if (rows < 0 || dim < 1 || dim > KDA_NORM_MAX_DIM || rows >= (int64_t(1) << 40) / dim)
+    return KDA_ERR_INVALID_SHAPE;
+  if ((dtype != KDA_ROW_BF16 && dtype != KDA_ROW_FP32) ||
+      (stream_dtype != KDA_ROW_FP32 && stream_dtype != dtype) || !(eps >= 0.f) ||
+      !std::isfinite(eps) || (!scale && !std::isfinite(scale_value)))
+    return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+
+kda_status run_norm(void (*kernel)(NormParams), const NormPlan& n, const NormParams& p,
+                    int64_t grid, size_t smem, cudaStream_t stream) {
+  if (!kernel) return KDA_ERR_INVALID_SHAPE;
+  kernel<<<(unsigned)grid, n.threads, smem, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status run_norm_bwd(void (*kernel)(NormParams), const NormPlan& n, NormParams& p, int num_sms,
+                        void* workspace, float* dweight, float* dscale, cudaStream_t stream) {
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + KDA_STATUS_BYTES);
+  int64_t grid = norm_grid(n, p.n_rows, num_sms, n.G ? 4 : 2);
+  if (grid > kMaxBlocks) grid = kMaxBlocks;
+  const size_t smem = n.G ? 2 * (size_t)p.dim * sizeof(float) : 0;
+  if (grid > 0) {
+    const kda_status st = run_norm(kernel, n, p, grid, smem, stream);
+    if (st != KDA_OK) return st;
+  }
+  return launch_column_sums(p.part, grid, (p.want_scale ? 2 : 1) * (int64_t)p.dim, p.dim, p.dim,
+                            dweight, dscale, nullptr, stream) ==
+                 cudaSuccess
+             ? KDA_OK
+             : KDA_ERR_CUDA;
+}
+
+}  // namespace
+
+cudaError_t launch_column_sums(const float* part, int64_t rows, int64_t cols, int64_t n0,
+                               int64_t n1, float* out0, float* out1, float* out2,
+                               cudaStream_t stream) {
+  if (cols <= 0) return cudaSuccess;
+  column_sums_kernel<<<(unsigned)((cols + 31) / 32), 1024, 0, stream>>>(part, rows, cols, n0, n1,
+                                                                       out0, out1, out2);
+  return cudaGetLastError();
+}
+
+}  // namespace kda
+
+extern "C" {
+
+kda_status kda_norm_bwd_get_workspace_size(int64_t rows, int32_t dim, size_t* bytes) {
+  if (!bytes) return KDA_ERR_NULL_POINTER;
+  if (rows < 0 || dim < 1 || dim > KDA_NORM_MAX_DIM) return KDA_ERR_INVALID_SHAPE;
+  const int64_t blocks = rows < kda::kMaxBlocks ? rows : kda::kMaxBlocks;
+  *bytes = KDA_STATUS_BYTES + (size_t)blocks * 2 * dim * sizeof(float);
+  return KDA_OK;
+}
+
+kda_status kda_prenorm_fwd(const void* x, const void* residual, const float* weight,
+                           const float* res_scale, float res_scale_value, float eps, void* out,
+                           void* residual_out, int64_t rows, int32_t dim, int32_t dtype,
+                           int32_t stream_dtype, cudaStream_t stream) {
+  using namespace kda;
+  kda_status st = check_norm(rows, dim, dtype, stream_dtype, eps, res_scale, res_scale_value);
+  if (st != KDA_OK) return st;
+  if (!weight || (rows > 0 && (!x || !out))) return KDA_ERR_NULL_POINTER;
+  const size_t e = dtype == KDA_ROW_FP32 ? 4 : 2, se = stream_dtype == KDA_ROW_FP32 ? 4 : 2;
+  if (!al_to(x, e) || !al_to(out, e) || !al_to(residual, se) || !al_to(residual_out, se) ||
+      !al_to(weight, 4) || !al_to(res_scale, 4))
+    return KDA_ERR_MISALIGNED;
+  st = check_device();
+  if (st != KDA_OK || rows == 0) return st;
+  int num_sms = 0;
+  if (sm_count(&num_sms) != KDA_OK) return KDA_ERR_CUDA;
+  const NormPlan n = norm_plan(dim, dim % 8 == 0 && al16(x) && al16(out) && al16(residual) &&
+                                        al16(residual_out) && al16(weight) && al16(res_scale));
+  NormParams p = {};
+  p.a = x, p.b = residual, p.o0 = out, p.o1 = residual_out;
+  p.weight = weight, p.scale = res_scale, p.scale_value = res_scale_value, p.eps = eps;
+  p.n_rows = rows, p.dim = dim, p.f32 = dtype == KDA_ROW_FP32;
+  p.stream_f32 = stream_dtype == KDA_ROW_FP32;
+  return run_norm(pick_prenorm_fwd(n), n, p, norm_grid(n, rows, num_sms, 32), 0, stream);
+}
+
+kda_status kda_prenorm_bwd(const void* dout, const void* dresidual_out, const void* h,
+                           const float* weight, const void* x, const float* res_scale,
+                           float res_scale_value, float eps, void* dx, void* dresidual,
+                           float* dweight, float* dres_scale, int64_t rows, int32_t dim,
+                           int32_t dtype, int32_t stream_dtype, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream) {
+  using namespace kda;
+  kda_status st = check_norm(rows, dim, dtype, stream_dtype, eps, res_scale, res_scale_value);
+  if (st != KDA_OK) return st;
+  if (!weight || !dweight || !workspace ||
+      (rows > 0 && (!dout || !h || (!dx && !dresidual) || (dres_scale && !x))))
+    return KDA_ERR_NULL_POINTER;
+  const size_t e = dtype == KDA_ROW_FP32 ? 4 : 2, se = stream_dtype == KDA_ROW_FP32 ? 4 : 2;
+  if (!al_to(x, e) || !al_to(dout, e) || !al_to(dx, e) || !al_to(dresidual_out, se) ||
+      !al_to(h, se) || !al_to(dresidual, se) || !al_to(weight, 4) || !al_to(res_scale, 4) ||
+      !al_to(dweight, 4) || !al_to(dres_scale, 4) || !al_to(workspace, 128))
+    return KDA_ERR_MISALIGNED;
+  size_t need = 0;
+  kda_norm_bwd_get_workspace_size(rows, dim, &need);
+  if (workspace_bytes < need) return KDA_ERR_WORKSPACE_TOO_SMALL;
+  st = check_device();
+  if (st != KDA_OK) return st;
+  int num_sms = 0;
+  if (sm_count(&num_sms) != KDA_OK) return KDA_ERR_CUDA;
+  const NormPlan n =
+      norm_plan(dim, dim % 8 == 0 && al16(dout) && al16(dresidual_out) && al16(h) &&
+                         (!dres_scale || al16(x)) && al16(dx) && al16(dresidual) && al16(weight) &&
+                         al16(res_scale));
+  NormParams p = {};
+  p.a = dout, p.b = dresidual_out, p.c = h, p.d = x, p.o0 = dx, p.o1 = dresidual;
+  p.weight = weight, p.scale = res_scale, p.scale_value = res_scale_value, p.eps = eps;
+  p.n_rows = rows, p.dim = dim, p.f32 = dtype == KDA_ROW_FP32;
+  p.stream_f32 = stream_dtype == KDA_ROW_FP32, p.want_scale = dres_scale != nullptr;
+  return run_norm_bwd(pick_prenorm_bwd(n), n, p, num_sms, workspace, dweight, dres_scale, stream);
+}
+
+kda_status kda_postnorm_fwd(const void* x, const float* weight, const void* gate,
+                            int64_t gate_stride, int32_t heads, const void* residual,
+                            const float* res_scale, float res_scale_value, float eps, int32_t fn,
+                            void* out, int64_t rows, int32_t dim, int32_t dtype,
+                            cudaStream_t stream) {
+  using namespace kda;
+  kda_status st = check_norm(rows, dim, dtype, dtype, eps, res_scale, res_scale_value);
+  if (st != KDA_OK) return st;
+  if (fn != KDA_FN_SILU && fn != KDA_FN_SIGMOID) return KDA_ERR_INVALID_ARG;
+  if (gate && (heads < 1 || rows % heads != 0 || gate_stride < (int64_t)heads * dim ||
+               gate_stride >= (int64_t(1) << 31)))
+    return KDA_ERR_INVALID_SHAPE;
+  if (!weight || (rows > 0 && (!x || !out))) return KDA_ERR_NULL_POINTER;
+  const size_t e = dtype == KDA_ROW_FP32 ? 4 : 2;
+  if (!al_to(x, e) || !al_to(out, e) || !al_to(gate, e) || !al_to(residual, e) ||
+      !al_to(weight, 4) || !al_to(res_scale, 4))
+    return KDA_ERR_MISALIGNED;
+  st = check_device();
+  if (st != KDA_OK || rows == 0) return st;
+  int num_sms = 0;
+  if (sm_count(&num_sms) != KDA_OK) return KDA_ERR_CUDA;
+  const NormPlan n = norm_plan(dim, dim % 8 == 0 && al16(x) && al16(out) && al16(residual) &&
+                                        al16(gate) && (!gate || gate_stride * e % 16 == 0) && al16(weight) &&
+                                        al16(res_scale));
+  NormParams p = {};
+  p.a = x, p.b = gate, p.c = residual, p.o0 = out, p.fn = fn;
+  p.gate_stride = gate ? gate_stride : dim, p.heads = gate ? heads : 1;
+  p.weight = weight, p.scale = res_scale, p.scale_value = res_scale_value, p.eps = eps;
+  p.n_rows = rows, p.dim = dim, p.f32 = dtype == KDA_ROW_FP32;
+  return run_norm(pick_postnorm_fwd(n), n, p, norm_grid(n, rows, num_sms, 32), 0, stream);
+}
+
+kda_status kda_postnorm_bwd(const void* dout, const void* x, const float* weight, const void* gate,
+                            int64_t gate_stride, int32_t heads, const float* res_scale,
+                            float res_scale_value, float eps, int32_t fn, void* dx, void* dgate,
+                            float* dweight, float* dres_scale, int64_t rows, int32_t dim,
+                            int32_t dtype, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+  using namespace kda;
+  kda_status st = check_norm(rows, dim, dtype, dtype, eps, res_scale, res_scale_value);
+  if (st != KDA_OK) return st;
+  if (fn != KDA_FN_SILU && fn != KDA_FN_SIGMOID) return KDA_ERR_INVALID_ARG;
+  if (gate && (heads < 1 || rows % heads != 0 || gate_stride < (int64_t)heads * dim ||
+               gate_stride >= (int64_t(1) << 31)))
+    return KDA_ERR_INVALID_SHAPE;
+  if (!weight || !dweight || !workspace || (rows > 0 && (!dout || !x || !dx)) || (dgate && !gate))
+    return KDA_ERR_NULL_POINTER;
+  const size_t e = dtype == KDA_ROW_FP32 ? 4 : 2;
+  if (!al_to(x, e) || !al_to(dout, e) || !al_to(gate, e) || !al_to(dx, e) || !al_to(dgate, e) ||
+      !al_to(weight, 4) || !al_to(res_scale, 4) || !al_to(dweight, 4) || !al_to(dres_scale, 4) ||
+      !al_to(workspace, 128))
+    return KDA_ERR_MISALIGNED;
+  size_t need = 0;
+  kda_norm_bwd_get_workspace_size(rows, dim, &need);
+  if (workspace_bytes < need) return KDA_ERR_WORKSPACE_TOO_SMALL;
+  st = check_device();
+  if (st != KDA_OK) return st;
+  int num_sms = 0;
+  if (sm_count(&num_sms) != KDA_OK) return KDA_ERR_CUDA;
+  const NormPlan n = norm_plan(dim, dim % 8 == 0 && al16(dout) && al16(x) && al16(dx) &&
+                                        al16(dgate) && al16(gate) &&
+                                        (!gate || gate_stride * e % 16 == 0) && al16(weight) &&
+                                        al16(res_scale));
+  NormParams p = {};
+  p.a = dout, p.b = gate, p.c = x, p.o0 = dx, p.o1 = dgate, p.fn = fn;
+  p.gate_stride = gate ? gate_stride : dim, p.heads = gate ? heads : 1;
+  p.weight = weight, p.scale = res_scale, p.scale_value = res_scale_value, p.eps = eps;
+  p.n_rows = rows, p.dim = dim, p.f32 = dtype == KDA_ROW_FP32;
+  p.want_scale = dres_scale != nullptr;
+  return run_norm_bwd(pick_postnorm_bwd(n), n, p, num_sms, workspace, dweight, dres_scale, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,182 @@
+// kda_rows.cuh -- device helpers of the layer operators (convolution, scan, norms):
+// loads and stores of activation rows in bf16 or fp32, the activations, and the
+// sequence a token belongs to.  All arithmetic on rows is fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "kda_ptx.cuh"
+
+namespace kda {
+namespace rows {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+using bf16 = __nv_bfloat16;
+
+__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(bf16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ bf16 from_f<bf16>(float v) { return __float2bfloat16_rn(v); }
+
+// Raw bits of V consecutive elements, so that a thread can have several loads in
+// flight in few registers.  V * sizeof(T) is 4, 8, 16 or 32 bytes (or one element).
+template <typename T, int V>
+struct Raw {
+  static constexpr int kWords = (V * (int)sizeof(T) + 3) / 4;
+  uint32_t w[kWords];
+};
+
+// INPLACE: an output of the kernel may be this buffer, so the read-only path is out.
+template <bool INPLACE, typename W>
+__device__ __forceinline__ W load_one(const W* p) {
+  if constexpr (INPLACE) return *p;
+  else return __ldg(p);
+}
+template <bool INPLACE = false, int WORDS>
+__device__ __forceinline__ void load_words(uint32_t (&w)[WORDS], const void* p) {
+  if constexpr (WORDS % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < WORDS / 4; ++i) {
+      const uint4 v = load_one<INPLACE>(static_cast<const uint4*>(p) + i);
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (WORDS == 2) {
+    const uint2 v = load_one<INPLACE>(static_cast<const uint2*>(p));
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = load_one<INPLACE>(static_cast<const uint32_t*>(p));
+  }
+}
+template <int WORDS>
+__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[WORDS]) {
+  if constexpr (WORDS % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < WORDS / 4; ++i)
+      static_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  } else if constexpr (WORDS == 2) {
+    *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  } else {
+    *static_cast<uint32_t*>(p) = w[0];
+  }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Raw<T, V>& r, float (&f)[V]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = __uint_as_float(r.w[i]);
+  } else if constexpr (V == 1) {
+    f[0] = lo_bf16(r.w[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) f[2 * i] = lo_bf16(r.w[i]), f[2 * i + 1] = hi_bf16(r.w[i]);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void pack(Raw<T, V>& r, const float (&f)[V]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.w[i] = __float_as_uint(f[i]);
+  } else if constexpr (V == 1) {
+    r.w[0] = pack_bf16(f[0], 0.f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) r.w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+  }
+}
+
+// V elements of a row that one thread holds: consecutive on the vector path (VEC),
+// `step` elements apart on the scalar path (a warp's loads stay contiguous), where
+// elements at or past `left` read as zero and are not written.
+template <typename T, int V, bool VEC>
+__device__ __forceinline__ void load_row(Raw<T, V>& r, const T* p, int step, int64_t left) {
+  if constexpr (VEC) {
+    load_words(r.w, p);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      r.w[i] = (int64_t)i * step < left ? __float_as_uint(__ldg(reinterpret_cast<const float*>(p) + (int64_t)i * step)) : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const uint32_t b = (int64_t)i * step < left
+                             ? (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + (int64_t)i * step)
+                             : 0u;
+      if (i & 1) r.w[i / 2] |= b << 16;
+      else r.w[i / 2] = b;
+    }
+  }
+}
+template <typename T, int V, bool VEC>
+__device__ __forceinline__ void store_row(T* p, const float (&f)[V], int step, int64_t left) {
+  if constexpr (VEC) {
+    Raw<T, V> r;
+    pack(r, f);
+    store_words(p, r.w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if ((int64_t)i * step < left) p[(int64_t)i * step] = from_f<T>(f[i]);
+  }
+}
+
+// sigmoid(x): 1 / (1 + 2^(-x log2 e)) with the hardware exponential and reciprocal
+// (each a few 2^-23 off, far below a bf16 step and within the fp32 rows' tolerance).
+// ex2 reaches infinity at -x > 128 / log2 e, where the quotient is a clean zero.
+__device__ __forceinline__ float sigmoid(float x) {
+  return ptx::rcp_approx(1.0f + ptx::ex2_approx(-x * kLog2e));
+}
+
+// The sequence that holds token t: the largest n with cu[n] <= t (cu sorted), by a
+// search of 32 pivots a step, all lanes of the warp together.  The result lies in
+// [0, N - 1] whatever cu holds; the caller checks the token against its bounds.
+__device__ __forceinline__ int find_sequence(const int64_t* cu, int N, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = N;  // cu[lo] <= t (or lo == 0), and cu[hi] > t (or hi == N)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const bool le = at < hi && __ldg(cu + at) <= t;
+    const unsigned m = __ballot_sync(0xffffffffu, le) | 1u;
+    const int k = 31 - __clz(m);  // the last pivot that holds
+    hi = min(hi, lo + (k + 1) * step);
+    lo = lo + k * step;
+  }
+  return lo;
+}
+
+// Writes the status word of a workspace from a full check of cu_seqlens: one warp.
+// cu[0] = 0, non-decreasing, cu[N] <= total.
+__device__ __forceinline__ void check_seqlens(const int64_t* cu, int N, int64_t total,
+                                              unsigned* status, unsigned bad_bit) {
+  bool bad = false;
+  for (int i = threadIdx.x & 31; i <= N; i += 32) {
+    const int64_t c = cu[i];
+    bad |= c < 0 || c > total || (i == 0 && c != 0) || (i < N && cu[i + 1] < c);
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  if ((threadIdx.x & 31) == 0) *status = bad ? bad_bit : 0u;
+}
+
+}  // namespace rows
+
+// out[e] = sum over r < rows of part[r][e] in a fixed order: the first n0 columns go to
+// out0, the next n1 to out1, the rest to out2 (a null output drops its columns).
+cudaError_t launch_column_sums(const float* part, int64_t rows, int64_t cols, int64_t n0,
+                               int64_t n1, float* out0, float* out1, float* out2,
+                               cudaStream_t stream);
+
+}  // namespace kda

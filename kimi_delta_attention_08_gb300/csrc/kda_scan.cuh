@@ -1,0 +1,210 @@
+// kda_scan.cuh -- what the scan's forward and backward share: the division of the
+// (tokens, channels, states) space over threads, the segments of a split scan, the
+// staging of a block of tokens and the reductions across lanes.
+//
+// A thread holds SP states of one channel in registers; the LPC = state / SP lanes of a
+// channel are neighbours, so a warp covers 32 / LPC channels and reads a token's B and C
+// once from shared memory for all of them.  A CTA holds CH channels of one group and
+// walks its tokens in blocks of kScanBlock.
+//
+// Segments.  A sequence is cut into segments of seg_len tokens (0: not cut).  Segment s of
+// sequence n has slot floor(bos_n / seg_len) + n + s: distinct for all segments of all
+// sequences and below total / seg_len + N.
+#pragma once
+
+#include "kda_internal.h"
+#include "kda_rows.cuh"
+#include "../../include/kda_layer.h"
+
+namespace kda {
+namespace scan {
+
+using namespace rows;
+
+constexpr int kScanBlock = KDA_SCAN_CHUNK;  // 32 tokens: one saved state each
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct ScanParams {
+  const void *x, *dt, *z, *B, *C, *dout;
+  int64_t x_s, dt_s, z_s, b_s, c_s;
+  const float *A_log, *D, *dt_bias;
+  const void *init, *dfin;
+  int32_t state_bf16, prescan;
+  const int64_t* cu;
+  int64_t T, total;
+  int32_t N, dim, groups, per;   // per: channels per group
+  int32_t tiles_per_group;
+  int64_t tiles, slots, seg_len;
+  void *out, *fin;
+  float* chunk_states;
+  float* seg_state;              // [slots][dim][state]: ends, then starts, of segments
+  float* seg_sum;                // [slots][dim]: sum of delta
+  unsigned* status;
+  void *dx, *ddt, *dz;           // backward
+  float *part_bc, *part_par;     // [tiles][total][2][state], [slots][dim][state + 2]
+  float* dinit;
+};
+
+// What a unit (one slot, one channel tile) works on.
+struct Segment {
+  int n;              // sequence
+  int64_t bos, eos;   // its tokens
+  int64_t t0, t1;     // the segment's tokens
+  bool first, last;   // of the sequence
+  bool live;          // false: an unused slot
+};
+
+__device__ __forceinline__ void seq_bounds(const ScanParams& p, int n, int64_t& bos, int64_t& eos) {
+  if (p.cu) {
+    bos = __ldg(p.cu + n);
+    eos = __ldg(p.cu + n + 1);
+    bos = bos < 0 ? 0 : bos > p.total ? p.total : bos;
+    eos = eos > p.total ? p.total : eos < bos ? bos : eos;
+  } else {
+    bos = (int64_t)n * p.T;
+    eos = bos + p.T;
+  }
+}
+
+__device__ __forceinline__ int64_t first_slot(const ScanParams& p, int n) {
+  int64_t bos, eos;
+  seq_bounds(p, n, bos, eos);
+  return p.seg_len ? bos / p.seg_len + n : n;
+}
+
+// All lanes of a warp together (a search of 32 pivots a step, as find_sequence).
+__device__ __forceinline__ Segment find_unit(const ScanParams& p, int64_t slot) {
+  Segment u;
+  int64_t s = 0;
+  if (p.seg_len == 0) {
+    u.n = (int)slot;
+  } else {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = p.N;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32;
+      const int at = lo + lane * step;
+      const bool le = at < hi && first_slot(p, at) <= slot;
+      const unsigned m = __ballot_sync(0xffffffffu, le) | 1u;
+      const int k = 31 - __clz(m);
+      hi = min(hi, lo + (k + 1) * step);
+      lo = lo + k * step;
+    }
+    u.n = lo;
+    s = slot - first_slot(p, lo);
+  }
+  seq_bounds(p, u.n, u.bos, u.eos);
+  const int64_t len = p.seg_len ? p.seg_len : u.eos - u.bos;
+  u.t0 = u.bos + s * len;
+  u.live = s >= 0 && (s == 0 || u.t0 < u.eos);
+  u.t1 = u.t0 + len < u.eos ? u.t0 + len : u.eos;
+  u.first = s == 0;
+  u.last = u.t1 == u.eos;
+  return u;
+}
+
+// States per thread: 4 keep the backward's recomputed tokens in registers; 8 for the
+// larger state counts, whose channels would otherwise spread over 8 or 16 lanes.
+template <int NS>
+constexpr int kStates = NS >= 32 ? 8 : 4;
+
+// softplus(v) = max(v, 0) + log1p(u), u = exp(-|v|) in (0, 1], with the relative accuracy
+// that small steps need: log1p(u) = 2 atanh(w), w = u / (2 + u) in (0, 1/3], by the series
+// of atanh, whose first term left out is w^15 / 15 (relative 2e-8 at w = 1/3).  `sig` is
+// sigmoid(v), the derivative.
+__device__ __forceinline__ float softplus(float v, float& sig) {
+  const float u = ptx::ex2_approx(-fabsf(v) * kLog2e);
+  const float w = u * ptx::rcp_approx(2.0f + u), q = w * w;
+  float s = 1.0f / 13.0f;
+  s = fmaf(s, q, 1.0f / 11.0f);
+  s = fmaf(s, q, 1.0f / 9.0f);
+  s = fmaf(s, q, 1.0f / 7.0f);
+  s = fmaf(s, q, 1.0f / 5.0f);
+  s = fmaf(s, q, 1.0f / 3.0f);
+  s = fmaf(s, q, 1.0f);
+  const float r = ptx::rcp_approx(1.0f + u);
+  sig = v >= 0.f ? r : u * r;
+  return fmaxf(v, 0.f) + 2.0f * w * s;
+}
+
+// v[0 .. L) summed over the lanes that differ in the bits from `BIT` down to `LOW`: each
+// step the lanes of a pair keep one half of the values each.  Afterwards the thread holds
+// max(L / 2^steps, 1) sums, those from value `off` on (all lanes of a group hold the same
+// one where values ran out).
+template <int L, int BIT, int LOW>
+__device__ __forceinline__ void reduce_scatter(float* v, int lane, int& off) {
+  if constexpr (BIT >= LOW) {
+    if constexpr (L > 1) {
+      const bool up = lane & BIT;
+#pragma unroll
+      for (int i = 0; i < L / 2; ++i) {
+        const float give = up ? v[i] : v[i + L / 2];
+        const float keep = up ? v[i + L / 2] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, BIT);
+      }
+      off += up ? L / 2 : 0;
+      reduce_scatter<L / 2, BIT / 2, LOW>(v, lane, off);
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], BIT);
+      reduce_scatter<1, BIT / 2, LOW>(v, lane, off);
+    }
+  }
+}
+
+template <int SP>
+__device__ __forceinline__ void load_state(float (&h)[SP], const void* p, int64_t at, bool b16) {
+#pragma unroll
+  for (int i = 0; i < SP; i += 4) {
+    if (b16) {
+      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at + i);
+      h[i] = lo_bf16(w.x), h[i + 1] = hi_bf16(w.x), h[i + 2] = lo_bf16(w.y), h[i + 3] = hi_bf16(w.y);
+    } else {
+      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + i);
+      h[i] = v.x, h[i + 1] = v.y, h[i + 2] = v.z, h[i + 3] = v.w;
+    }
+  }
+}
+template <int SP>
+__device__ __forceinline__ void store_state(void* p, int64_t at, const float (&h)[SP], bool b16) {
+#pragma unroll
+  for (int i = 0; i < SP; i += 4) {
+    if (b16)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at + i) =
+          make_uint2(pack_bf16(h[i], h[i + 1]), pack_bf16(h[i + 2], h[i + 3]));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + at + i) =
+          make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+  }
+}
+
+// Decay rates in base 2: A2 = -exp(A_log) log2 e, so that exp(-delta exp(A_log)) = 2^(delta A2).
+template <int SP>
+__device__ __forceinline__ void load_rates(float (&a)[SP], const float* A_log, int64_t at) {
+#pragma unroll
+  for (int i = 0; i < SP; ++i) a[i] = -expf(__ldg(A_log + at + i)) * kLog2e;
+}
+
+// How sequences are cut for a pass whose SMs hold ctas_per_sm CTAs of one tile each.
+struct ScanPlan {
+  int64_t seg_len, slots;
+};
+ScanPlan scan_plan(const ScanParams& p, int64_t tiles, int64_t ctas_per_sm);
+
+// The checks of sizes and of arguments that the entry points share; they fill the
+// problem's part of `s`, and whether every row starts on 16 bytes.
+kda_status check_scan_sizes(const kda_scan_problem* q, ScanParams& s);
+kda_status check_scan(const kda_scan_problem* q, ScanParams& s, bool& vec);
+
+// The status word from a check of cu_seqlens.
+cudaError_t seqlens_status(const ScanParams& p, unsigned* status, cudaStream_t stream);
+
+// The forward's tiles and plan, the bytes it needs for segments and their place.
+void scan_fwd_plan(ScanParams& p);
+size_t fwd_ws_bytes(const ScanParams& p, int state);
+void carve_fwd(ScanParams& p, int state, void* ws);
+// All its passes (out: the main pass writes outputs, else saved states only).
+cudaError_t launch_scan_fwd(ScanParams p, int state, bool f32, bool vec, bool out,
+                            cudaStream_t stream);
+
+}  // namespace scan
+}  // namespace kda

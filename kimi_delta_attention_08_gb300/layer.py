@@ -1,0 +1,506 @@
+"""Binding of the operators around the KDA recurrence in a layer (include/kda_layer.h):
+the short causal convolution, the selective state space scan, and the norms before
+and after a block.
+
+As in the rest of the binding, arguments are only checked and passed on: every
+tensor has to have the documented dtype, device and layout.  Row arguments marked
+"rows" may be a slice of a wider projection's output (contiguous channels, tokens
+one fixed stride apart).  Work goes to torch's current stream of the tensors'
+device, or to `stream`.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+
+KDA_OK = 0
+ROW_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+CONV_ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
+GATE_ACTIVATIONS = {"silu": 1, "sigmoid": 2}
+_f32 = torch.float32
+
+
+def _raise(status, where):
+    from . import KdaError
+    raise KdaError(status, where)
+
+
+def _row_dtype(t, name):
+    code = ROW_DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected bfloat16 or float32, got {t.dtype} (no implicit conversion)")
+    return code
+
+
+def _need(t, name, dtype, dev, shape):
+    """A contiguous tensor of this dtype, device and shape."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype} (no implicit conversion)")
+    if t.device != dev:
+        raise ValueError(f"{name}: expected device {dev}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous (no implicit copy)")
+    return t.data_ptr()
+
+
+def _opt(t, name, dtype, dev, shape):
+    return None if t is None else _need(t, name, dtype, dev, shape)
+
+
+def _rows(t, name, dtype, dev, shape):
+    """(pointer, row stride) of [B, T, ...] rows with contiguous channels."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype} (no implicit conversion)")
+    if t.device != dev:
+        raise ValueError(f"{name}: expected device {dev}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    st, sh = t.stride(), t.shape
+    width = 1
+    for i in range(t.dim() - 1, 1, -1):
+        if sh[i] != 1 and st[i] != width:
+            raise ValueError(f"{name}: channels must be contiguous (no implicit copy)")
+        width *= sh[i]
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    row = st[1] if sh[1] > 1 else st[0] if sh[0] > 1 else width
+    if (sh[0] > 1 and st[0] != row * sh[1]) or row < width:
+        raise ValueError(f"{name}: rows must lie one fixed stride apart (no implicit copy)")
+    return t.data_ptr(), row
+
+
+def _seqlens(cu, dev, B):
+    """(pointer, N)"""
+    if cu is None:
+        return None, B
+    if cu.dtype != torch.int64 or cu.dim() != 1 or cu.device != dev or not cu.is_contiguous():
+        raise ValueError("cu_seqlens: expected a contiguous int64 vector on the tensors' device")
+    return cu.data_ptr(), cu.numel() - 1
+
+
+class _On:
+    """The stream to enqueue on, with the tensors' device current while it is used."""
+
+    __slots__ = ("handle", "guard", "own")
+
+    def __init__(self, dev, stream):
+        if dev.type != "cuda":
+            raise ValueError("expected CUDA tensors")
+        self.guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        self.own = stream
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        self.handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def workspace(self, given, size, dev):
+        """The caller's workspace, or one from torch's allocator that lives as long as the
+        work on this call's stream."""
+        if given is not None:
+            if given.dtype != torch.uint8 or given.device != dev or not given.is_contiguous():
+                raise ValueError("workspace: expected a contiguous uint8 tensor on the tensors' device")
+            return given
+        if self.own is not None and not isinstance(self.own, torch.cuda.Stream):
+            raise ValueError("workspace: required with a raw stream handle")
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        if self.own is not None:
+            ws.record_stream(self.own)
+        return ws
+
+
+def _size(fn, *args):
+    n = ctypes.c_size_t(0)
+    st = getattr(_lib.load(), fn)(*args, ctypes.byref(n))
+    if st != KDA_OK:
+        _raise(st, fn)
+    return n.value
+
+
+def _scale_args(res_scale, dev, D):
+    """(pointer of a per-channel scale or None, the number)"""
+    if isinstance(res_scale, torch.Tensor):
+        return _need(res_scale, "res_scale", _f32, dev, (D,)), 1.0
+    return None, float(res_scale)
+
+
+# ------------------------------------------------------------- convolution --
+def _parts(outs, name, dtype, dev, B, T, C):
+    """The pointers and channel counts of one [B, T, C] tensor or of a sequence of tensors
+    [B, T, ...] that share the channels."""
+    if isinstance(outs, torch.Tensor):
+        outs = (outs,)
+    if not 1 <= len(outs) <= 4:
+        raise ValueError(f"{name}: expected one to four tensors")
+    ptrs, counts = (ctypes.c_void_p * len(outs))(), (ctypes.c_int32 * len(outs))()
+    total = 0
+    for i, o in enumerate(outs):
+        if o.dim() < 3 or o.shape[0] != B or o.shape[1] != T:
+            raise ValueError(f"{name}[{i}]: expected [{B}, {T}, ...], got {tuple(o.shape)}")
+        ptrs[i] = _need(o, f"{name}[{i}]", dtype, dev, o.shape)
+        n = o.shape[2]
+        for k in o.shape[3:]:
+            n *= k
+        counts[i] = n
+        total += n
+    if total != C:
+        raise ValueError(f"{name}: {total} channels, x has {C}")
+    return ptrs, counts, len(outs)
+
+
+def _conv_common(x, weight, bias, activation):
+    if x.dim() != 3 or weight.dim() != 2:
+        raise ValueError("x must be [B, T, C] and weight [C, width]")
+    B, T, C = x.shape
+    dev = x.device
+    if activation not in CONV_ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(CONV_ACTIVATIONS)}")
+    W = weight.shape[1]
+    return (B, T, C, W, dev, _row_dtype(x, "x"), CONV_ACTIVATIONS[activation],
+            _need(weight, "weight", _f32, dev, (C, W)), _opt(bias, "bias", _f32, dev, (C,)))
+
+
+def kda_conv_fwd(x, weight, bias, out, initial_state=None, final_state=None, cu_seqlens=None,
+                 workspace=None, *, activation="silu", stream=None) -> None:
+    """Enqueue the short causal depthwise convolution (include/kda_layer.h, kda_conv_fwd).
+
+    x: rows [B, T, C] bf16 or fp32; weight fp32 [C, width], width 2 to 4; bias fp32 [C] or
+    None; out: [B, T, C] in x's dtype, or up to four tensors [B, T, ...] that share the
+    channels in order (q, k and v for kda_fwd), written.  initial_state / final_state:
+    [N, width - 1, C] in x's dtype, the rows before the first and up to the last token; they
+    may be one buffer.  cu_seqlens as in kda_fwd; its check is reported in `workspace`
+    (uint8, 256 bytes or more) where one is given."""
+    B, T, C, W, dev, dt, fn, w, b = _conv_common(x, weight, bias, activation)
+    xp, xs = _rows(x, "x", x.dtype, dev, x.shape)
+    ptrs, counts, k = _parts(out, "out", x.dtype, dev, B, T, C)
+    cu, N = _seqlens(cu_seqlens, dev, B)
+    st = (N, W - 1, C)
+    ip = _opt(initial_state, "initial_state", x.dtype, dev, st)
+    fp = _opt(final_state, "final_state", x.dtype, dev, st)
+    with _On(dev, stream) as handle:
+        s = _lib.load().kda_conv_fwd(xp, xs, w, b, ptrs, counts, k, ip, fp, cu, B, T, C, N, W, fn,
+                                     dt, None if workspace is None else workspace.data_ptr(),
+                                     0 if workspace is None else workspace.numel(), handle)
+    if s != KDA_OK:
+        _raise(s, "kda_conv_fwd")
+
+
+def make_conv_bwd_workspace(total_tokens, C, width, device=None):
+    """Workspace for kda_conv_bwd."""
+    return torch.empty(_size("kda_conv_bwd_get_workspace_size", int(total_tokens), int(C), int(width)),
+                       dtype=torch.uint8, device=device if device is not None else "cuda")
+
+
+def kda_conv_bwd(x, weight, bias, dout, initial_state=None, dfinal_state=None, cu_seqlens=None,
+                 workspace=None, *, activation="silu", stream=None):
+    """Enqueue the convolution's backward (include/kda_layer.h, kda_conv_bwd).  dout: as
+    `out` of kda_conv_fwd, in x's dtype or fp32 (kda_bwd's dq, dk and dv as they are).
+    Returns a dict: dx in x's dtype, dweight, dbias (with a bias) and dinitial_state (with
+    an initial state) in fp32, and the workspace, whose status word tells of cu_seqlens."""
+    B, T, C, W, dev, dt, fn, w, b = _conv_common(x, weight, bias, activation)
+    xp, xs = _rows(x, "x", x.dtype, dev, x.shape)
+    first = dout if isinstance(dout, torch.Tensor) else dout[0]
+    ddt = _row_dtype(first, "dout")
+    ptrs, counts, k = _parts(dout, "dout", first.dtype, dev, B, T, C)
+    cu, N = _seqlens(cu_seqlens, dev, B)
+    st = (N, W - 1, C)
+    ip = _opt(initial_state, "initial_state", x.dtype, dev, st)
+    dfp = _opt(dfinal_state, "dfinal_state", x.dtype, dev, st)
+    on = _On(dev, stream)
+    with on as handle:
+        ws = on.workspace(workspace, _size("kda_conv_bwd_get_workspace_size", B * T, C, W), dev)
+        g = {"dx": torch.empty((B, T, C), dtype=x.dtype, device=dev),
+             "dweight": torch.empty((C, W), dtype=_f32, device=dev)}
+        if b is not None:
+            g["dbias"] = torch.empty((C,), dtype=_f32, device=dev)
+        if ip is not None:
+            g["dinitial_state"] = torch.empty(st, dtype=_f32, device=dev)
+        P = lambda nm: g[nm].data_ptr() if nm in g else None
+        s = _lib.load().kda_conv_bwd(xp, xs, w, b, ptrs, counts, k, ddt, ip, dfp, cu, P("dx"),
+                                     P("dweight"), P("dbias"), P("dinitial_state"), B, T, C, N, W,
+                                     fn, dt, ws.data_ptr(), ws.numel(), handle)
+    if s != KDA_OK:
+        _raise(s, "kda_conv_bwd")
+    g["workspace"] = ws
+    return g
+
+
+# --------------------------------------------------------------------- scan --
+STATE_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _scan_problem(x, dt, A_log, B, C, D, z, dt_bias, initial_state, other_state, cu_seqlens, names):
+    """The C problem of a call, and (B, T, N, D, state, groups, device)."""
+    if x.dim() != 3 or A_log.dim() != 2 or B.dim() != 4:
+        raise ValueError("x must be [B, T, D], A_log [D, state] and B [B, T, groups, state]")
+    dev, ty = x.device, x.dtype
+    q = _lib.kda_scan_problem()
+    q.batch, q.T, q.dim = x.shape
+    q.groups, q.state = B.shape[2:]
+    q.dtype = _row_dtype(x, "x")
+    d, n = q.dim, q.state
+    q.x, q.x_stride = _rows(x, "x", ty, dev, x.shape)
+    q.dt, q.dt_stride = _rows(dt, "dt", ty, dev, x.shape)
+    if z is not None:
+        q.z, q.z_stride = _rows(z, "z", ty, dev, x.shape)
+    bc = torch.Size((x.shape[0], x.shape[1], q.groups, n))
+    q.B, q.B_stride = _rows(B, "B", ty, dev, bc)
+    q.C, q.C_stride = _rows(C, "C", ty, dev, bc)
+    q.A_log = _need(A_log, "A_log", _f32, dev, (d, n))
+    q.D = _opt(D, "D", _f32, dev, (d,))
+    q.dt_bias = _opt(dt_bias, "dt_bias", _f32, dev, (d,))
+    q.cu_seqlens, q.N = _seqlens(cu_seqlens, dev, x.shape[0])
+    one = initial_state if initial_state is not None else other_state
+    if one is not None:
+        if one.dtype not in STATE_DTYPES:
+            raise TypeError(f"{names[0]}: states must be float32 or bfloat16, got {one.dtype}")
+        q.state_dtype = STATE_DTYPES[one.dtype]
+    sty = None if one is None else one.dtype
+    q.initial_state = _opt(initial_state, names[0], sty, dev, (q.N, d, n))
+    return q, _opt(other_state, names[1], sty, dev, (q.N, d, n)), sty
+
+
+def make_scan_states(total_tokens, N, dim, state, device=None):
+    """Buffer for the states that kda_scan_fwd(..., chunk_states=buf) saves and
+    kda_scan_bwd(..., chunk_states=buf) starts from."""
+    return torch.empty(_size("kda_scan_get_states_size", int(total_tokens), int(N), int(dim), int(state)),
+                       dtype=torch.uint8, device=device if device is not None else "cuda")
+
+
+def make_scan_workspace(batch, T, dim, state, groups=1, N=None, *, backward=False,
+                        have_states=False, device=None):
+    """Workspace for kda_scan_fwd, or with `backward` for kda_scan_bwd (have_states: it is
+    given chunk_states).  N: the number of packed sequences when cu_seqlens is used."""
+    q = _lib.kda_scan_problem()
+    q.batch, q.T, q.dim, q.state, q.groups, q.N = batch, T, dim, state, groups, N or batch
+    if N is not None:
+        q.cu_seqlens = 8  # only whether there is one counts here
+    if backward:
+        n = _size("kda_scan_bwd_get_workspace_size", ctypes.byref(q), int(have_states))
+    else:
+        n = _size("kda_scan_get_workspace_size", ctypes.byref(q))
+    return torch.empty(n, dtype=torch.uint8, device=device if device is not None else "cuda")
+
+
+def _states_arg(buf, dev):
+    if buf is None:
+        return None, 0
+    if buf.dtype != torch.uint8 or buf.device != dev or not buf.is_contiguous():
+        raise ValueError("chunk_states: expected make_scan_states's buffer on the tensors' device")
+    return buf.data_ptr(), buf.numel()
+
+
+def kda_scan_fwd(x, dt, A_log, B, C, out, D=None, z=None, dt_bias=None, initial_state=None,
+                 final_state=None, cu_seqlens=None, workspace=None, *, chunk_states=None,
+                 stream=None) -> None:
+    """Enqueue the selective state space scan (include/kda_layer.h, kda_scan_fwd):
+    delta = softplus(dt + dt_bias), h = exp(-delta exp(A_log)) h + delta x B,
+    out = (C . h + D x) silu(z).
+
+    x, dt, z: rows [B, T, D] bf16 or fp32; B, C: rows [B, T, groups, state] in x's dtype, state
+    8, 16, 32 or 64; out [B, T, D] in x's dtype, written; A_log fp32 [D, state]; D, dt_bias
+    fp32 [D]; D, z and dt_bias may be None.  initial_state / final_state: [N, D, state],
+    both fp32 or both bf16; they may be one buffer.  cu_seqlens as in kda_fwd, its check
+    reported in `workspace` (make_scan_workspace; allocated here when None).
+    chunk_states: make_scan_states's buffer, written for kda_scan_bwd."""
+    q, fp, _ = _scan_problem(x, dt, A_log, B, C, D, z, dt_bias, initial_state, final_state,
+                             cu_seqlens, ("initial_state", "final_state"))
+    dev = x.device
+    op = _need(out, "out", x.dtype, dev, x.shape)
+    cp, cb = _states_arg(chunk_states, dev)
+    lib = _lib.load()
+    on = _On(dev, stream)
+    with on as handle:
+        wp = wb = 0
+        if workspace is not None or q.T > 8 or q.cu_seqlens or cp:
+            ws = on.workspace(workspace, _size("kda_scan_get_workspace_size", ctypes.byref(q)), dev)
+            wp, wb = ws.data_ptr(), ws.numel()
+        s = lib.kda_scan_fwd(ctypes.byref(q), op, fp, cp, cb, wp, wb, handle)
+    if s != KDA_OK:
+        _raise(s, "kda_scan_fwd")
+
+
+def kda_scan_bwd(x, dt, A_log, B, C, dout, D=None, z=None, dt_bias=None, initial_state=None,
+                 dfinal_state=None, cu_seqlens=None, workspace=None, *, chunk_states=None,
+                 stream=None):
+    """Enqueue the scan's backward (include/kda_layer.h, kda_scan_bwd) for the forward call
+    with the same inputs.  chunk_states: what that call saved; without it the states are
+    computed again.  Returns a dict: dx, ddt, dB, dC (and dz) in x's dtype, dA_log (and dD,
+    ddt_bias, dinitial_state, each where its input is given) in fp32, and the workspace."""
+    q, dfp, _ = _scan_problem(x, dt, A_log, B, C, D, z, dt_bias, initial_state, dfinal_state,
+                              cu_seqlens, ("initial_state", "dfinal_state"))
+    dev, ty = x.device, x.dtype
+    dop = _need(dout, "dout", ty, dev, x.shape)
+    cp, cb = _states_arg(chunk_states, dev)
+    lib = _lib.load()
+    on = _On(dev, stream)
+    with on as handle:
+        ws = on.workspace(workspace, _size("kda_scan_bwd_get_workspace_size", ctypes.byref(q),
+                                           int(cp is not None)), dev)
+        E = lambda shape, t=_f32: torch.empty(shape, dtype=t, device=dev)
+        g = {"dx": E(x.shape, ty), "ddt": E(x.shape, ty), "dB": E(B.shape, ty), "dC": E(B.shape, ty),
+             "dA_log": E(A_log.shape)}
+        if z is not None:
+            g["dz"] = E(x.shape, ty)
+        if D is not None:
+            g["dD"] = E((q.dim,))
+        if dt_bias is not None:
+            g["ddt_bias"] = E((q.dim,))
+        if initial_state is not None:
+            g["dinitial_state"] = E(initial_state.shape)
+        P = lambda nm: g[nm].data_ptr() if nm in g else None
+        s = lib.kda_scan_bwd(ctypes.byref(q), dop, dfp, cp, cb, P("dx"), P("ddt"), P("dz"), P("dB"),
+                             P("dC"), P("dA_log"), P("dD"), P("ddt_bias"), P("dinitial_state"),
+                             ws.data_ptr(), ws.numel(), handle)
+    if s != KDA_OK:
+        _raise(s, "kda_scan_bwd")
+    g["workspace"] = ws
+    return g
+
+
+# -------------------------------------------------------------------- norms --
+def kda_prenorm_fwd(x, residual, weight, out, residual_out=None, *, res_scale=1.0, eps=1e-6,
+                    stream=None) -> None:
+    """Enqueue the norm before a block (include/kda_layer.h, kda_prenorm_fwd):
+    residual_out = residual + res_scale * x, out = unit(residual_out) * weight.
+
+    x, out: [..., D] bf16 or fp32; residual (or None) and residual_out (or None; it may be
+    residual): the same shape in x's dtype or fp32; weight fp32 [D]; res_scale: a number or
+    an fp32 tensor [D]."""
+    dev, D, shape = x.device, x.shape[-1], x.shape
+    dt = _row_dtype(x, "x")
+    xp = _need(x, "x", x.dtype, dev, shape)
+    stream_t = residual if residual is not None else residual_out
+    sdt = dt if stream_t is None else _row_dtype(stream_t, "residual")
+    sty = x.dtype if stream_t is None else stream_t.dtype
+    sp, sv = _scale_args(res_scale, dev, D)
+    with _On(dev, stream) as handle:
+        s = _lib.load().kda_prenorm_fwd(
+            xp, _opt(residual, "residual", sty, dev, shape),
+            _need(weight, "weight", _f32, dev, (D,)), sp, sv, eps,
+            _need(out, "out", x.dtype, dev, shape),
+            _opt(residual_out, "residual_out", sty, dev, shape), x.numel() // D if D else 0, D, dt,
+            sdt, handle)
+    if s != KDA_OK:
+        _raise(s, "kda_prenorm_fwd")
+
+
+def make_norm_bwd_workspace(rows, dim, device=None):
+    """Workspace for kda_prenorm_bwd and kda_postnorm_bwd over `rows` rows of `dim` values."""
+    return torch.empty(_size("kda_norm_bwd_get_workspace_size", int(rows), int(dim)),
+                       dtype=torch.uint8, device=device if device is not None else "cuda")
+
+
+def kda_prenorm_bwd(dout, dresidual_out, h, weight, x=None, workspace=None, *, res_scale=1.0,
+                    eps=1e-6, stream=None):
+    """Enqueue the backward of kda_prenorm_fwd.  h: the forward's residual_out;
+    dresidual_out: its gradient from elsewhere (h's dtype) or None.  Returns a dict: dx
+    (dout's dtype), dresidual (h's dtype), dweight, and with a per-channel res_scale, for
+    which x is needed, dres_scale; dx is dresidual itself where they are equal (res_scale 1
+    and one dtype)."""
+    dev, D, shape = dout.device, dout.shape[-1], dout.shape
+    dt, sdt = _row_dtype(dout, "dout"), _row_dtype(h, "h")
+    sp, sv = _scale_args(res_scale, dev, D)
+    if sp is not None and x is None:
+        raise ValueError("x: needed for the gradient of a per-channel res_scale")
+    rows = dout.numel() // D if D else 0
+    on = _On(dev, stream)
+    with on as handle:
+        ws = on.workspace(workspace, _size("kda_norm_bwd_get_workspace_size", rows, D), dev)
+        g = {"dresidual": torch.empty(shape, dtype=h.dtype, device=dev),
+             "dweight": torch.empty((D,), dtype=_f32, device=dev)}
+        same = sp is None and sv == 1.0 and dt == sdt
+        g["dx"] = g["dresidual"] if same else torch.empty(shape, dtype=dout.dtype, device=dev)
+        if sp is not None:
+            g["dres_scale"] = torch.empty((D,), dtype=_f32, device=dev)
+        s = _lib.load().kda_prenorm_bwd(
+            _need(dout, "dout", dout.dtype, dev, shape),
+            _opt(dresidual_out, "dresidual_out", h.dtype, dev, shape),
+            _need(h, "h", h.dtype, dev, shape), _need(weight, "weight", _f32, dev, (D,)),
+            None if sp is None else _need(x, "x", dout.dtype, dev, shape), sp, sv, eps,
+            None if same else g["dx"].data_ptr(), g["dresidual"].data_ptr(),
+            g["dweight"].data_ptr(), None if sp is None else g["dres_scale"].data_ptr(), rows, D,
+            dt, sdt, ws.data_ptr(), ws.numel(), handle)
+    if s != KDA_OK:
+        _raise(s, "kda_prenorm_bwd")
+    g["workspace"] = ws
+    return g
+
+
+def _gate_args(gate, x, dev):
+    """(pointer, token stride, heads) of a gate [..., D] or [B, T, H, D] rows."""
+    if gate is None:
+        return None, 0, 1
+    if gate.dim() == 4 and not gate.is_contiguous():
+        p, st = _rows(gate, "gate", x.dtype, dev, x.shape)
+        return p, st, x.shape[2]
+    return _need(gate, "gate", x.dtype, dev, x.shape), x.shape[-1], 1
+
+
+def kda_postnorm_fwd(x, weight, gate, out, residual=None, *, res_scale=1.0, activation="sigmoid",
+                     eps=1e-6, stream=None) -> None:
+    """Enqueue the norm after a block (include/kda_layer.h, kda_postnorm_fwd):
+    out = residual + res_scale * unit(x) * weight * activation(gate).
+
+    x, out, residual (or None): [..., D] bf16 or fp32, out may be x; gate: None, x's shape,
+    or for x [B, T, H, D] rows whose H * D channels are contiguous; weight fp32 [D]."""
+    dev, D, shape = x.device, x.shape[-1], x.shape
+    dt = _row_dtype(x, "x")
+    if activation not in GATE_ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(GATE_ACTIVATIONS)}")
+    gp, gs, heads = _gate_args(gate, x, dev)
+    sp, sv = _scale_args(res_scale, dev, D)
+    with _On(dev, stream) as handle:
+        s = _lib.load().kda_postnorm_fwd(
+            _need(x, "x", x.dtype, dev, shape), _need(weight, "weight", _f32, dev, (D,)), gp, gs,
+            heads, _opt(residual, "residual", x.dtype, dev, shape), sp, sv, eps,
+            GATE_ACTIVATIONS[activation], _need(out, "out", x.dtype, dev, shape),
+            x.numel() // D if D else 0, D, dt, handle)
+    if s != KDA_OK:
+        _raise(s, "kda_postnorm_fwd")
+
+
+def kda_postnorm_bwd(dout, x, weight, gate=None, workspace=None, *, res_scale=1.0,
+                     activation="sigmoid", eps=1e-6, stream=None):
+    """Enqueue the backward of kda_postnorm_fwd; the gradient of its residual is dout.
+    Returns a dict: dx, dgate (with a gate) in x's dtype, dweight, and dres_scale (with a
+    per-channel res_scale) in fp32."""
+    dev, D, shape = x.device, x.shape[-1], x.shape
+    dt = _row_dtype(x, "x")
+    if activation not in GATE_ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(GATE_ACTIVATIONS)}")
+    gp, gs, heads = _gate_args(gate, x, dev)
+    sp, sv = _scale_args(res_scale, dev, D)
+    rows = x.numel() // D if D else 0
+    on = _On(dev, stream)
+    with on as handle:
+        ws = on.workspace(workspace, _size("kda_norm_bwd_get_workspace_size", rows, D), dev)
+        g = {"dx": torch.empty(shape, dtype=x.dtype, device=dev),
+             "dweight": torch.empty((D,), dtype=_f32, device=dev)}
+        if gate is not None:
+            g["dgate"] = torch.empty(shape, dtype=x.dtype, device=dev)
+        if sp is not None:
+            g["dres_scale"] = torch.empty((D,), dtype=_f32, device=dev)
+        s = _lib.load().kda_postnorm_bwd(
+            _need(dout, "dout", x.dtype, dev, shape), _need(x, "x", x.dtype, dev, shape),
+            _need(weight, "weight", _f32, dev, (D,)), gp, gs, heads, sp, sv, eps,
+            GATE_ACTIVATIONS[activation], g["dx"].data_ptr(),
+            None if gate is None else g["dgate"].data_ptr(), g["dweight"].data_ptr(),
+            None if sp is None else g["dres_scale"].data_ptr(), rows, D, dt, ws.data_ptr(),
+            ws.numel(), handle)
+    if s != KDA_OK:
+        _raise(s, "kda_postnorm_bwd")
+    g["workspace"] = ws
+    return g
