@@ -234,16 +234,6 @@ __device__ __forceinline__ void stage_store(const Ctx& c, uint8_t* dst, const ui
     *reinterpret_cast<uint4*>(dst + (uint32_t)idx * 16u) = w[it];
   }
 }
-// Asynchronous 16-byte global -> shared copies (no registers); src_bytes 0 fills
-// zeros.  A thread waits for its own copies with cp_async_wait_all; a barrier
-// after that makes every thread's copies visible.
-__device__ __forceinline__ void cp_async16(void* smem, const void* gmem, uint32_t src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem)), "l"(gmem),
-               "r"(src_bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 // The 64 rows of 128 bf16 at `src` (rows `stride` elements apart, rows past n zero)
 // into `dst` as unswizzled [64][128] rows, asynchronously.
 __device__ __forceinline__ void stage_async(const Ctx& c, uint8_t* dst, const uint16_t* src,

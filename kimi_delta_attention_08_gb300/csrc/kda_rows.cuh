@@ -98,6 +98,14 @@ __device__ __forceinline__ void pack(Raw<T, V>& r, const float (&f)[V]) {
   }
 }
 
+// V consecutive elements from shared memory, aligned to their size.
+template <typename T, int V>
+__device__ __forceinline__ void load_smem(float (&f)[V], const T* p) {
+  Raw<T, V> r;
+  load_words<true>(r.w, p);
+  unpack(r, f);
+}
+
 // V elements of a row that one thread holds: consecutive on the vector path (VEC),
 // `step` elements apart on the scalar path (a warp's loads stay contiguous), where
 // elements at or past `left` read as zero and are not written.
@@ -131,6 +139,41 @@ __device__ __forceinline__ void store_row(T* p, const float (&f)[V], int step, i
     for (int i = 0; i < V; ++i)
       if ((int64_t)i * step < left) p[(int64_t)i * step] = from_f<T>(f[i]);
   }
+}
+
+// Pairs of fp32 values in one 64-bit register: the packed operations run 128 values a clock
+// on an SM, scalar ones 80 (measured, three-operand mix).  Kept as integers so that a pair
+// loaded from memory is used as it is.
+using pair = unsigned long long;
+__device__ __forceinline__ pair pr(float a, float b) {
+  pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ pair pr(float a) { return pr(a, a); }
+__device__ __forceinline__ float2 un(pair v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ pair pmul(pair a, pair b) {
+  pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ pair padd(pair a, pair b) {
+  pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ pair pfma(pair a, pair b, pair c) {
+  pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ pair pex2(pair v) {
+  const float2 e = un(v);
+  return pr(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y));
 }
 
 // sigmoid(x): 1 / (1 + 2^(-x log2 e)) with the hardware exponential and reciprocal

@@ -2,10 +2,13 @@
 // (tokens, channels, states) space over threads, the segments of a split scan, the
 // staging of a block of tokens and the reductions across lanes.
 //
-// A thread holds SP states of one channel in registers; the LPC = state / SP lanes of a
-// channel are neighbours, so a warp covers 32 / LPC channels and reads a token's B and C
-// once from shared memory for all of them.  A CTA holds CH channels of one group and
-// walks its tokens in blocks of kScanBlock.
+// A thread holds SP states of a channel (or of two) in registers, and a warp 32 / LPC of
+// these with LPC = state / SP lanes each: bit 0 of the lane and its top bits choose the states' part, the
+// bits between them the channel.  So two neighbouring lanes always share a channel, and a
+// quarter of the warp reads two addresses of B and C: a 16-byte read from shared memory
+// then takes 2.1 cycles, and one of 8 bytes by channel 1.1, where other orders of the same
+// lanes take 4 and 2 (measured).  A CTA holds CH channels of one group and walks its tokens
+// in blocks of kScanBlock.
 //
 // Segments.  A sequence is cut into segments of seg_len tokens (0: not cut).  Segment s of
 // sequence n has slot floor(bos_n / seg_len) + n + s: distinct for all segments of all
@@ -103,52 +106,96 @@ __device__ __forceinline__ Segment find_unit(const ScanParams& p, int64_t slot) 
   return u;
 }
 
-// States per thread: 4 keep the backward's recomputed tokens in registers; 8 for the
-// larger state counts, whose channels would otherwise spread over 8 or 16 lanes.
-template <int NS>
-constexpr int kStates = NS >= 32 ? 8 : 4;
-
 // softplus(v) = max(v, 0) + log1p(u), u = exp(-|v|) in (0, 1], with the relative accuracy
-// that small steps need: log1p(u) = 2 atanh(w), w = u / (2 + u) in (0, 1/3], by the series
-// of atanh, whose first term left out is w^15 / 15 (relative 2e-8 at w = 1/3).  `sig` is
-// sigmoid(v), the derivative.
-__device__ __forceinline__ float softplus(float v, float& sig) {
-  const float u = ptx::ex2_approx(-fabsf(v) * kLog2e);
-  const float w = u * ptx::rcp_approx(2.0f + u), q = w * w;
-  float s = 1.0f / 13.0f;
-  s = fmaf(s, q, 1.0f / 11.0f);
-  s = fmaf(s, q, 1.0f / 9.0f);
-  s = fmaf(s, q, 1.0f / 7.0f);
-  s = fmaf(s, q, 1.0f / 5.0f);
-  s = fmaf(s, q, 1.0f / 3.0f);
-  s = fmaf(s, q, 1.0f);
-  const float r = ptx::rcp_approx(1.0f + u);
-  sig = v >= 0.f ? r : u * r;
-  return fmaxf(v, 0.f) + 2.0f * w * s;
+// that small steps need: log1p(u) = u P(u), P of degree 8 fitted to log1p(u) / u on [0, 1]
+// by reweighted least squares to an even relative error (3e-8; 1.2e-7 as evaluated in
+// fp32).  No reciprocal: that costs as much as two exponentials.
+__device__ __forceinline__ pair softplus(pair v, pair& u) {
+  const float2 w = un(v);
+  u = pr(ptx::ex2_approx(-fabsf(w.x) * kLog2e), ptx::ex2_approx(-fabsf(w.y) * kLog2e));
+  pair s = pfma(pr(0.00523267686f), u, pr(-0.029505169f));
+  s = pfma(s, u, pr(0.0782258362f));
+  s = pfma(s, u, pr(-0.136632353f));
+  s = pfma(s, u, pr(0.191060022f));
+  s = pfma(s, u, pr(-0.248429805f));
+  s = pfma(s, u, pr(0.333190978f));
+  s = pfma(s, u, pr(-0.499994934f));
+  s = pfma(s, u, pr(0.99999994f));
+  return pfma(u, s, pr(fmaxf(w.x, 0.f), fmaxf(w.y, 0.f)));
 }
+__device__ __forceinline__ float softplus(float v, float& u) {
+  pair w;
+  const float r = un(softplus(pr(v, 0.f), w)).x;
+  u = un(w).x;
+  return r;
+}
+// Its derivative sigmoid(v) from the same u.
+__device__ __forceinline__ float softplus_slope(float v, float u) {
+  const float r = ptx::rcp_approx(1.0f + u);
+  return v >= 0.f ? r : u * r;
+}
+
+__device__ __forceinline__ pair silu(pair z) {
+  const float2 s = un(padd(pex2(pmul(z, pr(-kLog2e))), pr(1.0f)));
+  return pmul(z, pr(ptx::rcp_approx(s.x), ptx::rcp_approx(s.y)));
+}
+
+// Where a channel's 16 bytes (delta, delta, delta x, delta x) lie in a token's row: channels
+// are exchanged within groups of eight so that the staging writes (neighbouring lanes 8
+// channels apart, two rows in 8 lanes) use every bank once, as the reads (neighbouring
+// channels of one token) do anyway.
+__device__ __forceinline__ int unit_at(int tok, int c) {
+  return c ^ ((c >> 3 & 3) | (tok & 1) << 2);
+}
+
+// A lane's channel within the warp and its states' part.
+template <int LPC>
+__device__ __forceinline__ int lane_channel(int lane) {
+  return LPC == 1 ? lane : (lane >> 1) % (32 / LPC);
+}
+template <int LPC>
+__device__ __forceinline__ int lane_part(int lane) {
+  return LPC == 1 ? 0 : (lane & 1) | (lane / (64 / LPC) << 1);
+}
+
+// h <- 2^(delta A2) h + (delta x) B for a state of two channels; b = (B, B).
+__device__ __forceinline__ pair advance(pair h, pair A2, pair delta, pair dx, pair b) {
+  return pfma(pex2(pmul(delta, A2)), h, pmul(dx, b));
+}
+
+__device__ __forceinline__ float sum_of(float a, float b) { return a + b; }
+__device__ __forceinline__ pair sum_of(pair a, pair b) { return padd(a, b); }
 
 // v[0 .. L) summed over the lanes that differ in the bits from `BIT` down to `LOW`: each
 // step the lanes of a pair keep one half of the values each.  Afterwards the thread holds
 // max(L / 2^steps, 1) sums, those from value `off` on (all lanes of a group hold the same
-// one where values ran out).
-template <int L, int BIT, int LOW>
-__device__ __forceinline__ void reduce_scatter(float* v, int lane, int& off) {
+// one where values ran out).  V: float, or a pair of them.
+template <int L, int BIT, int LOW, typename V>
+__device__ __forceinline__ void reduce_scatter(V* v, int lane, int& off) {
   if constexpr (BIT >= LOW) {
     if constexpr (L > 1) {
       const bool up = lane & BIT;
 #pragma unroll
       for (int i = 0; i < L / 2; ++i) {
-        const float give = up ? v[i] : v[i + L / 2];
-        const float keep = up ? v[i + L / 2] : v[i];
-        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, BIT);
+        const V give = up ? v[i] : v[i + L / 2];
+        const V keep = up ? v[i + L / 2] : v[i];
+        v[i] = sum_of(keep, __shfl_xor_sync(0xffffffffu, give, BIT));
       }
       off += up ? L / 2 : 0;
       reduce_scatter<L / 2, BIT / 2, LOW>(v, lane, off);
     } else {
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], BIT);
+      v[0] = sum_of(v[0], __shfl_xor_sync(0xffffffffu, v[0], BIT));
       reduce_scatter<1, BIT / 2, LOW>(v, lane, off);
     }
   }
+}
+
+// The same over a channel's lanes.
+template <int L, int LPC, typename V>
+__device__ __forceinline__ void reduce_states(V* v, int lane, int& off) {
+  if constexpr (LPC > 2) reduce_scatter<L, 16, 64 / LPC>(v, lane, off);
+  constexpr int ROUNDS = LPC > 1 ? LPC / 2 : 1, LEFT = L / ROUNDS > 1 ? L / ROUNDS : 1;
+  if constexpr (LPC > 1) reduce_scatter<LEFT, 1, 1>(v, lane, off);
 }
 
 template <int SP>
@@ -184,11 +231,12 @@ __device__ __forceinline__ void load_rates(float (&a)[SP], const float* A_log, i
   for (int i = 0; i < SP; ++i) a[i] = -expf(__ldg(A_log + at + i)) * kLog2e;
 }
 
-// How sequences are cut for a pass whose SMs hold ctas_per_sm CTAs of one tile each.
+// How sequences are cut for a pass over `tiles` channel tiles: not at all with `enough` CTAs
+// per SM, else into `want` per SM.
 struct ScanPlan {
   int64_t seg_len, slots;
 };
-ScanPlan scan_plan(const ScanParams& p, int64_t tiles, int64_t ctas_per_sm);
+ScanPlan scan_plan(const ScanParams& p, int64_t tiles, int64_t enough, int64_t want);
 
 // The checks of sizes and of arguments that the entry points share; they fill the
 // problem's part of `s`, and whether every row starts on 16 bytes.
@@ -199,7 +247,7 @@ kda_status check_scan(const kda_scan_problem* q, ScanParams& s, bool& vec);
 cudaError_t seqlens_status(const ScanParams& p, unsigned* status, cudaStream_t stream);
 
 // The forward's tiles and plan, the bytes it needs for segments and their place.
-void scan_fwd_plan(ScanParams& p);
+void scan_fwd_plan(ScanParams& p, int state);
 size_t fwd_ws_bytes(const ScanParams& p, int state);
 void carve_fwd(ScanParams& p, int state, void* ws);
 // All its passes (out: the main pass writes outputs, else saved states only).

@@ -33,6 +33,8 @@ using namespace scan;
 constexpr int kRevCh = 32;
 
 template <int NS>
+constexpr int kStates = NS >= 32 ? 8 : 4;
+template <int NS>
 constexpr int kBwdCh = NS == 64 ? 32 : 64;
 
 template <typename T, int NS>
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(BwdShape<T, NS>::NT, 2) scan_bwd_kernel(const 
       unpack(ro, ov);
 #pragma unroll
       for (int i = 0; i < SV; ++i) {
-        float sig, d = softplus(tv[i] + bias[i], sig);
+        float ex, d = softplus(tv[i] + bias[i], ex);
         if (tok >= nt) d = 0.f;
         s_dx[tok][sc + i * sstep] = make_float2(d, d * xv[i]);
         s_dy[tok][sc + i * sstep] = p.z ? ov[i] * zv[i] * sigmoid(zv[i]) : ov[i];
@@ -288,8 +290,9 @@ __global__ void __launch_bounds__(BwdShape<T, NS>::NT, 2) scan_bwd_kernel(const 
 #pragma unroll
       for (int i = 0; i < SV; ++i) {
         const float2 qs = s_dx[tok][sc + i * sstep];
-        float sig;
-        const float d = softplus(tv[i] + bias[i], sig);
+        float ex;
+        const float d = softplus(tv[i] + bias[i], ex);
+        const float sig = softplus_slope(tv[i] + bias[i], ex);
         float dy = ov[i];
         dz[i] = 0.f;
         if (p.z) {
@@ -387,8 +390,9 @@ __global__ void __launch_bounds__(kRevCh * NS / kStates<NS>)
 #pragma unroll
       for (int i = 0; i < SV; ++i) {
         const int cc = sc + i * sstep;
-        float sig;
-        const float d = softplus(tv[i] + (cc < c_n && p.dt_bias ? __ldg(p.dt_bias + ch0 + cc) : 0.f), sig);
+        float ex;
+        const float d =
+            softplus(tv[i] + (cc < c_n && p.dt_bias ? __ldg(p.dt_bias + ch0 + cc) : 0.f), ex);
         s_d[tok][cc] = make_float2(tok < nt ? d : 0.f,
                                    p.z ? ov[i] * zv[i] * sigmoid(zv[i]) : ov[i]);
       }
@@ -531,7 +535,7 @@ BwdLayout bwd_layout(ScanParams& p, int state, bool have_states) {
   BwdLayout w;
   size_t at = KDA_STATUS_BYTES;
   ScanParams f = p;
-  scan_fwd_plan(f);
+  scan_fwd_plan(f, state);
   w.fwd = at;
   if (!have_states) at = up256(at + fwd_ws_bytes(f, state));
   w.states = at;
@@ -542,7 +546,7 @@ BwdLayout bwd_layout(ScanParams& p, int state, bool have_states) {
   p.tiles_per_group = (p.per + ch - 1) / ch;
   p.tiles = (int64_t)p.tiles_per_group * p.groups;
   // 2 CTAs of 256 threads per SM at the kernel's registers and shared memory
-  const ScanPlan r = scan_plan(p, p.tiles, 2);
+  const ScanPlan r = scan_plan(p, p.tiles, 1, 2);
   p.seg_len = r.seg_len, p.slots = r.slots;
   w.seg = at;
   if (p.seg_len) at = up256(at + (size_t)p.slots * p.dim * (state + 1) * sizeof(float));
@@ -605,7 +609,7 @@ kda_status kda_scan_bwd(const kda_scan_problem* problem, const void* dout,
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   vec = vec && al_to(dout, 16) && al_to(dx, 16) && al_to(ddt, 16) && al_to(dz, 16);
   if (!chunk_states) {
-    scan::scan_fwd_plan(f);
+    scan::scan_fwd_plan(f, state);
     scan::carve_fwd(f, state, ws + w.fwd);
     f.chunk_states = reinterpret_cast<float*>(ws + w.states);
     if (scan::launch_scan_fwd(f, state, f32, vec, false, stream) != cudaSuccess)

@@ -26,28 +26,27 @@ namespace {
 
 using namespace scan;
 
-constexpr int kCh = 32;      // channels per CTA
-constexpr int kYPitch = 40;  // floats per token of the y tile: spreads 4 tokens over the banks
-
-// A thread's staged elements: SN vectors of SV channels, vector q of token tok(q).
-template <int NT>
-struct Stage {
-  static constexpr int EPT = kScanBlock * kCh / NT;
-  static constexpr int SV = EPT < 8 ? EPT : 8;
-  static constexpr int SN = EPT / SV;
-  static constexpr int PER_ROW = kCh / SV;
+// A thread holds 8 states of two neighbouring channels, as pairs of fp32 values that the
+// packed operations take: 22 instructions per 4 states of 32 channels with everything (a
+// version that paired states and staged rows in shared memory took 31 to 35).  Of U tokens
+// loaded together, each of a channel pair's LPC lanes owns OWN: it loads their rows,
+// computes their steps, hands those round by shuffles, ends up with their dot products and
+// writes their outputs.  Shared memory only carries B and C, each value twice.
+template <int NS>
+struct FwdShape {
+  static constexpr int SP = 8, LPC = NS / SP, NT = 64, CH = 2 * NT / LPC;
+  static constexpr int TB = 16;                  // tokens of B and C staged at once
+  static constexpr int U = LPC == 8 ? 8 : 4, OWN = U / LPC;
+  static constexpr int BV = 2 * TB * NS / NT;    // elements of B and C per thread ...
+  static constexpr int BW = BV < 8 ? BV : 8;     // ... in vectors of BW
 };
 
 template <typename T, int NS, bool VEC, bool OUT>
-__global__ void __launch_bounds__(kCh * NS / kStates<NS>)
-    scan_fwd_kernel(const ScanParams p) {
-  constexpr int SP = kStates<NS>, LPC = NS / SP, NT = kCh * LPC;
-  using S = Stage<NT>;
-  constexpr int SV = S::SV, SN = S::SN, PER_ROW = S::PER_ROW;
-  __shared__ float2 s_dx[kScanBlock][kCh];  // delta, delta x
-  __shared__ __align__(16) float s_b[kScanBlock][NS];
-  __shared__ __align__(16) float s_c[OUT ? kScanBlock : 1][NS];
-  __shared__ __align__(16) float s_y[OUT ? kScanBlock : 1][kYPitch];
+__global__ void __launch_bounds__(FwdShape<NS>::NT, 5) scan_fwd_kernel(const ScanParams p) {
+  using S = FwdShape<NS>;
+  constexpr int SP = S::SP, LPC = S::LPC, NT = S::NT, CH = S::CH, TB = S::TB, U = S::U;
+  constexpr int OWN = S::OWN, BW = S::BW, BN = S::BV / BW;
+  __shared__ __align__(16) pair s_bc[2][2][TB][NS];  // [buffer][B, C]
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int64_t slot = blockIdx.x / p.tiles;
@@ -61,143 +60,176 @@ __global__ void __launch_bounds__(kCh * NS / kStates<NS>)
   const bool prescan = !OUT && p.prescan;
   if (prescan && u.last) return;  // its end starts no segment
   const int grp = tile / p.tiles_per_group;
-  const int c_lo = (tile % p.tiles_per_group) * kCh;     // within the group
-  const int c_n = min(kCh, p.per - c_lo);
-  const int64_t ch0 = (int64_t)grp * p.per + c_lo;       // first channel of the tile
-  const int c = tid / LPC, l = tid % LPC;
-  const bool mine = c < c_n;
-  const int64_t st_at = (ch0 + c) * NS + l * SP;         // state offset within [dim][NS]
+  const int l = lane_part<LPC>(lane);
+  // the thread's channels within the group, cg and cg + 1; `left` of them exist
+  const int cg = (tile % p.tiles_per_group) * CH + 2 * (tid / 32 * (32 / LPC) + lane_channel<LPC>(lane));
+  const int left = min(2, p.per - cg);
+  const int64_t ch = (int64_t)grp * p.per + (left > 0 ? cg : 0);
+  const int64_t st_at = ch * NS + l * SP;              // state offset within [dim][NS]
   const int64_t st_seq = (int64_t)p.dim * NS;
+  auto per_channel = [&](const float* v) {
+    return pr(v && left > 0 ? __ldg(v + ch) : 0.f, v && left > 1 ? __ldg(v + ch + 1) : 0.f);
+  };
+  const pair bias = per_channel(p.dt_bias), skip = per_channel(OUT ? p.D : nullptr);
 
-  float A2[SP], h[SP];
+  pair A2[SP], h[SP];
+  {
+    float a[2][SP], v[2][SP];
 #pragma unroll
-  for (int i = 0; i < SP; ++i) A2[i] = h[i] = 0.f;
-  if (mine) {
-    load_rates<SP>(A2, p.A_log, st_at);
-    if (p.seg_state && !prescan) load_state<SP>(h, p.seg_state, slot * st_seq + st_at, false);
-    else if (u.first && p.init) load_state<SP>(h, p.init, u.n * st_seq + st_at, p.state_bf16);
-  }
-  float sum_delta = 0.f;
-
-  // the staged channels of this thread
-  const int sc = VEC ? (tid % PER_ROW) * SV : tid % PER_ROW;   // first channel
-  const int sstep = VEC ? 1 : PER_ROW;
-  const int sleft = VEC ? (sc < c_n ? kCh : 0) : c_n - sc;
-  float bias[SV], dsk[SV];
+    for (int q = 0; q < 2; ++q) {
 #pragma unroll
-  for (int i = 0; i < SV; ++i) {
-    const int cc = sc + i * sstep;
-    bias[i] = cc < c_n && p.dt_bias ? __ldg(p.dt_bias + ch0 + cc) : 0.f;
-    dsk[i] = OUT && cc < c_n && p.D ? __ldg(p.D + ch0 + cc) : 0.f;
-  }
-  Raw<T, SV> rx[SN], rt[SN], rz[SN];
-  Raw<T, SP> rb, rc;
-  auto fetch = [&](int64_t t0) {
-#pragma unroll
-    for (int q = 0; q < SN; ++q) {
-      const int64_t t = t0 + (q * NT + tid) / PER_ROW;
-      rx[q] = rt[q] = rz[q] = Raw<T, SV>{};
-      if (t >= u.t1 || sleft <= 0) continue;
-      load_row<T, SV, VEC>(rx[q], static_cast<const T*>(p.x) + t * p.x_s + ch0 + sc, sstep, (int64_t)sleft);
-      load_row<T, SV, VEC>(rt[q], static_cast<const T*>(p.dt) + t * p.dt_s + ch0 + sc, sstep, (int64_t)sleft);
-      if (OUT && p.z)
-        load_row<T, SV, VEC>(rz[q], static_cast<const T*>(p.z) + t * p.z_s + ch0 + sc, sstep, (int64_t)sleft);
+      for (int i = 0; i < SP; ++i) a[q][i] = v[q][i] = 0.f;
+      if (q < left) {
+        load_rates<SP>(a[q], p.A_log, st_at + q * NS);
+        if (p.seg_state && !prescan) load_state<SP>(v[q], p.seg_state, slot * st_seq + st_at + q * NS, false);
+        else if (u.first && p.init) load_state<SP>(v[q], p.init, u.n * st_seq + st_at + q * NS, p.state_bf16);
+      }
     }
-    rb = rc = Raw<T, SP>{};
-    const int64_t t = t0 + tid / LPC;  // the thread's channel index doubles as a token
-    if (t < u.t1) {
-      load_row<T, SP, VEC>(rb, static_cast<const T*>(p.B) + t * p.b_s + grp * NS + l * SP, 1, SP);
-      if (OUT) load_row<T, SP, VEC>(rc, static_cast<const T*>(p.C) + t * p.c_s + grp * NS + l * SP, 1, SP);
+#pragma unroll
+    for (int i = 0; i < SP; ++i) A2[i] = pr(a[0][i], a[1][i]), h[i] = pr(v[0][i], v[1][i]);
+  }
+  auto put_state = [&](void* to, int64_t at, bool b16) {
+    float v[2][SP];
+#pragma unroll
+    for (int i = 0; i < SP; ++i) v[0][i] = un(h[i]).x, v[1][i] = un(h[i]).y;
+    if (left > 0) store_state<SP>(to, at, v[0], b16);
+    if (left > 1) store_state<SP>(to, at + NS, v[1], b16);
+  };
+  const int tokens = (int)(u.t1 - u.t0);
+  pair sum_delta = 0;
+
+  // B and C of a block: vector q * NT + tid of [B, C][TB][NS]
+  Raw<T, BW> rbc[BN];
+  auto fetch_bc = [&](int t0) {
+#pragma unroll
+    for (int q = 0; q < BN; ++q) {
+      const int e = (q * NT + tid) * BW, m = e / (TB * NS), tok = e / NS % TB, n = e % NS;
+      rbc[q] = Raw<T, BW>{};
+      if (t0 + tok < tokens && (OUT || m == 0)) {
+        const T* const row = m == 0 ? static_cast<const T*>(p.B) + (u.t0 + t0 + tok) * p.b_s
+                                    : static_cast<const T*>(p.C) + (u.t0 + t0 + tok) * p.c_s;
+        load_row<T, BW, VEC>(rbc[q], row + grp * NS + n, 1, BW);
+      }
     }
   };
-  fetch(u.t0);
-  for (int64_t t0 = u.t0; t0 < u.t1; t0 += kScanBlock) {
-    const int nt = (int)min((int64_t)kScanBlock, u.t1 - t0);
-    // tokens past nt are staged as zero steps, which leave the state as it is
+  auto put_bc = [&](int buf) {
 #pragma unroll
-    for (int q = 0; q < SN; ++q) {
-      const int tok = (q * NT + tid) / PER_ROW;
-      float xv[SV], tv[SV];
-      unpack(rx[q], xv);
-      unpack(rt[q], tv);
+    for (int q = 0; q < BN; ++q) {
+      float v[BW];
+      unpack(rbc[q], v);
+      float4* const to = reinterpret_cast<float4*>(&s_bc[buf][0][0][0] + (q * NT + tid) * BW);
 #pragma unroll
-      for (int i = 0; i < SV; ++i) {
-        float sig, d = softplus(tv[i] + bias[i], sig);
-        if (tok >= nt) d = 0.f;
-        s_dx[tok][sc + i * sstep] = make_float2(d, d * xv[i]);
+      for (int i = 0; i < BW; i += 2) to[i / 2] = make_float4(v[i], v[i], v[i + 1], v[i + 1]);
+    }
+  };
+  // the rows of the lane's own tokens; one past the end has dt = -infinity, a step of zero
+  const T* px = static_cast<const T*>(p.x) + (u.t0 + l * OWN) * p.x_s + ch;
+  const T* pt = static_cast<const T*>(p.dt) + (u.t0 + l * OWN) * p.dt_s + ch;
+  const T* pz = static_cast<const T*>(p.z) + (u.t0 + l * OWN) * p.z_s + ch;
+  T* po = static_cast<T*>(p.out) + (u.t0 + l * OWN) * p.dim + ch;
+  constexpr int G = TB / U;  // groups of U tokens in flight: a block's worth
+  Raw<T, 2> rx[G][OWN], rt[G][OWN], rz[G][OWN], none;
+  const float minus_inf[2] = {-INFINITY, -INFINITY};
+  pack(none, minus_inf);
+  auto fetch = [&](int g, int t) {
+#pragma unroll
+    for (int k = 0; k < OWN; ++k) {
+      rx[g][k] = rz[g][k] = Raw<T, 2>{};
+      rt[g][k] = none;
+      if (t + l * OWN + k < tokens && left > 0) {
+        load_row<T, 2, VEC>(rx[g][k], px + k * p.x_s, 1, left);
+        load_row<T, 2, VEC>(rt[g][k], pt + k * p.dt_s, 1, left);
+        if (OUT && p.z) load_row<T, 2, VEC>(rz[g][k], pz + k * p.z_s, 1, left);
       }
     }
-    {
-      float v[SP];
-      unpack(rb, v);
+    px += U * p.x_s, pt += U * p.dt_s;
+    if (OUT && p.z) pz += U * p.z_s;
+  };
+  auto as_pair = [](const Raw<T, 2>& r) {
+    float f[2];
+    unpack(r, f);
+    return pr(f[0], f[1]);
+  };
+  // the lane of these channels that owns token k of U
+  auto owner = [&](int k) {
+    const int part = k / OWN;
+    return LPC == 1 ? lane : (lane & (64 / LPC - 2)) | (part & 1) | (part >> 1) * (64 / LPC);
+  };
+  float* chunk = p.chunk_states
+                     ? p.chunk_states + (u.bos / kScanBlock + u.n + (u.t0 - u.bos) / kScanBlock) * st_seq
+                     : nullptr;
+
+  fetch_bc(0);
 #pragma unroll
-      for (int i = 0; i < SP; ++i) s_b[tid / LPC][l * SP + i] = v[i];
-      if (OUT) {
-        unpack(rc, v);
+  for (int g = 0; g < G; ++g) fetch(g, g * U);
+  put_bc(0);
+  __syncthreads();
+  for (int t0 = 0, buf = 0; t0 < tokens; t0 += TB, buf ^= 1) {
+    fetch_bc(t0 + TB);
+    if (chunk && t0 % kScanBlock == 0) {
+      put_state(chunk, st_at, false);
+      chunk += st_seq;
+    }
 #pragma unroll
-        for (int i = 0; i < SP; ++i) s_c[tid / LPC][l * SP + i] = v[i];
+    for (int g = 0; g < G; ++g) {
+      const int j0 = g * U;
+      if (t0 + j0 >= tokens) break;
+      pair delta[OWN], dx[OWN], xv[OWN], zv[OWN];
+#pragma unroll
+      for (int k = 0; k < OWN; ++k) {
+        pair ex;
+        xv[k] = as_pair(rx[g][k]);
+        if (OUT && p.z) zv[k] = as_pair(rz[g][k]);
+        delta[k] = softplus(padd(as_pair(rt[g][k]), bias), ex);
+        dx[k] = pmul(delta[k], xv[k]);
+        if (!OUT) sum_delta = padd(sum_delta, delta[k]);
       }
-    }
-    Raw<T, SV> cx[SN], cz[SN];
+      fetch(g, t0 + TB + j0);
+      pair y[U];
 #pragma unroll
-    for (int q = 0; q < SN; ++q) cx[q] = rx[q], cz[q] = rz[q];
-    __syncthreads();
-    if (t0 + kScanBlock < u.t1) fetch(t0 + kScanBlock);
-    if (p.chunk_states && mine) {
-      const int64_t chunk = u.bos / kScanBlock + u.n + (t0 - u.bos) / kScanBlock;
-      store_state<SP>(p.chunk_states, chunk * st_seq + st_at, h, false);
-    }
-    for (int j0 = 0; j0 < nt; j0 += LPC) {
-      float y[LPC];
-#pragma unroll
-      for (int k = 0; k < LPC; ++k) {
-        const float2 d = s_dx[j0 + k][c];
-        float2 acc = make_float2(0.f, 0.f);
+      for (int k = 0; k < U; ++k) {
+        const pair d = LPC == 1 ? delta[k % OWN] : __shfl_sync(0xffffffffu, delta[k % OWN], owner(k));
+        const pair m = LPC == 1 ? dx[k % OWN] : __shfl_sync(0xffffffffu, dx[k % OWN], owner(k));
+        const pair* const b = &s_bc[buf][0][j0 + k][l * SP];
+        const pair* const cc = &s_bc[buf][1][j0 + k][l * SP];
+        pair acc[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < SP; i += 2) {
-          const float2 b2 = *reinterpret_cast<const float2*>(&s_b[j0 + k][l * SP + i]);
-          const float2 e = ptx::f2mul(make_float2(d.x, d.x), make_float2(A2[i], A2[i + 1]));
-          const float2 a = make_float2(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y));
-          const float2 hn = ptx::f2fma(a, make_float2(h[i], h[i + 1]),
-                                       ptx::f2mul(make_float2(d.y, d.y), b2));
-          h[i] = hn.x, h[i + 1] = hn.y;
-          if (OUT)
-            acc = ptx::f2fma(*reinterpret_cast<const float2*>(&s_c[j0 + k][l * SP + i]), hn, acc);
+          const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(b + i);
+          h[i] = advance(h[i], A2[i], d, m, b2.x);
+          h[i + 1] = advance(h[i + 1], A2[i + 1], d, m, b2.y);
+          if (OUT) {
+            const ulonglong2 c2 = *reinterpret_cast<const ulonglong2*>(cc + i);
+            acc[0] = i ? pfma(c2.x, h[i], acc[0]) : pmul(c2.x, h[i]);
+            acc[1] = i ? pfma(c2.y, h[i + 1], acc[1]) : pmul(c2.y, h[i + 1]);
+          }
         }
-        if (OUT) y[k] = acc.x + acc.y;
-        else sum_delta += d.x;
+        if (OUT) y[k] = padd(acc[0], acc[1]);
       }
-      if (OUT) {
-        int off = 0;
-        reduce_scatter<LPC, LPC / 2, 1>(y, lane, off);
-        s_y[j0 + off][c] = y[0];
+      if (!OUT) continue;
+      int off = 0;  // l * OWN
+      reduce_states<U, LPC>(y, lane, off);
+#pragma unroll
+      for (int k = 0; k < OWN; ++k) {
+        y[k] = pfma(skip, xv[k], y[k]);
+        if (p.z) y[k] = pmul(y[k], silu(zv[k]));
+        const float o[2] = {un(y[k]).x, un(y[k]).y};
+        if (t0 + j0 + l * OWN + k < tokens && left > 0)
+          store_row<T, 2, VEC>(po + (int64_t)k * p.dim, o, 1, left);
       }
+      po += (int64_t)U * p.dim;
     }
+    put_bc(buf ^ 1);
     __syncthreads();
-    if (OUT) {
-#pragma unroll
-      for (int q = 0; q < SN; ++q) {
-        const int tok = (q * NT + tid) / PER_ROW;
-        if (tok >= nt || sleft <= 0) continue;
-        float xv[SV], zv[SV], o[SV];
-        unpack(cx[q], xv);
-        unpack(cz[q], zv);
-#pragma unroll
-        for (int i = 0; i < SV; ++i) {
-          o[i] = fmaf(dsk[i], xv[i], s_y[tok][sc + i * sstep]);
-          if (p.z) o[i] *= zv[i] * sigmoid(zv[i]);
-        }
-        store_row<T, SV, VEC>(static_cast<T*>(p.out) + (t0 + tok) * p.dim + ch0 + sc, o, sstep,
-                              (int64_t)sleft);
-      }
-    }
   }
-  if (!mine) return;
   if (prescan) {
-    store_state<SP>(p.seg_state, slot * st_seq + st_at, h, false);
-    if (l == 0) p.seg_sum[slot * p.dim + ch0 + c] = sum_delta;
+    int off = 0;
+    if constexpr (LPC > 1) reduce_states<1, LPC>(&sum_delta, lane, off);
+    put_state(p.seg_state, slot * st_seq + st_at, false);
+    if (l == 0 && left > 0) p.seg_sum[slot * p.dim + ch] = un(sum_delta).x;
+    if (l == 0 && left > 1) p.seg_sum[slot * p.dim + ch + 1] = un(sum_delta).y;
   } else if (OUT && u.last && p.fin) {
-    store_state<SP>(p.fin, u.n * st_seq + st_at, h, p.state_bf16);
+    put_state(p.fin, u.n * st_seq + st_at, p.state_bf16);
   }
 }
 
@@ -242,7 +274,7 @@ __global__ void scan_carry_kernel(const ScanParams p, int state) {
 // the states, whose loads and stores are contiguous over the warp.
 template <typename T, int NS>
 __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
-  constexpr int SP = kStates<NS>, LPC = NS / SP;
+  constexpr int SP = NS >= 32 ? 8 : 4, LPC = NS / SP;
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i == 0 && p.status) *p.status = 0u;
   const int64_t per_seq = (int64_t)p.dim * LPC;
@@ -260,8 +292,8 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
   const float bias = p.dt_bias ? __ldg(p.dt_bias + ch) : 0.f, D = p.D ? __ldg(p.D + ch) : 0.f;
   for (int64_t t = n * p.T; t < (n + 1) * p.T; ++t) {
     const float x = to_f(static_cast<const T*>(p.x)[t * p.x_s + ch]);
-    float sig;
-    const float d = softplus(to_f(static_cast<const T*>(p.dt)[t * p.dt_s + ch]) + bias, sig);
+    float ex;
+    const float d = softplus(to_f(static_cast<const T*>(p.dt)[t * p.dt_s + ch]) + bias, ex);
     const T* B = static_cast<const T*>(p.B) + t * p.b_s + grp * NS + l * SP;
     const T* C = static_cast<const T*>(p.C) + t * p.c_s + grp * NS + l * SP;
     float y = 0.f;
@@ -290,11 +322,12 @@ cudaError_t launch_main(const ScanParams& p, int state, cudaStream_t stream) {
   if (grid == 0) return cudaSuccess;
   if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   const unsigned g = (unsigned)grid;
+  constexpr int NT = FwdShape<16>::NT;
   switch (state) {
-    case 8: scan_fwd_kernel<T, 8, VEC, OUT><<<g, kCh * 2, 0, stream>>>(p); break;
-    case 16: scan_fwd_kernel<T, 16, VEC, OUT><<<g, kCh * 4, 0, stream>>>(p); break;
-    case 32: scan_fwd_kernel<T, 32, VEC, OUT><<<g, kCh * 4, 0, stream>>>(p); break;
-    default: scan_fwd_kernel<T, 64, VEC, OUT><<<g, kCh * 8, 0, stream>>>(p); break;
+    case 8: scan_fwd_kernel<T, 8, VEC, OUT><<<g, NT, 0, stream>>>(p); break;
+    case 16: scan_fwd_kernel<T, 16, VEC, OUT><<<g, NT, 0, stream>>>(p); break;
+    case 32: scan_fwd_kernel<T, 32, VEC, OUT><<<g, NT, 0, stream>>>(p); break;
+    default: scan_fwd_kernel<T, 64, VEC, OUT><<<g, NT, 0, stream>>>(p); break;
   }
   return cudaGetLastError();
 }
@@ -331,19 +364,19 @@ bool al_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a 
 
 namespace scan {
 
-// A unit is one CTA's walk over one segment; sequences are cut until there are about 8 CTAs
-// of 128 threads for each SM, but not below 256 tokens.
+// A unit is one CTA's walk over one segment.  Sequences stay whole where that gives every SM
+// `enough` units; else they are cut until there are `want` for each, but not below 256
+// tokens: the two passes that cutting adds cost as much as half the main one.
 constexpr int64_t kMinSegment = 256;
 constexpr int64_t kSms = 152;
 
-ScanPlan scan_plan(const ScanParams& p, int64_t tiles, int64_t ctas_per_sm) {
+ScanPlan scan_plan(const ScanParams& p, int64_t tiles, int64_t enough, int64_t want) {
   const bool packed = p.cu != nullptr;
   const int64_t N = p.N, T = p.T, total = p.total;
   ScanPlan r = {0, N};
-  const int64_t want = kSms * ctas_per_sm;
   const int64_t whole = packed ? tiles : tiles * N;        // CTAs that surely run side by side
-  if (whole * 4 >= want * 3 || total == 0) return r;
-  const int64_t pieces = (want + whole - 1) / whole;
+  if (whole >= kSms * enough || total == 0) return r;
+  const int64_t pieces = (kSms * want + whole - 1) / whole;
   const int64_t span = packed ? total : T;
   int64_t len = (span + pieces - 1) / pieces;
   len = (len + kScanBlock - 1) / kScanBlock * kScanBlock;
@@ -354,11 +387,11 @@ ScanPlan scan_plan(const ScanParams& p, int64_t tiles, int64_t ctas_per_sm) {
   return r;
 }
 
-void scan_fwd_plan(ScanParams& p) {
-  p.tiles_per_group = (p.per + kCh - 1) / kCh;
+void scan_fwd_plan(ScanParams& p, int state) {
+  const int ch = 1024 / state;  // FwdShape::CH
+  p.tiles_per_group = (p.per + ch - 1) / ch;
   p.tiles = (int64_t)p.tiles_per_group * p.groups;
-  // 8 CTAs of 128 threads: all that an SM holds at the kernel's registers
-  const ScanPlan r = scan_plan(p, p.tiles, 8);
+  const ScanPlan r = scan_plan(p, p.tiles, 3, 16);
   p.seg_len = r.seg_len, p.slots = r.slots;
 }
 
@@ -481,7 +514,7 @@ kda_status kda_scan_get_workspace_size(const kda_scan_problem* problem, size_t* 
   scan::ScanParams p;
   const kda_status st = scan::check_scan_sizes(problem, p);
   if (st != KDA_OK) return st;
-  scan::scan_fwd_plan(p);
+  scan::scan_fwd_plan(p, problem->state);
   *bytes = KDA_STATUS_BYTES + scan::fwd_ws_bytes(p, problem->state);
   return KDA_OK;
 }
@@ -506,7 +539,7 @@ kda_status kda_scan_fwd(const kda_scan_problem* problem, void* out, void* final_
     if (chunk_states_bytes < need) return KDA_ERR_WORKSPACE_TOO_SMALL;
   }
   const bool step = !p.cu && p.T > 0 && p.T <= kStepTokens && !chunk_states;
-  scan::scan_fwd_plan(p);
+  scan::scan_fwd_plan(p, problem->state);
   if (step) p.seg_len = 0;
   const size_t need = scan::fwd_ws_bytes(p, state);
   if (need > 0 && !workspace) return KDA_ERR_NULL_POINTER;
