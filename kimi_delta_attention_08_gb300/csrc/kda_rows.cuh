@@ -183,6 +183,12 @@ __device__ __forceinline__ float sigmoid(float x) {
   return ptx::rcp_approx(1.0f + ptx::ex2_approx(-x * kLog2e));
 }
 
+__device__ __forceinline__ pair sigmoid(pair x) {
+  const float2 s = un(padd(pex2(pmul(x, pr(-kLog2e))), pr(1.0f)));
+  return pr(ptx::rcp_approx(s.x), ptx::rcp_approx(s.y));
+}
+__device__ __forceinline__ pair silu(pair x) { return pmul(x, sigmoid(x)); }
+
 // The sequence that holds token t: the largest n with cu[n] <= t (cu sorted), by a
 // search of 32 pivots a step, all lanes of the warp together.  The result lies in
 // [0, N - 1] whatever cu holds; the caller checks the token against its bounds.

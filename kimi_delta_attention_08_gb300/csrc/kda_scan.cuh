@@ -135,11 +135,6 @@ __device__ __forceinline__ float softplus_slope(float v, float u) {
   return v >= 0.f ? r : u * r;
 }
 
-__device__ __forceinline__ pair silu(pair z) {
-  const float2 s = un(padd(pex2(pmul(z, pr(-kLog2e))), pr(1.0f)));
-  return pmul(z, pr(ptx::rcp_approx(s.x), ptx::rcp_approx(s.y)));
-}
-
 // Where a channel's 16 bytes (delta, delta, delta x, delta x) lie in a token's row: channels
 // are exchanged within groups of eight so that the staging writes (neighbouring lanes 8
 // channels apart, two rows in 8 lanes) use every bank once, as the reads (neighbouring
