@@ -19,6 +19,7 @@
 #include "../../include/kda_layer.h"
 
 #include <cmath>
+#include <type_traits>
 
 namespace kda {
 namespace {
@@ -32,52 +33,42 @@ struct NormParams {
   float scale_value, eps;
   int64_t n_rows, gate_stride;
   int heads, dim, fn;
-  int f32, stream_f32;        // types of the rows and of the residual stream
   float* part;                // [blocks][1 or 2][dim] partial dweight (, dscale)
   int want_scale;
 };
 
-// Position of a thread's vector i within its row: V = 8 consecutive values (16 bytes of
-// bf16, 32 of fp32) or single ones (V = 1, rows that are not 16-byte aligned).
-template <int V>
-__device__ __forceinline__ void load_vec(float (&f)[V], const void* p, int64_t at, int f32) {
-  if constexpr (V == 1) {
-    f[0] = f32 ? static_cast<const float*>(p)[at] : to_f(static_cast<const bf16*>(p)[at]);
-  } else if (f32) {
-    Raw<float, V> r;
-    load_words<true>(r.w, static_cast<const float*>(p) + at);
-    unpack(r, f);
-  } else {
-    Raw<bf16, V> r;
-    load_words<true>(r.w, static_cast<const bf16*>(p) + at);
-    unpack(r, f);
-  }
+// A thread's values of a row come in vectors of V = 8 consecutive ones (16 bytes of bf16, 32
+// of fp32), or singly (V = 1) where rows are not 16-byte aligned.  They are kept as they
+// were read until they are needed, so that the next row's are on their way meanwhile.
+template <typename T, int V>
+__device__ __forceinline__ void load_vec(Raw<T, V>& r, const void* p, int64_t at) {
+  if constexpr (V == 1) r.w[0] = __float_as_uint(to_f(static_cast<const T*>(p)[at]));
+  else load_words<true>(r.w, static_cast<const T*>(p) + at);
 }
-template <int V>
-__device__ __forceinline__ void store_vec(void* p, int64_t at, const float (&f)[V], int f32) {
-  if constexpr (V == 1) {
-    if (f32) static_cast<float*>(p)[at] = f[0];
-    else static_cast<bf16*>(p)[at] = from_f<bf16>(f[0]);
-  } else if (f32) {
-    Raw<float, V> r;
-    pack(r, f);
-    store_words(static_cast<float*>(p) + at, r.w);
-  } else {
-    Raw<bf16, V> r;
-    pack(r, f);
-    store_words(static_cast<bf16*>(p) + at, r.w);
-  }
+template <typename T, int V>
+__device__ __forceinline__ Vals<V> values(const Raw<T, V>& r) {
+  float f[V];
+  if constexpr (V == 1) f[0] = __uint_as_float(r.w[0]);
+  else unpack(r, f);
+  return vals_from(f);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(void* p, int64_t at, const Vals<V>& v) {
+  float f[V];
+  vals_to(v, f);
+  store_row<T, V, (V > 1)>(static_cast<T*>(p) + at, f, 1, 1);
 }
 
-// Sum over the G threads of a row (G = 16, 32: lanes; G = 0: the whole block, one
-// barrier, `red` alternates between two halves so that no second one is needed).
-template <int G>
+// Sums over the G threads of a row (G = 16, 32: lanes; G = 0: the whole block, one barrier,
+// `red` alternates between two halves so that no second one is needed).  Every thread
+// gets the same bits.  TWO: both sums are wanted.
+template <int G, bool TWO>
 __device__ __forceinline__ float2 row_sum(float2 v, float2* red, int turn) {
   constexpr int W = G == 16 ? 16 : 32;
 #pragma unroll
   for (int o = W / 2; o > 0; o >>= 1) {
     v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    if (TWO) v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
   }
   if constexpr (G != 0) return v;
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -88,19 +79,26 @@ __device__ __forceinline__ float2 row_sum(float2 v, float2* red, int turn) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    if (TWO) v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
   }
   return v;
 }
 
-__device__ __forceinline__ float gate_fn(float p, int fn, float& d) {
-  const float s = sigmoid(p);
-  if (fn == KDA_FN_SILU) {
-    d = s * (1.f + p * (1.f - s));
-    return p * s;
-  }
-  d = s * (1.f - s);
-  return s;
+// The gate's activation and its slope.
+template <int V>
+__device__ __forceinline__ Vals<V> gate_fn(const Vals<V>& p, int fn, Vals<V>& slope) {
+  const Vals<V> s = sigmoid(p);
+  const Vals<V> ds = fma_of(mul_of(s, splat<V>(-1.f)), s, s);  // s (1 - s)
+  slope = ds;
+  if (fn != KDA_FN_SILU) return s;
+  slope = fma_of(p, ds, s);
+  return mul_of(p, s);
+}
+
+// How far row's gate lies from where it would lie without a stride of its own.
+__device__ __forceinline__ int64_t gate_shift(const NormParams& p, int64_t row) {
+  const int64_t own = (int64_t)p.heads * p.dim;
+  return p.gate_stride == own ? 0 : row / p.heads * (p.gate_stride - own);
 }
 
 // The rows of a block: group `grp` of the block's rows_per_block takes row
@@ -116,99 +114,102 @@ __device__ __forceinline__ float gate_fn(float p, int fn, float& d) {
   const int D = p.dim, nv = (D + V - 1) / V;                                             \
   const float inv_d = 1.0f / (float)D;                                                   \
   const int64_t stride = (int64_t)gridDim.x * rpb;                                       \
-  float w[E][V] = {}, sc[E][V];                                                          \
+  Vals<V> w[E], sc[E];                                                                   \
   _Pragma("unroll") for (int i = 0; i < E; ++i) {                                        \
     const int vi = i * gsz + g;                                                          \
-    _Pragma("unroll") for (int k = 0; k < V; ++k) sc[i][k] = p.scale_value;              \
-    if (vi < nv) load_vec<V>(w[i], p.weight, (int64_t)vi * V, 1);                        \
-    if (vi < nv && p.scale) load_vec<V>(sc[i], p.scale, (int64_t)vi * V, 1);             \
-  }
+    Raw<float, V> r;                                                                     \
+    w[i] = splat<V>(0.f), sc[i] = splat<V>(p.scale_value);                               \
+    if (vi < nv) load_vec(r, p.weight, (int64_t)vi * V), w[i] = values(r);               \
+    if (vi < nv && p.scale) load_vec(r, p.scale, (int64_t)vi * V), sc[i] = values(r);    \
+  }                                                                                      \
+  /* f(i, offset) for the thread's vectors of a row that exists */                       \
+  auto each = [&](int64_t row, auto f) {                                                 \
+    _Pragma("unroll") for (int i = 0; i < E; ++i) {                                      \
+      const int vi = i * gsz + g;                                                        \
+      if (row < p.n_rows && vi < nv) f(i, row * D + (int64_t)vi * V);                    \
+    }                                                                                    \
+  };                                                                                     \
+  int64_t row = (int64_t)blockIdx.x * rpb + grp;
 
-template <int G, int E, int V>
-__global__ void __launch_bounds__(G ? 256 : E * V >= 8 && V == 1 ? 1024 : 512) prenorm_fwd_kernel(const NormParams p) {
+// Threads of a block.  The backward over long rows is held to two blocks per SM: with their
+// 64 registers it spills a few and still takes 309 us where one block of 86 takes 393
+// (32,768 rows of 4,096 bf16 values).
+constexpr int norm_threads(int G, int E, int V) { return G ? 256 : V == 1 && E == 8 ? 1024 : 512; }
+
+template <int G, int E, int V, typename T, typename TS>
+__global__ void __launch_bounds__(norm_threads(G, E, V)) prenorm_fwd_kernel(const NormParams p) {
   KDA_NORM_ROWS(G)
-  for (int64_t base = (int64_t)blockIdx.x * rpb; base < p.n_rows; base += stride, ++turn) {
-    const int64_t row = base + grp;
-    const bool live = row < p.n_rows;
-    float h[E][V];
-    float2 s = make_float2(0.f, 0.f);
+  Raw<T, V> rx[E] = {};
+  Raw<TS, V> rr[E] = {};
+  auto fetch = [&](int64_t at_row) {
+    each(at_row, [&](int i, int64_t at) {
+      load_vec(rx[i], p.a, at);
+      if (p.b) load_vec(rr[i], p.b, at);
+    });
+  };
+  fetch(row);
+  for (int64_t base = row - grp; base < p.n_rows; base += stride, row += stride, ++turn) {
+    Vals<V> h[E], sq = splat<V>(0.f);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int vi = i * gsz + g;
-      const bool ok = live && vi < nv;
-      const int64_t at = row * D + (int64_t)vi * V;
-      float x[V] = {}, r[V] = {};
-      if (ok) load_vec<V>(x, p.a, at, p.f32);
-      if (ok && p.b) load_vec<V>(r, p.b, at, p.stream_f32);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        h[i][k] = fmaf(sc[i][k], x[k], r[k]);
-        s.x = fmaf(h[i][k], h[i][k], s.x);
-      }
+      h[i] = fma_of(sc[i], values(rx[i]), values(rr[i]));
+      sq = fma_of(h[i], h[i], sq);
     }
-    s = row_sum<G>(s, red, turn);
-    const float rstd = rsqrtf(s.x * inv_d + p.eps);
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int vi = i * gsz + g;
-      if (!live || vi >= nv) continue;
-      const int64_t at = row * D + (int64_t)vi * V;
-      if (p.o1) store_vec<V>(p.o1, at, h[i], p.stream_f32);
-      float y[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) y[k] = h[i][k] * rstd * w[i][k];
-      store_vec<V>(p.o0, at, y, p.f32);
-    }
+    fetch(row + stride);
+    const float s = row_sum<G, false>(make_float2(sum_of(sq), 0.f), red, turn).x;
+    const float rstd = rsqrtf(s * inv_d + p.eps);
+    each(row, [&](int i, int64_t at) {
+      if (p.o1) store_vec<TS, V>(p.o1, at, h[i]);
+      store_vec<T, V>(p.o0, at, mul_of(mul_of(h[i], splat<V>(rstd)), w[i]));
+    });
   }
 }
 
-template <int G, int E, int V>
-__global__ void __launch_bounds__(G ? 256 : E * V >= 8 && V == 1 ? 1024 : 512) postnorm_fwd_kernel(const NormParams p) {
+template <int G, int E, int V, typename T, typename TS>
+__global__ void __launch_bounds__(norm_threads(G, E, V)) postnorm_fwd_kernel(const NormParams p) {
   KDA_NORM_ROWS(G)
-  for (int64_t base = (int64_t)blockIdx.x * rpb; base < p.n_rows; base += stride, ++turn) {
-    const int64_t row = base + grp;
-    const bool live = row < p.n_rows;
-    const int64_t grow = (row / p.heads) * p.gate_stride + (row % p.heads) * (int64_t)D;
-    float x[E][V], gt[E][V];
-    float2 s = make_float2(0.f, 0.f);
+  Raw<T, V> rx[E] = {}, rg[E] = {}, rr[E] = {};
+  auto fetch_x = [&](int64_t at_row) {
+    each(at_row, [&](int i, int64_t at) { load_vec(rx[i], p.a, at); });
+  };
+  auto fetch_rest = [&](int64_t at_row) {
+    const int64_t shift = gate_shift(p, at_row);
+    each(at_row, [&](int i, int64_t at) {
+      if (p.b) load_vec(rg[i], p.b, at + shift);
+      if (p.c) load_vec(rr[i], p.c, at);
+    });
+  };
+  fetch_x(row);
+  fetch_rest(row);
+  for (int64_t base = row - grp; base < p.n_rows; base += stride, row += stride, ++turn) {
+    Vals<V> x[E], sq = splat<V>(0.f);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int vi = i * gsz + g;
-      const bool ok = live && vi < nv;
-#pragma unroll
-      for (int k = 0; k < V; ++k) x[i][k] = gt[i][k] = 0.f;
-      if (ok) load_vec<V>(x[i], p.a, row * D + (int64_t)vi * V, p.f32);
-      if (ok && p.b) load_vec<V>(gt[i], p.b, grow + (int64_t)vi * V, p.f32);
-#pragma unroll
-      for (int k = 0; k < V; ++k) s.x = fmaf(x[i][k], x[i][k], s.x);
+      x[i] = values(rx[i]);
+      sq = fma_of(x[i], x[i], sq);
     }
-    s = row_sum<G>(s, red, turn);
-    const float rstd = rsqrtf(s.x * inv_d + p.eps);
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int vi = i * gsz + g;
-      if (!live || vi >= nv) continue;
-      const int64_t at = row * D + (int64_t)vi * V;
-      float y[V], r[V] = {};
-      if (p.c) load_vec<V>(r, p.c, at, p.f32);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        float n = x[i][k] * rstd * w[i][k], d;
-        if (p.b) n *= gate_fn(gt[i][k], p.fn, d);
-        y[k] = fmaf(sc[i][k], n, r[k]);
-      }
-      store_vec<V>(p.o0, at, y, p.f32);
-    }
+    fetch_x(row + stride);
+    const float s = row_sum<G, false>(make_float2(sum_of(sq), 0.f), red, turn).x;
+    const float rstd = rsqrtf(s * inv_d + p.eps);
+    each(row, [&](int i, int64_t at) {
+      Vals<V> n = mul_of(mul_of(x[i], splat<V>(rstd)), w[i]), slope;
+      if (p.b) n = mul_of(n, gate_fn(values(rg[i]), p.fn, slope));
+      store_vec<T, V>(p.o0, at, fma_of(sc[i], n, values(rr[i])));
+    });
+    fetch_rest(row + stride);
   }
 }
 
 // Adds the block's row groups' dweight and dscale in the groups' order and writes the
 // block's partial row.
 template <int G, int E, int V>
-__device__ __forceinline__ void write_partials(const NormParams& p, const float (&dw)[E][V],
-                                               const float (&ds)[E][V], int g, int grp, int gsz,
+__device__ __forceinline__ void write_partials(const NormParams& p, const Vals<V> (&dwv)[E],
+                                               const Vals<V> (&dsv)[E], int g, int grp, int gsz,
                                                int rpb, int nv) {
   extern __shared__ float acc[];  // [2][dim] when several rows share a block
+  float dw[E][V], ds[E][V];
+#pragma unroll
+  for (int i = 0; i < E; ++i) vals_to(dwv[i], dw[i]), vals_to(dsv[i], ds[i]);
   const int pitch = (p.want_scale ? 2 : 1) * p.dim;
   float* out = p.part + (int64_t)blockIdx.x * pitch;
   if constexpr (G == 0) {
@@ -244,109 +245,101 @@ __device__ __forceinline__ void write_partials(const NormParams& p, const float 
 }
 
 // a = dout, b = dresidual_out or null, c = h, d = x or null (dscale)
-template <int G, int E, int V>
-__global__ void __launch_bounds__(G ? 256 : E * V >= 8 && V == 1 ? 1024 : 512) prenorm_bwd_kernel(const NormParams p) {
+template <int G, int E, int V, typename T, typename TS>
+__global__ void __launch_bounds__(norm_threads(G, E, V), G || E > 1 ? 1 : 2) prenorm_bwd_kernel(const NormParams p) {
   KDA_NORM_ROWS(G)
-  float dw[E][V] = {}, ds[E][V] = {};
-  for (int64_t base = (int64_t)blockIdx.x * rpb; base < p.n_rows; base += stride, ++turn) {
-    const int64_t row = base + grp;
-    const bool live = row < p.n_rows;
-    float h[E][V], dy[E][V];
-    float2 s = make_float2(0.f, 0.f);
+  Vals<V> dw[E], ds[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) dw[i] = ds[i] = splat<V>(0.f);
+  Raw<TS, V> rh[E] = {}, rd[E] = {};
+  Raw<T, V> ry[E] = {}, rx[E] = {};
+  auto fetch_sums = [&](int64_t at_row) {
+    each(at_row, [&](int i, int64_t at) {
+      load_vec(rh[i], p.c, at);
+      load_vec(ry[i], p.a, at);
+    });
+  };
+  auto fetch_rest = [&](int64_t at_row) {
+    each(at_row, [&](int i, int64_t at) {
+      if (p.b) load_vec(rd[i], p.b, at);
+      if (p.want_scale) load_vec(rx[i], p.d, at);
+    });
+  };
+  fetch_sums(row);
+  fetch_rest(row);
+  for (int64_t base = row - grp; base < p.n_rows; base += stride, row += stride, ++turn) {
+    Vals<V> h[E], dy[E], s1 = splat<V>(0.f), s2 = s1;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int vi = i * gsz + g;
-      const bool ok = live && vi < nv;
-      const int64_t at = row * D + (int64_t)vi * V;
-#pragma unroll
-      for (int k = 0; k < V; ++k) h[i][k] = dy[i][k] = 0.f;
-      if (ok) load_vec<V>(h[i], p.c, at, p.stream_f32);
-      if (ok) load_vec<V>(dy[i], p.a, at, p.f32);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        s.x = fmaf(h[i][k], h[i][k], s.x);
-        s.y = fmaf(dy[i][k] * w[i][k], h[i][k], s.y);
-      }
+      h[i] = values(rh[i]);
+      dy[i] = values(ry[i]);
+      s1 = fma_of(h[i], h[i], s1);
+      s2 = fma_of(mul_of(dy[i], w[i]), h[i], s2);
     }
-    s = row_sum<G>(s, red, turn);
+    fetch_sums(row + stride);
+    const float2 s = row_sum<G, true>(make_float2(sum_of(s1), sum_of(s2)), red, turn);
     const float rstd = rsqrtf(s.x * inv_d + p.eps);
     const float c = s.y * inv_d * rstd * rstd * rstd;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int vi = i * gsz + g;
-      if (!live || vi >= nv) continue;
-      const int64_t at = row * D + (int64_t)vi * V;
-      float dh[V] = {}, x[V] = {};
-      if (p.b) load_vec<V>(dh, p.b, at, p.stream_f32);
-      if (p.want_scale) load_vec<V>(x, p.d, at, p.f32);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        dh[k] += rstd * dy[i][k] * w[i][k] - c * h[i][k];
-        dw[i][k] = fmaf(dy[i][k] * rstd, h[i][k], dw[i][k]);
-        ds[i][k] = fmaf(dh[k], x[k], ds[i][k]);
-      }
-      if (p.o1) store_vec<V>(p.o1, at, dh, p.stream_f32);
-      if (p.o0) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) dh[k] *= sc[i][k];
-        store_vec<V>(p.o0, at, dh, p.f32);
-      }
-    }
+    each(row, [&](int i, int64_t at) {
+      const Vals<V> dr = mul_of(dy[i], splat<V>(rstd));
+      Vals<V> dh = fma_of(dr, w[i], values(rd[i]));
+      dh = fma_of(h[i], splat<V>(-c), dh);
+      dw[i] = fma_of(dr, h[i], dw[i]);
+      ds[i] = fma_of(dh, values(rx[i]), ds[i]);
+      if (p.o1) store_vec<TS, V>(p.o1, at, dh);
+      if (p.o0) store_vec<T, V>(p.o0, at, mul_of(dh, sc[i]));
+    });
+    fetch_rest(row + stride);
   }
   write_partials<G, E, V>(p, dw, ds, g, grp, gsz, rpb, nv);
 }
 
-// a = dout, b = gate or null, c = x; o0 = dx, o1 = dgate
-template <int G, int E, int V>
-__global__ void __launch_bounds__(G ? 256 : E * V >= 8 && V == 1 ? 1024 : 512) postnorm_bwd_kernel(const NormParams p) {
+// a = dout, b = gate or null, c = x; o0 = dx, o1 = dgate.  With a = fn(gate), a' its slope:
+// P = dout a and Q = dout a' are all that is kept of dout and the gate.
+template <int G, int E, int V, typename T, typename TS>
+__global__ void __launch_bounds__(norm_threads(G, E, V), G || E > 1 ? 1 : 2) postnorm_bwd_kernel(const NormParams p) {
   KDA_NORM_ROWS(G)
-  float dw[E][V] = {}, ds[E][V] = {};
-  for (int64_t base = (int64_t)blockIdx.x * rpb; base < p.n_rows; base += stride, ++turn) {
-    const int64_t row = base + grp;
-    const bool live = row < p.n_rows;
-    const int64_t grow = (row / p.heads) * p.gate_stride + (row % p.heads) * (int64_t)D;
-    float x[E][V], dy[E][V], gt[E][V];
-    float2 s = make_float2(0.f, 0.f);
+  Vals<V> dw[E], ds[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) dw[i] = ds[i] = splat<V>(0.f);
+  Raw<T, V> rx[E] = {}, ry[E] = {}, rg[E] = {};
+  auto fetch = [&](int64_t at_row) {
+    const int64_t shift = gate_shift(p, at_row);
+    each(at_row, [&](int i, int64_t at) {
+      load_vec(rx[i], p.c, at);
+      load_vec(ry[i], p.a, at);
+      if (p.b) load_vec(rg[i], p.b, at + shift);
+    });
+  };
+  fetch(row);
+  for (int64_t base = row - grp; base < p.n_rows; base += stride, row += stride, ++turn) {
+    Vals<V> x[E], P[E], Q[E], s1 = splat<V>(0.f), s2 = s1;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int vi = i * gsz + g;
-      const bool ok = live && vi < nv;
-      const int64_t at = row * D + (int64_t)vi * V;
-#pragma unroll
-      for (int k = 0; k < V; ++k) x[i][k] = dy[i][k] = gt[i][k] = 0.f;
-      if (ok) load_vec<V>(x[i], p.c, at, p.f32);
-      if (ok) load_vec<V>(dy[i], p.a, at, p.f32);
-      if (ok && p.b) load_vec<V>(gt[i], p.b, grow + (int64_t)vi * V, p.f32);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        float d, act = 1.f;
-        if (p.b) act = gate_fn(gt[i][k], p.fn, d);
-        s.x = fmaf(x[i][k], x[i][k], s.x);
-        s.y = fmaf(dy[i][k] * sc[i][k] * act * w[i][k], x[i][k], s.y);
+      x[i] = values(rx[i]);
+      P[i] = values(ry[i]);
+      Q[i] = splat<V>(0.f);
+      if (p.b) {
+        Vals<V> slope;
+        const Vals<V> act = gate_fn(values(rg[i]), p.fn, slope);
+        Q[i] = mul_of(P[i], slope);
+        P[i] = mul_of(P[i], act);
       }
+      s1 = fma_of(x[i], x[i], s1);
+      s2 = fma_of(mul_of(mul_of(P[i], sc[i]), w[i]), x[i], s2);
     }
-    s = row_sum<G>(s, red, turn);
+    fetch(row + stride);
+    const float2 s = row_sum<G, true>(make_float2(sum_of(s1), sum_of(s2)), red, turn);
     const float rstd = rsqrtf(s.x * inv_d + p.eps);
     const float c = s.y * inv_d * rstd * rstd * rstd;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int vi = i * gsz + g;
-      if (!live || vi >= nv) continue;
-      const int64_t at = row * D + (int64_t)vi * V;
-      float dx[V], dg[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        float d = 0.f, act = 1.f;
-        if (p.b) act = gate_fn(gt[i][k], p.fn, d);
-        const float u = x[i][k] * rstd, dn = dy[i][k] * sc[i][k];
-        dx[k] = rstd * dn * act * w[i][k] - c * x[i][k];
-        dg[k] = dn * u * w[i][k] * d;
-        dw[i][k] = fmaf(dn * act, u, dw[i][k]);
-        ds[i][k] = fmaf(dy[i][k], u * w[i][k] * act, ds[i][k]);
-      }
-      store_vec<V>(p.o0, at, dx, p.f32);
-      if (p.o1) store_vec<V>(p.o1, at, dg, p.f32);
-    }
+    each(row, [&](int i, int64_t at) {
+      const Vals<V> u = mul_of(x[i], splat<V>(rstd)), su = mul_of(sc[i], u);
+      const Vals<V> rws = mul_of(mul_of(w[i], sc[i]), splat<V>(rstd));
+      store_vec<T, V>(p.o0, at, fma_of(rws, P[i], mul_of(x[i], splat<V>(-c))));
+      if (p.o1) store_vec<T, V>(p.o1, at, mul_of(mul_of(w[i], su), Q[i]));
+      dw[i] = fma_of(su, P[i], dw[i]);
+      ds[i] = fma_of(mul_of(w[i], u), P[i], ds[i]);
+    });
   }
   write_partials<G, E, V>(p, dw, ds, g, grp, gsz, rpb, nv);
 }
@@ -406,26 +399,38 @@ int64_t norm_grid(const NormPlan& n, int64_t rows, int num_sms, int per_sm) {
   return need < most ? need : most;
 }
 
+using NormKernel = void (*)(NormParams);
+
 #define KDA_NORM_CASE(KERNEL, G_, E_, V_) \
-  if (n.G == G_ && n.E == E_ && n.V == V_) return KERNEL<G_, E_, V_>;
-#define KDA_NORM_PICK(NAME, KERNEL)             \
-  void (*NAME(const NormPlan& n))(NormParams) { \
-    KDA_NORM_CASE(KERNEL, 16, 1, 8)             \
-    KDA_NORM_CASE(KERNEL, 32, 1, 8)             \
-    KDA_NORM_CASE(KERNEL, 32, 2, 8)             \
-    KDA_NORM_CASE(KERNEL, 0, 1, 8)              \
-    KDA_NORM_CASE(KERNEL, 0, 2, 8)              \
-    KDA_NORM_CASE(KERNEL, 16, 1, 1)             \
-    KDA_NORM_CASE(KERNEL, 32, 1, 1)             \
-    KDA_NORM_CASE(KERNEL, 32, 2, 1)             \
-    KDA_NORM_CASE(KERNEL, 0, 4, 1)              \
-    KDA_NORM_CASE(KERNEL, 0, 8, 1)              \
-    return nullptr;                             \
+  if (n.G == G_ && n.E == E_ && n.V == V_) return KERNEL<G_, E_, V_, T, TS>;
+#define KDA_NORM_PICK(NAME, KERNEL)                                                \
+  template <typename T, typename TS>                                               \
+  NormKernel NAME##_of(const NormPlan& n) {                                        \
+    KDA_NORM_CASE(KERNEL, 16, 1, 8)                                                \
+    KDA_NORM_CASE(KERNEL, 32, 1, 8)                                                \
+    KDA_NORM_CASE(KERNEL, 32, 2, 8)                                                \
+    KDA_NORM_CASE(KERNEL, 0, 1, 8)                                                 \
+    KDA_NORM_CASE(KERNEL, 0, 2, 8)                                                 \
+    KDA_NORM_CASE(KERNEL, 16, 1, 1)                                                \
+    KDA_NORM_CASE(KERNEL, 32, 1, 1)                                                \
+    KDA_NORM_CASE(KERNEL, 32, 2, 1)                                                \
+    KDA_NORM_CASE(KERNEL, 0, 4, 1)                                                 \
+    KDA_NORM_CASE(KERNEL, 0, 8, 1)                                                 \
+    return nullptr;                                                                \
+  }                                                                                \
+  NormKernel NAME(const NormPlan& n, int32_t dtype, int32_t stream_dtype) {        \
+    if (dtype == KDA_ROW_FP32) return NAME##_of<float, float>(n);                  \
+    return stream_dtype == KDA_ROW_FP32 && NORM_TWO_TYPES ? NAME##_of<bf16, std::conditional_t<NORM_TWO_TYPES, float, bf16>>(n) \
+                                                          : NAME##_of<bf16, bf16>(n);  \
   }
+#define NORM_TWO_TYPES true
 KDA_NORM_PICK(pick_prenorm_fwd, prenorm_fwd_kernel)
-KDA_NORM_PICK(pick_postnorm_fwd, postnorm_fwd_kernel)
 KDA_NORM_PICK(pick_prenorm_bwd, prenorm_bwd_kernel)
+#undef NORM_TWO_TYPES
+#define NORM_TWO_TYPES false
+KDA_NORM_PICK(pick_postnorm_fwd, postnorm_fwd_kernel)
 KDA_NORM_PICK(pick_postnorm_bwd, postnorm_bwd_kernel)
+#undef NORM_TWO_TYPES
 
 bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 bool al_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -441,14 +446,14 @@ kda_status check_norm(int64_t rows, int32_t dim, int32_t dtype, int32_t stream_d
   return KDA_OK;
 }
 
-kda_status run_norm(void (*kernel)(NormParams), const NormPlan& n, const NormParams& p,
+kda_status run_norm(NormKernel kernel, const NormPlan& n, const NormParams& p,
                     int64_t grid, size_t smem, cudaStream_t stream) {
   if (!kernel) return KDA_ERR_INVALID_SHAPE;
   kernel<<<(unsigned)grid, n.threads, smem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
-kda_status run_norm_bwd(void (*kernel)(NormParams), const NormPlan& n, NormParams& p, int num_sms,
+kda_status run_norm_bwd(NormKernel kernel, const NormPlan& n, NormParams& p, int num_sms,
                         void* workspace, float* dweight, float* dscale, cudaStream_t stream) {
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + KDA_STATUS_BYTES);
   int64_t grid = norm_grid(n, p.n_rows, num_sms, n.G ? 4 : 2);
@@ -509,9 +514,8 @@ kda_status kda_prenorm_fwd(const void* x, const void* residual, const float* wei
   NormParams p = {};
   p.a = x, p.b = residual, p.o0 = out, p.o1 = residual_out;
   p.weight = weight, p.scale = res_scale, p.scale_value = res_scale_value, p.eps = eps;
-  p.n_rows = rows, p.dim = dim, p.f32 = dtype == KDA_ROW_FP32;
-  p.stream_f32 = stream_dtype == KDA_ROW_FP32;
-  return run_norm(pick_prenorm_fwd(n), n, p, norm_grid(n, rows, num_sms, 32), 0, stream);
+  p.n_rows = rows, p.dim = dim;
+  return run_norm(pick_prenorm_fwd(n, dtype, stream_dtype), n, p, norm_grid(n, rows, num_sms, 32), 0, stream);
 }
 
 kda_status kda_prenorm_bwd(const void* dout, const void* dresidual_out, const void* h,
@@ -545,9 +549,8 @@ kda_status kda_prenorm_bwd(const void* dout, const void* dresidual_out, const vo
   NormParams p = {};
   p.a = dout, p.b = dresidual_out, p.c = h, p.d = x, p.o0 = dx, p.o1 = dresidual;
   p.weight = weight, p.scale = res_scale, p.scale_value = res_scale_value, p.eps = eps;
-  p.n_rows = rows, p.dim = dim, p.f32 = dtype == KDA_ROW_FP32;
-  p.stream_f32 = stream_dtype == KDA_ROW_FP32, p.want_scale = dres_scale != nullptr;
-  return run_norm_bwd(pick_prenorm_bwd(n), n, p, num_sms, workspace, dweight, dres_scale, stream);
+  p.n_rows = rows, p.dim = dim, p.want_scale = dres_scale != nullptr;
+  return run_norm_bwd(pick_prenorm_bwd(n, dtype, stream_dtype), n, p, num_sms, workspace, dweight, dres_scale, stream);
 }
 
 kda_status kda_postnorm_fwd(const void* x, const float* weight, const void* gate,
@@ -578,8 +581,8 @@ kda_status kda_postnorm_fwd(const void* x, const float* weight, const void* gate
   p.a = x, p.b = gate, p.c = residual, p.o0 = out, p.fn = fn;
   p.gate_stride = gate ? gate_stride : dim, p.heads = gate ? heads : 1;
   p.weight = weight, p.scale = res_scale, p.scale_value = res_scale_value, p.eps = eps;
-  p.n_rows = rows, p.dim = dim, p.f32 = dtype == KDA_ROW_FP32;
-  return run_norm(pick_postnorm_fwd(n), n, p, norm_grid(n, rows, num_sms, 32), 0, stream);
+  p.n_rows = rows, p.dim = dim;
+  return run_norm(pick_postnorm_fwd(n, dtype, dtype), n, p, norm_grid(n, rows, num_sms, 32), 0, stream);
 }
 
 kda_status kda_postnorm_bwd(const void* dout, const void* x, const float* weight, const void* gate,
@@ -617,9 +620,9 @@ kda_status kda_postnorm_bwd(const void* dout, const void* x, const float* weight
   p.a = dout, p.b = gate, p.c = x, p.o0 = dx, p.o1 = dgate, p.fn = fn;
   p.gate_stride = gate ? gate_stride : dim, p.heads = gate ? heads : 1;
   p.weight = weight, p.scale = res_scale, p.scale_value = res_scale_value, p.eps = eps;
-  p.n_rows = rows, p.dim = dim, p.f32 = dtype == KDA_ROW_FP32;
+  p.n_rows = rows, p.dim = dim;
   p.want_scale = dres_scale != nullptr;
-  return run_norm_bwd(pick_postnorm_bwd(n), n, p, num_sms, workspace, dweight, dres_scale, stream);
+  return run_norm_bwd(pick_postnorm_bwd(n, dtype, dtype), n, p, num_sms, workspace, dweight, dres_scale, stream);
 }
 
 }  // extern "C"

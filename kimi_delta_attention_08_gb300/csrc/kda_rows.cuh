@@ -189,6 +189,88 @@ __device__ __forceinline__ pair sigmoid(pair x) {
 }
 __device__ __forceinline__ pair silu(pair x) { return pmul(x, sigmoid(x)); }
 
+// V fp32 values that are computed with together: in pairs, or one alone.
+template <int V>
+struct Vals {
+  pair v[V / 2];
+};
+template <>
+struct Vals<1> {
+  float v[1];
+};
+#define KDA_VALS_OP(NAME, PACKED, ONE)                                                     \
+  template <int V>                                                                         \
+  __device__ __forceinline__ Vals<V> NAME(const Vals<V>& a, const Vals<V>& b,              \
+                                          const Vals<V>& c) {                              \
+    Vals<V> r;                                                                             \
+    if constexpr (V == 1) {                                                                \
+      r.v[0] = ONE;                                                                        \
+    } else {                                                                               \
+      _Pragma("unroll") for (int i = 0; i < V / 2; ++i) r.v[i] = PACKED;                   \
+    }                                                                                      \
+    return r;                                                                              \
+  }
+KDA_VALS_OP(fma_of, pfma(a.v[i], b.v[i], c.v[i]), fmaf(a.v[0], b.v[0], c.v[0]))
+KDA_VALS_OP(mul_first, pmul(a.v[i], b.v[i]), a.v[0] * b.v[0])
+#undef KDA_VALS_OP
+template <int V>
+__device__ __forceinline__ Vals<V> mul_of(const Vals<V>& a, const Vals<V>& b) {
+  return mul_first(a, b, b);
+}
+template <int V>
+__device__ __forceinline__ Vals<V> splat(float f) {
+  Vals<V> r;
+  if constexpr (V == 1) {
+    r.v[0] = f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) r.v[i] = pr(f);
+  }
+  return r;
+}
+template <int V>
+__device__ __forceinline__ Vals<V> sigmoid(const Vals<V>& x) {
+  Vals<V> r;
+  if constexpr (V == 1) {
+    r.v[0] = sigmoid(x.v[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) r.v[i] = sigmoid(x.v[i]);
+  }
+  return r;
+}
+template <int V>
+__device__ __forceinline__ float sum_of(const Vals<V>& a) {
+  if constexpr (V == 1) {
+    return a.v[0];
+  } else {
+    pair s = a.v[0];
+#pragma unroll
+    for (int i = 1; i < V / 2; ++i) s = padd(s, a.v[i]);
+    return un(s).x + un(s).y;
+  }
+}
+template <int V>
+__device__ __forceinline__ Vals<V> vals_from(const float (&f)[V]) {
+  Vals<V> r;
+  if constexpr (V == 1) {
+    r.v[0] = f[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) r.v[i] = pr(f[2 * i], f[2 * i + 1]);
+  }
+  return r;
+}
+template <int V>
+__device__ __forceinline__ void vals_to(const Vals<V>& a, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = a.v[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) f[2 * i] = un(a.v[i]).x, f[2 * i + 1] = un(a.v[i]).y;
+  }
+}
+
 // The sequence that holds token t: the largest n with cu[n] <= t (cu sorted), by a
 // search of 32 pivots a step, all lanes of the warp together.  The result lies in
 // [0, N - 1] whatever cu holds; the caller checks the token against its bounds.

@@ -220,10 +220,17 @@ __device__ __forceinline__ void store_state(void* p, int64_t at, const float (&h
 }
 
 // Decay rates in base 2: A2 = -exp(A_log) log2 e, so that exp(-delta exp(A_log)) = 2^(delta A2).
+// exp(v) = 2^(v log2 e) with the product's rounding error put back: 2^e (1 + e' ln 2).
+__device__ __forceinline__ float rate_of(float v) {
+  const float hi = v * kLog2e;
+  const float lo = fmaf(v, 1.925963033500e-8f, fmaf(v, kLog2e, -hi));  // log2 e - kLog2e
+  const float e = ptx::ex2_approx(hi);
+  return -kLog2e * fmaf(e, lo * kLn2, e);
+}
 template <int SP>
 __device__ __forceinline__ void load_rates(float (&a)[SP], const float* A_log, int64_t at) {
 #pragma unroll
-  for (int i = 0; i < SP; ++i) a[i] = -expf(__ldg(A_log + at + i)) * kLog2e;
+  for (int i = 0; i < SP; ++i) a[i] = rate_of(__ldg(A_log + at + i));
 }
 
 // How sequences are cut for a pass over `tiles` channel tiles: not at all with `enough` CTAs

@@ -440,7 +440,7 @@ __global__ void scan_rev_carry_kernel(const ScanParams p, int state) {
   int64_t bos, eos;
   seq_bounds(p, n, bos, eos);
   const int64_t ns = (eos - bos + p.seg_len - 1) / p.seg_len, slot = first_slot(p, n);
-  const float A2 = -expf(__ldg(p.A_log + i)) * kLog2e;
+  const float A2 = rate_of(__ldg(p.A_log + i));
   const int64_t ch = i / state;
   float g = 0.f;
   constexpr int kAhead = 8;

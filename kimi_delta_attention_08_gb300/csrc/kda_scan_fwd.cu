@@ -49,8 +49,9 @@ __global__ void __launch_bounds__(FwdShape<NS>::NT, 5) scan_fwd_kernel(const Sca
   __shared__ __align__(16) pair s_bc[2][2][TB][NS];  // [buffer][B, C]
 
   const int tid = threadIdx.x, lane = tid & 31;
-  const int64_t slot = blockIdx.x / p.tiles;
-  const int tile = (int)(blockIdx.x % p.tiles);
+  const unsigned tiles = (unsigned)p.tiles;
+  const int64_t slot = blockIdx.x / tiles;
+  const int tile = (int)(blockIdx.x % tiles);
   if (blockIdx.x == 0 && tid < 32 && p.status) {
     if (p.cu) check_seqlens(p.cu, p.N, p.total, p.status, kDevStatusBadSeqlens);
     else if (tid == 0) *p.status = 0u;
@@ -244,7 +245,7 @@ __global__ void scan_carry_kernel(const ScanParams p, int state) {
   int64_t bos, eos;
   seq_bounds(p, n, bos, eos);
   const int64_t ns = (eos - bos + p.seg_len - 1) / p.seg_len, slot = first_slot(p, n);
-  const float A2 = -expf(__ldg(p.A_log + i)) * kLog2e;
+  const float A2 = rate_of(__ldg(p.A_log + i));
   float h = 0.f;
   if (p.init)
     h = p.state_bf16 ? to_f(static_cast<const bf16*>(p.init)[n * st_seq + i])
@@ -269,51 +270,97 @@ __global__ void scan_carry_kernel(const ScanParams p, int state) {
   }
 }
 
-// Single tokens and prompts of a few: no staging.  A thread loads its states of one
-// (sequence, channel), walks the tokens and writes the states back; bound by HBM through
-// the states, whose loads and stores are contiguous over the warp.
-template <typename T, int NS>
-__global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
-  constexpr int SP = NS >= 32 ? 8 : 4, LPC = NS / SP;
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i == 0 && p.status) *p.status = 0u;
-  const int64_t per_seq = (int64_t)p.dim * LPC;
-  const bool mine = i < p.N * per_seq;
-  const int n = mine ? (int)(i / per_seq) : p.N - 1;
-  const int64_t r = mine ? i % per_seq : 0;
-  const int64_t ch = r / LPC;
-  const int l = (int)(r % LPC), grp = (int)(ch / p.per);
-  const int64_t st_at = n * (int64_t)p.dim * NS + ch * NS + l * SP;
-  float A2[SP], h[SP];
+// Single tokens and prompts of a few: bound by HBM through the states.  A thread holds 4
+// states of a channel (a warp's lie in a row) for kStepSeqs sequences, whose states are all
+// in flight at once.  Of these sequences each of a channel's lanes owns OWN: it reads their
+// rows, computes their steps, hands those to the others, ends up with their dot products
+// and writes their outputs.  (One thread for all 16 states of a channel computes as little
+// but reads 64 bytes apart: 36.8 us for 256 sequences of 4,096 channels.)
+constexpr int kStepSeqs = 4;
+constexpr int kStepTokens = 8;  // the longest such prompt
+
+template <typename T, int NS, bool VEC>
+__global__ void __launch_bounds__(128, 8) scan_step_kernel(const ScanParams p) {
+  constexpr int SP = 4, LPC = NS / SP, OWN = LPC >= 4 ? 1 : 2, OWNERS = kStepSeqs / OWN;
+  const int lane = threadIdx.x & 31;
+  const unsigned tiles = (unsigned)p.tiles;  // 32-bit divisions: 64-bit ones cost as much as a token
+  const unsigned i = blockIdx.x % tiles * blockDim.x + threadIdx.x;
+  const int n0 = (int)(blockIdx.x / tiles) * kStepSeqs;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) *p.status = 0u;
+  const bool mine = i / LPC < (unsigned)p.dim;
+  const int ch = mine ? (int)(i / LPC) : 0, l = (int)(i % LPC);
+  const int grp = p.groups == 1 ? 0 : ch / p.per;
+  const int first = l % OWNERS * OWN;  // the sequences it owns
+  const int64_t st_at = (int64_t)ch * NS + l * SP, st_seq = (int64_t)p.dim * NS;
+  pair h[kStepSeqs][2], A2[2];
 #pragma unroll
-  for (int k = 0; k < SP; ++k) h[k] = 0.f;
-  if (p.init && mine) load_state<SP>(h, p.init, st_at, p.state_bf16);
-  load_rates<SP>(A2, p.A_log, ch * NS + l * SP);
+  for (int q = 0; q < kStepSeqs; ++q) {
+    float v[SP] = {};
+    if (p.init && n0 + q < p.N) load_state<SP>(v, p.init, (n0 + q) * st_seq + st_at, p.state_bf16);
+    h[q][0] = pr(v[0], v[1]), h[q][1] = pr(v[2], v[3]);
+  }
+  {
+    float a[SP];
+    load_rates<SP>(a, p.A_log, st_at);
+    A2[0] = pr(a[0], a[1]), A2[1] = pr(a[2], a[3]);
+  }
   const float bias = p.dt_bias ? __ldg(p.dt_bias + ch) : 0.f, D = p.D ? __ldg(p.D + ch) : 0.f;
-  for (int64_t t = n * p.T; t < (n + 1) * p.T; ++t) {
-    const float x = to_f(static_cast<const T*>(p.x)[t * p.x_s + ch]);
-    float ex;
-    const float d = softplus(to_f(static_cast<const T*>(p.dt)[t * p.dt_s + ch]) + bias, ex);
-    const T* B = static_cast<const T*>(p.B) + t * p.b_s + grp * NS + l * SP;
-    const T* C = static_cast<const T*>(p.C) + t * p.c_s + grp * NS + l * SP;
-    float y = 0.f;
+  const int T_ = (int)p.T;
+  for (int j = 0; j < T_; ++j) {
+    float x[OWN], v[OWN], z[OWN], delta[OWN], dx[OWN];
+    Raw<T, SP> rb[kStepSeqs], rc[kStepSeqs];
 #pragma unroll
-    for (int k = 0; k < SP; ++k) {
-      h[k] = fmaf(ptx::ex2_approx(d * A2[k]), h[k], d * x * to_f(B[k]));
-      y = fmaf(to_f(C[k]), h[k], y);
+    for (int k = 0; k < OWN; ++k) {
+      const int64_t t = (int64_t)min(n0 + first + k, p.N - 1) * T_ + j;
+      x[k] = to_f(static_cast<const T*>(p.x)[t * p.x_s + ch]);
+      v[k] = to_f(static_cast<const T*>(p.dt)[t * p.dt_s + ch]) + bias;
+      z[k] = p.z ? to_f(static_cast<const T*>(p.z)[t * p.z_s + ch]) : 0.f;
     }
 #pragma unroll
-    for (int o = 1; o < LPC; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (l == 0 && mine) {
-      y = fmaf(D, x, y);
-      if (p.z) {
-        const float z = to_f(static_cast<const T*>(p.z)[t * p.z_s + ch]);
-        y *= z * sigmoid(z);
-      }
-      static_cast<T*>(p.out)[t * p.dim + ch] = from_f<T>(y);
+    for (int q = 0; q < kStepSeqs; ++q) {
+      const int64_t t = (int64_t)min(n0 + q, p.N - 1) * T_ + j;
+      load_row<T, SP, VEC>(rb[q], static_cast<const T*>(p.B) + t * p.b_s + grp * NS + l * SP, 1, SP);
+      load_row<T, SP, VEC>(rc[q], static_cast<const T*>(p.C) + t * p.c_s + grp * NS + l * SP, 1, SP);
+    }
+#pragma unroll
+    for (int k = 0; k < OWN; ++k) {
+      float ex;
+      delta[k] = softplus(v[k], ex);
+      dx[k] = delta[k] * x[k];
+    }
+    float y[kStepSeqs];
+#pragma unroll
+    for (int q = 0; q < kStepSeqs; ++q) {
+      const int from = (lane & ~(OWNERS - 1)) | q / OWN;
+      const pair d = pr(__shfl_sync(0xffffffffu, delta[q % OWN], from));
+      const pair m = pr(__shfl_sync(0xffffffffu, dx[q % OWN], from));
+      float b[SP], c[SP];
+      unpack(rb[q], b);
+      unpack(rc[q], c);
+      h[q][0] = advance(h[q][0], A2[0], d, m, pr(b[0], b[1]));
+      h[q][1] = advance(h[q][1], A2[1], d, m, pr(b[2], b[3]));
+      const float2 s = un(pfma(pr(c[2], c[3]), h[q][1], pmul(pr(c[0], c[1]), h[q][0])));
+      y[q] = s.x + s.y;
+    }
+    int off = 0;  // first
+    reduce_scatter<kStepSeqs, OWNERS / 2, 1>(y, lane, off);
+#pragma unroll
+    for (int k = 0; k < OWN; ++k) {
+#pragma unroll
+      for (int o = OWNERS; o < LPC; o <<= 1) y[k] += __shfl_xor_sync(0xffffffffu, y[k], o);
+      y[k] = fmaf(D, x[k], y[k]);
+      if (p.z) y[k] *= z[k] * sigmoid(z[k]);
+      const int n = n0 + first + k;
+      if (mine && l < OWNERS && n < p.N)
+        static_cast<T*>(p.out)[((int64_t)n * T_ + j) * p.dim + ch] = from_f<T>(y[k]);
     }
   }
-  if (p.fin && mine) store_state<SP>(p.fin, st_at, h, p.state_bf16);
+  if (!p.fin || !mine) return;
+#pragma unroll
+  for (int q = 0; q < kStepSeqs; ++q) {
+    const float v[SP] = {un(h[q][0]).x, un(h[q][0]).y, un(h[q][1]).x, un(h[q][1]).y};
+    if (n0 + q < p.N) store_state<SP>(p.fin, (n0 + q) * st_seq + st_at, v, p.state_bf16);
+  }
 }
 
 template <typename T, bool VEC, bool OUT>
@@ -340,23 +387,21 @@ cudaError_t launch_pass(const ScanParams& p, int state, bool f32, bool vec, cuda
              : launch_main<bf16, false, OUT>(p, state, stream);
 }
 
-template <typename T>
-cudaError_t launch_step(const ScanParams& p, int state, cudaStream_t stream) {
-  const int lpc = state >= 32 ? state / 8 : state / 4;
-  const int64_t grid = ((int64_t)p.N * p.dim * lpc + 255) / 256;
+template <typename T, bool VEC>
+cudaError_t launch_step(ScanParams p, int state, cudaStream_t stream) {
+  p.tiles = ((int64_t)p.dim * (state / 4) + 127) / 128;
+  const int64_t grid = p.tiles * (((int64_t)p.N + kStepSeqs - 1) / kStepSeqs);
   if (grid == 0) return cudaSuccess;
   if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   const unsigned g = (unsigned)grid;
   switch (state) {
-    case 8: scan_step_kernel<T, 8><<<g, 256, 0, stream>>>(p); break;
-    case 16: scan_step_kernel<T, 16><<<g, 256, 0, stream>>>(p); break;
-    case 32: scan_step_kernel<T, 32><<<g, 256, 0, stream>>>(p); break;
-    default: scan_step_kernel<T, 64><<<g, 256, 0, stream>>>(p); break;
+    case 8: scan_step_kernel<T, 8, VEC><<<g, 128, 0, stream>>>(p); break;
+    case 16: scan_step_kernel<T, 16, VEC><<<g, 128, 0, stream>>>(p); break;
+    case 32: scan_step_kernel<T, 32, VEC><<<g, 128, 0, stream>>>(p); break;
+    default: scan_step_kernel<T, 64, VEC><<<g, 128, 0, stream>>>(p); break;
   }
   return cudaGetLastError();
 }
-
-constexpr int kStepTokens = 8;  // longest prompt of the single-token kernel
 
 bool al_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -552,7 +597,10 @@ kda_status kda_scan_fwd(const kda_scan_problem* problem, void* out, void* final_
   vec = vec && al_to(out, 16);
   cudaError_t e;
   if (step)
-    e = f32 ? launch_step<float>(p, state, stream) : launch_step<bf16>(p, state, stream);
+    e = f32 ? (vec ? launch_step<float, true>(p, state, stream)
+                   : launch_step<float, false>(p, state, stream))
+            : (vec ? launch_step<scan::bf16, true>(p, state, stream)
+                   : launch_step<scan::bf16, false>(p, state, stream));
   else
     e = scan::launch_scan_fwd(p, state, f32, vec, true, stream);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;

@@ -36,16 +36,18 @@ def _row_dtype(t, name):
 
 
 def _need(t, name, dtype, dev, shape):
-    """A contiguous tensor of this dtype, device and shape."""
+    """The pointer of a contiguous tensor of this dtype, device and shape."""
+    if t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype} (no implicit conversion)")
     if t.device != dev:
         raise ValueError(f"{name}: expected device {dev}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous (no implicit copy)")
-    return t.data_ptr()
+    raise ValueError(f"{name}: must be contiguous (no implicit copy)")
 
 
 def _opt(t, name, dtype, dev, shape):
@@ -83,42 +85,51 @@ def _seqlens(cu, dev, B):
     return cu.data_ptr(), cu.numel() - 1
 
 
-class _On:
-    """The stream to enqueue on, with the tensors' device current while it is used."""
+# The current stream's handle without a Stream object, where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    __slots__ = ("handle", "guard", "own")
 
-    def __init__(self, dev, stream):
+def _call(name, dev, stream, *args):
+    """The library's `name` with these arguments and the stream, the tensors' device current."""
+    if dev.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    fn = getattr(_lib.load(), name)
+    if stream is None:
+        handle = _raw_stream(dev.index)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status != KDA_OK:
+        _raise(status, name)
+
+
+def _workspace(given, size, dev, stream):
+    """(tensor, pointer, bytes): the caller's workspace, or one of size() bytes from torch's
+    allocator that lives as long as the work on this call's stream."""
+    if given is None:
         if dev.type != "cuda":
             raise ValueError("expected CUDA tensors")
-        self.guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-        self.own = stream
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        self.handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def workspace(self, given, size, dev):
-        """The caller's workspace, or one from torch's allocator that lives as long as the
-        work on this call's stream."""
-        if given is not None:
-            if given.dtype != torch.uint8 or given.device != dev or not given.is_contiguous():
-                raise ValueError("workspace: expected a contiguous uint8 tensor on the tensors' device")
-            return given
-        if self.own is not None and not isinstance(self.own, torch.cuda.Stream):
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
             raise ValueError("workspace: required with a raw stream handle")
-        ws = torch.empty(size, dtype=torch.uint8, device=dev)
-        if self.own is not None:
-            ws.record_stream(self.own)
-        return ws
+        given = torch.empty(size(), dtype=torch.uint8, device=dev)
+        if stream is not None:
+            given.record_stream(stream)
+    elif given.dtype != torch.uint8 or given.device != dev or not given.is_contiguous():
+        raise ValueError("workspace: expected a contiguous uint8 tensor on the tensors' device")
+    return given, given.data_ptr(), given.numel()
+
+
+def _results(stream, grads):
+    """New tensors that another stream than the current one writes live until it has."""
+    if isinstance(stream, torch.cuda.Stream):
+        for t in grads.values():
+            t.record_stream(stream)
+    return grads
 
 
 def _size(fn, *args):
@@ -189,12 +200,9 @@ def kda_conv_fwd(x, weight, bias, out, initial_state=None, final_state=None, cu_
     st = (N, W - 1, C)
     ip = _opt(initial_state, "initial_state", x.dtype, dev, st)
     fp = _opt(final_state, "final_state", x.dtype, dev, st)
-    with _On(dev, stream) as handle:
-        s = _lib.load().kda_conv_fwd(xp, xs, w, b, ptrs, counts, k, ip, fp, cu, B, T, C, N, W, fn,
-                                     dt, None if workspace is None else workspace.data_ptr(),
-                                     0 if workspace is None else workspace.numel(), handle)
-    if s != KDA_OK:
-        _raise(s, "kda_conv_fwd")
+    wp, wb = (None, 0) if workspace is None else _workspace(workspace, None, dev, stream)[1:]
+    _call("kda_conv_fwd", dev, stream, xp, xs, w, b, ptrs, counts, k, ip, fp, cu, B, T, C, N, W, fn,
+          dt, wp, wb)
 
 
 def make_conv_bwd_workspace(total_tokens, C, width, device=None):
@@ -218,23 +226,19 @@ def kda_conv_bwd(x, weight, bias, dout, initial_state=None, dfinal_state=None, c
     st = (N, W - 1, C)
     ip = _opt(initial_state, "initial_state", x.dtype, dev, st)
     dfp = _opt(dfinal_state, "dfinal_state", x.dtype, dev, st)
-    on = _On(dev, stream)
-    with on as handle:
-        ws = on.workspace(workspace, _size("kda_conv_bwd_get_workspace_size", B * T, C, W), dev)
-        g = {"dx": torch.empty((B, T, C), dtype=x.dtype, device=dev),
-             "dweight": torch.empty((C, W), dtype=_f32, device=dev)}
-        if b is not None:
-            g["dbias"] = torch.empty((C,), dtype=_f32, device=dev)
-        if ip is not None:
-            g["dinitial_state"] = torch.empty(st, dtype=_f32, device=dev)
-        P = lambda nm: g[nm].data_ptr() if nm in g else None
-        s = _lib.load().kda_conv_bwd(xp, xs, w, b, ptrs, counts, k, ddt, ip, dfp, cu, P("dx"),
-                                     P("dweight"), P("dbias"), P("dinitial_state"), B, T, C, N, W,
-                                     fn, dt, ws.data_ptr(), ws.numel(), handle)
-    if s != KDA_OK:
-        _raise(s, "kda_conv_bwd")
+    ws, wp, wb = _workspace(workspace, lambda: _size("kda_conv_bwd_get_workspace_size", B * T, C, W),
+                            dev, stream)
+    g = {"dx": torch.empty((B, T, C), dtype=x.dtype, device=dev),
+         "dweight": torch.empty((C, W), dtype=_f32, device=dev)}
+    if b is not None:
+        g["dbias"] = torch.empty((C,), dtype=_f32, device=dev)
+    if ip is not None:
+        g["dinitial_state"] = torch.empty(st, dtype=_f32, device=dev)
+    P = lambda nm: g[nm].data_ptr() if nm in g else None
+    _call("kda_conv_bwd", dev, stream, xp, xs, w, b, ptrs, counts, k, ddt, ip, dfp, cu, P("dx"),
+          P("dweight"), P("dbias"), P("dinitial_state"), B, T, C, N, W, fn, dt, wp, wb)
     g["workspace"] = ws
-    return g
+    return _results(stream, g)
 
 
 # --------------------------------------------------------------------- scan --
@@ -320,16 +324,11 @@ def kda_scan_fwd(x, dt, A_log, B, C, out, D=None, z=None, dt_bias=None, initial_
     dev = x.device
     op = _need(out, "out", x.dtype, dev, x.shape)
     cp, cb = _states_arg(chunk_states, dev)
-    lib = _lib.load()
-    on = _On(dev, stream)
-    with on as handle:
-        wp = wb = 0
-        if workspace is not None or q.T > 8 or q.cu_seqlens or cp:
-            ws = on.workspace(workspace, _size("kda_scan_get_workspace_size", ctypes.byref(q)), dev)
-            wp, wb = ws.data_ptr(), ws.numel()
-        s = lib.kda_scan_fwd(ctypes.byref(q), op, fp, cp, cb, wp, wb, handle)
-    if s != KDA_OK:
-        _raise(s, "kda_scan_fwd")
+    wp = wb = 0
+    if workspace is not None or q.T > 8 or q.cu_seqlens or cp:
+        _, wp, wb = _workspace(workspace, lambda: _size("kda_scan_get_workspace_size", ctypes.byref(q)),
+                               dev, stream)
+    _call("kda_scan_fwd", dev, stream, ctypes.byref(q), op, fp, cp, cb, wp, wb)
 
 
 def kda_scan_bwd(x, dt, A_log, B, C, dout, D=None, z=None, dt_bias=None, initial_state=None,
@@ -344,30 +343,24 @@ def kda_scan_bwd(x, dt, A_log, B, C, dout, D=None, z=None, dt_bias=None, initial
     dev, ty = x.device, x.dtype
     dop = _need(dout, "dout", ty, dev, x.shape)
     cp, cb = _states_arg(chunk_states, dev)
-    lib = _lib.load()
-    on = _On(dev, stream)
-    with on as handle:
-        ws = on.workspace(workspace, _size("kda_scan_bwd_get_workspace_size", ctypes.byref(q),
-                                           int(cp is not None)), dev)
-        E = lambda shape, t=_f32: torch.empty(shape, dtype=t, device=dev)
-        g = {"dx": E(x.shape, ty), "ddt": E(x.shape, ty), "dB": E(B.shape, ty), "dC": E(B.shape, ty),
-             "dA_log": E(A_log.shape)}
-        if z is not None:
-            g["dz"] = E(x.shape, ty)
-        if D is not None:
-            g["dD"] = E((q.dim,))
-        if dt_bias is not None:
-            g["ddt_bias"] = E((q.dim,))
-        if initial_state is not None:
-            g["dinitial_state"] = E(initial_state.shape)
-        P = lambda nm: g[nm].data_ptr() if nm in g else None
-        s = lib.kda_scan_bwd(ctypes.byref(q), dop, dfp, cp, cb, P("dx"), P("ddt"), P("dz"), P("dB"),
-                             P("dC"), P("dA_log"), P("dD"), P("ddt_bias"), P("dinitial_state"),
-                             ws.data_ptr(), ws.numel(), handle)
-    if s != KDA_OK:
-        _raise(s, "kda_scan_bwd")
+    ws, wp, wb = _workspace(workspace, lambda: _size("kda_scan_bwd_get_workspace_size",
+                                                     ctypes.byref(q), int(cp is not None)), dev, stream)
+    E = lambda shape, t=_f32: torch.empty(shape, dtype=t, device=dev)
+    g = {"dx": E(x.shape, ty), "ddt": E(x.shape, ty), "dB": E(B.shape, ty), "dC": E(B.shape, ty),
+         "dA_log": E(A_log.shape)}
+    if z is not None:
+        g["dz"] = E(x.shape, ty)
+    if D is not None:
+        g["dD"] = E((q.dim,))
+    if dt_bias is not None:
+        g["ddt_bias"] = E((q.dim,))
+    if initial_state is not None:
+        g["dinitial_state"] = E(initial_state.shape)
+    P = lambda nm: g[nm].data_ptr() if nm in g else None
+    _call("kda_scan_bwd", dev, stream, ctypes.byref(q), dop, dfp, cp, cb, P("dx"), P("ddt"), P("dz"),
+          P("dB"), P("dC"), P("dA_log"), P("dD"), P("ddt_bias"), P("dinitial_state"), wp, wb)
     g["workspace"] = ws
-    return g
+    return _results(stream, g)
 
 
 # -------------------------------------------------------------------- norms --
@@ -386,15 +379,10 @@ def kda_prenorm_fwd(x, residual, weight, out, residual_out=None, *, res_scale=1.
     sdt = dt if stream_t is None else _row_dtype(stream_t, "residual")
     sty = x.dtype if stream_t is None else stream_t.dtype
     sp, sv = _scale_args(res_scale, dev, D)
-    with _On(dev, stream) as handle:
-        s = _lib.load().kda_prenorm_fwd(
-            xp, _opt(residual, "residual", sty, dev, shape),
-            _need(weight, "weight", _f32, dev, (D,)), sp, sv, eps,
-            _need(out, "out", x.dtype, dev, shape),
-            _opt(residual_out, "residual_out", sty, dev, shape), x.numel() // D if D else 0, D, dt,
-            sdt, handle)
-    if s != KDA_OK:
-        _raise(s, "kda_prenorm_fwd")
+    _call("kda_prenorm_fwd", dev, stream, xp, _opt(residual, "residual", sty, dev, shape),
+          _need(weight, "weight", _f32, dev, (D,)), sp, sv, eps,
+          _need(out, "out", x.dtype, dev, shape),
+          _opt(residual_out, "residual_out", sty, dev, shape), x.numel() // D if D else 0, D, dt, sdt)
 
 
 def make_norm_bwd_workspace(rows, dim, device=None):
@@ -416,27 +404,22 @@ def kda_prenorm_bwd(dout, dresidual_out, h, weight, x=None, workspace=None, *, r
     if sp is not None and x is None:
         raise ValueError("x: needed for the gradient of a per-channel res_scale")
     rows = dout.numel() // D if D else 0
-    on = _On(dev, stream)
-    with on as handle:
-        ws = on.workspace(workspace, _size("kda_norm_bwd_get_workspace_size", rows, D), dev)
-        g = {"dresidual": torch.empty(shape, dtype=h.dtype, device=dev),
-             "dweight": torch.empty((D,), dtype=_f32, device=dev)}
-        same = sp is None and sv == 1.0 and dt == sdt
-        g["dx"] = g["dresidual"] if same else torch.empty(shape, dtype=dout.dtype, device=dev)
-        if sp is not None:
-            g["dres_scale"] = torch.empty((D,), dtype=_f32, device=dev)
-        s = _lib.load().kda_prenorm_bwd(
-            _need(dout, "dout", dout.dtype, dev, shape),
-            _opt(dresidual_out, "dresidual_out", h.dtype, dev, shape),
-            _need(h, "h", h.dtype, dev, shape), _need(weight, "weight", _f32, dev, (D,)),
-            None if sp is None else _need(x, "x", dout.dtype, dev, shape), sp, sv, eps,
-            None if same else g["dx"].data_ptr(), g["dresidual"].data_ptr(),
-            g["dweight"].data_ptr(), None if sp is None else g["dres_scale"].data_ptr(), rows, D,
-            dt, sdt, ws.data_ptr(), ws.numel(), handle)
-    if s != KDA_OK:
-        _raise(s, "kda_prenorm_bwd")
+    ws, wp, wb = _workspace(workspace, lambda: _size("kda_norm_bwd_get_workspace_size", rows, D), dev,
+                            stream)
+    g = {"dresidual": torch.empty(shape, dtype=h.dtype, device=dev),
+         "dweight": torch.empty((D,), dtype=_f32, device=dev)}
+    same = sp is None and sv == 1.0 and dt == sdt
+    g["dx"] = g["dresidual"] if same else torch.empty(shape, dtype=dout.dtype, device=dev)
+    if sp is not None:
+        g["dres_scale"] = torch.empty((D,), dtype=_f32, device=dev)
+    _call("kda_prenorm_bwd", dev, stream, _need(dout, "dout", dout.dtype, dev, shape),
+          _opt(dresidual_out, "dresidual_out", h.dtype, dev, shape),
+          _need(h, "h", h.dtype, dev, shape), _need(weight, "weight", _f32, dev, (D,)),
+          None if sp is None else _need(x, "x", dout.dtype, dev, shape), sp, sv, eps,
+          None if same else g["dx"].data_ptr(), g["dresidual"].data_ptr(), g["dweight"].data_ptr(),
+          None if sp is None else g["dres_scale"].data_ptr(), rows, D, dt, sdt, wp, wb)
     g["workspace"] = ws
-    return g
+    return _results(stream, g)
 
 
 def _gate_args(gate, x, dev):
@@ -462,14 +445,11 @@ def kda_postnorm_fwd(x, weight, gate, out, residual=None, *, res_scale=1.0, acti
         raise ValueError(f"activation must be one of {list(GATE_ACTIVATIONS)}")
     gp, gs, heads = _gate_args(gate, x, dev)
     sp, sv = _scale_args(res_scale, dev, D)
-    with _On(dev, stream) as handle:
-        s = _lib.load().kda_postnorm_fwd(
-            _need(x, "x", x.dtype, dev, shape), _need(weight, "weight", _f32, dev, (D,)), gp, gs,
-            heads, _opt(residual, "residual", x.dtype, dev, shape), sp, sv, eps,
-            GATE_ACTIVATIONS[activation], _need(out, "out", x.dtype, dev, shape),
-            x.numel() // D if D else 0, D, dt, handle)
-    if s != KDA_OK:
-        _raise(s, "kda_postnorm_fwd")
+    _call("kda_postnorm_fwd", dev, stream, _need(x, "x", x.dtype, dev, shape),
+          _need(weight, "weight", _f32, dev, (D,)), gp, gs, heads,
+          _opt(residual, "residual", x.dtype, dev, shape), sp, sv, eps,
+          GATE_ACTIVATIONS[activation], _need(out, "out", x.dtype, dev, shape),
+          x.numel() // D if D else 0, D, dt)
 
 
 def kda_postnorm_bwd(dout, x, weight, gate=None, workspace=None, *, res_scale=1.0,
@@ -484,23 +464,18 @@ def kda_postnorm_bwd(dout, x, weight, gate=None, workspace=None, *, res_scale=1.
     gp, gs, heads = _gate_args(gate, x, dev)
     sp, sv = _scale_args(res_scale, dev, D)
     rows = x.numel() // D if D else 0
-    on = _On(dev, stream)
-    with on as handle:
-        ws = on.workspace(workspace, _size("kda_norm_bwd_get_workspace_size", rows, D), dev)
-        g = {"dx": torch.empty(shape, dtype=x.dtype, device=dev),
-             "dweight": torch.empty((D,), dtype=_f32, device=dev)}
-        if gate is not None:
-            g["dgate"] = torch.empty(shape, dtype=x.dtype, device=dev)
-        if sp is not None:
-            g["dres_scale"] = torch.empty((D,), dtype=_f32, device=dev)
-        s = _lib.load().kda_postnorm_bwd(
-            _need(dout, "dout", x.dtype, dev, shape), _need(x, "x", x.dtype, dev, shape),
-            _need(weight, "weight", _f32, dev, (D,)), gp, gs, heads, sp, sv, eps,
-            GATE_ACTIVATIONS[activation], g["dx"].data_ptr(),
-            None if gate is None else g["dgate"].data_ptr(), g["dweight"].data_ptr(),
-            None if sp is None else g["dres_scale"].data_ptr(), rows, D, dt, ws.data_ptr(),
-            ws.numel(), handle)
-    if s != KDA_OK:
-        _raise(s, "kda_postnorm_bwd")
+    ws, wp, wb = _workspace(workspace, lambda: _size("kda_norm_bwd_get_workspace_size", rows, D), dev,
+                            stream)
+    g = {"dx": torch.empty(shape, dtype=x.dtype, device=dev),
+         "dweight": torch.empty((D,), dtype=_f32, device=dev)}
+    if gate is not None:
+        g["dgate"] = torch.empty(shape, dtype=x.dtype, device=dev)
+    if sp is not None:
+        g["dres_scale"] = torch.empty((D,), dtype=_f32, device=dev)
+    _call("kda_postnorm_bwd", dev, stream, _need(dout, "dout", x.dtype, dev, shape),
+          _need(x, "x", x.dtype, dev, shape), _need(weight, "weight", _f32, dev, (D,)), gp, gs, heads,
+          sp, sv, eps, GATE_ACTIVATIONS[activation], g["dx"].data_ptr(),
+          None if gate is None else g["dgate"].data_ptr(), g["dweight"].data_ptr(),
+          None if sp is None else g["dres_scale"].data_ptr(), rows, D, dt, wp, wb)
     g["workspace"] = ws
-    return g
+    return _results(stream, g)
