@@ -897,7 +897,8 @@ kda_status kda_conv_bwd(const void* x, int64_t x_stride, const float* weight, co
   } else if (cudaMemsetAsync(p.status, 0, 4, stream) != cudaSuccess) {
     return KDA_ERR_CUDA;
   }
-  if (launch_column_sums(p.part, blocks, (int64_t)(width + 1) * C, (int64_t)width * C, C,
+  if (launch_column_sums(p.part, blocks, (int64_t)(width + 1) * C, (int64_t)(width + 1) * C,
+                         (int64_t)width * C, C,
                          dweight, dbias, nullptr, stream) != cudaSuccess)
     return KDA_ERR_CUDA;
   return KDA_OK;

@@ -346,15 +346,15 @@ __global__ void __launch_bounds__(norm_threads(G, E, V), G || E > 1 ? 1 : 2) pos
 
 // A block per 32 columns: 32 row groups add every 32nd row, then their sums are added
 // in order.
-__global__ void column_sums_kernel(const float* part, int64_t rows, int64_t cols, int64_t n0,
-                                   int64_t n1, float* out0, float* out1, float* out2) {
+__global__ void column_sums_kernel(const float* part, int64_t rows, int64_t pitch, int64_t cols,
+                                   int64_t n0, int64_t n1, float* out0, float* out1, float* out2) {
   __shared__ float sums[32][33];
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int64_t e = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.f;
   if (e < cols) {
 #pragma unroll 4
-    for (int64_t r = grp; r < rows; r += 32) s += part[r * cols + e];
+    for (int64_t r = grp; r < rows; r += 32) s += part[r * pitch + e];
   }
   sums[grp][lane] = s;
   __syncthreads();
@@ -463,8 +463,9 @@ kda_status run_norm_bwd(NormKernel kernel, const NormPlan& n, NormParams& p, int
     const kda_status st = run_norm(kernel, n, p, grid, smem, stream);
     if (st != KDA_OK) return st;
   }
-  return launch_column_sums(p.part, grid, (p.want_scale ? 2 : 1) * (int64_t)p.dim, p.dim, p.dim,
-                            dweight, dscale, nullptr, stream) ==
+  return launch_column_sums(p.part, grid, (p.want_scale ? 2 : 1) * (int64_t)p.dim,
+                            (p.want_scale ? 2 : 1) * (int64_t)p.dim, p.dim, p.dim, dweight, dscale,
+                            nullptr, stream) ==
                  cudaSuccess
              ? KDA_OK
              : KDA_ERR_CUDA;
@@ -472,11 +473,11 @@ kda_status run_norm_bwd(NormKernel kernel, const NormPlan& n, NormParams& p, int
 
 }  // namespace
 
-cudaError_t launch_column_sums(const float* part, int64_t rows, int64_t cols, int64_t n0,
-                               int64_t n1, float* out0, float* out1, float* out2,
+cudaError_t launch_column_sums(const float* part, int64_t rows, int64_t pitch, int64_t cols,
+                               int64_t n0, int64_t n1, float* out0, float* out1, float* out2,
                                cudaStream_t stream) {
   if (cols <= 0) return cudaSuccess;
-  column_sums_kernel<<<(unsigned)((cols + 31) / 32), 1024, 0, stream>>>(part, rows, cols, n0, n1,
+  column_sums_kernel<<<(unsigned)((cols + 31) / 32), 1024, 0, stream>>>(part, rows, pitch, cols, n0, n1,
                                                                        out0, out1, out2);
   return cudaGetLastError();
 }

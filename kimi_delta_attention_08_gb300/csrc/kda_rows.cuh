@@ -304,10 +304,10 @@ __device__ __forceinline__ void check_seqlens(const int64_t* cu, int N, int64_t 
 
 }  // namespace rows
 
-// out[e] = sum over r < rows of part[r][e] in a fixed order: the first n0 columns go to
+// out[e] = sum over r < rows of part[r * pitch + e] in a fixed order: the first n0 columns go to
 // out0, the next n1 to out1, the rest to out2 (a null output drops its columns).
-cudaError_t launch_column_sums(const float* part, int64_t rows, int64_t cols, int64_t n0,
-                               int64_t n1, float* out0, float* out1, float* out2,
+cudaError_t launch_column_sums(const float* part, int64_t rows, int64_t pitch, int64_t cols,
+                               int64_t n0, int64_t n1, float* out0, float* out1, float* out2,
                                cudaStream_t stream);
 
 }  // namespace kda

@@ -256,5 +256,9 @@ void carve_fwd(ScanParams& p, int state, void* ws);
 cudaError_t launch_scan_fwd(ScanParams p, int state, bool f32, bool vec, bool out,
                             cudaStream_t stream);
 
+// The gradient that leaves each segment at its start, from a zero gradient at its end (the
+// last one's: dfinal_state), into p.seg_state, and its sum of delta.
+cudaError_t launch_scan_rev(ScanParams p, int state, bool f32, bool vec, cudaStream_t stream);
+
 }  // namespace scan
 }  // namespace kda

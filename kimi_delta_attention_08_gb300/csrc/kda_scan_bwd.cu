@@ -30,44 +30,55 @@ namespace {
 
 using namespace scan;
 
-constexpr int kRevCh = 32;
+// Floats of a slot's row of partial sums [dim][state], [dim], [dim]: whole 16-byte units.
+__host__ __device__ __forceinline__ int64_t par_pitch(int64_t dim, int state) {
+  return (dim * (state + 2) + 3) / 4 * 4;
+}
 
-template <int NS>
-constexpr int kStates = NS >= 32 ? 8 : 4;
-template <int NS>
-constexpr int kBwdCh = NS == 64 ? 32 : 64;
-
+// A thread holds SP states of two neighbouring channels, as pairs.
 template <typename T, int NS>
 struct BwdShape {
-  static constexpr int CH = kBwdCh<NS>;
-  static constexpr int SP = kStates<NS>, LPC = NS / SP, NT = CH * LPC, NW = NT / 32;
-  static constexpr int SB = 32 / SP, NSB = kScanBlock / SB;   // tokens per piece, pieces
-  static constexpr int CL = 32 / LPC;                         // channels per warp
+  static constexpr int SP = 4, LPC = NS / SP, NT = NS >= 32 ? 256 : 128, NW = NT / 32;
+  static constexpr int CL = 32 / LPC;                         // channel pairs per warp
+  static constexpr int CH = 2 * CL * NW;                      // channels per CTA
+  static constexpr int SB = 4, NSB = kScanBlock / SB;         // tokens per piece, pieces
   static constexpr int EPT = kScanBlock * CH / NT, SV = EPT < 8 ? EPT : 8, SN = EPT / SV;
   static constexpr int PER_ROW = CH / SV;
+  static constexpr int BV = kScanBlock * NS / NT;             // of B and of C staged per thread
   // shared memory, in floats
-  static constexpr int DX = 0;                                // float2 [32][CH]: delta, delta x,
-                                                              // then q and s of done tokens
+  static constexpr int DX = 0;                                // [32][CH / 2] of (delta, delta',
+                                                              // delta x, delta' x'), then (q, q',
+                                                              // s, s') of done tokens
   static constexpr int DY = DX + 2 * kScanBlock * CH;         // [32][CH]: dy, then y
-  static constexpr int SB_ = DY + kScanBlock * CH;            // B [32][NS]
-  static constexpr int SC_ = SB_ + kScanBlock * NS;           // C [32][NS]
-  static constexpr int PART = SC_ + kScanBlock * NS;          // [NW][SB][2 NS]
-  static constexpr int CKPT = PART + NW * SB * 2 * NS;        // [NSB - 1][NT][SP]
-  static constexpr int FLOATS = CKPT + (NSB - 1) * NT * SP;
+  static constexpr int SB_ = DY + kScanBlock * CH;            // B [32][NS], each value twice
+  static constexpr int SC_ = SB_ + 2 * kScanBlock * NS;       // C
+  static constexpr int PART = SC_ + 2 * kScanBlock * NS;      // [NW][SB][2 NS]
+  static constexpr int CKPT = PART + NW * SB * 2 * NS;        // [NSB - 1][2][NT] of 4
+  static constexpr int SUMA = CKPT + (NSB - 1) * 2 * 4 * NT;  // [2][NT] of 4
+  static constexpr int FLOATS = SUMA + 2 * 4 * NT;
 };
 
+// Where the 16 bytes of a channel pair lie in a token's row of DX: exchanged within groups
+// of four, so that the staging writes (neighbouring lanes 64 bytes apart, two rows in 8
+// lanes) use every bank once, as the reads do anyway.
+__device__ __forceinline__ int pair_unit(int tok, int u) {
+  return u ^ ((u >> 3 & 1) | (tok & 1) << 1);
+}
+
 template <typename T, int NS, bool VEC>
-__global__ void __launch_bounds__(BwdShape<T, NS>::NT, 2) scan_bwd_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(BwdShape<T, NS>::NT, 384 / BwdShape<T, NS>::NT)
+    scan_bwd_kernel(const ScanParams p) {
   using H = BwdShape<T, NS>;
   constexpr int CH = H::CH, SP = H::SP, LPC = H::LPC, NT = H::NT, NW = H::NW, SB = H::SB;
-  constexpr int NSB = H::NSB, SV = H::SV, SN = H::SN, PER_ROW = H::PER_ROW;
+  constexpr int CL = H::CL, SV = H::SV, SN = H::SN, PER_ROW = H::PER_ROW, BV = H::BV;
   extern __shared__ __align__(16) float sm[];
-  float2(*s_dx)[CH] = reinterpret_cast<float2(*)[CH]>(sm + H::DX);
+  float4(*s_dx)[CH / 2] = reinterpret_cast<float4(*)[CH / 2]>(sm + H::DX);
   float(*s_dy)[CH] = reinterpret_cast<float(*)[CH]>(sm + H::DY);
-  float(*s_b)[NS] = reinterpret_cast<float(*)[NS]>(sm + H::SB_);
-  float(*s_c)[NS] = reinterpret_cast<float(*)[NS]>(sm + H::SC_);
+  pair(*s_b)[NS] = reinterpret_cast<pair(*)[NS]>(sm + H::SB_);
+  pair(*s_c)[NS] = reinterpret_cast<pair(*)[NS]>(sm + H::SC_);
   float* const s_part = sm + H::PART;
-  float* const s_ck = sm + H::CKPT;
+  float4* const s_ck = reinterpret_cast<float4*>(sm + H::CKPT);
+  float4* const s_da = reinterpret_cast<float4*>(sm + H::SUMA);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t st_seq = (int64_t)p.dim * NS;
@@ -81,31 +92,43 @@ __global__ void __launch_bounds__(BwdShape<T, NS>::NT, 2) scan_bwd_kernel(const 
     }
     return;
   }
-  const int64_t slot = blockIdx.x / p.tiles;
-  const int tile = (int)(blockIdx.x % p.tiles);
+  const int64_t slot = blockIdx.x / (unsigned)p.tiles;
+  const int tile = (int)(blockIdx.x % (unsigned)p.tiles);
   const Segment u = find_unit(p, slot);
   const int grp = tile / p.tiles_per_group;
   const int c_lo = (tile % p.tiles_per_group) * CH;
   const int c_n = min(CH, p.per - c_lo);
   const int64_t ch0 = (int64_t)grp * p.per + c_lo;
-  const int c = tid / LPC, l = tid % LPC;
-  const bool mine = c < c_n;
-  const int64_t st_at = (ch0 + c) * NS + l * SP;
+  const int cp = warp * CL + lane_channel<LPC>(lane), l = lane_part<LPC>(lane);
+  const int left = max(0, min(2, c_n - 2 * cp));  // channels of the thread's pair that exist
+  const int64_t st_at = (ch0 + 2 * cp) * NS + l * SP;
 
-  float A2[SP], g[SP], dA[SP], h0[SP];
+  // a state array of the thread's two channels, from [dim][NS]
+  auto get_pairs = [&](pair (&v)[SP], const void* from, int64_t at, bool b16) {
+    float f[2][SP] = {};
+    if (left > 0) load_state<SP>(f[0], from, at + st_at, b16);
+    if (left > 1) load_state<SP>(f[1], from, at + st_at + NS, b16);
 #pragma unroll
-  for (int i = 0; i < SP; ++i) A2[i] = g[i] = dA[i] = 0.f;
-  if (mine) {
-    load_rates<SP>(A2, p.A_log, st_at);
-    if (u.live && u.last) {
-      if (p.dfin) load_state<SP>(g, p.dfin, u.n * st_seq + st_at, p.state_bf16);
-    } else if (u.live) {
-      load_state<SP>(g, p.seg_state, slot * st_seq + st_at, false);
-    }
+    for (int i = 0; i < SP; ++i) v[i] = pr(f[0][i], f[1][i]);
+  };
+  pair A2[SP], g[SP], h0[SP];
+  {
+    float a[2][SP] = {};
+    if (left > 0) load_rates<SP>(a[0], p.A_log, st_at);
+    if (left > 1) load_rates<SP>(a[1], p.A_log, st_at + NS);
+#pragma unroll
+    for (int i = 0; i < SP; ++i) A2[i] = pr(a[0][i], a[1][i]), g[i] = 0;
   }
+  if (u.live && u.last) {
+    if (p.dfin) get_pairs(g, p.dfin, u.n * st_seq, p.state_bf16);
+  } else if (u.live) {
+    get_pairs(g, p.seg_state, slot * st_seq, false);
+  }
+  s_da[tid] = s_da[NT + tid] = make_float4(0.f, 0.f, 0.f, 0.f);  // read by this thread alone
   const int sc = VEC ? (tid % PER_ROW) * SV : tid % PER_ROW;
   const int sstep = VEC ? 1 : PER_ROW;
   const int64_t sleft = VEC ? (sc < c_n ? CH : 0) : c_n - sc;
+  const int btok = tid / (NS / BV), bn = tid % (NS / BV) * BV;
   float bias[SV], dsk[SV], sum_d[SV], sum_b[SV];
 #pragma unroll
   for (int i = 0; i < SV; ++i) {
@@ -114,6 +137,7 @@ __global__ void __launch_bounds__(BwdShape<T, NS>::NT, 2) scan_bwd_kernel(const 
     dsk[i] = cc < c_n && p.D ? __ldg(p.D + ch0 + cc) : 0.f;
     sum_d[i] = sum_b[i] = 0.f;
   }
+  const int u_even = pair_unit(0, cp), u_odd = pair_unit(1, cp);
 
   const int64_t blocks = u.live ? (u.t1 - u.t0 + kScanBlock - 1) / kScanBlock : 0;
   for (int64_t blk = blocks - 1; blk >= 0; --blk) {
@@ -138,127 +162,145 @@ __global__ void __launch_bounds__(BwdShape<T, NS>::NT, 2) scan_bwd_kernel(const 
       unpack(rz, zv);
       unpack(ro, ov);
 #pragma unroll
-      for (int i = 0; i < SV; ++i) {
-        float ex, d = softplus(tv[i] + bias[i], ex);
-        if (tok >= nt) d = 0.f;
-        s_dx[tok][sc + i * sstep] = make_float2(d, d * xv[i]);
-        s_dy[tok][sc + i * sstep] = p.z ? ov[i] * zv[i] * sigmoid(zv[i]) : ov[i];
+      for (int i = 0; i < SV; i += 2) {
+        pair ex;
+        pair d = softplus(padd(pr(tv[i], tv[i + 1]), pr(bias[i], bias[i + 1])), ex);
+        d = tok < nt ? d : 0;
+        const pair m = pmul(d, pr(xv[i], xv[i + 1]));
+        pair dy = pr(ov[i], ov[i + 1]);
+        if (p.z) dy = pmul(dy, silu(pr(zv[i], zv[i + 1])));
+        if constexpr (VEC) {
+          *reinterpret_cast<ulonglong2*>(&s_dx[tok][pair_unit(tok, (sc + i) / 2)]) = make_ulonglong2(d, m);
+          *reinterpret_cast<pair*>(&s_dy[tok][sc + i]) = dy;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int cc = sc + (i + k) * sstep;
+            float* const unit = &s_dx[tok][pair_unit(tok, cc / 2)].x;
+            unit[cc & 1] = k ? un(d).y : un(d).x;
+            unit[2 + (cc & 1)] = k ? un(m).y : un(m).x;
+            s_dy[tok][cc] = k ? un(dy).y : un(dy).x;
+          }
+        }
       }
     }
-    if (tid < kScanBlock * LPC) {
-      const int tok = tid / LPC;
-      Raw<T, SP> rb = {}, rc = {};
-      if (tok < nt) {
-        load_row<T, SP, VEC>(rb, static_cast<const T*>(p.B) + (t0 + tok) * p.b_s + grp * NS + l * SP, 1, SP);
-        load_row<T, SP, VEC>(rc, static_cast<const T*>(p.C) + (t0 + tok) * p.c_s + grp * NS + l * SP, 1, SP);
+    {
+      Raw<T, BV> rb = {}, rc = {};
+      if (btok < nt) {
+        load_row<T, BV, VEC>(rb, static_cast<const T*>(p.B) + (t0 + btok) * p.b_s + grp * NS + bn, 1, BV);
+        load_row<T, BV, VEC>(rc, static_cast<const T*>(p.C) + (t0 + btok) * p.c_s + grp * NS + bn, 1, BV);
       }
-      float v[SP];
+      float v[BV];
       unpack(rb, v);
 #pragma unroll
-      for (int i = 0; i < SP; ++i) s_b[tok][l * SP + i] = v[i];
+      for (int i = 0; i < BV; ++i) s_b[btok][bn + i] = pr(v[i]);
       unpack(rc, v);
 #pragma unroll
-      for (int i = 0; i < SP; ++i) s_c[tok][l * SP + i] = v[i];
+      for (int i = 0; i < BV; ++i) s_c[btok][bn + i] = pr(v[i]);
     }
-    if (mine) {
-      const int64_t chunk = u.bos / kScanBlock + u.n + (t0 - u.bos) / kScanBlock;
-      load_state<SP>(h0, p.chunk_states, chunk * st_seq + st_at, false);
-    } else {
-#pragma unroll
-      for (int i = 0; i < SP; ++i) h0[i] = 0.f;
-    }
+    get_pairs(h0, p.chunk_states, (u.bos / kScanBlock + u.n + (t0 - u.bos) / kScanBlock) * st_seq, false);
     __syncthreads();
 
     // ---- forward over the block: a checkpoint before every piece but the first
     const int pieces = (nt + SB - 1) / SB;
-    float h[SP];
+    pair h[SP];
 #pragma unroll
     for (int i = 0; i < SP; ++i) h[i] = h0[i];
-    auto step = [&](int tok, float (&a)[SP]) {
-      const float2 d = s_dx[tok][c];
+    auto step = [&](int tok, int unit, pair (&a)[SP]) {
+      const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(&s_dx[tok][unit]);
 #pragma unroll
       for (int i = 0; i < SP; i += 2) {
-        const float2 b2 = *reinterpret_cast<const float2*>(&s_b[tok][l * SP + i]);
-        const float2 e = ptx::f2mul(make_float2(d.x, d.x), make_float2(A2[i], A2[i + 1]));
-        a[i] = ptx::ex2_approx(e.x), a[i + 1] = ptx::ex2_approx(e.y);
-        const float2 hn = ptx::f2fma(make_float2(a[i], a[i + 1]), make_float2(h[i], h[i + 1]),
-                                     ptx::f2mul(make_float2(d.y, d.y), b2));
-        h[i] = hn.x, h[i + 1] = hn.y;
+        const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(&s_b[tok][l * SP + i]);
+        a[i] = pex2(pmul(d.x, A2[i])), a[i + 1] = pex2(pmul(d.x, A2[i + 1]));
+        h[i] = pfma(a[i], h[i], pmul(d.y, b2.x));
+        h[i + 1] = pfma(a[i + 1], h[i + 1], pmul(d.y, b2.y));
       }
     };
     for (int k = 0; k + 1 < pieces; ++k) {
-      float a[SP];
+      pair a[SP];
 #pragma unroll
-      for (int j = 0; j < SB; ++j) step(k * SB + j, a);
+      for (int j = 0; j < SB; ++j) step(k * SB + j, j & 1 ? u_odd : u_even, a);
 #pragma unroll
-      for (int i = 0; i < SP; i += 4)
-        *reinterpret_cast<float4*>(&s_ck[(k * NT + tid) * SP + i]) =
-            make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<ulonglong2*>(&s_ck[(k * 2 + q) * NT + tid]) = make_ulonglong2(h[2 * q], h[2 * q + 1]);
     }
     // ---- the pieces in reverse
-    for (int k = pieces - 1; k >= 0; --k) {
+    pair dA[SP];
 #pragma unroll
-      for (int i = 0; i < SP; ++i) h[i] = k ? s_ck[((k - 1) * NT + tid) * SP + i] : h0[i];
-      float a[SB][SP], hp[SB][SP];
+    for (int i = 0; i < SP; ++i) dA[i] = 0;
+    for (int k = pieces - 1; k >= 0; --k) {
+      if (k) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&s_ck[((k - 1) * 2 + q) * NT + tid]);
+          h[2 * q] = v.x, h[2 * q + 1] = v.y;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < SP; ++i) h[i] = h0[i];
+      }
+      pair a[SB][SP], hp[SB][SP];
 #pragma unroll
       for (int j = 0; j < SB; ++j) {
 #pragma unroll
         for (int i = 0; i < SP; ++i) hp[j][i] = h[i];
-        step(k * SB + j, a[j]);
+        step(k * SB + j, j & 1 ? u_odd : u_even, a[j]);
       }
-      constexpr int L = SB < LPC ? SB : LPC;   // tokens whose state sums are reduced together
-      constexpr int GT = 16 / (2 * SP);        // tokens whose channel sums are
-      float qv[L], sv[L], yv[L], bc[16];
+      pair qv[SB], sv[SB], yv[SB];
 #pragma unroll
       for (int j = SB - 1; j >= 0; --j) {
         const int tok = k * SB + j;
-        const float2 d = s_dx[tok][c];
-        const float dy = s_dy[tok][c];
-        float2 q2 = make_float2(0.f, 0.f), s2 = q2, y2 = q2;
+        const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(&s_dx[tok][j & 1 ? u_odd : u_even]);
+        const pair dy = *reinterpret_cast<const pair*>(&s_dy[tok][2 * cp]);
+        float bc[2 * SP];
+        pair q2 = 0, s2 = 0, y2 = 0;
 #pragma unroll
         for (int i = 0; i < SP; i += 2) {
-          const float2 b2 = *reinterpret_cast<const float2*>(&s_b[tok][l * SP + i]);
-          const float2 c2 = *reinterpret_cast<const float2*>(&s_c[tok][l * SP + i]);
-          const float2 ht = j == SB - 1 ? make_float2(h[i], h[i + 1])
-                                        : make_float2(hp[(j + 1) % SB][i], hp[(j + 1) % SB][i + 1]);
-          float2 g2 = ptx::f2fma(make_float2(dy, dy), c2, make_float2(g[i], g[i + 1]));
-          const float2 vb = ptx::f2mul(make_float2(d.y, d.y), g2);
-          const float2 vc = ptx::f2mul(make_float2(dy, dy), ht);
-          const int at = (j % GT) * 2 * SP + i;
-          bc[at] = vb.x, bc[at + 1] = vb.y;
-          bc[at + SP] = vc.x, bc[at + SP + 1] = vc.y;
-          q2 = ptx::f2fma(g2, b2, q2);
-          y2 = ptx::f2fma(c2, ht, y2);
-          g2 = ptx::f2mul(g2, make_float2(a[j][i], a[j][i + 1]));
-          const float2 w2 = ptx::f2mul(g2, make_float2(hp[j][i], hp[j][i + 1]));
-          s2 = ptx::f2fma(w2, make_float2(A2[i], A2[i + 1]), s2);
-          const float2 da = ptx::f2fma(w2, make_float2(d.x, d.x), make_float2(dA[i], dA[i + 1]));
-          dA[i] = da.x, dA[i + 1] = da.y;
-          g[i] = g2.x, g[i + 1] = g2.y;
-        }
-        qv[j % L] = q2.x + q2.y, sv[j % L] = s2.x + s2.y, yv[j % L] = y2.x + y2.y;
-        if (j % GT == 0) {  // sums over the warp's channels
-          int off = 0;
-          reduce_scatter<16, 16, LPC>(bc, lane, off);
-          constexpr int LEFT = 16 / H::CL > 0 ? 16 / H::CL : 1;
+          const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(&s_b[tok][l * SP + i]);
+          const ulonglong2 c2 = *reinterpret_cast<const ulonglong2*>(&s_c[tok][l * SP + i]);
 #pragma unroll
-          for (int i = 0; i < LEFT; ++i) {
-            const int o = off + i;
-            const int tk = j + o / (2 * SP), kind = o / SP % 2;
-            s_part[(warp * SB + tk) * 2 * NS + kind * NS + l * SP + o % SP] = bc[i];
+          for (int e = 0; e < 2; ++e) {
+            const int n = i + e;
+            const pair bn2 = e ? b2.y : b2.x, cn2 = e ? c2.y : c2.x;
+            const pair ht = j == SB - 1 ? h[n] : hp[(j + 1) % SB][n];
+            pair gn = pfma(dy, cn2, g[n]);
+            const float2 vb = un(pmul(d.y, gn)), vc = un(pmul(dy, ht));
+            bc[n] = vb.x + vb.y, bc[SP + n] = vc.x + vc.y;
+            q2 = n ? pfma(gn, bn2, q2) : pmul(gn, bn2);
+            y2 = n ? pfma(cn2, ht, y2) : pmul(cn2, ht);
+            gn = pmul(gn, a[j][n]);
+            const pair w = pmul(gn, hp[j][n]);
+            s2 = n ? pfma(w, A2[n], s2) : pmul(w, A2[n]);
+            dA[n] = pfma(w, d.x, dA[n]);
+            g[n] = gn;
           }
         }
-        if (j % L == 0) {  // sums over the channel's states: one token per lane
-          int off = 0;
-          reduce_scatter<L, LPC / 2, 1>(qv, lane, off);
-          off = 0;
-          reduce_scatter<L, LPC / 2, 1>(sv, lane, off);
-          off = 0;
-          reduce_scatter<L, LPC / 2, 1>(yv, lane, off);
-          __syncwarp();  // the channel's lanes are done with these tokens
-          s_dx[k * SB + j + off][c] = make_float2(qv[0], sv[0] * kLn2);
-          s_dy[k * SB + j + off][c] = yv[0];
+        qv[j] = q2, sv[j] = s2, yv[j] = y2;
+        // over the warp's channels: lane bits 1 .. CL (see lane_channel)
+        int off = 0;
+        reduce_scatter<2 * SP, CL, 2>(bc, lane, off);
+        constexpr int LEFT = 2 * SP / CL > 0 ? 2 * SP / CL : 1;
+#pragma unroll
+        for (int i = 0; i < LEFT; ++i) {
+          const int o = off + i;
+          s_part[(warp * SB + j) * 2 * NS + o / SP * NS + l * SP + o % SP] = bc[i];
         }
+      }
+      // over the channels' states: a token per lane
+      constexpr int TOK = LPC < SB ? SB / LPC : 1;
+      int off = 0;
+      reduce_states<SB, LPC>(qv, lane, off);
+      off = 0;
+      reduce_states<SB, LPC>(sv, lane, off);
+      off = 0;
+      reduce_states<SB, LPC>(yv, lane, off);
+      __syncwarp();  // the pair's lanes are done with these tokens
+#pragma unroll
+      for (int j = 0; j < TOK; ++j) {
+        const int tok = k * SB + off + j;
+        *reinterpret_cast<ulonglong2*>(&s_dx[tok][pair_unit(tok, cp)]) =
+            make_ulonglong2(qv[j], pmul(sv[j], pr(kLn2)));
+        *reinterpret_cast<pair*>(&s_dy[tok][2 * cp]) = yv[j];
       }
       __syncthreads();
       for (int e = tid; e < SB * 2 * NS; e += NT) {  // over the CTA's warps
@@ -269,6 +311,13 @@ __global__ void __launch_bounds__(BwdShape<T, NS>::NT, 2) scan_bwd_kernel(const 
         if (tk < nt) p.part_bc[((int64_t)tile * p.total + t0 + tk) * 2 * NS + e % (2 * NS)] = v;
       }
       __syncthreads();
+    }
+    // a block's share of dA joins the rest in one addition
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      ulonglong2* const to = reinterpret_cast<ulonglong2*>(&s_da[q * NT + tid]);
+      const ulonglong2 v = *to;
+      *to = make_ulonglong2(padd(v.x, dA[2 * q]), padd(v.y, dA[2 * q + 1]));
     }
     // ---- the gradients of the block's rows
 #pragma unroll
@@ -288,23 +337,39 @@ __global__ void __launch_bounds__(BwdShape<T, NS>::NT, 2) scan_bwd_kernel(const 
       unpack(rz, zv);
       unpack(ro, ov);
 #pragma unroll
-      for (int i = 0; i < SV; ++i) {
-        const float2 qs = s_dx[tok][sc + i * sstep];
-        float ex;
-        const float d = softplus(tv[i] + bias[i], ex);
-        const float sig = softplus_slope(tv[i] + bias[i], ex);
-        float dy = ov[i];
-        dz[i] = 0.f;
-        if (p.z) {
-          const float sz = sigmoid(zv[i]);
-          dy *= zv[i] * sz;
-          const float y = fmaf(dsk[i], xv[i], s_dy[tok][sc + i * sstep]);
-          dz[i] = ov[i] * y * sz * fmaf(zv[i], 1.f - sz, 1.f);
+      for (int i = 0; i < SV; i += 2) {
+        pair qi, si, yi;
+        if constexpr (VEC) {
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&s_dx[tok][pair_unit(tok, (sc + i) / 2)]);
+          qi = v.x, si = v.y;
+          yi = *reinterpret_cast<const pair*>(&s_dy[tok][sc + i]);
+        } else {
+          const int c0 = sc + i * sstep, c1 = c0 + sstep;
+          const float* const u0 = &s_dx[tok][pair_unit(tok, c0 / 2)].x;
+          const float* const u1 = &s_dx[tok][pair_unit(tok, c1 / 2)].x;
+          qi = pr(u0[c0 & 1], u1[c1 & 1]), si = pr(u0[2 + (c0 & 1)], u1[2 + (c1 & 1)]);
+          yi = pr(s_dy[tok][c0], s_dy[tok][c1]);
         }
-        dx[i] = fmaf(d, qs.x, dy * dsk[i]);
-        dt[i] = fmaf(xv[i], qs.x, qs.y) * sig;
-        sum_d[i] = fmaf(dy, xv[i], sum_d[i]);
-        sum_b[i] += dt[i];
+        const pair x2 = pr(xv[i], xv[i + 1]), o2 = pr(ov[i], ov[i + 1]);
+        const pair v = padd(pr(tv[i], tv[i + 1]), pr(bias[i], bias[i + 1]));
+        pair ex, dy = o2, dz2 = 0;
+        const pair d = softplus(v, ex);
+        const pair sig = pr(softplus_slope(un(v).x, un(ex).x), softplus_slope(un(v).y, un(ex).y));
+        const pair sk = pr(dsk[i], dsk[i + 1]);
+        if (p.z) {
+          const pair z2 = pr(zv[i], zv[i + 1]), sz = sigmoid(z2), zs = pmul(z2, sz);
+          dy = pmul(o2, zs);
+          // silu' = s + z s - (z s) s
+          const pair slope = pfma(pmul(zs, pr(-1.f)), sz, padd(sz, zs));
+          dz2 = pmul(pmul(o2, pfma(sk, x2, yi)), slope);
+        }
+        const pair dx2 = pfma(d, qi, pmul(dy, sk)), dt2 = pmul(pfma(x2, qi, si), sig);
+        const float2 sd = un(pmul(dy, x2));
+        sum_d[i] += sd.x, sum_d[i + 1] += sd.y;
+        dx[i] = un(dx2).x, dx[i + 1] = un(dx2).y;
+        dt[i] = un(dt2).x, dt[i + 1] = un(dt2).y;
+        dz[i] = un(dz2).x, dz[i + 1] = un(dz2).y;
+        sum_b[i] += dt[i], sum_b[i + 1] += dt[i + 1];
       }
       const int64_t at = t * p.dim + ch0 + sc;
       store_row<T, SV, VEC>(static_cast<T*>(p.dx) + at, dx, sstep, sleft);
@@ -314,12 +379,24 @@ __global__ void __launch_bounds__(BwdShape<T, NS>::NT, 2) scan_bwd_kernel(const 
     __syncthreads();
   }
   // ---- what is summed over tokens: a partial row per slot
-  float* const par = p.part_par + slot * (int64_t)p.dim * (NS + 2);
-  if (mine) {
+  float* const par = p.part_par + slot * par_pitch(p.dim, NS);
+  {
+    float f[2][SP], gi[2][SP];
 #pragma unroll
-    for (int i = 0; i < SP; ++i) par[st_at + i] = dA[i] * A2[i] * kLn2;
-    if (u.live && u.first && p.dinit) store_state<SP>(p.dinit, u.n * st_seq + st_at, g, false);
+    for (int i = 0; i < SP; ++i) {
+      const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&s_da[i / 2 * NT + tid]);
+      const float2 da = un(pmul(i & 1 ? v.y : v.x, pmul(A2[i], pr(kLn2))));
+      f[0][i] = da.x, f[1][i] = da.y;
+      gi[0][i] = un(g[i]).x, gi[1][i] = un(g[i]).y;
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (q >= left) break;
+      store_state<SP>(par, st_at + q * NS, f[q], false);
+      if (u.live && u.first && p.dinit) store_state<SP>(p.dinit, u.n * st_seq + st_at + q * NS, gi[q], false);
+    }
   }
+  __syncthreads();
   float(*s_red)[CH] = reinterpret_cast<float(*)[CH]>(sm);  // [NT / PER_ROW][CH], twice
   constexpr int ROWS = NT / PER_ROW;
 #pragma unroll
@@ -334,98 +411,6 @@ __global__ void __launch_bounds__(BwdShape<T, NS>::NT, 2) scan_bwd_kernel(const 
     for (int r = 0; r < ROWS; ++r) v += s_red[k * ROWS + r][cc];
     if (cc < c_n) par[st_seq + k * (int64_t)p.dim + ch0 + cc] = v;
   }
-}
-
-// The gradient that leaves a segment at its start, from a zero gradient at its end (the
-// last segment: from dfinal_state), and the segment's sum of delta.
-template <typename T, int NS, bool VEC>
-__global__ void __launch_bounds__(kRevCh * NS / kStates<NS>)
-    scan_rev_kernel(const ScanParams p) {
-  constexpr int SP = kStates<NS>, LPC = NS / SP, CH = kRevCh, NT = CH * LPC;
-  constexpr int EPT = kScanBlock * CH / NT, SV = EPT < 8 ? EPT : 8, SN = EPT / SV;
-  constexpr int PER_ROW = CH / SV;
-  __shared__ float2 s_d[kScanBlock][CH];  // delta, dy
-  __shared__ __align__(16) float s_c[kScanBlock][NS];
-  const int tid = threadIdx.x;
-  const int tpg = (p.per + CH - 1) / CH;
-  const int64_t tiles = (int64_t)tpg * p.groups;
-  const int64_t slot = blockIdx.x / tiles;
-  const int tile = (int)(blockIdx.x % tiles);
-  const Segment u = find_unit(p, slot);
-  if (!u.live || u.first) return;  // nothing before the first segment asks for its gradient
-  const int grp = tile / tpg, c_lo = (tile % tpg) * CH, c_n = min(CH, p.per - c_lo);
-  const int64_t ch0 = (int64_t)grp * p.per + c_lo, st_seq = (int64_t)p.dim * NS;
-  const int c = tid / LPC, l = tid % LPC;
-  const bool mine = c < c_n;
-  const int64_t st_at = (ch0 + c) * NS + l * SP;
-  float A2[SP], g[SP], sum_delta = 0.f;
-#pragma unroll
-  for (int i = 0; i < SP; ++i) A2[i] = g[i] = 0.f;
-  if (mine) {
-    load_rates<SP>(A2, p.A_log, st_at);
-    if (u.last && p.dfin) load_state<SP>(g, p.dfin, u.n * st_seq + st_at, p.state_bf16);
-  }
-  const int sc = VEC ? (tid % PER_ROW) * SV : tid % PER_ROW;
-  const int sstep = VEC ? 1 : PER_ROW;
-  const int64_t sleft = VEC ? (sc < c_n ? CH : 0) : c_n - sc;
-  for (int64_t blk = (u.t1 - u.t0 + kScanBlock - 1) / kScanBlock - 1; blk >= 0; --blk) {
-    const int64_t t0 = u.t0 + blk * kScanBlock;
-    const int nt = (int)min((int64_t)kScanBlock, u.t1 - t0);
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < SN; ++q) {
-      const int tok = (q * NT + tid) / PER_ROW;
-      Raw<T, SV> rt = {}, rz = {}, ro = {};
-      const int64_t t = t0 + tok;
-      if (tok < nt && sleft > 0) {
-        load_row<T, SV, VEC>(rt, static_cast<const T*>(p.dt) + t * p.dt_s + ch0 + sc, sstep, sleft);
-        if (p.z)
-          load_row<T, SV, VEC>(rz, static_cast<const T*>(p.z) + t * p.z_s + ch0 + sc, sstep, sleft);
-        load_row<T, SV, VEC>(ro, static_cast<const T*>(p.dout) + t * p.dim + ch0 + sc, sstep, sleft);
-      }
-      float tv[SV], zv[SV], ov[SV];
-      unpack(rt, tv);
-      unpack(rz, zv);
-      unpack(ro, ov);
-#pragma unroll
-      for (int i = 0; i < SV; ++i) {
-        const int cc = sc + i * sstep;
-        float ex;
-        const float d =
-            softplus(tv[i] + (cc < c_n && p.dt_bias ? __ldg(p.dt_bias + ch0 + cc) : 0.f), ex);
-        s_d[tok][cc] = make_float2(tok < nt ? d : 0.f,
-                                   p.z ? ov[i] * zv[i] * sigmoid(zv[i]) : ov[i]);
-      }
-    }
-    {
-      const int tok = tid / LPC;
-      Raw<T, SP> rc = {};
-      if (tok < nt)
-        load_row<T, SP, VEC>(rc, static_cast<const T*>(p.C) + (t0 + tok) * p.c_s + grp * NS + l * SP, 1, SP);
-      float v[SP];
-      unpack(rc, v);
-#pragma unroll
-      for (int i = 0; i < SP; ++i) s_c[tok][l * SP + i] = v[i];
-    }
-    __syncthreads();
-#pragma unroll 4
-    for (int tok = kScanBlock - 1; tok >= 0; --tok) {
-      const float2 d = s_d[tok][c];
-      sum_delta += d.x;
-#pragma unroll
-      for (int i = 0; i < SP; i += 2) {
-        const float2 c2 = *reinterpret_cast<const float2*>(&s_c[tok][l * SP + i]);
-        const float2 e = ptx::f2mul(make_float2(d.x, d.x), make_float2(A2[i], A2[i + 1]));
-        const float2 a = make_float2(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y));
-        const float2 gn = ptx::f2mul(
-            a, ptx::f2fma(make_float2(d.y, d.y), c2, make_float2(g[i], g[i + 1])));
-        g[i] = gn.x, g[i + 1] = gn.y;
-      }
-    }
-  }
-  if (!mine) return;
-  store_state<SP>(p.seg_state, slot * st_seq + st_at, g, false);
-  if (l == 0) p.seg_sum[slot * p.dim + ch0 + c] = sum_delta;
 }
 
 // Carries the gradients over a sequence's segments, last to first: in place, the gradient
@@ -495,31 +480,22 @@ cudaError_t launch_bwd_ns(const ScanParams& p, int64_t tail, cudaStream_t stream
   return cudaGetLastError();
 }
 
-template <typename T, int NS, bool VEC>
-cudaError_t launch_rev_ns(const ScanParams& p, cudaStream_t stream) {
-  const int64_t grid = (int64_t)((p.per + kRevCh - 1) / kRevCh) * p.groups * p.slots;
-  if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  scan_rev_kernel<T, NS, VEC>
-      <<<(unsigned)grid, kRevCh * NS / kStates<NS>, 0, stream>>>(p);
-  return cudaGetLastError();
-}
-
 template <typename T, bool VEC>
-cudaError_t launch_bwd(const ScanParams& p, int state, bool rev, int64_t tail, cudaStream_t s) {
+cudaError_t launch_bwd(const ScanParams& p, int state, int64_t tail, cudaStream_t s) {
   switch (state) {
-    case 8: return rev ? launch_rev_ns<T, 8, VEC>(p, s) : launch_bwd_ns<T, 8, VEC>(p, tail, s);
-    case 16: return rev ? launch_rev_ns<T, 16, VEC>(p, s) : launch_bwd_ns<T, 16, VEC>(p, tail, s);
-    case 32: return rev ? launch_rev_ns<T, 32, VEC>(p, s) : launch_bwd_ns<T, 32, VEC>(p, tail, s);
-    default: return rev ? launch_rev_ns<T, 64, VEC>(p, s) : launch_bwd_ns<T, 64, VEC>(p, tail, s);
+    case 8: return launch_bwd_ns<T, 8, VEC>(p, tail, s);
+    case 16: return launch_bwd_ns<T, 16, VEC>(p, tail, s);
+    case 32: return launch_bwd_ns<T, 32, VEC>(p, tail, s);
+    default: return launch_bwd_ns<T, 64, VEC>(p, tail, s);
   }
 }
 
-cudaError_t launch_bwd_pass(const ScanParams& p, int state, bool f32, bool vec, bool rev,
-                            int64_t tail, cudaStream_t s) {
-  if (f32) return vec ? launch_bwd<float, true>(p, state, rev, tail, s)
-                      : launch_bwd<float, false>(p, state, rev, tail, s);
-  return vec ? launch_bwd<bf16, true>(p, state, rev, tail, s)
-             : launch_bwd<bf16, false>(p, state, rev, tail, s);
+cudaError_t launch_bwd_pass(const ScanParams& p, int state, bool f32, bool vec, int64_t tail,
+                            cudaStream_t s) {
+  if (f32) return vec ? launch_bwd<float, true>(p, state, tail, s)
+                      : launch_bwd<float, false>(p, state, tail, s);
+  return vec ? launch_bwd<bf16, true>(p, state, tail, s)
+             : launch_bwd<bf16, false>(p, state, tail, s);
 }
 
 bool al_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -542,18 +518,17 @@ BwdLayout bwd_layout(ScanParams& p, int state, bool have_states) {
   size_t n = 0;
   kda_scan_get_states_size(p.total, p.N, p.dim, state, &n);
   if (!have_states) at = up256(at + n);
-  const int ch = state == 64 ? kBwdCh<64> : kBwdCh<16>;
+  const int ch = state == 8 ? 128 : state <= 32 ? 64 : 32;  // BwdShape::CH
   p.tiles_per_group = (p.per + ch - 1) / ch;
   p.tiles = (int64_t)p.tiles_per_group * p.groups;
-  // 2 CTAs of 256 threads per SM at the kernel's registers and shared memory
-  const ScanPlan r = scan_plan(p, p.tiles, 1, 2);
+  const ScanPlan r = scan_plan(p, p.tiles, 2, 6);
   p.seg_len = r.seg_len, p.slots = r.slots;
   w.seg = at;
   if (p.seg_len) at = up256(at + (size_t)p.slots * p.dim * (state + 1) * sizeof(float));
   w.bc = at;
   at = up256(at + (size_t)p.tiles * p.total * 2 * state * sizeof(float));
   w.par = at;
-  at += (size_t)p.slots * p.dim * (state + 2) * sizeof(float);
+  at += (size_t)p.slots * par_pitch(p.dim, state) * sizeof(float);
   w.total = at;
   return w;
 }
@@ -624,13 +599,13 @@ kda_status kda_scan_bwd(const kda_scan_problem* problem, const void* dout,
   if (p.seg_len) {
     p.seg_state = reinterpret_cast<float*>(ws + w.seg);
     p.seg_sum = p.seg_state + p.slots * p.dim * state;
-    if (launch_bwd_pass(p, state, f32, vec, true, 0, stream) != cudaSuccess) return KDA_ERR_CUDA;
+    if (scan::launch_scan_rev(p, state, f32, vec, stream) != cudaSuccess) return KDA_ERR_CUDA;
     const int64_t grid = ((int64_t)p.dim * state + 127) / 128 * p.N;
     if (grid >= (int64_t(1) << 31)) return KDA_ERR_INVALID_SHAPE;
     scan_rev_carry_kernel<<<(unsigned)grid, 128, 0, stream>>>(p, state);
     if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
   }
-  if (launch_bwd_pass(p, state, f32, vec, false, p.cu ? 32 : 0, stream) != cudaSuccess)
+  if (launch_bwd_pass(p, state, f32, vec, p.cu ? 32 : 0, stream) != cudaSuccess)
     return KDA_ERR_CUDA;
   if (p.total > 0) {
     const int64_t grid = (p.total * p.groups * 2 * state + 255) / 256;
@@ -643,8 +618,8 @@ kda_status kda_scan_bwd(const kda_scan_problem* problem, const void* dout,
     if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
   }
   const int64_t n = (int64_t)p.dim * state;
-  if (launch_column_sums(p.part_par, p.slots, n + 2 * (int64_t)p.dim, n, p.dim, dA_log, dD,
-                         ddt_bias, stream) != cudaSuccess ||
+  if (launch_column_sums(p.part_par, p.slots, par_pitch(p.dim, state), n + 2 * (int64_t)p.dim, n,
+                         p.dim, dA_log, dD, ddt_bias, stream) != cudaSuccess ||
       seqlens_status(p, static_cast<unsigned*>(workspace), stream) != cudaSuccess)
     return KDA_ERR_CUDA;
   return KDA_OK;

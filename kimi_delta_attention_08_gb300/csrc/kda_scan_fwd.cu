@@ -26,6 +26,8 @@ namespace {
 
 using namespace scan;
 
+enum ScanPass { kOutputs, kStatesOnly, kReverse };
+
 // A thread holds 8 states of two neighbouring channels, as pairs of fp32 values that the
 // packed operations take: 22 instructions per 4 states of 32 channels with everything (a
 // version that paired states and staged rows in shared memory took 31 to 35).  Of U tokens
@@ -41,8 +43,12 @@ struct FwdShape {
   static constexpr int BW = BV < 8 ? BV : 8;     // ... in vectors of BW
 };
 
-template <typename T, int NS, bool VEC, bool OUT>
-__global__ void __launch_bounds__(FwdShape<NS>::NT, 5) scan_fwd_kernel(const ScanParams p) {
+// PASS kOutputs: the main pass.  kStatesOnly: states only (of every block, or the end of a
+// segment).  kReverse: the backward's like pass over segments, from their last token to
+// their first, of the gradient: g <- 2^(delta A2) (g + dy C) with dy = dout silu(z).
+template <typename T, int NS, bool VEC, int PASS>
+__global__ void __launch_bounds__(FwdShape<NS>::NT, PASS == kOutputs ? 4 : 5) scan_fwd_kernel(const ScanParams p) {
+  constexpr bool OUT = PASS == kOutputs, REV = PASS == kReverse;
   using S = FwdShape<NS>;
   constexpr int SP = S::SP, LPC = S::LPC, NT = S::NT, CH = S::CH, TB = S::TB, U = S::U;
   constexpr int OWN = S::OWN, BW = S::BW, BN = S::BV / BW;
@@ -59,7 +65,8 @@ __global__ void __launch_bounds__(FwdShape<NS>::NT, 5) scan_fwd_kernel(const Sca
   const Segment u = find_unit(p, slot);
   if (!u.live) return;
   const bool prescan = !OUT && p.prescan;
-  if (prescan && u.last) return;  // its end starts no segment
+  // the last segment's end starts no segment; nothing before the first asks for its gradient
+  if (prescan && (REV ? u.first : u.last)) return;
   const int grp = tile / p.tiles_per_group;
   const int l = lane_part<LPC>(lane);
   // the thread's channels within the group, cg and cg + 1; `left` of them exist
@@ -82,7 +89,9 @@ __global__ void __launch_bounds__(FwdShape<NS>::NT, 5) scan_fwd_kernel(const Sca
       for (int i = 0; i < SP; ++i) a[q][i] = v[q][i] = 0.f;
       if (q < left) {
         load_rates<SP>(a[q], p.A_log, st_at + q * NS);
-        if (p.seg_state && !prescan) load_state<SP>(v[q], p.seg_state, slot * st_seq + st_at + q * NS, false);
+        if (REV) {
+          if (u.last && p.dfin) load_state<SP>(v[q], p.dfin, u.n * st_seq + st_at + q * NS, p.state_bf16);
+        } else if (p.seg_state && !prescan) load_state<SP>(v[q], p.seg_state, slot * st_seq + st_at + q * NS, false);
         else if (u.first && p.init) load_state<SP>(v[q], p.init, u.n * st_seq + st_at + q * NS, p.state_bf16);
       }
     }
@@ -106,9 +115,10 @@ __global__ void __launch_bounds__(FwdShape<NS>::NT, 5) scan_fwd_kernel(const Sca
     for (int q = 0; q < BN; ++q) {
       const int e = (q * NT + tid) * BW, m = e / (TB * NS), tok = e / NS % TB, n = e % NS;
       rbc[q] = Raw<T, BW>{};
-      if (t0 + tok < tokens && (OUT || m == 0)) {
-        const T* const row = m == 0 ? static_cast<const T*>(p.B) + (u.t0 + t0 + tok) * p.b_s
-                                    : static_cast<const T*>(p.C) + (u.t0 + t0 + tok) * p.c_s;
+      if (t0 + tok < tokens && (OUT || m == (REV ? 1 : 0))) {
+        const int64_t t = REV ? u.t1 - 1 - t0 - tok : u.t0 + t0 + tok;
+        const T* const row = m == 0 ? static_cast<const T*>(p.B) + t * p.b_s
+                                    : static_cast<const T*>(p.C) + t * p.c_s;
         load_row<T, BW, VEC>(rbc[q], row + grp * NS + n, 1, BW);
       }
     }
@@ -124,9 +134,12 @@ __global__ void __launch_bounds__(FwdShape<NS>::NT, 5) scan_fwd_kernel(const Sca
     }
   };
   // the rows of the lane's own tokens; one past the end has dt = -infinity, a step of zero
-  const T* px = static_cast<const T*>(p.x) + (u.t0 + l * OWN) * p.x_s + ch;
-  const T* pt = static_cast<const T*>(p.dt) + (u.t0 + l * OWN) * p.dt_s + ch;
-  const T* pz = static_cast<const T*>(p.z) + (u.t0 + l * OWN) * p.z_s + ch;
+  constexpr int DIR = REV ? -1 : 1;
+  const int64_t own0 = REV ? u.t1 - 1 - l * OWN : u.t0 + l * OWN;
+  const int64_t x_s = DIR * (REV ? (int64_t)p.dim : p.x_s), t_s = DIR * p.dt_s, z_s = DIR * p.z_s;
+  const T* px = static_cast<const T*>(REV ? p.dout : p.x) + own0 * (DIR * x_s) + ch;
+  const T* pt = static_cast<const T*>(p.dt) + own0 * p.dt_s + ch;
+  const T* pz = static_cast<const T*>(p.z) + own0 * p.z_s + ch;
   T* po = static_cast<T*>(p.out) + (u.t0 + l * OWN) * p.dim + ch;
   constexpr int G = TB / U;  // groups of U tokens in flight: a block's worth
   Raw<T, 2> rx[G][OWN], rt[G][OWN], rz[G][OWN], none;
@@ -138,13 +151,13 @@ __global__ void __launch_bounds__(FwdShape<NS>::NT, 5) scan_fwd_kernel(const Sca
       rx[g][k] = rz[g][k] = Raw<T, 2>{};
       rt[g][k] = none;
       if (t + l * OWN + k < tokens && left > 0) {
-        load_row<T, 2, VEC>(rx[g][k], px + k * p.x_s, 1, left);
-        load_row<T, 2, VEC>(rt[g][k], pt + k * p.dt_s, 1, left);
-        if (OUT && p.z) load_row<T, 2, VEC>(rz[g][k], pz + k * p.z_s, 1, left);
+        load_row<T, 2, VEC>(rx[g][k], px + k * x_s, 1, left);
+        load_row<T, 2, VEC>(rt[g][k], pt + k * t_s, 1, left);
+        if ((OUT || REV) && p.z) load_row<T, 2, VEC>(rz[g][k], pz + k * z_s, 1, left);
       }
     }
-    px += U * p.x_s, pt += U * p.dt_s;
-    if (OUT && p.z) pz += U * p.z_s;
+    px += U * x_s, pt += U * t_s;
+    if ((OUT || REV) && p.z) pz += U * z_s;
   };
   auto as_pair = [](const Raw<T, 2>& r) {
     float f[2];
@@ -182,7 +195,8 @@ __global__ void __launch_bounds__(FwdShape<NS>::NT, 5) scan_fwd_kernel(const Sca
         xv[k] = as_pair(rx[g][k]);
         if (OUT && p.z) zv[k] = as_pair(rz[g][k]);
         delta[k] = softplus(padd(as_pair(rt[g][k]), bias), ex);
-        dx[k] = pmul(delta[k], xv[k]);
+        if (REV) dx[k] = p.z ? pmul(xv[k], silu(as_pair(rz[g][k]))) : xv[k];  // dy
+        else dx[k] = pmul(delta[k], xv[k]);
         if (!OUT) sum_delta = padd(sum_delta, delta[k]);
       }
       fetch(g, t0 + TB + j0);
@@ -191,12 +205,17 @@ __global__ void __launch_bounds__(FwdShape<NS>::NT, 5) scan_fwd_kernel(const Sca
       for (int k = 0; k < U; ++k) {
         const pair d = LPC == 1 ? delta[k % OWN] : __shfl_sync(0xffffffffu, delta[k % OWN], owner(k));
         const pair m = LPC == 1 ? dx[k % OWN] : __shfl_sync(0xffffffffu, dx[k % OWN], owner(k));
-        const pair* const b = &s_bc[buf][0][j0 + k][l * SP];
+        const pair* const b = &s_bc[buf][REV ? 1 : 0][j0 + k][l * SP];
         const pair* const cc = &s_bc[buf][1][j0 + k][l * SP];
         pair acc[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < SP; i += 2) {
           const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(b + i);
+          if constexpr (REV) {
+            h[i] = pmul(pex2(pmul(d, A2[i])), pfma(m, b2.x, h[i]));
+            h[i + 1] = pmul(pex2(pmul(d, A2[i + 1])), pfma(m, b2.y, h[i + 1]));
+            continue;
+          }
           h[i] = advance(h[i], A2[i], d, m, b2.x);
           h[i + 1] = advance(h[i + 1], A2[i + 1], d, m, b2.y);
           if (OUT) {
@@ -363,7 +382,7 @@ __global__ void __launch_bounds__(128, 8) scan_step_kernel(const ScanParams p) {
   }
 }
 
-template <typename T, bool VEC, bool OUT>
+template <typename T, bool VEC, int PASS>
 cudaError_t launch_main(const ScanParams& p, int state, cudaStream_t stream) {
   const int64_t grid = p.slots * p.tiles;
   if (grid == 0) return cudaSuccess;
@@ -371,20 +390,20 @@ cudaError_t launch_main(const ScanParams& p, int state, cudaStream_t stream) {
   const unsigned g = (unsigned)grid;
   constexpr int NT = FwdShape<16>::NT;
   switch (state) {
-    case 8: scan_fwd_kernel<T, 8, VEC, OUT><<<g, NT, 0, stream>>>(p); break;
-    case 16: scan_fwd_kernel<T, 16, VEC, OUT><<<g, NT, 0, stream>>>(p); break;
-    case 32: scan_fwd_kernel<T, 32, VEC, OUT><<<g, NT, 0, stream>>>(p); break;
-    default: scan_fwd_kernel<T, 64, VEC, OUT><<<g, NT, 0, stream>>>(p); break;
+    case 8: scan_fwd_kernel<T, 8, VEC, PASS><<<g, NT, 0, stream>>>(p); break;
+    case 16: scan_fwd_kernel<T, 16, VEC, PASS><<<g, NT, 0, stream>>>(p); break;
+    case 32: scan_fwd_kernel<T, 32, VEC, PASS><<<g, NT, 0, stream>>>(p); break;
+    default: scan_fwd_kernel<T, 64, VEC, PASS><<<g, NT, 0, stream>>>(p); break;
   }
   return cudaGetLastError();
 }
 
-template <bool OUT>
+template <int PASS>
 cudaError_t launch_pass(const ScanParams& p, int state, bool f32, bool vec, cudaStream_t stream) {
-  if (f32) return vec ? launch_main<float, true, OUT>(p, state, stream)
-                      : launch_main<float, false, OUT>(p, state, stream);
-  return vec ? launch_main<bf16, true, OUT>(p, state, stream)
-             : launch_main<bf16, false, OUT>(p, state, stream);
+  if (f32) return vec ? launch_main<float, true, PASS>(p, state, stream)
+                      : launch_main<float, false, PASS>(p, state, stream);
+  return vec ? launch_main<bf16, true, PASS>(p, state, stream)
+             : launch_main<bf16, false, PASS>(p, state, stream);
 }
 
 template <typename T, bool VEC>
@@ -511,6 +530,18 @@ cudaError_t seqlens_status(const ScanParams& p, unsigned* status, cudaStream_t s
   return cudaGetLastError();
 }
 
+// The reverse pass over segments (its tiles are the forward's), then the gradients carried
+// over them.
+cudaError_t launch_scan_rev(ScanParams p, int state, bool f32, bool vec, cudaStream_t stream) {
+  const int64_t seg_len = p.seg_len, slots = p.slots;
+  scan_fwd_plan(p, state);
+  p.seg_len = seg_len, p.slots = slots;
+  p.prescan = 1;
+  p.chunk_states = nullptr;
+  p.status = nullptr;
+  return launch_pass<kReverse>(p, state, f32, vec, stream);
+}
+
 // The forward's own tiles and segments, the first two passes where sequences are cut, and
 // the main pass.  p.seg_state holds the workspace's state region.
 cudaError_t launch_scan_fwd(ScanParams p, int state, bool f32, bool vec, bool out,
@@ -525,7 +556,7 @@ cudaError_t launch_scan_fwd(ScanParams p, int state, bool f32, bool vec, bool ou
     q.seg_state = ws_state, q.seg_sum = ws_sum;
     q.chunk_states = nullptr;
     q.prescan = 1;
-    e = launch_pass<false>(q, state, f32, vec, stream);
+    e = launch_pass<kStatesOnly>(q, state, f32, vec, stream);
     if (e != cudaSuccess) return e;
     const int64_t grid = ((int64_t)p.dim * state + 127) / 128 * p.N;
     if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
@@ -535,8 +566,8 @@ cudaError_t launch_scan_fwd(ScanParams p, int state, bool f32, bool vec, bool ou
     p.seg_state = ws_state;
   }
   p.status = p.seg_len ? nullptr : status;
-  return out ? launch_pass<true>(p, state, f32, vec, stream)
-             : launch_pass<false>(p, state, f32, vec, stream);
+  return out ? launch_pass<kOutputs>(p, state, f32, vec, stream)
+             : launch_pass<kStatesOnly>(p, state, f32, vec, stream);
 }
 
 }  // namespace scan
