@@ -14,6 +14,12 @@
 // warp's loads in flight); longer ones to a block with one barrier per row.  Weight
 // gradients are summed over a block's rows in registers, then over the blocks by a
 // second launch, in a fixed order.
+//
+// Device time, and bytes of the rows over it: forward before a block, 32,768 rows of 4,096
+// bf16 values with an fp32 residual, 238 us (6.8 TB/s); forward after one, 1,048,576 rows of
+// 128 bf16 with a gate, 141 us (5.7 TB/s); backward before a block, 32,768 x 4,096 bf16
+// with a learned scale, 247 us (6.5 TB/s); backward after one, 74,097 rows of 1,001 fp32
+// with gate and scale (no 16-byte alignment, so single values), 298 us (5.0 TB/s).
 #include "kda_internal.h"
 #include "kda_rows.cuh"
 #include "../../include/kda_layer.h"
@@ -131,10 +137,26 @@ __device__ __forceinline__ int64_t gate_shift(const NormParams& p, int64_t row) 
   };                                                                                     \
   int64_t row = (int64_t)blockIdx.x * rpb + grp;
 
-// Threads of a block.  The backward over long rows is held to two blocks per SM: with their
-// 64 registers it spills a few and still takes 309 us where one block of 86 takes 393
-// (32,768 rows of 4,096 bf16 values).
+// Rows on their way through shared memory: the backward over long rows (G = 0, one vector
+// of 8 per thread) keeps the next ones there by asynchronous copies, since the weights and
+// their gradients fill its registers.  Each thread reads back what it asked for, so no
+// barrier is needed.  A slot has at most 128 bytes per thread, so that three fit with 512.
+// Backward before a block over 2^27 bf16 values in rows of 1,024 and 4,096, with a learned
+// scale: 270 and 246 us, against 726 and 319 with the next row in registers.
+constexpr int kNormRing = 3;
+__host__ __device__ constexpr bool norm_has_ring(int G, int E, int V) { return G == 0 && E == 1 && V == 8; }
+
+template <typename T>
+__device__ __forceinline__ void copy_vec(void* to, const void* from, int64_t at) {
+#pragma unroll
+  for (int b = 0; b < 8 * (int)sizeof(T); b += 16)
+    ptx::cp_async16(static_cast<uint8_t*>(to) + b, static_cast<const uint8_t*>(from) + at * sizeof(T) + b, 16);
+}
+
+// Threads of a block, and the blocks per SM that a backward's registers leave room for: one of
+// 512 threads with a ring (its rows in flight need no second block, and 64 registers spill).
 constexpr int norm_threads(int G, int E, int V) { return G ? 256 : V == 1 && E == 8 ? 1024 : 512; }
+constexpr int norm_bwd_blocks(int G, int E, int V) { return G || E > 1 || V == 8 ? 1 : 2; }
 
 template <int G, int E, int V, typename T, typename TS>
 __global__ void __launch_bounds__(norm_threads(G, E, V)) prenorm_fwd_kernel(const NormParams p) {
@@ -206,7 +228,8 @@ template <int G, int E, int V>
 __device__ __forceinline__ void write_partials(const NormParams& p, const Vals<V> (&dwv)[E],
                                                const Vals<V> (&dsv)[E], int g, int grp, int gsz,
                                                int rpb, int nv) {
-  extern __shared__ float acc[];  // [2][dim] when several rows share a block
+  extern __shared__ __align__(16) uint8_t norm_ring[];
+  float* const acc = reinterpret_cast<float*>(norm_ring);  // [2][dim], rows sharing a block
   float dw[E][V], ds[E][V];
 #pragma unroll
   for (int i = 0; i < E; ++i) vals_to(dwv[i], dw[i]), vals_to(dsv[i], ds[i]);
@@ -246,28 +269,63 @@ __device__ __forceinline__ void write_partials(const NormParams& p, const Vals<V
 
 // a = dout, b = dresidual_out or null, c = h, d = x or null (dscale)
 template <int G, int E, int V, typename T, typename TS>
-__global__ void __launch_bounds__(norm_threads(G, E, V), G || E > 1 ? 1 : 2) prenorm_bwd_kernel(const NormParams p) {
+__global__ void __launch_bounds__(norm_threads(G, E, V), norm_bwd_blocks(G, E, V))
+    prenorm_bwd_kernel(const NormParams p) {
+  constexpr bool RING = norm_has_ring(G, E, V);
+  extern __shared__ __align__(16) uint8_t norm_ring[];
   KDA_NORM_ROWS(G)
   Vals<V> dw[E], ds[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) dw[i] = ds[i] = splat<V>(0.f);
   Raw<TS, V> rh[E] = {}, rd[E] = {};
   Raw<T, V> ry[E] = {}, rx[E] = {};
+  // a ring slot: h, dresidual_out, dout, x of all threads
+  constexpr int SLOT = 16 * (int)(sizeof(TS) + sizeof(T));
+  constexpr int AHEAD = kNormRing - 1;
+  auto slot_of = [&](int k) { return norm_ring + k % kNormRing * (int)blockDim.x * SLOT; };
+  auto issue = [&](int64_t at_row, int k) {
+    if constexpr (RING) {
+      uint8_t* const to = slot_of(k);
+      const int n = blockDim.x;
+      each(at_row, [&](int, int64_t at) {
+        copy_vec<TS>(to + g * 8 * sizeof(TS), p.c, at);
+        if (p.b) copy_vec<TS>(to + (n + g) * 8 * sizeof(TS), p.b, at);
+        copy_vec<T>(to + 2 * n * 8 * sizeof(TS) + g * 8 * sizeof(T), p.a, at);
+        if (p.want_scale) copy_vec<T>(to + 2 * n * 8 * sizeof(TS) + (n + g) * 8 * sizeof(T), p.d, at);
+      });
+      ptx::cp_async_commit();
+    }
+  };
   auto fetch_sums = [&](int64_t at_row) {
-    each(at_row, [&](int i, int64_t at) {
-      load_vec(rh[i], p.c, at);
-      load_vec(ry[i], p.a, at);
-    });
+    if constexpr (!RING) {
+      each(at_row, [&](int i, int64_t at) {
+        load_vec(rh[i], p.c, at);
+        load_vec(ry[i], p.a, at);
+      });
+    }
   };
   auto fetch_rest = [&](int64_t at_row) {
-    each(at_row, [&](int i, int64_t at) {
-      if (p.b) load_vec(rd[i], p.b, at);
-      if (p.want_scale) load_vec(rx[i], p.d, at);
-    });
+    if constexpr (!RING) {
+      each(at_row, [&](int i, int64_t at) {
+        if (p.b) load_vec(rd[i], p.b, at);
+        if (p.want_scale) load_vec(rx[i], p.d, at);
+      });
+    }
   };
+  for (int k = 0; k < AHEAD; ++k) issue(row + k * stride, k);
   fetch_sums(row);
   fetch_rest(row);
   for (int64_t base = row - grp; base < p.n_rows; base += stride, row += stride, ++turn) {
+    if constexpr (RING) {
+      issue(row + AHEAD * stride, turn + AHEAD);
+      ptx::cp_async_wait<AHEAD>();
+      const uint8_t* const from = slot_of(turn);
+      const int n = blockDim.x;
+      load_words<true>(rh[0].w, from + g * 8 * sizeof(TS));
+      if (p.b) load_words<true>(rd[0].w, from + (n + g) * 8 * sizeof(TS));
+      load_words<true>(ry[0].w, from + 2 * n * 8 * sizeof(TS) + g * 8 * sizeof(T));
+      if (p.want_scale) load_words<true>(rx[0].w, from + 2 * n * 8 * sizeof(TS) + (n + g) * 8 * sizeof(T));
+    }
     Vals<V> h[E], dy[E], s1 = splat<V>(0.f), s2 = s1;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -297,22 +355,53 @@ __global__ void __launch_bounds__(norm_threads(G, E, V), G || E > 1 ? 1 : 2) pre
 // a = dout, b = gate or null, c = x; o0 = dx, o1 = dgate.  With a = fn(gate), a' its slope:
 // P = dout a and Q = dout a' are all that is kept of dout and the gate.
 template <int G, int E, int V, typename T, typename TS>
-__global__ void __launch_bounds__(norm_threads(G, E, V), G || E > 1 ? 1 : 2) postnorm_bwd_kernel(const NormParams p) {
+__global__ void __launch_bounds__(norm_threads(G, E, V), norm_bwd_blocks(G, E, V))
+    postnorm_bwd_kernel(const NormParams p) {
+  constexpr bool RING = norm_has_ring(G, E, V);
+  extern __shared__ __align__(16) uint8_t norm_ring[];
   KDA_NORM_ROWS(G)
   Vals<V> dw[E], ds[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) dw[i] = ds[i] = splat<V>(0.f);
   Raw<T, V> rx[E] = {}, ry[E] = {}, rg[E] = {};
-  auto fetch = [&](int64_t at_row) {
-    const int64_t shift = gate_shift(p, at_row);
-    each(at_row, [&](int i, int64_t at) {
-      load_vec(rx[i], p.c, at);
-      load_vec(ry[i], p.a, at);
-      if (p.b) load_vec(rg[i], p.b, at + shift);
-    });
+  constexpr int SLOT = 8 * 3 * (int)sizeof(T);  // x, dout, gate of all threads
+  constexpr int AHEAD = kNormRing - 1;
+  auto slot_of = [&](int k) { return norm_ring + k % kNormRing * (int)blockDim.x * SLOT; };
+  auto issue = [&](int64_t at_row, int k) {
+    if constexpr (RING) {
+      uint8_t* const to = slot_of(k);
+      const int64_t shift = gate_shift(p, at_row);
+      const int n = blockDim.x;
+      each(at_row, [&](int, int64_t at) {
+        copy_vec<T>(to + g * 8 * sizeof(T), p.c, at);
+        copy_vec<T>(to + (n + g) * 8 * sizeof(T), p.a, at);
+        if (p.b) copy_vec<T>(to + (2 * n + g) * 8 * sizeof(T), p.b, at + shift);
+      });
+      ptx::cp_async_commit();
+    }
   };
+  auto fetch = [&](int64_t at_row) {
+    if constexpr (!RING) {
+      const int64_t shift = gate_shift(p, at_row);
+      each(at_row, [&](int i, int64_t at) {
+        load_vec(rx[i], p.c, at);
+        load_vec(ry[i], p.a, at);
+        if (p.b) load_vec(rg[i], p.b, at + shift);
+      });
+    }
+  };
+  for (int k = 0; k < AHEAD; ++k) issue(row + k * stride, k);
   fetch(row);
   for (int64_t base = row - grp; base < p.n_rows; base += stride, row += stride, ++turn) {
+    if constexpr (RING) {
+      issue(row + AHEAD * stride, turn + AHEAD);
+      ptx::cp_async_wait<AHEAD>();
+      const uint8_t* const from = slot_of(turn);
+      const int n = blockDim.x;
+      load_words<true>(rx[0].w, from + g * 8 * sizeof(T));
+      load_words<true>(ry[0].w, from + (n + g) * 8 * sizeof(T));
+      if (p.b) load_words<true>(rg[0].w, from + (2 * n + g) * 8 * sizeof(T));
+    }
     Vals<V> x[E], P[E], Q[E], s1 = splat<V>(0.f), s2 = s1;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -454,11 +543,20 @@ kda_status run_norm(NormKernel kernel, const NormPlan& n, const NormParams& p,
 }
 
 kda_status run_norm_bwd(NormKernel kernel, const NormPlan& n, NormParams& p, int num_sms,
-                        void* workspace, float* dweight, float* dscale, cudaStream_t stream) {
+                        int ring_bytes, void* workspace, float* dweight, float* dscale,
+                        cudaStream_t stream) {
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + KDA_STATUS_BYTES);
-  int64_t grid = norm_grid(n, p.n_rows, num_sms, n.G ? 4 : 2);
+  // as many blocks as run at once, so that the partial rows are few
+  const bool ring = norm_has_ring(n.G, n.E, n.V);
+  const int per_sm = n.G ? 4 : n.V == 8 ? 512 / n.threads : n.threads >= 512 ? 2 : 1024 / n.threads;
+  int64_t grid = norm_grid(n, p.n_rows, num_sms, per_sm < 8 ? per_sm : 8);
   if (grid > kMaxBlocks) grid = kMaxBlocks;
-  const size_t smem = n.G ? 2 * (size_t)p.dim * sizeof(float) : 0;
+  const size_t smem = n.G ? 2 * (size_t)p.dim * sizeof(float)
+                          : ring ? (size_t)kNormRing * n.threads * ring_bytes : 0;
+  if (smem > 40 * 1024 &&  // 48 KB with the static part need no request
+      cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return KDA_ERR_CUDA;
   if (grid > 0) {
     const kda_status st = run_norm(kernel, n, p, grid, smem, stream);
     if (st != KDA_OK) return st;
@@ -551,7 +649,8 @@ kda_status kda_prenorm_bwd(const void* dout, const void* dresidual_out, const vo
   p.a = dout, p.b = dresidual_out, p.c = h, p.d = x, p.o0 = dx, p.o1 = dresidual;
   p.weight = weight, p.scale = res_scale, p.scale_value = res_scale_value, p.eps = eps;
   p.n_rows = rows, p.dim = dim, p.want_scale = dres_scale != nullptr;
-  return run_norm_bwd(pick_prenorm_bwd(n, dtype, stream_dtype), n, p, num_sms, workspace, dweight, dres_scale, stream);
+  return run_norm_bwd(pick_prenorm_bwd(n, dtype, stream_dtype), n, p, num_sms, 16 * (int)(e + se),
+                      workspace, dweight, dres_scale, stream);
 }
 
 kda_status kda_postnorm_fwd(const void* x, const float* weight, const void* gate,
@@ -623,7 +722,8 @@ kda_status kda_postnorm_bwd(const void* dout, const void* x, const float* weight
   p.weight = weight, p.scale = res_scale, p.scale_value = res_scale_value, p.eps = eps;
   p.n_rows = rows, p.dim = dim;
   p.want_scale = dres_scale != nullptr;
-  return run_norm_bwd(pick_postnorm_bwd(n, dtype, dtype), n, p, num_sms, workspace, dweight, dres_scale, stream);
+  return run_norm_bwd(pick_postnorm_bwd(n, dtype, dtype), n, p, num_sms, 24 * (int)e, workspace,
+                      dweight, dres_scale, stream);
 }
 
 }  // extern "C"
