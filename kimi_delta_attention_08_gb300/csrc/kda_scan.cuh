@@ -1,19 +1,21 @@
 // kda_scan.cuh -- what the scan's forward and backward share: the division of the
-// (tokens, channels, states) space over threads, the segments of a split scan, the
-// staging of a block of tokens and the reductions across lanes.
+// (tokens, channels, states) space over threads, the segments of a split scan and the
+// reductions across lanes.
 //
-// A thread holds SP states of a channel (or of two) in registers, and a warp 32 / LPC of
-// these with LPC = state / SP lanes each: bit 0 of the lane and its top bits choose the states' part, the
-// bits between them the channel.  So two neighbouring lanes always share a channel, and a
-// quarter of the warp reads two addresses of B and C: a 16-byte read from shared memory
-// then takes 2.1 cycles, and one of 8 bytes by channel 1.1, where other orders of the same
-// lanes take 4 and 2 (measured).  A CTA holds CH channels of one group and walks its tokens
-// in blocks of kScanBlock.
+// A thread holds SP states of a channel pair in registers (the single-token kernel: of one
+// channel), and a warp 32 / LPC of these with LPC = state / SP lanes each: bit 0 of the lane
+// and its top bits choose the states' part, the bits between them the channels.  So two
+// neighbouring lanes always share a channel, and a quarter of the warp reads two addresses
+// of B and C: a 16-byte read from shared memory then takes 2.1 cycles, and one of 8 bytes by
+// channel 1.1, where other orders of the same lanes take 4 and 2 (measured).  A CTA holds CH
+// channels of one group and walks the tokens of a sequence or a segment.
 //
 // Segments.  A sequence is cut into segments of seg_len tokens (0: not cut).  Segment s of
 // sequence n has slot floor(bos_n / seg_len) + n + s: distinct for all segments of all
 // sequences and below total / seg_len + N.
 #pragma once
+
+#include <cfloat>
 
 #include "kda_internal.h"
 #include "kda_rows.cuh"
@@ -24,7 +26,7 @@ namespace scan {
 
 using namespace rows;
 
-constexpr int kScanBlock = KDA_SCAN_CHUNK;  // 32 tokens: one saved state each
+constexpr int kScanBlock = KDA_SCAN_CHUNK;  // 32 tokens: one saved state each, the backward's block
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct ScanParams {
@@ -107,20 +109,21 @@ __device__ __forceinline__ Segment find_unit(const ScanParams& p, int64_t slot) 
 }
 
 // softplus(v) = max(v, 0) + log1p(u), u = exp(-|v|) in (0, 1], with the relative accuracy
-// that small steps need: log1p(u) = u P(u), P of degree 8 fitted to log1p(u) / u on [0, 1]
-// by reweighted least squares to an even relative error (3e-8; 1.2e-7 as evaluated in
-// fp32).  No reciprocal: that costs as much as two exponentials.
+// that small steps need: log1p(u) = u P(u), P of degree 8 with P(0) = 1, fitted to
+// log1p(u) / u on [0, 1] by reweighted least squares to an even relative error (3.3e-8;
+// 1.4e-7 at most and 7e-9 on average as evaluated in fp32).  No reciprocal: that costs as
+// much as two exponentials.
 __device__ __forceinline__ pair softplus(pair v, pair& u) {
   const float2 w = un(v);
   u = pr(ptx::ex2_approx(-fabsf(w.x) * kLog2e), ptx::ex2_approx(-fabsf(w.y) * kLog2e));
-  pair s = pfma(pr(0.00523267686f), u, pr(-0.029505169f));
-  s = pfma(s, u, pr(0.0782258362f));
-  s = pfma(s, u, pr(-0.136632353f));
-  s = pfma(s, u, pr(0.191060022f));
-  s = pfma(s, u, pr(-0.248429805f));
-  s = pfma(s, u, pr(0.333190978f));
-  s = pfma(s, u, pr(-0.499994934f));
-  s = pfma(s, u, pr(0.99999994f));
+  pair s = pfma(pr(0.00536481664f), u, pr(-0.0300657619f));
+  s = pfma(s, u, pr(0.0792044848f));
+  s = pfma(s, u, pr(-0.137537986f));
+  s = pfma(s, u, pr(0.191536531f));
+  s = pfma(s, u, pr(-0.248571634f));
+  s = pfma(s, u, pr(0.33321324f));
+  s = pfma(s, u, pr(-0.499996483f));
+  s = pfma(s, u, pr(1.0f));
   return pfma(u, s, pr(fmaxf(w.x, 0.f), fmaxf(w.y, 0.f)));
 }
 __device__ __forceinline__ float softplus(float v, float& u) {
@@ -135,14 +138,6 @@ __device__ __forceinline__ float softplus_slope(float v, float u) {
   return v >= 0.f ? r : u * r;
 }
 
-// Where a channel's 16 bytes (delta, delta, delta x, delta x) lie in a token's row: channels
-// are exchanged within groups of eight so that the staging writes (neighbouring lanes 8
-// channels apart, two rows in 8 lanes) use every bank once, as the reads (neighbouring
-// channels of one token) do anyway.
-__device__ __forceinline__ int unit_at(int tok, int c) {
-  return c ^ ((c >> 3 & 3) | (tok & 1) << 2);
-}
-
 // A lane's channel within the warp and its states' part.
 template <int LPC>
 __device__ __forceinline__ int lane_channel(int lane) {
@@ -153,9 +148,18 @@ __device__ __forceinline__ int lane_part(int lane) {
   return LPC == 1 ? 0 : (lane & 1) | (lane / (64 / LPC) << 1);
 }
 
+// The decay 2^(delta A2) of two channels.  The hardware's exponential lies 1.8e-8 low on
+// average where its result is in (1/2, 1) (measured over 4 million points in each of
+// several ranges), and long products of decays multiply that up, so the exponent is raised
+// by as much.  A step of zero still leaves exactly 1.  At no cost this takes the error of
+// the decay rates' gradient from 1.0e-6 to 3.8e-7 (16,384 tokens of 1,024 channels).
+__device__ __forceinline__ pair decay(pair delta, pair A2) {
+  return pex2(pfma(delta, A2, pr(2.5e-8f)));
+}
+
 // h <- 2^(delta A2) h + (delta x) B for a state of two channels; b = (B, B).
 __device__ __forceinline__ pair advance(pair h, pair A2, pair delta, pair dx, pair b) {
-  return pfma(pex2(pmul(delta, A2)), h, pmul(dx, b));
+  return pfma(decay(delta, A2), h, pmul(dx, b));
 }
 
 __device__ __forceinline__ float sum_of(float a, float b) { return a + b; }
@@ -220,12 +224,16 @@ __device__ __forceinline__ void store_state(void* p, int64_t at, const float (&h
 }
 
 // Decay rates in base 2: A2 = -exp(A_log) log2 e, so that exp(-delta exp(A_log)) = 2^(delta A2).
-// exp(v) = 2^(v log2 e) with the product's rounding error put back: 2^e (1 + e' ln 2).
+// exp(v) = 2^(v log2 e) with the product's rounding error put back: 2^e (1 + e' ln 2); not
+// where that error is no number because v or the result is infinite.  An infinite rate
+// becomes the largest finite one, so that a step of zero still leaves 1.
 __device__ __forceinline__ float rate_of(float v) {
   const float hi = v * kLog2e;
   const float lo = fmaf(v, 1.925963033500e-8f, fmaf(v, kLog2e, -hi));  // log2 e - kLog2e
   const float e = ptx::ex2_approx(hi);
-  return -kLog2e * fmaf(e, lo * kLn2, e);
+  const float r = fmaf(e, lo * kLn2, e);
+  const float a = -kLog2e * (fabsf(r) < INFINITY ? r : e);
+  return a < -FLT_MAX ? -FLT_MAX : a;
 }
 template <int SP>
 __device__ __forceinline__ void load_rates(float (&a)[SP], const float* A_log, int64_t at) {
@@ -257,7 +265,7 @@ cudaError_t launch_scan_fwd(ScanParams p, int state, bool f32, bool vec, bool ou
                             cudaStream_t stream);
 
 // The gradient that leaves each segment at its start, from a zero gradient at its end (the
-// last one's: dfinal_state), into p.seg_state, and its sum of delta.
+// last one's: dfinal_state), into p.seg_state, and the segment's sum of delta.
 cudaError_t launch_scan_rev(ScanParams p, int state, bool f32, bool vec, cudaStream_t stream);
 
 }  // namespace scan

@@ -5,13 +5,17 @@
 //   y = C_t . h_t + D x,  out = y silu(z),     A2 = -exp(A_log) log2 e
 //
 // Per (token, channel, state) this takes one exponential and four fp32 operations, against
-// 8 bytes of rows per (token, channel) in bf16, so at 16 states it is bound by the special
-// function and FMA pipes, not by HBM.  The state never leaves the registers: a thread
-// walks all tokens of its sequence (or segment).  Blocks of 32 tokens are staged through
-// shared memory: every (token, channel)'s softplus is computed once by the thread that
-// loads it, and the next block's rows are in flight meanwhile.  The dot product over a
-// channel's lanes is reduced for as many tokens at a time as there are lanes, so each lane
-// ends up with one token's sum.
+// 8 bytes of rows per (token, channel) in bf16, so at 16 states it is bound by the FMA and
+// special function pipes and the issue of their instructions, not by HBM.  The state never
+// leaves the registers: a thread walks all tokens of its sequence (or segment).  Every
+// (token, channel)'s softplus is computed once, by the lane that loads its rows, and handed
+// to the channel's other lanes; the rows of the next 16 tokens are in flight meanwhile.  The
+// dot product over a channel's lanes is reduced for as many tokens at a time as there are
+// lanes, so each lane ends up with the tokens that it loaded.
+//
+// 8 sequences of 4,096 tokens, 4,096 channels, 16 states in bf16 take 784 us (1.4 TB/s; the
+// exponentials alone 230 us, those and the packed operations 290); one of 65,536 tokens
+// and five of 1,024 with 1,024 channels, which has to be cut, 641 us.
 //
 // Where the channels alone do not fill the GPU, sequences are cut into segments: a first
 // pass computes each segment's end state from zero and its sum of delta, a second carries
@@ -29,8 +33,9 @@ using namespace scan;
 enum ScanPass { kOutputs, kStatesOnly, kReverse };
 
 // A thread holds 8 states of two neighbouring channels, as pairs of fp32 values that the
-// packed operations take: 22 instructions per 4 states of 32 channels with everything (a
-// version that paired states and staged rows in shared memory took 31 to 35).  Of U tokens
+// packed operations take: with everything about 27 instructions per 4 states of a warp's
+// channels (4 states a thread, with the rows staged in shared memory: 31 to 35 and 884 us
+// for the 784 above; 16 states a thread: 887).  Of U tokens
 // loaded together, each of a channel pair's LPC lanes owns OWN: it loads their rows,
 // computes their steps, hands those round by shuffles, ends up with their dot products and
 // writes their outputs.  Shared memory only carries B and C, each value twice.
@@ -212,8 +217,8 @@ __global__ void __launch_bounds__(FwdShape<NS>::NT, PASS == kOutputs ? 4 : 5) sc
         for (int i = 0; i < SP; i += 2) {
           const ulonglong2 b2 = *reinterpret_cast<const ulonglong2*>(b + i);
           if constexpr (REV) {
-            h[i] = pmul(pex2(pmul(d, A2[i])), pfma(m, b2.x, h[i]));
-            h[i + 1] = pmul(pex2(pmul(d, A2[i + 1])), pfma(m, b2.y, h[i + 1]));
+            h[i] = pmul(decay(d, A2[i]), pfma(m, b2.x, h[i]));
+            h[i + 1] = pmul(decay(d, A2[i + 1]), pfma(m, b2.y, h[i + 1]));
             continue;
           }
           h[i] = advance(h[i], A2[i], d, m, b2.x);
@@ -294,7 +299,8 @@ __global__ void scan_carry_kernel(const ScanParams p, int state) {
 // in flight at once.  Of these sequences each of a channel's lanes owns OWN: it reads their
 // rows, computes their steps, hands those to the others, ends up with their dot products
 // and writes their outputs.  (One thread for all 16 states of a channel computes as little
-// but reads 64 bytes apart: 36.8 us for 256 sequences of 4,096 channels.)
+// but reads 64 bytes apart: 36.8 us for 256 sequences of 4,096 channels and 16 fp32 states,
+// where this takes 33.1 at 4.3 TB/s.)
 constexpr int kStepSeqs = 4;
 constexpr int kStepTokens = 8;  // the longest such prompt
 
@@ -530,8 +536,7 @@ cudaError_t seqlens_status(const ScanParams& p, unsigned* status, cudaStream_t s
   return cudaGetLastError();
 }
 
-// The reverse pass over segments (its tiles are the forward's), then the gradients carried
-// over them.
+// The reverse pass over segments; its tiles are the forward's.
 cudaError_t launch_scan_rev(ScanParams p, int state, bool f32, bool vec, cudaStream_t stream) {
   const int64_t seg_len = p.seg_len, slots = p.slots;
   scan_fwd_plan(p, state);

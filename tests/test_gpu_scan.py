@@ -232,6 +232,35 @@ def test_extreme_steps(kda_lib):
         R.close(g[nm], ref[nm], mag[nm], 17 * T + 256, nm)
 
 
+@pytest.mark.parametrize("seq", ["one", "batch", SPLIT["packed"]])
+def test_steps_of_zero_keep_the_state(kda_lib, seq):
+    """softplus(-200) is 0 in fp32: every decay is exactly 1 and nothing is added."""
+    import kimi_delta_attention_08_gb300 as kda
+    a, b, _, cu, cud, (B, T, N) = make(seq, 64, 16, 1, BF)
+    a["dt"].fill_(-200.0)
+    out = torch.empty(B, T, 64, dtype=BF, device="cuda")
+    fin = torch.full((N, 64, 16), float("nan"), device="cuda")
+    ws = kda.make_scan_workspace(B, T, 64, 16, 1, N if cu else None)
+    kda.kda_scan_fwd(**a, out=out, **b, final_state=fin, cu_seqlens=cud, workspace=ws)
+    assert torch.equal(fin, b["initial_state"])
+
+
+@pytest.mark.parametrize("seq", ["one", "batch"])
+@pytest.mark.parametrize("v", [-float("inf"), 100.0, 300.0])
+def test_rates_of_zero_and_infinity(kda_lib, seq, v):
+    """exp(A_log) of 0 keeps a state for ever, one of infinity forgets it at each step."""
+    import kimi_delta_attention_08_gb300 as kda
+    a, b, _, cu, _, (B, T, N) = make(seq, 64, 16, 1, F)
+    a["A_log"][:, ::2] = v
+    out = torch.empty(B, T, 64, device="cuda")
+    fin = torch.empty(N, 64, 16, device="cuda")
+    kda.kda_scan_fwd(**a, out=out, **b, final_state=fin)
+    ref, rfin = R.scan(*ref_args(a, b, cu))
+    mag, mfin = R.scan(*ref_args(a, b, cu), mag=True)
+    R.close(out, ref, mag, 6 * T + 64, "out")
+    R.close(fin, rfin, mfin, 6 * T + 64, "final_state")
+
+
 def test_no_tokens(kda_lib):
     import kimi_delta_attention_08_gb300 as kda
     a, b, c, _, _, _ = make((2, 0, None), 64, 16, 1, BF)
