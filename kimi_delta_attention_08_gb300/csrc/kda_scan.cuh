@@ -241,12 +241,13 @@ __device__ __forceinline__ void load_rates(float (&a)[SP], const float* A_log, i
   for (int i = 0; i < SP; ++i) a[i] = rate_of(__ldg(A_log + at + i));
 }
 
-// How sequences are cut for a pass over `tiles` channel tiles: not at all with `enough` CTAs
-// per SM, else into `want` per SM.
+// How sequences are cut (seg_len 0: not at all) for a pass over `tiles` channel tiles whose
+// SMs hold `resident` CTAs; and the CTAs that run side by side without cutting.
 struct ScanPlan {
   int64_t seg_len, slots;
 };
-ScanPlan scan_plan(const ScanParams& p, int64_t tiles, int64_t enough, int64_t want);
+ScanPlan scan_plan(const ScanParams& p, int64_t tiles, int64_t resident, bool cut);
+int64_t scan_whole_units(const ScanParams& p, int64_t tiles);
 
 // The checks of sizes and of arguments that the entry points share; they fill the
 // problem's part of `s`, and whether every row starts on 16 bytes.

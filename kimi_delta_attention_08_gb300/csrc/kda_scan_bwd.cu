@@ -20,8 +20,8 @@
 // pairs of channels, and about as many other instructions (shared-memory reads, the sums over
 // channels and over states), so it is bound by the rate at which a scheduler issues: about
 // 0.5 instructions a clock, a packed one taking two or three.  4 sequences of 4,096 tokens,
-// 4,096 channels, 16 states in bf16: 2.58 ms with the forward that saves the states, at
-// 0.58 TB/s; the exponentials alone would take 0.23 ms.  As in the forward, sequences are cut
+// 4,096 channels, 16 states in bf16: 1.70 ms, 2.28 with the forward that saves the states
+// (0.65 TB/s); the exponentials alone would take 0.23 ms.  As in the forward, sequences are cut
 // into segments where channels alone do not fill the GPU: a reverse pass computes each
 // segment's gradient at its start from a zero gradient at its end, and a second launch
 // carries the gradients over the segments.
@@ -56,8 +56,8 @@ struct BwdShape {
   static constexpr int DY = DX + 2 * kScanBlock * CH;         // [32][CH]: dy, then y
   static constexpr int SB_ = DY + kScanBlock * CH;            // B [32][NS], each value twice
   static constexpr int SC_ = SB_ + 2 * kScanBlock * NS;       // C
-  static constexpr int PART = SC_ + 2 * kScanBlock * NS;      // [NW][SB][2 NS]
-  static constexpr int CKPT = PART + NW * SB * 2 * NS;        // [NSB - 1][2][NT] of 4
+  static constexpr int PART = SC_ + 2 * kScanBlock * NS;      // [2][NW][SB][2 NS]
+  static constexpr int CKPT = PART + 2 * NW * SB * 2 * NS;        // [NSB - 1][2][NT] of 4
   static constexpr int SUMA = CKPT + (NSB - 1) * 2 * 4 * NT;  // [2][NT] of 4
   static constexpr int FLOATS = SUMA + 2 * 4 * NT;
 };
@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(BwdShape<T, NS>::NT, 384 / BwdShape<T, NS>::NT
 #pragma unroll
         for (int i = 0; i < SP; ++i) h[i] = h0[i];
       }
+      float* const part = s_part + (k & 1) * NW * SB * 2 * NS;
       pair a[SB][SP], hp[SB][SP];
 #pragma unroll
       for (int j = 0; j < SB; ++j) {
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(BwdShape<T, NS>::NT, 384 / BwdShape<T, NS>::NT
 #pragma unroll
         for (int i = 0; i < LEFT; ++i) {
           const int o = off + i;
-          s_part[(warp * SB + j) * 2 * NS + o / SP * NS + l * SP + o % SP] = bc[i];
+          part[(warp * SB + j) * 2 * NS + o / SP * NS + l * SP + o % SP] = bc[i];
         }
       }
       // over the channels' states: a token per lane
@@ -310,12 +311,12 @@ __global__ void __launch_bounds__(BwdShape<T, NS>::NT, 384 / BwdShape<T, NS>::NT
       for (int e = tid; e < SB * 2 * NS; e += NT) {  // over the CTA's warps
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) v += s_part[w * SB * 2 * NS + e];
+        for (int w = 0; w < NW; ++w) v += part[w * SB * 2 * NS + e];
         const int tk = k * SB + e / (2 * NS);
         if (tk < nt) p.part_bc[((int64_t)tile * p.total + t0 + tk) * 2 * NS + e % (2 * NS)] = v;
       }
-      __syncthreads();
     }
+    __syncthreads();
     // a block's share of dA joins the rest in one addition
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -525,7 +526,13 @@ BwdLayout bwd_layout(ScanParams& p, int state, bool have_states) {
   const int ch = state == 8 ? 128 : state <= 32 ? 64 : 32;  // BwdShape::CH
   p.tiles_per_group = (p.per + ch - 1) / ch;
   p.tiles = (int64_t)p.tiles_per_group * p.groups;
-  const ScanPlan r = scan_plan(p, p.tiles, 2, 6);
+  // 3 CTAs of four warps on an SM.  The reverse pass that cutting adds costs a seventh of the
+  // main one, so sequences stay whole where they fill 85 % of the turns that they take
+  // (4,096 tokens, 4,096 channels: 6 sequences whole 2,580 us, cut 2,510; 7 whole 2,589,
+  // cut 2,987; 8 whole 4,069, cut 3,337).
+  const int64_t whole = scan_whole_units(p, p.tiles), turn = 3 * 152;
+  const bool cut = 100 * whole < 85 * ((whole + turn - 1) / turn * turn);
+  const ScanPlan r = scan_plan(p, p.tiles, 3, cut);
   p.seg_len = r.seg_len, p.slots = r.slots;
   w.seg = at;
   if (p.seg_len) at = up256(at + (size_t)p.slots * p.dim * (state + 1) * sizeof(float));

@@ -15,7 +15,7 @@
 //
 // 8 sequences of 4,096 tokens, 4,096 channels, 16 states in bf16 take 784 us (1.4 TB/s; the
 // exponentials alone 230 us, those and the packed operations 290); one of 65,536 tokens
-// and five of 1,024 with 1,024 channels, which has to be cut, 641 us.
+// and five of 1,024 with 1,024 channels, which has to be cut, 633 us.
 //
 // Where the channels alone do not fill the GPU, sequences are cut into segments: a first
 // pass computes each segment's end state from zero and its sum of delta, a second carries
@@ -434,19 +434,31 @@ bool al_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a 
 
 namespace scan {
 
-// A unit is one CTA's walk over one segment.  Sequences stay whole where that gives every SM
-// `enough` units; else they are cut until there are `want` for each, but not below 256
-// tokens: the two passes that cutting adds cost as much as half the main one.
-constexpr int64_t kMinSegment = 256;
+// A unit is one CTA's walk over one segment; an SM holds `resident` of them at a time.  Units
+// are as long as one another, so they run in turns over the GPU, and sequences are cut so
+// that they nearly fill a whole number of turns, with segments of 128 tokens at least.
+// (Training at 4 sequences of 4,096 tokens, 4,096 channels, 256 units if whole: cut into 7
+// pieces, 3.9 turns of the backward, it takes 1.70 ms; into 4, which take a third turn for
+// the last eighth, 1.96 ms.)
+constexpr int64_t kMinSegment = 128;
 constexpr int64_t kSms = 152;
 
-ScanPlan scan_plan(const ScanParams& p, int64_t tiles, int64_t enough, int64_t want) {
+int64_t scan_whole_units(const ScanParams& p, int64_t tiles) { return p.cu ? tiles : tiles * p.N; }
+
+ScanPlan scan_plan(const ScanParams& p, int64_t tiles, int64_t resident, bool cut) {
   const bool packed = p.cu != nullptr;
   const int64_t N = p.N, T = p.T, total = p.total;
   ScanPlan r = {0, N};
-  const int64_t whole = packed ? tiles : tiles * N;        // CTAs that surely run side by side
-  if (whole >= kSms * enough || total == 0) return r;
-  const int64_t pieces = (kSms * want + whole - 1) / whole;
+  if (!cut || total == 0) return r;
+  const int64_t whole = scan_whole_units(p, tiles), turn = kSms * resident;
+  const int64_t turns_whole = (whole + turn - 1) / turn;
+  int64_t pieces = 0;
+  double best = 0.0;
+  for (int64_t turns = turns_whole + 2; turns <= turns_whole + 7 && best < 0.95; ++turns) {
+    const int64_t room = turn * turns, n = room / whole;
+    const double fill = (double)(n * whole) / (double)room;
+    if (fill > best) best = fill, pieces = n;
+  }
   const int64_t span = packed ? total : T;
   int64_t len = (span + pieces - 1) / pieces;
   len = (len + kScanBlock - 1) / kScanBlock * kScanBlock;
@@ -457,11 +469,15 @@ ScanPlan scan_plan(const ScanParams& p, int64_t tiles, int64_t enough, int64_t w
   return r;
 }
 
+// 4 CTAs of two warps on an SM.  Cutting costs half the main pass once more, while a GPU with
+// half of that room taken still runs at 7 tenths of its rate, so sequences stay whole from
+// 4 tenths on (4,096 tokens, 4,096 channels: 3 sequences whole 555 us, cut 466; 4 whole
+// 565, cut 597; 5 whole 770, cut 731; 8 whole 784, cut 1,126).
 void scan_fwd_plan(ScanParams& p, int state) {
   const int ch = 1024 / state;  // FwdShape::CH
   p.tiles_per_group = (p.per + ch - 1) / ch;
   p.tiles = (int64_t)p.tiles_per_group * p.groups;
-  const ScanPlan r = scan_plan(p, p.tiles, 3, 16);
+  const ScanPlan r = scan_plan(p, p.tiles, 4, 10 * scan_whole_units(p, p.tiles) < 4 * 4 * kSms);
   p.seg_len = r.seg_len, p.slots = r.slots;
 }
 
