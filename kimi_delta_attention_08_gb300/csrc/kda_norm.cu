@@ -321,10 +321,13 @@ __global__ void __launch_bounds__(norm_threads(G, E, V), norm_bwd_blocks(G, E, V
       ptx::cp_async_wait<AHEAD>();
       const uint8_t* const from = slot_of(turn);
       const int n = blockDim.x;
-      load_words<true>(rh[0].w, from + g * 8 * sizeof(TS));
-      if (p.b) load_words<true>(rd[0].w, from + (n + g) * 8 * sizeof(TS));
-      load_words<true>(ry[0].w, from + 2 * n * 8 * sizeof(TS) + g * 8 * sizeof(T));
-      if (p.want_scale) load_words<true>(rx[0].w, from + 2 * n * 8 * sizeof(TS) + (n + g) * 8 * sizeof(T));
+      if (g < nv) {  // the others' part of a slot is never filled: their values stay zero
+        load_words<true>(rh[0].w, from + g * 8 * sizeof(TS));
+        if (p.b) load_words<true>(rd[0].w, from + (n + g) * 8 * sizeof(TS));
+        load_words<true>(ry[0].w, from + 2 * n * 8 * sizeof(TS) + g * 8 * sizeof(T));
+        if (p.want_scale)
+          load_words<true>(rx[0].w, from + 2 * n * 8 * sizeof(TS) + (n + g) * 8 * sizeof(T));
+      }
     }
     Vals<V> h[E], dy[E], s1 = splat<V>(0.f), s2 = s1;
 #pragma unroll
@@ -398,9 +401,11 @@ __global__ void __launch_bounds__(norm_threads(G, E, V), norm_bwd_blocks(G, E, V
       ptx::cp_async_wait<AHEAD>();
       const uint8_t* const from = slot_of(turn);
       const int n = blockDim.x;
-      load_words<true>(rx[0].w, from + g * 8 * sizeof(T));
-      load_words<true>(ry[0].w, from + (n + g) * 8 * sizeof(T));
-      if (p.b) load_words<true>(rg[0].w, from + (2 * n + g) * 8 * sizeof(T));
+      if (g < nv) {  // the others' part of a slot is never filled: their values stay zero
+        load_words<true>(rx[0].w, from + g * 8 * sizeof(T));
+        load_words<true>(ry[0].w, from + (n + g) * 8 * sizeof(T));
+        if (p.b) load_words<true>(rg[0].w, from + (2 * n + g) * 8 * sizeof(T));
+      }
     }
     Vals<V> x[E], P[E], Q[E], s1 = splat<V>(0.f), s2 = s1;
 #pragma unroll

@@ -104,6 +104,29 @@ def test_postnorm(kda_lib, rows, D, ty, act, res, per_channel):
         R.close(r[nm], ref[nm], mag[nm], 64 + (rows if nm in ("dweight", "dres_scale") else 0), nm)
 
 
+@pytest.mark.parametrize("ty", [BF, F])
+@pytest.mark.parametrize("D", [520, 1000, 2008])
+def test_backward_after_other_rows(kda_lib, D, ty):
+    """Widths that leave threads of a block without values, after a call whose rows were NaN
+    everywhere: nothing of them is left in what the next call reads."""
+    import kimi_delta_attention_08_gb300 as kda
+    g = torch.Generator().manual_seed(D)
+    bad = torch.full((2000, 2048), float("nan"), dtype=ty, device="cuda")
+    x, dout, gate, w = rnd(g, 400, D, t=ty), rnd(g, 400, D, t=ty), rnd(g, 400, D, t=ty), rnd(g, D)
+    s = rnd(g, D)
+    kda.kda_prenorm_bwd(bad, bad, bad, torch.ones(2048, device="cuda"), bad,
+                        res_scale=torch.ones(2048, device="cuda"), eps=EPS)
+    r = kda.kda_prenorm_bwd(dout, gate, x, w, x, res_scale=s, eps=EPS)
+    ref, mag = R.prenorm_bwd(dout, gate, x, w, x, s, EPS)
+    for nm in ref:
+        R.close(r[nm], ref[nm], mag[nm], 64 + (400 if nm in ("dweight", "dres_scale") else 0), nm)
+    kda.kda_postnorm_bwd(bad, bad, torch.ones(2048, device="cuda"), bad, eps=EPS)
+    r = kda.kda_postnorm_bwd(dout, x, w, gate, res_scale=s, activation="silu", eps=EPS)
+    ref, mag = R.postnorm_bwd(dout, x, w, gate, s, "silu", EPS)
+    for nm in ref:
+        R.close(r[nm], ref[nm], mag[nm], 64 + (400 if nm in ("dweight", "dres_scale") else 0), nm)
+
+
 @pytest.mark.parametrize("extra", [128, 5])
 def test_gate_in_a_projection(kda_lib, extra):
     """The gate as a slice of wider rows [B, T, H, D]: the bits of a contiguous one."""
