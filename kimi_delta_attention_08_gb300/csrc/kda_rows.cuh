@@ -98,14 +98,6 @@ __device__ __forceinline__ void pack(Raw<T, V>& r, const float (&f)[V]) {
   }
 }
 
-// V consecutive elements from shared memory, aligned to their size.
-template <typename T, int V>
-__device__ __forceinline__ void load_smem(float (&f)[V], const T* p) {
-  Raw<T, V> r;
-  load_words<true>(r.w, p);
-  unpack(r, f);
-}
-
 // V elements of a row that one thread holds: consecutive on the vector path (VEC),
 // `step` elements apart on the scalar path (a warp's loads stay contiguous), where
 // elements at or past `left` read as zero and are not written.
