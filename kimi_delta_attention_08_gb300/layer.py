@@ -50,12 +50,21 @@ def _need(t, name, dtype, dev, shape):
     raise ValueError(f"{name}: must be contiguous (no implicit copy)")
 
 
+def _own(t, name):
+    """The pointer of the tensor that the others are measured by."""
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous (no implicit copy)")
+    return t.data_ptr()
+
+
 def _opt(t, name, dtype, dev, shape):
     return None if t is None else _need(t, name, dtype, dev, shape)
 
 
 def _rows(t, name, dtype, dev, shape):
     """(pointer, row stride) of [B, T, ...] rows with contiguous channels."""
+    if len(shape) == 3 and t.dtype == dtype and t.device == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr(), shape[2]
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype} (no implicit conversion)")
     if t.device != dev:
@@ -90,6 +99,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _call(name, dev, stream, *args):
     """The library's `name` with these arguments and the stream, the tensors' device current."""
     if dev.type != "cuda":
@@ -99,7 +111,7 @@ def _call(name, dev, stream, *args):
         handle = _raw_stream(dev.index)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == dev.index:
+    if _current_device() == dev.index:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -148,27 +160,34 @@ def _scale_args(res_scale, dev, D):
 
 
 # ------------------------------------------------------------- convolution --
+_POINTERS = [ctypes.c_void_p * k for k in range(5)]
+_COUNTS = [ctypes.c_int32 * k for k in range(5)]
+
+
 def _parts(outs, name, dtype, dev, B, T, C):
     """The pointers and channel counts of one [B, T, C] tensor or of a sequence of tensors
     [B, T, ...] that share the channels."""
     if isinstance(outs, torch.Tensor):
         outs = (outs,)
-    if not 1 <= len(outs) <= 4:
+    k = len(outs)
+    if not 1 <= k <= 4:
         raise ValueError(f"{name}: expected one to four tensors")
-    ptrs, counts = (ctypes.c_void_p * len(outs))(), (ctypes.c_int32 * len(outs))()
-    total = 0
+    ptrs, counts = [], []
     for i, o in enumerate(outs):
-        if o.dim() < 3 or o.shape[0] != B or o.shape[1] != T:
-            raise ValueError(f"{name}[{i}]: expected [{B}, {T}, ...], got {tuple(o.shape)}")
-        ptrs[i] = _need(o, f"{name}[{i}]", dtype, dev, o.shape)
-        n = o.shape[2]
-        for k in o.shape[3:]:
-            n *= k
-        counts[i] = n
-        total += n
-    if total != C:
-        raise ValueError(f"{name}: {total} channels, x has {C}")
-    return ptrs, counts, len(outs)
+        sh = o.shape
+        if len(sh) < 3 or sh[0] != B or sh[1] != T:
+            raise ValueError(f"{name}[{i}]: expected [{B}, {T}, ...], got {tuple(sh)}")
+        if o.dtype == dtype and o.device == dev and o.is_contiguous():
+            ptrs.append(o.data_ptr())
+        else:
+            _need(o, f"{name}[{i}]", dtype, dev, sh)
+        n = sh[2]
+        for m in sh[3:]:
+            n *= m
+        counts.append(n)
+    if sum(counts) != C:
+        raise ValueError(f"{name}: {sum(counts)} channels, x has {C}")
+    return _POINTERS[k](*ptrs), _COUNTS[k](*counts), k
 
 
 def _conv_common(x, weight, bias, activation):
@@ -374,7 +393,7 @@ def kda_prenorm_fwd(x, residual, weight, out, residual_out=None, *, res_scale=1.
     an fp32 tensor [D]."""
     dev, D, shape = x.device, x.shape[-1], x.shape
     dt = _row_dtype(x, "x")
-    xp = _need(x, "x", x.dtype, dev, shape)
+    xp = _own(x, "x")
     stream_t = residual if residual is not None else residual_out
     sdt = dt if stream_t is None else _row_dtype(stream_t, "residual")
     sty = x.dtype if stream_t is None else stream_t.dtype
@@ -412,7 +431,7 @@ def kda_prenorm_bwd(dout, dresidual_out, h, weight, x=None, workspace=None, *, r
     g["dx"] = g["dresidual"] if same else torch.empty(shape, dtype=dout.dtype, device=dev)
     if sp is not None:
         g["dres_scale"] = torch.empty((D,), dtype=_f32, device=dev)
-    _call("kda_prenorm_bwd", dev, stream, _need(dout, "dout", dout.dtype, dev, shape),
+    _call("kda_prenorm_bwd", dev, stream, _own(dout, "dout"),
           _opt(dresidual_out, "dresidual_out", h.dtype, dev, shape),
           _need(h, "h", h.dtype, dev, shape), _need(weight, "weight", _f32, dev, (D,)),
           None if sp is None else _need(x, "x", dout.dtype, dev, shape), sp, sv, eps,
@@ -445,7 +464,7 @@ def kda_postnorm_fwd(x, weight, gate, out, residual=None, *, res_scale=1.0, acti
         raise ValueError(f"activation must be one of {list(GATE_ACTIVATIONS)}")
     gp, gs, heads = _gate_args(gate, x, dev)
     sp, sv = _scale_args(res_scale, dev, D)
-    _call("kda_postnorm_fwd", dev, stream, _need(x, "x", x.dtype, dev, shape),
+    _call("kda_postnorm_fwd", dev, stream, _own(x, "x"),
           _need(weight, "weight", _f32, dev, (D,)), gp, gs, heads,
           _opt(residual, "residual", x.dtype, dev, shape), sp, sv, eps,
           GATE_ACTIVATIONS[activation], _need(out, "out", x.dtype, dev, shape),
@@ -473,7 +492,7 @@ def kda_postnorm_bwd(dout, x, weight, gate=None, workspace=None, *, res_scale=1.
     if sp is not None:
         g["dres_scale"] = torch.empty((D,), dtype=_f32, device=dev)
     _call("kda_postnorm_bwd", dev, stream, _need(dout, "dout", x.dtype, dev, shape),
-          _need(x, "x", x.dtype, dev, shape), _need(weight, "weight", _f32, dev, (D,)), gp, gs, heads,
+          _own(x, "x"), _need(weight, "weight", _f32, dev, (D,)), gp, gs, heads,
           sp, sv, eps, GATE_ACTIVATIONS[activation], g["dx"].data_ptr(),
           None if gate is None else g["dgate"].data_ptr(), g["dweight"].data_ptr(),
           None if sp is None else g["dres_scale"].data_ptr(), rows, D, dt, wp, wb)

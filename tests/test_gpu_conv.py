@@ -140,6 +140,21 @@ def test_backward_options(kda_lib, kw):
     check_bwd(kda, "packed", 256, 4, BF, **kw)
 
 
+@pytest.mark.parametrize("n", [150, 1500])
+@pytest.mark.parametrize("C", [64, 33])
+def test_many_sequences(kda_lib, n, C):
+    """More sequences than one search step tells apart, from empty to longer than a run."""
+    import itertools
+    import kimi_delta_attention_08_gb300 as kda
+    cu = list(itertools.accumulate([(7 * i * i + 3 * i) % 41 if i % 50 else 140 for i in range(n)], initial=0))
+    SEQS["many"] = (1, cu[-1] + 3, cu)
+    try:
+        check_fwd(kda, "many", C, 4, BF)
+        check_bwd(kda, "many", C, 4, BF)
+    finally:
+        del SEQS["many"]
+
+
 def test_backward_repeats_its_bits(kda_lib):
     import kimi_delta_attention_08_gb300 as kda
     a = check_bwd(kda, "long", 264, 4, BF)

@@ -207,6 +207,15 @@ def test_backward_with_saved_states(kda_lib, seq):
         assert torch.equal(g[0][nm], g[1][nm]) and torch.equal(g[0][nm], g[2][nm]), nm
 
 
+def test_many_sequences(kda_lib):
+    """More sequences than one search step tells apart, from empty to longer than a segment."""
+    import itertools
+    import kimi_delta_attention_08_gb300 as kda
+    cu = list(itertools.accumulate([(7 * i * i + 3 * i) % 41 if i % 50 else 300 for i in range(120)], initial=0))
+    check_fwd(kda, (1, cu[-1] + 5, cu), 24, 16, 1, F, saved=True)
+    check_bwd(kda, (1, cu[-1] + 5, cu), 24, 16, 1, F)
+
+
 def test_bf16_state_gradients(kda_lib):
     import kimi_delta_attention_08_gb300 as kda
     check_bwd(kda, "packed", 64, 16, 1, BF, sty=BF)
