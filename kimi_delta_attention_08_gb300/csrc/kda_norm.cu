@@ -17,7 +17,7 @@
 //
 // Device time, and bytes of the rows over it: forward before a block, 32,768 rows of 4,096
 // bf16 values with an fp32 residual, 238 us (6.8 TB/s); forward after one, 1,048,576 rows of
-// 128 bf16 with a gate, 141 us (5.7 TB/s); backward before a block, 32,768 x 4,096 bf16
+// 128 bf16 with a gate, 137 us (5.9 TB/s); backward before a block, 32,768 x 4,096 bf16
 // with a learned scale, 247 us (6.5 TB/s); backward after one, 74,097 rows of 1,001 fp32
 // with gate and scale (no 16-byte alignment, so single values), 298 us (5.0 TB/s).
 #include "kda_internal.h"
@@ -190,6 +190,9 @@ __global__ void __launch_bounds__(norm_threads(G, E, V)) prenorm_fwd_kernel(cons
 template <int G, int E, int V, typename T, typename TS>
 __global__ void __launch_bounds__(norm_threads(G, E, V)) postnorm_fwd_kernel(const NormParams p) {
   KDA_NORM_ROWS(G)
+  Vals<V> sw[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) sw[i] = mul_of(w[i], sc[i]);
   Raw<T, V> rx[E] = {}, rg[E] = {}, rr[E] = {};
   auto fetch_x = [&](int64_t at_row) {
     each(at_row, [&](int i, int64_t at) { load_vec(rx[i], p.a, at); });
@@ -214,9 +217,10 @@ __global__ void __launch_bounds__(norm_threads(G, E, V)) postnorm_fwd_kernel(con
     const float s = row_sum<G, false>(make_float2(sum_of(sq), 0.f), red, turn).x;
     const float rstd = rsqrtf(s * inv_d + p.eps);
     each(row, [&](int i, int64_t at) {
-      Vals<V> n = mul_of(mul_of(x[i], splat<V>(rstd)), w[i]), slope;
+      Vals<V> n = mul_of(mul_of(x[i], splat<V>(rstd)), sw[i]), slope;
       if (p.b) n = mul_of(n, gate_fn(values(rg[i]), p.fn, slope));
-      store_vec<T, V>(p.o0, at, fma_of(sc[i], n, values(rr[i])));
+      if (p.c) n = fma_of(n, splat<V>(1.f), values(rr[i]));
+      store_vec<T, V>(p.o0, at, n);
     });
     fetch_rest(row + stride);
   }
@@ -619,7 +623,8 @@ kda_status kda_prenorm_fwd(const void* x, const void* residual, const float* wei
   p.a = x, p.b = residual, p.o0 = out, p.o1 = residual_out;
   p.weight = weight, p.scale = res_scale, p.scale_value = res_scale_value, p.eps = eps;
   p.n_rows = rows, p.dim = dim;
-  return run_norm(pick_prenorm_fwd(n, dtype, stream_dtype), n, p, norm_grid(n, rows, num_sms, 32), 0, stream);
+  return run_norm(pick_prenorm_fwd(n, dtype, stream_dtype), n, p, norm_grid(n, rows, num_sms, 32), 0,
+                  stream);
 }
 
 kda_status kda_prenorm_bwd(const void* dout, const void* dresidual_out, const void* h,
@@ -687,7 +692,12 @@ kda_status kda_postnorm_fwd(const void* x, const float* weight, const void* gate
   p.gate_stride = gate ? gate_stride : dim, p.heads = gate ? heads : 1;
   p.weight = weight, p.scale = res_scale, p.scale_value = res_scale_value, p.eps = eps;
   p.n_rows = rows, p.dim = dim;
-  return run_norm(pick_postnorm_fwd(n, dtype, dtype), n, p, norm_grid(n, rows, num_sms, 32), 0, stream);
+  // bf16 rows of some lanes: as many blocks as run at once (2^27 gated values in rows of 128:
+  // 137 us, with eight times as many 140), while fp32 rows, twice the bytes for the same work,
+  // gain from more (7.0 TB/s against 6.4)
+  const int per_sm = n.G && dtype == KDA_ROW_BF16 ? 4 : 32;
+  return run_norm(pick_postnorm_fwd(n, dtype, dtype), n, p, norm_grid(n, rows, num_sms, per_sm), 0,
+                  stream);
 }
 
 kda_status kda_postnorm_bwd(const void* dout, const void* x, const float* weight, const void* gate,
