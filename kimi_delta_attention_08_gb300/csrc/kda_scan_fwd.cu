@@ -295,17 +295,19 @@ __global__ void scan_carry_kernel(const ScanParams p, int state) {
 }
 
 // Single tokens and prompts of a few: bound by HBM through the states.  A thread holds 4
-// states of a channel (a warp's lie in a row) for kStepSeqs sequences, whose states are all
-// in flight at once.  Of these sequences each of a channel's lanes owns OWN: it reads their
-// rows, computes their steps, hands those to the others, ends up with their dot products
-// and writes their outputs.  (One thread for all 16 states of a channel computes as little
-// but reads 64 bytes apart: 36.8 us for 256 sequences of 4,096 channels and 16 fp32 states,
-// where this takes 33.1 at 4.3 TB/s.)
+// states of a channel (a warp's lie in a row) for kStepSeqs sequences, whose states and rows
+// are all in flight at once.  Of these sequences each of a channel's lanes owns OWN: it
+// reads their rows, computes their steps, hands those to the others, ends up with their
+// dot products and writes their outputs.  256 sequences of 4,096 channels and 16 fp32 states
+// take 24.9 us (5.7 TB/s) in blocks of 7 per SM; with 8 it spills (29.2), with 5 too few
+// loads are in flight (36).  Before the rates were computed behind the last load it took
+// 33.1; one thread for all 16 states of a channel reads 64 bytes apart (36.8); CTAs that
+// stay, with the next states on their way into shared memory, take 32 to 43.
 constexpr int kStepSeqs = 4;
 constexpr int kStepTokens = 8;  // the longest such prompt
 
 template <typename T, int NS, bool VEC>
-__global__ void __launch_bounds__(128, 8) scan_step_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(128, NS == 8 ? 6 : 7) scan_step_kernel(const ScanParams p) {
   constexpr int SP = 4, LPC = NS / SP, OWN = LPC >= 4 ? 1 : 2, OWNERS = kStepSeqs / OWN;
   const int lane = threadIdx.x & 31;
   const unsigned tiles = (unsigned)p.tiles;  // 32-bit divisions: 64-bit ones cost as much as a token
@@ -317,40 +319,67 @@ __global__ void __launch_bounds__(128, 8) scan_step_kernel(const ScanParams p) {
   const int grp = p.groups == 1 ? 0 : ch / p.per;
   const int first = l % OWNERS * OWN;  // the sequences it owns
   const int64_t st_at = (int64_t)ch * NS + l * SP, st_seq = (int64_t)p.dim * NS;
-  pair h[kStepSeqs][2], A2[2];
+  // everything that the first token needs is asked for before anything is waited for
+  const int nq = min(kStepSeqs, p.N - n0);  // the others repeat the last one's rows
+  float v[kStepSeqs][SP] = {};
+  int64_t at = n0 * st_seq + st_at;
 #pragma unroll
-  for (int q = 0; q < kStepSeqs; ++q) {
-    float v[SP] = {};
-    if (p.init && n0 + q < p.N) load_state<SP>(v, p.init, (n0 + q) * st_seq + st_at, p.state_bf16);
-    h[q][0] = pr(v[0], v[1]), h[q][1] = pr(v[2], v[3]);
-  }
-  {
-    float a[SP];
-    load_rates<SP>(a, p.A_log, st_at);
-    A2[0] = pr(a[0], a[1]), A2[1] = pr(a[2], a[3]);
-  }
-  const float bias = p.dt_bias ? __ldg(p.dt_bias + ch) : 0.f, D = p.D ? __ldg(p.D + ch) : 0.f;
+  for (int q = 0; q < kStepSeqs; ++q, at += st_seq)
+    if (p.init && q < nq) load_state<SP>(v[q], p.init, at, p.state_bf16);
   const int T_ = (int)p.T;
-  for (int j = 0; j < T_; ++j) {
-    float x[OWN], v[OWN], z[OWN], delta[OWN], dx[OWN];
-    Raw<T, SP> rb[kStepSeqs], rc[kStepSeqs];
+  const int64_t t0 = (int64_t)n0 * T_;
+  const T *px[OWN], *pt[OWN], *pz[OWN];
+#pragma unroll
+  for (int k = 0; k < OWN; ++k) {
+    const int64_t t = t0 + (int64_t)min(first + k, nq - 1) * T_;
+    px[k] = static_cast<const T*>(p.x) + t * p.x_s + ch;
+    pt[k] = static_cast<const T*>(p.dt) + t * p.dt_s + ch;
+    pz[k] = static_cast<const T*>(p.z) + t * p.z_s + ch;
+  }
+  const T* pb = static_cast<const T*>(p.B) + t0 * p.b_s + grp * NS + l * SP;
+  const T* pc = static_cast<const T*>(p.C) + t0 * p.c_s + grp * NS + l * SP;
+  const int64_t b_step = T_ * p.b_s, c_step = T_ * p.c_s;
+  Raw<T, 1> rx[OWN], rt[OWN], rz[OWN];
+  Raw<T, SP> rb[kStepSeqs], rc[kStepSeqs];
+  auto rows = [&] {  // of the next token
 #pragma unroll
     for (int k = 0; k < OWN; ++k) {
-      const int64_t t = (int64_t)min(n0 + first + k, p.N - 1) * T_ + j;
-      x[k] = to_f(static_cast<const T*>(p.x)[t * p.x_s + ch]);
-      v[k] = to_f(static_cast<const T*>(p.dt)[t * p.dt_s + ch]) + bias;
-      z[k] = p.z ? to_f(static_cast<const T*>(p.z)[t * p.z_s + ch]) : 0.f;
+      load_row<T, 1, false>(rx[k], px[k], 1, 1);
+      load_row<T, 1, false>(rt[k], pt[k], 1, 1);
+      rz[k] = Raw<T, 1>{};
+      if (p.z) load_row<T, 1, false>(rz[k], pz[k], 1, 1);
+      px[k] += p.x_s, pt[k] += p.dt_s, pz[k] += p.z_s;
     }
+    const T *qb = pb, *qc = pc;
 #pragma unroll
     for (int q = 0; q < kStepSeqs; ++q) {
-      const int64_t t = (int64_t)min(n0 + q, p.N - 1) * T_ + j;
-      load_row<T, SP, VEC>(rb[q], static_cast<const T*>(p.B) + t * p.b_s + grp * NS + l * SP, 1, SP);
-      load_row<T, SP, VEC>(rc[q], static_cast<const T*>(p.C) + t * p.c_s + grp * NS + l * SP, 1, SP);
+      load_row<T, SP, VEC>(rb[q], qb, 1, SP);
+      load_row<T, SP, VEC>(rc[q], qc, 1, SP);
+      if (q + 1 < nq) qb += b_step, qc += c_step;
     }
+    pb += p.b_s, pc += p.c_s;
+  };
+  rows();
+  float log_a[SP];
+#pragma unroll
+  for (int i = 0; i < SP; ++i) log_a[i] = __ldg(p.A_log + st_at + i);
+  const float bias = p.dt_bias ? __ldg(p.dt_bias + ch) : 0.f, D = p.D ? __ldg(p.D + ch) : 0.f;
+  pair h[kStepSeqs][2];
+#pragma unroll
+  for (int q = 0; q < kStepSeqs; ++q) h[q][0] = pr(v[q][0], v[q][1]), h[q][1] = pr(v[q][2], v[q][3]);
+  const pair A2[2] = {pr(rate_of(log_a[0]), rate_of(log_a[1])), pr(rate_of(log_a[2]), rate_of(log_a[3]))};
+  T* po = static_cast<T*>(p.out) + (t0 + (int64_t)first * T_) * p.dim + ch;
+  for (int j = 0;; ++j) {
+    float x[OWN], z[OWN], delta[OWN], dx[OWN];
 #pragma unroll
     for (int k = 0; k < OWN; ++k) {
-      float ex;
-      delta[k] = softplus(v[k], ex);
+      float f[1], ex;
+      unpack(rx[k], f);
+      x[k] = f[0];
+      unpack(rz[k], f);
+      z[k] = f[0];
+      unpack(rt[k], f);
+      delta[k] = softplus(f[0] + bias, ex);
       dx[k] = delta[k] * x[k];
     }
     float y[kStepSeqs];
@@ -375,16 +404,17 @@ __global__ void __launch_bounds__(128, 8) scan_step_kernel(const ScanParams p) {
       for (int o = OWNERS; o < LPC; o <<= 1) y[k] += __shfl_xor_sync(0xffffffffu, y[k], o);
       y[k] = fmaf(D, x[k], y[k]);
       if (p.z) y[k] *= z[k] * sigmoid(z[k]);
-      const int n = n0 + first + k;
-      if (mine && l < OWNERS && n < p.N)
-        static_cast<T*>(p.out)[((int64_t)n * T_ + j) * p.dim + ch] = from_f<T>(y[k]);
+      if (mine && l < OWNERS && first + k < nq) po[(int64_t)(k * T_ + j) * p.dim] = from_f<T>(y[k]);
     }
+    if (j + 1 >= T_) break;
+    rows();
   }
   if (!p.fin || !mine) return;
+  at = n0 * st_seq + st_at;
 #pragma unroll
-  for (int q = 0; q < kStepSeqs; ++q) {
-    const float v[SP] = {un(h[q][0]).x, un(h[q][0]).y, un(h[q][1]).x, un(h[q][1]).y};
-    if (n0 + q < p.N) store_state<SP>(p.fin, (n0 + q) * st_seq + st_at, v, p.state_bf16);
+  for (int q = 0; q < kStepSeqs; ++q, at += st_seq) {
+    const float f[SP] = {un(h[q][0]).x, un(h[q][0]).y, un(h[q][1]).x, un(h[q][1]).y};
+    if (q < nq) store_state<SP>(p.fin, at, f, p.state_bf16);
   }
 }
 
