@@ -8,7 +8,7 @@
 //   dw[j] = sum_t dp[t] xx[t - W + 1 + j],   dbias = sum_t dp[t]
 //
 // Each value takes W multiplications, so the operator is bound by HBM: x is read once and
-// out written once.  A thread holds 16 bytes of channels and walks a run of consecutive
+// out written once.  A thread holds 16 bytes of channels and walks a run of 8 to 256
 // tokens with the last W - 1 rows in registers, so a row is loaded once per run, plus the
 // W - 1 rows before the run (its neighbour's, from L2).  The next rows are on their way
 // into shared memory meanwhile, asked for by the thread that reads them, so without a barrier.
@@ -16,7 +16,7 @@
 // Device time, and bytes of the rows over it (SiLU, width 4, bf16): 74,080 packed tokens of
 // 6,144 channels with states 285 us (6.4 TB/s; 413 with the next rows in registers); single
 // tokens of 256 sequences of 12,288 channels 9.8 us; backward of 32,768 tokens of 12,288
-// channels 467 us (5.2 TB/s; 636 with the rows in registers), which the FMA pipe's latency
+// channels 451 us (5.4 TB/s; 636 with the rows in registers), which the FMA pipe's latency
 // with 12 warps of 166 registers per SM keeps from the 356 us that its bytes take.
 #include "kda_internal.h"
 #include "kda_rows.cuh"
@@ -703,10 +703,20 @@ void (*conv_kernel(bool f32, bool dout_f32, bool vec, int width, int fn))(ConvPa
 }
 
 // Tokens per run.  A run loads W - 1 rows more than its own (the backward 2 (W - 1)) and
-// looks its sequence up, so long runs are cheaper where there are tokens enough.
-int64_t run_of(int64_t total, bool bwd) { return total >= 16384 ? (bwd ? 128 : 64) : 32; }
-int64_t row_blocks(int64_t total, bool bwd) {
-  const int64_t per = run_of(total, bwd) * kWarps;
+// looks its sequence up, so long runs are cheaper where there are values enough to fill the
+// GPU with them; short ones take less from their first token to their last.  Measured with
+// 8 to 256 tokens over 1,024, 4,096 and 12,288 bf16 channels, the best one follows the
+// number of values: forward, 0.5 million 4.7 us with 8 (32: 8.1), 8 million 10.4 with 32
+// (8: 13.4), 402 million 250 with 64 (32: 267); backward, 2 million 11.0 with 16 (8: 14.4),
+// 8 million 20.6 with 64 (32: 23.4), 402 million 446 with 256 (128: 464, 32: 643).
+int64_t run_of(int64_t total, int32_t C, bool bwd) {
+  const int64_t values = total * C, million = 1000000;
+  if (!bwd) return values < 3 * million ? 8 : values < 8 * million ? 16 : values < 20 * million ? 32 : 64;
+  return values < 3 * million / 2 ? 8 : values < 4 * million ? 16 : values < 7 * million ? 32
+         : values < 12 * million ? 64 : values < 300 * million ? 128 : 256;
+}
+int64_t row_blocks(int64_t total, int32_t C, bool bwd) {
+  const int64_t per = run_of(total, C, bwd) * kWarps;
   return (total + per - 1) / per;
 }
 
@@ -809,7 +819,7 @@ kda_status kda_conv_fwd(const void* x, int64_t x_stride, const float* weight, co
     p.run = (int32_t)T;
     p.runs = N;
   } else {
-    p.run = (int32_t)run_of(p.total, false);
+    p.run = (int32_t)run_of(p.total, C, false);
     p.runs = (p.total + p.run - 1) / p.run;
   }
   const int64_t per_block = kWarps * (step ? kStepSeqs : 1);
@@ -847,7 +857,7 @@ kda_status kda_conv_bwd_get_workspace_size(int64_t total_tokens, int32_t C, int3
       width > KDA_CONV_MAX_WIDTH)
     return KDA_ERR_INVALID_SHAPE;
   *bytes = KDA_STATUS_BYTES +
-           (size_t)kda::row_blocks(total_tokens, true) * (width + 1) * (size_t)C * sizeof(float);
+           (size_t)kda::row_blocks(total_tokens, C, true) * (width + 1) * (size_t)C * sizeof(float);
   return KDA_OK;
 }
 
@@ -884,10 +894,10 @@ kda_status kda_conv_bwd(const void* x, int64_t x_stride, const float* weight, co
   p.dfin = dfinal_state, p.dx = dx, p.dinit = dinitial_state;
   p.status = static_cast<unsigned*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + KDA_STATUS_BYTES);
-  p.run = (int32_t)run_of(p.total, true);
+  p.run = (int32_t)run_of(p.total, C, true);
   p.weight_vec = al_to(weight, 16);
   const int64_t tiles = (C + 32 * V - 1) / (32 * V);
-  const int64_t blocks = row_blocks(p.total, true);
+  const int64_t blocks = row_blocks(p.total, C, true);
   // empty sequences can only come with cu_seqlens or T = 0
   const int64_t state_blocks =
       dinitial_state && (cu_seqlens || T == 0) ? ((int64_t)N + kWarps - 1) / kWarps : 0;

@@ -5,7 +5,8 @@ wider rows, split outputs, channel counts off the vector width.
 Bounds: a pre-activation is a sum of width + 1 terms (5 roundings of 2^-24 at most); the
 activation adds the exponential (2^-22), a reciprocal and three products: under 16 steps
 of 2^-24 of the magnitudes of tests/layer_ref.py.  A weight's gradient is a sum over
-tokens, added 64 at a time, then by 4 and by row blocks: 80 steps and one per 256 tokens."""
+tokens, added a run at a time (8 to 32 tokens at these sizes), then by 4 and by row blocks,
+every 32nd together: 80 steps and one per 256 tokens."""
 import zlib
 
 import pytest
