@@ -497,10 +497,19 @@ int64_t norm_grid(const NormPlan& n, int64_t rows, int num_sms, int per_sm) {
   return need < most ? need : most;
 }
 
-using NormKernel = void (*)(NormParams);
+// A kernel, and on which devices its limit of dynamic shared memory has been raised.
+struct NormKernel {
+  void (*run)(NormParams);
+  bool (*raised)[64];
+};
+template <void (*KERNEL)(NormParams)>
+NormKernel norm_kernel() {
+  static bool raised[64];
+  return {KERNEL, &raised};
+}
 
 #define KDA_NORM_CASE(KERNEL, G_, E_, V_) \
-  if (n.G == G_ && n.E == E_ && n.V == V_) return KERNEL<G_, E_, V_, T, TS>;
+  if (n.G == G_ && n.E == E_ && n.V == V_) return norm_kernel<KERNEL<G_, E_, V_, T, TS>>();
 #define KDA_NORM_PICK(NAME, KERNEL)                                                \
   template <typename T, typename TS>                                               \
   NormKernel NAME##_of(const NormPlan& n) {                                        \
@@ -514,7 +523,7 @@ using NormKernel = void (*)(NormParams);
     KDA_NORM_CASE(KERNEL, 32, 2, 1)                                                \
     KDA_NORM_CASE(KERNEL, 0, 4, 1)                                                 \
     KDA_NORM_CASE(KERNEL, 0, 8, 1)                                                 \
-    return nullptr;                                                                \
+    return {};                                                                     \
   }                                                                                \
   NormKernel NAME(const NormPlan& n, int32_t dtype, int32_t stream_dtype) {        \
     if (dtype == KDA_ROW_FP32) return NAME##_of<float, float>(n);                  \
@@ -546,8 +555,8 @@ kda_status check_norm(int64_t rows, int32_t dim, int32_t dtype, int32_t stream_d
 
 kda_status run_norm(NormKernel kernel, const NormPlan& n, const NormParams& p,
                     int64_t grid, size_t smem, cudaStream_t stream) {
-  if (!kernel) return KDA_ERR_INVALID_SHAPE;
-  kernel<<<(unsigned)grid, n.threads, smem, stream>>>(p);
+  if (!kernel.run) return KDA_ERR_INVALID_SHAPE;
+  kernel.run<<<(unsigned)grid, n.threads, smem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -562,9 +571,12 @@ kda_status run_norm_bwd(NormKernel kernel, const NormPlan& n, NormParams& p, int
   if (grid > kMaxBlocks) grid = kMaxBlocks;
   const size_t smem = n.G ? 2 * (size_t)p.dim * sizeof(float)
                           : ring ? (size_t)kNormRing * n.threads * ring_bytes : 0;
-  if (smem > 40 * 1024 &&  // 48 KB with the static part need no request
-      cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  // The limit belongs to the kernel, for all threads of the host: raised once to the most that
+  // a block of 512 threads takes, never to this call's own size.  (No instance but those with
+  // a ring goes beyond what needs no request.)
+  if (ring && kernel.run &&
+      ensure_smem_attr(reinterpret_cast<const void*>(kernel.run), kNormRing * 512 * ring_bytes,
+                       *kernel.raised) != cudaSuccess)
     return KDA_ERR_CUDA;
   if (grid > 0) {
     const kda_status st = run_norm(kernel, n, p, grid, smem, stream);
