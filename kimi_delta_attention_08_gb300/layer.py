@@ -6,11 +6,12 @@ As in the rest of the binding, arguments are only checked and passed on: every
 tensor has to have the documented dtype, device and layout.  Row arguments marked
 "rows" may be a slice of a wider projection's output (contiguous channels, tokens
 one fixed stride apart).  Work goes to torch's current stream of the tensors'
-device, or to `stream`.
+device, or to `stream`; what is allocated for it then comes from that stream's memory.
 """
 from __future__ import annotations
 
 import ctypes
+from contextlib import nullcontext
 
 import torch
 
@@ -120,28 +121,44 @@ def _call(name, dev, stream, *args):
         _raise(status, name)
 
 
+def _pool(stream, dev):
+    """A context whose new tensors come from the memory of the stream that will write them.  A
+    block of the current stream's memory may still be read by work that is queued there, which
+    another stream does not wait for."""
+    if stream is None:
+        return nullcontext()
+    if dev.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
+
+
+def _results(stream, dev, grads):
+    """Results in another stream's memory live until the current stream is done with them, and
+    a caller's workspace until the other one is."""
+    if stream is not None:
+        here = torch.cuda.current_stream(dev)
+        for t in grads.values():
+            t.record_stream(here)
+            if isinstance(stream, torch.cuda.Stream):
+                t.record_stream(stream)
+    return grads
+
+
 def _workspace(given, size, dev, stream):
-    """(tensor, pointer, bytes): the caller's workspace, or one of size() bytes from torch's
-    allocator that lives as long as the work on this call's stream."""
+    """(tensor, pointer, bytes): the caller's workspace, or one of size() bytes of the stream's
+    memory (the caller of this function is within _pool)."""
     if given is None:
         if dev.type != "cuda":
             raise ValueError("expected CUDA tensors")
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
             raise ValueError("workspace: required with a raw stream handle")
         given = torch.empty(size(), dtype=torch.uint8, device=dev)
-        if stream is not None:
-            given.record_stream(stream)
     elif given.dtype != torch.uint8 or given.device != dev or not given.is_contiguous():
         raise ValueError("workspace: expected a contiguous uint8 tensor on the tensors' device")
     return given, given.data_ptr(), given.numel()
-
-
-def _results(stream, grads):
-    """New tensors that another stream than the current one writes live until it has."""
-    if isinstance(stream, torch.cuda.Stream):
-        for t in grads.values():
-            t.record_stream(stream)
-    return grads
 
 
 def _size(fn, *args):
@@ -245,19 +262,20 @@ def kda_conv_bwd(x, weight, bias, dout, initial_state=None, dfinal_state=None, c
     st = (N, W - 1, C)
     ip = _opt(initial_state, "initial_state", x.dtype, dev, st)
     dfp = _opt(dfinal_state, "dfinal_state", x.dtype, dev, st)
-    ws, wp, wb = _workspace(workspace, lambda: _size("kda_conv_bwd_get_workspace_size", B * T, C, W),
-                            dev, stream)
-    g = {"dx": torch.empty((B, T, C), dtype=x.dtype, device=dev),
-         "dweight": torch.empty((C, W), dtype=_f32, device=dev)}
-    if b is not None:
-        g["dbias"] = torch.empty((C,), dtype=_f32, device=dev)
-    if ip is not None:
-        g["dinitial_state"] = torch.empty(st, dtype=_f32, device=dev)
+    with _pool(stream, dev):
+        ws, wp, wb = _workspace(workspace, lambda: _size("kda_conv_bwd_get_workspace_size", B * T, C, W),
+                                dev, stream)
+        g = {"dx": torch.empty((B, T, C), dtype=x.dtype, device=dev),
+             "dweight": torch.empty((C, W), dtype=_f32, device=dev)}
+        if b is not None:
+            g["dbias"] = torch.empty((C,), dtype=_f32, device=dev)
+        if ip is not None:
+            g["dinitial_state"] = torch.empty(st, dtype=_f32, device=dev)
     P = lambda nm: g[nm].data_ptr() if nm in g else None
     _call("kda_conv_bwd", dev, stream, xp, xs, w, b, ptrs, counts, k, ddt, ip, dfp, cu, P("dx"),
           P("dweight"), P("dbias"), P("dinitial_state"), B, T, C, N, W, fn, dt, wp, wb)
     g["workspace"] = ws
-    return _results(stream, g)
+    return _results(stream, dev, g)
 
 
 # --------------------------------------------------------------------- scan --
@@ -345,8 +363,9 @@ def kda_scan_fwd(x, dt, A_log, B, C, out, D=None, z=None, dt_bias=None, initial_
     cp, cb = _states_arg(chunk_states, dev)
     wp = wb = 0
     if workspace is not None or q.T > 8 or q.cu_seqlens or cp:
-        _, wp, wb = _workspace(workspace, lambda: _size("kda_scan_get_workspace_size", ctypes.byref(q)),
-                               dev, stream)
+        with _pool(stream, dev):
+            _, wp, wb = _workspace(workspace, lambda: _size("kda_scan_get_workspace_size", ctypes.byref(q)),
+                                   dev, stream)
     _call("kda_scan_fwd", dev, stream, ctypes.byref(q), op, fp, cp, cb, wp, wb)
 
 
@@ -362,24 +381,25 @@ def kda_scan_bwd(x, dt, A_log, B, C, dout, D=None, z=None, dt_bias=None, initial
     dev, ty = x.device, x.dtype
     dop = _need(dout, "dout", ty, dev, x.shape)
     cp, cb = _states_arg(chunk_states, dev)
-    ws, wp, wb = _workspace(workspace, lambda: _size("kda_scan_bwd_get_workspace_size",
-                                                     ctypes.byref(q), int(cp is not None)), dev, stream)
     E = lambda shape, t=_f32: torch.empty(shape, dtype=t, device=dev)
-    g = {"dx": E(x.shape, ty), "ddt": E(x.shape, ty), "dB": E(B.shape, ty), "dC": E(B.shape, ty),
-         "dA_log": E(A_log.shape)}
-    if z is not None:
-        g["dz"] = E(x.shape, ty)
-    if D is not None:
-        g["dD"] = E((q.dim,))
-    if dt_bias is not None:
-        g["ddt_bias"] = E((q.dim,))
-    if initial_state is not None:
-        g["dinitial_state"] = E(initial_state.shape)
+    with _pool(stream, dev):
+        ws, wp, wb = _workspace(workspace, lambda: _size("kda_scan_bwd_get_workspace_size",
+                                                         ctypes.byref(q), int(cp is not None)), dev, stream)
+        g = {"dx": E(x.shape, ty), "ddt": E(x.shape, ty), "dB": E(B.shape, ty), "dC": E(B.shape, ty),
+             "dA_log": E(A_log.shape)}
+        if z is not None:
+            g["dz"] = E(x.shape, ty)
+        if D is not None:
+            g["dD"] = E((q.dim,))
+        if dt_bias is not None:
+            g["ddt_bias"] = E((q.dim,))
+        if initial_state is not None:
+            g["dinitial_state"] = E(initial_state.shape)
     P = lambda nm: g[nm].data_ptr() if nm in g else None
     _call("kda_scan_bwd", dev, stream, ctypes.byref(q), dop, dfp, cp, cb, P("dx"), P("ddt"), P("dz"),
           P("dB"), P("dC"), P("dA_log"), P("dD"), P("ddt_bias"), P("dinitial_state"), wp, wb)
     g["workspace"] = ws
-    return _results(stream, g)
+    return _results(stream, dev, g)
 
 
 # -------------------------------------------------------------------- norms --
@@ -423,14 +443,15 @@ def kda_prenorm_bwd(dout, dresidual_out, h, weight, x=None, workspace=None, *, r
     if sp is not None and x is None:
         raise ValueError("x: needed for the gradient of a per-channel res_scale")
     rows = dout.numel() // D if D else 0
-    ws, wp, wb = _workspace(workspace, lambda: _size("kda_norm_bwd_get_workspace_size", rows, D), dev,
-                            stream)
-    g = {"dresidual": torch.empty(shape, dtype=h.dtype, device=dev),
-         "dweight": torch.empty((D,), dtype=_f32, device=dev)}
     same = sp is None and sv == 1.0 and dt == sdt
-    g["dx"] = g["dresidual"] if same else torch.empty(shape, dtype=dout.dtype, device=dev)
-    if sp is not None:
-        g["dres_scale"] = torch.empty((D,), dtype=_f32, device=dev)
+    with _pool(stream, dev):
+        ws, wp, wb = _workspace(workspace, lambda: _size("kda_norm_bwd_get_workspace_size", rows, D), dev,
+                                stream)
+        g = {"dresidual": torch.empty(shape, dtype=h.dtype, device=dev),
+             "dweight": torch.empty((D,), dtype=_f32, device=dev)}
+        g["dx"] = g["dresidual"] if same else torch.empty(shape, dtype=dout.dtype, device=dev)
+        if sp is not None:
+            g["dres_scale"] = torch.empty((D,), dtype=_f32, device=dev)
     _call("kda_prenorm_bwd", dev, stream, _own(dout, "dout"),
           _opt(dresidual_out, "dresidual_out", h.dtype, dev, shape),
           _need(h, "h", h.dtype, dev, shape), _need(weight, "weight", _f32, dev, (D,)),
@@ -438,7 +459,7 @@ def kda_prenorm_bwd(dout, dresidual_out, h, weight, x=None, workspace=None, *, r
           None if same else g["dx"].data_ptr(), g["dresidual"].data_ptr(), g["dweight"].data_ptr(),
           None if sp is None else g["dres_scale"].data_ptr(), rows, D, dt, sdt, wp, wb)
     g["workspace"] = ws
-    return _results(stream, g)
+    return _results(stream, dev, g)
 
 
 def _gate_args(gate, x, dev):
@@ -483,18 +504,19 @@ def kda_postnorm_bwd(dout, x, weight, gate=None, workspace=None, *, res_scale=1.
     gp, gs, heads = _gate_args(gate, x, dev)
     sp, sv = _scale_args(res_scale, dev, D)
     rows = x.numel() // D if D else 0
-    ws, wp, wb = _workspace(workspace, lambda: _size("kda_norm_bwd_get_workspace_size", rows, D), dev,
-                            stream)
-    g = {"dx": torch.empty(shape, dtype=x.dtype, device=dev),
-         "dweight": torch.empty((D,), dtype=_f32, device=dev)}
-    if gate is not None:
-        g["dgate"] = torch.empty(shape, dtype=x.dtype, device=dev)
-    if sp is not None:
-        g["dres_scale"] = torch.empty((D,), dtype=_f32, device=dev)
+    with _pool(stream, dev):
+        ws, wp, wb = _workspace(workspace, lambda: _size("kda_norm_bwd_get_workspace_size", rows, D), dev,
+                                stream)
+        g = {"dx": torch.empty(shape, dtype=x.dtype, device=dev),
+             "dweight": torch.empty((D,), dtype=_f32, device=dev)}
+        if gate is not None:
+            g["dgate"] = torch.empty(shape, dtype=x.dtype, device=dev)
+        if sp is not None:
+            g["dres_scale"] = torch.empty((D,), dtype=_f32, device=dev)
     _call("kda_postnorm_bwd", dev, stream, _need(dout, "dout", x.dtype, dev, shape),
           _own(x, "x"), _need(weight, "weight", _f32, dev, (D,)), gp, gs, heads,
           sp, sv, eps, GATE_ACTIVATIONS[activation], g["dx"].data_ptr(),
           None if gate is None else g["dgate"].data_ptr(), g["dweight"].data_ptr(),
           None if sp is None else g["dres_scale"].data_ptr(), rows, D, dt, wp, wb)
     g["workspace"] = ws
-    return _results(stream, g)
+    return _results(stream, dev, g)

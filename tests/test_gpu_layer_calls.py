@@ -61,3 +61,49 @@ def test_two_widths_from_two_threads(kda_lib, op, monkeypatch):
     for g, w in zip(got, want):
         for k in w:
             assert torch.equal(g[k], w[k]), k
+
+
+def backward(kda, op):
+    """A call that allocates what it returns, as a function of (stream, workspace), and a
+    workspace for it."""
+    g = torch.Generator().manual_seed(3)
+    T, C = 300, 256
+    r = lambda *s, t=BF: torch.randn(*s, generator=g).to(t).cuda()  # noqa: E731
+    x, dt, z, dout = (r(2, T, C) for _ in range(4))
+    w, b, B, Cm = r(C, 4, t=F), r(C, t=F), r(2, T, 1, 16), r(2, T, 1, 16)
+    A, wn, init, st = r(C, 16, t=F), r(C, t=F), r(2, 3, C), r(2, C, 16, t=F)
+    kw = lambda s, ws: dict(stream=s, workspace=ws)  # noqa: E731
+    if op == "conv":
+        return (lambda s, ws: kda.kda_conv_bwd(x, w, b, dout, init, **kw(s, ws)),
+                kda.make_conv_bwd_workspace(2 * T, C, 4))
+    if op == "scan":
+        return (lambda s, ws: kda.kda_scan_bwd(x, dt, A, B, Cm, dout, wn, z, b, st, **kw(s, ws)),
+                kda.make_scan_workspace(2, T, C, 16, backward=True))
+    ws = kda.make_norm_bwd_workspace(2 * T, C)
+    if op == "prenorm":
+        return lambda s, ws: kda.kda_prenorm_bwd(dout, None, x, wn, z, res_scale=b, **kw(s, ws)), ws
+    return lambda s, ws: kda.kda_postnorm_bwd(dout, x, wn, z, res_scale=b, **kw(s, ws)), ws
+
+
+@pytest.mark.parametrize("op", ["conv", "scan", "prenorm", "postnorm"])
+@pytest.mark.parametrize("raw", [False, True])
+def test_results_do_not_take_memory_that_is_still_read(kda_lib, op, raw):
+    """Tensors that were freed while the current stream still has to read them: a call on
+    another stream (an object, or a raw handle with a workspace) right after that must not
+    write its results there."""
+    import kimi_delta_attention_08_gb300 as kda
+    run, ws = backward(kda, op)
+    want = {k: v.clone() for k, v in run(None, None).items() if k != "workspace"}
+    sizes = [v.numel() * v.element_size() for v in want.values()] + [ws.numel()]
+    s = torch.cuda.Stream()
+    old = [(torch.arange(n, device="cuda") % 251).to(torch.uint8) for n in sizes * 2]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)                       # some 50 ms
+    kept = [t.clone() for t in old]                      # queued behind it
+    del old
+    got = run(s.cuda_stream, ws) if raw else run(s, None)
+    torch.cuda.synchronize()
+    for t, n in zip(kept, sizes * 2):
+        assert torch.equal(t, (torch.arange(n, device="cuda") % 251).to(torch.uint8))
+    for k, v in want.items():
+        assert torch.equal(got[k], v), k

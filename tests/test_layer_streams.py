@@ -1,0 +1,113 @@
+"""Which stream's memory the layer operators' results come from, checked on the host: streams,
+allocations and the library's call are stand-ins, nothing reaches a GPU."""
+from contextlib import contextmanager
+
+import pytest
+import torch
+
+from kimi_delta_attention_08_gb300 import layer
+
+CUDA = torch.device("cuda", 0)
+
+
+class Stream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+@pytest.fixture
+def seen(monkeypatch):
+    """Every allocation as [handle of the stream that is current then, recorded streams]."""
+    now, made = [100], []
+    real = torch.empty
+
+    @contextmanager
+    def stream(s):
+        now.append(s.cuda_stream)
+        yield
+        now.pop()
+
+    class Result:
+        def __init__(self, entry):
+            self.entry = entry
+
+        def data_ptr(self):
+            return 256
+
+        def numel(self):
+            return 1 << 30
+
+        def record_stream(self, s):
+            self.entry[1].append(s.cuda_stream)
+
+    def empty(*size, dtype=None, device=None, **kw):
+        if device != CUDA:
+            return real(*size, dtype=dtype, device=device, **kw)
+        made.append([now[-1], []])
+        return Result(made[-1])
+
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream(handle))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: Stream(0))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(now[-1]))
+    monkeypatch.setattr(layer, "_call", lambda *a: None)
+    monkeypatch.setattr(layer, "_size", lambda *a: 1 << 20)
+    return made
+
+
+class Tensor:
+    """What the binding reads of a contiguous tensor on the GPU."""
+    device = CUDA
+
+    def __init__(self, *shape, dtype=torch.float32):
+        self.shape, self.dtype = torch.Size(shape), dtype
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def is_contiguous(self):
+        return True
+
+    def stride(self):
+        return torch.empty(self.shape, device="meta").stride()
+
+    def data_ptr(self):
+        return 256
+
+    def record_stream(self, s):
+        pass
+
+
+def calls(stream, workspace):
+    x, w, b = Tensor(2, 5, 8), Tensor(8, 4), Tensor(8)
+    B, A, ini, st = Tensor(2, 5, 1, 16), Tensor(8, 16), Tensor(2, 3, 8), Tensor(2, 8, 16)
+    kw = dict(stream=stream, workspace=workspace)
+    return {"conv": lambda: layer.kda_conv_bwd(x, w, b, (x,), ini, **kw),
+            "scan": lambda: layer.kda_scan_bwd(x, x, A, B, B, x, b, x, b, st, **kw),
+            "prenorm": lambda: layer.kda_prenorm_bwd(x, None, x, b, res_scale=0.5, **kw),
+            "postnorm": lambda: layer.kda_postnorm_bwd(x, x, b, x, res_scale=0.5, **kw)}
+
+
+@pytest.mark.parametrize("op", ["conv", "scan", "prenorm", "postnorm"])
+def test_results_come_from_the_stream_that_writes_them(seen, op):
+    calls(None, None)[op]()
+    assert len(seen) > 2 and all(e == [100, []] for e in seen)
+    seen.clear()
+    calls(Stream(7), None)[op]()
+    assert len(seen) > 2 and all(h == 7 and 100 in r for h, r in seen), seen
+    for handle in (7, 0):
+        seen.clear()
+        calls(handle, Tensor(1 << 20, dtype=torch.uint8))[op]()
+        assert len(seen) > 1 and all(h == handle for h, _ in seen), seen
+        assert all(r == [100] for _, r in seen)
+
+
+def test_workspace_of_a_forward_call(seen):
+    x, A, B = Tensor(2, 50, 8), Tensor(8, 16), Tensor(2, 50, 1, 16)
+    layer.kda_scan_fwd(x, x, A, B, B, x, stream=Stream(7))
+    assert seen == [[7, []]]
