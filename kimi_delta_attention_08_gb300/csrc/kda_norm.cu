@@ -90,11 +90,16 @@ __device__ __forceinline__ float2 row_sum(float2 v, float2* red, int turn) {
   return v;
 }
 
-// The gate's activation and its slope.
+// The gate's activation, and with its slope.
+template <int V>
+__device__ __forceinline__ Vals<V> gate_fn(const Vals<V>& p, int fn) {
+  const Vals<V> s = sigmoid(p);
+  return fn == KDA_FN_SILU ? mul_of(p, s) : s;
+}
 template <int V>
 __device__ __forceinline__ Vals<V> gate_fn(const Vals<V>& p, int fn, Vals<V>& slope) {
-  const Vals<V> s = sigmoid(p);
-  const Vals<V> ds = fma_of(mul_of(s, splat<V>(-1.f)), s, s);  // s (1 - s)
+  Vals<V> ds;
+  const Vals<V> s = sigmoid(p, ds);
   slope = ds;
   if (fn != KDA_FN_SILU) return s;
   slope = fma_of(p, ds, s);
@@ -217,8 +222,8 @@ __global__ void __launch_bounds__(norm_threads(G, E, V)) postnorm_fwd_kernel(con
     const float s = row_sum<G, false>(make_float2(sum_of(sq), 0.f), red, turn).x;
     const float rstd = rsqrtf(s * inv_d + p.eps);
     each(row, [&](int i, int64_t at) {
-      Vals<V> n = mul_of(mul_of(x[i], splat<V>(rstd)), sw[i]), slope;
-      if (p.b) n = mul_of(n, gate_fn(values(rg[i]), p.fn, slope));
+      Vals<V> n = mul_of(mul_of(x[i], splat<V>(rstd)), sw[i]);
+      if (p.b) n = mul_of(n, gate_fn(values(rg[i]), p.fn));
       if (p.c) n = fma_of(n, splat<V>(1.f), values(rr[i]));
       store_vec<T, V>(p.o0, at, n);
     });

@@ -5,6 +5,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <cfloat>
 #include <cstdint>
 
 #include "kda_ptx.cuh"
@@ -181,6 +182,21 @@ __device__ __forceinline__ pair sigmoid(pair x) {
 }
 __device__ __forceinline__ pair silu(pair x) { return pmul(x, sigmoid(x)); }
 
+// sigmoid(x) and its slope sigmoid(x) sigmoid(-x) = e s^2 with e = exp(-x).  As s - s^2 it would
+// lose its digits where s nears 1: all of them from x = 17 on.  (An infinite e meets s = 0.)
+__device__ __forceinline__ float sigmoid(float x, float& slope) {
+  const float e = ptx::ex2_approx(-x * kLog2e), s = ptx::rcp_approx(1.0f + e);
+  slope = fminf(e, FLT_MAX) * s * s;
+  return s;
+}
+__device__ __forceinline__ pair sigmoid(pair x, pair& slope) {
+  const pair e = pex2(pmul(x, pr(-kLog2e)));
+  const float2 d = un(padd(e, pr(1.0f)));
+  const pair s = pr(ptx::rcp_approx(d.x), ptx::rcp_approx(d.y));
+  slope = pmul(pmul(pr(fminf(un(e).x, FLT_MAX), fminf(un(e).y, FLT_MAX)), s), s);
+  return s;
+}
+
 // V fp32 values that are computed with together: in pairs, or one alone.
 template <int V>
 struct Vals {
@@ -228,6 +244,17 @@ __device__ __forceinline__ Vals<V> sigmoid(const Vals<V>& x) {
   } else {
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) r.v[i] = sigmoid(x.v[i]);
+  }
+  return r;
+}
+template <int V>
+__device__ __forceinline__ Vals<V> sigmoid(const Vals<V>& x, Vals<V>& slope) {
+  Vals<V> r;
+  if constexpr (V == 1) {
+    r.v[0] = sigmoid(x.v[0], slope.v[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) r.v[i] = sigmoid(x.v[i], slope.v[i]);
   }
   return r;
 }
