@@ -491,10 +491,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(const ConvParams 
         pre_activation<W, V>(w, b, h, x, s);
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) {
-          const pair g = sigmoid(s[i]);
-          // g (1 + s (1 - g)) = g + s g - (s g) g
-          const pair sg = pmul(s[i], g);
-          d[i] = pmul(d[i], pfma(pmul(sg, pr(-1.f)), g, padd(g, sg)));
+          d[i] = pmul(d[i], silu_slope(s[i], sigmoid(s[i])));
         }
       }
       if (sum) {

@@ -182,6 +182,13 @@ __device__ __forceinline__ pair sigmoid(pair x) {
 }
 __device__ __forceinline__ pair silu(pair x) { return pmul(x, sigmoid(x)); }
 
+// silu'(x) = s + x s (1 - s) from s = sigmoid(x).  1 - s is within 2^-23, and zero once s is 1
+// (x = 17), so the slope is within 17 such steps of 1 however large x is; expanded to
+// s + x s - x s^2 its error would grow with x.
+__device__ __forceinline__ pair silu_slope(pair x, pair s) {
+  return pfma(pmul(x, s), pfma(s, pr(-1.0f), pr(1.0f)), s);
+}
+
 // sigmoid(x) and its slope sigmoid(x) sigmoid(-x) = e s^2 with e = exp(-x).  As s - s^2 it would
 // lose its digits where s nears 1: all of them from x = 17 on.  (An infinite e meets s = 0.)
 __device__ __forceinline__ float sigmoid(float x, float& slope) {

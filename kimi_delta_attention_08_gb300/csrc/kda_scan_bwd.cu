@@ -364,9 +364,7 @@ __global__ void __launch_bounds__(BwdShape<T, NS>::NT, 384 / BwdShape<T, NS>::NT
         if (p.z) {
           const pair z2 = pr(zv[i], zv[i + 1]), sz = sigmoid(z2), zs = pmul(z2, sz);
           dy = pmul(o2, zs);
-          // silu' = s + z s - (z s) s
-          const pair slope = pfma(pmul(zs, pr(-1.f)), sz, padd(sz, zs));
-          dz2 = pmul(pmul(o2, pfma(sk, x2, yi)), slope);
+          dz2 = pmul(pmul(o2, pfma(sk, x2, yi)), silu_slope(z2, sz));
         }
         const pair dx2 = pfma(d, qi, pmul(dy, sk)), dt2 = pmul(pfma(x2, qi, si), sig);
         const float2 sd = un(pmul(dy, x2));

@@ -44,3 +44,53 @@ def test_gate_gradient_near_saturation(kda_lib, ty, act, D):
     du = R.d(dout) * R.d(x) / torch.sqrt((R.d(x) ** 2).mean(-1, keepdim=True) + 1e-6) * R.d(w)
     ref, part = (du * ds, du.abs() * ds) if act == "sigmoid" else (du * (s + p * ds), du.abs() * (s + p.abs() * ds))
     within(r["dgate"], ref, part, 64 + 1.5 * p.abs(), "dgate")
+
+
+LARGE = [3.0, 12.0, 17.0, 30.0, 1e3, 12345.678, 1e6, 1e8]
+
+
+def silu_bounds(p):
+    """silu'(p), and the error of s + p s (1 - s) from an s that is off by 8 + 1.5 |p| steps of
+    itself (none where it has rounded to 1) and 1 - s by two steps of 1, p itself exact."""
+    s, c = R.sig(p), R.sig(-p)
+    live = p < 18
+    rel = torch.where(live, 8 + 1.5 * p.abs(), torch.zeros_like(p))
+    steps = s * (rel + 4) + (p * s).abs() * (c * (rel + 4) + torch.where(live, s * rel + 2, 0 * p))
+    # beyond, 1 - s is zero: what is left out is p c
+    return s + p * s * c, steps + torch.where(live, 0 * p, (p * c).abs() * 2.0 ** 24)
+
+
+@pytest.mark.parametrize("C", [64, 37])
+def test_convolution_slope_at_large_arguments(kda_lib, C):
+    """Width 2 with weights (0, 1): the pre-activation is x itself and dx = dout silu'(x)."""
+    import kimi_delta_attention_08_gb300 as kda
+    g = torch.Generator().manual_seed(C)
+    v = torch.tensor(LARGE + [-x for x in LARGE])
+    x = v[torch.randint(len(v), (1, 200, C), generator=g)].cuda()
+    w = torch.tensor([0.0, 1.0]).repeat(C, 1).cuda()
+    dout = torch.randn(1, 200, C, generator=g).cuda()
+    r = kda.kda_conv_bwd(x, w, None, dout)
+    slope, steps = silu_bounds(R.d(x))
+    ref = R.d(dout) * slope
+    within(r["dx"], ref, R.d(dout).abs(), steps + 2, "dx")
+    # dweight[1] = sum dout silu' x: as large as x, each term to its own error
+    t = ref * R.d(x)
+    err = (R.d(dout) * R.d(x)).abs() * (steps + 2)
+    within(r["dweight"][:, 1], t.sum((0, 1)), t.abs().sum((0, 1)).clamp(min=1e-30),
+           80 + err.sum((0, 1)) / t.abs().sum((0, 1)).clamp(min=1e-30), "dweight")
+
+
+@pytest.mark.parametrize("dim", [64, 33])
+def test_scan_gate_slope_at_large_arguments(kda_lib, dim):
+    """Steps of zero and D = 1: y = x, so dz = dout x silu'(z)."""
+    import kimi_delta_attention_08_gb300 as kda
+    g = torch.Generator().manual_seed(dim)
+    v = torch.tensor(LARGE + [-x for x in LARGE])
+    z = v[torch.randint(len(v), (2, 50, dim), generator=g)].cuda()
+    x, dout = (torch.randn(2, 50, dim, generator=g).cuda() for _ in range(2))
+    B = torch.randn(2, 50, 1, 16, generator=g).cuda()
+    r = kda.kda_scan_bwd(x, torch.full_like(x, -200.0), torch.zeros(dim, 16, device="cuda"), B, B, dout,
+                         torch.ones(dim, device="cuda"), z)
+    slope, steps = silu_bounds(R.d(z))
+    du = R.d(dout) * R.d(x)
+    within(r["dz"], du * slope, du.abs(), steps + 4, "dz")
