@@ -188,10 +188,10 @@ __device__ __forceinline__ void load_xx(const ConvParams& p, const Chan<V, VEC>&
   if (pos >= 0)
     load_row<T, V, VEC>(r, static_cast<const T*>(p.x) + (bos + pos) * p.x_stride + ch.c0, ch.step,
                         p.C - ch.c0);
-  else if (p.init && pos >= 1 - W)
-    load_row<T, V, VEC>(r,
-                        static_cast<const T*>(p.init) + ((int64_t)n * (W - 1) + pos + W - 1) * p.C + ch.c0,
-                        ch.step, p.C - ch.c0);
+  else if (p.init && pos >= 1 - W)  // the final state may be this buffer
+    load_row<T, V, VEC, true>(r,
+                              static_cast<const T*>(p.init) + ((int64_t)n * (W - 1) + pos + W - 1) * p.C + ch.c0,
+                              ch.step, p.C - ch.c0);
 }
 
 // A thread's rows on their way through shared memory: kRing slots, a group of copies for
@@ -377,10 +377,10 @@ __global__ void __launch_bounds__(32 * kWarps) conv_step_kernel(const ConvParams
     if (n >= p.N) continue;
 #pragma unroll
     for (int r = 0; r < W - 1; ++r)
-      if (p.init)
-        load_row<T, V, VEC>(rows[q][r],
-                            static_cast<const T*>(p.init) + ((int64_t)n * (W - 1) + r) * p.C + ch.c0,
-                            ch.step, p.C - ch.c0);
+      if (p.init)  // the final state may be this buffer
+        load_row<T, V, VEC, true>(rows[q][r],
+                                  static_cast<const T*>(p.init) + ((int64_t)n * (W - 1) + r) * p.C + ch.c0,
+                                  ch.step, p.C - ch.c0);
     load_row<T, V, VEC>(rows[q][W - 1], static_cast<const T*>(p.x) + (int64_t)n * p.x_stride + ch.c0,
                         ch.step, p.C - ch.c0);
   }

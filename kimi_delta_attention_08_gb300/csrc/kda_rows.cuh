@@ -102,19 +102,21 @@ __device__ __forceinline__ void pack(Raw<T, V>& r, const float (&f)[V]) {
 // V elements of a row that one thread holds: consecutive on the vector path (VEC),
 // `step` elements apart on the scalar path (a warp's loads stay contiguous), where
 // elements at or past `left` read as zero and are not written.
-template <typename T, int V, bool VEC>
+template <typename T, int V, bool VEC, bool INPLACE = false>
 __device__ __forceinline__ void load_row(Raw<T, V>& r, const T* p, int step, int64_t left) {
   if constexpr (VEC) {
-    load_words(r.w, p);
+    load_words<INPLACE>(r.w, p);
   } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      r.w[i] = (int64_t)i * step < left ? __float_as_uint(__ldg(reinterpret_cast<const float*>(p) + (int64_t)i * step)) : 0u;
+      r.w[i] = (int64_t)i * step < left
+                   ? __float_as_uint(load_one<INPLACE>(reinterpret_cast<const float*>(p) + (int64_t)i * step))
+                   : 0u;
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const uint32_t b = (int64_t)i * step < left
-                             ? (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p) + (int64_t)i * step)
+                             ? (uint32_t)load_one<INPLACE>(reinterpret_cast<const unsigned short*>(p) + (int64_t)i * step)
                              : 0u;
       if (i & 1) r.w[i / 2] |= b << 16;
       else r.w[i / 2] = b;

@@ -107,3 +107,24 @@ def test_results_do_not_take_memory_that_is_still_read(kda_lib, op, raw):
         assert torch.equal(t, (torch.arange(n, device="cuda") % 251).to(torch.uint8))
     for k, v in want.items():
         assert torch.equal(got[k], v), k
+
+
+@pytest.mark.parametrize("ty", [BF, F])
+@pytest.mark.parametrize("N,T,C", [(301, 1, 512), (301, 1, 259), (97, 2, 1024), (50, 32, 264), (9, 33, 1024),
+                                   (3, 700, 259)])
+def test_convolution_state_in_place(kda_lib, ty, N, T, C):
+    """Every kernel that writes a final state (single tokens, runs that are whole sequences,
+    runs of longer ones), with the initial state in the same buffer, call after call."""
+    import kimi_delta_attention_08_gb300 as kda
+    g = torch.Generator().manual_seed(N * T + C)
+    w, b = torch.randn(C, 4, generator=g).cuda(), torch.randn(C, generator=g).cuda()
+    one = torch.randn(N, 3, C, generator=g).to(ty).cuda()
+    two = one.clone()
+    for _ in range(4):
+        x = torch.randn(N, T, C, generator=g).to(ty).cuda()
+        a, o, end = torch.empty_like(x), torch.empty_like(x), torch.empty_like(one)
+        kda.kda_conv_fwd(x, w, b, a, two, end)
+        two = end
+        kda.kda_conv_fwd(x, w, b, o, one, one)
+        assert torch.equal(a, o) and torch.equal(one, two)
+        assert torch.equal(one[:, max(0, 3 - T):], x[:, max(0, T - 3):])
