@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_fwd_kernel(const ConvParams 
     pre_activation<W, V>(w, b, h, x, s);
     if constexpr (SILU) {
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) s[i] = silu(s[i]);
+      for (int i = 0; i < V / 2; ++i) s[i] = silu<T>(s[i]);
     }
     float y[V];
     from_pairs<V>(s, y);
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_step_kernel(const ConvParams
     pre_activation<W, V>(w, b, h, x, s);
     if constexpr (SILU) {
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) s[i] = silu(s[i]);
+      for (int i = 0; i < V / 2; ++i) s[i] = silu<T>(s[i]);
     }
     float y[V];
     from_pairs<V>(s, y);
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_bwd_kernel(const ConvParams 
         pre_activation<W, V>(w, b, h, x, s);
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) {
-          d[i] = pmul(d[i], silu_slope(s[i], sigmoid(s[i])));
+          d[i] = pmul(d[i], silu_slope(s[i], sigmoid<T>(s[i])));
         }
       }
       if (sum) {

@@ -91,15 +91,15 @@ __device__ __forceinline__ float2 row_sum(float2 v, float2* red, int turn) {
 }
 
 // The gate's activation, and with its slope.
-template <int V>
+template <typename T, int V>
 __device__ __forceinline__ Vals<V> gate_fn(const Vals<V>& p, int fn) {
-  const Vals<V> s = sigmoid(p);
+  const Vals<V> s = sigmoid<T>(p);
   return fn == KDA_FN_SILU ? mul_of(p, s) : s;
 }
-template <int V>
+template <typename T, int V>
 __device__ __forceinline__ Vals<V> gate_fn(const Vals<V>& p, int fn, Vals<V>& slope) {
   Vals<V> ds;
-  const Vals<V> s = sigmoid(p, ds);
+  const Vals<V> s = sigmoid<T>(p, ds);
   slope = ds;
   if (fn != KDA_FN_SILU) return s;
   slope = fma_of(p, ds, s);
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(norm_threads(G, E, V)) postnorm_fwd_kernel(con
     const float rstd = rsqrtf(s * inv_d + p.eps);
     each(row, [&](int i, int64_t at) {
       Vals<V> n = mul_of(mul_of(x[i], splat<V>(rstd)), sw[i]);
-      if (p.b) n = mul_of(n, gate_fn(values(rg[i]), p.fn));
+      if (p.b) n = mul_of(n, gate_fn<T>(values(rg[i]), p.fn));
       if (p.c) n = fma_of(n, splat<V>(1.f), values(rr[i]));
       store_vec<T, V>(p.o0, at, n);
     });
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(norm_threads(G, E, V), norm_bwd_blocks(G, E, V
       Q[i] = splat<V>(0.f);
       if (p.b) {
         Vals<V> slope;
-        const Vals<V> act = gate_fn(values(rg[i]), p.fn, slope);
+        const Vals<V> act = gate_fn<T>(values(rg[i]), p.fn, slope);
         Q[i] = mul_of(P[i], slope);
         P[i] = mul_of(P[i], act);
       }

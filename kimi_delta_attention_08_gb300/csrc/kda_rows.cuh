@@ -13,7 +13,8 @@
 namespace kda {
 namespace rows {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLog2eRest = 1.925963033500e-8f;  // log2 e: fp32, and the rest
+constexpr float kLn2 = 0.6931471805599453f;
 
 using bf16 = __nv_bfloat16;
 
@@ -171,18 +172,41 @@ __device__ __forceinline__ pair pex2(pair v) {
   return pr(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y));
 }
 
-// sigmoid(x): 1 / (1 + 2^(-x log2 e)) with the hardware exponential and reciprocal
-// (each a few 2^-23 off, far below a bf16 step and within the fp32 rows' tolerance).
-// ex2 reaches infinity at -x > 128 / log2 e, where the quotient is a clean zero.
-__device__ __forceinline__ float sigmoid(float x) {
-  return ptx::rcp_approx(1.0f + ptx::ex2_approx(-x * kLog2e));
+// exp(-x) = 2^h, h = -x log2 e, with the hardware exponential (2^-22).  Rounding h makes the
+// error grow by 1.5 steps of 2^-24 for each unit of x: nothing to a step of bf16, but for rows
+// of fp32 (T) what the rounding left out, l, is put back as 2^h (1 + l ln 2); not where that
+// is no number because x or the result is infinite.
+template <typename T>
+__device__ __forceinline__ float exp_minus(float x) {
+  const float n = x * kLog2e, e = ptx::ex2_approx(-n);
+  if constexpr (sizeof(T) < 4) return e;
+  const float l = fmaf(x, -kLog2eRest, fmaf(x, -kLog2e, n)), r = fmaf(e, l * kLn2, e);
+  return fabsf(r) < INFINITY ? r : e;
+}
+template <typename T>
+__device__ __forceinline__ pair exp_minus(pair x) {
+  const pair n = pmul(x, pr(kLog2e));
+  const float2 h = un(n);
+  const pair e = pr(ptx::ex2_approx(-h.x), ptx::ex2_approx(-h.y));
+  if constexpr (sizeof(T) < 4) return e;
+  const pair l = pfma(x, pr(-kLog2eRest), pfma(x, pr(-kLog2e), n));
+  const float2 r = un(pfma(e, pmul(l, pr(kLn2)), e)), f = un(e);
+  return pr(fabsf(r.x) < INFINITY ? r.x : f.x, fabsf(r.y) < INFINITY ? r.y : f.y);
 }
 
+// sigmoid(x) = 1 / (1 + exp(-x)) with the hardware reciprocal (2^-23): a clean zero where the
+// exponential is infinite.  T: the rows' type.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float x) {
+  return ptx::rcp_approx(1.0f + exp_minus<T>(x));
+}
+template <typename T>
 __device__ __forceinline__ pair sigmoid(pair x) {
-  const float2 s = un(padd(pex2(pmul(x, pr(-kLog2e))), pr(1.0f)));
+  const float2 s = un(padd(exp_minus<T>(x), pr(1.0f)));
   return pr(ptx::rcp_approx(s.x), ptx::rcp_approx(s.y));
 }
-__device__ __forceinline__ pair silu(pair x) { return pmul(x, sigmoid(x)); }
+template <typename T>
+__device__ __forceinline__ pair silu(pair x) { return pmul(x, sigmoid<T>(x)); }
 
 // silu'(x) = s + x s (1 - s) from s = sigmoid(x).  1 - s is within 2^-23, and zero once s is 1
 // (x = 17), so the slope is within 17 such steps of 1 however large x is; expanded to
@@ -193,13 +217,15 @@ __device__ __forceinline__ pair silu_slope(pair x, pair s) {
 
 // sigmoid(x) and its slope sigmoid(x) sigmoid(-x) = e s^2 with e = exp(-x).  As s - s^2 it would
 // lose its digits where s nears 1: all of them from x = 17 on.  (An infinite e meets s = 0.)
+template <typename T>
 __device__ __forceinline__ float sigmoid(float x, float& slope) {
-  const float e = ptx::ex2_approx(-x * kLog2e), s = ptx::rcp_approx(1.0f + e);
+  const float e = exp_minus<T>(x), s = ptx::rcp_approx(1.0f + e);
   slope = fminf(e, FLT_MAX) * s * s;
   return s;
 }
+template <typename T>
 __device__ __forceinline__ pair sigmoid(pair x, pair& slope) {
-  const pair e = pex2(pmul(x, pr(-kLog2e)));
+  const pair e = exp_minus<T>(x);
   const float2 d = un(padd(e, pr(1.0f)));
   const pair s = pr(ptx::rcp_approx(d.x), ptx::rcp_approx(d.y));
   slope = pmul(pmul(pr(fminf(un(e).x, FLT_MAX), fminf(un(e).y, FLT_MAX)), s), s);
@@ -245,25 +271,25 @@ __device__ __forceinline__ Vals<V> splat(float f) {
   }
   return r;
 }
-template <int V>
+template <typename T, int V>
 __device__ __forceinline__ Vals<V> sigmoid(const Vals<V>& x) {
   Vals<V> r;
   if constexpr (V == 1) {
-    r.v[0] = sigmoid(x.v[0]);
+    r.v[0] = sigmoid<T>(x.v[0]);
   } else {
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) r.v[i] = sigmoid(x.v[i]);
+    for (int i = 0; i < V / 2; ++i) r.v[i] = sigmoid<T>(x.v[i]);
   }
   return r;
 }
-template <int V>
+template <typename T, int V>
 __device__ __forceinline__ Vals<V> sigmoid(const Vals<V>& x, Vals<V>& slope) {
   Vals<V> r;
   if constexpr (V == 1) {
-    r.v[0] = sigmoid(x.v[0], slope.v[0]);
+    r.v[0] = sigmoid<T>(x.v[0], slope.v[0]);
   } else {
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) r.v[i] = sigmoid(x.v[i], slope.v[i]);
+    for (int i = 0; i < V / 2; ++i) r.v[i] = sigmoid<T>(x.v[i], slope.v[i]);
   }
   return r;
 }

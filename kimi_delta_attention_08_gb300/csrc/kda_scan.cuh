@@ -27,7 +27,6 @@ namespace scan {
 using namespace rows;
 
 constexpr int kScanBlock = KDA_SCAN_CHUNK;  // 32 tokens: one saved state each, the backward's block
-constexpr float kLn2 = 0.6931471805599453f;
 
 struct ScanParams {
   const void *x, *dt, *z, *B, *C, *dout;
@@ -229,7 +228,7 @@ __device__ __forceinline__ void store_state(void* p, int64_t at, const float (&h
 // becomes the largest finite one, so that a step of zero still leaves 1.
 __device__ __forceinline__ float rate_of(float v) {
   const float hi = v * kLog2e;
-  const float lo = fmaf(v, 1.925963033500e-8f, fmaf(v, kLog2e, -hi));  // log2 e - kLog2e
+  const float lo = fmaf(v, kLog2eRest, fmaf(v, kLog2e, -hi));
   const float e = ptx::ex2_approx(hi);
   const float r = fmaf(e, lo * kLn2, e);
   const float a = -kLog2e * (fabsf(r) < INFINITY ? r : e);

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(BwdShape<T, NS>::NT, 384 / BwdShape<T, NS>::NT
         d = tok < nt ? d : 0;
         const pair m = pmul(d, pr(xv[i], xv[i + 1]));
         pair dy = pr(ov[i], ov[i + 1]);
-        if (p.z) dy = pmul(dy, silu(pr(zv[i], zv[i + 1])));
+        if (p.z) dy = pmul(dy, silu<T>(pr(zv[i], zv[i + 1])));
         if constexpr (VEC) {
           *reinterpret_cast<ulonglong2*>(&s_dx[tok][pair_unit(tok, (sc + i) / 2)]) = make_ulonglong2(d, m);
           *reinterpret_cast<pair*>(&s_dy[tok][sc + i]) = dy;
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(BwdShape<T, NS>::NT, 384 / BwdShape<T, NS>::NT
         const pair sig = pr(softplus_slope(un(v).x, un(ex).x), softplus_slope(un(v).y, un(ex).y));
         const pair sk = pr(dsk[i], dsk[i + 1]);
         if (p.z) {
-          const pair z2 = pr(zv[i], zv[i + 1]), sz = sigmoid(z2), zs = pmul(z2, sz);
+          const pair z2 = pr(zv[i], zv[i + 1]), sz = sigmoid<T>(z2), zs = pmul(z2, sz);
           dy = pmul(o2, zs);
           dz2 = pmul(pmul(o2, pfma(sk, x2, yi)), silu_slope(z2, sz));
         }

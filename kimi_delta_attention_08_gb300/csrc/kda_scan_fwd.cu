@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(FwdShape<NS>::NT, PASS == kOutputs ? 4 : 5) sc
         xv[k] = as_pair(rx[g][k]);
         if (OUT && p.z) zv[k] = as_pair(rz[g][k]);
         delta[k] = softplus(padd(as_pair(rt[g][k]), bias), ex);
-        if (REV) dx[k] = p.z ? pmul(xv[k], silu(as_pair(rz[g][k]))) : xv[k];  // dy
+        if (REV) dx[k] = p.z ? pmul(xv[k], silu<T>(as_pair(rz[g][k]))) : xv[k];  // dy
         else dx[k] = pmul(delta[k], xv[k]);
         if (!OUT) sum_delta = padd(sum_delta, delta[k]);
       }
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(FwdShape<NS>::NT, PASS == kOutputs ? 4 : 5) sc
 #pragma unroll
       for (int k = 0; k < OWN; ++k) {
         y[k] = pfma(skip, xv[k], y[k]);
-        if (p.z) y[k] = pmul(y[k], silu(zv[k]));
+        if (p.z) y[k] = pmul(y[k], silu<T>(zv[k]));
         const float o[2] = {un(y[k]).x, un(y[k]).y};
         if (t0 + j0 + l * OWN + k < tokens && left > 0)
           store_row<T, 2, VEC>(po + (int64_t)k * p.dim, o, 1, left);
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(128, NS == 8 ? 6 : 7) scan_step_kernel(const S
 #pragma unroll
       for (int o = OWNERS; o < LPC; o <<= 1) y[k] += __shfl_xor_sync(0xffffffffu, y[k], o);
       y[k] = fmaf(D, x[k], y[k]);
-      if (p.z) y[k] *= z[k] * sigmoid(z[k]);
+      if (p.z) y[k] *= z[k] * sigmoid<T>(z[k]);
       if (mine && l < OWNERS && first + k < nq) po[(int64_t)(k * T_ + j) * p.dim] = from_f<T>(y[k]);
     }
     if (j + 1 >= T_) break;

@@ -94,3 +94,62 @@ def test_scan_gate_slope_at_large_arguments(kda_lib, dim):
     slope, steps = silu_bounds(R.d(z))
     du = R.d(dout) * R.d(x)
     within(r["dz"], du * slope, du.abs(), steps + 4, "dz")
+
+
+FAR = [-85.0, -80.0, -60.0, -40.0, -20.0, -8.0, -1.0, 0.5, 3.0, 20.0, 85.0]
+
+
+def far(g, *shape):
+    """Arguments around FAR, not whole numbers: their products with log2 e are rounded."""
+    v = torch.tensor(FAR)
+    return (v[torch.randint(len(v), shape, generator=g)] * (1 + 0.02 * torch.rand(shape, generator=g))).clamp(-86, 86).cuda()
+
+
+def test_fp32_activations_far_from_zero(kda_lib):
+    """sigmoid and SiLU of fp32 rows to 16 steps of 2^-24 at any argument: the exponential (4),
+    what is put back of its argument's rounding, 1 + e, the reciprocal (2) and the products
+    (and 48 for the norm itself)."""
+    import kimi_delta_attention_08_gb300 as kda
+    g = torch.Generator().manual_seed(5)
+    x = far(g, 1, 60, 64)
+    w = torch.tensor([0.0, 1.0]).repeat(64, 1).cuda()
+    out = torch.empty_like(x)
+    kda.kda_conv_fwd(x, w, None, out)
+    ref = R.silu(R.d(x))
+    within(out, ref, ref.abs(), 16, "convolution")
+    rows, step = x.view(60, 1, 64), torch.empty(60, 1, 64, device="cuda")
+    kda.kda_conv_fwd(rows, w, None, step)
+    assert torch.equal(step.view_as(out), out)
+    u, gate = torch.randn(40, 128, generator=g).cuda(), far(g, 40, 128)
+    wn, o = torch.ones(128, device="cuda"), torch.empty(40, 128, device="cuda")
+    for act in ("sigmoid", "silu"):
+        kda.kda_postnorm_fwd(u, wn, gate, o, activation=act)
+        ref = R.postnorm(u, wn, gate, None, 1.0, act, 1e-6)
+        within(o, ref, ref.abs(), 64, "gated norm " + act)
+    # a scan with steps of zero and D = 1: out = x silu(z)
+    for T in (40, 1):
+        z, y = far(g, 2, T, 64), torch.randn(2, T, 64, generator=g).cuda()
+        B, out = torch.randn(2, T, 1, 16, generator=g).cuda(), torch.empty(2, T, 64, device="cuda")
+        kda.kda_scan_fwd(y, torch.full_like(y, -200.0), torch.zeros(64, 16, device="cuda"), B, B, out,
+                         torch.ones(64, device="cuda"), z)
+        ref = R.d(y) * R.silu(R.d(z))
+        within(out, ref, ref.abs(), 16, "scan")
+
+
+@pytest.mark.parametrize("ty", [BF, F])
+def test_activations_at_infinity(kda_lib, ty):
+    """sigmoid is 1 and 0 at the infinities, and what is no number stays none."""
+    import kimi_delta_attention_08_gb300 as kda
+    inf = float("inf")
+    gate = torch.tensor([inf, -inf, float("nan"), 1e30, -1e30, 0.0, 90.0, -200.0]).to(ty).cuda().repeat(3, 16)
+    x, w = torch.randn(3, 128).to(ty).cuda(), torch.ones(128, device="cuda")
+    gated, plain = torch.empty_like(x), torch.empty_like(x)
+    kda.kda_postnorm_fwd(x, w, gate, gated)
+    kda.kda_postnorm_fwd(x, w, None, plain)
+    for i, f in ((0, 1.0), (1, 0.0), (3, 1.0), (4, 0.0), (5, 0.5), (6, 1.0), (7, 0.0)):
+        assert torch.equal(gated[:, i::8], plain[:, i::8] * f), i
+    assert gated[:, 2::8].isnan().all()
+    r = kda.kda_postnorm_bwd(x, x, w, gate)["dgate"]
+    for i in (0, 1, 3, 4, 7):
+        assert not r[:, i::8].any(), i
+    assert r[:, 2::8].isnan().all() and r[:, 5::8].isfinite().all()
