@@ -240,6 +240,8 @@ __device__ __forceinline__ void load_rates(float (&a)[SP], const float* A_log, i
   for (int i = 0; i < SP; ++i) a[i] = rate_of(__ldg(A_log + at + i));
 }
 
+constexpr int64_t kSms = 152;  // a GB300's: a workspace's size is asked for without a device
+
 // How sequences are cut (seg_len 0: not at all) for a pass over `tiles` channel tiles whose
 // SMs hold `resident` CTAs; and the CTAs that run side by side without cutting.
 struct ScanPlan {

@@ -60,7 +60,24 @@ struct BwdShape {
   static constexpr int CKPT = PART + 2 * NW * SB * 2 * NS;        // [NSB - 1][2][NT] of 4
   static constexpr int SUMA = CKPT + (NSB - 1) * 2 * 4 * NT;  // [2][NT] of 4
   static constexpr int FLOATS = SUMA + 2 * 4 * NT;
+  // CTAs on an SM, by registers (12 warps) and by shared memory: 2 with 8 states, 3 with 16, 1
+  // with 32 and 64
+  static constexpr int BY_SMEM = 228 * 1024 / (FLOATS * 4 + 1024);
+  static constexpr int RESIDENT = 384 / NT < BY_SMEM ? 384 / NT : BY_SMEM;
 };
+
+// The channels of a CTA and the CTAs on an SM.
+struct BwdFit {
+  int channels, resident;
+};
+template <int NS>
+BwdFit bwd_fit_of() {
+  return {BwdShape<float, NS>::CH, BwdShape<float, NS>::RESIDENT};
+}
+BwdFit bwd_fit(int state) {
+  return state == 8 ? bwd_fit_of<8>() : state == 16 ? bwd_fit_of<16>() : state == 32 ? bwd_fit_of<32>()
+                                                                                     : bwd_fit_of<64>();
+}
 
 // Where the 16 bytes of a channel pair lie in a token's row of DX: exchanged within groups
 // of four, so that the staging writes (neighbouring lanes 64 bytes apart, two rows in 8
@@ -521,16 +538,19 @@ BwdLayout bwd_layout(ScanParams& p, int state, bool have_states) {
   size_t n = 0;
   kda_scan_get_states_size(p.total, p.N, p.dim, state, &n);
   if (!have_states) at = up256(at + n);
-  const int ch = state == 8 ? 128 : state <= 32 ? 64 : 32;  // BwdShape::CH
-  p.tiles_per_group = (p.per + ch - 1) / ch;
+  const BwdFit fit = bwd_fit(state);
+  p.tiles_per_group = (p.per + fit.channels - 1) / fit.channels;
   p.tiles = (int64_t)p.tiles_per_group * p.groups;
-  // 3 CTAs of four warps on an SM.  The reverse pass that cutting adds costs a seventh of the
-  // main one, so sequences stay whole where they fill 85 % of the turns that they take
-  // (4,096 tokens, 4,096 channels: 6 sequences whole 2,580 us, cut 2,510; 7 whole 2,589,
-  // cut 2,987; 8 whole 4,069, cut 3,337).
-  const int64_t whole = scan_whole_units(p, p.tiles), turn = 3 * 152;
-  const bool cut = 100 * whole < 85 * ((whole + turn - 1) / turn * turn);
-  const ScanPlan r = scan_plan(p, p.tiles, 3, cut);
+  // The reverse pass that cutting adds costs a seventh of the main one, so sequences stay whole
+  // where they fill nearly all of the turns that they take: 85 % with three CTAs on an SM, 80 %
+  // with fewer.  Sequences of 4,096 channels, whole / cut: 16 states, 4,096 tokens, 6 (84 %)
+  // 2,580 / 2,510 us, 7 (98 %) 2,589 / 2,987; 8 states, 2,048 tokens, 7 (74 %) 1,247 / 1,089,
+  // 8 (84 %) 1,243 / 1,303; 32 states, 5 (70 %) 2,456 / 2,169, 2 (84 %) 843 / 931; 64 states, 1
+  // (84 %) 918 / 1,014.
+  const int64_t whole = scan_whole_units(p, p.tiles), turn = fit.resident * kSms;
+  const int64_t enough = fit.resident == 3 ? 85 : 80;
+  const bool cut = 100 * whole < enough * ((whole + turn - 1) / turn * turn);
+  const ScanPlan r = scan_plan(p, p.tiles, fit.resident, cut);
   p.seg_len = r.seg_len, p.slots = r.slots;
   w.seg = at;
   if (p.seg_len) at = up256(at + (size_t)p.slots * p.dim * (state + 1) * sizeof(float));

@@ -471,7 +471,6 @@ namespace scan {
 // pieces, 3.9 turns of the backward, it takes 1.70 ms; into 4, which take a third turn for
 // the last eighth, 1.96 ms.)
 constexpr int64_t kMinSegment = 128;
-constexpr int64_t kSms = 152;
 
 int64_t scan_whole_units(const ScanParams& p, int64_t tiles) { return p.cu ? tiles : tiles * p.N; }
 
