@@ -498,15 +498,21 @@ ScanPlan scan_plan(const ScanParams& p, int64_t tiles, int64_t resident, bool cu
   return r;
 }
 
-// 4 CTAs of two warps on an SM.  Cutting costs half the main pass once more, while a GPU with
-// half of that room taken still runs at 7 tenths of its rate, so sequences stay whole from
-// 4 tenths on (4,096 tokens, 4,096 channels: 3 sequences whole 555 us, cut 466; 4 whole
-// 565, cut 597; 5 whole 770, cut 731; 8 whole 784, cut 1,126).
+// Counted with 4 CTAs of two warps on an SM; with 16 and more states 5 fit in bf16, but segments
+// for 5 take as long (2 sequences of 4,096 tokens and channels, 16 states, 323 / 317 us, 5 735 /
+// 740).  Cutting costs half the main pass once more, while a GPU with half of that room taken
+// still runs at 7 tenths of its rate, so sequences stay whole from a part of the room on: 6
+// tenths with 8 states, whose CTA is the slowest alone, 4 with 16 and 32, 3 with 64, whose first
+// pass is as long as the main one.  Sequences of 4,096 tokens and channels, whole / cut: 8
+// states, 9 (47 %) 924 / 857 us, 11 (58 %) 1,051 / 974, 12 (63 %) 1,052 / 1,092; 16 states, 3
+// (32 %) 568 / 468, 4 (42 %) 572 / 598; 32 states, 1 (21 %) 517 / 317, 2 (42 %) 535 / 579; 64
+// states, 1 of 2,048 channels (21 %) 443 / 411, 1 of 3,200 (33 %) 557 / 606.
 void scan_fwd_plan(ScanParams& p, int state) {
   const int ch = 1024 / state;  // FwdShape::CH
   p.tiles_per_group = (p.per + ch - 1) / ch;
   p.tiles = (int64_t)p.tiles_per_group * p.groups;
-  const ScanPlan r = scan_plan(p, p.tiles, 4, 10 * scan_whole_units(p, p.tiles) < 4 * 4 * kSms);
+  const int64_t tenths = state == 8 ? 6 : state == 64 ? 3 : 4;
+  const ScanPlan r = scan_plan(p, p.tiles, 4, 10 * scan_whole_units(p, p.tiles) < tenths * 4 * kSms);
   p.seg_len = r.seg_len, p.slots = r.slots;
 }
 

@@ -44,3 +44,15 @@ def test_backward_is_cut_by_what_fits_an_sm(lib, state, dim, B, cut):
     fill = B * tiles / (152 * fit)
     fill /= -(-B * tiles // (152 * fit))
     assert (fill < (0.85 if fit == 3 else 0.8)) == cut
+
+
+@pytest.mark.parametrize("state,dim,B,cut", [
+    (8, 4096, 8, True), (8, 4096, 11, True), (8, 4096, 12, False), (16, 4096, 3, True), (16, 4096, 4, False),
+    (16, 4096, 8, False), (32, 4096, 1, True), (32, 4096, 2, False), (64, 2048, 1, True), (64, 3200, 1, False),
+    (64, 4096, 1, False)])
+def test_forward_is_cut_by_the_room_that_it_takes(lib, state, dim, B, cut):
+    """Whole sequences need the status word alone; in tenths of the 4 x 152 places, they stay
+    whole from 6 on with 8 states, 4 with 16 and 32, 3 with 64."""
+    n = ctypes.c_size_t(0)
+    assert lib.kda_scan_get_workspace_size(ctypes.byref(problem(B, 4096, dim, state)), ctypes.byref(n)) == 0
+    assert (n.value > 256) == cut
