@@ -50,7 +50,7 @@ struct ConvParams {
   const int64_t* cu;
   unsigned* status;
   int64_t T, total;
-  int32_t N, C, fn;
+  int32_t N, C;
   int32_t run;                        // tokens per run
   int32_t whole;                      // 1: run r is the whole of sequence r (batched)
   int32_t weight_vec;                 // weight is 16-byte aligned
@@ -766,7 +766,7 @@ bool conv_vec(const void* x, int64_t x_stride, const void* const* outs,
 
 void fill(ConvParams& p, const void* x, int64_t x_stride, const float* weight, const float* bias,
           const void* const* outs, const int32_t* out_channels, int32_t num_outs, const void* init,
-          const int64_t* cu, int64_t B, int64_t T, int32_t C, int32_t N, int32_t fn) {
+          const int64_t* cu, int64_t B, int64_t T, int32_t C, int32_t N) {
   p.x = x, p.x_stride = x_stride, p.weight = weight, p.bias = bias, p.init = init, p.cu = cu;
   p.num_outs = num_outs;
   p.out_lo[0] = 0;
@@ -774,7 +774,7 @@ void fill(ConvParams& p, const void* x, int64_t x_stride, const float* weight, c
     p.outs[i] = i < num_outs ? const_cast<void*>(outs[i]) : nullptr;
     p.out_lo[i + 1] = p.out_lo[i] + (i < num_outs ? out_channels[i] : 0);
   }
-  p.T = T, p.total = B * T, p.N = N, p.C = C, p.fn = fn;
+  p.T = T, p.total = B * T, p.N = N, p.C = C;
 }
 
 }  // namespace
@@ -797,8 +797,6 @@ kda_status kda_conv_fwd(const void* x, int64_t x_stride, const float* weight, co
   if (!al_to(workspace, 128)) return KDA_ERR_MISALIGNED;
   st = check_device();
   if (st != KDA_OK) return st;
-  int num_sms = 0;
-  if (sm_count(&num_sms) != KDA_OK) return KDA_ERR_CUDA;
   const bool f32 = dtype == KDA_ROW_FP32;
   const bool step = !cu_seqlens && T == 1;
   const int V = f32 ? kFwdV32 : step ? kStepV : kFwdV16;
@@ -806,7 +804,7 @@ kda_status kda_conv_fwd(const void* x, int64_t x_stride, const float* weight, co
                             C, V, f32 ? 4 : 2, f32 ? 4 : 2);
   ConvParams p = {};
   fill(p, x, x_stride, weight, bias, outs, out_channels, num_outs, initial_state, cu_seqlens, B, T,
-       C, N, fn);
+       C, N);
   p.fin = final_state;
   p.status = static_cast<unsigned*>(workspace);
   const int64_t tiles = (C + 32 * V - 1) / (32 * V);
@@ -887,7 +885,7 @@ kda_status kda_conv_bwd(const void* x, int64_t x_stride, const float* weight, co
                    al_to(dx, 16) && al_to(dinitial_state, 16);
   ConvParams p = {};
   fill(p, x, x_stride, weight, bias, douts, out_channels, num_outs, initial_state, cu_seqlens, B,
-       T, C, N, fn);
+       T, C, N);
   p.dfin = dfinal_state, p.dx = dx, p.dinit = dinitial_state;
   p.status = static_cast<unsigned*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + KDA_STATUS_BYTES);

@@ -577,8 +577,7 @@ kda_status check_scan(const kda_scan_problem* q, ScanParams& s, bool& vec) {
 }
 
 __global__ void scan_status_kernel(const int64_t* cu, int N, int64_t total, unsigned* status) {
-  if (cu) check_seqlens(cu, N, total, status, kDevStatusBadSeqlens);
-  else if (threadIdx.x == 0) *status = 0u;
+  check_seqlens(cu, N, total, status, kDevStatusBadSeqlens);
 }
 
 cudaError_t seqlens_status(const ScanParams& p, unsigned* status, cudaStream_t stream) {
