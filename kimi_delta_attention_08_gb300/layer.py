@@ -29,20 +29,38 @@ def _raise(status, where):
     raise KdaError(status, where)
 
 
+def _tensor(t, name):
+    """t, which has to be a tensor.  (Single tokens are bound by the host: what they check looks
+    first and asks this only where that fails.)"""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    return t
+
+
+def _tensors(**given):
+    for name, t in given.items():
+        _tensor(t, name)
+
+
 def _row_dtype(t, name):
-    code = ROW_DTYPES.get(t.dtype)
+    try:
+        code = ROW_DTYPES.get(t.dtype)
+    except AttributeError:
+        code = None
     if code is None:
+        _tensor(t, name)
         raise TypeError(f"{name}: expected bfloat16 or float32, got {t.dtype} (no implicit conversion)")
     return code
 
 
 def _need(t, name, dtype, dev, shape):
     """The pointer of a contiguous tensor of this dtype, device and shape."""
-    if t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous():
-        return t.data_ptr()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype != dtype:
+    try:
+        if t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if _tensor(t, name).dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype} (no implicit conversion)")
     if t.device != dev:
         raise ValueError(f"{name}: expected device {dev}, got {t.device}")
@@ -64,9 +82,12 @@ def _opt(t, name, dtype, dev, shape):
 
 def _rows(t, name, dtype, dev, shape):
     """(pointer, row stride) of [B, T, ...] rows with contiguous channels."""
-    if len(shape) == 3 and t.dtype == dtype and t.device == dev and t.shape == shape and t.is_contiguous():
-        return t.data_ptr(), shape[2]
-    if t.dtype != dtype:
+    try:
+        if len(shape) == 3 and t.dtype == dtype and t.device == dev and t.shape == shape and t.is_contiguous():
+            return t.data_ptr(), shape[2]
+    except AttributeError:
+        pass
+    if _tensor(t, name).dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype} (no implicit conversion)")
     if t.device != dev:
         raise ValueError(f"{name}: expected device {dev}, got {t.device}")
@@ -90,7 +111,7 @@ def _seqlens(cu, dev, B):
     """(pointer, N)"""
     if cu is None:
         return None, B
-    if cu.dtype != torch.int64 or cu.dim() != 1 or cu.device != dev or not cu.is_contiguous():
+    if _tensor(cu, "cu_seqlens").dtype != torch.int64 or cu.dim() != 1 or cu.device != dev or not cu.is_contiguous():
         raise ValueError("cu_seqlens: expected a contiguous int64 vector on the tensors' device")
     return cu.data_ptr(), cu.numel() - 1
 
@@ -121,12 +142,15 @@ def _call(name, dev, stream, *args):
         _raise(status, name)
 
 
+_CURRENT = nullcontext()
+
+
 def _pool(stream, dev):
     """A context whose new tensors come from the memory of the stream that will write them.  A
     block of the current stream's memory may still be read by work that is queued there, which
     another stream does not wait for."""
     if stream is None:
-        return nullcontext()
+        return _CURRENT
     if dev.type != "cuda":
         raise ValueError("expected CUDA tensors")
     if not isinstance(stream, torch.cuda.Stream):
@@ -156,7 +180,7 @@ def _workspace(given, size, dev, stream):
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
             raise ValueError("workspace: required with a raw stream handle")
         given = torch.empty(size(), dtype=torch.uint8, device=dev)
-    elif given.dtype != torch.uint8 or given.device != dev or not given.is_contiguous():
+    elif _tensor(given, "workspace").dtype != torch.uint8 or given.device != dev or not given.is_contiguous():
         raise ValueError("workspace: expected a contiguous uint8 tensor on the tensors' device")
     return given, given.data_ptr(), given.numel()
 
@@ -181,17 +205,30 @@ _POINTERS = [ctypes.c_void_p * k for k in range(5)]
 _COUNTS = [ctypes.c_int32 * k for k in range(5)]
 
 
+def _list(outs, name):
+    """One to four tensors, given as one or as a sequence."""
+    if isinstance(outs, torch.Tensor):
+        return (outs,)
+    try:
+        if 1 <= len(outs) <= 4:
+            return outs
+    except TypeError:
+        raise TypeError(f"{name}: expected a torch.Tensor or a sequence of them, got "
+                        f"{type(outs).__name__}") from None
+    raise ValueError(f"{name}: expected one to four tensors")
+
+
 def _parts(outs, name, dtype, dev, B, T, C):
     """The pointers and channel counts of one [B, T, C] tensor or of a sequence of tensors
     [B, T, ...] that share the channels."""
-    if isinstance(outs, torch.Tensor):
-        outs = (outs,)
+    outs = _list(outs, name)
     k = len(outs)
-    if not 1 <= k <= 4:
-        raise ValueError(f"{name}: expected one to four tensors")
     ptrs, counts = [], []
     for i, o in enumerate(outs):
-        sh = o.shape
+        try:
+            sh = o.shape
+        except AttributeError:
+            sh = _tensor(o, f"{name}[{i}]").shape
         if len(sh) < 3 or sh[0] != B or sh[1] != T:
             raise ValueError(f"{name}[{i}]: expected [{B}, {T}, ...], got {tuple(sh)}")
         if o.dtype == dtype and o.device == dev and o.is_contiguous():
@@ -208,7 +245,12 @@ def _parts(outs, name, dtype, dev, B, T, C):
 
 
 def _conv_common(x, weight, bias, activation):
-    if x.dim() != 3 or weight.dim() != 2:
+    try:
+        ok = x.dim() == 3 and weight.dim() == 2
+    except AttributeError:
+        _tensors(x=x, weight=weight)
+        raise
+    if not ok:
         raise ValueError("x must be [B, T, C] and weight [C, width]")
     B, T, C = x.shape
     dev = x.device
@@ -255,7 +297,7 @@ def kda_conv_bwd(x, weight, bias, dout, initial_state=None, dfinal_state=None, c
     an initial state) in fp32, and the workspace, whose status word tells of cu_seqlens."""
     B, T, C, W, dev, dt, fn, w, b = _conv_common(x, weight, bias, activation)
     xp, xs = _rows(x, "x", x.dtype, dev, x.shape)
-    first = dout if isinstance(dout, torch.Tensor) else dout[0]
+    first = _list(dout, "dout")[0]
     ddt = _row_dtype(first, "dout")
     ptrs, counts, k = _parts(dout, "dout", first.dtype, dev, B, T, C)
     cu, N = _seqlens(cu_seqlens, dev, B)
@@ -284,7 +326,12 @@ STATE_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 def _scan_problem(x, dt, A_log, B, C, D, z, dt_bias, initial_state, other_state, cu_seqlens, names):
     """The C problem of a call, and (B, T, N, D, state, groups, device)."""
-    if x.dim() != 3 or A_log.dim() != 2 or B.dim() != 4:
+    try:
+        ok = x.dim() == 3 and A_log.dim() == 2 and B.dim() == 4
+    except AttributeError:
+        _tensors(x=x, A_log=A_log, B=B)
+        raise
+    if not ok:
         raise ValueError("x must be [B, T, D], A_log [D, state] and B [B, T, groups, state]")
     dev, ty = x.device, x.dtype
     q = _lib.kda_scan_problem()
@@ -305,7 +352,7 @@ def _scan_problem(x, dt, A_log, B, C, D, z, dt_bias, initial_state, other_state,
     q.cu_seqlens, q.N = _seqlens(cu_seqlens, dev, x.shape[0])
     one = initial_state if initial_state is not None else other_state
     if one is not None:
-        if one.dtype not in STATE_DTYPES:
+        if _tensor(one, names[0]).dtype not in STATE_DTYPES:
             raise TypeError(f"{names[0]}: states must be float32 or bfloat16, got {one.dtype}")
         q.state_dtype = STATE_DTYPES[one.dtype]
     sty = None if one is None else one.dtype
@@ -338,7 +385,7 @@ def make_scan_workspace(batch, T, dim, state, groups=1, N=None, *, backward=Fals
 def _states_arg(buf, dev):
     if buf is None:
         return None, 0
-    if buf.dtype != torch.uint8 or buf.device != dev or not buf.is_contiguous():
+    if _tensor(buf, "chunk_states").dtype != torch.uint8 or buf.device != dev or not buf.is_contiguous():
         raise ValueError("chunk_states: expected make_scan_states's buffer on the tensors' device")
     return buf.data_ptr(), buf.numel()
 
@@ -411,8 +458,8 @@ def kda_prenorm_fwd(x, residual, weight, out, residual_out=None, *, res_scale=1.
     x, out: [..., D] bf16 or fp32; residual (or None) and residual_out (or None; it may be
     residual): the same shape in x's dtype or fp32; weight fp32 [D]; res_scale: a number or
     an fp32 tensor [D]."""
-    dev, D, shape = x.device, x.shape[-1], x.shape
     dt = _row_dtype(x, "x")
+    dev, D, shape = x.device, x.shape[-1], x.shape
     xp = _own(x, "x")
     stream_t = residual if residual is not None else residual_out
     sdt = dt if stream_t is None else _row_dtype(stream_t, "residual")
@@ -437,8 +484,8 @@ def kda_prenorm_bwd(dout, dresidual_out, h, weight, x=None, workspace=None, *, r
     (dout's dtype), dresidual (h's dtype), dweight, and with a per-channel res_scale, for
     which x is needed, dres_scale; dx is dresidual itself where they are equal (res_scale 1
     and one dtype)."""
-    dev, D, shape = dout.device, dout.shape[-1], dout.shape
     dt, sdt = _row_dtype(dout, "dout"), _row_dtype(h, "h")
+    dev, D, shape = dout.device, dout.shape[-1], dout.shape
     sp, sv = _scale_args(res_scale, dev, D)
     if sp is not None and x is None:
         raise ValueError("x: needed for the gradient of a per-channel res_scale")
@@ -466,7 +513,7 @@ def _gate_args(gate, x, dev):
     """(pointer, token stride, heads) of a gate [..., D] or [B, T, H, D] rows."""
     if gate is None:
         return None, 0, 1
-    if gate.dim() == 4 and not gate.is_contiguous():
+    if _tensor(gate, "gate").dim() == 4 and not gate.is_contiguous():
         p, st = _rows(gate, "gate", x.dtype, dev, x.shape)
         return p, st, x.shape[2]
     return _need(gate, "gate", x.dtype, dev, x.shape), x.shape[-1], 1
@@ -479,8 +526,8 @@ def kda_postnorm_fwd(x, weight, gate, out, residual=None, *, res_scale=1.0, acti
 
     x, out, residual (or None): [..., D] bf16 or fp32, out may be x; gate: None, x's shape,
     or for x [B, T, H, D] rows whose H * D channels are contiguous; weight fp32 [D]."""
-    dev, D, shape = x.device, x.shape[-1], x.shape
     dt = _row_dtype(x, "x")
+    dev, D, shape = x.device, x.shape[-1], x.shape
     if activation not in GATE_ACTIVATIONS:
         raise ValueError(f"activation must be one of {list(GATE_ACTIVATIONS)}")
     gp, gs, heads = _gate_args(gate, x, dev)
@@ -497,10 +544,11 @@ def kda_postnorm_bwd(dout, x, weight, gate=None, workspace=None, *, res_scale=1.
     """Enqueue the backward of kda_postnorm_fwd; the gradient of its residual is dout.
     Returns a dict: dx, dgate (with a gate) in x's dtype, dweight, and dres_scale (with a
     per-channel res_scale) in fp32."""
-    dev, D, shape = x.device, x.shape[-1], x.shape
     dt = _row_dtype(x, "x")
+    dev, D, shape = x.device, x.shape[-1], x.shape
     if activation not in GATE_ACTIVATIONS:
         raise ValueError(f"activation must be one of {list(GATE_ACTIVATIONS)}")
+    dop = _need(dout, "dout", x.dtype, dev, shape)
     gp, gs, heads = _gate_args(gate, x, dev)
     sp, sv = _scale_args(res_scale, dev, D)
     rows = x.numel() // D if D else 0
@@ -513,9 +561,9 @@ def kda_postnorm_bwd(dout, x, weight, gate=None, workspace=None, *, res_scale=1.
             g["dgate"] = torch.empty(shape, dtype=x.dtype, device=dev)
         if sp is not None:
             g["dres_scale"] = torch.empty((D,), dtype=_f32, device=dev)
-    _call("kda_postnorm_bwd", dev, stream, _need(dout, "dout", x.dtype, dev, shape),
-          _own(x, "x"), _need(weight, "weight", _f32, dev, (D,)), gp, gs, heads,
-          sp, sv, eps, GATE_ACTIVATIONS[activation], g["dx"].data_ptr(),
+    _call("kda_postnorm_bwd", dev, stream, dop, _own(x, "x"),
+          _need(weight, "weight", _f32, dev, (D,)), gp, gs, heads, sp, sv, eps,
+          GATE_ACTIVATIONS[activation], g["dx"].data_ptr(),
           None if gate is None else g["dgate"].data_ptr(), g["dweight"].data_ptr(),
           None if sp is None else g["dres_scale"].data_ptr(), rows, D, dt, wp, wb)
     g["workspace"] = ws
