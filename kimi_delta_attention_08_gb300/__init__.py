@@ -283,7 +283,7 @@ def kda_bwd(q, k, v, g, beta, scale, A_log, dt_bias, lower_bound, dout, initial_
     """Enqueue the backward pass (include/kda.h, kda_bwd) for the forward call with
     the same inputs, given dout (bf16, out's shape) and optionally the gradient of
     the final state.  Returns a dict of fp32 gradients dq, dk, dv, dg, dbeta,
-    dA_log, ddt_bias and dinitial_state (allocated here with torch).
+    dA_log, ddt_bias and dinitial_state (allocated here with torch, from `stream`'s memory).
     path: "auto" / "chunked" (tensor cores, bf16 operands) or "recurrent" (token
     by token, fp32).  chunk_states: the buffer that a kda_fwd of the same inputs
     filled (chunked path); the backward then skips its own state-checkpoint pass."""
@@ -326,26 +326,27 @@ def kda_bwd(q, k, v, g, beta, scale, A_log, dt_bias, lower_bound, dout, initial_
         _need(t, nm, sdt, dev, 4)
         if tuple(t.shape) != (N, HV, D, D):
             raise ValueError(f"{nm}: expected shape {(N, HV, D, D)}, got {tuple(t.shape)}")
-    if workspace is None:
-        workspace = make_bwd_workspace(B * T, N, H, HV, dev)
-    _need(workspace, "workspace", torch.uint8, dev, 1)
-    grads = {"dq": torch.empty((B, T, H, D), dtype=f32, device=dev),
-             "dk": torch.empty((B, T, H, D), dtype=f32, device=dev),
-             "dv": torch.empty((B, T, HV, D), dtype=f32, device=dev),
-             "dg": torch.empty((B, T, HV, D), dtype=f32, device=dev),
-             "dbeta": torch.empty((B, T, HV), dtype=f32, device=dev),
-             "dA_log": torch.empty((HV,), dtype=f32, device=dev),
-             "ddt_bias": torch.empty((HV, D), dtype=f32, device=dev),
-             "dinitial_state": torch.empty((N, HV, D, D), dtype=f32, device=dev)}
+    from .layer import _pool, _results
+    with _pool(stream, dev):
+        if workspace is None:
+            workspace = make_bwd_workspace(B * T, N, H, HV, dev)
+        _need(workspace, "workspace", torch.uint8, dev, 1)
+        grads = {"dq": torch.empty((B, T, H, D), dtype=f32, device=dev),
+                 "dk": torch.empty((B, T, H, D), dtype=f32, device=dev),
+                 "dv": torch.empty((B, T, HV, D), dtype=f32, device=dev),
+                 "dg": torch.empty((B, T, HV, D), dtype=f32, device=dev),
+                 "dbeta": torch.empty((B, T, HV), dtype=f32, device=dev),
+                 "dA_log": torch.empty((HV,), dtype=f32, device=dev),
+                 "ddt_bias": torch.empty((HV, D), dtype=f32, device=dev),
+                 "dinitial_state": torch.empty((N, HV, D, D), dtype=f32, device=dev)}
     opts = _lib.kda_options()
     opts.num_v_heads = HV if HV != H else 0
     opts.g_dtype = GATE_FP32 if g.dtype == f32 else GATE_BF16
     opts.path = PATHS[path]
     opts.debug_stall = int(debug_stall)  # timeout tests only (see include/kda.h)
     _set_chunk_states(opts, chunk_states, dev)  # states a kda_fwd of these inputs wrote
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    sh = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    on = torch.cuda.current_stream(dev) if stream is None else stream
+    sh = on.cuda_stream if hasattr(on, "cuda_stream") else int(on)
     G = grads
     st = _lib.load().kda_bwd(
         _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale), _ptr(A_log), _ptr(dt_bias),
@@ -357,7 +358,7 @@ def kda_bwd(q, k, v, g, beta, scale, A_log, dt_bias, lower_bound, dout, initial_
     if st != KDA_OK:
         raise KdaError(st, "kda_bwd")
     grads["workspace"] = workspace
-    return grads
+    return _results(stream, dev, grads)
 
 
 def kda_get_device_status(workspace, stream=None) -> int:

@@ -128,3 +128,27 @@ def test_convolution_state_in_place(kda_lib, ty, N, T, C):
         kda.kda_conv_fwd(x, w, b, o, one, one)
         assert torch.equal(a, o) and torch.equal(one, two)
         assert torch.equal(one[:, max(0, 3 - T):], x[:, max(0, T - 3):])
+
+
+def test_recurrence_gradients_do_not_take_memory_that_is_still_read(kda_lib):
+    """The same for kda_bwd on another stream."""
+    import kimi_delta_attention_08_gb300 as kda
+    g = torch.Generator().manual_seed(4)
+    r = lambda *s, t=BF: torch.randn(*s, generator=g).to(t).cuda()  # noqa: E731
+    q, k, v, gt, dout, beta = (*(r(2, 100, 2, 128) for _ in range(5)), r(2, 100, 2))
+    A, bias = r(2, t=F), r(2, 128, t=F)
+    run = lambda s: kda.kda_bwd(q, k, v, gt, beta, 128 ** -0.5, A, bias, -5.0, dout, stream=s)  # noqa: E731
+    want = {n: t.clone() for n, t in run(None).items() if n != "workspace"}
+    sizes = [t.numel() * 4 for t in want.values()] + [kda.make_bwd_workspace(200, 2, 2).numel()]
+    s = torch.cuda.Stream()
+    old = [(torch.arange(n, device="cuda") % 251).to(torch.uint8) for n in sizes * 2]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)                       # some 50 ms
+    kept = [t.clone() for t in old]                      # queued behind it
+    del old
+    got = run(s)
+    torch.cuda.synchronize()
+    for t, n in zip(kept, sizes * 2):
+        assert torch.equal(t, (torch.arange(n, device="cuda") % 251).to(torch.uint8))
+    for n, t in want.items():
+        assert torch.equal(got[n], t), n

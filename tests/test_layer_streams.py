@@ -103,3 +103,24 @@ def test_workspace_of_a_forward_call(seen):
     x, A, B = Tensor(2, 50, 8), Tensor(8, 16), Tensor(2, 50, 1, 16)
     layer.kda_scan_fwd(x, x, A, B, B, x, stream=Stream(7))
     assert seen == [[7, []]]
+
+
+def test_gradients_of_the_recurrence(seen, monkeypatch):
+    """kda_bwd with a stream: the same."""
+    import kimi_delta_attention_08_gb300 as kda
+
+    class Library:
+        def kda_bwd(self, *args):
+            return 0
+
+        def kda_bwd_get_workspace_size(self, *args):
+            return 0
+
+    monkeypatch.setattr(kda._lib, "load", Library)
+    bf = torch.bfloat16
+    q, beta, A, bias = Tensor(1, 9, 2, 128, dtype=bf), Tensor(1, 9, 2, dtype=bf), Tensor(2), Tensor(2, 128)
+    ws = Tensor(1 << 20, dtype=torch.uint8)
+    for stream, handle, kept in ((None, 100, []), (Stream(7), 7, [100, 7]), (7, 7, [100]), (0, 0, [100])):
+        seen.clear()
+        kda.kda_bwd(q, q, q, q, beta, 1.0, A, bias, -5.0, q, workspace=ws, stream=stream)
+        assert len(seen) == 8 and all(e == [handle, kept] for e in seen), (stream, seen)
