@@ -41,19 +41,21 @@ def shard_piece(rank, q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound,
     """Phase 1 on rank `rank`: its piece, float32 [2, N, HV, 128, 128] = (M_r, B_r).
     Rank 0 also writes its outputs into `out`."""
     import torch
+    from .layer import _pool, _results
     _check_fp32_state(initial_state, "initial_state")
     B, T, HV = v.shape[0], v.shape[1], v.shape[2]
     dev = v.device
-    if workspace is None:
-        workspace = make_workspace(B * T, HV, dev)
-    piece = torch.zeros((2, B, HV, 128, 128), dtype=torch.float32, device=dev)
-    if rank == 0:
-        kda_fwd(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, initial_state,
-                piece[1], None, workspace, stream=stream)
-    else:
-        kda_fwd_transition(q, k, v, g, beta, A_log, dt_bias, lower_bound, piece[0], piece[1],
-                           None, workspace, stream=stream)
-    return piece
+    with _pool(stream, dev):  # all of it on the caller's stream
+        if workspace is None:
+            workspace = make_workspace(B * T, HV, dev)
+        piece = torch.zeros((2, B, HV, 128, 128), dtype=torch.float32, device=dev)
+        if rank == 0:
+            kda_fwd(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, initial_state,
+                    piece[1], None, workspace)
+        else:
+            kda_fwd_transition(q, k, v, g, beta, A_log, dt_bias, lower_bound, piece[0], piece[1],
+                               None, workspace)
+    return _results(stream, dev, {"piece": piece})["piece"]
 
 
 def exchange(piece, group=None):
@@ -72,21 +74,23 @@ def shard_finish(rank, pieces, q, k, v, g, beta, scale, out, A_log, dt_bias, low
     ranks before it and rerun its shard, writing `out` and (if given) its final
     state.  On rank 0 only the final state is copied out of its piece."""
     import torch
+    from .layer import _pool
     _check_fp32_state(final_state, "final_state")
     B, T, HV = v.shape[0], v.shape[1], v.shape[2]
-    if rank == 0:
-        if final_state is not None:
-            final_state.copy_(pieces[0, 1])
-        return
     dev = v.device
-    start = torch.empty((B, HV, 128, 128), dtype=torch.float32, device=dev)
-    M = pieces[:rank, 0].contiguous()
-    Bo = pieces[:rank, 1].contiguous()
-    kda_compose_states(M, Bo, start, None, stream=stream)
-    if workspace is None:
-        workspace = make_workspace(B * T, HV, dev)
-    kda_fwd(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, start, final_state, None,
-            workspace, stream=stream)
+    with _pool(stream, dev):
+        if rank == 0:
+            if final_state is not None:
+                final_state.copy_(pieces[0, 1])
+            return
+        start = torch.empty((B, HV, 128, 128), dtype=torch.float32, device=dev)
+        M = pieces[:rank, 0].contiguous()
+        Bo = pieces[:rank, 1].contiguous()
+        kda_compose_states(M, Bo, start, None)
+        if workspace is None:
+            workspace = make_workspace(B * T, HV, dev)
+        kda_fwd(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound, start, final_state, None,
+                workspace)
 
 
 def fwd_sequence_shard(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound,
@@ -95,9 +99,11 @@ def fwd_sequence_shard(q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound
     `initial_state` is read on rank 0 only, `final_state` is the sequence's final
     state on the last rank (the state at the end of this rank's shard elsewhere)."""
     import torch.distributed as dist
+    from .layer import _pool
     rank = dist.get_rank(group)
-    piece = shard_piece(rank, q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound,
-                        initial_state if rank == 0 else None, stream=stream)
-    pieces = exchange(piece, group)
-    shard_finish(rank, pieces, q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound,
-                 final_state, stream=stream)
+    with _pool(stream, v.device):  # the exchange is in the stream's order too
+        piece = shard_piece(rank, q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound,
+                            initial_state if rank == 0 else None)
+        pieces = exchange(piece, group)
+        shard_finish(rank, pieces, q, k, v, g, beta, scale, out, A_log, dt_bias, lower_bound,
+                     final_state)

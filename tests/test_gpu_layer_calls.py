@@ -152,3 +152,31 @@ def test_recurrence_gradients_do_not_take_memory_that_is_still_read(kda_lib):
         assert torch.equal(t, (torch.arange(n, device="cuda") % 251).to(torch.uint8))
     for n, t in want.items():
         assert torch.equal(got[n], t), n
+
+
+def test_shards_on_another_stream(kda_lib):
+    """A sharded forward on a stream that is not the current one, which is busy: the zeros of a
+    piece, the copies between the phases and the final state are in that stream's order."""
+    from kimi_delta_attention_08_gb300 import shard
+    g = torch.Generator().manual_seed(6)
+    r = lambda *s, t=BF: torch.randn(*s, generator=g).to(t).cuda()  # noqa: E731
+    x = [r(1, 200, 2, 128) for _ in range(4)] + [r(1, 200, 2)]
+    A, bias = r(2, t=F), r(2, 128, t=F)
+    cut = [[t[:, a:b].contiguous() for t in x] for a, b in ((0, 80), (80, 200))]
+
+    def run(stream):
+        outs = [torch.full_like(c[2], float("nan")) for c in cut]
+        fins = [torch.full((1, 2, 128, 128), float("nan"), device="cuda") for _ in cut]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)                   # some 50 ms of the current stream
+        args = lambda i: (*cut[i], 128 ** -0.5, outs[i], A, bias, -5.0)  # noqa: E731
+        pieces = [shard.shard_piece(i, *args(i), stream=stream) for i in range(2)]
+        with torch.cuda.stream(stream or torch.cuda.current_stream()):
+            pieces = torch.stack(pieces)
+        for i in range(2):
+            shard.shard_finish(i, pieces, *args(i), fins[i], stream=stream)
+        torch.cuda.synchronize()
+        return outs + fins
+
+    for a, b in zip(run(None), run(torch.cuda.Stream())):
+        assert torch.equal(a, b)
