@@ -160,15 +160,19 @@ def _pool(stream, dev):
 
 
 def _results(stream, dev, grads):
-    """Results in another stream's memory live until the current stream is done with them, and
-    a caller's workspace until the other one is."""
+    """Results in another stream's memory live until the current stream is done with them."""
     if stream is not None:
         here = torch.cuda.current_stream(dev)
         for t in grads.values():
             t.record_stream(here)
-            if isinstance(stream, torch.cuda.Stream):
-                t.record_stream(stream)
+            _in_use(t, stream)
     return grads
+
+
+def _in_use(t, stream):
+    """A buffer that a caller made for a call lives until the call's stream is done with it."""
+    if isinstance(stream, torch.cuda.Stream):
+        t.record_stream(stream)
 
 
 def _workspace(given, size, dev, stream):
@@ -182,6 +186,8 @@ def _workspace(given, size, dev, stream):
         given = torch.empty(size(), dtype=torch.uint8, device=dev)
     elif _tensor(given, "workspace").dtype != torch.uint8 or given.device != dev or not given.is_contiguous():
         raise ValueError("workspace: expected a contiguous uint8 tensor on the tensors' device")
+    else:
+        _in_use(given, stream)
     return given, given.data_ptr(), given.numel()
 
 
@@ -382,11 +388,12 @@ def make_scan_workspace(batch, T, dim, state, groups=1, N=None, *, backward=Fals
     return torch.empty(n, dtype=torch.uint8, device=device if device is not None else "cuda")
 
 
-def _states_arg(buf, dev):
+def _states_arg(buf, dev, stream):
     if buf is None:
         return None, 0
     if _tensor(buf, "chunk_states").dtype != torch.uint8 or buf.device != dev or not buf.is_contiguous():
         raise ValueError("chunk_states: expected make_scan_states's buffer on the tensors' device")
+    _in_use(buf, stream)
     return buf.data_ptr(), buf.numel()
 
 
@@ -407,7 +414,7 @@ def kda_scan_fwd(x, dt, A_log, B, C, out, D=None, z=None, dt_bias=None, initial_
                              cu_seqlens, ("initial_state", "final_state"))
     dev = x.device
     op = _need(out, "out", x.dtype, dev, x.shape)
-    cp, cb = _states_arg(chunk_states, dev)
+    cp, cb = _states_arg(chunk_states, dev, stream)
     wp = wb = 0
     if workspace is not None or q.T > 8 or q.cu_seqlens or cp:
         with _pool(stream, dev):
@@ -427,7 +434,7 @@ def kda_scan_bwd(x, dt, A_log, B, C, dout, D=None, z=None, dt_bias=None, initial
                               cu_seqlens, ("initial_state", "dfinal_state"))
     dev, ty = x.device, x.dtype
     dop = _need(dout, "dout", ty, dev, x.shape)
-    cp, cb = _states_arg(chunk_states, dev)
+    cp, cb = _states_arg(chunk_states, dev, stream)
     E = lambda shape, t=_f32: torch.empty(shape, dtype=t, device=dev)
     with _pool(stream, dev):
         ws, wp, wb = _workspace(workspace, lambda: _size("kda_scan_bwd_get_workspace_size",

@@ -124,3 +124,24 @@ def test_gradients_of_the_recurrence(seen, monkeypatch):
         seen.clear()
         kda.kda_bwd(q, q, q, q, beta, 1.0, A, bias, -5.0, q, workspace=ws, stream=stream)
         assert len(seen) == 8 and all(e == [handle, kept] for e in seen), (stream, seen)
+
+
+def test_buffers_made_for_a_call_live_until_its_stream_is_done(seen, monkeypatch):
+    """Saved states and workspaces may be dropped right after the call."""
+    kept = []
+    monkeypatch.setattr(Tensor, "record_stream", lambda self, s: kept.append((self, s.cuda_stream)))
+    x, A, B, w, b = Tensor(2, 50, 8), Tensor(8, 16), Tensor(2, 50, 1, 16), Tensor(8, 4), Tensor(8)
+    ws, st = (Tensor(1 << 20, dtype=torch.uint8) for _ in range(2))
+    for run, buffers in (
+            (lambda s: layer.kda_scan_fwd(x, x, A, B, B, x, workspace=ws, chunk_states=st, stream=s), {ws, st}),
+            (lambda s: layer.kda_scan_bwd(x, x, A, B, B, x, workspace=ws, chunk_states=st, stream=s), {ws, st}),
+            (lambda s: layer.kda_conv_fwd(x, w, b, x, workspace=ws, stream=s), {ws}),
+            (lambda s: layer.kda_conv_bwd(x, w, b, x, workspace=ws, stream=s), {ws}),
+            (lambda s: layer.kda_prenorm_bwd(x, None, x, b, workspace=ws, stream=s), {ws}),
+            (lambda s: layer.kda_postnorm_bwd(x, x, b, None, ws, stream=s), {ws})):
+        kept.clear()
+        run(Stream(7))
+        assert {id(t) for t, s in kept if s == 7} == {id(t) for t in buffers}
+        kept.clear()
+        run(None)
+        assert not kept
