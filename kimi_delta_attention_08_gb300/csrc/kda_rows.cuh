@@ -14,7 +14,7 @@ namespace kda {
 namespace rows {
 
 constexpr float kLog2e = 1.4426950408889634f, kLog2eRest = 1.925963033500e-8f;  // log2 e: fp32, and the rest
-constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLn2 = 0.6931471805599453f, kLn2Rest = -1.904654e-9f;  // and ln 2
 
 using bf16 = __nv_bfloat16;
 
@@ -172,26 +172,30 @@ __device__ __forceinline__ pair pex2(pair v) {
   return pr(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y));
 }
 
-// exp(-x) = 2^h, h = -x log2 e, with the hardware exponential (2^-22).  Rounding h makes the
+// exp(-x) = 2^-n, n = x log2 e, with the hardware exponential (2^-22).  Rounding n makes the
 // error grow by 1.5 steps of 2^-24 for each unit of x: nothing to a step of bf16, but for rows
-// of fp32 (T) what the rounding left out, l, is put back as 2^h (1 + l ln 2); not where that
-// is no number because x or the result is infinite.
+// of fp32 (T) the rounding is put back as exp(-x) = 2^-n (1 + (n ln 2 - x)).  That takes an x
+// whose exponential is finite; at the ends sigmoid(x) is 0 and 1 as it is beyond them.
+__device__ __forceinline__ float exp_range(float x) {  // what is no number stays none
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(-88.5f));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(128.f));
+  return x;
+}
 template <typename T>
 __device__ __forceinline__ float exp_minus(float x) {
+  if constexpr (sizeof(T) < 4) return ptx::ex2_approx(-x * kLog2e);
+  x = exp_range(x);
   const float n = x * kLog2e, e = ptx::ex2_approx(-n);
-  if constexpr (sizeof(T) < 4) return e;
-  const float l = fmaf(x, -kLog2eRest, fmaf(x, -kLog2e, n)), r = fmaf(e, l * kLn2, e);
-  return fabsf(r) < INFINITY ? r : e;
+  return fmaf(e, fmaf(n, kLn2Rest, fmaf(n, kLn2, -x)), e);
 }
 template <typename T>
 __device__ __forceinline__ pair exp_minus(pair x) {
+  if constexpr (sizeof(T) < 4) return pex2(pmul(x, pr(-kLog2e)));
+  const float2 v = un(x);
+  x = pr(exp_range(v.x), exp_range(v.y));
   const pair n = pmul(x, pr(kLog2e));
-  const float2 h = un(n);
-  const pair e = pr(ptx::ex2_approx(-h.x), ptx::ex2_approx(-h.y));
-  if constexpr (sizeof(T) < 4) return e;
-  const pair l = pfma(x, pr(-kLog2eRest), pfma(x, pr(-kLog2e), n));
-  const float2 r = un(pfma(e, pmul(l, pr(kLn2)), e)), f = un(e);
-  return pr(fabsf(r.x) < INFINITY ? r.x : f.x, fabsf(r.y) < INFINITY ? r.y : f.y);
+  const pair e = pr(ptx::ex2_approx(-un(n).x), ptx::ex2_approx(-un(n).y));
+  return pfma(e, pfma(n, pr(kLn2Rest), pfma(n, pr(kLn2), pmul(x, pr(-1.f)))), e);
 }
 
 // sigmoid(x) = 1 / (1 + exp(-x)) with the hardware reciprocal (2^-23): a clean zero where the
@@ -216,11 +220,12 @@ __device__ __forceinline__ pair silu_slope(pair x, pair s) {
 }
 
 // sigmoid(x) and its slope sigmoid(x) sigmoid(-x) = e s^2 with e = exp(-x).  As s - s^2 it would
-// lose its digits where s nears 1: all of them from x = 17 on.  (An infinite e meets s = 0.)
+// lose its digits where s nears 1: all of them from x = 17 on.  (An infinite e, which fp32 rows do
+// not have, meets s = 0.)
 template <typename T>
 __device__ __forceinline__ float sigmoid(float x, float& slope) {
   const float e = exp_minus<T>(x), s = ptx::rcp_approx(1.0f + e);
-  slope = fminf(e, FLT_MAX) * s * s;
+  slope = (sizeof(T) < 4 ? fminf(e, FLT_MAX) : e) * s * s;
   return s;
 }
 template <typename T>
@@ -228,7 +233,8 @@ __device__ __forceinline__ pair sigmoid(pair x, pair& slope) {
   const pair e = exp_minus<T>(x);
   const float2 d = un(padd(e, pr(1.0f)));
   const pair s = pr(ptx::rcp_approx(d.x), ptx::rcp_approx(d.y));
-  slope = pmul(pmul(pr(fminf(un(e).x, FLT_MAX), fminf(un(e).y, FLT_MAX)), s), s);
+  const pair f = sizeof(T) < 4 ? pr(fminf(un(e).x, FLT_MAX), fminf(un(e).y, FLT_MAX)) : e;
+  slope = pmul(pmul(f, s), s);
   return s;
 }
 
