@@ -18,8 +18,9 @@
  *
  * Sequences.  cu_seqlens as in kda_fwd: NULL (batched), or int64 [N+1] on the
  * device with B == 1, cu[0] = 0, non-decreasing, cu[N] <= T; rows from cu[N] on
- * belong to no sequence: they are neither read nor written, and a backward writes
- * zeros as their gradients.  Empty sequences are allowed: their final state is their initial one.
+ * belong to no sequence: their values count for nothing, outputs are left as they were
+ * there, and a backward writes zeros as their gradients.  Empty sequences are allowed:
+ * their final state is their initial one.
  * An inconsistent cu_seqlens is recorded as KDA_ERR_BAD_SEQLENS in the workspace's
  * status word (kda_get_device_status); the tokens it misplaces are skipped or
  * computed from a wrong start, and no access leaves the buffers.
@@ -53,7 +54,8 @@ typedef enum { KDA_FN_NONE = 0, KDA_FN_SILU = 1, KDA_FN_SIGMOID = 2 } kda_fn;
  *     out[t][c] = fn(p[t][c])
  * where xx is the sequence's x with the width - 1 rows of its initial state before
  * it (zeros when initial_state is NULL).  The final state is the last width - 1
- * rows of xx.  One token at a time is the case T == 1 with the states carried.
+ * rows of xx.  One token at a time is the case T == 1 with the states carried, which has
+ * a kernel of its own; single tokens packed with cu_seqlens do not reach it.
  *   x               rows [B, T, C], x_stride.
  *   weight          fp32 [C, width]; bias fp32 [C] or NULL (zero).
  *   outs            num_outs (1 .. KDA_CONV_MAX_OUTS) host array of device buffers;
@@ -106,7 +108,10 @@ KDA_API kda_status kda_conv_bwd(const void* x, int64_t x_stride, const float* we
  *     h_t[d][n] = exp(-delta exp(A_log[d][n])) h_{t-1}[d][n] + delta x[t][d] B[t][g][n]
  *     y[t][d]   = sum_n C[t][g][n] h_t[d][n] + D[d] x[t][d],     out = y silu(z)
  * with g = d / (dim / groups).  D, z and dt_bias may be NULL (no term, no gate,
- * zero); h starts at the sequence's initial state.
+ * zero); h starts at the sequence's initial state.  States, their gradients and saved
+ * states are 16-byte aligned (KDA_ERR_MISALIGNED).  Prompts of up to 8 tokens, single ones
+ * above all, have a kernel of their own, without cu_seqlens and without saved states;
+ * packed single tokens take 15 times as long.
  */
 typedef struct {
   const void* x;              /* rows [B, T, dim]                                    */
@@ -167,6 +172,7 @@ KDA_API kda_status kda_scan_bwd(const kda_scan_problem* p, const void* dout,
  *
  * kda_prenorm_fwd -- before a block:
  *     residual_out = residual + s * x          out = unit(residual_out) * weight
+ * (out from the sum before it is rounded to stream_dtype).
  *   x, out          rows [rows, dim] of type dtype.
  *   residual        NULL (zero) or rows of type stream_dtype (dtype or fp32).
  *   residual_out    NULL (not written) or rows of type stream_dtype; it may be residual.

@@ -14,10 +14,12 @@
 // into shared memory meanwhile, asked for by the thread that reads them, so without a barrier.
 //
 // Device time, and bytes of the rows over it (SiLU, width 4, bf16): 74,080 packed tokens of
-// 6,144 channels with states 285 us (6.4 TB/s; 413 with the next rows in registers); single
-// tokens of 256 sequences of 12,288 channels 9.8 us; backward of 32,768 tokens of 12,288
-// channels 451 us (5.4 TB/s; 636 with the rows in registers), which the FMA pipe's latency
-// with 12 warps of 166 registers per SM keeps from the 356 us that its bytes take.
+// 6,144 channels with states 284 us (6.4 TB/s; 413 with the next rows in registers; fp32 538,
+// 6.8 TB/s); single tokens of 256 sequences of 12,288 channels 9.8 us (fp32 17.6); backward of
+// 32,768 tokens of 12,288 channels 441 us (5.5 TB/s; 636 with the rows in registers; fp32 723,
+// 6.7 TB/s; bf16 with fp32 gradients of the outputs 497, 6.5 TB/s), which the FMA pipe's latency
+// with 12 warps of 164 registers per SM keeps from the 356 us that its bytes take.  The weights'
+// gradients are summed in fp32 and within 2.3e-7 of their 64-bit values over 32,768 tokens.
 #include "kda_internal.h"
 #include "kda_rows.cuh"
 #include "../../include/kda_layer.h"
@@ -682,7 +684,7 @@ void (*conv_kernel_v(int width, int fn))(ConvParams) {
 
 // Channels per thread.  Forward: 16 bytes (one token: 8, for twice the threads: 10.3 us
 // against 13.3 for 256 sequences of 12,288 channels); backward: 4, whose weights, their gradients
-// and two histories take 166 registers, 12 warps per SM.
+// and two histories take 164 registers, 12 warps per SM.
 constexpr int kFwdV16 = 8, kFwdV32 = 4, kStepV = 4, kBwdV = 4;
 
 template <int PASS>

@@ -13,13 +13,19 @@
 // of up to 64 vectors belong to 16 or 32 lanes (no barrier, several rows per
 // warp's loads in flight); longer ones to a block with one barrier per row.  Weight
 // gradients are summed over a block's rows in registers, then over the blocks by a
-// second launch, in a fixed order.
+// second launch, in a fixed order and in fp32: 2 to 3e-7 from their 64-bit values over 2^27
+// values.  Sums of 16 rows at a time, added apart, and a second launch in 64 bits halve that
+// and take 3 to 33 % longer.
 //
 // Device time, and bytes of the rows over it: forward before a block, 32,768 rows of 4,096
 // bf16 values with an fp32 residual, 238 us (6.8 TB/s); forward after one, 1,048,576 rows of
-// 128 bf16 with a gate, 137 us (5.9 TB/s); backward before a block, 32,768 x 4,096 bf16
-// with a learned scale, 247 us (6.5 TB/s); backward after one, 74,097 rows of 1,001 fp32
-// with gate and scale (no 16-byte alignment, so single values), 298 us (5.0 TB/s).
+// 128 bf16 with a gate, 136 us (5.9 TB/s); backward before a block, 32,768 x 4,096 bf16
+// with a learned scale, 245 us (6.6 TB/s); backward after one, 74,097 rows of 1,001 fp32
+// with gate and scale (no 16-byte alignment, so single values), 303 us (4.9 TB/s).  Backward
+// over rows wider than 4,096, whose two vectors per thread and next rows in registers spill:
+// 2^27 bf16 values with a learned scale in rows of 5,120 396, of 8,192 318 us before a block;
+// after one, with a SiLU gate, 395 and 368.  Backward without a gate, bf16, where a row brings
+// too few bytes to hide its two sums and the barrier: 2^27 values in rows of 1,024 169 us.
 #include "kda_internal.h"
 #include "kda_rows.cuh"
 #include "../../include/kda_layer.h"

@@ -20,8 +20,9 @@
 // pairs of channels, and about as many other instructions (shared-memory reads, the sums over
 // channels and over states), so it is bound by the rate at which a scheduler issues: about
 // 0.5 instructions a clock, a packed one taking two or three.  4 sequences of 4,096 tokens,
-// 4,096 channels, 16 states in bf16: 1.70 ms, 2.28 with the forward that saves the states
-// (0.65 TB/s); the exponentials alone would take 0.23 ms.  As in the forward, sequences are cut
+// 4,096 channels, 16 states in bf16: 1.69 ms, 2.27 with the forward that saves the states
+// (0.65 TB/s; fp32 2.41); the exponentials alone would take 0.23 ms.  At 168 registers the
+// kernels for 8 and 16 states spill 68 to 128 bytes.  As in the forward, sequences are cut
 // into segments where channels alone do not fill the GPU: a reverse pass computes each
 // segment's gradient at its start from a zero gradient at its end, and a second launch
 // carries the gradients over the segments.

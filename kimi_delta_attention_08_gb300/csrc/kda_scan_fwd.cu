@@ -13,8 +13,9 @@
 // dot product over a channel's lanes is reduced for as many tokens at a time as there are
 // lanes, so each lane ends up with the tokens that it loaded.
 //
-// 8 sequences of 4,096 tokens, 4,096 channels, 16 states in bf16 take 784 us (1.4 TB/s; the
-// exponentials alone 230 us, those and the packed operations 290); one of 65,536 tokens
+// 8 sequences of 4,096 tokens, 4,096 channels, 16 states in bf16 take 783 us (1.4 TB/s; the
+// exponentials alone 230 us, those and the packed operations 290; fp32 rows 797 us; 8 states
+// 749, 32 states 1,513); one of 65,536 tokens
 // and five of 1,024 with 1,024 channels, which has to be cut, 633 us.
 //
 // Where the channels alone do not fill the GPU, sequences are cut into segments: a first
@@ -301,7 +302,8 @@ __global__ void scan_carry_kernel(const ScanParams p, int state) {
 // dot products and writes their outputs.  256 sequences of 4,096 channels and 16 fp32 states
 // take 24.9 us (5.7 TB/s) in blocks of 7 per SM; with 8 it spills (29.2), with 5 too few
 // loads are in flight (36).  Before the rates were computed behind the last load it took
-// 33.1; one thread for all 16 states of a channel reads 64 bytes apart (36.8); CTAs that
+// 33.1; with fp32 rows, whose kernels spill 64 bytes, it takes 31.5 us; one thread for all 16 states
+// of a channel reads 64 bytes apart (36.8); CTAs that
 // stay, with the next states on their way into shared memory, take 32 to 43.
 constexpr int kStepSeqs = 4;
 constexpr int kStepTokens = 8;  // the longest such prompt
