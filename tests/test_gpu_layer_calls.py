@@ -180,3 +180,54 @@ def test_shards_on_another_stream(kda_lib):
 
     for a, b in zip(run(None), run(torch.cuda.Stream())):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("op", ["prenorm", "postnorm"])
+def test_two_widths_in_one_graph(kda_lib, op):
+    """Rows of 4,096, 2,048 and 4,096 again in one captured graph, direct calls of another width
+    between its replays."""
+    import kimi_delta_attention_08_gb300 as kda
+    cases = [norm_case(D, D, F) for D in (4096, 2048, 4096)]
+    want = [run_norm(kda, op, a) for a in cases]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [run_norm(kda, op, a) for a in cases]
+    other = norm_case(1024, 3, F)
+    for _ in range(3):
+        for r in got:
+            for t in r.values():
+                t.fill_(float("nan"))
+        run_norm(kda, op, other)
+        graph.replay()
+        torch.cuda.synchronize()
+        for r, w in zip(got, want):
+            for k in w:
+                assert torch.equal(r[k], w[k]), k
+
+
+@pytest.mark.parametrize("op", ["conv", "scan", "prenorm", "postnorm"])
+def test_captured_on_a_side_stream(kda_lib, op):
+    """A call on a stream that a capture forks to, its memory from there: replays give the bits
+    of a direct call, also while another graph of the same call is alive."""
+    import kimi_delta_attention_08_gb300 as kda
+    run, ws = backward(kda, op)
+    want = {k: v.clone() for k, v in run(None, None).items() if k != "workspace"}
+    torch.cuda.synchronize()
+    s, graphs, got = torch.cuda.Stream(), [], []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            s.wait_stream(torch.cuda.current_stream())
+            got.append(run(s, None))
+            torch.cuda.current_stream().wait_stream(s)
+    for _ in range(2):
+        for r in got:
+            for k in want:
+                r[k].fill_(float("nan"))
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for r in got:
+            for k, v in want.items():
+                assert torch.equal(r[k], v), k
