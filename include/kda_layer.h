@@ -1,7 +1,8 @@
 /*
  * kda_layer.h -- C ABI of the operators that stand around the KDA recurrence in a
- * layer: the short causal convolution before it, the selective state space scan as
- * its sibling token mixer, and the norms before and after a block.  The conventions
+ * layer: the short causal convolution before it, the selective state space scan and the
+ * gated linear recurrence as its sibling token mixers, the norms before and after a
+ * block, and the gated feed-forward product between them.  The conventions
  * of kda.h hold (device pointers, caller-owned buffers, nothing allocated or
  * synchronised, work enqueued on `stream` only, errors as kda_status before
  * anything is enqueued, no implicit conversion), and every entry point can be
@@ -45,6 +46,7 @@ typedef enum { KDA_FN_NONE = 0, KDA_FN_SILU = 1, KDA_FN_SIGMOID = 2 } kda_fn;
 #define KDA_CONV_MAX_OUTS 4
 #define KDA_NORM_MAX_DIM 8192
 #define KDA_SCAN_CHUNK 32       /* tokens between two saved states of the scan */
+#define KDA_LINREC_CHUNK 64     /* rows between two saved states of the linear recurrence */
 #define KDA_STATUS_BYTES 256    /* a workspace that holds a status word only    */
 
 /* ----------------------------------------------------------- convolution --
@@ -164,6 +166,68 @@ KDA_API kda_status kda_scan_bwd(const kda_scan_problem* p, const void* dout,
                                 void* dC, float* dA_log, float* dD, float* ddt_bias,
                                 float* dinitial_state, void* workspace, size_t workspace_bytes,
                                 cudaStream_t stream);
+
+/* ------------------------------------------------------ linear recurrence --
+ * The gated linear recurrence, per channel d with one state:
+ *     L = exp(A_log[d]) sigmoid(r[t][d] + r_bias[d]),   a = exp(-L)
+ *     h_t[d] = a h_{t-1}[d] + sqrt(1 - a^2) sigmoid(i[t][d] + i_bias[d]) x[t][d]
+ *     out = h silu(z)
+ * z, r_bias and i_bias may be NULL (no gate, zero); h starts at the sequence's initial
+ * state.  Prompts of up to 8 tokens, single ones above all, have a kernel of their own,
+ * without cu_seqlens and without saved states, which needs no workspace.  A value that is
+ * not finite leaves its channel not finite up to the end of its sequence.
+ */
+typedef struct {
+  const void* x;              /* rows [B, T, dim]                                    */
+  const void* r;              /* rows [B, T, dim]: raw decay gate                    */
+  const void* i;              /* rows [B, T, dim]: raw input gate                    */
+  const void* z;              /* NULL or rows [B, T, dim]: raw output gate           */
+  int64_t x_stride, r_stride, i_stride, z_stride;
+  const float* A_log;         /* fp32 [dim]                                          */
+  const float* r_bias;        /* NULL or fp32 [dim]                                  */
+  const float* i_bias;        /* NULL or fp32 [dim]                                  */
+  const void* initial_state;  /* NULL (zero) or [N, dim] in state_dtype              */
+  const int64_t* cu_seqlens;
+  int64_t batch, T;           /* batch: B                                            */
+  int32_t N;                  /* sequences (taken as batch without cu_seqlens)       */
+  int32_t dim;
+  int32_t dtype;              /* kda_row_dtype of x, r, i, z, out and gradients      */
+  int32_t state_dtype;        /* kda_state_dtype of initial, final states, dfinal    */
+  int32_t debug_stall;        /* 0; 1 (a test's hook): the first tile's result is    */
+                              /* never handed on, waits for it run out and the       */
+                              /* status word reads KDA_ERR_DEVICE_TIMEOUT            */
+  int32_t reserved;           /* 0                                                   */
+} kda_linrec_problem;
+
+/* Bytes of the buffer of saved states that kda_linrec_fwd writes for kda_linrec_bwd: fp32
+ * [total_tokens / KDA_LINREC_CHUNK + 1][dim], the state before each such row of the batch. */
+KDA_API kda_status kda_linrec_get_states_size(int64_t total_tokens, int32_t dim, size_t* bytes);
+/* Bytes of workspace (128-byte aligned) of kda_linrec_fwd and, with or without saved states,
+ * of kda_linrec_bwd; only the problem's sizes are read, and whether cu_seqlens is NULL. */
+KDA_API kda_status kda_linrec_get_workspace_size(const kda_linrec_problem* p, size_t* bytes);
+KDA_API kda_status kda_linrec_bwd_get_workspace_size(const kda_linrec_problem* p,
+                                                     int32_t have_states, size_t* bytes);
+
+/* kda_linrec_fwd -- out [B, T, dim] and (unless NULL) final_state [N, dim], written;
+ * final_state may be initial_state itself.  chunk_states: NULL, or the buffer of saved
+ * states (16-byte aligned), written.  workspace: may be NULL for prompts of up to 8 tokens
+ * without cu_seqlens and chunk_states.  After KDA_ERR_DEVICE_TIMEOUT in its status word
+ * what the call wrote is not to be used. */
+KDA_API kda_status kda_linrec_fwd(const kda_linrec_problem* p, void* out, void* final_state,
+                                  void* chunk_states, size_t chunk_states_bytes, void* workspace,
+                                  size_t workspace_bytes, cudaStream_t stream);
+
+/* kda_linrec_bwd -- the gradients of <dout, out> + <dfinal_state, final_state> for the
+ * forward call of the same problem.  chunk_states: NULL (recomputed), or what that call
+ * saved.  dx, dr, di, dz, dout: [B, T, dim] in the rows' type (dz only where the problem
+ * has z).  dA_log, dr_bias, di_bias [dim], dinitial_state [N, dim]: fp32; the last three
+ * may be NULL (not written). */
+KDA_API kda_status kda_linrec_bwd(const kda_linrec_problem* p, const void* dout,
+                                  const void* dfinal_state, const void* chunk_states,
+                                  size_t chunk_states_bytes, void* dx, void* dr, void* di, void* dz,
+                                  float* dA_log, float* dr_bias, float* di_bias,
+                                  float* dinitial_state, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream);
 
 /* ------------------------------------------------------------------ norms --
  * unit(h) = h / sqrt(mean(h^2) + eps) over the last axis of dim values.

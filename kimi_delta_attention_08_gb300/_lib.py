@@ -17,7 +17,9 @@ EXPORTS = ("kda_status_string", "kda_get_workspace_size", "kda_fwd", "kda_get_de
            "kda_scan_fwd", "kda_scan_bwd", "kda_scan_get_states_size",
            "kda_scan_get_workspace_size", "kda_scan_bwd_get_workspace_size",
            "kda_prenorm_fwd", "kda_prenorm_bwd", "kda_postnorm_fwd", "kda_postnorm_bwd",
-           "kda_norm_bwd_get_workspace_size")
+           "kda_norm_bwd_get_workspace_size",
+           "kda_linrec_fwd", "kda_linrec_bwd", "kda_linrec_get_states_size",
+           "kda_linrec_get_workspace_size", "kda_linrec_bwd_get_workspace_size")
 
 _lib = None
 
@@ -38,6 +40,16 @@ class kda_scan_problem(ctypes.Structure):
                 [("batch", ctypes.c_int64), ("T", ctypes.c_int64)] +
                 [(n, ctypes.c_int32) for n in ("N", "dim", "state", "groups", "dtype",
                                                "state_dtype")])
+
+
+class kda_linrec_problem(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "r", "i", "z")] +
+                [(n + "_stride", ctypes.c_int64) for n in ("x", "r", "i", "z")] +
+                [(n, ctypes.c_void_p) for n in ("A_log", "r_bias", "i_bias", "initial_state",
+                                                "cu_seqlens")] +
+                [("batch", ctypes.c_int64), ("T", ctypes.c_int64)] +
+                [(n, ctypes.c_int32) for n in ("N", "dim", "dtype", "state_dtype", "debug_stall",
+                                               "reserved")])
 
 
 def load():
@@ -79,6 +91,7 @@ def load():
     lib.kda_static_scratch_device_status.argtypes = [ctypes.POINTER(ctypes.c_int), P]
     S, Z = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
     Q = ctypes.POINTER(kda_scan_problem)
+    L = ctypes.POINTER(kda_linrec_problem)
     for name, args in (
             ("kda_conv_fwd", [P, I64, P, P, P, P, I32, P, P, P, I64, I64, I32, I32, I32, I32, I32, P,
                               S, P]),
@@ -90,6 +103,11 @@ def load():
             ("kda_scan_bwd_get_workspace_size", [Q, I32, Z]),
             ("kda_scan_fwd", [Q, P, P, P, S, P, S, P]),
             ("kda_scan_bwd", [Q, P, P, P, S] + [P] * 10 + [S, P]),
+            ("kda_linrec_get_states_size", [I64, I32, Z]),
+            ("kda_linrec_get_workspace_size", [L, Z]),
+            ("kda_linrec_bwd_get_workspace_size", [L, I32, Z]),
+            ("kda_linrec_fwd", [L, P, P, P, S, P, S, P]),
+            ("kda_linrec_bwd", [L, P, P, P, S] + [P] * 9 + [S, P]),
             ("kda_prenorm_fwd", [P, P, P, P, F, F, P, P, I64, I32, I32, I32, P]),
             ("kda_norm_bwd_get_workspace_size", [I64, I32, Z]),
             ("kda_prenorm_bwd", [P, P, P, P, P, P, F, F, P, P, P, P, I64, I32, I32, I32, P, S, P]),

@@ -1,6 +1,6 @@
 """Binding of the operators around the KDA recurrence in a layer (include/kda_layer.h):
-the short causal convolution, the selective state space scan, and the norms before
-and after a block.
+the short causal convolution, the selective state space scan, the gated linear
+recurrence, and the norms before and after a block.
 
 As in the rest of the binding, arguments are only checked and passed on: every
 tensor has to have the documented dtype, device and layout.  Row arguments marked
@@ -388,11 +388,11 @@ def make_scan_workspace(batch, T, dim, state, groups=1, N=None, *, backward=Fals
     return torch.empty(n, dtype=torch.uint8, device=device if device is not None else "cuda")
 
 
-def _states_arg(buf, dev, stream):
+def _states_arg(buf, dev, stream, maker="make_scan_states"):
     if buf is None:
         return None, 0
     if _tensor(buf, "chunk_states").dtype != torch.uint8 or buf.device != dev or not buf.is_contiguous():
-        raise ValueError("chunk_states: expected make_scan_states's buffer on the tensors' device")
+        raise ValueError(f"chunk_states: expected {maker}'s buffer on the tensors' device")
     _in_use(buf, stream)
     return buf.data_ptr(), buf.numel()
 
@@ -452,6 +452,121 @@ def kda_scan_bwd(x, dt, A_log, B, C, dout, D=None, z=None, dt_bias=None, initial
     P = lambda nm: g[nm].data_ptr() if nm in g else None
     _call("kda_scan_bwd", dev, stream, ctypes.byref(q), dop, dfp, cp, cb, P("dx"), P("ddt"), P("dz"),
           P("dB"), P("dC"), P("dA_log"), P("dD"), P("ddt_bias"), P("dinitial_state"), wp, wb)
+    g["workspace"] = ws
+    return _results(stream, dev, g)
+
+
+# ------------------------------------------------------- linear recurrence --
+def _linrec_problem(x, r, i, A_log, z, r_bias, i_bias, initial_state, other_state, cu_seqlens, names,
+                    debug_stall):
+    """The C problem of a call, and the pointer of the other state."""
+    try:
+        ok = x.dim() == 3 and A_log.dim() == 1
+    except AttributeError:
+        _tensors(x=x, A_log=A_log)
+        raise
+    if not ok:
+        raise ValueError("x must be [B, T, D] and A_log [D]")
+    dev, ty, sh = x.device, x.dtype, x.shape
+    q = _lib.kda_linrec_problem()
+    q.batch, q.T, q.dim = sh
+    q.dtype = _row_dtype(x, "x")
+    d = q.dim
+    q.x, q.x_stride = _rows(x, "x", ty, dev, sh)
+    q.r, q.r_stride = _rows(r, "r", ty, dev, sh)
+    q.i, q.i_stride = _rows(i, "i", ty, dev, sh)
+    if z is not None:
+        q.z, q.z_stride = _rows(z, "z", ty, dev, sh)
+    q.A_log = _need(A_log, "A_log", _f32, dev, (d,))
+    q.r_bias = _opt(r_bias, "r_bias", _f32, dev, (d,))
+    q.i_bias = _opt(i_bias, "i_bias", _f32, dev, (d,))
+    q.cu_seqlens, q.N = _seqlens(cu_seqlens, dev, sh[0])
+    q.debug_stall = int(debug_stall)
+    one, sty = (initial_state, names[0]) if initial_state is not None else (other_state, names[1])
+    if one is not None:
+        if _tensor(one, sty).dtype not in STATE_DTYPES:
+            raise TypeError(f"{sty}: states must be float32 or bfloat16, got {one.dtype}")
+        q.state_dtype = STATE_DTYPES[one.dtype]
+    sty = None if one is None else one.dtype
+    q.initial_state = _opt(initial_state, names[0], sty, dev, (q.N, d))
+    return q, _opt(other_state, names[1], sty, dev, (q.N, d))
+
+
+def make_linrec_states(total_tokens, dim, device=None):
+    """Buffer for the states that kda_linrec_fwd(..., chunk_states=buf) saves and
+    kda_linrec_bwd(..., chunk_states=buf) starts from."""
+    return torch.empty(_size("kda_linrec_get_states_size", int(total_tokens), int(dim)),
+                       dtype=torch.uint8, device=device if device is not None else "cuda")
+
+
+def make_linrec_workspace(batch, T, dim, N=None, *, backward=False, have_states=False, device=None):
+    """Workspace for kda_linrec_fwd, or with `backward` for kda_linrec_bwd (have_states: it is
+    given chunk_states).  N: the number of packed sequences when cu_seqlens is used."""
+    q = _lib.kda_linrec_problem()
+    q.batch, q.T, q.dim, q.N = batch, T, dim, N or batch
+    if N is not None:
+        q.cu_seqlens = 8  # only whether there is one counts here
+    if backward:
+        n = _size("kda_linrec_bwd_get_workspace_size", ctypes.byref(q), int(have_states))
+    else:
+        n = _size("kda_linrec_get_workspace_size", ctypes.byref(q))
+    return torch.empty(n, dtype=torch.uint8, device=device if device is not None else "cuda")
+
+
+def kda_linrec_fwd(x, r, i, A_log, out, z=None, r_bias=None, i_bias=None, initial_state=None,
+                   final_state=None, cu_seqlens=None, workspace=None, *, chunk_states=None,
+                   stream=None, debug_stall=False) -> None:
+    """Enqueue the gated linear recurrence (include/kda_layer.h, kda_linrec_fwd):
+    L = exp(A_log) sigmoid(r + r_bias), a = exp(-L),
+    h = a h + sqrt(1 - a^2) sigmoid(i + i_bias) x, out = h silu(z).
+
+    x, r, i, z: rows [B, T, D] bf16 or fp32; out [B, T, D] in x's dtype, written; A_log,
+    r_bias, i_bias fp32 [D]; z and the biases may be None.  initial_state / final_state:
+    [N, D], both fp32 or both bf16; they may be one buffer.  cu_seqlens as in kda_fwd, its
+    check reported in `workspace` (make_linrec_workspace; allocated here when None).
+    chunk_states: make_linrec_states's buffer, written for kda_linrec_bwd."""
+    q, fp = _linrec_problem(x, r, i, A_log, z, r_bias, i_bias, initial_state, final_state, cu_seqlens,
+                            ("initial_state", "final_state"), debug_stall)
+    dev = x.device
+    op = _need(out, "out", x.dtype, dev, x.shape)
+    cp, cb = _states_arg(chunk_states, dev, stream, "make_linrec_states")
+    wp = wb = 0
+    if workspace is not None or not 0 < q.T <= 8 or q.cu_seqlens or cp:
+        with _pool(stream, dev):
+            _, wp, wb = _workspace(workspace, lambda: _size("kda_linrec_get_workspace_size", ctypes.byref(q)),
+                                   dev, stream)
+    _call("kda_linrec_fwd", dev, stream, ctypes.byref(q), op, fp, cp, cb, wp, wb)
+
+
+def kda_linrec_bwd(x, r, i, A_log, dout, z=None, r_bias=None, i_bias=None, initial_state=None,
+                   dfinal_state=None, cu_seqlens=None, workspace=None, *, chunk_states=None,
+                   stream=None, debug_stall=False):
+    """Enqueue the backward of kda_linrec_fwd (include/kda_layer.h, kda_linrec_bwd) for the
+    forward call with the same inputs.  chunk_states: what that call saved; without it the
+    states are computed again.  dfinal_state: [N, D] in initial_state's dtype.  Returns a
+    dict: dx, dr, di (and dz) in x's dtype, dA_log (and dr_bias, di_bias, dinitial_state, each
+    where its input is given) in fp32, and the workspace."""
+    q, dfp = _linrec_problem(x, r, i, A_log, z, r_bias, i_bias, initial_state, dfinal_state, cu_seqlens,
+                             ("initial_state", "dfinal_state"), debug_stall)
+    dev, ty, d = x.device, x.dtype, q.dim
+    dop = _need(dout, "dout", ty, dev, x.shape)
+    cp, cb = _states_arg(chunk_states, dev, stream, "make_linrec_states")
+    E = lambda shape, t=_f32: torch.empty(shape, dtype=t, device=dev)
+    with _pool(stream, dev):
+        ws, wp, wb = _workspace(workspace, lambda: _size("kda_linrec_bwd_get_workspace_size",
+                                                         ctypes.byref(q), int(cp is not None)), dev, stream)
+        g = {"dx": E(x.shape, ty), "dr": E(x.shape, ty), "di": E(x.shape, ty), "dA_log": E((d,))}
+        if z is not None:
+            g["dz"] = E(x.shape, ty)
+        if r_bias is not None:
+            g["dr_bias"] = E((d,))
+        if i_bias is not None:
+            g["di_bias"] = E((d,))
+        if initial_state is not None:
+            g["dinitial_state"] = E(initial_state.shape)
+    P = lambda nm: g[nm].data_ptr() if nm in g else None
+    _call("kda_linrec_bwd", dev, stream, ctypes.byref(q), dop, dfp, cp, cb, P("dx"), P("dr"), P("di"),
+          P("dz"), P("dA_log"), P("dr_bias"), P("di_bias"), P("dinitial_state"), wp, wb)
     g["workspace"] = ws
     return _results(stream, dev, g)
 
