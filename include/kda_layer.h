@@ -39,8 +39,9 @@ extern "C" {
 /* Storage type of activation rows. */
 typedef enum { KDA_ROW_BF16 = 0, KDA_ROW_FP32 = 1 } kda_row_dtype;
 
-/* Elementwise function: of the convolution (NONE, SILU) and of a norm's gate. */
-typedef enum { KDA_FN_NONE = 0, KDA_FN_SILU = 1, KDA_FN_SIGMOID = 2 } kda_fn;
+/* Elementwise function: of the convolution (NONE, SILU), of a norm's gate (SILU, SIGMOID)
+ * and of the gated feed-forward product (SILU, SIGMOID, GELU). */
+typedef enum { KDA_FN_NONE = 0, KDA_FN_SILU = 1, KDA_FN_SIGMOID = 2, KDA_FN_GELU = 3 } kda_fn;
 
 #define KDA_CONV_MAX_WIDTH 4
 #define KDA_CONV_MAX_OUTS 4
@@ -228,6 +229,46 @@ KDA_API kda_status kda_linrec_bwd(const kda_linrec_problem* p, const void* dout,
                                   float* dA_log, float* dr_bias, float* di_bias,
                                   float* dinitial_state, void* workspace, size_t workspace_bytes,
                                   cudaStream_t stream);
+
+/* ------------------------------------------- gated feed-forward product --
+ * Both projections of a gated feed-forward block, the activation and the product:
+ *     g = x w_gate^T,   u = x w_up^T,   out = fn(g) u
+ * KDA_FN_GELU is the tanh form, g sigmoid(sqrt(8 / pi) (g + 0.044715 g^3)).  Everything is
+ * bf16, sums are fp32; dim, hidden and x_stride are multiples of 8 and every buffer is
+ * 16-byte aligned (the products read through tensor maps).  The block's output projection,
+ * like those before the recurrence, is a plain matrix product and the caller's.
+ */
+typedef struct {
+  const void* x;              /* rows [rows, dim]                                    */
+  const void* w_gate;         /* [hidden, dim]; both may be parts of one matrix      */
+  const void* w_up;           /* [hidden, dim]                                       */
+  int64_t x_stride;           /* >= dim                                              */
+  int64_t rows;               /* < 2^31                                              */
+  int32_t dim, hidden;
+  int32_t fn;                 /* KDA_FN_SILU, KDA_FN_SIGMOID or KDA_FN_GELU          */
+  int32_t dtype;              /* KDA_ROW_BF16                                        */
+  int32_t debug_stall;        /* 0; 1 (a test's hook): nothing is loaded, the waits  */
+                              /* run out and the status word reads                   */
+                              /* KDA_ERR_DEVICE_TIMEOUT                              */
+  int32_t reserved;           /* 0                                                   */
+} kda_glu_problem;
+
+/* kda_glu_fwd -- out [rows, hidden], written, and (unless NULL) pre [rows, 2 hidden], g then
+ * u of each row, rounded to bf16: kda_glu_bwd then computes them from there and not again.
+ * workspace: NULL, or KDA_STATUS_BYTES (128-byte aligned) whose first word receives the
+ * status; after KDA_ERR_DEVICE_TIMEOUT what the call wrote is not to be used. */
+KDA_API kda_status kda_glu_fwd(const kda_glu_problem* p, void* out, void* pre, void* workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace of kda_glu_bwd (status word, and the gradients of g and u in bf16). */
+KDA_API kda_status kda_glu_bwd_get_workspace_size(int64_t rows, int32_t hidden, size_t* bytes);
+
+/* kda_glu_bwd -- the gradients of <dout, out>: dx [rows, dim], dw_gate and dw_up
+ * [hidden, dim].  pre: NULL (g and u are computed again, in fp32), or what the forward kept;
+ * that saves a third of the products and adds the error of their rounding. */
+KDA_API kda_status kda_glu_bwd(const kda_glu_problem* p, const void* dout, const void* pre, void* dx,
+                               void* dw_gate, void* dw_up, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
 
 /* ------------------------------------------------------------------ norms --
  * unit(h) = h / sqrt(mean(h^2) + eps) over the last axis of dim values.

@@ -20,7 +20,8 @@ __all__ = ["KdaError", "kda_fwd", "kda_bwd", "kda_fwd_transition", "kda_compose_
 _LAYER = ("kda_conv_fwd", "kda_conv_bwd", "make_conv_bwd_workspace", "kda_scan_fwd", "kda_scan_bwd",
           "make_scan_states", "make_scan_workspace", "kda_prenorm_fwd", "kda_prenorm_bwd",
           "kda_postnorm_fwd", "kda_postnorm_bwd", "make_norm_bwd_workspace",
-          "kda_linrec_fwd", "kda_linrec_bwd", "make_linrec_states", "make_linrec_workspace")
+          "kda_linrec_fwd", "kda_linrec_bwd", "make_linrec_states", "make_linrec_workspace",
+          "kda_glu_fwd", "kda_glu_bwd", "make_glu_bwd_workspace")
 __all__ += list(_LAYER)
 
 

@@ -19,7 +19,8 @@ EXPORTS = ("kda_status_string", "kda_get_workspace_size", "kda_fwd", "kda_get_de
            "kda_prenorm_fwd", "kda_prenorm_bwd", "kda_postnorm_fwd", "kda_postnorm_bwd",
            "kda_norm_bwd_get_workspace_size",
            "kda_linrec_fwd", "kda_linrec_bwd", "kda_linrec_get_states_size",
-           "kda_linrec_get_workspace_size", "kda_linrec_bwd_get_workspace_size")
+           "kda_linrec_get_workspace_size", "kda_linrec_bwd_get_workspace_size",
+           "kda_glu_fwd", "kda_glu_bwd", "kda_glu_bwd_get_workspace_size")
 
 _lib = None
 
@@ -49,6 +50,13 @@ class kda_linrec_problem(ctypes.Structure):
                                                 "cu_seqlens")] +
                 [("batch", ctypes.c_int64), ("T", ctypes.c_int64)] +
                 [(n, ctypes.c_int32) for n in ("N", "dim", "dtype", "state_dtype", "debug_stall",
+                                               "reserved")])
+
+
+class kda_glu_problem(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "w_gate", "w_up")] +
+                [(n, ctypes.c_int64) for n in ("x_stride", "rows")] +
+                [(n, ctypes.c_int32) for n in ("dim", "hidden", "fn", "dtype", "debug_stall",
                                                "reserved")])
 
 
@@ -92,6 +100,7 @@ def load():
     S, Z = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
     Q = ctypes.POINTER(kda_scan_problem)
     L = ctypes.POINTER(kda_linrec_problem)
+    U = ctypes.POINTER(kda_glu_problem)
     for name, args in (
             ("kda_conv_fwd", [P, I64, P, P, P, P, I32, P, P, P, I64, I64, I32, I32, I32, I32, I32, P,
                               S, P]),
@@ -108,6 +117,9 @@ def load():
             ("kda_linrec_bwd_get_workspace_size", [L, I32, Z]),
             ("kda_linrec_fwd", [L, P, P, P, S, P, S, P]),
             ("kda_linrec_bwd", [L, P, P, P, S] + [P] * 9 + [S, P]),
+            ("kda_glu_fwd", [U, P, P, P, S, P]),
+            ("kda_glu_bwd_get_workspace_size", [I64, I32, Z]),
+            ("kda_glu_bwd", [U, P, P, P, P, P, P, S, P]),
             ("kda_prenorm_fwd", [P, P, P, P, F, F, P, P, I64, I32, I32, I32, P]),
             ("kda_norm_bwd_get_workspace_size", [I64, I32, Z]),
             ("kda_prenorm_bwd", [P, P, P, P, P, P, F, F, P, P, P, P, I64, I32, I32, I32, P, S, P]),

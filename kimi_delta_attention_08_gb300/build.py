@@ -18,7 +18,7 @@ ROOT = os.path.dirname(HERE)
 
 SOURCES = ["kda_api.cu", "kda_chunk_fwd.cu", "kda_plan.cu", "kda_noalloc.cu", "kda_recurrent.cu",
            "kda_bwd.cu", "kda_bwd_chunk.cu", "kda_norm.cu", "kda_conv.cu", "kda_scan_fwd.cu",
-           "kda_scan_bwd.cu", "kda_linrec.cu"]
+           "kda_scan_bwd.cu", "kda_linrec.cu", "kda_glu.cu"]
 HEADERS = ["kda_internal.h", "kda_ptx.cuh", "kda_inverse.cuh", "kda_rows.cuh", "kda_scan.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler",

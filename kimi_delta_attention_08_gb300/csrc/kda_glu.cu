@@ -1,0 +1,446 @@
+// kda_glu.cu -- the gated feed-forward product, forward and backward.
+//
+//   g = x Wg^T,  u = x Wu^T,  out = f(g) u                      (x: M x D, W: F x D)
+//   dg = dout u f'(g),  du = dout f(g),
+//   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
+//
+// Four products on the tensor cores, one kernel.  A pair of CTAs computes 256 x 256 values in
+// tensor memory, 128 rows each, as tcgen05.mma.cta_group::2 with M = N = 256: per 64
+// values of the summed axis a CTA loads 16 KB of each operand by TMA where a CTA alone
+// would load 48 KB, and reads half of B from its peer.  Forward, the 256 columns are 128 of
+// the gate and the same 128 of the other projection, so both meet in one thread of the
+// epilogue, and neither g nor u goes to memory; the recomputing backward multiplies dout in
+// there.  dx sums over both projections in one accumulator.  Operands whose summed axis is
+// not contiguous (W in dx, all of dW) are read as they lie, as MN-major tiles: nothing is
+// transposed.  Two accumulators alternate, so the epilogue of a tile runs under the next
+// one's products.
+//
+// Accumulation is fp32.  dg and du are rounded to bf16 between the two steps of the backward,
+// since the tensor cores take bf16: their error, half a step of bf16 each and independent
+// over the summed axis, adds as much to dx and dW as the outputs' own rounding.
+#include <cstring>
+
+#include "kda_internal.h"
+#include "kda_rows.cuh"
+#include "../../include/kda_layer.h"
+
+namespace kda {
+namespace {
+
+using namespace rows;
+
+constexpr int kTileM = 256, kTileN = 256, kTileK = 64, kStages = 6;
+constexpr int kHalf = 128;                       // rows of A, columns of B in each CTA
+constexpr uint32_t kOperand = kHalf * kTileK * 2;  // bytes of each in a stage
+constexpr uint32_t kSmem = kStages * 2 * kOperand + 1024 + 256;
+constexpr uint64_t kWaitNs = 500000000ull;
+constexpr int kEpilogueWarp = 4;                 // warps 4 .. 7
+
+// What a launch computes.
+enum GluPass : int { kForward = 0, kRecompute = 1, kInput = 2, kWeights = 3 };
+
+struct GluParams {
+  CUtensorMap a[2], b[2];  // of the gate and the other projection, or one for both
+  int64_t M, N;            // of the output (columns: of one projection)
+  int32_t k_blocks;        // of each of `sums` products that one tile adds up
+  int32_t m_tiles, n_tiles;
+  int32_t fn, stall;
+  bf16 *o0, *o1;
+  const bf16* dout;
+  unsigned* status;
+};
+
+constexpr float kGelu = 1.5957691216057308f, kGeluCube = 0.044715f;  // sqrt(8 / pi)
+
+// f(g) and f'(g).  gelu is its tanh form, g sigmoid(sqrt(8 / pi) (g + 0.044715 g^3)).
+__device__ __forceinline__ float act_of(float g, int fn) {
+  if (fn == KDA_FN_GELU) return g * sigmoid<bf16>(kGelu * g * fmaf(kGeluCube * g, g, 1.f));
+  const float s = sigmoid<bf16>(g);
+  return fn == KDA_FN_SILU ? g * s : s;
+}
+__device__ __forceinline__ float act_of(float g, int fn, float& slope) {
+  if (fn == KDA_FN_GELU) {
+    const float c = kGeluCube * g * g;
+    float t;
+    const float s = sigmoid<bf16>(kGelu * g * (1.f + c), t);
+    slope = fmaf(g * t, kGelu * fmaf(3.f, c, 1.f), s);
+    return g * s;
+  }
+  float t;
+  const float s = sigmoid<bf16>(g, t);
+  slope = fn == KDA_FN_SILU ? fmaf(g, t, s) : t;
+  return fn == KDA_FN_SILU ? g * s : s;
+}
+
+// A tile of the walk: groups of eight tiles down, so that the pairs at work share operands.
+__device__ __forceinline__ void tile_of(const GluParams& p, int t, int& m, int& n) {
+  constexpr int kDown = 8;
+  const int per = kDown * p.n_tiles, g = t / per, r = t % per;
+  const int down = min(kDown, p.m_tiles - g * kDown);
+  m = g * kDown + r % down, n = r / down;
+}
+
+__device__ __forceinline__ void store8(bf16* p, const float* f) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+}
+
+template <int PASS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
+    glu_kernel(const __grid_constant__ GluParams p) {
+  constexpr bool A_MN = PASS == kWeights, B_MN = PASS == kInput || PASS == kWeights;
+  constexpr bool DUAL = PASS == kForward || PASS == kRecompute;
+  constexpr int SUMS = PASS == kInput ? 2 : 1;
+  extern __shared__ uint8_t raw[];
+  uint8_t* const tiles = ptx::smem_align1024(raw);
+  __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2];
+  __shared__ uint32_t tmem_at;
+  __shared__ int failed;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = ptx::cluster_rank();
+  const int total = p.m_tiles * p.n_tiles, first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int blocks = SUMS * p.k_blocks;
+  if (threadIdx.x == 0) {
+    failed = 0;
+    for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[s], 1), ptx::mbar_init(&empty[s], 1);
+    for (int b = 0; b < 2; ++b) ptx::mbar_init(&tfull[b], 1), ptx::mbar_init(&tempty[b], 8);
+    ptx::fence_mbar_init();
+  }
+  if (warp == 2) ptx::tmem_alloc_pair(&tmem_at, 512);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_at;
+
+  if (warp == 0 && lane == 0) {
+    // loads: this CTA's half of both operands
+    uint32_t stage = 0, parity = 1;
+    bool ok = !p.stall;
+    for (int t = first; t < total && ok; t += step) {
+      int m, n;
+      tile_of(p, t, m, n);
+      for (int kb = 0; kb < blocks && ok; ++kb) {
+        ok = ptx::mbar_wait(&empty[stage], parity, kWaitNs);
+        if (!ok) break;
+        if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 4 * kOperand);
+        const uint32_t bar = ptx::cluster_addr(&full[stage], 0);
+        uint8_t* const A = tiles + stage * 2 * kOperand;
+        uint8_t* const B = A + kOperand;
+        const int part = SUMS == 2 && kb >= p.k_blocks, k0 = (kb - part * p.k_blocks) * kTileK;
+        if constexpr (A_MN) {
+          // tiles of the gate's gradient first, then of the other's
+          const int half = p.m_tiles / 2, which = m >= half;
+          const int at = (m - which * half) * kTileM + rank * kHalf;
+          ptx::tma_load_2d_pair(A, &p.a[which], bar, at, k0);
+          ptx::tma_load_2d_pair(A + kOperand / 2, &p.a[which], bar, at + 64, k0);
+        } else {
+          ptx::tma_load_2d_pair(A, &p.a[part], bar, k0, m * kTileM + (int)rank * kHalf);
+        }
+        if constexpr (B_MN) {
+          const int at = n * kTileN + rank * kHalf;
+          ptx::tma_load_2d_pair(B, &p.b[part], bar, at, k0);
+          ptx::tma_load_2d_pair(B + kOperand / 2, &p.b[part], bar, at + 64, k0);
+        } else {
+          ptx::tma_load_2d_pair(B, &p.b[rank], bar, k0, n * kHalf);
+        }
+        if (++stage == kStages) stage = 0, parity ^= 1;
+      }
+    }
+    // every stage is read before the pair may go
+    for (int s = 0; s < kStages && ok; ++s) {
+      ok = ptx::mbar_wait(&empty[stage], parity, kWaitNs);
+      if (++stage == kStages) stage = 0, parity ^= 1;
+    }
+    if (!ok) failed = 1;
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // products of the pair
+    constexpr uint32_t idesc = ptx::idesc_bf16_f32(kTileM, kTileN, A_MN, B_MN);
+    constexpr uint32_t a_step = A_MN ? 16 * 128 : 32, b_step = B_MN ? 16 * 128 : 32;
+    uint32_t stage = 0, parity = 0, buf = 0, tparity = 1;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step) {
+      ok = ptx::mbar_wait(&tempty[buf], tparity, kWaitNs);
+      ptx::tc_fence_after();
+      for (int kb = 0; kb < blocks && ok; ++kb) {
+        ok = ptx::mbar_wait(&full[stage], parity, kWaitNs);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t A = ptx::smem_u32(tiles + stage * 2 * kOperand), B = A + kOperand;
+#pragma unroll
+        for (int k = 0; k < kTileK / 16; ++k)
+          ptx::mma_bf16_ss_pair(tmem + buf * kTileN, ptx::sw128_desc(A + k * a_step, kOperand / 2, 1024),
+                                ptx::sw128_desc(B + k * b_step, kOperand / 2, 1024), idesc, kb + k > 0);
+        ptx::mma_commit_pair(&empty[stage]);
+        if (++stage == kStages) stage = 0, parity ^= 1;
+      }
+      if (!ok) break;
+      ptx::mma_commit_pair(&tfull[buf]);
+      buf ^= 1;
+      if (buf == 0) tparity ^= 1;
+    }
+    if (!ok) failed = 1;
+  } else if (warp >= kEpilogueWarp) {
+    const int w = warp - kEpilogueWarp;
+    const uint64_t limit = kWaitNs + (uint64_t)blocks * 2000;  // a whole tile's sum may be long
+    uint32_t buf = 0, parity = 0;
+    bool ok = true;
+    for (int t = first; t < total; t += step) {
+      int m, n;
+      tile_of(p, t, m, n);
+      ok = __all_sync(0xffffffffu, ptx::mbar_wait(&tfull[buf], parity, limit));
+      if (!ok) break;
+      ptx::tc_fence_after();
+      int64_t row;
+      bf16* o0 = p.o0;
+      if constexpr (PASS == kWeights) {
+        const int half = p.m_tiles / 2, which = m >= half;
+        row = (int64_t)(m - which * half) * kTileM;
+        o0 = which ? p.o1 : p.o0;
+      } else {
+        row = (int64_t)m * kTileM;
+      }
+      row += rank * kHalf + w * 32 + lane;
+      const bool in = row < p.M;
+      const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(w * 32) << 16);
+#pragma unroll 1
+      for (int c = 0; c < (DUAL ? kHalf : kTileN); c += 32) {
+        uint32_t v[32];
+        ptx::tmem_ld32(acc + c, v);
+        const int64_t col = (int64_t)n * (DUAL ? kHalf : kTileN) + c;
+        const int64_t at = row * p.N + col;
+        if constexpr (DUAL) {
+          uint32_t q[32];
+          ptx::tmem_ld32(acc + kHalf + c, q);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            if (!in || col + j >= p.N) continue;
+            float y[8], h[8];
+            if constexpr (PASS == kForward) {
+              float g[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                g[k] = __uint_as_float(v[j + k]), h[k] = __uint_as_float(q[j + k]);
+                y[k] = act_of(g[k], p.fn) * h[k];
+              }
+              store8(p.o0 + at + j, y);
+              if (p.o1) {
+                store8(p.o1 + row * 2 * p.N + col + j, g);
+                store8(p.o1 + row * 2 * p.N + p.N + col + j, h);
+              }
+            } else {
+              const uint4 d = __ldg(reinterpret_cast<const uint4*>(p.dout + at + j));
+              const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float dy = k & 1 ? hi_bf16(dw[k / 2]) : lo_bf16(dw[k / 2]);
+                float slope;
+                h[k] = dy * act_of(__uint_as_float(v[j + k]), p.fn, slope);
+                y[k] = dy * __uint_as_float(q[j + k]) * slope;
+              }
+              store8(p.o0 + at + j, y);
+              store8(p.o1 + at + j, h);
+            }
+          }
+        } else {
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; j += 8)
+            if (in && col + j < p.N) store8(o0 + at + j, reinterpret_cast<const float*>(v) + j);
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(ptx::cluster_addr(&tempty[buf], 0));
+      buf ^= 1;
+      if (buf == 0) parity ^= 1;
+    }
+    if (!ok && lane == 0) failed = 1;
+  }
+  __syncwarp();
+  __syncthreads();
+  if (failed) {  // a wait ran out: what is in flight comes to rest before anything is freed
+    if (threadIdx.x == 0 && p.status) atomicOr(p.status, kDevStatusTimeout);
+    const uint64_t t0 = ptx::global_timer_ns();
+    while (ptx::global_timer_ns() - t0 < 2000000) {
+    }
+  }
+  ptx::tc_fence_before();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  if (warp == 2) ptx::tmem_dealloc_pair(tmem, 512);
+}
+
+// dg and du from kept pre-activations, eight values a thread.
+__global__ void __launch_bounds__(256) glu_slope_kernel(const bf16* pre, const bf16* dout, bf16* dg, bf16* du,
+                                                        int64_t M, int64_t F, int fn) {
+  const int64_t per = F / 8, n = M * per;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
+    const int64_t row = e / per, col = e % per * 8;
+    Raw<bf16, 8> rg, ru, rd;
+    load_words(rg.w, pre + row * 2 * F + col);
+    load_words(ru.w, pre + row * 2 * F + F + col);
+    load_words(rd.w, dout + row * F + col);
+    float g[8], u[8], d[8];
+    unpack(rg, g), unpack(ru, u), unpack(rd, d);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float slope;
+      const float f = act_of(g[k], fn, slope);
+      g[k] = d[k] * u[k] * slope, u[k] = d[k] * f;
+    }
+    store8(dg + row * F + col, g);
+    store8(du + row * F + col, u);
+  }
+}
+
+// ------------------------------------------------------------------- host --
+bool al_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// A map of bf16 [rows, cols] with boxes of 64 columns by `box` rows, 128-byte swizzled.
+cudaError_t map_of(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t stride, uint32_t box) {
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)stride * 2};
+  const uint32_t b[2] = {64, box};
+  return encode_tiled_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, b,
+                          CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int PASS>
+cudaError_t launch(GluParams& p, cudaStream_t stream) {
+  static bool done[64];
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(glu_kernel<PASS>), kSmem, done);
+  if (e != cudaSuccess) return e;
+  int sms = 0;
+  if (sm_count(&sms) != KDA_OK) return cudaErrorUnknown;
+  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles, pairs = tiles < sms / 2 ? tiles : sms / 2;
+  glu_kernel<PASS><<<(unsigned)(2 * pairs), 256, kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+kda_status check_glu(const kda_glu_problem* q) {
+  if (!q) return KDA_ERR_NULL_POINTER;
+  const int64_t lim = int64_t(1) << 31;
+  if (q->rows < 0 || q->rows >= lim || q->dim < 8 || q->hidden < 8 || q->dim % 8 || q->hidden % 8 ||
+      q->x_stride < q->dim || q->x_stride >= lim || q->x_stride % 8)
+    return KDA_ERR_INVALID_SHAPE;
+  if (up(q->rows, kTileM) * up(q->hidden, kHalf) >= lim || 2 * up(q->hidden, kTileM) * up(q->dim, kTileN) >= lim)
+    return KDA_ERR_INVALID_SHAPE;
+  if (q->dtype != KDA_ROW_BF16 || (q->fn != KDA_FN_SILU && q->fn != KDA_FN_SIGMOID && q->fn != KDA_FN_GELU))
+    return KDA_ERR_INVALID_ARG;
+  if (!q->w_gate || !q->w_up || (q->rows > 0 && !q->x)) return KDA_ERR_NULL_POINTER;
+  if (!al_to(q->x, 16) || !al_to(q->w_gate, 16) || !al_to(q->w_up, 16)) return KDA_ERR_MISALIGNED;
+  return KDA_OK;
+}
+
+// The forward's tiles (also of the recomputing backward).
+template <int PASS>
+cudaError_t launch_dual(const kda_glu_problem* q, bf16* o0, bf16* o1, const void* dout, unsigned* status,
+                        cudaStream_t stream) {
+  GluParams p = {};
+  cudaError_t e = map_of(&p.a[0], q->x, q->rows, q->dim, q->x_stride, kHalf);
+  if (e == cudaSuccess) e = map_of(&p.b[0], q->w_gate, q->hidden, q->dim, q->dim, kHalf);
+  if (e == cudaSuccess) e = map_of(&p.b[1], q->w_up, q->hidden, q->dim, q->dim, kHalf);
+  if (e != cudaSuccess) return e;
+  p.a[1] = p.a[0];
+  p.M = q->rows, p.N = q->hidden;
+  p.k_blocks = (int32_t)up(q->dim, kTileK);
+  p.m_tiles = (int32_t)up(q->rows, kTileM), p.n_tiles = (int32_t)up(q->hidden, kHalf);
+  p.fn = q->fn, p.stall = q->debug_stall, p.status = status;
+  p.o0 = o0, p.o1 = o1, p.dout = static_cast<const bf16*>(dout);
+  return launch<PASS>(p, stream);
+}
+
+}  // namespace
+}  // namespace kda
+
+extern "C" {
+
+kda_status kda_glu_fwd(const kda_glu_problem* problem, void* out, void* pre, void* workspace,
+                       size_t workspace_bytes, cudaStream_t stream) {
+  using namespace kda;
+  kda_status st = check_glu(problem);
+  if (st != KDA_OK) return st;
+  if (problem->rows > 0 && !out) return KDA_ERR_NULL_POINTER;
+  if (!al_to(out, 16) || !al_to(pre, 16) || !al_to(workspace, 128)) return KDA_ERR_MISALIGNED;
+  if (workspace && workspace_bytes < KDA_STATUS_BYTES) return KDA_ERR_WORKSPACE_TOO_SMALL;
+  st = check_device();
+  if (st != KDA_OK) return st;
+  unsigned* const status = static_cast<unsigned*>(workspace);
+  if (status && cudaMemsetAsync(status, 0, 4, stream) != cudaSuccess) return KDA_ERR_CUDA;
+  if (problem->rows == 0) return KDA_OK;
+  return launch_dual<kForward>(problem, static_cast<bf16*>(out), static_cast<bf16*>(pre), nullptr, status,
+                               stream) == cudaSuccess
+             ? KDA_OK
+             : KDA_ERR_CUDA;
+}
+
+kda_status kda_glu_bwd_get_workspace_size(int64_t rows, int32_t hidden, size_t* bytes) {
+  if (!bytes) return KDA_ERR_NULL_POINTER;
+  if (rows < 0 || rows >= (int64_t(1) << 31) || hidden < 8 || hidden % 8) return KDA_ERR_INVALID_SHAPE;
+  *bytes = KDA_STATUS_BYTES + 2 * kda::up256((size_t)rows * hidden * 2);
+  return KDA_OK;
+}
+
+kda_status kda_glu_bwd(const kda_glu_problem* problem, const void* dout, const void* pre, void* dx,
+                       void* dw_gate, void* dw_up, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream) {
+  using namespace kda;
+  kda_status st = check_glu(problem);
+  if (st != KDA_OK) return st;
+  const kda_glu_problem& q = *problem;
+  if (!dw_gate || !dw_up || !workspace || (q.rows > 0 && (!dout || !dx))) return KDA_ERR_NULL_POINTER;
+  for (const void* v : {dout, pre, (const void*)dx, (const void*)dw_gate, (const void*)dw_up})
+    if (!al_to(v, 16)) return KDA_ERR_MISALIGNED;
+  if (!al_to(workspace, 128)) return KDA_ERR_MISALIGNED;
+  size_t need = 0;
+  st = kda_glu_bwd_get_workspace_size(q.rows, q.hidden, &need);
+  if (st != KDA_OK) return st;
+  if (workspace_bytes < need) return KDA_ERR_WORKSPACE_TOO_SMALL;
+  st = check_device();
+  if (st != KDA_OK) return st;
+  unsigned* const status = static_cast<unsigned*>(workspace);
+  const int64_t M = q.rows, D = q.dim, F = q.hidden;
+  cudaError_t e = cudaMemsetAsync(status, 0, 4, stream);
+  if (M == 0) {  // sums of nothing
+    if (e == cudaSuccess) e = cudaMemsetAsync(dw_gate, 0, (size_t)F * D * 2, stream);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dw_up, 0, (size_t)F * D * 2, stream);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+  }
+  bf16* const dg = reinterpret_cast<bf16*>(static_cast<uint8_t*>(workspace) + KDA_STATUS_BYTES);
+  bf16* const du = dg + up256((size_t)M * F * 2) / 2;
+  if (e == cudaSuccess) {
+    if (pre) {
+      const int64_t blocks = up(M * (F / 8), 256);
+      glu_slope_kernel<<<(unsigned)(blocks < 152 * 32 ? blocks : 152 * 32), 256, 0, stream>>>(
+          static_cast<const bf16*>(pre), static_cast<const bf16*>(dout), dg, du, M, F, q.fn);
+      e = cudaGetLastError();
+    } else {
+      e = launch_dual<kRecompute>(problem, dg, du, dout, status, stream);
+    }
+  }
+  GluParams p = {};
+  p.stall = q.debug_stall, p.status = status;
+  // dx: both projections' products in one sum
+  if (e == cudaSuccess) e = map_of(&p.a[0], dg, M, F, F, kHalf);
+  if (e == cudaSuccess) e = map_of(&p.a[1], du, M, F, F, kHalf);
+  if (e == cudaSuccess) e = map_of(&p.b[0], q.w_gate, F, D, D, kTileK);
+  if (e == cudaSuccess) e = map_of(&p.b[1], q.w_up, F, D, D, kTileK);
+  p.M = M, p.N = D, p.k_blocks = (int32_t)up(F, kTileK);
+  p.m_tiles = (int32_t)up(M, kTileM), p.n_tiles = (int32_t)up(D, kTileN);
+  p.o0 = static_cast<bf16*>(dx);
+  if (e == cudaSuccess) e = launch<kInput>(p, stream);
+  // the weights' gradients: the gate's rows, then the other's
+  if (e == cudaSuccess) e = map_of(&p.a[0], dg, M, F, F, kTileK);
+  if (e == cudaSuccess) e = map_of(&p.a[1], du, M, F, F, kTileK);
+  if (e == cudaSuccess) e = map_of(&p.b[0], q.x, M, D, q.x_stride, kTileK);
+  p.M = F, p.N = D, p.k_blocks = (int32_t)up(M, kTileK);
+  p.m_tiles = (int32_t)(2 * up(F, kTileM)), p.n_tiles = (int32_t)up(D, kTileN);
+  p.o0 = static_cast<bf16*>(dw_gate), p.o1 = static_cast<bf16*>(dw_up);
+  if (e == cudaSuccess) e = launch<kWeights>(p, stream);
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

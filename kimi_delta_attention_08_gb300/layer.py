@@ -1,6 +1,6 @@
 """Binding of the operators around the KDA recurrence in a layer (include/kda_layer.h):
 the short causal convolution, the selective state space scan, the gated linear
-recurrence, and the norms before and after a block.
+recurrence, the norms before and after a block, and the gated feed-forward product.
 
 As in the rest of the binding, arguments are only checked and passed on: every
 tensor has to have the documented dtype, device and layout.  Row arguments marked
@@ -21,6 +21,7 @@ KDA_OK = 0
 ROW_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 CONV_ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
 GATE_ACTIVATIONS = {"silu": 1, "sigmoid": 2}
+GLU_ACTIVATIONS = {"silu": 1, "sigmoid": 2, "gelu": 3}
 _f32 = torch.float32
 
 
@@ -567,6 +568,77 @@ def kda_linrec_bwd(x, r, i, A_log, dout, z=None, r_bias=None, i_bias=None, initi
     P = lambda nm: g[nm].data_ptr() if nm in g else None
     _call("kda_linrec_bwd", dev, stream, ctypes.byref(q), dop, dfp, cp, cb, P("dx"), P("dr"), P("di"),
           P("dz"), P("dA_log"), P("dr_bias"), P("di_bias"), P("dinitial_state"), wp, wb)
+    g["workspace"] = ws
+    return _results(stream, dev, g)
+
+
+# ----------------------------------------------- gated feed-forward product --
+def _glu_problem(x, w_gate, w_up, activation, debug_stall):
+    """The C problem of a call, and the hidden width."""
+    try:
+        ok = x.dim() == 3 and w_gate.dim() == 2
+    except AttributeError:
+        _tensors(x=x, w_gate=w_gate)
+        raise
+    if not ok:
+        raise ValueError("x must be [B, T, D] and w_gate [F, D]")
+    if activation not in GLU_ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(GLU_ACTIVATIONS)}")
+    B, T, D = x.shape
+    F, dev = w_gate.shape[0], x.device
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"x: expected bfloat16, got {x.dtype} (no implicit conversion)")
+    q = _lib.kda_glu_problem()
+    q.x, q.x_stride = _rows(x, "x", x.dtype, dev, x.shape)
+    q.w_gate = _need(w_gate, "w_gate", x.dtype, dev, (F, D))
+    q.w_up = _need(w_up, "w_up", x.dtype, dev, (F, D))
+    q.rows, q.dim, q.hidden = B * T, D, F
+    q.fn, q.dtype, q.debug_stall = GLU_ACTIVATIONS[activation], 0, int(debug_stall)
+    return q, F
+
+
+def kda_glu_fwd(x, w_gate, w_up, out, workspace=None, *, pre=None, activation="silu", stream=None,
+                debug_stall=False) -> None:
+    """Enqueue the gated feed-forward product (include/kda_layer.h, kda_glu_fwd):
+    out = activation(x w_gate^T) * (x w_up^T), one kernel.
+
+    x: rows [B, T, D] bf16, D and the rows' stride multiples of 8; w_gate, w_up: [F, D] bf16, F a
+    multiple of 8 (both may be parts of one matrix); out: [B, T, F] bf16, written; activation:
+    "silu", "sigmoid" or "gelu" (the tanh form).  pre: None, or [B, T, 2 F] bf16, which
+    receives both projections for kda_glu_bwd.  workspace: uint8, 256 bytes or more, whose
+    first word receives the status, or None."""
+    q, F = _glu_problem(x, w_gate, w_up, activation, debug_stall)
+    B, T, dev = x.shape[0], x.shape[1], x.device
+    op = _need(out, "out", x.dtype, dev, (B, T, F))
+    pp = _opt(pre, "pre", x.dtype, dev, (B, T, 2 * F))
+    wp, wb = (None, 0) if workspace is None else _workspace(workspace, None, dev, stream)[1:]
+    _call("kda_glu_fwd", dev, stream, ctypes.byref(q), op, pp, wp, wb)
+
+
+def make_glu_bwd_workspace(rows, hidden, device=None):
+    """Workspace for kda_glu_bwd over `rows` rows (B * T)."""
+    return torch.empty(_size("kda_glu_bwd_get_workspace_size", int(rows), int(hidden)), dtype=torch.uint8,
+                       device=device if device is not None else "cuda")
+
+
+def kda_glu_bwd(x, w_gate, w_up, dout, workspace=None, *, pre=None, activation="silu", stream=None,
+                debug_stall=False):
+    """Enqueue the backward of kda_glu_fwd (include/kda_layer.h, kda_glu_bwd).  dout: [B, T, F]
+    bf16.  pre: what the forward kept; without it both projections are computed again.
+    Returns a dict: dx [B, T, D], dw_gate, dw_up [F, D] in bf16, and the workspace."""
+    q, F = _glu_problem(x, w_gate, w_up, activation, debug_stall)
+    B, T, D = x.shape
+    dev, ty = x.device, x.dtype
+    dop = _need(dout, "dout", ty, dev, (B, T, F))
+    pp = _opt(pre, "pre", ty, dev, (B, T, 2 * F))
+    with _pool(stream, dev):
+        ws, wp, wb = _workspace(workspace, lambda: _size("kda_glu_bwd_get_workspace_size", B * T, F), dev,
+                                stream)
+        g = {"dx": torch.empty((B, T, D), dtype=ty, device=dev),
+             "dw_gate": torch.empty((F, D), dtype=ty, device=dev),
+             "dw_up": torch.empty((F, D), dtype=ty, device=dev)}
+    _call("kda_glu_bwd", dev, stream, ctypes.byref(q), dop, pp, g["dx"].data_ptr(), g["dw_gate"].data_ptr(),
+          g["dw_up"].data_ptr(), wp, wb)
     g["workspace"] = ws
     return _results(stream, dev, g)
 
