@@ -8,20 +8,20 @@
 //   e = g L (a^2 / m I x - a h_{t-1}),  dr = e (1 - R),  dA_log = sum of e.
 // L / m, not 1 / m, is what e needs: it goes to zero with L where 1 / m has no bound.
 //
-// Bound by HBM: each row is read once and written once.  A block takes a tile of rows by
-// channels; its warps take consecutive runs of rows, a lane one or two channels.  A run is
-// scanned in registers from zero (h) along with the product of its decays (P), runs are
-// joined in shared memory, tiles through the workspace: h_t = h + P_t X with X the state
-// before the tile.  So a prompt of any length fills the GPU in one pass over its rows.
+// Each row is read once and written once.  A block takes a tile of 64 rows by 32 to 128
+// channels; its warps take consecutive runs of rows, a lane one to four channels.  A run is
+// scanned in registers from zero along with the product of its decays, runs are joined in
+// shared memory by one thread per channel, tiles through the workspace; then each run is
+// walked again from the state before it.  So a prompt of any length fills the GPU in one
+// pass over its rows, and the bits are those of one walk over the tiles.
 //
-// X.  Each tile publishes what it does to a state, (product, end), as soon as it has it.
-// Every kGroup tiles one also publishes its end state itself.  A tile composes what the
-// tiles since then published, in their order, and that state: the same sums in every run.
-// A tile that holds the sequence's first row ends the look back.  Tiles are handed out by
-// an atomic counter in the order of their rows, so a tile only waits for tiles that
-// already run, and what is published is its own flag: words that were filled with ones
-// before (no arithmetic result has these bits).  Waits give up after half a second.
-#include <cstring>
+// Tiles.  Each publishes what it does to a state, (product, end from zero), as soon as it has
+// it, and its end state once it knows the one before it (at once where a sequence starts
+// within it).  Tiles are handed out by an atomic counter in the order of their rows, so a tile
+// only waits for tiles that already run, and what is published is its own flag: words that
+// were filled with ones before (no arithmetic result has these bits).  Waits give up after
+// half a second.
+#include <algorithm>
 
 #include "kda_internal.h"
 #include "kda_rows.cuh"
@@ -34,14 +34,11 @@ namespace {
 using namespace rows;
 
 constexpr int kWarps = 8;
-constexpr int kRowsF = 16, kRowsB = 8;            // rows per warp: forward, backward
-constexpr int kTileF = kWarps * kRowsF, kTileB = kWarps * kRowsB;
-constexpr int kGroup = 16;                        // tiles between two published end states
+constexpr int kRows = 8, kTile = kWarps * kRows;  // rows per warp and tile
 constexpr int kStepTokens = 8;                    // prompts up to this length: the step kernel
 constexpr uint64_t kWaitNs = 500000000ull;
 constexpr uint64_t kUnset = ~0ull;
-static_assert(kTileF % KDA_LINREC_CHUNK == 0 && kTileB == KDA_LINREC_CHUNK, "saved states");
-static_assert(kGroup == 2 * kWarps, "each warp looks at two tiles");
+static_assert(kTile == KDA_LINREC_CHUNK, "one saved state per tile");
 
 struct LinrecParams {
   const void *x, *r, *i, *z, *dout;
@@ -56,8 +53,8 @@ struct LinrecParams {
   void *out, *fin;
   float* states;             // [total / KDA_LINREC_CHUNK + 1][dim]
   unsigned *status, *ticket;
-  uint64_t* agg;             // [tiles][dim]: (product, end) of each tile
-  unsigned* ends;            // [tiles / kGroup][dim]: end states
+  uint64_t* agg;             // [tiles][dim]: (product, end from zero) of each tile
+  unsigned* ends;            // [tiles][dim]: the state after each tile
   void *dx, *dr, *di, *dz;
   float *part, *dinit;       // part: [tiles][3][dim]
 };
@@ -153,80 +150,28 @@ __device__ __forceinline__ void store_vals(void* p, int64_t at, const float (&f)
   store_row<T, V, (V > 1)>(static_cast<T*>(p) + at, f, 1, 1);
 }
 
-// The channel's rate (base 2, negative) and biases.
-template <int V>
-struct Channel {
-  float A2[V], rb[V], ib[V];
-};
-template <int V>
-__device__ __forceinline__ void load_channel(Channel<V>& c, const LinrecParams& p, int ch, bool ok) {
-#pragma unroll
-  for (int k = 0; k < V; ++k) {
-    c.A2[k] = ok ? scan::rate_of(__ldg(p.A_log + ch + k)) : 0.f;
-    c.rb[k] = ok && p.r_bias ? __ldg(p.r_bias + ch + k) : 0.f;
-    c.ib[k] = ok && p.i_bias ? __ldg(p.i_bias + ch + k) : 0.f;
-  }
-}
-
-// a = 2^L2 and m^2 = 1 - a^2 from L2 = -L log2 e <= 0.  The exponent is raised by the
-// hardware exponential's mean error (see the scan's decay).  Small steps, u = 2 L up to 1/2,
-// take 1 - exp(-u) = u P(u), P of degree 5 with P(0) = 1 fitted by reweighted least squares
-// to an even relative error (1.5e-9; 1e-7 as evaluated in fp32); 1 - a^2 would have none
-// of its digits right for them.  From there on 1 - a^2 is good to 4e-7.
-__device__ __forceinline__ float decay_of(float L2, float& m2) {
-  const float a = ptx::ex2_approx(L2 + 2.5e-8f);
-  const float u = L2 * (-2.f * kLn2);
-  float s = fmaf(-0.00112592906f, u, 0.00819330197f);
-  s = fmaf(s, u, -0.0416320525f);
-  s = fmaf(s, u, 0.166662887f);
-  s = fmaf(s, u, -0.499999851f);
-  s = fmaf(s, u, 1.0f);
-  m2 = u > 0.5f ? fmaf(-a, a, 1.0f) : u * s;
-  return a;
-}
-// Finite at zero; scaled, since the hardware takes what is below 2^-126 for zero.
-__device__ __forceinline__ float rsqrt_of(float m2) {
-  float r;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaxf(m2 * 0x1p64f, 1e-37f)));
-  return r * 0x1p32f;
-}
-
-// a and b = m I x of one value.
-template <typename T>
-__device__ __forceinline__ void step_of(float x, float r, float i, float A2, float& a, float& b) {
-  float m2;
-  a = decay_of(A2 * sigmoid<T>(r), m2);
-  b = m2 * rsqrt_of(m2) * sigmoid<T>(i) * x;
-}
-
 // What a warp knows about its rows: bit j for row j.
 struct RowBits {
   unsigned start, last, live;
 };
 
-// Rows of the tile: every row's sequence (shared), and for the look back the first row's
-// sequence start and the last row's end.
+// Rows of the tile: every row's sequence.
 struct TileRows {
-  int n[kTileF];
-  unsigned char flags[kTileF];   // 1: first row of its sequence, 2: last, 4: of a sequence
-  int64_t bos, eos;
+  int n[kTile];
+  unsigned char flags[kTile];    // 1: first row of its sequence, 2: last, 4: of a sequence
 };
-template <int TILE>
 __device__ __forceinline__ void find_rows(TileRows& s, const LinrecParams& p, int64_t row0) {
-  if (threadIdx.x < TILE) {
+  if (threadIdx.x < kTile) {
     const int64_t t = row0 + threadIdx.x;
     int n = 0;
     int64_t bos = 0, eos = 0;
     const bool live = row_sequence(p, t, n, bos, eos);
     s.n[threadIdx.x] = n;
     s.flags[threadIdx.x] = live ? 4 | (t == bos ? 1 : 0) | (t + 1 == eos ? 2 : 0) : 0;
-    if (threadIdx.x == 0) s.bos = bos;
-    if (threadIdx.x == TILE - 1) s.eos = eos;
   }
 }
-template <int R>
 __device__ __forceinline__ RowBits warp_rows(const TileRows& s, int warp, int lane) {
-  const unsigned f = lane < R ? s.flags[warp * R + lane] : 0u;
+  const unsigned f = lane < kRows ? s.flags[warp * kRows + lane] : 0u;
   RowBits b;
   b.start = __ballot_sync(0xffffffffu, f & 1);
   b.last = __ballot_sync(0xffffffffu, f & 2);
@@ -234,97 +179,195 @@ __device__ __forceinline__ RowBits warp_rows(const TileRows& s, int warp, int la
   return b;
 }
 
-// An affine step (product, end) of a lane's channels, joined along the rows.
+// What a value's gates and step need of its channel, in the form that Gates<T> takes.
 template <int V>
-struct Affine {
-  float P[V], H[V];
+struct Gates {
+  Vals<V> A2, cr, ci;
 };
-template <int V>
-__device__ __forceinline__ void unit_of(Affine<V>& e) {
+template <typename T, int V>
+__device__ __forceinline__ void load_gates(Gates<V>& c, const LinrecParams& p, int ch, bool ok) {
+  // bf16 rows: exp(-(v + bias)) = 2^(-v log2 e - bias log2 e)
+  constexpr float k = sizeof(T) < 4 ? -kLog2e : 1.f;
+  float A2[V], cr[V], ci[V];
 #pragma unroll
-  for (int k = 0; k < V; ++k) e.P[k] = 1.f, e.H[k] = 0.f;
-}
-// e <- e, then f; `cut`: f does not depend on what was before it.
-template <int V>
-__device__ __forceinline__ void then(Affine<V>& e, const Affine<V>& f, bool cut) {
-#pragma unroll
-  for (int k = 0; k < V; ++k) {
-    e.H[k] = cut ? f.H[k] : fmaf(f.P[k], e.H[k], f.H[k]);
-    e.P[k] = cut ? f.P[k] : e.P[k] * f.P[k];
+  for (int e = 0; e < V; ++e) {
+    A2[e] = ok ? scan::rate_of(__ldg(p.A_log + ch + e)) : 0.f;
+    cr[e] = ok && p.r_bias ? k * __ldg(p.r_bias + ch + e) : 0.f;
+    ci[e] = ok && p.i_bias ? k * __ldg(p.i_bias + ch + e) : 0.f;
   }
+  c.A2 = vals_from(A2), c.cr = vals_from(cr), c.ci = vals_from(ci);
 }
 
+// a and b = m I x of a pair of values.  m^2 and m come scaled by 2^24 and 2^12, so that what
+// the hardware takes for zero (below 2^-126) is zero in fp32 too, and I by 2^-12.  From
+// L2 = -L log2 e: small steps, u = 2 L up to 1/4, take 1 - exp(-u) = u P(u), P of degree 3 with
+// P(0) = 1 fitted by reweighted least squares to an even relative error (2.9e-7, half of
+// that in m); 1 - a^2 would have none of its digits right for them.  From there on 1 - a^2
+// is good to 8e-7.  The exponent is raised by the hardware exponential's mean error (see the
+// scan's decay).
+template <typename T>
+__device__ __forceinline__ pair gate_exp(pair v, pair c) {  // exp(-(v + bias))
+  if constexpr (sizeof(T) < 4) return pex2(pfma(v, pr(-kLog2e), c));
+  else return exp_minus<T>(padd(v, c));
+}
+__device__ __forceinline__ pair rcp_of(pair v) {
+  return pr(ptx::rcp_approx(un(v).x), ptx::rcp_approx(un(v).y));
+}
+__device__ __forceinline__ float sqrt_approx(float v) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+constexpr float kSmallStep = -0.18033688f;  // L2 at u = 1/4
+__device__ __forceinline__ pair scaled_m2(pair L2, pair a) {
+  pair q = pfma(pr(-2346124.25f), L2, pr(-7425258.5f));
+  q = pfma(q, L2, pr(-16120601.f));
+  q = pfma(q, L2, pr(-23258160.f));
+  const float2 small = un(pmul(q, L2)), big = un(pfma(pmul(a, pr(-0x1p24f)), a, pr(0x1p24f))), l = un(L2);
+  return pr(l.x < kSmallStep ? big.x : small.x, l.y < kSmallStep ? big.y : small.y);
+}
+template <typename T>
+__device__ __forceinline__ void step_of(pair x, pair r, pair i, pair A2, pair cr, pair ci, pair& a, pair& b) {
+  const pair L2 = pmul(A2, rcp_of(padd(gate_exp<T>(r, cr), pr(1.f))));
+  const pair I = rcp_of(pfma(gate_exp<T>(i, ci), pr(4096.f), pr(4096.f)));
+  a = pex2(padd(L2, pr(2.5e-8f)));
+  const pair m2 = scaled_m2(L2, a);
+  b = pmul(pmul(pr(sqrt_approx(un(m2).x), sqrt_approx(un(m2).y)), I), x);
+}
+template <typename T, int V>
+__device__ __forceinline__ void step_of(const Vals<V>& x, const Vals<V>& r, const Vals<V>& i, const Gates<V>& c,
+                                        Vals<V>& a, Vals<V>& b) {
+  if constexpr (V == 1) {
+    pair pa, pb;
+    step_of<T>(pr(x.v[0]), pr(r.v[0]), pr(i.v[0]), pr(c.A2.v[0]), pr(c.cr.v[0]), pr(c.ci.v[0]), pa, pb);
+    a.v[0] = un(pa).x, b.v[0] = un(pb).x;
+  } else {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k)
+      step_of<T>(x.v[k], r.v[k], i.v[k], c.A2.v[k], c.cr.v[k], c.ci.v[k], a.v[k], b.v[k]);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ Vals<V> vals_of(const Raw<T, V>& r) {
+  float f[V];
+  vals_of(r, f);
+  return vals_from(f);
+}
+template <typename T, int V>
+__device__ __forceinline__ Vals<V> silu_of(const Vals<V>& z) {
+  return mul_of(z, sigmoid<T>(z));
+}
+
+// The runs of a tile, joined by one thread per channel.
 template <int V>
-struct JoinShared {
-  Affine<V> run[kWarps][32];   // of the warps' runs
-  Affine<V> back[kWarps][32];  // of the tiles looked back at
-  int cut[kWarps];
+struct TileShared {
+  float P[kWarps][32 * V], H[kWarps][32 * V];  // what each run does to a state
+  float S[kWarps][32 * V];                     // the state before each run
+  int cut[kWarps];                             // whether a run holds a sequence's start
   unsigned next;
 };
-
-// What the tile does to a state, published by the warp that holds its last run.
 template <int V>
-__device__ __forceinline__ void publish(const LinrecParams& p, int64_t slot, int ch, const Affine<V>& e) {
+__device__ __forceinline__ void put(float (&at)[32 * V], int lane, const Vals<V>& v) {
+  float f[V];
+  vals_to(v, f);
 #pragma unroll
-  for (int k = 0; k < V; ++k)
-    st_word(p.agg + slot * p.dim + ch + k,
-            (uint64_t)published(e.P[k]) | ((uint64_t)published(e.H[k]) << 32));
+  for (int k = 0; k < V; ++k) at[lane * V + k] = f[k];
+}
+template <int V>
+__device__ __forceinline__ Vals<V> get(const float (&at)[32 * V], int lane) {
+  float f[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) f[k] = at[lane * V + k];
+  return vals_from(f);
 }
 
-// The warp's part of the look back from slot `s`: tiles first + 2 warp and the next one, of
-// first .. s - 1; `edge`: the slot whose tile starts the sequence (its step is cut off from
-// what was before), or below `first`.
-template <int V>
-__device__ __forceinline__ void look_back(const LinrecParams& p, int64_t s, int64_t first, int64_t edge,
-                                          int warp, int ch, bool ok, Affine<V>& e) {
-  unit_of(e);
-  const int64_t at = first + 2 * warp;
-  uint64_t w[2][V];
+// The state before tile s: the end state of the nearest tile that has published one, taken
+// through what the tiles since then do to it, one after the other.  Every end state is
+// published as the same chain of products, so the result does not depend on which is found.
+constexpr int kWindow = 8;
+__device__ __forceinline__ float state_before(const LinrecParams& p, int64_t s, int ch) {
+  const unsigned* const ends = p.ends + ch;
+  unsigned v = ld_word(ends + (s - 1) * p.dim);
+  if (v != ~0u) return __uint_as_float(v);
+  const uint64_t* const agg = p.agg + ch;
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (int turn = 1;; ++turn) {
+    unsigned e[kWindow];
+    uint64_t w[kWindow];
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-      w[q][k] = ok && at + q < s ? ld_word(p.agg + (at + q) * p.dim + ch + k) : 0;
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    if (at + q >= s) break;
-    Affine<V> f;
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      if (w[q][k] == kUnset) w[q][k] = await_word(p.agg + (at + q) * p.dim + ch + k, p.status);
-      f.P[k] = __uint_as_float((unsigned)w[q][k]);
-      f.H[k] = __uint_as_float((unsigned)(w[q][k] >> 32));
+    for (int q = 0; q < kWindow; ++q) {
+      const int64_t at = s - 1 - q;
+      e[q] = at >= 0 ? ld_word(ends + at * p.dim) : ~0u;
+      w[q] = at >= 0 ? ld_word(agg + at * p.dim) : kUnset;
     }
-    then(e, f, at + q == edge);
+    int found = -1;
+#pragma unroll
+    for (int q = kWindow - 1; q >= 0; --q) {
+      if (e[q] != ~0u) found = q;       // the nearest one counts
+    }
+    bool whole = found >= 0;
+    float X = 0.f;
+#pragma unroll
+    for (int q = kWindow - 1; q >= 0; --q) {
+      if (q == found) X = __uint_as_float(e[q]);
+      if (q < found) {
+        whole = whole && w[q] != kUnset;
+        X = fmaf(__uint_as_float((unsigned)w[q]), X, __uint_as_float((unsigned)(w[q] >> 32)));
+      }
+    }
+    if (whole) return X;
+    if (turn % 16 == 0) {
+      const uint64_t now = ptx::global_timer_ns();
+      if (!t0) t0 = now;
+      if (now - t0 > kWaitNs || (ld_word(p.status) & kDevStatusTimeout)) {
+        atomicOr(p.status, kDevStatusTimeout);
+        return 0.f;
+      }
+    }
   }
 }
 
-// The state before the tile in slot s of the walking order (X), once the warps' parts are
-// in shared memory.
-template <int V>
-__device__ __forceinline__ void carried(float (&X)[V], const LinrecParams& p, const JoinShared<V>& sh,
-                                        int64_t s, int64_t first, int64_t edge, int lane, int ch, bool ok) {
-  const bool from_end = edge < first;
+// One channel of a tile: its runs joined, published, and the state before each.
+// FORWARD: runs in the order of their rows.  `carry`: the tile's first row goes on.
+template <int V, bool FORWARD>
+__device__ __forceinline__ float join_runs(const LinrecParams& p, TileShared<V>& sh, int64_t s, int c, int ch,
+                                           bool carry) {
+  float P = 1.f, H = 0.f;
+  bool any = false;
 #pragma unroll
-  for (int k = 0; k < V; ++k)
-    X[k] = from_end && ok
-               ? __uint_as_float(await_word(p.ends + (first / kGroup - 1) * p.dim + ch + k, p.status))
-               : 0.f;
-  const int parts = (int)((s - first + 1) / 2);
-  for (int w = 0; w < parts; ++w) {
-    const Affine<V> f = sh.back[w][lane];
-    const bool cut = edge >= first + 2 * w && edge < first + 2 * w + 2;
-#pragma unroll
-    for (int k = 0; k < V; ++k) X[k] = cut ? f.H[k] : fmaf(f.P[k], X[k], f.H[k]);
+  for (int q = 0; q < kWarps; ++q) {
+    const int w = FORWARD ? q : kWarps - 1 - q;
+    const bool cut = sh.cut[w];
+    const float Pw = sh.P[w][c], Hw = sh.H[w][c];
+    H = cut ? Hw : fmaf(Pw, H, Hw);
+    P *= Pw;
+    any |= cut;
   }
+  const bool quiet = p.stall && s == 0;
+  if (any) {
+    if (!quiet) st_word(p.ends + s * p.dim + ch, published(H));
+  } else if (carry && !quiet) {
+    st_word(p.agg + s * p.dim + ch, (uint64_t)published(P) | ((uint64_t)published(H) << 32));
+  }
+  const float X = carry ? state_before(p, s, ch) : 0.f;
+  if (!any && !quiet) st_word(p.ends + s * p.dim + ch, published(carry ? fmaf(P, X, H) : H));
+  float S = X;
+#pragma unroll
+  for (int q = 0; q < kWarps; ++q) {
+    const int w = FORWARD ? q : kWarps - 1 - q;
+    sh.S[w][c] = S;
+    S = sh.cut[w] ? sh.H[w][c] : fmaf(sh.P[w][c], S, sh.H[w][c]);
+  }
+  return X;
 }
 
 // ---------------------------------------------------------------- forward --
 template <typename T, int V, bool OUT>
 __global__ void __launch_bounds__(32 * kWarps, 2) linrec_fwd_kernel(LinrecParams p) {
-  constexpr int R = kRowsF;
+  constexpr int R = kRows;
   __shared__ TileRows rows_s;
-  __shared__ JoinShared<V> sh;
+  __shared__ __align__(16) TileShared<V> sh;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t units = p.tiles * p.blocks;
   if (threadIdx.x == 0) sh.next = atomicAdd(p.ticket, 1u);
@@ -332,9 +375,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_fwd_kernel(LinrecParams
   int64_t unit = sh.next;
   while (unit < units) {
     const int64_t s = unit / p.blocks;
-    const int ch = (int)(unit % p.blocks) * 32 * V + lane * V;
+    const int c0 = (int)(unit % p.blocks) * 32 * V, ch = c0 + lane * V;
     const bool ok = ch < p.dim;
-    const int64_t row0 = s * kTileF + warp * R;
+    const int64_t row0 = s * kTile + warp * R;
     unsigned next = 0;
     if (threadIdx.x == 0) next = atomicAdd(p.ticket, 1u);
     Raw<T, V> rx[R], rr[R], ri[R];
@@ -348,20 +391,15 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_fwd_kernel(LinrecParams
         load_vals<T, V>(ri[j], p.i, (row0 + j) * p.i_s + ch);
       }
     }
-    Channel<V> c;
-    load_channel(c, p, ch, ok);
-    find_rows<kTileF>(rows_s, p, s * kTileF);
+    Gates<V> c;
+    load_gates<T>(c, p, ch, ok);
+    find_rows(rows_s, p, s * kTile);
     __syncthreads();
-    const RowBits bits = warp_rows<R>(rows_s, warp, lane);
-    float a[R][V], b[R][V];
+    const RowBits bits = warp_rows(rows_s, warp, lane);
+    Vals<V> a[R], b[R];
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      float x[V], r[V], i[V];
-      vals_of(rx[j], x), vals_of(rr[j], r), vals_of(ri[j], i);
-#pragma unroll
-      for (int k = 0; k < V; ++k) step_of<T>(x[k], r[k] + c.rb[k], i[k] + c.ib[k], c.A2[k], a[j][k], b[j][k]);
-    }
-    if (bits.start && p.init) {
+    for (int j = 0; j < R; ++j) step_of<T>(vals_of(rx[j]), vals_of(rr[j]), vals_of(ri[j]), c, a[j], b[j]);
+    if (bits.start && p.init) {  // a sequence's first step starts from its initial state
       float h0[R][V];
 #pragma unroll
       for (int j = 0; j < R; ++j)
@@ -369,84 +407,49 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_fwd_kernel(LinrecParams
           load_state<V>(h0[j], p.init, (int64_t)rows_s.n[warp * R + j] * p.dim + ch, p.state_bf16);
 #pragma unroll
       for (int j = 0; j < R; ++j)
-        if (ok && (bits.start >> j & 1)) {
-#pragma unroll
-          for (int k = 0; k < V; ++k) b[j][k] = fmaf(a[j][k], h0[j][k], b[j][k]);
-        }
+        if (ok && (bits.start >> j & 1)) b[j] = fma_of(a[j], vals_from(h0[j]), b[j]);
     }
-    // the run from zero: a <- the product of decays, b <- h
+    // what the run does to a state
+    Vals<V> P = a[0], h = b[0];
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
+    for (int j = 1; j < R; ++j) {
       const bool cut = bits.start >> j & 1;
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        if (j == 0) {
-          a[0][k] = cut ? 0.f : a[0][k];
-        } else {
-          b[j][k] = cut ? b[j][k] : fmaf(a[j][k], b[j - 1][k], b[j][k]);
-          a[j][k] = cut ? 0.f : a[j][k] * a[j - 1][k];
-        }
-      }
+      h = cut ? b[j] : fma_of(a[j], h, b[j]);
+      P = mul_of(P, a[j]);
     }
-    Affine<V> own;
-#pragma unroll
-    for (int k = 0; k < V; ++k) own.P[k] = a[R - 1][k], own.H[k] = b[R - 1][k];
-    sh.run[warp][lane] = own;
+    put<V>(sh.P[warp], lane, P);
+    put<V>(sh.H[warp], lane, h);
     if (lane == 0) sh.cut[warp] = bits.start != 0;
-    __syncthreads();
-    Affine<V> ex;
-    unit_of(ex);
-    bool cut_before = false;
-    for (int w = 0; w < warp; ++w) {
-      then(ex, sh.run[w][lane], sh.cut[w]);
-      cut_before |= sh.cut[w] != 0;
-    }
-    if (warp == kWarps - 1 && ok && !(p.stall && s == 0)) {
-      Affine<V> all = ex;
-      then(all, own, bits.start != 0);
-      publish(p, s, ch, all);
-    }
-    // the state before the tile
-    float X[V] = {};
-    const unsigned char f0 = rows_s.flags[0];
-    if ((f0 & 4) && !(f0 & 1) && s > 0) {
-      const int64_t group = s / kGroup * kGroup, edge = rows_s.bos / kTileF;
-      const int64_t first = edge > group ? edge : group;
-      look_back(p, s, first, edge, warp, ch, ok, sh.back[warp][lane]);
-      __syncthreads();
-      carried(X, p, sh, s, first, edge, lane, ch, ok);
-    }
-#pragma unroll
-    for (int k = 0; k < V; ++k) X[k] = cut_before ? ex.H[k] : fmaf(ex.P[k], X[k], ex.H[k]);
-    if (p.states && ok && row0 % KDA_LINREC_CHUNK == 0 && row0 < p.total) {
-#pragma unroll
-      for (int k = 0; k < V; ++k) p.states[row0 / KDA_LINREC_CHUNK * p.dim + ch + k] = X[k];
-    }
-    const int open = bits.start ? __ffs(bits.start) - 1 : R;  // rows that X reaches
-    if (warp == kWarps - 1 && ok && s % kGroup == kGroup - 1) {
-#pragma unroll
-      for (int k = 0; k < V; ++k)
-        st_word(p.ends + s / kGroup * p.dim + ch + k,
-                published(open < R ? own.H[k] : fmaf(own.P[k], X[k], own.H[k])));
-    }
+    Raw<T, V> rz[R];
     if constexpr (OUT) {
 #pragma unroll
       for (int j = 0; j < R; ++j) {
+        rz[j] = {};
+        if (p.z && ok && row0 + j < p.total) load_vals<T, V>(rz[j], p.z, (row0 + j) * p.z_s + ch);
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < 32 * V && c0 + (int)threadIdx.x < p.dim) {
+      const unsigned char f0 = rows_s.flags[0];
+      const float X = join_runs<V, true>(p, sh, s, threadIdx.x, c0 + threadIdx.x, (f0 & 4) && !(f0 & 1) && s > 0);
+      if (p.states) p.states[s * p.dim + c0 + threadIdx.x] = X;
+    }
+    if constexpr (OUT) {
+      __syncthreads();
+      h = get<V>(sh.S[warp], lane);
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const bool cut = bits.start >> j & 1;
+        h = cut ? b[j] : fma_of(a[j], h, b[j]);
         if (!ok || !(bits.live >> j & 1)) continue;
-        float h[V], y[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) y[k] = h[k] = j < open ? fmaf(a[j][k], X[k], b[j][k]) : b[j][k];
-        if (p.z) {
-          Raw<T, V> rz;
-          float z[V];
-          load_vals<T, V>(rz, p.z, (row0 + j) * p.z_s + ch);
-          vals_of(rz, z);
-#pragma unroll
-          for (int k = 0; k < V; ++k) y[k] = h[k] * z[k] * sigmoid<T>(z[k]);
-        }
+        float y[V];
+        if (p.z) vals_to(mul_of(h, silu_of<T>(vals_of(rz[j]))), y);
+        else vals_to(h, y);
         store_vals<T, V>(p.out, (row0 + j) * p.dim + ch, y);
-        if (p.fin && (bits.last >> j & 1))
-          store_state<V>(p.fin, (int64_t)rows_s.n[warp * R + j] * p.dim + ch, h, p.state_bf16);
+        if (p.fin && (bits.last >> j & 1)) {
+          vals_to(h, y);
+          store_state<V>(p.fin, (int64_t)rows_s.n[warp * R + j] * p.dim + ch, y, p.state_bf16);
+        }
       }
     }
     if (threadIdx.x == 0) sh.next = next;
@@ -463,39 +466,88 @@ __global__ void __launch_bounds__(256) linrec_step_kernel(LinrecParams p) {
   const int64_t n = at / per;
   const int ch = (int)(at % per) * V;
   if (n >= p.N) return;
-  float h[V] = {};
-  if (p.init) load_state<V>(h, p.init, n * p.dim + ch, p.state_bf16);
-  Channel<V> c;
-  load_channel(c, p, ch, true);
+  float h0[V] = {};
+  if (p.init) load_state<V>(h0, p.init, n * p.dim + ch, p.state_bf16);
+  Gates<V> c;
+  load_gates<T>(c, p, ch, true);
+  Vals<V> h = vals_from(h0);
   for (int64_t t = n * p.T; t < (n + 1) * p.T; ++t) {
     Raw<T, V> rx, rr, ri, rz = {};
     load_vals<T, V>(rx, p.x, t * p.x_s + ch);
     load_vals<T, V>(rr, p.r, t * p.r_s + ch);
     load_vals<T, V>(ri, p.i, t * p.i_s + ch);
     if (p.z) load_vals<T, V>(rz, p.z, t * p.z_s + ch);
-    float x[V], r[V], i[V], z[V], y[V];
-    vals_of(rx, x), vals_of(rr, r), vals_of(ri, i), vals_of(rz, z);
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      float a, b;
-      step_of<T>(x[k], r[k] + c.rb[k], i[k] + c.ib[k], c.A2[k], a, b);
-      h[k] = fmaf(a, h[k], b);
-      y[k] = p.z ? h[k] * z[k] * sigmoid<T>(z[k]) : h[k];
-    }
-    store_vals<T, V>(p.out, t * p.dim + ch, y);
+    Vals<V> a, b;
+    step_of<T>(vals_of(rx), vals_of(rr), vals_of(ri), c, a, b);
+    h = fma_of(a, h, b);
+    vals_to(p.z ? mul_of(h, silu_of<T>(vals_of(rz))) : h, h0);
+    store_vals<T, V>(p.out, t * p.dim + ch, h0);
   }
-  if (p.fin) store_state<V>(p.fin, n * p.dim + ch, h, p.state_bf16);
+  vals_to(h, h0);
+  if (p.fin) store_state<V>(p.fin, n * p.dim + ch, h0, p.state_bf16);
 }
 
 // --------------------------------------------------------------- backward --
+// The gradients of a pair of values: g of the state, a its decay, h the state before.  On
+// return g holds a g, what goes on to the row before.  Exponentials stop at 2^120, so that
+// 1 - sigmoid(v) = exp(-v) sigmoid(v) keeps its digits on both sides.
+__device__ __forceinline__ pair at_most(pair v, float top) {
+  return pr(fminf(un(v).x, top), fminf(un(v).y, top));
+}
+template <typename T>
+__device__ __forceinline__ void grads_of(pair x, pair r, pair i, pair A2, pair cr, pair ci, pair a, pair h,
+                                         pair& g, pair& e, pair& dx, pair& dr, pair& di) {
+  const pair er = at_most(gate_exp<T>(r, cr), 0x1p120f), ei = at_most(gate_exp<T>(i, ci), 0x1p108f);
+  const pair R = rcp_of(padd(er, pr(1.f)));
+  const pair I = rcp_of(pfma(ei, pr(4096.f), pr(4096.f)));  // by 2^-12, as m is by 2^12
+  const pair L2 = pmul(A2, R);
+  const float2 m2 = un(scaled_m2(L2, a));
+  float2 rs;                                                // 2^-12 / m, finite at zero
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(rs.x) : "f"(fmaxf(m2.x, 1e-37f)));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(rs.y) : "f"(fmaxf(m2.y, 1e-37f)));
+  const pair rsm = pr(rs.x, rs.y);
+  dx = pmul(pmul(g, pmul(pr(m2.x, m2.y), rsm)), I);
+  di = pmul(pmul(dx, x), pmul(pmul(ei, pr(4096.f)), I));
+  g = pmul(g, a);
+  // g L2 and L2 / m before what could leave the range for an infinite rate
+  const pair in = pmul(pmul(a, pmul(pmul(L2, rsm), I)), x);  // by 2^-24
+  e = pfma(pmul(g, in), pr(-kLn2 * 0x1p24f), pmul(pmul(pmul(g, L2), h), pr(kLn2)));
+  dr = pmul(e, pmul(er, R));
+}
+template <typename T, int V>
+__device__ __forceinline__ void grads_of(const Vals<V>& x, const Vals<V>& r, const Vals<V>& i, const Gates<V>& c,
+                                         const Vals<V>& a, const Vals<V>& h, Vals<V>& g, Vals<V>& e, Vals<V>& dx,
+                                         Vals<V>& dr, Vals<V>& di) {
+  if constexpr (V == 1) {
+    pair gg = pr(g.v[0]), pe, px, pq, pi;
+    grads_of<T>(pr(x.v[0]), pr(r.v[0]), pr(i.v[0]), pr(c.A2.v[0]), pr(c.cr.v[0]), pr(c.ci.v[0]), pr(a.v[0]),
+                pr(h.v[0]), gg, pe, px, pq, pi);
+    g.v[0] = un(gg).x, e.v[0] = un(pe).x, dx.v[0] = un(px).x, dr.v[0] = un(pq).x, di.v[0] = un(pi).x;
+  } else {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k)
+      grads_of<T>(x.v[k], r.v[k], i.v[k], c.A2.v[k], c.cr.v[k], c.ci.v[k], a.v[k], h.v[k], g.v[k], e.v[k], dx.v[k],
+                  dr.v[k], di.v[k]);
+  }
+}
+template <int V>
+__device__ __forceinline__ Vals<V> add_of(const Vals<V>& a, const Vals<V>& b) {
+  return fma_of(a, splat<V>(1.f), b);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_of(void* p, int64_t at, const Vals<V>& v) {
+  float f[V];
+  vals_to(v, f);
+  store_vals<T, V>(p, at, f);
+}
+
 template <typename T, int V>
 __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams p) {
-  constexpr int R = kRowsB;
+  constexpr int R = kRows, CH = 32 * V;
   __shared__ TileRows rows_s;
-  __shared__ JoinShared<V> sh;           // of the gradients, last run first
-  __shared__ Affine<V> fwd[kWarps][32];  // of the states
-  __shared__ int fwd_cut[kWarps];
-  __shared__ float sums[3][kWarps][32 * V];
+  __shared__ __align__(16) TileShared<V> sh, fw;  // of the gradients (last run first), of the states
+  __shared__ __align__(16) float sums[3][kWarps][CH];
+  static_assert(2 * CH <= 32 * kWarps, "a thread per channel for each of the two joins");
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t units = p.tiles * p.blocks;
   if (threadIdx.x == 0) sh.next = atomicAdd(p.ticket, 1u);
@@ -504,10 +556,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
   while (unit < units) {
     const int64_t s = unit / p.blocks;            // counted from the last tile back
     const int64_t tile = p.tiles - 1 - s;
-    const int cb = (int)(unit % p.blocks) * 32 * V;
-    const int ch = cb + lane * V;
+    const int c0 = (int)(unit % p.blocks) * CH, ch = c0 + lane * V;
     const bool ok = ch < p.dim;
-    const int64_t row0 = tile * kTileB + warp * R;
+    const int64_t row0 = tile * kTile + warp * R;
     unsigned next = 0;
     if (threadIdx.x == 0) next = atomicAdd(p.ticket, 1u);
     Raw<T, V> rx[R], rr[R], ri[R], rd[R], rz[R];
@@ -523,180 +574,119 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
         if (p.z) load_vals<T, V>(rz[j], p.z, (row0 + j) * p.z_s + ch);
       }
     }
-    Channel<V> c;
-    load_channel(c, p, ch, ok);
-    float X[V] = {};
-    if (ok) {
-#pragma unroll
-      for (int k = 0; k < V; ++k) X[k] = __ldg(p.states + tile * p.dim + ch + k);
-    }
-    find_rows<kTileB>(rows_s, p, tile * kTileB);
+    Gates<V> c;
+    load_gates<T>(c, p, ch, ok);
+    find_rows(rows_s, p, tile * kTile);
     __syncthreads();
-    const RowBits bits = warp_rows<R>(rows_s, warp, lane);
+    const RowBits bits = warp_rows(rows_s, warp, lane);
     if (bits.live != (1u << R) - 1) {  // rows of no sequence count for nothing
 #pragma unroll
       for (int j = 0; j < R; ++j)
         if (!(bits.live >> j & 1)) rx[j] = {}, rr[j] = {}, ri[j] = {}, rd[j] = {}, rz[j] = {};
     }
-    // what the run does to a state, and backwards to a gradient
-    float a[R][V], b[R][V], dy[R][V];
+    Vals<V> a[R], b[R], dy[R], dq[R];  // dq: dout silu'(z), what dz takes times h
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      float x[V], r[V], i[V], z[V];
-      vals_of(rx[j], x), vals_of(rr[j], r), vals_of(ri[j], i), vals_of(rd[j], dy[j]), vals_of(rz[j], z);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        step_of<T>(x[k], r[k] + c.rb[k], i[k] + c.ib[k], c.A2[k], a[j][k], b[j][k]);
-        if (p.z) dy[j][k] *= z[k] * sigmoid<T>(z[k]);
+      step_of<T>(vals_of(rx[j]), vals_of(rr[j]), vals_of(ri[j]), c, a[j], b[j]);
+      dy[j] = vals_of(rd[j]);
+      if (p.z) {
+        const Vals<V> z = vals_of(rz[j]), q = sigmoid<T>(z);
+        // silu' = q + z q (1 - q)
+        dq[j] = mul_of(dy[j], fma_of(mul_of(z, q), fma_of(q, splat<V>(-1.f), splat<V>(1.f)), q));
+        dy[j] = mul_of(dy[j], mul_of(z, q));
       }
     }
-    auto initial = [&](int j, float (&h0)[V]) {
-#pragma unroll
-      for (int k = 0; k < V; ++k) h0[k] = 0.f;
+    auto initial = [&](int j) {
+      float h0[V] = {};
       if (p.init && ok) load_state<V>(h0, p.init, (int64_t)rows_s.n[warp * R + j] * p.dim + ch, p.state_bf16);
+      return vals_from(h0);
     };
-    Affine<V> own;
-    unit_of(own);
+    // what the run does to a state
+    Vals<V> h = splat<V>(0.f), P = splat<V>(1.f);
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      if (bits.start >> j & 1) {
-        initial(j, own.H);
-#pragma unroll
-        for (int k = 0; k < V; ++k) own.P[k] = 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < V; ++k) own.H[k] = fmaf(a[j][k], own.H[k], b[j][k]), own.P[k] *= a[j][k];
+      if (bits.start >> j & 1) h = initial(j);
+      h = fma_of(a[j], h, b[j]);
+      P = mul_of(P, a[j]);
     }
-    fwd[warp][lane] = own;
+    put<V>(fw.P[warp], lane, P);
+    put<V>(fw.H[warp], lane, h);
     if (bits.last && p.dfin && ok) {  // the final state's gradient joins the last row's
 #pragma unroll
       for (int j = 0; j < R; ++j)
         if (bits.last >> j & 1) {
           float d[V];
           load_state<V>(d, p.dfin, (int64_t)rows_s.n[warp * R + j] * p.dim + ch, p.state_bf16);
-#pragma unroll
-          for (int k = 0; k < V; ++k) dy[j][k] += d[k];
+          dy[j] = add_of(dy[j], vals_from(d));
         }
     }
-    unit_of(own);
+    // and to a gradient
+    h = splat<V>(0.f);
 #pragma unroll
     for (int j = R - 1; j >= 0; --j) {
       const bool cut = bits.last >> j & 1;
+      h = mul_of(a[j], cut ? dy[j] : add_of(h, dy[j]));
+    }
+    put<V>(sh.P[warp], lane, P);
+    put<V>(sh.H[warp], lane, h);
+    if (lane == 0) sh.cut[warp] = bits.last != 0, fw.cut[warp] = bits.start != 0;
+    __syncthreads();
+    if (threadIdx.x < CH && c0 + (int)threadIdx.x < p.dim) {
+      const unsigned char f = rows_s.flags[kTile - 1];
+      join_runs<V, false>(p, sh, s, threadIdx.x, c0 + threadIdx.x, (f & 4) && !(f & 2) && s > 0);
+    } else if (threadIdx.x >= 128 && threadIdx.x < 128 + CH && c0 + (int)threadIdx.x - 128 < p.dim) {
+      const int k = threadIdx.x - 128;
+      float S = __ldg(p.states + tile * p.dim + c0 + k);
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        own.H[k] = a[j][k] * (cut ? dy[j][k] : dy[j][k] + own.H[k]);
-        own.P[k] = cut ? 0.f : a[j][k] * own.P[k];
+      for (int w = 0; w < kWarps; ++w) {
+        fw.S[w][k] = S;
+        S = fw.cut[w] ? fw.H[w][k] : fmaf(fw.P[w][k], S, fw.H[w][k]);
       }
     }
-    sh.run[warp][lane] = own;
-    if (lane == 0) sh.cut[warp] = bits.last != 0, fwd_cut[warp] = bits.start != 0;
     __syncthreads();
-    Affine<V> ex;
-    unit_of(ex);
-    bool cut_before = false;
-    for (int w = kWarps - 1; w > warp; --w) {
-      then(ex, sh.run[w][lane], sh.cut[w]);
-      cut_before |= sh.cut[w] != 0;
-    }
-    if (warp == 0 && ok && !(p.stall && s == 0)) {
-      Affine<V> all = ex;
-      then(all, own, bits.last != 0);
-      publish(p, s, ch, all);
-    }
-    for (int w = 0; w < warp; ++w) {
-      const Affine<V> f = fwd[w][lane];
-#pragma unroll
-      for (int k = 0; k < V; ++k) X[k] = fwd_cut[w] ? f.H[k] : fmaf(f.P[k], X[k], f.H[k]);
-    }
-    // the gradient that the rows after the tile hand on
-    float C[V] = {};
-    const unsigned char fl = rows_s.flags[kTileB - 1];
-    if ((fl & 4) && !(fl & 2) && s > 0) {
-      const int64_t group = s / kGroup * kGroup, edge = p.tiles - 1 - (rows_s.eos - 1) / kTileB;
-      const int64_t first = edge > group ? edge : group;
-      look_back(p, s, first, edge, warp, ch, ok, sh.back[warp][lane]);
-      __syncthreads();
-      carried(C, p, sh, s, first, edge, lane, ch, ok);
-    }
-#pragma unroll
-    for (int k = 0; k < V; ++k) C[k] = cut_before ? ex.H[k] : fmaf(ex.P[k], C[k], ex.H[k]);
-    if (warp == 0 && ok && s % kGroup == kGroup - 1) {
-#pragma unroll
-      for (int k = 0; k < V; ++k)
-        st_word(p.ends + s / kGroup * p.dim + ch + k,
-                published(bits.last ? own.H[k] : fmaf(own.P[k], C[k], own.H[k])));
-    }
     // states again, b <- the one before each row; dz
+    h = get<V>(fw.S[warp], lane);
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      if (bits.start >> j & 1) initial(j, X);
-      float h[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) h[k] = fmaf(a[j][k], X[k], b[j][k]), b[j][k] = X[k], X[k] = h[k];
-      if (p.z && ok && row0 + j < p.total) {
-        float z[V], d[V];
-        vals_of(rz[j], z), vals_of(rd[j], d);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const float q = sigmoid<T>(z[k]);
-          d[k] *= h[k] * fmaf(z[k] * q, 1.f - q, q);
-        }
-        if (!(bits.live >> j & 1)) {
-#pragma unroll
-          for (int k = 0; k < V; ++k) d[k] = 0.f;
-        }
-        store_vals<T, V>(p.dz, (row0 + j) * p.dim + ch, d);
-      }
+      if (bits.start >> j & 1) h = initial(j);
+      const Vals<V> before = h;
+      h = fma_of(a[j], h, b[j]);
+      b[j] = before;
+      if (p.z && ok && row0 + j < p.total)
+        store_of<T>(p.dz, (row0 + j) * p.dim + ch, bits.live >> j & 1 ? mul_of(dq[j], h) : splat<V>(0.f));
     }
-    float se[V] = {}, sr[V] = {}, si[V] = {};
+    Vals<V> C = get<V>(sh.S[warp], lane);
+    Vals<V> se = splat<V>(0.f), sr = se, si = se;
 #pragma unroll
     for (int j = R - 1; j >= 0; --j) {
-      const bool live = bits.live >> j & 1;
-      float x[V], r[V], i[V], dx[V], dr[V], di[V];
-      vals_of(rx[j], x), vals_of(rr[j], r), vals_of(ri[j], i);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float er = exp_minus<T>(r[k] + c.rb[k]), Rg = ptx::rcp_approx(1.f + er);
-        float di_slope;
-        const float I = sigmoid<T>(i[k] + c.ib[k], di_slope);
-        const float g = bits.last >> j & 1 ? dy[j][k] : dy[j][k] + C[k];
-        float m2;
-        const float L2 = c.A2[k] * Rg;
-        decay_of(L2, m2);
-        const float rs = rsqrt_of(m2), m = m2 * rs, L = -kLn2 * L2;
-        const float gm = g * m, av = a[j][k];
-        const float e = live ? g * (av * av * (L * rs) * (I * x[k]) - av * b[j][k] * L) : 0.f;
-        C[k] = av * g;
-        dx[k] = live ? gm * I : 0.f;
-        di[k] = live ? gm * x[k] * di_slope : 0.f;
-        dr[k] = e * (er < 1.f ? er * Rg : 1.f - Rg);
-        se[k] += e, sr[k] += dr[k], si[k] += di[k];
-      }
+      Vals<V> e, dx, dr, di;
+      C = bits.last >> j & 1 ? dy[j] : add_of(C, dy[j]);
+      grads_of<T>(vals_of(rx[j]), vals_of(rr[j]), vals_of(ri[j]), c, a[j], b[j], C, e, dx, dr, di);
+      if (!(bits.live >> j & 1)) e = dx = dr = di = splat<V>(0.f);
+      se = add_of(se, e), sr = add_of(sr, dr), si = add_of(si, di);
       if (ok && row0 + j < p.total) {
         const int64_t at = (row0 + j) * p.dim + ch;
-        store_vals<T, V>(p.dx, at, dx);
-        store_vals<T, V>(p.dr, at, dr);
-        store_vals<T, V>(p.di, at, di);
+        store_of<T>(p.dx, at, dx);
+        store_of<T>(p.dr, at, dr);
+        store_of<T>(p.di, at, di);
         if (p.dinit && (bits.start >> j & 1)) {
-#pragma unroll
-          for (int k = 0; k < V; ++k) p.dinit[(int64_t)rows_s.n[warp * R + j] * p.dim + ch + k] = C[k];
+          float f[V];
+          vals_to(C, f);
+          store_state<V>(p.dinit, (int64_t)rows_s.n[warp * R + j] * p.dim + ch, f, false);
         }
       }
     }
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      sums[0][warp][lane * V + k] = se[k];
-      sums[1][warp][lane * V + k] = sr[k];
-      sums[2][warp][lane * V + k] = si[k];
-    }
+    put<V>(sums[0][warp], lane, se);
+    put<V>(sums[1][warp], lane, sr);
+    put<V>(sums[2][warp], lane, si);
     if (threadIdx.x == 0) sh.next = next;
     __syncthreads();
-    for (int q = threadIdx.x; q < 3 * 32 * V; q += 32 * kWarps) {
-      const int w = q / (32 * V), l = q % (32 * V);
+    for (int q = threadIdx.x; q < 3 * CH; q += 32 * kWarps) {
+      const int w = q / CH, l = q % CH;
       float v = 0.f;
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) v += sums[w][k][l];
-      if (cb + l < p.dim) p.part[(tile * 3 + w) * p.dim + cb + l] = v;
+      if (c0 + l < p.dim) p.part[(tile * 3 + w) * p.dim + c0 + l] = v;
     }
     unit = sh.next;
     __syncthreads();
@@ -738,9 +728,9 @@ __global__ void __launch_bounds__(256) linrec_setup_kernel(SetupParams p) {
 // ------------------------------------------------------------------- host --
 bool al_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-int64_t tiles_of(int64_t total, int rows) { return (total + rows - 1) / rows; }
-size_t join_bytes(int64_t tiles, int32_t dim) {  // what tiles publish
-  return up256((size_t)tiles * dim * 8) + up256((size_t)(tiles / kGroup) * dim * 4);
+int64_t tiles_of(int64_t total) { return (total + kTile - 1) / kTile; }
+size_t join_bytes(int64_t total, int32_t dim) {  // what tiles publish
+  return up256((size_t)tiles_of(total) * dim * 8) + up256((size_t)tiles_of(total) * dim * 4);
 }
 
 kda_status check_sizes(const kda_linrec_problem* q, LinrecParams& p) {
@@ -754,8 +744,8 @@ kda_status check_sizes(const kda_linrec_problem* q, LinrecParams& p) {
   return KDA_OK;
 }
 
-// `pairs`: every row can be read two channels at a time.
-kda_status check_linrec(const kda_linrec_problem* q, LinrecParams& p, bool& pairs) {
+// `lanes`: the channels that a thread can read at a time, 1, 2 or 4, by the rows' alignment.
+kda_status check_linrec(const kda_linrec_problem* q, LinrecParams& p, int& lanes) {
   const kda_status sizes = check_sizes(q, p);
   if (sizes != KDA_OK) return sizes;
   if (!q->A_log) return KDA_ERR_NULL_POINTER;
@@ -768,10 +758,11 @@ kda_status check_linrec(const kda_linrec_problem* q, LinrecParams& p, bool& pair
     return KDA_ERR_INVALID_ARG;
   if (p.total > 0 && (!q->x || !q->r || !q->i)) return KDA_ERR_NULL_POINTER;
   const size_t e = q->dtype == KDA_ROW_FP32 ? 4 : 2, se = q->state_dtype == KDA_STATE_FP32 ? 4 : 2;
-  pairs = q->dtype == KDA_ROW_BF16 && q->dim % 2 == 0;
+  lanes = 4;
+  while (lanes > 1 && q->dim % lanes) lanes /= 2;
   for (int k = 0; k < 4; ++k) {
     if (!al_to(row[k], e)) return KDA_ERR_MISALIGNED;
-    pairs = pairs && al_to(row[k], 4) && stride[k] % 2 == 0;
+    while (lanes > 1 && (!al_to(row[k], lanes * e) || stride[k] % lanes)) lanes /= 2;
   }
   if (!al_to(q->A_log, 4) || !al_to(q->r_bias, 4) || !al_to(q->i_bias, 4) ||
       !al_to(q->initial_state, se) || !al_to(q->cu_seqlens, 8))
@@ -783,14 +774,17 @@ kda_status check_linrec(const kda_linrec_problem* q, LinrecParams& p, bool& pair
   p.stall = q->debug_stall;
   return KDA_OK;
 }
+void lanes_for(int& lanes, const void* p, size_t e) {  // contiguous rows
+  while (lanes > 1 && !al_to(p, lanes * e)) lanes /= 2;
+}
 
 // Tiles and channel blocks of a pass, and its part of the workspace.
-bool plan_pass(LinrecParams& p, int rows, int channels, uint8_t*& ws) {
-  p.tiles = tiles_of(p.total, rows);
-  p.blocks = (p.dim + channels - 1) / channels;
+bool plan_pass(LinrecParams& p, int lanes, uint8_t*& ws) {
+  p.tiles = tiles_of(p.total);
+  p.blocks = (p.dim + 32 * lanes - 1) / (32 * lanes);
   p.agg = reinterpret_cast<uint64_t*>(ws);
   p.ends = reinterpret_cast<unsigned*>(ws + up256((size_t)p.tiles * p.dim * 8));
-  ws += join_bytes(p.tiles, p.dim);
+  ws += join_bytes(p.total, p.dim);
   return p.tiles * p.blocks < (int64_t(1) << 31);
 }
 
@@ -813,18 +807,27 @@ cudaError_t launch_tiles(K kernel, const LinrecParams& p, cudaStream_t stream) {
   kernel<<<(unsigned)(units < most ? units : most), 32 * kWarps, 0, stream>>>(p);
   return cudaGetLastError();
 }
+// Channels per thread: 8 bytes of a row where its alignment allows, 4 in the backward, which
+// keeps more of each value in registers.
+constexpr int kFwd16 = 4, kFwd32 = 2, kBwd16 = 2, kBwd32 = 1;
+int lanes_of(int lanes, bool f32, bool bwd) {
+  return std::min(lanes, bwd ? (f32 ? kBwd32 : kBwd16) : f32 ? kFwd32 : kFwd16);
+}
 template <bool OUT>
-cudaError_t launch_fwd(const LinrecParams& p, bool f32, bool pairs, cudaStream_t stream) {
-  return f32     ? launch_tiles(linrec_fwd_kernel<float, 1, OUT>, p, stream)
-         : pairs ? launch_tiles(linrec_fwd_kernel<bf16, 2, OUT>, p, stream)
-                 : launch_tiles(linrec_fwd_kernel<bf16, 1, OUT>, p, stream);
+cudaError_t launch_fwd(const LinrecParams& p, bool f32, int lanes, cudaStream_t stream) {
+  if (f32)
+    return lanes == 2 ? launch_tiles(linrec_fwd_kernel<float, 2, OUT>, p, stream)
+                      : launch_tiles(linrec_fwd_kernel<float, 1, OUT>, p, stream);
+  return lanes == 4   ? launch_tiles(linrec_fwd_kernel<bf16, 4, OUT>, p, stream)
+         : lanes == 2 ? launch_tiles(linrec_fwd_kernel<bf16, 2, OUT>, p, stream)
+                      : launch_tiles(linrec_fwd_kernel<bf16, 1, OUT>, p, stream);
 }
 
 size_t states_bytes(int64_t total, int32_t dim) {
   return (size_t)(total / KDA_LINREC_CHUNK + 1) * dim * sizeof(float);
 }
 size_t fwd_bytes(const LinrecParams& p) {
-  return KDA_STATUS_BYTES + join_bytes(tiles_of(p.total, kTileF), p.dim);
+  return KDA_STATUS_BYTES + join_bytes(p.total, p.dim);
 }
 
 }  // namespace
@@ -855,10 +858,10 @@ kda_status kda_linrec_bwd_get_workspace_size(const kda_linrec_problem* problem, 
   LinrecParams p = {};
   const kda_status st = check_sizes(problem, p);
   if (st != KDA_OK) return st;
-  const int64_t tiles = tiles_of(p.total, kTileB);
-  *bytes = KDA_STATUS_BYTES + join_bytes(tiles, p.dim) + up256((size_t)tiles * 3 * p.dim * sizeof(float));
+  const int64_t tiles = tiles_of(p.total);
+  *bytes = KDA_STATUS_BYTES + join_bytes(p.total, p.dim) + up256((size_t)tiles * 3 * p.dim * sizeof(float));
   if (!have_states)
-    *bytes += join_bytes(tiles_of(p.total, kTileF), p.dim) + up256(states_bytes(p.total, p.dim));
+    *bytes += join_bytes(p.total, p.dim) + up256(states_bytes(p.total, p.dim));
   return KDA_OK;
 }
 
@@ -867,8 +870,8 @@ kda_status kda_linrec_fwd(const kda_linrec_problem* problem, void* out, void* fi
                           size_t workspace_bytes, cudaStream_t stream) {
   using namespace kda;
   LinrecParams p = {};
-  bool pairs = false;
-  kda_status st = check_linrec(problem, p, pairs);
+  int lanes = 1;
+  kda_status st = check_linrec(problem, p, lanes);
   if (st != KDA_OK) return st;
   const bool f32 = problem->dtype == KDA_ROW_FP32;
   if (p.total > 0 && !out) return KDA_ERR_NULL_POINTER;
@@ -882,24 +885,25 @@ kda_status kda_linrec_fwd(const kda_linrec_problem* problem, void* out, void* fi
     return KDA_ERR_WORKSPACE_TOO_SMALL;
   st = check_device();
   if (st != KDA_OK) return st;
-  pairs = pairs && al_to(out, 4);
+  lanes_for(lanes, out, f32 ? 4 : 2);
   p.out = out, p.fin = final_state, p.states = static_cast<float*>(chunk_states);
   p.status = static_cast<unsigned*>(workspace);
   if (step) {
     if (workspace && cudaMemsetAsync(workspace, 0, 4, stream) != cudaSuccess) return KDA_ERR_CUDA;
-    const int V = pairs ? 2 : 1;
+    const int V = std::min(lanes, f32 ? 1 : 2);
     const int64_t blocks = ((int64_t)p.N * ((p.dim + V - 1) / V) + 255) / 256;
     if (blocks >= (int64_t(1) << 31)) return KDA_ERR_INVALID_SHAPE;
-    auto kernel = f32 ? linrec_step_kernel<float, 1> : pairs ? linrec_step_kernel<bf16, 2> : linrec_step_kernel<bf16, 1>;
+    auto kernel = f32 ? linrec_step_kernel<float, 1> : V == 2 ? linrec_step_kernel<bf16, 2> : linrec_step_kernel<bf16, 1>;
     kernel<<<(unsigned)blocks, 256, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
   }
   uint8_t* ws = static_cast<uint8_t*>(workspace) + KDA_STATUS_BYTES;
-  if (!plan_pass(p, kTileF, pairs ? 64 : 32, ws)) return KDA_ERR_INVALID_SHAPE;
+  lanes = lanes_of(lanes, f32, false);
+  if (!plan_pass(p, lanes, ws)) return KDA_ERR_INVALID_SHAPE;
   p.ticket = p.status + 1;
   cudaError_t e = launch_setup(p, p.agg, fwd_bytes(p) - KDA_STATUS_BYTES, p.init, p.state_bf16,
                                p.fin == p.init ? nullptr : p.fin, p.state_bf16, stream);
-  if (e == cudaSuccess && p.total > 0) e = launch_fwd<true>(p, f32, pairs, stream);
+  if (e == cudaSuccess && p.total > 0) e = launch_fwd<true>(p, f32, lanes, stream);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -910,8 +914,8 @@ kda_status kda_linrec_bwd(const kda_linrec_problem* problem, const void* dout, c
                           cudaStream_t stream) {
   using namespace kda;
   LinrecParams p = {};
-  bool pairs = false;
-  kda_status st = check_linrec(problem, p, pairs);
+  int lanes = 1;
+  kda_status st = check_linrec(problem, p, lanes);
   if (st != KDA_OK) return st;
   const bool f32 = problem->dtype == KDA_ROW_FP32;
   const size_t e = f32 ? 4 : 2;
@@ -919,7 +923,7 @@ kda_status kda_linrec_bwd(const kda_linrec_problem* problem, const void* dout, c
     return KDA_ERR_NULL_POINTER;
   for (const void* q : {dout, (const void*)dx, (const void*)dr, (const void*)di, (const void*)dz}) {
     if (!al_to(q, e)) return KDA_ERR_MISALIGNED;
-    pairs = pairs && al_to(q, 4);
+    lanes_for(lanes, q, e);
   }
   if (!al_to(dA_log, 4) || !al_to(dr_bias, 4) || !al_to(di_bias, 4) || !al_to(dinitial_state, 4) ||
       !al_to(dfinal_state, p.state_bf16 ? 2 : 4) || !al_to(chunk_states, 16) || !al_to(workspace, 128))
@@ -936,9 +940,9 @@ kda_status kda_linrec_bwd(const kda_linrec_problem* problem, const void* dout, c
   uint8_t* const published_at = ws;
   LinrecParams f = p;
   f.stall = 0;
-  const int channels = pairs ? 64 : 32;
-  bool fits = plan_pass(p, kTileB, channels, ws);
-  if (!chunk_states) fits = fits && plan_pass(f, kTileF, channels, ws);
+  const int back = lanes_of(lanes, f32, true);
+  bool fits = plan_pass(p, back, ws);
+  if (!chunk_states) fits = fits && plan_pass(f, lanes_of(lanes, f32, false), ws);
   if (!fits) return KDA_ERR_INVALID_SHAPE;
   const size_t published_bytes = (size_t)(ws - published_at);
   p.part = reinterpret_cast<float*>(ws);
@@ -951,10 +955,10 @@ kda_status kda_linrec_bwd(const kda_linrec_problem* problem, const void* dout, c
   cudaError_t err = launch_setup(p, published_at, published_bytes, dfinal_state, p.state_bf16,
                                  dinitial_state, false, stream);
   if (err == cudaSuccess && p.total > 0) {
-    if (!chunk_states) err = launch_fwd<false>(f, f32, pairs, stream);
+    if (!chunk_states) err = launch_fwd<false>(f, f32, lanes_of(lanes, f32, false), stream);
     if (err == cudaSuccess)
       err = f32     ? launch_tiles(linrec_bwd_kernel<float, 1>, p, stream)
-            : pairs ? launch_tiles(linrec_bwd_kernel<bf16, 2>, p, stream)
+            : back == 2 ? launch_tiles(linrec_bwd_kernel<bf16, 2>, p, stream)
                     : launch_tiles(linrec_bwd_kernel<bf16, 1>, p, stream);
   }
   if (err == cudaSuccess)
