@@ -35,6 +35,7 @@ using namespace rows;
 
 constexpr int kWarps = 8;
 constexpr int kRows = 8, kTile = kWarps * kRows;  // rows per warp and tile
+constexpr int kGroup = 16;                        // tiles of a group
 constexpr int kStepTokens = 8;                    // prompts up to this length: the step kernel
 constexpr uint64_t kWaitNs = 500000000ull;
 constexpr uint64_t kUnset = ~0ull;
@@ -42,7 +43,8 @@ static_assert(kTile == KDA_LINREC_CHUNK, "one saved state per tile");
 
 struct LinrecParams {
   const void *x, *r, *i, *z, *dout;
-  int64_t x_s, r_s, i_s, z_s;
+  uint32_t x_s, r_s, i_s, z_s;
+  float* gates;              // [3][dim]: what load_gates computes
   const float *A_log, *r_bias, *i_bias;
   const void *init, *dfin;
   int32_t state_bf16, stall;
@@ -54,6 +56,7 @@ struct LinrecParams {
   float* states;             // [total / KDA_LINREC_CHUNK + 1][dim]
   unsigned *status, *ticket;
   uint64_t* agg;             // [tiles][dim]: (product, end from zero) of each tile
+  uint64_t* group_agg;       // [tiles / kGroup][dim]: the same of each whole group
   unsigned* ends;            // [tiles][dim]: the state after each tile
   void *dx, *dr, *di, *dz;
   float *part, *dinit;       // part: [tiles][3][dim]
@@ -74,25 +77,6 @@ __device__ __forceinline__ void st_word(uint64_t* p, uint64_t v) {
 }
 __device__ __forceinline__ void st_word(unsigned* p, unsigned v) {
   asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-
-// The word at p once it is set; after the limit (or another wait's) zero, with the status.
-template <typename W>
-__device__ __forceinline__ W await_word(const W* p, unsigned* status) {
-  W v = ld_word(p);
-  if (v != static_cast<W>(kUnset)) return v;
-  const uint64_t t0 = ptx::global_timer_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i) {
-      v = ld_word(p);
-      if (v != static_cast<W>(kUnset)) return v;
-    }
-    if (ptx::global_timer_ns() - t0 > kWaitNs || (ld_word(status) & kDevStatusTimeout)) {
-      atomicOr(status, kDevStatusTimeout);
-      return 0;
-    }
-  }
 }
 
 // Bits that are published: those of all ones mean "not set", so that NaN becomes another.
@@ -140,6 +124,17 @@ __device__ __forceinline__ void load_vals(Raw<T, V>& r, const void* p, int64_t a
   if constexpr (V == 1) r.w[0] = __float_as_uint(to_f(__ldg(static_cast<const T*>(p) + at)));
   else load_words(r.w, static_cast<const T*>(p) + at);
 }
+// A run's rows of an array from `p`, `stride` elements apart; with EDGE only the first n exist.
+template <bool EDGE, typename T, int V>
+__device__ __forceinline__ void load_run(Raw<T, V> (&r)[kRows], const void* p, int64_t row0, uint32_t stride, int ch,
+                                         int n) {
+  const char* const at = reinterpret_cast<const char*>(static_cast<const T*>(p) + row0 * stride + ch);
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    if constexpr (EDGE) r[j] = {};
+    if (!EDGE || j < n) load_vals<T, V>(r[j], at + (uint64_t)stride * (uint32_t)(j * sizeof(T)), 0);
+  }
+}
 template <typename T, int V>
 __device__ __forceinline__ void vals_of(const Raw<T, V>& r, float (&f)[V]) {
   if constexpr (V == 1) f[0] = __uint_as_float(r.w[0]);
@@ -159,6 +154,7 @@ struct RowBits {
 struct TileRows {
   int n[kTile];
   unsigned char flags[kTile];    // 1: first row of its sequence, 2: last, 4: of a sequence
+  int64_t bos, eos;              // of the first row's sequence, of the last row's
 };
 __device__ __forceinline__ void find_rows(TileRows& s, const LinrecParams& p, int64_t row0) {
   if (threadIdx.x < kTile) {
@@ -168,6 +164,8 @@ __device__ __forceinline__ void find_rows(TileRows& s, const LinrecParams& p, in
     const bool live = row_sequence(p, t, n, bos, eos);
     s.n[threadIdx.x] = n;
     s.flags[threadIdx.x] = live ? 4 | (t == bos ? 1 : 0) | (t + 1 == eos ? 2 : 0) : 0;
+    if (threadIdx.x == 0) s.bos = bos;
+    if (threadIdx.x == kTile - 1) s.eos = eos;
   }
 }
 __device__ __forceinline__ RowBits warp_rows(const TileRows& s, int warp, int lane) {
@@ -184,10 +182,11 @@ template <int V>
 struct Gates {
   Vals<V> A2, cr, ci;
 };
+constexpr float kBiasScale16 = -kLog2e, kBiasScale32 = 1.f;
 template <typename T, int V>
 __device__ __forceinline__ void load_gates(Gates<V>& c, const LinrecParams& p, int ch, bool ok) {
   // bf16 rows: exp(-(v + bias)) = 2^(-v log2 e - bias log2 e)
-  constexpr float k = sizeof(T) < 4 ? -kLog2e : 1.f;
+  constexpr float k = sizeof(T) < 4 ? kBiasScale16 : kBiasScale32;
   float A2[V], cr[V], ci[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
@@ -213,10 +212,11 @@ __device__ __forceinline__ pair gate_exp(pair v, pair c) {  // exp(-(v + bias))
 __device__ __forceinline__ pair rcp_of(pair v) {
   return pr(ptx::rcp_approx(un(v).x), ptx::rcp_approx(un(v).y));
 }
-__device__ __forceinline__ float sqrt_approx(float v) {
-  float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
+__device__ __forceinline__ pair rsqrt_of(pair v) {  // finite at zero
+  float2 r = un(v);
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(fmaxf(r.x, 1e-37f)));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(fmaxf(r.y, 1e-37f)));
+  return pr(r.x, r.y);
 }
 constexpr float kSmallStep = -0.18033688f;  // L2 at u = 1/4
 __device__ __forceinline__ pair scaled_m2(pair L2, pair a) {
@@ -232,7 +232,7 @@ __device__ __forceinline__ void step_of(pair x, pair r, pair i, pair A2, pair cr
   const pair I = rcp_of(pfma(gate_exp<T>(i, ci), pr(4096.f), pr(4096.f)));
   a = pex2(padd(L2, pr(2.5e-8f)));
   const pair m2 = scaled_m2(L2, a);
-  b = pmul(pmul(pr(sqrt_approx(un(m2).x), sqrt_approx(un(m2).y)), I), x);
+  b = pmul(pmul(pmul(m2, rsqrt_of(m2)), I), x);
 }
 template <typename T, int V>
 __device__ __forceinline__ void step_of(const Vals<V>& x, const Vals<V>& r, const Vals<V>& i, const Gates<V>& c,
@@ -263,7 +263,7 @@ template <int V>
 struct TileShared {
   float P[kWarps][32 * V], H[kWarps][32 * V];  // what each run does to a state
   float S[kWarps][32 * V];                     // the state before each run
-  int cut[kWarps];                             // whether a run holds a sequence's start
+  unsigned char cut[kWarps];                   // whether a run holds a sequence's start
   unsigned next;
 };
 template <int V>
@@ -274,6 +274,20 @@ __device__ __forceinline__ void put(float (&at)[32 * V], int lane, const Vals<V>
   for (int k = 0; k < V; ++k) at[lane * V + k] = f[k];
 }
 template <int V>
+__device__ __forceinline__ Vals<V> read_vals(const float* at) {
+  Raw<float, V> r;
+  load_words(r.w, at);
+  float f[V];
+  unpack(r, f);
+  return vals_from(f);
+}
+template <int V>
+__device__ __forceinline__ void read_gates(Gates<V>& c, const LinrecParams& p, int ch) {
+  c.A2 = read_vals<V>(p.gates + ch);
+  c.cr = read_vals<V>(p.gates + p.dim + ch);
+  c.ci = read_vals<V>(p.gates + 2 * (int64_t)p.dim + ch);
+}
+template <int V>
 __device__ __forceinline__ Vals<V> get(const float (&at)[32 * V], int lane) {
   float f[V];
 #pragma unroll
@@ -281,83 +295,166 @@ __device__ __forceinline__ Vals<V> get(const float (&at)[32 * V], int lane) {
   return vals_from(f);
 }
 
-// The state before tile s: the end state of the nearest tile that has published one, taken
-// through what the tiles since then do to it, one after the other.  Every end state is
-// published as the same chain of products, so the result does not depend on which is found.
-constexpr int kWindow = 8;
-__device__ __forceinline__ float state_before(const LinrecParams& p, int64_t s, int ch) {
-  const unsigned* const ends = p.ends + ch;
-  unsigned v = ld_word(ends + (s - 1) * p.dim);
-  if (v != ~0u) return __uint_as_float(v);
-  const uint64_t* const agg = p.agg + ch;
-  uint64_t t0 = 0;
+// The word at `p` once it is set; after the limit (or another wait's) zero, with the status.
+template <typename W>
+__device__ __noinline__ W await_word(const W* p, unsigned* status) {
+  const uint64_t t0 = ptx::global_timer_ns();
+  while (true) {
 #pragma unroll 1
-  for (int turn = 1;; ++turn) {
-    unsigned e[kWindow];
-    uint64_t w[kWindow];
-#pragma unroll
-    for (int q = 0; q < kWindow; ++q) {
-      const int64_t at = s - 1 - q;
-      e[q] = at >= 0 ? ld_word(ends + at * p.dim) : ~0u;
-      w[q] = at >= 0 ? ld_word(agg + at * p.dim) : kUnset;
+    for (int i = 0; i < 16; ++i) {
+      const W v = ld_word(p);
+      if (v != static_cast<W>(kUnset)) return v;
     }
-    int found = -1;
-#pragma unroll
-    for (int q = kWindow - 1; q >= 0; --q) {
-      if (e[q] != ~0u) found = q;       // the nearest one counts
-    }
-    bool whole = found >= 0;
-    float X = 0.f;
-#pragma unroll
-    for (int q = kWindow - 1; q >= 0; --q) {
-      if (q == found) X = __uint_as_float(e[q]);
-      if (q < found) {
-        whole = whole && w[q] != kUnset;
-        X = fmaf(__uint_as_float((unsigned)w[q]), X, __uint_as_float((unsigned)(w[q] >> 32)));
-      }
-    }
-    if (whole) return X;
-    if (turn % 16 == 0) {
-      const uint64_t now = ptx::global_timer_ns();
-      if (!t0) t0 = now;
-      if (now - t0 > kWaitNs || (ld_word(p.status) & kDevStatusTimeout)) {
-        atomicOr(p.status, kDevStatusTimeout);
-        return 0.f;
-      }
+    if (ptx::global_timer_ns() - t0 > kWaitNs || (ld_word(status) & kDevStatusTimeout)) {
+      atomicOr(status, kDevStatusTimeout);
+      return 0;
     }
   }
+}
+
+// Tiles form groups of kGroup.  A group's last tile also publishes what the whole group does
+// to a state, so the states at the ends of groups follow one from the other without the tiles
+// between: each is the one before it through one group, in this order in every run.  Within a
+// group a state is the group's first one taken through its tiles one after the other.
+__device__ __forceinline__ float stepped(uint64_t w, float X) {
+  return fmaf(__uint_as_float((unsigned)w), X, __uint_as_float((unsigned)(w >> 32)));
+}
+
+// X taken through tiles from .. to - 1.
+__device__ __forceinline__ float through_tiles(const LinrecParams& p, float X, int64_t from, int64_t to, int ch) {
+  constexpr int kBatch = 8;
+  const uint64_t* at = p.agg + from * p.dim + ch;
+#pragma unroll 1
+  for (int left = (int)(to - from); left > 0; left -= kBatch, at += kBatch * (int64_t)p.dim) {
+    uint64_t w[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) w[q] = q < left ? ld_word(at + q * (int64_t)p.dim) : 0;
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q)
+      if (q < left) {
+        if (w[q] == kUnset) w[q] = await_word(at + q * (int64_t)p.dim, p.status);
+        X = stepped(w[q], X);
+      }
+  }
+  return X;
+}
+
+// The state at the end of group g, in a sequence that starts in group `edge` or before the
+// window: that of the nearest group which has published one (the window's last is waited
+// for), taken through the groups since then.
+constexpr int kWindow = 8;
+__device__ __forceinline__ float state_after_group(const LinrecParams& p, int64_t g, int64_t edge, int ch) {
+  const int64_t dim = p.dim;
+  const unsigned* const ends = p.ends + (g * kGroup + kGroup - 1) * dim + ch;
+  unsigned found = ld_word(ends);
+  if (found != ~0u) return __uint_as_float(found);
+  const uint64_t* const agg = p.group_agg + g * dim + ch;
+  const int last = (int)min((int64_t)kWindow - 1, g - edge);
+  unsigned e[kWindow];
+  uint64_t w[kWindow - 1];
+#pragma unroll
+  for (int q = 0; q < kWindow; ++q) {
+    e[q] = q <= last ? ld_word(ends - q * kGroup * dim) : ~0u;
+    if (q < kWindow - 1) w[q] = q < last ? ld_word(agg - q * dim) : 0;
+  }
+  int at = last;
+#pragma unroll
+  for (int q = kWindow - 1; q >= 0; --q)
+    if (e[q] != ~0u) at = q, found = e[q];
+  if (found == ~0u) found = await_word(ends - last * kGroup * dim, p.status);
+  float X = __uint_as_float(found);
+#pragma unroll
+  for (int q = kWindow - 2; q >= 0; --q)
+    if (q < at) {
+      if (w[q] == kUnset) w[q] = await_word(agg - q * dim, p.status);
+      X = stepped(w[q], X);
+    }
+  return X;
+}
+
+// The state before tile s, which goes on with a sequence that starts in tile `edge`.  (P, H) is
+// the tile's own step, for what a group's last tile publishes.
+__device__ __forceinline__ float state_before(const LinrecParams& p, int64_t s, int64_t edge, int ch, float P,
+                                              float H, bool cut) {
+  const int64_t g = s / kGroup, first = g * kGroup;
+  const bool whole = edge < first;               // the group goes on with what is before it
+  if (whole && s == first + kGroup - 1 && !cut) {
+    const uint64_t* at = p.agg + first * p.dim + ch;
+    uint64_t w = ld_word(at);
+    if (w == kUnset) w = await_word(at, p.status);
+    float Pg = __uint_as_float((unsigned)w), Hg = __uint_as_float((unsigned)(w >> 32));
+#pragma unroll 1
+    for (int q = 1; q < kGroup - 1; q += 2) {
+      uint64_t u[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) u[k] = ld_word(at + (q + k) * (int64_t)p.dim);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (u[k] == kUnset) u[k] = await_word(at + (q + k) * (int64_t)p.dim, p.status);
+        Hg = stepped(u[k], Hg), Pg *= __uint_as_float((unsigned)u[k]);
+      }
+    }
+    Hg = fmaf(P, Hg, H), Pg *= P;
+    st_word(p.group_agg + g * p.dim + ch, (uint64_t)published(Pg) | ((uint64_t)published(Hg) << 32));
+    const float before = state_after_group(p, g - 1, edge / kGroup, ch);
+    st_word(p.ends + s * p.dim + ch, published(fmaf(Pg, before, Hg)));
+    return through_tiles(p, before, first, s, ch);
+  }
+  float X;
+  const int64_t from = whole ? first : edge + 1;
+  unsigned v = s > from ? ld_word(p.ends + (s - 1) * p.dim + ch) : ~0u;
+  if (v != ~0u) {
+    X = __uint_as_float(v);
+  } else {
+    if (whole) {
+      X = state_after_group(p, g - 1, edge / kGroup, ch);
+    } else {
+      const unsigned* at = p.ends + edge * p.dim + ch;
+      v = ld_word(at);
+      X = __uint_as_float(v != ~0u ? v : await_word(at, p.status));
+    }
+    X = through_tiles(p, X, from, s, ch);
+  }
+  if (!cut) {
+    const float end = fmaf(P, X, H);
+    st_word(p.ends + s * p.dim + ch, published(end));
+    if (s == first + kGroup - 1) st_word(p.group_agg + g * p.dim + ch, (uint64_t)published(end) << 32);
+  }
+  return X;
 }
 
 // One channel of a tile: its runs joined, published, and the state before each.
 // FORWARD: runs in the order of their rows.  `carry`: the tile's first row goes on.
 template <int V, bool FORWARD>
-__device__ __forceinline__ float join_runs(const LinrecParams& p, TileShared<V>& sh, int64_t s, int c, int ch,
-                                           bool carry) {
-  float P = 1.f, H = 0.f;
-  bool any = false;
+__device__ __forceinline__ float join_runs(const LinrecParams& p, TileShared<V>& sh, int64_t s, int64_t edge, int c,
+                                           int ch, bool carry) {
+  static_assert(kWarps == 8, "eight flags in one word");
+  const uint64_t cuts = *reinterpret_cast<const uint64_t*>(sh.cut);
+  float Pw[kWarps], Hw[kWarps], P = 1.f, H = 0.f;
 #pragma unroll
   for (int q = 0; q < kWarps; ++q) {
     const int w = FORWARD ? q : kWarps - 1 - q;
-    const bool cut = sh.cut[w];
-    const float Pw = sh.P[w][c], Hw = sh.H[w][c];
-    H = cut ? Hw : fmaf(Pw, H, Hw);
-    P *= Pw;
-    any |= cut;
+    Pw[q] = sh.P[w][c], Hw[q] = sh.H[w][c];
+    H = cuts >> (8 * w) & 1 ? Hw[q] : fmaf(Pw[q], H, Hw[q]);
+    P *= Pw[q];
   }
-  const bool quiet = p.stall && s == 0;
-  if (any) {
-    if (!quiet) st_word(p.ends + s * p.dim + ch, published(H));
-  } else if (carry && !quiet) {
-    st_word(p.agg + s * p.dim + ch, (uint64_t)published(P) | ((uint64_t)published(H) << 32));
+  if (!(p.stall && s == 0)) {
+    // (a tile that does not hand on what it is given is only asked for its step where
+    // cu_seqlens is inconsistent; no wait is left without an answer then either)
+    st_word(p.agg + s * p.dim + ch, (uint64_t)published(cuts ? 0.f : P) | ((uint64_t)published(H) << 32));
+    if (!carry || cuts) {
+      st_word(p.ends + s * p.dim + ch, published(H));
+      if (s % kGroup == kGroup - 1)
+        st_word(p.group_agg + s / kGroup * p.dim + ch, (uint64_t)published(H) << 32);
+    }
   }
-  const float X = carry ? state_before(p, s, ch) : 0.f;
-  if (!any && !quiet) st_word(p.ends + s * p.dim + ch, published(carry ? fmaf(P, X, H) : H));
-  float S = X;
+  float S = carry ? state_before(p, s, edge, ch, P, H, cuts != 0) : 0.f;
+  const float X = S;
 #pragma unroll
   for (int q = 0; q < kWarps; ++q) {
     const int w = FORWARD ? q : kWarps - 1 - q;
     sh.S[w][c] = S;
-    S = sh.cut[w] ? sh.H[w][c] : fmaf(sh.P[w][c], S, sh.H[w][c]);
+    S = cuts >> (8 * w) & 1 ? Hw[q] : fmaf(Pw[q], S, Hw[q]);
   }
   return X;
 }
@@ -380,19 +477,19 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_fwd_kernel(LinrecParams
     const int64_t row0 = s * kTile + warp * R;
     unsigned next = 0;
     if (threadIdx.x == 0) next = atomicAdd(p.ticket, 1u);
-    Raw<T, V> rx[R], rr[R], ri[R];
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const bool in = ok && row0 + j < p.total;
-      rx[j] = {}, rr[j] = {}, ri[j] = {};
-      if (in) {
-        load_vals<T, V>(rx[j], p.x, (row0 + j) * p.x_s + ch);
-        load_vals<T, V>(rr[j], p.r, (row0 + j) * p.r_s + ch);
-        load_vals<T, V>(ri[j], p.i, (row0 + j) * p.i_s + ch);
-      }
+    const int n = ok ? (int)min((int64_t)R, p.total - row0) : 0;  // rows that exist
+    Raw<T, V> rx[R], rr[R], ri[R], rz[R];
+    Gates<V> c = {};
+    if (n == R) {
+      load_run<false>(rx, p.x, row0, p.x_s, ch, n);
+      load_run<false>(rr, p.r, row0, p.r_s, ch, n);
+      load_run<false>(ri, p.i, row0, p.i_s, ch, n);
+    } else {
+      load_run<true>(rx, p.x, row0, p.x_s, ch, n);
+      load_run<true>(rr, p.r, row0, p.r_s, ch, n);
+      load_run<true>(ri, p.i, row0, p.i_s, ch, n);
     }
-    Gates<V> c;
-    load_gates<T>(c, p, ch, ok);
+    if (ok) read_gates(c, p, ch);
     find_rows(rows_s, p, s * kTile);
     __syncthreads();
     const RowBits bits = warp_rows(rows_s, warp, lane);
@@ -411,44 +508,56 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_fwd_kernel(LinrecParams
     }
     // what the run does to a state
     Vals<V> P = a[0], h = b[0];
+    if (!bits.start) {
 #pragma unroll
-    for (int j = 1; j < R; ++j) {
-      const bool cut = bits.start >> j & 1;
-      h = cut ? b[j] : fma_of(a[j], h, b[j]);
-      P = mul_of(P, a[j]);
+      for (int j = 1; j < R; ++j) h = fma_of(a[j], h, b[j]), P = mul_of(P, a[j]);
+    } else {
+#pragma unroll
+      for (int j = 1; j < R; ++j) h = bits.start >> j & 1 ? b[j] : fma_of(a[j], h, b[j]);
     }
     put<V>(sh.P[warp], lane, P);
     put<V>(sh.H[warp], lane, h);
     if (lane == 0) sh.cut[warp] = bits.start != 0;
-    Raw<T, V> rz[R];
-    if constexpr (OUT) {
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        rz[j] = {};
-        if (p.z && ok && row0 + j < p.total) load_vals<T, V>(rz[j], p.z, (row0 + j) * p.z_s + ch);
-      }
+    if (OUT && p.z) {
+      if (n == R) load_run<false>(rz, p.z, row0, p.z_s, ch, n);
+      else load_run<true>(rz, p.z, row0, p.z_s, ch, n);
     }
     __syncthreads();
     if (threadIdx.x < 32 * V && c0 + (int)threadIdx.x < p.dim) {
       const unsigned char f0 = rows_s.flags[0];
-      const float X = join_runs<V, true>(p, sh, s, threadIdx.x, c0 + threadIdx.x, (f0 & 4) && !(f0 & 1) && s > 0);
+      const float X = join_runs<V, true>(p, sh, s, rows_s.bos / kTile, threadIdx.x, c0 + threadIdx.x,
+                                         (f0 & 4) && !(f0 & 1) && s > 0);
       if (p.states) p.states[s * p.dim + c0 + threadIdx.x] = X;
     }
     if constexpr (OUT) {
       __syncthreads();
       h = get<V>(sh.S[warp], lane);
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        const bool cut = bits.start >> j & 1;
-        h = cut ? b[j] : fma_of(a[j], h, b[j]);
-        if (!ok || !(bits.live >> j & 1)) continue;
+      char* const at = reinterpret_cast<char*>(static_cast<T*>(p.out) + row0 * p.dim + ch);
+      auto put_row = [&](int j) {
         float y[V];
         if (p.z) vals_to(mul_of(h, silu_of<T>(vals_of(rz[j]))), y);
         else vals_to(h, y);
-        store_vals<T, V>(p.out, (row0 + j) * p.dim + ch, y);
-        if (p.fin && (bits.last >> j & 1)) {
-          vals_to(h, y);
-          store_state<V>(p.fin, (int64_t)rows_s.n[warp * R + j] * p.dim + ch, y, p.state_bf16);
+        store_vals<T, V>(at + (uint64_t)(uint32_t)p.dim * (uint32_t)(j * sizeof(T)), 0, y);
+      };
+      if (!ok) {
+      } else if (!bits.start && !bits.last && bits.live == (1u << R) - 1) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          h = fma_of(a[j], h, b[j]);
+          put_row(j);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          const bool cut = bits.start >> j & 1;
+          h = cut ? b[j] : fma_of(a[j], h, b[j]);
+          if (!(bits.live >> j & 1)) continue;
+          put_row(j);
+          if (p.fin && (bits.last >> j & 1)) {
+            float f[V];
+            vals_to(h, f);
+            store_state<V>(p.fin, (int64_t)rows_s.n[warp * R + j] * p.dim + ch, f, p.state_bf16);
+          }
         }
       }
     }
@@ -501,12 +610,8 @@ __device__ __forceinline__ void grads_of(pair x, pair r, pair i, pair A2, pair c
   const pair R = rcp_of(padd(er, pr(1.f)));
   const pair I = rcp_of(pfma(ei, pr(4096.f), pr(4096.f)));  // by 2^-12, as m is by 2^12
   const pair L2 = pmul(A2, R);
-  const float2 m2 = un(scaled_m2(L2, a));
-  float2 rs;                                                // 2^-12 / m, finite at zero
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(rs.x) : "f"(fmaxf(m2.x, 1e-37f)));
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(rs.y) : "f"(fmaxf(m2.y, 1e-37f)));
-  const pair rsm = pr(rs.x, rs.y);
-  dx = pmul(pmul(g, pmul(pr(m2.x, m2.y), rsm)), I);
+  const pair m2 = scaled_m2(L2, a), rsm = rsqrt_of(m2);     // 2^-12 / m
+  dx = pmul(pmul(g, pmul(m2, rsm)), I);
   di = pmul(pmul(dx, x), pmul(pmul(ei, pr(4096.f)), I));
   g = pmul(g, a);
   // g L2 and L2 / m before what could leave the range for an infinite rate
@@ -561,21 +666,23 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
     const int64_t row0 = tile * kTile + warp * R;
     unsigned next = 0;
     if (threadIdx.x == 0) next = atomicAdd(p.ticket, 1u);
+    const int n = ok ? (int)min((int64_t)R, p.total - row0) : 0;  // rows that exist
     Raw<T, V> rx[R], rr[R], ri[R], rd[R], rz[R];
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const bool in = ok && row0 + j < p.total;
-      rx[j] = {}, rr[j] = {}, ri[j] = {}, rd[j] = {}, rz[j] = {};
-      if (in) {
-        load_vals<T, V>(rx[j], p.x, (row0 + j) * p.x_s + ch);
-        load_vals<T, V>(rr[j], p.r, (row0 + j) * p.r_s + ch);
-        load_vals<T, V>(ri[j], p.i, (row0 + j) * p.i_s + ch);
-        load_vals<T, V>(rd[j], p.dout, (row0 + j) * p.dim + ch);
-        if (p.z) load_vals<T, V>(rz[j], p.z, (row0 + j) * p.z_s + ch);
-      }
+    Gates<V> c = {};
+    if (n == R) {
+      load_run<false>(rx, p.x, row0, p.x_s, ch, n);
+      load_run<false>(rr, p.r, row0, p.r_s, ch, n);
+      load_run<false>(ri, p.i, row0, p.i_s, ch, n);
+      load_run<false>(rd, p.dout, row0, p.dim, ch, n);
+      if (p.z) load_run<false>(rz, p.z, row0, p.z_s, ch, n);
+    } else {
+      load_run<true>(rx, p.x, row0, p.x_s, ch, n);
+      load_run<true>(rr, p.r, row0, p.r_s, ch, n);
+      load_run<true>(ri, p.i, row0, p.i_s, ch, n);
+      load_run<true>(rd, p.dout, row0, p.dim, ch, n);
+      if (p.z) load_run<true>(rz, p.z, row0, p.z_s, ch, n);
     }
-    Gates<V> c;
-    load_gates<T>(c, p, ch, ok);
+    if (ok) read_gates(c, p, ch);
     find_rows(rows_s, p, tile * kTile);
     __syncthreads();
     const RowBits bits = warp_rows(rows_s, warp, lane);
@@ -633,7 +740,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
     __syncthreads();
     if (threadIdx.x < CH && c0 + (int)threadIdx.x < p.dim) {
       const unsigned char f = rows_s.flags[kTile - 1];
-      join_runs<V, false>(p, sh, s, threadIdx.x, c0 + threadIdx.x, (f & 4) && !(f & 2) && s > 0);
+      join_runs<V, false>(p, sh, s, p.tiles - 1 - (rows_s.eos - 1) / kTile, threadIdx.x, c0 + threadIdx.x,
+                          (f & 4) && !(f & 2) && s > 0);
     } else if (threadIdx.x >= 128 && threadIdx.x < 128 + CH && c0 + (int)threadIdx.x - 128 < p.dim) {
       const int k = threadIdx.x - 128;
       float S = __ldg(p.states + tile * p.dim + c0 + k);
@@ -652,10 +760,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
       const Vals<V> before = h;
       h = fma_of(a[j], h, b[j]);
       b[j] = before;
-      if (p.z && ok && row0 + j < p.total)
-        store_of<T>(p.dz, (row0 + j) * p.dim + ch, bits.live >> j & 1 ? mul_of(dq[j], h) : splat<V>(0.f));
+      if (p.z && j < n)
+        store_of<T>(p.dz, row0 * p.dim + ch + (uint64_t)(uint32_t)p.dim * (uint32_t)j, bits.live >> j & 1 ? mul_of(dq[j], h) : splat<V>(0.f));
     }
     Vals<V> C = get<V>(sh.S[warp], lane);
+    const int64_t row_at = row0 * p.dim + ch;
     Vals<V> se = splat<V>(0.f), sr = se, si = se;
 #pragma unroll
     for (int j = R - 1; j >= 0; --j) {
@@ -664,8 +773,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
       grads_of<T>(vals_of(rx[j]), vals_of(rr[j]), vals_of(ri[j]), c, a[j], b[j], C, e, dx, dr, di);
       if (!(bits.live >> j & 1)) e = dx = dr = di = splat<V>(0.f);
       se = add_of(se, e), sr = add_of(sr, dr), si = add_of(si, di);
-      if (ok && row0 + j < p.total) {
-        const int64_t at = (row0 + j) * p.dim + ch;
+      if (j < n) {
+        const int64_t at = row_at + (uint64_t)(uint32_t)p.dim * (uint32_t)j;
         store_of<T>(p.dx, at, dx);
         store_of<T>(p.dr, at, dr);
         store_of<T>(p.di, at, di);
@@ -702,6 +811,9 @@ struct SetupParams {
   const int64_t* cu;
   int64_t T, total;
   int32_t N, dim;
+  float* gates;              // [3][dim], written
+  const float *A_log, *r_bias, *i_bias;
+  float bias_scale;
   const void* src;           // NULL: zeros
   void* dst;                 // NULL: nothing
   int32_t src_bf16, dst_bf16;
@@ -713,6 +825,11 @@ __global__ void __launch_bounds__(256) linrec_setup_kernel(SetupParams p) {
     if (p.cu) check_seqlens(p.cu, p.N, p.total, p.status, kDevStatusBadSeqlens);
     else if (threadIdx.x == 0) p.status[0] = 0u;
     if (threadIdx.x >= 1) p.status[threadIdx.x] = 0u;
+  }
+  for (int64_t d = at; d < p.dim; d += step) {
+    p.gates[d] = scan::rate_of(p.A_log[d]);
+    p.gates[p.dim + d] = p.r_bias ? p.bias_scale * p.r_bias[d] : 0.f;
+    p.gates[2 * (int64_t)p.dim + d] = p.i_bias ? p.bias_scale * p.i_bias[d] : 0.f;
   }
   if (!p.dst || (!p.cu && p.T > 0)) return;
   for (int64_t n = blockIdx.x; n < p.N; n += gridDim.x) {
@@ -730,7 +847,8 @@ bool al_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 int64_t tiles_of(int64_t total) { return (total + kTile - 1) / kTile; }
 size_t join_bytes(int64_t total, int32_t dim) {  // what tiles publish
-  return up256((size_t)tiles_of(total) * dim * 8) + up256((size_t)tiles_of(total) * dim * 4);
+  const size_t tiles = (size_t)tiles_of(total);
+  return up256(tiles * dim * 8) + up256(tiles / kGroup * dim * 8) + up256(tiles * dim * 4);
 }
 
 kda_status check_sizes(const kda_linrec_problem* q, LinrecParams& p) {
@@ -768,7 +886,8 @@ kda_status check_linrec(const kda_linrec_problem* q, LinrecParams& p, int& lanes
       !al_to(q->initial_state, se) || !al_to(q->cu_seqlens, 8))
     return KDA_ERR_MISALIGNED;
   p.x = q->x, p.r = q->r, p.i = q->i, p.z = q->z;
-  p.x_s = q->x_stride, p.r_s = q->r_stride, p.i_s = q->i_stride, p.z_s = stride[3];
+  p.x_s = (uint32_t)q->x_stride, p.r_s = (uint32_t)q->r_stride, p.i_s = (uint32_t)q->i_stride;
+  p.z_s = (uint32_t)stride[3];
   p.A_log = q->A_log, p.r_bias = q->r_bias, p.i_bias = q->i_bias;
   p.init = q->initial_state, p.state_bf16 = q->state_dtype == KDA_STATE_BF16;
   p.stall = q->debug_stall;
@@ -783,16 +902,20 @@ bool plan_pass(LinrecParams& p, int lanes, uint8_t*& ws) {
   p.tiles = tiles_of(p.total);
   p.blocks = (p.dim + 32 * lanes - 1) / (32 * lanes);
   p.agg = reinterpret_cast<uint64_t*>(ws);
-  p.ends = reinterpret_cast<unsigned*>(ws + up256((size_t)p.tiles * p.dim * 8));
+  p.group_agg = reinterpret_cast<uint64_t*>(ws + up256((size_t)p.tiles * p.dim * 8));
+  p.ends = reinterpret_cast<unsigned*>(reinterpret_cast<uint8_t*>(p.group_agg) +
+                                       up256((size_t)(p.tiles / kGroup) * p.dim * 8));
   ws += join_bytes(p.total, p.dim);
   return p.tiles * p.blocks < (int64_t(1) << 31);
 }
 
-cudaError_t launch_setup(const LinrecParams& p, void* words, size_t bytes, const void* src, bool src_bf16,
+cudaError_t launch_setup(const LinrecParams& p, bool f32, void* words, size_t bytes, const void* src, bool src_bf16,
                          void* dst, bool dst_bf16, cudaStream_t stream) {
   SetupParams s = {};
   s.status = p.status, s.words = static_cast<uint64_t*>(words), s.count = (int64_t)(bytes / 8);
   s.cu = p.cu, s.T = p.T, s.total = p.total, s.N = p.N, s.dim = p.dim;
+  s.gates = p.gates, s.A_log = p.A_log, s.r_bias = p.r_bias, s.i_bias = p.i_bias;
+  s.bias_scale = f32 ? kBiasScale32 : kBiasScale16;
   s.src = src, s.dst = dst, s.src_bf16 = src_bf16, s.dst_bf16 = dst_bf16;
   const int64_t want = (s.count + 1023) / 1024 + (dst && p.cu ? p.N : 1);
   linrec_setup_kernel<<<(unsigned)(want < 608 ? want : 608), 256, 0, stream>>>(s);
@@ -826,8 +949,9 @@ cudaError_t launch_fwd(const LinrecParams& p, bool f32, int lanes, cudaStream_t 
 size_t states_bytes(int64_t total, int32_t dim) {
   return (size_t)(total / KDA_LINREC_CHUNK + 1) * dim * sizeof(float);
 }
+size_t gates_bytes(int32_t dim) { return up256((size_t)dim * 3 * sizeof(float)); }
 size_t fwd_bytes(const LinrecParams& p) {
-  return KDA_STATUS_BYTES + join_bytes(p.total, p.dim);
+  return KDA_STATUS_BYTES + gates_bytes(p.dim) + join_bytes(p.total, p.dim);
 }
 
 }  // namespace
@@ -859,7 +983,8 @@ kda_status kda_linrec_bwd_get_workspace_size(const kda_linrec_problem* problem, 
   const kda_status st = check_sizes(problem, p);
   if (st != KDA_OK) return st;
   const int64_t tiles = tiles_of(p.total);
-  *bytes = KDA_STATUS_BYTES + join_bytes(p.total, p.dim) + up256((size_t)tiles * 3 * p.dim * sizeof(float));
+  *bytes = KDA_STATUS_BYTES + gates_bytes(p.dim) + join_bytes(p.total, p.dim) +
+           up256((size_t)tiles * 3 * p.dim * sizeof(float));
   if (!have_states)
     *bytes += join_bytes(p.total, p.dim) + up256(states_bytes(p.total, p.dim));
   return KDA_OK;
@@ -898,10 +1023,11 @@ kda_status kda_linrec_fwd(const kda_linrec_problem* problem, void* out, void* fi
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
   }
   uint8_t* ws = static_cast<uint8_t*>(workspace) + KDA_STATUS_BYTES;
+  p.gates = reinterpret_cast<float*>(ws), ws += gates_bytes(p.dim);
   lanes = lanes_of(lanes, f32, false);
   if (!plan_pass(p, lanes, ws)) return KDA_ERR_INVALID_SHAPE;
   p.ticket = p.status + 1;
-  cudaError_t e = launch_setup(p, p.agg, fwd_bytes(p) - KDA_STATUS_BYTES, p.init, p.state_bf16,
+  cudaError_t e = launch_setup(p, f32, p.agg, join_bytes(p.total, p.dim), p.init, p.state_bf16,
                                p.fin == p.init ? nullptr : p.fin, p.state_bf16, stream);
   if (e == cudaSuccess && p.total > 0) e = launch_fwd<true>(p, f32, lanes, stream);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
@@ -937,6 +1063,7 @@ kda_status kda_linrec_bwd(const kda_linrec_problem* problem, const void* dout, c
   if (st != KDA_OK) return st;
   p.status = static_cast<unsigned*>(workspace);
   uint8_t* ws = static_cast<uint8_t*>(workspace) + KDA_STATUS_BYTES;
+  p.gates = reinterpret_cast<float*>(ws), ws += gates_bytes(p.dim);
   uint8_t* const published_at = ws;
   LinrecParams f = p;
   f.stall = 0;
@@ -952,7 +1079,7 @@ kda_status kda_linrec_bwd(const kda_linrec_problem* problem, const void* dout, c
   p.ticket = p.status + 1, f.ticket = p.status + 2;
   p.dout = dout, p.dfin = dfinal_state;
   p.dx = dx, p.dr = dr, p.di = di, p.dz = dz, p.dinit = dinitial_state;
-  cudaError_t err = launch_setup(p, published_at, published_bytes, dfinal_state, p.state_bf16,
+  cudaError_t err = launch_setup(p, f32, published_at, published_bytes, dfinal_state, p.state_bf16,
                                  dinitial_state, false, stream);
   if (err == cudaSuccess && p.total > 0) {
     if (!chunk_states) err = launch_fwd<false>(f, f32, lanes_of(lanes, f32, false), stream);
