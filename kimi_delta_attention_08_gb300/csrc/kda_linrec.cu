@@ -52,6 +52,7 @@ struct LinrecParams {
   int64_t T, total;
   int32_t N, dim, blocks;    // blocks: of channels
   int64_t tiles;             // of rows
+  unsigned units, strips, strip_tiles;  // see set_unit
   void *out, *fin;
   float* states;             // [total / KDA_LINREC_CHUNK + 1][dim]
   unsigned *status, *ticket;
@@ -212,10 +213,10 @@ __device__ __forceinline__ pair gate_exp(pair v, pair c) {  // exp(-(v + bias))
 __device__ __forceinline__ pair rcp_of(pair v) {
   return pr(ptx::rcp_approx(un(v).x), ptx::rcp_approx(un(v).y));
 }
-__device__ __forceinline__ pair rsqrt_of(pair v) {  // finite at zero
-  float2 r = un(v);
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(fmaxf(r.x, 1e-37f)));
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(fmaxf(r.y, 1e-37f)));
+__device__ __forceinline__ pair rsqrt_of(pair v) {  // finite at zero; v is at least 2^-98 where it is not
+  float2 r = un(padd(v, pr(FLT_MIN)));
+  asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(r.x));
+  asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(r.y));
   return pr(r.x, r.y);
 }
 constexpr float kSmallStep = -0.18033688f;  // L2 at u = 1/4
@@ -264,8 +265,20 @@ struct TileShared {
   float P[kWarps][32 * V], H[kWarps][32 * V];  // what each run does to a state
   float S[kWarps][32 * V];                     // the state before each run
   unsigned char cut[kWarps];                   // whether a run holds a sequence's start
-  unsigned next;
+  int tile, block;                             // the tile at work, in the order of the walk
 };
+
+// The unit of work that `ticket` stands for: rows' tile first, all channel blocks of one before
+// the next.  A batch of sequences that are whole tiles is walked a tile of each in turn: a tile
+// then rarely waits for the one before it (8 x 4,096 tokens of 4,096 channels 379 us without,
+// 311 with it).
+template <int V>
+__device__ __forceinline__ void set_unit(const LinrecParams& p, TileShared<V>& sh, unsigned ticket) {
+  const unsigned blocks = p.blocks, w = ticket / blocks;
+  sh.block = (int)(ticket - w * blocks);
+  const unsigned q = w / p.strips;
+  sh.tile = ticket < p.units ? (int)((w - q * p.strips) * p.strip_tiles + q) : -1;
+}
 template <int V>
 __device__ __forceinline__ void put(float (&at)[32 * V], int lane, const Vals<V>& v) {
   float f[V];
@@ -466,13 +479,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_fwd_kernel(LinrecParams
   __shared__ TileRows rows_s;
   __shared__ __align__(16) TileShared<V> sh;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t units = p.tiles * p.blocks;
-  if (threadIdx.x == 0) sh.next = atomicAdd(p.ticket, 1u);
+  if (threadIdx.x == 0) set_unit(p, sh, atomicAdd(p.ticket, 1u));
   __syncthreads();
-  int64_t unit = sh.next;
-  while (unit < units) {
-    const int64_t s = unit / p.blocks;
-    const int c0 = (int)(unit % p.blocks) * 32 * V, ch = c0 + lane * V;
+  while (sh.tile >= 0) {
+    const int64_t s = sh.tile;
+    const int c0 = sh.block * 32 * V, ch = c0 + lane * V;
     const bool ok = ch < p.dim;
     const int64_t row0 = s * kTile + warp * R;
     unsigned next = 0;
@@ -561,9 +572,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_fwd_kernel(LinrecParams
         }
       }
     }
-    if (threadIdx.x == 0) sh.next = next;
     __syncthreads();
-    unit = sh.next;
+    if (threadIdx.x == 0) set_unit(p, sh, next);
+    __syncthreads();
   }
 }
 
@@ -654,14 +665,12 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
   __shared__ __align__(16) float sums[3][kWarps][CH];
   static_assert(2 * CH <= 32 * kWarps, "a thread per channel for each of the two joins");
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t units = p.tiles * p.blocks;
-  if (threadIdx.x == 0) sh.next = atomicAdd(p.ticket, 1u);
+  if (threadIdx.x == 0) set_unit(p, sh, atomicAdd(p.ticket, 1u));
   __syncthreads();
-  int64_t unit = sh.next;
-  while (unit < units) {
-    const int64_t s = unit / p.blocks;            // counted from the last tile back
+  while (sh.tile >= 0) {
+    const int64_t s = sh.tile;                    // counted from the last tile back
     const int64_t tile = p.tiles - 1 - s;
-    const int c0 = (int)(unit % p.blocks) * CH, ch = c0 + lane * V;
+    const int c0 = sh.block * CH, ch = c0 + lane * V;
     const bool ok = ch < p.dim;
     const int64_t row0 = tile * kTile + warp * R;
     unsigned next = 0;
@@ -788,8 +797,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
     put<V>(sums[0][warp], lane, se);
     put<V>(sums[1][warp], lane, sr);
     put<V>(sums[2][warp], lane, si);
-    if (threadIdx.x == 0) sh.next = next;
     __syncthreads();
+    if (threadIdx.x == 0) set_unit(p, sh, next);
     for (int q = threadIdx.x; q < 3 * CH; q += 32 * kWarps) {
       const int w = q / CH, l = q % CH;
       float v = 0.f;
@@ -797,7 +806,6 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
       for (int k = 0; k < kWarps; ++k) v += sums[w][k][l];
       if (c0 + l < p.dim) p.part[(tile * 3 + w) * p.dim + c0 + l] = v;
     }
-    unit = sh.next;
     __syncthreads();
   }
 }
@@ -906,6 +914,10 @@ bool plan_pass(LinrecParams& p, int lanes, uint8_t*& ws) {
   p.ends = reinterpret_cast<unsigned*>(reinterpret_cast<uint8_t*>(p.group_agg) +
                                        up256((size_t)(p.tiles / kGroup) * p.dim * 8));
   ws += join_bytes(p.total, p.dim);
+  const bool whole = !p.cu && p.T > 0 && p.T % kTile == 0;
+  p.units = (unsigned)(p.tiles * p.blocks);
+  p.strips = whole ? (unsigned)(p.total / p.T) : 1u;
+  p.strip_tiles = whole ? (unsigned)(p.T / kTile) : (unsigned)p.tiles;
   return p.tiles * p.blocks < (int64_t(1) << 31);
 }
 
