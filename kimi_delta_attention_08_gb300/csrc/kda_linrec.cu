@@ -125,17 +125,79 @@ __device__ __forceinline__ void load_vals(Raw<T, V>& r, const void* p, int64_t a
   if constexpr (V == 1) r.w[0] = __float_as_uint(to_f(__ldg(static_cast<const T*>(p) + at)));
   else load_words(r.w, static_cast<const T*>(p) + at);
 }
-// A run's rows of an array from `p`, `stride` elements apart; with EDGE only the first n exist.
-template <bool EDGE, typename T, int V>
-__device__ __forceinline__ void load_run(Raw<T, V> (&r)[kRows], const void* p, int64_t row0, uint32_t stride, int ch,
-                                         int n) {
-  const char* const at = reinterpret_cast<const char*>(static_cast<const T*>(p) + row0 * stride + ch);
-#pragma unroll
-  for (int j = 0; j < kRows; ++j) {
-    if constexpr (EDGE) r[j] = {};
-    if (!EDGE || j < n) load_vals<T, V>(r[j], at + (uint64_t)stride * (uint32_t)(j * sizeof(T)), 0);
+// What a value's gates and step need of its channel (load_gates).
+template <int V>
+struct Gates {
+  Vals<V> A2, cr, ci;
+};
+// Copies of a thread's own: its values of the tile to come wait in shared memory, in slots
+// that no other thread touches, so that nothing but its own copies is waited for.
+template <int BYTES>
+__device__ __forceinline__ void copy_own(uint32_t slot, const void* p, bool there) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot), "l"(p), "r"(there ? 16 : 0) : "memory");
+  else if constexpr (BYTES == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(slot), "l"(p), "r"(there ? 8 : 0) : "memory");
+  else if constexpr (BYTES == 4)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(slot), "l"(p), "r"(there ? 4 : 0) : "memory");
+  else {  // rows at odd addresses
+    const unsigned short v = there ? __ldg(static_cast<const unsigned short*>(p)) : (unsigned short)0;
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(slot), "h"(v) : "memory");
   }
 }
+template <typename T, int V>
+struct Slots {
+  static constexpr int kBytes = V * (int)sizeof(T), kRow = 32 * kBytes;  // of a lane, of a warp's row
+  static constexpr int kRun = kRows * kRow, kArray = kWarps * kRun;      // of a run, of a tile, of one array
+  // the lane's values of a run's rows, `stride` elements apart, of which the first n exist
+  static __device__ __forceinline__ void copy(uint32_t at, const void* p, int64_t row0, uint32_t stride, int ch,
+                                              int n) {
+    const char* const from = reinterpret_cast<const char*>(static_cast<const T*>(p) + row0 * stride + ch);
+    if (n == kRows) {
+#pragma unroll
+      for (int j = 0; j < kRows; ++j)
+        copy_own<kBytes>(at + j * kRow, from + (uint64_t)stride * (uint32_t)(j * sizeof(T)), true);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kRows; ++j)
+        copy_own<kBytes>(at + j * kRow,
+                         j < n ? from + (uint64_t)stride * (uint32_t)(j * sizeof(T)) : static_cast<const char*>(p),
+                         j < n);
+    }
+  }
+  static __device__ __forceinline__ Vals<V> get(const uint8_t* at, int j) {
+    Raw<T, V> r;
+    const uint8_t* const q = at + j * kRow;
+    if constexpr (kBytes == 2) r.w[0] = (uint32_t)*reinterpret_cast<const unsigned short*>(q);
+    else if constexpr (kBytes == 4) r.w[0] = *reinterpret_cast<const uint32_t*>(q);
+    else {
+      const uint2 v = *reinterpret_cast<const uint2*>(q);
+      r.w[0] = v.x, r.w[1] = v.y;
+    }
+    float f[V];
+    if constexpr (V == 1 && sizeof(T) == 4) f[0] = __uint_as_float(r.w[0]);
+    else unpack(r, f);
+    return vals_from(f);
+  }
+  // the channel's gates, one lane's after the other's
+  static constexpr int kGates = 3 * 32 * kWarps * V * 4;
+  static __device__ __forceinline__ void copy_gates(uint32_t at, const float* g, int dim, int ch, bool ok) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      copy_own<4 * V>(at + k * 32 * kWarps * V * 4, ok ? g + k * (int64_t)dim + ch : g, ok);
+  }
+  static __device__ __forceinline__ void gates(Gates<V>& c, const uint8_t* at) {
+    Vals<V>* const to[3] = {&c.A2, &c.cr, &c.ci};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      Raw<float, V> r;
+      load_words<true>(r.w, at + k * 32 * kWarps * V * 4);
+      float f[V];
+      unpack(r, f);
+      *to[k] = vals_from(f);
+    }
+  }
+};
 template <typename T, int V>
 __device__ __forceinline__ void vals_of(const Raw<T, V>& r, float (&f)[V]) {
   if constexpr (V == 1) f[0] = __uint_as_float(r.w[0]);
@@ -146,43 +208,40 @@ __device__ __forceinline__ void store_vals(void* p, int64_t at, const float (&f)
   store_row<T, V, (V > 1)>(static_cast<T*>(p) + at, f, 1, 1);
 }
 
-// What a warp knows about its rows: bit j for row j.
-struct RowBits {
-  unsigned start, last, live;
-};
-
-// Rows of the tile: every row's sequence.
+// Rows of a tile: every row's sequence, and a bit per row.
 struct TileRows {
   int n[kTile];
-  unsigned char flags[kTile];    // 1: first row of its sequence, 2: last, 4: of a sequence
+  uint64_t start, last, live;    // first row of its sequence, last one, of a sequence at all
   int64_t bos, eos;              // of the first row's sequence, of the last row's
 };
-__device__ __forceinline__ void find_rows(TileRows& s, const LinrecParams& p, int64_t row0) {
-  if (threadIdx.x < kTile) {
-    const int64_t t = row0 + threadIdx.x;
+__device__ __forceinline__ void find_rows(TileRows& s, const LinrecParams& p, int64_t row0, int lane) {
+  static_assert(kTile == 64, "two rows per lane, a bit each");
+  uint64_t start = 0, last = 0, alive = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t t = row0 + 32 * h + lane;
     int n = 0;
     int64_t bos = 0, eos = 0;
     const bool live = row_sequence(p, t, n, bos, eos);
-    s.n[threadIdx.x] = n;
-    s.flags[threadIdx.x] = live ? 4 | (t == bos ? 1 : 0) | (t + 1 == eos ? 2 : 0) : 0;
-    if (threadIdx.x == 0) s.bos = bos;
-    if (threadIdx.x == kTile - 1) s.eos = eos;
+    s.n[32 * h + lane] = n;
+    start |= (uint64_t)__ballot_sync(0xffffffffu, live && t == bos) << (32 * h);
+    last |= (uint64_t)__ballot_sync(0xffffffffu, live && t + 1 == eos) << (32 * h);
+    alive |= (uint64_t)__ballot_sync(0xffffffffu, live) << (32 * h);
+    if (h == 0 && lane == 0) s.bos = bos;
+    if (h == 1 && lane == 31) s.eos = eos;
   }
+  if (lane == 0) s.start = start, s.last = last, s.live = alive;
 }
-__device__ __forceinline__ RowBits warp_rows(const TileRows& s, int warp, int lane) {
-  const unsigned f = lane < kRows ? s.flags[warp * kRows + lane] : 0u;
-  RowBits b;
-  b.start = __ballot_sync(0xffffffffu, f & 1);
-  b.last = __ballot_sync(0xffffffffu, f & 2);
-  b.live = __ballot_sync(0xffffffffu, f & 4);
-  return b;
+// A run's rows: bit j for row j.
+struct RowBits {
+  unsigned start, last, live;
+};
+__device__ __forceinline__ RowBits run_rows(const TileRows& s, int warp) {
+  constexpr unsigned mask = (1u << kRows) - 1;
+  return {(unsigned)(s.start >> (warp * kRows)) & mask, (unsigned)(s.last >> (warp * kRows)) & mask,
+          (unsigned)(s.live >> (warp * kRows)) & mask};
 }
 
-// What a value's gates and step need of its channel, in the form that Gates<T> takes.
-template <int V>
-struct Gates {
-  Vals<V> A2, cr, ci;
-};
 constexpr float kBiasScale16 = -kLog2e, kBiasScale32 = 1.f;
 template <typename T, int V>
 __device__ __forceinline__ void load_gates(Gates<V>& c, const LinrecParams& p, int ch, bool ok) {
@@ -261,23 +320,38 @@ __device__ __forceinline__ Vals<V> silu_of(const Vals<V>& z) {
 
 // The runs of a tile, joined by one thread per channel.
 template <int V>
-struct TileShared {
-  float P[kWarps][32 * V], H[kWarps][32 * V];  // what each run does to a state
-  float S[kWarps][32 * V];                     // the state before each run
+struct Runs {
+  float P[kWarps][32 * V], H[kWarps][32 * V];  // what each run does to a state; H then holds
+                                               // the state before it
   unsigned char cut[kWarps];                   // whether a run holds a sequence's start
-  int tile, block;                             // the tile at work, in the order of the walk
 };
-
-// The unit of work that `ticket` stands for: rows' tile first, all channel blocks of one before
+// The unit of work that a ticket stands for: rows' tile first, all channel blocks of one before
 // the next.  A batch of sequences that are whole tiles is walked a tile of each in turn: a tile
 // then rarely waits for the one before it (8 x 4,096 tokens of 4,096 channels 379 us without,
 // 311 with it).
+struct Unit {
+  int tile, block;                             // the tile in the order of the walk; -1: none
+};
+__device__ __forceinline__ Unit unit_of(const LinrecParams& p, unsigned ticket) {
+  const unsigned blocks = p.blocks, w = ticket / blocks, q = w / p.strips;
+  return {ticket < p.units ? (int)((w - q * p.strips) * p.strip_tiles + q) : -1, (int)(ticket - w * blocks)};
+}
+// What a block's warps share.  This turn's unit and rows and the next one's alternate, so that
+// two barriers a turn are enough: the runs are there, and the states before them are.
 template <int V>
-__device__ __forceinline__ void set_unit(const LinrecParams& p, TileShared<V>& sh, unsigned ticket) {
-  const unsigned blocks = p.blocks, w = ticket / blocks;
-  sh.block = (int)(ticket - w * blocks);
-  const unsigned q = w / p.strips;
-  sh.tile = ticket < p.units ? (int)((w - q * p.strips) * p.strip_tiles + q) : -1;
+struct BlockShared {
+  Runs<V> runs;
+  TileRows rows[2];
+  Unit unit[3];
+};
+// The first turn's unit and rows.
+template <int V, bool FORWARD>
+__device__ __forceinline__ void start_block(const LinrecParams& p, BlockShared<V>& sh, int warp, int lane) {
+  if (threadIdx.x < 2) sh.unit[threadIdx.x] = unit_of(p, atomicAdd(p.ticket, 1u));
+  __syncthreads();
+  const int64_t s = sh.unit[0].tile;
+  if (warp == 0 && s >= 0) find_rows(sh.rows[0], p, (FORWARD ? s : p.tiles - 1 - s) * kTile, lane);
+  __syncthreads();
 }
 template <int V>
 __device__ __forceinline__ void put(float (&at)[32 * V], int lane, const Vals<V>& v) {
@@ -335,7 +409,7 @@ __device__ __forceinline__ float stepped(uint64_t w, float X) {
 
 // X taken through tiles from .. to - 1.
 __device__ __forceinline__ float through_tiles(const LinrecParams& p, float X, int64_t from, int64_t to, int ch) {
-  constexpr int kBatch = 8;
+  constexpr int kBatch = 4;
   const uint64_t* at = p.agg + from * p.dim + ch;
 #pragma unroll 1
   for (int left = (int)(to - from); left > 0; left -= kBatch, at += kBatch * (int64_t)p.dim) {
@@ -355,7 +429,7 @@ __device__ __forceinline__ float through_tiles(const LinrecParams& p, float X, i
 // The state at the end of group g, in a sequence that starts in group `edge` or before the
 // window: that of the nearest group which has published one (the window's last is waited
 // for), taken through the groups since then.
-constexpr int kWindow = 8;
+constexpr int kWindow = 4;
 __device__ __forceinline__ float state_after_group(const LinrecParams& p, int64_t g, int64_t edge, int ch) {
   const int64_t dim = p.dim;
   const unsigned* const ends = p.ends + (g * kGroup + kGroup - 1) * dim + ch;
@@ -439,7 +513,7 @@ __device__ __forceinline__ float state_before(const LinrecParams& p, int64_t s, 
 // One channel of a tile: its runs joined, published, and the state before each.
 // FORWARD: runs in the order of their rows.  `carry`: the tile's first row goes on.
 template <int V, bool FORWARD>
-__device__ __forceinline__ float join_runs(const LinrecParams& p, TileShared<V>& sh, int64_t s, int64_t edge, int c,
+__device__ __forceinline__ float join_runs(const LinrecParams& p, Runs<V>& sh, int64_t s, int64_t edge, int c,
                                            int ch, bool carry) {
   static_assert(kWarps == 8, "eight flags in one word");
   const uint64_t cuts = *reinterpret_cast<const uint64_t*>(sh.cut);
@@ -466,56 +540,114 @@ __device__ __forceinline__ float join_runs(const LinrecParams& p, TileShared<V>&
 #pragma unroll
   for (int q = 0; q < kWarps; ++q) {
     const int w = FORWARD ? q : kWarps - 1 - q;
-    sh.S[w][c] = S;
+    sh.H[w][c] = S;
     S = cuts >> (8 * w) & 1 ? Hw[q] : fmaf(Pw[q], S, Hw[q]);
   }
   return X;
 }
 
 // ---------------------------------------------------------------- forward --
-template <typename T, int V, bool OUT>
-__global__ void __launch_bounds__(32 * kWarps, 2) linrec_fwd_kernel(LinrecParams p) {
-  constexpr int R = kRows;
-  __shared__ TileRows rows_s;
-  __shared__ __align__(16) TileShared<V> sh;
+// TMA: rows come by tensor maps, one copy per run and array (16-byte aligned rows); else each
+// lane copies its own.  A warp asks for the next tile's rows as soon as it has read this one's.
+struct LinrecMaps {
+  CUtensorMap x, r, i, z;
+};
+template <typename T, int V, bool OUT, bool TMA>
+__global__ void __launch_bounds__(32 * kWarps, 2)
+    linrec_fwd_kernel(const __grid_constant__ LinrecParams p, const __grid_constant__ LinrecMaps maps) {
+  constexpr int R = kRows, CH = 32 * V;
+  using S = Slots<T, V>;
+  extern __shared__ __align__(128) uint8_t slots[];  // x, r, i, z
+  __shared__ __align__(16) BlockShared<V> sh;
+  __shared__ uint64_t full[2][kWarps];               // x, r, i are there; z is
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (threadIdx.x == 0) set_unit(p, sh, atomicAdd(p.ticket, 1u));
-  __syncthreads();
-  while (sh.tile >= 0) {
-    const int64_t s = sh.tile;
-    const int c0 = sh.block * 32 * V, ch = c0 + lane * V;
-    const bool ok = ch < p.dim;
-    const int64_t row0 = s * kTile + warp * R;
-    unsigned next = 0;
-    if (threadIdx.x == 0) next = atomicAdd(p.ticket, 1u);
-    const int n = ok ? (int)min((int64_t)R, p.total - row0) : 0;  // rows that exist
-    Raw<T, V> rx[R], rr[R], ri[R], rz[R];
-    Gates<V> c = {};
-    if (n == R) {
-      load_run<false>(rx, p.x, row0, p.x_s, ch, n);
-      load_run<false>(rr, p.r, row0, p.r_s, ch, n);
-      load_run<false>(ri, p.i, row0, p.i_s, ch, n);
+  if (TMA && threadIdx.x < 2 * kWarps) {
+    ptx::mbar_init(&full[0][threadIdx.x], 1);
+    ptx::fence_mbar_init();
+  }
+  start_block<V, true>(p, sh, warp, lane);
+  uint8_t* const run = slots + warp * S::kRun;
+  const uint8_t* const mine = run + lane * S::kBytes;
+  auto place = [&](const Unit& u, int64_t& row0, int& ch) {  // the rows that exist
+    row0 = (int64_t)u.tile * kTile + warp * R;
+    ch = u.block * CH + lane * V;
+    return ch < p.dim && u.tile >= 0 ? (int)max((int64_t)0, min((int64_t)R, p.total - row0)) : 0;
+  };
+  auto copy = [&](const Unit& u) {
+    if constexpr (TMA) {
+      if (u.tile >= 0 && lane == 0) {
+        const int row0 = u.tile * kTile + warp * R, c0 = u.block * CH;
+        ptx::mbar_arrive_expect_tx(&full[0][warp], 3 * S::kRun);
+        ptx::tma_load_2d(run, &maps.x, &full[0][warp], c0, row0);
+        ptx::tma_load_2d(run + S::kArray, &maps.r, &full[0][warp], c0, row0);
+        ptx::tma_load_2d(run + 2 * S::kArray, &maps.i, &full[0][warp], c0, row0);
+      }
     } else {
-      load_run<true>(rx, p.x, row0, p.x_s, ch, n);
-      load_run<true>(rr, p.r, row0, p.r_s, ch, n);
-      load_run<true>(ri, p.i, row0, p.i_s, ch, n);
+      if (u.tile >= 0) {
+        int64_t row0;
+        int ch;
+        const int n = place(u, row0, ch);
+        const uint32_t at = ptx::smem_u32(mine);
+        S::copy(at, p.x, row0, p.x_s, ch, n);
+        S::copy(at + S::kArray, p.r, row0, p.r_s, ch, n);
+        S::copy(at + 2 * S::kArray, p.i, row0, p.i_s, ch, n);
+      }
+      ptx::cp_async_commit();
     }
-    if (ok) read_gates(c, p, ch);
-    find_rows(rows_s, p, s * kTile);
-    __syncthreads();
-    const RowBits bits = warp_rows(rows_s, warp, lane);
+  };
+  auto copy_z = [&](const Unit& u) {
+    const bool want = OUT && p.z && u.tile >= 0;
+    if constexpr (TMA) {
+      if (want && lane == 0) {
+        ptx::mbar_arrive_expect_tx(&full[1][warp], S::kRun);
+        ptx::tma_load_2d(run + 3 * S::kArray, &maps.z, &full[1][warp], u.block * CH, u.tile * kTile + warp * R);
+      }
+    } else {
+      if (want) {
+        int64_t row0;
+        int ch;
+        const int n = place(u, row0, ch);
+        S::copy(ptx::smem_u32(mine) + 3 * S::kArray, p.z, row0, p.z_s, ch, n);
+      }
+      ptx::cp_async_commit();
+    }
+  };
+  auto arrived = [&](int which, unsigned turn) {
+    if constexpr (TMA) {
+      if (!ptx::mbar_wait(&full[which][warp], turn & 1, kWaitNs)) atomicOr(p.status, kDevStatusTimeout);
+    } else {
+      ptx::cp_async_wait<1>();
+    }
+  };
+  copy(sh.unit[0]);
+  copy_z(sh.unit[0]);
+  for (unsigned turn = 0, slot = 0;; ++turn, slot = slot == 2 ? 0 : slot + 1) {
+    const Unit unit = sh.unit[slot];
+    if (unit.tile < 0) break;
+    const int64_t s = unit.tile;
+    const int c0 = unit.block * CH;
+    int64_t row0;
+    int ch;
+    const bool ok = place(unit, row0, ch) > 0;
+    unsigned ticket = 0;
+    if (threadIdx.x == 32 * kWarps - 32) ticket = atomicAdd(p.ticket, 1u);
+    const TileRows& rows = sh.rows[turn & 1];
+    const RowBits bits = run_rows(rows, warp);
+    Gates<V> c = {};
+    if (ch < p.dim) read_gates(c, p, ch);
+    arrived(0, turn);
     Vals<V> a[R], b[R];
 #pragma unroll
-    for (int j = 0; j < R; ++j) step_of<T>(vals_of(rx[j]), vals_of(rr[j]), vals_of(ri[j]), c, a[j], b[j]);
+    for (int j = 0; j < R; ++j)
+      step_of<T>(S::get(mine, j), S::get(mine + S::kArray, j), S::get(mine + 2 * S::kArray, j), c, a[j], b[j]);
     if (bits.start && p.init) {  // a sequence's first step starts from its initial state
-      float h0[R][V];
 #pragma unroll
       for (int j = 0; j < R; ++j)
-        if (ok && (bits.start >> j & 1))
-          load_state<V>(h0[j], p.init, (int64_t)rows_s.n[warp * R + j] * p.dim + ch, p.state_bf16);
-#pragma unroll
-      for (int j = 0; j < R; ++j)
-        if (ok && (bits.start >> j & 1)) b[j] = fma_of(a[j], vals_from(h0[j]), b[j]);
+        if (ok && (bits.start >> j & 1)) {
+          float h0[V];
+          load_state<V>(h0, p.init, (int64_t)rows.n[warp * R + j] * p.dim + ch, p.state_bf16);
+          b[j] = fma_of(a[j], vals_from(h0), b[j]);
+        }
     }
     // what the run does to a state
     Vals<V> P = a[0], h = b[0];
@@ -526,29 +658,33 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_fwd_kernel(LinrecParams
 #pragma unroll
       for (int j = 1; j < R; ++j) h = bits.start >> j & 1 ? b[j] : fma_of(a[j], h, b[j]);
     }
-    put<V>(sh.P[warp], lane, P);
-    put<V>(sh.H[warp], lane, h);
-    if (lane == 0) sh.cut[warp] = bits.start != 0;
-    if (OUT && p.z) {
-      if (n == R) load_run<false>(rz, p.z, row0, p.z_s, ch, n);
-      else load_run<true>(rz, p.z, row0, p.z_s, ch, n);
-    }
+    put<V>(sh.runs.P[warp], lane, P);
+    put<V>(sh.runs.H[warp], lane, h);
+    if (lane == 0) sh.runs.cut[warp] = bits.start != 0;
+    __syncwarp();
+    const Unit next = sh.unit[slot == 2 ? 0 : slot + 1];
+    copy(next);
     __syncthreads();
-    if (threadIdx.x < 32 * V && c0 + (int)threadIdx.x < p.dim) {
-      const unsigned char f0 = rows_s.flags[0];
-      const float X = join_runs<V, true>(p, sh, s, rows_s.bos / kTile, threadIdx.x, c0 + threadIdx.x,
-                                         (f0 & 4) && !(f0 & 1) && s > 0);
+    if (threadIdx.x < CH && c0 + (int)threadIdx.x < p.dim) {
+      const float X = join_runs<V, true>(p, sh.runs, s, rows.bos / kTile, threadIdx.x, c0 + threadIdx.x,
+                                         (rows.live & 1) && !(rows.start & 1) && s > 0);
       if (p.states) p.states[s * p.dim + c0 + threadIdx.x] = X;
     }
+    if (warp == kWarps - 1) {  // meanwhile: the next turn's rows, and the unit after that
+      if (next.tile >= 0) find_rows(sh.rows[(turn + 1) & 1], p, (int64_t)next.tile * kTile, lane);
+      const Unit u = unit_of(p, __shfl_sync(0xffffffffu, ticket, 0));
+      if (lane == 0) sh.unit[slot == 0 ? 2 : slot - 1] = u;
+    }
+    __syncthreads();
     if constexpr (OUT) {
-      __syncthreads();
-      h = get<V>(sh.S[warp], lane);
-      char* const at = reinterpret_cast<char*>(static_cast<T*>(p.out) + row0 * p.dim + ch);
+      if (p.z) arrived(1, turn);
+      h = get<V>(sh.runs.H[warp], lane);
+      char* const to = reinterpret_cast<char*>(static_cast<T*>(p.out) + row0 * p.dim + ch);
       auto put_row = [&](int j) {
         float y[V];
-        if (p.z) vals_to(mul_of(h, silu_of<T>(vals_of(rz[j]))), y);
+        if (p.z) vals_to(mul_of(h, silu_of<T>(S::get(mine + 3 * S::kArray, j))), y);
         else vals_to(h, y);
-        store_vals<T, V>(at + (uint64_t)(uint32_t)p.dim * (uint32_t)(j * sizeof(T)), 0, y);
+        store_vals<T, V>(to + (uint64_t)(uint32_t)p.dim * (uint32_t)(j * sizeof(T)), 0, y);
       };
       if (!ok) {
       } else if (!bits.start && !bits.last && bits.live == (1u << R) - 1) {
@@ -560,22 +696,21 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_fwd_kernel(LinrecParams
       } else {
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-          const bool cut = bits.start >> j & 1;
-          h = cut ? b[j] : fma_of(a[j], h, b[j]);
+          h = bits.start >> j & 1 ? b[j] : fma_of(a[j], h, b[j]);
           if (!(bits.live >> j & 1)) continue;
           put_row(j);
           if (p.fin && (bits.last >> j & 1)) {
             float f[V];
             vals_to(h, f);
-            store_state<V>(p.fin, (int64_t)rows_s.n[warp * R + j] * p.dim + ch, f, p.state_bf16);
+            store_state<V>(p.fin, (int64_t)rows.n[warp * R + j] * p.dim + ch, f, p.state_bf16);
           }
         }
       }
+      __syncwarp();
     }
-    __syncthreads();
-    if (threadIdx.x == 0) set_unit(p, sh, next);
-    __syncthreads();
+    copy_z(next);
   }
+  if constexpr (!TMA) ptx::cp_async_wait_all();
 }
 
 // Single tokens and prompts of a few: a thread takes the channels of one sequence.
@@ -660,53 +795,75 @@ __device__ __forceinline__ void store_of(void* p, int64_t at, const Vals<V>& v) 
 template <typename T, int V>
 __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams p) {
   constexpr int R = kRows, CH = 32 * V;
-  __shared__ TileRows rows_s;
-  __shared__ __align__(16) TileShared<V> sh, fw;  // of the gradients (last run first), of the states
+  using S = Slots<T, V>;
+  constexpr int kBuffer = 5 * S::kArray + S::kGates;  // x, r, i, dout, z, gates; two by turns
+  extern __shared__ __align__(16) uint8_t slots[];
+  __shared__ __align__(16) BlockShared<V> sh;         // runs of the gradients, last run first
+  __shared__ __align__(16) Runs<V> fw;                // of the states; the products are shared
   __shared__ __align__(16) float sums[3][kWarps][CH];
-  static_assert(2 * CH <= 32 * kWarps, "a thread per channel for each of the two joins");
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (threadIdx.x == 0) set_unit(p, sh, atomicAdd(p.ticket, 1u));
-  __syncthreads();
-  while (sh.tile >= 0) {
-    const int64_t s = sh.tile;                    // counted from the last tile back
-    const int64_t tile = p.tiles - 1 - s;
-    const int c0 = sh.block * CH, ch = c0 + lane * V;
-    const bool ok = ch < p.dim;
-    const int64_t row0 = tile * kTile + warp * R;
-    unsigned next = 0;
-    if (threadIdx.x == 0) next = atomicAdd(p.ticket, 1u);
-    const int n = ok ? (int)min((int64_t)R, p.total - row0) : 0;  // rows that exist
-    Raw<T, V> rx[R], rr[R], ri[R], rd[R], rz[R];
-    Gates<V> c = {};
-    if (n == R) {
-      load_run<false>(rx, p.x, row0, p.x_s, ch, n);
-      load_run<false>(rr, p.r, row0, p.r_s, ch, n);
-      load_run<false>(ri, p.i, row0, p.i_s, ch, n);
-      load_run<false>(rd, p.dout, row0, p.dim, ch, n);
-      if (p.z) load_run<false>(rz, p.z, row0, p.z_s, ch, n);
-    } else {
-      load_run<true>(rx, p.x, row0, p.x_s, ch, n);
-      load_run<true>(rr, p.r, row0, p.r_s, ch, n);
-      load_run<true>(ri, p.i, row0, p.i_s, ch, n);
-      load_run<true>(rd, p.dout, row0, p.dim, ch, n);
-      if (p.z) load_run<true>(rz, p.z, row0, p.z_s, ch, n);
+  start_block<V, false>(p, sh, warp, lane);
+  static_assert(2 * CH <= 32 * (kWarps - 2), "a thread per channel for each of the two joins");
+  const uint8_t* const mine0 = slots + warp * S::kRun + lane * S::kBytes;
+  const uint32_t at0 = ptx::smem_u32(mine0), at_gates0 = ptx::smem_u32(slots + 5 * S::kArray + threadIdx.x * V * 4);
+  auto place = [&](const Unit& u, int64_t& row0, int& ch) {  // the rows that exist
+    row0 = (p.tiles - 1 - u.tile) * kTile + warp * R;
+    ch = u.block * CH + lane * V;
+    return ch < p.dim ? (int)max((int64_t)0, min((int64_t)R, p.total - row0)) : 0;
+  };
+  auto copy = [&](const Unit& u, unsigned turn) {
+    if (u.tile >= 0) {
+      int64_t row0;
+      int ch;
+      const int n = place(u, row0, ch);
+      const uint32_t at = at0 + (turn & 1) * kBuffer;
+      S::copy(at, p.x, row0, p.x_s, ch, n);
+      S::copy(at + S::kArray, p.r, row0, p.r_s, ch, n);
+      S::copy(at + 2 * S::kArray, p.i, row0, p.i_s, ch, n);
+      S::copy(at + 3 * S::kArray, p.dout, row0, p.dim, ch, n);
+      if (p.z) S::copy(at + 4 * S::kArray, p.z, row0, p.z_s, ch, n);
+      S::copy_gates(at_gates0 + (turn & 1) * kBuffer, p.gates, p.dim, ch, ch < p.dim);
     }
-    if (ok) read_gates(c, p, ch);
-    find_rows(rows_s, p, tile * kTile);
-    __syncthreads();
-    const RowBits bits = warp_rows(rows_s, warp, lane);
-    if (bits.live != (1u << R) - 1) {  // rows of no sequence count for nothing
+    ptx::cp_async_commit();
+  };
+  // the sums over a tile's rows, by a warp that has nothing else to do in the turn after
+  int64_t last_tile = -1;
+  int last_c0 = 0;
+  auto add_runs = [&](int64_t tile, int c0) {
+    for (int q = lane; q < 3 * CH; q += 32) {
+      const int w = q / CH, k = q % CH;
+      float v = 0.f;
 #pragma unroll
-      for (int j = 0; j < R; ++j)
-        if (!(bits.live >> j & 1)) rx[j] = {}, rr[j] = {}, ri[j] = {}, rd[j] = {}, rz[j] = {};
+      for (int e = 0; e < kWarps; ++e) v += sums[w][e][k];
+      if (c0 + k < p.dim) p.part[(tile * 3 + w) * p.dim + c0 + k] = v;
     }
+  };
+  copy(sh.unit[0], 0);
+  for (unsigned turn = 0;; ++turn) {
+    const Unit unit = sh.unit[turn % 3];
+    if (unit.tile < 0) break;
+    const int64_t s = unit.tile, tile = p.tiles - 1 - s;  // s: counted from the last tile back
+    const int c0 = unit.block * CH;
+    int64_t row0;
+    int ch;
+    const int n = place(unit, row0, ch);
+    const bool ok = n > 0;
+    const TileRows& rows = sh.rows[turn & 1];
+    const RowBits bits = run_rows(rows, warp);
+    const uint8_t* const mine = mine0 + (turn & 1) * kBuffer;
+    ptx::cp_async_wait_all();
+    Gates<V> c;
+    S::gates(c, slots + 5 * S::kArray + threadIdx.x * V * 4 + (turn & 1) * kBuffer);
+    const bool all = bits.live == (1u << R) - 1;
+    // rows of no sequence count for nothing
+    auto row = [&](int k, int j) { return all || (bits.live >> j & 1) ? S::get(mine + k * S::kArray, j) : splat<V>(0.f); };
     Vals<V> a[R], b[R], dy[R], dq[R];  // dq: dout silu'(z), what dz takes times h
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      step_of<T>(vals_of(rx[j]), vals_of(rr[j]), vals_of(ri[j]), c, a[j], b[j]);
-      dy[j] = vals_of(rd[j]);
+      step_of<T>(row(0, j), row(1, j), row(2, j), c, a[j], b[j]);
+      dy[j] = row(3, j);
       if (p.z) {
-        const Vals<V> z = vals_of(rz[j]), q = sigmoid<T>(z);
+        const Vals<V> z = row(4, j), q = sigmoid<T>(z);
         // silu' = q + z q (1 - q)
         dq[j] = mul_of(dy[j], fma_of(mul_of(z, q), fma_of(q, splat<V>(-1.f), splat<V>(1.f)), q));
         dy[j] = mul_of(dy[j], mul_of(z, q));
@@ -714,7 +871,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
     }
     auto initial = [&](int j) {
       float h0[V] = {};
-      if (p.init && ok) load_state<V>(h0, p.init, (int64_t)rows_s.n[warp * R + j] * p.dim + ch, p.state_bf16);
+      if (p.init && ok) load_state<V>(h0, p.init, (int64_t)rows.n[warp * R + j] * p.dim + ch, p.state_bf16);
       return vals_from(h0);
     };
     // what the run does to a state
@@ -725,44 +882,51 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
       h = fma_of(a[j], h, b[j]);
       P = mul_of(P, a[j]);
     }
-    put<V>(fw.P[warp], lane, P);
     put<V>(fw.H[warp], lane, h);
     if (bits.last && p.dfin && ok) {  // the final state's gradient joins the last row's
 #pragma unroll
       for (int j = 0; j < R; ++j)
         if (bits.last >> j & 1) {
           float d[V];
-          load_state<V>(d, p.dfin, (int64_t)rows_s.n[warp * R + j] * p.dim + ch, p.state_bf16);
+          load_state<V>(d, p.dfin, (int64_t)rows.n[warp * R + j] * p.dim + ch, p.state_bf16);
           dy[j] = add_of(dy[j], vals_from(d));
         }
     }
     // and to a gradient
     h = splat<V>(0.f);
 #pragma unroll
-    for (int j = R - 1; j >= 0; --j) {
-      const bool cut = bits.last >> j & 1;
-      h = mul_of(a[j], cut ? dy[j] : add_of(h, dy[j]));
-    }
-    put<V>(sh.P[warp], lane, P);
-    put<V>(sh.H[warp], lane, h);
-    if (lane == 0) sh.cut[warp] = bits.last != 0, fw.cut[warp] = bits.start != 0;
+    for (int j = R - 1; j >= 0; --j) h = mul_of(a[j], bits.last >> j & 1 ? dy[j] : add_of(h, dy[j]));
+    unsigned ticket = 0;
+    if (threadIdx.x == 32 * kWarps - 32) ticket = atomicAdd(p.ticket, 1u);
+    put<V>(sh.runs.P[warp], lane, P);
+    put<V>(sh.runs.H[warp], lane, h);
+    if (lane == 0) sh.runs.cut[warp] = bits.last != 0, fw.cut[warp] = bits.start != 0;
     __syncthreads();
-    if (threadIdx.x < CH && c0 + (int)threadIdx.x < p.dim) {
-      const unsigned char f = rows_s.flags[kTile - 1];
-      join_runs<V, false>(p, sh, s, p.tiles - 1 - (rows_s.eos - 1) / kTile, threadIdx.x, c0 + threadIdx.x,
-                          (f & 4) && !(f & 2) && s > 0);
-    } else if (threadIdx.x >= 128 && threadIdx.x < 128 + CH && c0 + (int)threadIdx.x - 128 < p.dim) {
-      const int k = threadIdx.x - 128;
-      float S = __ldg(p.states + tile * p.dim + c0 + k);
+    if (threadIdx.x < CH) {
+      if (c0 + (int)threadIdx.x < p.dim)
+        join_runs<V, false>(p, sh.runs, s, p.tiles - 1 - (rows.eos - 1) / kTile, threadIdx.x, c0 + threadIdx.x,
+                            (rows.live >> (kTile - 1)) && !(rows.last >> (kTile - 1)) && s > 0);
+    } else if (threadIdx.x < 2 * CH) {
+      const int k = threadIdx.x - CH;
+      float S = c0 + k < p.dim ? p.states[tile * p.dim + c0 + k] : 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        fw.S[w][k] = S;
-        S = fw.cut[w] ? fw.H[w][k] : fmaf(fw.P[w][k], S, fw.H[w][k]);
+        const float H = fw.H[w][k];
+        fw.H[w][k] = S;
+        S = fw.cut[w] ? H : fmaf(sh.runs.P[w][k], S, H);
       }
+    } else if (warp == kWarps - 1) {  // meanwhile: the next turn's unit and rows
+      const Unit next = sh.unit[(turn + 1) % 3];
+      if (next.tile >= 0) find_rows(sh.rows[(turn + 1) & 1], p, (p.tiles - 1 - next.tile) * kTile, lane);
+      const Unit u = unit_of(p, __shfl_sync(0xffffffffu, ticket, 0));
+      if (lane == 0) sh.unit[(turn + 2) % 3] = u;
     }
+    if (warp == kWarps - 2 && turn > 0) add_runs(last_tile, last_c0);
     __syncthreads();
+    copy(sh.unit[(turn + 1) % 3], turn + 1);
     // states again, b <- the one before each row; dz
-    h = get<V>(fw.S[warp], lane);
+    const int64_t row_at = row0 * p.dim + ch;
+    h = get<V>(fw.H[warp], lane);
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       if (bits.start >> j & 1) h = initial(j);
@@ -770,44 +934,38 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
       h = fma_of(a[j], h, b[j]);
       b[j] = before;
       if (p.z && j < n)
-        store_of<T>(p.dz, row0 * p.dim + ch + (uint64_t)(uint32_t)p.dim * (uint32_t)j, bits.live >> j & 1 ? mul_of(dq[j], h) : splat<V>(0.f));
+        store_of<T>(p.dz, row_at + (uint64_t)(uint32_t)p.dim * (uint32_t)j,
+                    bits.live >> j & 1 ? mul_of(dq[j], h) : splat<V>(0.f));
     }
-    Vals<V> C = get<V>(sh.S[warp], lane);
-    const int64_t row_at = row0 * p.dim + ch;
+    Vals<V> C = get<V>(sh.runs.H[warp], lane);
     Vals<V> se = splat<V>(0.f), sr = se, si = se;
 #pragma unroll
     for (int j = R - 1; j >= 0; --j) {
       Vals<V> e, dx, dr, di;
       C = bits.last >> j & 1 ? dy[j] : add_of(C, dy[j]);
-      grads_of<T>(vals_of(rx[j]), vals_of(rr[j]), vals_of(ri[j]), c, a[j], b[j], C, e, dx, dr, di);
+      grads_of<T>(row(0, j), row(1, j), row(2, j), c, a[j], b[j], C, e, dx, dr, di);
       if (!(bits.live >> j & 1)) e = dx = dr = di = splat<V>(0.f);
       se = add_of(se, e), sr = add_of(sr, dr), si = add_of(si, di);
       if (j < n) {
-        const int64_t at = row_at + (uint64_t)(uint32_t)p.dim * (uint32_t)j;
-        store_of<T>(p.dx, at, dx);
-        store_of<T>(p.dr, at, dr);
-        store_of<T>(p.di, at, di);
+        const int64_t to = row_at + (uint64_t)(uint32_t)p.dim * (uint32_t)j;
+        store_of<T>(p.dx, to, dx);
+        store_of<T>(p.dr, to, dr);
+        store_of<T>(p.di, to, di);
         if (p.dinit && (bits.start >> j & 1)) {
           float f[V];
           vals_to(C, f);
-          store_state<V>(p.dinit, (int64_t)rows_s.n[warp * R + j] * p.dim + ch, f, false);
+          store_state<V>(p.dinit, (int64_t)rows.n[warp * R + j] * p.dim + ch, f, false);
         }
       }
     }
     put<V>(sums[0][warp], lane, se);
     put<V>(sums[1][warp], lane, sr);
     put<V>(sums[2][warp], lane, si);
-    __syncthreads();
-    if (threadIdx.x == 0) set_unit(p, sh, next);
-    for (int q = threadIdx.x; q < 3 * CH; q += 32 * kWarps) {
-      const int w = q / CH, l = q % CH;
-      float v = 0.f;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) v += sums[w][k][l];
-      if (c0 + l < p.dim) p.part[(tile * 3 + w) * p.dim + c0 + l] = v;
-    }
-    __syncthreads();
+    last_tile = tile, last_c0 = c0;
   }
+  __syncthreads();
+  if (warp == kWarps - 2 && last_tile >= 0) add_runs(last_tile, last_c0);
+  ptx::cp_async_wait_all();
 }
 
 // Before a pass: what is published is unset, the counters are zero, cu_seqlens is checked
@@ -870,8 +1028,9 @@ kda_status check_sizes(const kda_linrec_problem* q, LinrecParams& p) {
   return KDA_OK;
 }
 
-// `lanes`: the channels that a thread can read at a time, 1, 2 or 4, by the rows' alignment.
-kda_status check_linrec(const kda_linrec_problem* q, LinrecParams& p, int& lanes) {
+// `lanes`: the channels that a thread can read at a time, 1, 2 or 4, by the rows' alignment;
+// `tma`: whether tensor maps can describe them.
+kda_status check_linrec(const kda_linrec_problem* q, LinrecParams& p, int& lanes, bool& tma) {
   const kda_status sizes = check_sizes(q, p);
   if (sizes != KDA_OK) return sizes;
   if (!q->A_log) return KDA_ERR_NULL_POINTER;
@@ -884,11 +1043,12 @@ kda_status check_linrec(const kda_linrec_problem* q, LinrecParams& p, int& lanes
     return KDA_ERR_INVALID_ARG;
   if (p.total > 0 && (!q->x || !q->r || !q->i)) return KDA_ERR_NULL_POINTER;
   const size_t e = q->dtype == KDA_ROW_FP32 ? 4 : 2, se = q->state_dtype == KDA_STATE_FP32 ? 4 : 2;
-  lanes = 4;
+  lanes = 4, tma = true;
   while (lanes > 1 && q->dim % lanes) lanes /= 2;
   for (int k = 0; k < 4; ++k) {
     if (!al_to(row[k], e)) return KDA_ERR_MISALIGNED;
     while (lanes > 1 && (!al_to(row[k], lanes * e) || stride[k] % lanes)) lanes /= 2;
+    tma = tma && al_to(row[k], 16) && stride[k] * e % 16 == 0;
   }
   if (!al_to(q->A_log, 4) || !al_to(q->r_bias, 4) || !al_to(q->i_bias, 4) ||
       !al_to(q->initial_state, se) || !al_to(q->cu_seqlens, 8))
@@ -935,13 +1095,56 @@ cudaError_t launch_setup(const LinrecParams& p, bool f32, void* words, size_t by
 }
 
 template <typename K>
-cudaError_t launch_tiles(K kernel, const LinrecParams& p, cudaStream_t stream) {
+cudaError_t launch_tiles(K kernel, bool (&done)[64], int smem, int blocks, const LinrecParams& p, cudaStream_t stream) {
   int sms = 0;
   if (sm_count(&sms) != KDA_OK) return cudaErrorUnknown;
-  const int64_t units = p.tiles * p.blocks, most = 2 * (int64_t)sms;
-  kernel<<<(unsigned)(units < most ? units : most), 32 * kWarps, 0, stream>>>(p);
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem, done);
+  if (e != cudaSuccess) return e;
+  kernel<<<std::min(p.units, (unsigned)(blocks * sms)), 32 * kWarps, smem, stream>>>(p);
   return cudaGetLastError();
 }
+template <typename T>
+cudaError_t rows_map(CUtensorMap* m, const void* p, const LinrecParams& q, uint32_t stride, int channels) {
+  const uint64_t dims[2] = {(uint64_t)q.dim, (uint64_t)q.total}, strides[1] = {(uint64_t)stride * sizeof(T)};
+  const uint32_t box[2] = {(uint32_t)channels, (uint32_t)kRows};
+  return encode_tiled_map(m, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p,
+                          dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+template <typename T, int V, bool OUT>
+cudaError_t launch_fwd_of(const LinrecParams& p, bool tma, cudaStream_t stream) {
+  LinrecMaps maps;
+  const int smem = (p.z && OUT ? 4 : 3) * Slots<T, V>::kArray;
+  int sms = 0;
+  if (sm_count(&sms) != KDA_OK) return cudaErrorUnknown;
+  const unsigned grid = std::min(p.units, 2u * sms);
+  cudaError_t e = cudaSuccess;
+  if constexpr (V * sizeof(T) == 8) {
+    if (tma) {
+      static bool done[64];
+      e = rows_map<T>(&maps.x, p.x, p, p.x_s, 32 * V);
+      if (e == cudaSuccess) e = rows_map<T>(&maps.r, p.r, p, p.r_s, 32 * V);
+      if (e == cudaSuccess) e = rows_map<T>(&maps.i, p.i, p, p.i_s, 32 * V);
+      if (e == cudaSuccess) e = rows_map<T>(&maps.z, p.z, p, p.z_s, 32 * V);
+      auto kernel = linrec_fwd_kernel<T, V, OUT, true>;
+      if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), 4 * Slots<T, V>::kArray, done);
+      if (e != cudaSuccess) return e;
+      kernel<<<grid, 32 * kWarps, smem, stream>>>(p, maps);
+      return cudaGetLastError();
+    }
+  }
+  static bool done[64];
+  auto kernel = linrec_fwd_kernel<T, V, OUT, false>;
+  e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), 4 * Slots<T, V>::kArray, done);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, 32 * kWarps, smem, stream>>>(p, maps);
+  return cudaGetLastError();
+}
+template <typename T, int V>
+cudaError_t launch_bwd_of(const LinrecParams& p, cudaStream_t stream) {
+  static bool done[64];
+  return launch_tiles(linrec_bwd_kernel<T, V>, done, 2 * (5 * Slots<T, V>::kArray + Slots<T, V>::kGates), 2, p, stream);
+}
+
 // Channels per thread: 8 bytes of a row where its alignment allows, 4 in the backward, which
 // keeps more of each value in registers.
 constexpr int kFwd16 = 4, kFwd32 = 2, kBwd16 = 2, kBwd32 = 1;
@@ -949,13 +1152,13 @@ int lanes_of(int lanes, bool f32, bool bwd) {
   return std::min(lanes, bwd ? (f32 ? kBwd32 : kBwd16) : f32 ? kFwd32 : kFwd16);
 }
 template <bool OUT>
-cudaError_t launch_fwd(const LinrecParams& p, bool f32, int lanes, cudaStream_t stream) {
+cudaError_t launch_fwd(const LinrecParams& p, bool f32, int lanes, bool tma, cudaStream_t stream) {
   if (f32)
-    return lanes == 2 ? launch_tiles(linrec_fwd_kernel<float, 2, OUT>, p, stream)
-                      : launch_tiles(linrec_fwd_kernel<float, 1, OUT>, p, stream);
-  return lanes == 4   ? launch_tiles(linrec_fwd_kernel<bf16, 4, OUT>, p, stream)
-         : lanes == 2 ? launch_tiles(linrec_fwd_kernel<bf16, 2, OUT>, p, stream)
-                      : launch_tiles(linrec_fwd_kernel<bf16, 1, OUT>, p, stream);
+    return lanes == 2 ? launch_fwd_of<float, 2, OUT>(p, tma, stream)
+                      : launch_fwd_of<float, 1, OUT>(p, tma, stream);
+  return lanes == 4   ? launch_fwd_of<bf16, 4, OUT>(p, tma, stream)
+         : lanes == 2 ? launch_fwd_of<bf16, 2, OUT>(p, tma, stream)
+                      : launch_fwd_of<bf16, 1, OUT>(p, tma, stream);
 }
 
 size_t states_bytes(int64_t total, int32_t dim) {
@@ -1008,7 +1211,8 @@ kda_status kda_linrec_fwd(const kda_linrec_problem* problem, void* out, void* fi
   using namespace kda;
   LinrecParams p = {};
   int lanes = 1;
-  kda_status st = check_linrec(problem, p, lanes);
+  bool tma = false;
+  kda_status st = check_linrec(problem, p, lanes, tma);
   if (st != KDA_OK) return st;
   const bool f32 = problem->dtype == KDA_ROW_FP32;
   if (p.total > 0 && !out) return KDA_ERR_NULL_POINTER;
@@ -1041,7 +1245,7 @@ kda_status kda_linrec_fwd(const kda_linrec_problem* problem, void* out, void* fi
   p.ticket = p.status + 1;
   cudaError_t e = launch_setup(p, f32, p.agg, join_bytes(p.total, p.dim), p.init, p.state_bf16,
                                p.fin == p.init ? nullptr : p.fin, p.state_bf16, stream);
-  if (e == cudaSuccess && p.total > 0) e = launch_fwd<true>(p, f32, lanes, stream);
+  if (e == cudaSuccess && p.total > 0) e = launch_fwd<true>(p, f32, lanes, tma, stream);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -1053,7 +1257,8 @@ kda_status kda_linrec_bwd(const kda_linrec_problem* problem, const void* dout, c
   using namespace kda;
   LinrecParams p = {};
   int lanes = 1;
-  kda_status st = check_linrec(problem, p, lanes);
+  bool tma = false;
+  kda_status st = check_linrec(problem, p, lanes, tma);
   if (st != KDA_OK) return st;
   const bool f32 = problem->dtype == KDA_ROW_FP32;
   const size_t e = f32 ? 4 : 2;
@@ -1094,11 +1299,11 @@ kda_status kda_linrec_bwd(const kda_linrec_problem* problem, const void* dout, c
   cudaError_t err = launch_setup(p, f32, published_at, published_bytes, dfinal_state, p.state_bf16,
                                  dinitial_state, false, stream);
   if (err == cudaSuccess && p.total > 0) {
-    if (!chunk_states) err = launch_fwd<false>(f, f32, lanes_of(lanes, f32, false), stream);
+    if (!chunk_states) err = launch_fwd<false>(f, f32, lanes_of(lanes, f32, false), tma, stream);
     if (err == cudaSuccess)
-      err = f32     ? launch_tiles(linrec_bwd_kernel<float, 1>, p, stream)
-            : back == 2 ? launch_tiles(linrec_bwd_kernel<bf16, 2>, p, stream)
-                    : launch_tiles(linrec_bwd_kernel<bf16, 1>, p, stream);
+      err = f32     ? launch_bwd_of<float, 1>(p, stream)
+            : back == 2 ? launch_bwd_of<bf16, 2>(p, stream)
+                    : launch_bwd_of<bf16, 1>(p, stream);
   }
   if (err == cudaSuccess)
     err = launch_column_sums(p.part, p.tiles, 3 * (int64_t)p.dim, 3 * (int64_t)p.dim, p.dim, p.dim, dA_log,
