@@ -58,7 +58,7 @@ struct LinrecParams {
   unsigned *status, *ticket;
   uint64_t* agg;             // [tiles][dim]: (product, end from zero) of each tile
   uint64_t* group_agg;       // [tiles / kGroup][dim]: the same of each whole group
-  unsigned* ends;            // [tiles][dim]: the state after each tile
+  unsigned* ends;            // [tiles / kGroup][dim]: the state after each whole group
   void *dx, *dr, *di, *dz;
   float *part, *dinit;       // part: [tiles][3][dim]
 };
@@ -323,6 +323,7 @@ template <int V>
 struct Runs {
   float P[kWarps][32 * V], H[kWarps][32 * V];  // what each run does to a state; H then holds
                                                // the state before it
+  float parts[kWarps / V][2][32 * V], tile[2][32 * V];  // the join's
   unsigned char cut[kWarps];                   // whether a run holds a sequence's start
 };
 // The unit of work that a ticket stands for: rows' tile first, all channel blocks of one before
@@ -399,56 +400,41 @@ __device__ __noinline__ W await_word(const W* p, unsigned* status) {
   }
 }
 
-// Tiles form groups of kGroup.  A group's last tile also publishes what the whole group does
-// to a state, so the states at the ends of groups follow one from the other without the tiles
-// between: each is the one before it through one group, in this order in every run.  Within a
-// group a state is the group's first one taken through its tiles one after the other.
+// Tiles form groups of kGroup.  The state before a tile is that before its group, taken through
+// what the tiles of the group before it do together; this is composed from zero in parts of
+// the group, by the threads that share a channel, and the parts in their order: the same sums
+// in every run.  A group's last tile also publishes what the whole group does, and the state
+// at its end, so those follow one from the other without the tiles between.
 __device__ __forceinline__ float stepped(uint64_t w, float X) {
   return fmaf(__uint_as_float((unsigned)w), X, __uint_as_float((unsigned)(w >> 32)));
 }
-
-// X taken through tiles from .. to - 1.
-__device__ __forceinline__ float through_tiles(const LinrecParams& p, float X, int64_t from, int64_t to, int ch) {
-  constexpr int kBatch = 4;
-  const uint64_t* at = p.agg + from * p.dim + ch;
-#pragma unroll 1
-  for (int left = (int)(to - from); left > 0; left -= kBatch, at += kBatch * (int64_t)p.dim) {
-    uint64_t w[kBatch];
-#pragma unroll
-    for (int q = 0; q < kBatch; ++q) w[q] = q < left ? ld_word(at + q * (int64_t)p.dim) : 0;
-#pragma unroll
-    for (int q = 0; q < kBatch; ++q)
-      if (q < left) {
-        if (w[q] == kUnset) w[q] = await_word(at + q * (int64_t)p.dim, p.status);
-        X = stepped(w[q], X);
-      }
-  }
-  return X;
+__device__ __forceinline__ uint64_t step_word(float P, float H) {
+  return (uint64_t)published(P) | ((uint64_t)published(H) << 32);
 }
 
 // The state at the end of group g, in a sequence that starts in group `edge` or before the
 // window: that of the nearest group which has published one (the window's last is waited
-// for), taken through the groups since then.
+// for), taken through the groups since then.  found: the word of group g, as it was.
 constexpr int kWindow = 4;
-__device__ __forceinline__ float state_after_group(const LinrecParams& p, int64_t g, int64_t edge, int ch) {
-  const int64_t dim = p.dim;
-  const unsigned* const ends = p.ends + (g * kGroup + kGroup - 1) * dim + ch;
-  unsigned found = ld_word(ends);
+__device__ __forceinline__ float state_after_group(const LinrecParams& p, int64_t g, int64_t edge, int ch,
+                                                   unsigned found) {
   if (found != ~0u) return __uint_as_float(found);
+  const int64_t dim = p.dim;
+  const unsigned* const ends = p.ends + g * dim + ch;
   const uint64_t* const agg = p.group_agg + g * dim + ch;
   const int last = (int)min((int64_t)kWindow - 1, g - edge);
   unsigned e[kWindow];
   uint64_t w[kWindow - 1];
 #pragma unroll
   for (int q = 0; q < kWindow; ++q) {
-    e[q] = q <= last ? ld_word(ends - q * kGroup * dim) : ~0u;
+    e[q] = q <= last ? ld_word(ends - q * dim) : ~0u;
     if (q < kWindow - 1) w[q] = q < last ? ld_word(agg - q * dim) : 0;
   }
   int at = last;
 #pragma unroll
   for (int q = kWindow - 1; q >= 0; --q)
     if (e[q] != ~0u) at = q, found = e[q];
-  if (found == ~0u) found = await_word(ends - last * kGroup * dim, p.status);
+  if (found == ~0u) found = await_word(ends - last * dim, p.status);
   float X = __uint_as_float(found);
 #pragma unroll
   for (int q = kWindow - 2; q >= 0; --q)
@@ -459,92 +445,107 @@ __device__ __forceinline__ float state_after_group(const LinrecParams& p, int64_
   return X;
 }
 
-// The state before tile s, which goes on with a sequence that starts in tile `edge`.  (P, H) is
-// the tile's own step, for what a group's last tile publishes.
-__device__ __forceinline__ float state_before(const LinrecParams& p, int64_t s, int64_t edge, int ch, float P,
-                                              float H, bool cut) {
-  const int64_t g = s / kGroup, first = g * kGroup;
-  const bool whole = edge < first;               // the group goes on with what is before it
-  if (whole && s == first + kGroup - 1 && !cut) {
-    const uint64_t* at = p.agg + first * p.dim + ch;
-    uint64_t w = ld_word(at);
-    if (w == kUnset) w = await_word(at, p.status);
-    float Pg = __uint_as_float((unsigned)w), Hg = __uint_as_float((unsigned)(w >> 32));
-#pragma unroll 1
-    for (int q = 1; q < kGroup - 1; q += 2) {
-      uint64_t u[2];
+// The join of a tile, by all threads: kParts of them share a channel.
+template <int V, bool FORWARD>
+struct Join {
+  static constexpr int kParts = kWarps / V, kPer = kGroup / kParts;
+  const LinrecParams& p;
+  int64_t s, first, from;    // the tile, its group's first, the first that is looked back at
+  int c, part, ch;
+  bool carry, whole, ok;     // the tile goes on; so does its group
+  uint64_t w[kPer];
+  unsigned before;           // the state before the group
+
+  // Before the runs are there: what the tiles before this one have published so far.
+  __device__ __forceinline__ Join(const LinrecParams& p, int64_t s, int64_t edge, bool carry, int c0)
+      : p(p), s(s), first(s / kGroup * kGroup), c(threadIdx.x % (32 * V)), part(threadIdx.x / (32 * V)),
+        ch(c0 + c), carry(carry), ok(ch < p.dim) {
+    from = edge > first ? edge : first;
+    whole = carry && edge < first;
+    before = ~0u;
+    if (!carry || !ok) return;
+    if (part == 0 && whole) before = ld_word(p.ends + (s / kGroup - 1) * p.dim + ch);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) u[k] = ld_word(at + (q + k) * (int64_t)p.dim);
+    for (int q = 0; q < kPer; ++q) {
+      const int64_t at = first + part * kPer + q;
+      w[q] = at >= from && at < s ? ld_word(p.agg + at * p.dim + ch) : 0;
+    }
+  }
+  // The runs are there: together they are published; the part's tiles are composed.
+  __device__ __forceinline__ void parts(Runs<V>& sh, float& P, float& H, float& Pt, float& Ht) {
+    Pt = 1.f, Ht = 0.f;      // of the tiles
+    if (part == kParts - 1 && ok) {
+      const uint64_t cuts = *reinterpret_cast<const uint64_t*>(sh.cut);
+      P = 1.f, H = 0.f;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (u[k] == kUnset) u[k] = await_word(at + (q + k) * (int64_t)p.dim, p.status);
-        Hg = stepped(u[k], Hg), Pg *= __uint_as_float((unsigned)u[k]);
+      for (int q = 0; q < kWarps; ++q) {
+        const int r = FORWARD ? q : kWarps - 1 - q;
+        const float Pr = sh.P[r][c], Hr = sh.H[r][c];
+        H = cuts >> (8 * r) & 1 ? Hr : fmaf(Pr, H, Hr);
+        P *= Pr;
+      }
+      if (cuts) P = 0.f;
+      // (a tile that does not hand on what it is given is only asked for its step where
+      // cu_seqlens is inconsistent; no wait is left without an answer then either)
+      if (!(p.stall && s == 0)) st_word(p.agg + s * p.dim + ch, step_word(P, H));
+      sh.tile[0][c] = P, sh.tile[1][c] = H;
+    }
+    if (carry && ok) {
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        const int64_t at = first + part * kPer + q;
+        if (at < from || at >= s) continue;
+        if (w[q] == kUnset) w[q] = await_word(p.agg + at * p.dim + ch, p.status);
+        Ht = stepped(w[q], Ht);
+        Pt *= __uint_as_float((unsigned)w[q]);
       }
     }
-    Hg = fmaf(P, Hg, H), Pg *= P;
-    st_word(p.group_agg + g * p.dim + ch, (uint64_t)published(Pg) | ((uint64_t)published(Hg) << 32));
-    const float before = state_after_group(p, g - 1, edge / kGroup, ch);
-    st_word(p.ends + s * p.dim + ch, published(fmaf(Pg, before, Hg)));
-    return through_tiles(p, before, first, s, ch);
+    if (part > 0) sh.parts[part - 1][0][c] = Pt, sh.parts[part - 1][1][c] = Ht;
   }
-  float X;
-  const int64_t from = whole ? first : edge + 1;
-  unsigned v = s > from ? ld_word(p.ends + (s - 1) * p.dim + ch) : ~0u;
-  if (v != ~0u) {
-    X = __uint_as_float(v);
-  } else {
-    if (whole) {
-      X = state_after_group(p, g - 1, edge / kGroup, ch);
-    } else {
-      const unsigned* at = p.ends + edge * p.dim + ch;
-      v = ld_word(at);
-      X = __uint_as_float(v != ~0u ? v : await_word(at, p.status));
-    }
-    X = through_tiles(p, X, from, s, ch);
-  }
-  if (!cut) {
-    const float end = fmaf(P, X, H);
-    st_word(p.ends + s * p.dim + ch, published(end));
-    if (s == first + kGroup - 1) st_word(p.group_agg + g * p.dim + ch, (uint64_t)published(end) << 32);
-  }
-  return X;
-}
-
-// One channel of a tile: its runs joined, published, and the state before each.
-// FORWARD: runs in the order of their rows.  `carry`: the tile's first row goes on.
-template <int V, bool FORWARD>
-__device__ __forceinline__ float join_runs(const LinrecParams& p, Runs<V>& sh, int64_t s, int64_t edge, int c,
-                                           int ch, bool carry) {
-  static_assert(kWarps == 8, "eight flags in one word");
-  const uint64_t cuts = *reinterpret_cast<const uint64_t*>(sh.cut);
-  float Pw[kWarps], Hw[kWarps], P = 1.f, H = 0.f;
+  // The parts are there (part 0 only): the state before the tile, and before each run.
+  __device__ __forceinline__ float finish(Runs<V>& sh, int64_t edge, float Pt, float Ht) {
+    float X = 0.f;
+    const uint64_t cuts = *reinterpret_cast<const uint64_t*>(sh.cut);
+    const float P = sh.tile[0][c], H = sh.tile[1][c];
+    const int64_t g = s / kGroup;
+    const bool last = s == first + kGroup - 1 && !(p.stall && s == 0);
+    if (carry) {
 #pragma unroll
-  for (int q = 0; q < kWarps; ++q) {
-    const int w = FORWARD ? q : kWarps - 1 - q;
-    Pw[q] = sh.P[w][c], Hw[q] = sh.H[w][c];
-    H = cuts >> (8 * w) & 1 ? Hw[q] : fmaf(Pw[q], H, Hw[q]);
-    P *= Pw[q];
+      for (int q = 0; q < kParts - 1; ++q) {
+        const float Pq = sh.parts[q][0][c];
+        Ht = fmaf(Pq, Ht, sh.parts[q][1][c]), Pt *= Pq;
+      }
+      const float Hg = fmaf(P, Ht, H), Pg = P * Pt;
+      X = Ht;
+      if (whole) {
+        if (last) st_word(p.group_agg + g * p.dim + ch, step_word(Pg, Hg));
+        const float G = state_after_group(p, g - 1, edge / kGroup, ch, before);
+        X = fmaf(Pt, G, Ht);
+        if (last) st_word(p.ends + g * p.dim + ch, published(cuts ? H : fmaf(Pg, G, Hg)));
+      } else if (last) {
+        st_word(p.group_agg + g * p.dim + ch, step_word(0.f, cuts ? H : Hg));
+        st_word(p.ends + g * p.dim + ch, published(cuts ? H : Hg));
+      }
+    } else if (last) {
+      st_word(p.group_agg + g * p.dim + ch, step_word(0.f, H));
+      st_word(p.ends + g * p.dim + ch, published(H));
+    }
+    before_runs<FORWARD>(sh.P, sh.H, cuts, X);
+    return X;
   }
-  if (!(p.stall && s == 0)) {
-    // (a tile that does not hand on what it is given is only asked for its step where
-    // cu_seqlens is inconsistent; no wait is left without an answer then either)
-    st_word(p.agg + s * p.dim + ch, (uint64_t)published(cuts ? 0.f : P) | ((uint64_t)published(H) << 32));
-    if (!carry || cuts) {
-      st_word(p.ends + s * p.dim + ch, published(H));
-      if (s % kGroup == kGroup - 1)
-        st_word(p.group_agg + s / kGroup * p.dim + ch, (uint64_t)published(H) << 32);
+  // H of each run becomes the state before it.
+  template <bool ORDER>
+  __device__ __forceinline__ void before_runs(const float (&P)[kWarps][32 * V], float (&H)[kWarps][32 * V],
+                                              uint64_t cuts, float S) const {
+#pragma unroll
+    for (int q = 0; q < kWarps; ++q) {
+      const int r = ORDER ? q : kWarps - 1 - q;
+      const float Hr = H[r][c];
+      H[r][c] = S;
+      S = cuts >> (8 * r) & 1 ? Hr : fmaf(P[r][c], S, Hr);
     }
   }
-  float S = carry ? state_before(p, s, edge, ch, P, H, cuts != 0) : 0.f;
-  const float X = S;
-#pragma unroll
-  for (int q = 0; q < kWarps; ++q) {
-    const int w = FORWARD ? q : kWarps - 1 - q;
-    sh.H[w][c] = S;
-    S = cuts >> (8 * w) & 1 ? Hw[q] : fmaf(Pw[q], S, Hw[q]);
-  }
-  return X;
-}
+};
 
 // ---------------------------------------------------------------- forward --
 // TMA: rows come by tensor maps, one copy per run and array (16-byte aligned rows); else each
@@ -664,11 +665,15 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
     __syncwarp();
     const Unit next = sh.unit[slot == 2 ? 0 : slot + 1];
     copy(next);
+    const int64_t edge = rows.bos / kTile;
+    Join<V, true> join(p, s, edge, (rows.live & 1) && !(rows.start & 1) && s > 0, c0);
     __syncthreads();
-    if (threadIdx.x < CH && c0 + (int)threadIdx.x < p.dim) {
-      const float X = join_runs<V, true>(p, sh.runs, s, rows.bos / kTile, threadIdx.x, c0 + threadIdx.x,
-                                         (rows.live & 1) && !(rows.start & 1) && s > 0);
-      if (p.states) p.states[s * p.dim + c0 + threadIdx.x] = X;
+    float Pj, Hj, Pt, Ht;
+    join.parts(sh.runs, Pj, Hj, Pt, Ht);
+    __syncthreads();
+    if (join.part == 0 && join.ok) {
+      const float X = join.finish(sh.runs, edge, Pt, Ht);
+      if (p.states) p.states[s * p.dim + join.ch] = X;
     }
     if (warp == kWarps - 1) {  // meanwhile: the next turn's rows, and the unit after that
       if (next.tile >= 0) find_rows(sh.rows[(turn + 1) & 1], p, (int64_t)next.tile * kTile, lane);
@@ -797,13 +802,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
   constexpr int R = kRows, CH = 32 * V;
   using S = Slots<T, V>;
   constexpr int kBuffer = 5 * S::kArray + S::kGates;  // x, r, i, dout, z, gates; two by turns
-  extern __shared__ __align__(16) uint8_t slots[];
+  extern __shared__ __align__(128) uint8_t slots[];
   __shared__ __align__(16) BlockShared<V> sh;         // runs of the gradients, last run first
-  __shared__ __align__(16) Runs<V> fw;                // of the states; the products are shared
+  __shared__ __align__(16) float fw_H[kWarps][CH];    // of the states; the products are the same
+  __shared__ __align__(8) unsigned char fw_cut[kWarps];
   __shared__ __align__(16) float sums[3][kWarps][CH];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   start_block<V, false>(p, sh, warp, lane);
-  static_assert(2 * CH <= 32 * (kWarps - 2), "a thread per channel for each of the two joins");
   const uint8_t* const mine0 = slots + warp * S::kRun + lane * S::kBytes;
   const uint32_t at0 = ptx::smem_u32(mine0), at_gates0 = ptx::smem_u32(slots + 5 * S::kArray + threadIdx.x * V * 4);
   auto place = [&](const Unit& u, int64_t& row0, int& ch) {  // the rows that exist
@@ -882,7 +887,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
       h = fma_of(a[j], h, b[j]);
       P = mul_of(P, a[j]);
     }
-    put<V>(fw.H[warp], lane, h);
+    put<V>(fw_H[warp], lane, h);
     if (bits.last && p.dfin && ok) {  // the final state's gradient joins the last row's
 #pragma unroll
       for (int j = 0; j < R; ++j)
@@ -900,22 +905,20 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
     if (threadIdx.x == 32 * kWarps - 32) ticket = atomicAdd(p.ticket, 1u);
     put<V>(sh.runs.P[warp], lane, P);
     put<V>(sh.runs.H[warp], lane, h);
-    if (lane == 0) sh.runs.cut[warp] = bits.last != 0, fw.cut[warp] = bits.start != 0;
+    if (lane == 0) sh.runs.cut[warp] = bits.last != 0, fw_cut[warp] = bits.start != 0;
+    const int64_t edge = p.tiles - 1 - (rows.eos - 1) / kTile;
+    Join<V, false> join(p, s, edge, (rows.live >> (kTile - 1)) && !(rows.last >> (kTile - 1)) && s > 0, c0);
     __syncthreads();
-    if (threadIdx.x < CH) {
-      if (c0 + (int)threadIdx.x < p.dim)
-        join_runs<V, false>(p, sh.runs, s, p.tiles - 1 - (rows.eos - 1) / kTile, threadIdx.x, c0 + threadIdx.x,
-                            (rows.live >> (kTile - 1)) && !(rows.last >> (kTile - 1)) && s > 0);
-    } else if (threadIdx.x < 2 * CH) {
-      const int k = threadIdx.x - CH;
-      float S = c0 + k < p.dim ? p.states[tile * p.dim + c0 + k] : 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float H = fw.H[w][k];
-        fw.H[w][k] = S;
-        S = fw.cut[w] ? H : fmaf(sh.runs.P[w][k], S, H);
-      }
-    } else if (warp == kWarps - 1) {  // meanwhile: the next turn's unit and rows
+    float Pj, Hj, Pt, Ht;
+    join.parts(sh.runs, Pj, Hj, Pt, Ht);
+    __syncthreads();
+    if (join.part == 0) {
+      if (join.ok) join.finish(sh.runs, edge, Pt, Ht);
+    } else if (join.part == 1) {
+      if (join.ok)
+        join.template before_runs<true>(sh.runs.P, fw_H, *reinterpret_cast<const uint64_t*>(fw_cut),
+                                        p.states[tile * p.dim + join.ch]);
+    } else if (warp == kWarps - 1) {  // meanwhile: the next turn's rows, and the unit after that
       const Unit next = sh.unit[(turn + 1) % 3];
       if (next.tile >= 0) find_rows(sh.rows[(turn + 1) & 1], p, (p.tiles - 1 - next.tile) * kTile, lane);
       const Unit u = unit_of(p, __shfl_sync(0xffffffffu, ticket, 0));
@@ -926,7 +929,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
     copy(sh.unit[(turn + 1) % 3], turn + 1);
     // states again, b <- the one before each row; dz
     const int64_t row_at = row0 * p.dim + ch;
-    h = get<V>(fw.H[warp], lane);
+    h = get<V>(fw_H[warp], lane);
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       if (bits.start >> j & 1) h = initial(j);
@@ -1014,7 +1017,7 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 int64_t tiles_of(int64_t total) { return (total + kTile - 1) / kTile; }
 size_t join_bytes(int64_t total, int32_t dim) {  // what tiles publish
   const size_t tiles = (size_t)tiles_of(total);
-  return up256(tiles * dim * 8) + up256(tiles / kGroup * dim * 8) + up256(tiles * dim * 4);
+  return up256(tiles * dim * 8) + up256(tiles / kGroup * dim * 8) + up256(tiles / kGroup * dim * 4);
 }
 
 kda_status check_sizes(const kda_linrec_problem* q, LinrecParams& p) {
@@ -1112,7 +1115,7 @@ cudaError_t rows_map(CUtensorMap* m, const void* p, const LinrecParams& q, uint3
 }
 template <typename T, int V, bool OUT>
 cudaError_t launch_fwd_of(const LinrecParams& p, bool tma, cudaStream_t stream) {
-  LinrecMaps maps;
+  LinrecMaps maps = {};
   const int smem = (p.z && OUT ? 4 : 3) * Slots<T, V>::kArray;
   int sms = 0;
   if (sm_count(&sms) != KDA_OK) return cudaErrorUnknown;
