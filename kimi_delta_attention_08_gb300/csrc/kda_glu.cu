@@ -18,7 +18,7 @@
 // Accumulation is fp32.  dg and du are rounded to bf16 between the two steps of the backward,
 // since the tensor cores take bf16: their error, half a step of bf16 each and independent
 // over the summed axis, adds as much to dx and dW as the outputs' own rounding.
-#include <cstring>
+#include <algorithm>
 
 #include "kda_internal.h"
 #include "kda_rows.cuh"
@@ -29,10 +29,16 @@ namespace {
 
 using namespace rows;
 
-constexpr int kTileM = 256, kTileN = 256, kTileK = 64, kStages = 6;
-constexpr int kHalf = 128;                       // rows of A, columns of B in each CTA
-constexpr uint32_t kOperand = kHalf * kTileK * 2;  // bytes of each in a stage
-constexpr uint32_t kSmem = kStages * 2 * kOperand + 1024 + 256;
+constexpr int kTileM = 256, kTileK = 64;
+constexpr int kHalf = 128;                       // rows of A in each CTA
+constexpr uint32_t kOperandA = kHalf * kTileK * 2;  // its bytes in a stage
+// Tiles of N = 256 or 128 columns: half of them, of B, in each CTA.
+template <int N>
+struct Tile {
+  static constexpr int kHalfN = N / 2, kStages = N == 256 ? 6 : 8;
+  static constexpr uint32_t kOperandB = kHalfN * kTileK * 2, kStage = kOperandA + kOperandB;
+  static constexpr uint32_t kSmem = kStages * kStage + 1024;
+};
 constexpr uint64_t kWaitNs = 500000000ull;
 constexpr int kEpilogueWarp = 4;                 // warps 4 .. 7
 
@@ -85,12 +91,14 @@ __device__ __forceinline__ void store8(bf16* p, const float* f) {
       make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
 }
 
-template <int PASS>
+template <int PASS, int N>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     glu_kernel(const __grid_constant__ GluParams p) {
   constexpr bool A_MN = PASS == kWeights, B_MN = PASS == kInput || PASS == kWeights;
   constexpr bool DUAL = PASS == kForward || PASS == kRecompute;
   constexpr int SUMS = PASS == kInput ? 2 : 1;
+  using L = Tile<N>;
+  constexpr int kStages = L::kStages, kHalfN = L::kHalfN;
   extern __shared__ uint8_t raw[];
   uint8_t* const tiles = ptx::smem_align1024(raw);
   __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2];
@@ -106,7 +114,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     for (int b = 0; b < 2; ++b) ptx::mbar_init(&tfull[b], 1), ptx::mbar_init(&tempty[b], 8);
     ptx::fence_mbar_init();
   }
-  if (warp == 2) ptx::tmem_alloc_pair(&tmem_at, 512);
+  if (warp == 2) ptx::tmem_alloc_pair(&tmem_at, 2 * N);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();
@@ -123,26 +131,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
       for (int kb = 0; kb < blocks && ok; ++kb) {
         ok = ptx::mbar_wait(&empty[stage], parity, kWaitNs);
         if (!ok) break;
-        if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 4 * kOperand);
+        if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * L::kStage);
         const uint32_t bar = ptx::cluster_addr(&full[stage], 0);
-        uint8_t* const A = tiles + stage * 2 * kOperand;
-        uint8_t* const B = A + kOperand;
+        uint8_t* const A = tiles + stage * L::kStage;
+        uint8_t* const B = A + kOperandA;
         const int part = SUMS == 2 && kb >= p.k_blocks, k0 = (kb - part * p.k_blocks) * kTileK;
         if constexpr (A_MN) {
           // tiles of the gate's gradient first, then of the other's
           const int half = p.m_tiles / 2, which = m >= half;
           const int at = (m - which * half) * kTileM + rank * kHalf;
           ptx::tma_load_2d_pair(A, &p.a[which], bar, at, k0);
-          ptx::tma_load_2d_pair(A + kOperand / 2, &p.a[which], bar, at + 64, k0);
+          ptx::tma_load_2d_pair(A + kOperandA / 2, &p.a[which], bar, at + 64, k0);
         } else {
           ptx::tma_load_2d_pair(A, &p.a[part], bar, k0, m * kTileM + (int)rank * kHalf);
         }
         if constexpr (B_MN) {
-          const int at = n * kTileN + rank * kHalf;
+          const int at = n * N + rank * kHalfN;
           ptx::tma_load_2d_pair(B, &p.b[part], bar, at, k0);
-          ptx::tma_load_2d_pair(B + kOperand / 2, &p.b[part], bar, at + 64, k0);
+          if constexpr (N == 256) ptx::tma_load_2d_pair(B + L::kOperandB / 2, &p.b[part], bar, at + 64, k0);
         } else {
-          ptx::tma_load_2d_pair(B, &p.b[rank], bar, k0, n * kHalf);
+          ptx::tma_load_2d_pair(B, &p.b[rank], bar, k0, n * kHalfN);
         }
         if (++stage == kStages) stage = 0, parity ^= 1;
       }
@@ -155,7 +163,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     if (!ok) failed = 1;
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // products of the pair
-    constexpr uint32_t idesc = ptx::idesc_bf16_f32(kTileM, kTileN, A_MN, B_MN);
+    constexpr uint32_t idesc = ptx::idesc_bf16_f32(kTileM, N, A_MN, B_MN);
     constexpr uint32_t a_step = A_MN ? 16 * 128 : 32, b_step = B_MN ? 16 * 128 : 32;
     uint32_t stage = 0, parity = 0, buf = 0, tparity = 1;
     bool ok = true;
@@ -166,11 +174,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         ok = ptx::mbar_wait(&full[stage], parity, kWaitNs);
         if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t A = ptx::smem_u32(tiles + stage * 2 * kOperand), B = A + kOperand;
+        const uint32_t A = ptx::smem_u32(tiles + stage * L::kStage), B = A + kOperandA;
 #pragma unroll
         for (int k = 0; k < kTileK / 16; ++k)
-          ptx::mma_bf16_ss_pair(tmem + buf * kTileN, ptx::sw128_desc(A + k * a_step, kOperand / 2, 1024),
-                                ptx::sw128_desc(B + k * b_step, kOperand / 2, 1024), idesc, kb + k > 0);
+          ptx::mma_bf16_ss_pair(tmem + buf * N, ptx::sw128_desc(A + k * a_step, kOperandA / 2, 1024),
+                                ptx::sw128_desc(B + k * b_step, kOperandA / 2, 1024), idesc, kb + k > 0);
         ptx::mma_commit_pair(&empty[stage]);
         if (++stage == kStages) stage = 0, parity ^= 1;
       }
@@ -202,16 +210,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
       }
       row += rank * kHalf + w * 32 + lane;
       const bool in = row < p.M;
-      const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(w * 32) << 16);
+      const uint32_t acc = tmem + buf * N + ((uint32_t)(w * 32) << 16);
 #pragma unroll 1
-      for (int c = 0; c < (DUAL ? kHalf : kTileN); c += 32) {
+      for (int c = 0; c < (DUAL ? kHalfN : N); c += 32) {
         uint32_t v[32];
         ptx::tmem_ld32(acc + c, v);
-        const int64_t col = (int64_t)n * (DUAL ? kHalf : kTileN) + c;
+        const int64_t col = (int64_t)n * (DUAL ? kHalfN : N) + c;
         const int64_t at = row * p.N + col;
         if constexpr (DUAL) {
           uint32_t q[32];
-          ptx::tmem_ld32(acc + kHalf + c, q);
+          ptx::tmem_ld32(acc + kHalfN + c, q);
           ptx::tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 32; j += 8) {
@@ -269,7 +277,135 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
   ptx::tc_fence_before();
   ptx::cluster_sync();
   ptx::tc_fence_after();
-  if (warp == 2) ptx::tmem_dealloc_pair(tmem, 512);
+  if (warp == 2) ptx::tmem_dealloc_pair(tmem, 2 * N);
+}
+
+// ------------------------------------------------------------- few rows --
+// The forward of up to kStepRows rows reads the weights once and is bound by that.  A CTA
+// takes 64 rows of both weights as the 128 rows of A, and all of x as B's columns, so the tensor
+// cores do no more work than the rows need; where the weights' rows alone do not fill the
+// GPU, a cluster splits the summed axis and adds up through its shared memory, in the order
+// of its CTAs.  Two CTAs fit an SM, each with 96 KB of weights and x in flight.
+constexpr int kStepRows = 128, kStepTile = 64, kStepMaxSplit = 8;
+constexpr uint32_t kStepRing = 98304, kStepSmem = kStepRing + 1024;
+constexpr int kStepPitch = 132;                  // floats between two rows' sums
+
+struct StepParams {
+  CUtensorMap w[2], x;
+  int32_t rows, cols;        // of x that exist; of the product, a multiple of 16
+  int32_t hidden, k_blocks, splits, stages, fn, stall;
+  bf16 *out, *pre;
+  unsigned* status;
+};
+
+__global__ void __launch_bounds__(256, 2) glu_step_kernel(const __grid_constant__ StepParams p) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* const ring = ptx::smem_align1024(raw);
+  __shared__ uint64_t full[6], empty[6], done;
+  __shared__ uint32_t tmem_at;
+  __shared__ int failed;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int split = blockIdx.x % p.splits, f0 = blockIdx.x / p.splits * kStepTile;
+  const int per = (p.k_blocks + p.splits - 1) / p.splits;
+  const int first = split * per, last = min(p.k_blocks, first + per);
+  const uint32_t stage_bytes = 2 * kStepTile * 128 + p.cols * 128;
+  if (threadIdx.x == 0) {
+    failed = 0;
+    for (int s = 0; s < p.stages; ++s) ptx::mbar_init(&full[s], 1), ptx::mbar_init(&empty[s], 1);
+    ptx::mbar_init(&done, 1);
+    ptx::fence_mbar_init();
+  }
+  if (warp == 2) {
+    ptx::tmem_alloc(&tmem_at, 128);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  if (warp == 0 && lane == 0) {
+    bool ok = !p.stall;
+    uint32_t stage = 0, parity = 1;
+    for (int kb = first; kb < last && ok; ++kb) {
+      ok = ptx::mbar_wait(&empty[stage], parity, kWaitNs);
+      if (!ok) break;
+      uint8_t* const A = ring + stage * stage_bytes;
+      ptx::mbar_arrive_expect_tx(&full[stage], stage_bytes);
+      ptx::tma_load_2d(A, &p.w[0], &full[stage], kb * kTileK, f0);
+      ptx::tma_load_2d(A + kStepTile * 128, &p.w[1], &full[stage], kb * kTileK, f0);
+      ptx::tma_load_2d(A + 2 * kStepTile * 128, &p.x, &full[stage], kb * kTileK, 0);
+      if (++stage == p.stages) stage = 0, parity ^= 1;
+    }
+    if (!ok) failed = 1;
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = ptx::idesc_bf16_f32(128, p.cols, 0, 0);
+    bool ok = true;
+    uint32_t stage = 0, parity = 0;
+    for (int kb = first; kb < last; ++kb) {
+      ok = ptx::mbar_wait(&full[stage], parity, kWaitNs);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const uint32_t A = ptx::smem_u32(ring + stage * stage_bytes), B = A + 2 * kStepTile * 128;
+#pragma unroll
+      for (int k = 0; k < kTileK / 16; ++k)
+        ptx::mma_bf16_ss(tmem, ptx::sw128_desc(A + k * 32, 16, 1024), ptx::sw128_desc(B + k * 32, 16, 1024), idesc,
+                         kb > first || k > 0);
+      ptx::mma_commit(&empty[stage]);
+      if (++stage == p.stages) stage = 0, parity ^= 1;
+    }
+    ptx::mma_commit(&done);
+    if (!ok) failed = 1;
+  }
+  __syncwarp();
+  // this CTA's sums, [x's row][weights' row], where the ring was
+  float* const sums = reinterpret_cast<float*>(ring);
+  const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait(&done, 0, 2 * kWaitNs));
+  if (!ok && lane == 0) failed = 1;
+  __syncthreads();
+  if (failed) {  // a wait ran out: what is in flight comes to rest before its place is used
+    if (threadIdx.x == 0 && p.status) atomicOr(p.status, kDevStatusTimeout);
+    const uint64_t t0 = ptx::global_timer_ns();
+    while (ptx::global_timer_ns() - t0 < 2000000) {
+    }
+  }
+  ptx::tc_fence_after();
+  if (warp >= 4) {
+    const int f = (warp - 4) * 32 + lane;
+    for (int c = 0; c < p.cols; c += 16) {
+      uint32_t v[16];
+      ptx::tmem_ld16(tmem + ((uint32_t)((warp - 4) * 32) << 16) + c, v);
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 16; ++k) sums[(c + k) * kStepPitch + f] = first < last ? __uint_as_float(v[k]) : 0.f;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  if (warp == 2) ptx::tmem_dealloc(tmem, 128);
+  // each CTA of the cluster adds up some of the rows: a warp a row, a lane two columns
+  const int col = f0 + 2 * lane;
+  for (int r = split * 8 + warp; r < p.rows; r += p.splits * 8) {
+    float2 g = make_float2(0.f, 0.f), u = g;
+    for (int q = 0; q < p.splits; ++q) {
+      const uint32_t at = ptx::cluster_addr(sums + r * kStepPitch + 2 * lane, q);
+      float2 v;
+      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+      g.x += v.x, g.y += v.y;
+      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at + 4 * kStepTile) : "memory");
+      u.x += v.x, u.y += v.y;
+    }
+    if (col < p.hidden) {
+      const int64_t at = (int64_t)r * p.hidden + col;
+      *reinterpret_cast<uint32_t*>(p.out + at) = pack_bf16(act_of(g.x, p.fn) * u.x, act_of(g.y, p.fn) * u.y);
+      if (p.pre) {
+        bf16* const to = p.pre + (int64_t)r * 2 * p.hidden + col;
+        *reinterpret_cast<uint32_t*>(to) = pack_bf16(g.x, g.y);
+        *reinterpret_cast<uint32_t*>(to + p.hidden) = pack_bf16(u.x, u.y);
+      }
+    }
+  }
+  ptx::cluster_sync();
 }
 
 // dg and du from kept pre-activations, eight values a thread.
@@ -308,16 +444,30 @@ cudaError_t map_of(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, in
                           CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int PASS>
-cudaError_t launch(GluParams& p, cudaStream_t stream) {
+template <int PASS, int N>
+cudaError_t launch_of(const GluParams& p, int sms, cudaStream_t stream) {
   static bool done[64];
-  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(glu_kernel<PASS>), kSmem, done);
+  constexpr int smem = Tile<N>::kSmem;
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(glu_kernel<PASS, N>), smem, done);
   if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles, pairs = tiles < sms / 2 ? tiles : sms / 2;
+  glu_kernel<PASS, N><<<(unsigned)(2 * pairs), 256, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+// B's maps depend on the tiles' width: `maps(half of it)` makes them.  Narrow tiles take where
+// wide ones leave more of the last turn over the pairs unused than their lower rate costs.
+template <int PASS, typename MAPS>
+cudaError_t launch(GluParams& p, int64_t columns, MAPS maps, cudaStream_t stream) {
   int sms = 0;
   if (sm_count(&sms) != KDA_OK) return cudaErrorUnknown;
-  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles, pairs = tiles < sms / 2 ? tiles : sms / 2;
-  glu_kernel<PASS><<<(unsigned)(2 * pairs), 256, kSmem, stream>>>(p);
-  return cudaGetLastError();
+  const int64_t pairs = sms / 2;
+  const int64_t wide = up(columns, 256), narrow = up(columns, 128);
+  const int64_t turns_wide = up(p.m_tiles * wide, pairs), turns_narrow = up(p.m_tiles * narrow, pairs);
+  const bool n128 = 10 * turns_wide > 6 * turns_narrow;
+  const cudaError_t e = maps(n128 ? 64 : 128);
+  if (e != cudaSuccess) return e;
+  p.n_tiles = (int32_t)(n128 ? narrow : wide);
+  return n128 ? launch_of<PASS, 128>(p, sms, stream) : launch_of<PASS, 256>(p, sms, stream);
 }
 
 kda_status check_glu(const kda_glu_problem* q) {
@@ -326,7 +476,8 @@ kda_status check_glu(const kda_glu_problem* q) {
   if (q->rows < 0 || q->rows >= lim || q->dim < 8 || q->hidden < 8 || q->dim % 8 || q->hidden % 8 ||
       q->x_stride < q->dim || q->x_stride >= lim || q->x_stride % 8)
     return KDA_ERR_INVALID_SHAPE;
-  if (up(q->rows, kTileM) * up(q->hidden, kHalf) >= lim || 2 * up(q->hidden, kTileM) * up(q->dim, kTileN) >= lim)
+  if (up(q->rows, kTileM) * up(q->hidden, 64) >= lim || up(q->rows, kTileM) * up(q->dim, 128) >= lim ||
+      2 * up(q->hidden, kTileM) * up(q->dim, 128) >= lim)
     return KDA_ERR_INVALID_SHAPE;
   if (q->dtype != KDA_ROW_BF16 || (q->fn != KDA_FN_SILU && q->fn != KDA_FN_SIGMOID && q->fn != KDA_FN_GELU))
     return KDA_ERR_INVALID_ARG;
@@ -340,17 +491,46 @@ template <int PASS>
 cudaError_t launch_dual(const kda_glu_problem* q, bf16* o0, bf16* o1, const void* dout, unsigned* status,
                         cudaStream_t stream) {
   GluParams p = {};
-  cudaError_t e = map_of(&p.a[0], q->x, q->rows, q->dim, q->x_stride, kHalf);
-  if (e == cudaSuccess) e = map_of(&p.b[0], q->w_gate, q->hidden, q->dim, q->dim, kHalf);
-  if (e == cudaSuccess) e = map_of(&p.b[1], q->w_up, q->hidden, q->dim, q->dim, kHalf);
+  const cudaError_t e = map_of(&p.a[0], q->x, q->rows, q->dim, q->x_stride, kHalf);
   if (e != cudaSuccess) return e;
-  p.a[1] = p.a[0];
   p.M = q->rows, p.N = q->hidden;
-  p.k_blocks = (int32_t)up(q->dim, kTileK);
-  p.m_tiles = (int32_t)up(q->rows, kTileM), p.n_tiles = (int32_t)up(q->hidden, kHalf);
+  p.k_blocks = (int32_t)up(q->dim, kTileK), p.m_tiles = (int32_t)up(q->rows, kTileM);
   p.fn = q->fn, p.stall = q->debug_stall, p.status = status;
   p.o0 = o0, p.o1 = o1, p.dout = static_cast<const bf16*>(dout);
-  return launch<PASS>(p, stream);
+  auto maps = [&](int rows) {  // a tile's columns are as many of both projections
+    const cudaError_t e = map_of(&p.b[0], q->w_gate, q->hidden, q->dim, q->dim, rows);
+    return e == cudaSuccess ? map_of(&p.b[1], q->w_up, q->hidden, q->dim, q->dim, rows) : e;
+  };
+  return launch<PASS>(p, 2 * (int64_t)q->hidden, maps, stream);
+}
+
+// Up to kStepRows rows.  As many CTAs share the summed axis as fit the GPU twice per SM, with four
+// steps of 64 at least for each.
+cudaError_t launch_step(const kda_glu_problem* q, bf16* out, bf16* pre, unsigned* status, cudaStream_t stream) {
+  StepParams p = {};
+  int sms = 0;
+  if (sm_count(&sms) != KDA_OK) return cudaErrorUnknown;
+  const int64_t tiles = up(q->hidden, kStepTile);
+  p.rows = (int32_t)q->rows, p.cols = (int32_t)up(q->rows, 16) * 16;
+  p.hidden = q->hidden, p.k_blocks = (int32_t)up(q->dim, kTileK);
+  p.splits = 1;
+  while (p.splits < kStepMaxSplit && tiles * p.splits * 2 <= 2 * sms && p.k_blocks >= 8 * p.splits) p.splits *= 2;
+  p.stages = std::min(6, (int)(kStepRing / (2 * kStepTile * 128 + p.cols * 128)));
+  p.fn = q->fn, p.stall = q->debug_stall, p.out = out, p.pre = pre, p.status = status;
+  cudaError_t e = map_of(&p.w[0], q->w_gate, q->hidden, q->dim, q->dim, kStepTile);
+  if (e == cudaSuccess) e = map_of(&p.w[1], q->w_up, q->hidden, q->dim, q->dim, kStepTile);
+  if (e == cudaSuccess) e = map_of(&p.x, q->x, q->rows, q->dim, q->x_stride, p.cols);
+  static bool done[64];
+  if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(glu_step_kernel), kStepSmem, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)(tiles * p.splits)), c.blockDim = dim3(256);
+  c.dynamicSmemBytes = kStepSmem, c.stream = stream;
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = p.splits, a.val.clusterDim.y = a.val.clusterDim.z = 1;
+  c.attrs = &a, c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, glu_step_kernel, p);
 }
 
 }  // namespace
@@ -371,10 +551,10 @@ kda_status kda_glu_fwd(const kda_glu_problem* problem, void* out, void* pre, voi
   unsigned* const status = static_cast<unsigned*>(workspace);
   if (status && cudaMemsetAsync(status, 0, 4, stream) != cudaSuccess) return KDA_ERR_CUDA;
   if (problem->rows == 0) return KDA_OK;
-  return launch_dual<kForward>(problem, static_cast<bf16*>(out), static_cast<bf16*>(pre), nullptr, status,
-                               stream) == cudaSuccess
-             ? KDA_OK
-             : KDA_ERR_CUDA;
+  bf16 *const to = static_cast<bf16*>(out), *const kept = static_cast<bf16*>(pre);
+  const cudaError_t e = problem->rows <= kStepRows ? launch_step(problem, to, kept, status, stream)
+                                                   : launch_dual<kForward>(problem, to, kept, nullptr, status, stream);
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 kda_status kda_glu_bwd_get_workspace_size(int64_t rows, int32_t hidden, size_t* bytes) {
@@ -424,22 +604,21 @@ kda_status kda_glu_bwd(const kda_glu_problem* problem, const void* dout, const v
   GluParams p = {};
   p.stall = q.debug_stall, p.status = status;
   // dx: both projections' products in one sum
+  auto none = [](int) { return cudaSuccess; };
   if (e == cudaSuccess) e = map_of(&p.a[0], dg, M, F, F, kHalf);
   if (e == cudaSuccess) e = map_of(&p.a[1], du, M, F, F, kHalf);
   if (e == cudaSuccess) e = map_of(&p.b[0], q.w_gate, F, D, D, kTileK);
   if (e == cudaSuccess) e = map_of(&p.b[1], q.w_up, F, D, D, kTileK);
-  p.M = M, p.N = D, p.k_blocks = (int32_t)up(F, kTileK);
-  p.m_tiles = (int32_t)up(M, kTileM), p.n_tiles = (int32_t)up(D, kTileN);
+  p.M = M, p.N = D, p.k_blocks = (int32_t)up(F, kTileK), p.m_tiles = (int32_t)up(M, kTileM);
   p.o0 = static_cast<bf16*>(dx);
-  if (e == cudaSuccess) e = launch<kInput>(p, stream);
+  if (e == cudaSuccess) e = launch<kInput>(p, D, none, stream);
   // the weights' gradients: the gate's rows, then the other's
   if (e == cudaSuccess) e = map_of(&p.a[0], dg, M, F, F, kTileK);
   if (e == cudaSuccess) e = map_of(&p.a[1], du, M, F, F, kTileK);
   if (e == cudaSuccess) e = map_of(&p.b[0], q.x, M, D, q.x_stride, kTileK);
-  p.M = F, p.N = D, p.k_blocks = (int32_t)up(M, kTileK);
-  p.m_tiles = (int32_t)(2 * up(F, kTileM)), p.n_tiles = (int32_t)up(D, kTileN);
+  p.M = F, p.N = D, p.k_blocks = (int32_t)up(M, kTileK), p.m_tiles = (int32_t)(2 * up(F, kTileM));
   p.o0 = static_cast<bf16*>(dw_gate), p.o1 = static_cast<bf16*>(dw_up);
-  if (e == cudaSuccess) e = launch<kWeights>(p, stream);
+  if (e == cudaSuccess) e = launch<kWeights>(p, D, none, stream);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -11,9 +11,11 @@ from tests.glu_ref import glu, within
 pytestmark = pytest.mark.gpu
 
 BF = torch.bfloat16
-# rows, dim, hidden: ragged and whole tiles, one step and many, more tiles than pairs of CTAs
+# rows, dim, hidden: ragged and whole tiles, one step and many, more tiles than pairs of CTAs;
+# up to 128 rows the forward splits the summed axis over clusters of 1 to 8, with a part left over
 SIZES = [(1, 8, 8), (3, 64, 128), (17, 72, 136), (127, 200, 264), (128, 256, 128), (129, 128, 256),
-         (256, 512, 512), (257, 520, 248), (300, 1000, 640), (513, 64, 2056), (1100, 264, 1032)]
+         (256, 512, 512), (257, 520, 248), (300, 1000, 640), (513, 64, 2056), (1100, 264, 1032),
+         (2, 1032, 200), (33, 2112, 72), (128, 4104, 1608), (64, 4096, 9800)]
 
 
 def make(M, D, Fh, seed=0, B=1, wide=0):
