@@ -343,12 +343,12 @@ template <int V>
 struct BlockShared {
   Runs<V> runs;
   TileRows rows[2];
-  Unit unit[3];
+  Unit unit[2];
 };
 // The first turn's unit and rows.
 template <int V, bool FORWARD>
 __device__ __forceinline__ void start_block(const LinrecParams& p, BlockShared<V>& sh, int warp, int lane) {
-  if (threadIdx.x < 2) sh.unit[threadIdx.x] = unit_of(p, atomicAdd(p.ticket, 1u));
+  if (threadIdx.x == 0) sh.unit[0] = unit_of(p, atomicAdd(p.ticket, 1u));
   __syncthreads();
   const int64_t s = sh.unit[0].tile;
   if (warp == 0 && s >= 0) find_rows(sh.rows[0], p, (FORWARD ? s : p.tiles - 1 - s) * kTile, lane);
@@ -622,8 +622,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
   };
   copy(sh.unit[0]);
   copy_z(sh.unit[0]);
-  for (unsigned turn = 0, slot = 0;; ++turn, slot = slot == 2 ? 0 : slot + 1) {
-    const Unit unit = sh.unit[slot];
+  for (unsigned turn = 0;; ++turn) {
+    const Unit unit = sh.unit[turn & 1];
     if (unit.tile < 0) break;
     const int64_t s = unit.tile;
     const int c0 = unit.block * CH;
@@ -662,12 +662,12 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
     put<V>(sh.runs.P[warp], lane, P);
     put<V>(sh.runs.H[warp], lane, h);
     if (lane == 0) sh.runs.cut[warp] = bits.start != 0;
-    __syncwarp();
-    const Unit next = sh.unit[slot == 2 ? 0 : slot + 1];
-    copy(next);
+    if (threadIdx.x == 32 * kWarps - 32) sh.unit[(turn + 1) & 1] = unit_of(p, ticket);
     const int64_t edge = rows.bos / kTile;
     Join<V, true> join(p, s, edge, (rows.live & 1) && !(rows.start & 1) && s > 0, c0);
     __syncthreads();
+    const Unit next = sh.unit[(turn + 1) & 1];
+    copy(next);
     float Pj, Hj, Pt, Ht;
     join.parts(sh.runs, Pj, Hj, Pt, Ht);
     __syncthreads();
@@ -675,11 +675,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
       const float X = join.finish(sh.runs, edge, Pt, Ht);
       if (p.states) p.states[s * p.dim + join.ch] = X;
     }
-    if (warp == kWarps - 1) {  // meanwhile: the next turn's rows, and the unit after that
-      if (next.tile >= 0) find_rows(sh.rows[(turn + 1) & 1], p, (int64_t)next.tile * kTile, lane);
-      const Unit u = unit_of(p, __shfl_sync(0xffffffffu, ticket, 0));
-      if (lane == 0) sh.unit[slot == 0 ? 2 : slot - 1] = u;
-    }
+    if (warp == kWarps - 1 && next.tile >= 0)  // meanwhile: the next turn's rows
+      find_rows(sh.rows[(turn + 1) & 1], p, (int64_t)next.tile * kTile, lane);
     __syncthreads();
     if constexpr (OUT) {
       if (p.z) arrived(1, turn);
@@ -845,10 +842,12 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
   };
   copy(sh.unit[0], 0);
   for (unsigned turn = 0;; ++turn) {
-    const Unit unit = sh.unit[turn % 3];
+    const Unit unit = sh.unit[turn & 1];
     if (unit.tile < 0) break;
     const int64_t s = unit.tile, tile = p.tiles - 1 - s;  // s: counted from the last tile back
     const int c0 = unit.block * CH;
+    unsigned ticket = 0;
+    if (threadIdx.x == 32 * kWarps - 32) ticket = atomicAdd(p.ticket, 1u);
     int64_t row0;
     int ch;
     const int n = place(unit, row0, ch);
@@ -901,11 +900,10 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
     h = splat<V>(0.f);
 #pragma unroll
     for (int j = R - 1; j >= 0; --j) h = mul_of(a[j], bits.last >> j & 1 ? dy[j] : add_of(h, dy[j]));
-    unsigned ticket = 0;
-    if (threadIdx.x == 32 * kWarps - 32) ticket = atomicAdd(p.ticket, 1u);
     put<V>(sh.runs.P[warp], lane, P);
     put<V>(sh.runs.H[warp], lane, h);
     if (lane == 0) sh.runs.cut[warp] = bits.last != 0, fw_cut[warp] = bits.start != 0;
+    if (threadIdx.x == 32 * kWarps - 32) sh.unit[(turn + 1) & 1] = unit_of(p, ticket);
     const int64_t edge = p.tiles - 1 - (rows.eos - 1) / kTile;
     Join<V, false> join(p, s, edge, (rows.live >> (kTile - 1)) && !(rows.last >> (kTile - 1)) && s > 0, c0);
     __syncthreads();
@@ -918,15 +916,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
       if (join.ok)
         join.template before_runs<true>(sh.runs.P, fw_H, *reinterpret_cast<const uint64_t*>(fw_cut),
                                         p.states[tile * p.dim + join.ch]);
-    } else if (warp == kWarps - 1) {  // meanwhile: the next turn's rows, and the unit after that
-      const Unit next = sh.unit[(turn + 1) % 3];
+    } else if (warp == kWarps - 1) {  // meanwhile: the next turn's rows
+      const Unit next = sh.unit[(turn + 1) & 1];
       if (next.tile >= 0) find_rows(sh.rows[(turn + 1) & 1], p, (p.tiles - 1 - next.tile) * kTile, lane);
-      const Unit u = unit_of(p, __shfl_sync(0xffffffffu, ticket, 0));
-      if (lane == 0) sh.unit[(turn + 2) % 3] = u;
     }
     if (warp == kWarps - 2 && turn > 0) add_runs(last_tile, last_c0);
     __syncthreads();
-    copy(sh.unit[(turn + 1) % 3], turn + 1);
+    copy(sh.unit[(turn + 1) & 1], turn + 1);
     // states again, b <- the one before each row; dz
     const int64_t row_at = row0 * p.dim + ch;
     h = get<V>(fw_H[warp], lane);
