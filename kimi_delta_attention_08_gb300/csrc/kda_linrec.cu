@@ -294,17 +294,31 @@ __device__ __forceinline__ void step_of(pair x, pair r, pair i, pair A2, pair cr
   const pair m2 = scaled_m2(L2, a);
   b = pmul(pmul(pmul(m2, rsqrt_of(m2)), I), x);
 }
+// Two rows' steps: single channels pair up across them.
+__device__ __forceinline__ pair two(const Vals<1>& u, const Vals<1>& v) { return pr(u.v[0], v.v[0]); }
+__device__ __forceinline__ void apart(pair p, Vals<1>& u, Vals<1>& v) { u.v[0] = un(p).x, v.v[0] = un(p).y; }
 template <typename T, int V>
-__device__ __forceinline__ void step_of(const Vals<V>& x, const Vals<V>& r, const Vals<V>& i, const Gates<V>& c,
-                                        Vals<V>& a, Vals<V>& b) {
+__device__ __forceinline__ void step_of(const Vals<V> (&x)[2], const Vals<V> (&r)[2], const Vals<V> (&i)[2],
+                                        const Gates<V>& c, Vals<V>& a0, Vals<V>& b0, Vals<V>& a1, Vals<V>& b1) {
   if constexpr (V == 1) {
-    pair pa, pb;
-    step_of<T>(pr(x.v[0]), pr(r.v[0]), pr(i.v[0]), pr(c.A2.v[0]), pr(c.cr.v[0]), pr(c.ci.v[0]), pa, pb);
-    a.v[0] = un(pa).x, b.v[0] = un(pb).x;
+    pair a, b;
+    step_of<T>(two(x[0], x[1]), two(r[0], r[1]), two(i[0], i[1]), pr(c.A2.v[0]), pr(c.cr.v[0]), pr(c.ci.v[0]), a, b);
+    apart(a, a0, a1), apart(b, b0, b1);
   } else {
 #pragma unroll
-    for (int k = 0; k < V / 2; ++k)
-      step_of<T>(x.v[k], r.v[k], i.v[k], c.A2.v[k], c.cr.v[k], c.ci.v[k], a.v[k], b.v[k]);
+    for (int k = 0; k < V / 2; ++k) {
+      step_of<T>(x[0].v[k], r[0].v[k], i[0].v[k], c.A2.v[k], c.cr.v[k], c.ci.v[k], a0.v[k], b0.v[k]);
+      step_of<T>(x[1].v[k], r[1].v[k], i[1].v[k], c.A2.v[k], c.cr.v[k], c.ci.v[k], a1.v[k], b1.v[k]);
+    }
+  }
+}
+// `row(array, j)`: the values of x, r and i.
+template <typename T, int V, typename ROW>
+__device__ __forceinline__ void steps_of(ROW row, const Gates<V>& c, Vals<V> (&a)[kRows], Vals<V> (&b)[kRows]) {
+#pragma unroll
+  for (int j = 0; j < kRows; j += 2) {
+    const Vals<V> x[2] = {row(0, j), row(0, j + 1)}, r[2] = {row(1, j), row(1, j + 1)}, i[2] = {row(2, j), row(2, j + 1)};
+    step_of<T>(x, r, i, c, a[j], b[j], a[j + 1], b[j + 1]);
   }
 }
 template <typename T, int V>
@@ -553,8 +567,10 @@ struct Join {
 struct LinrecMaps {
   CUtensorMap x, r, i, z;
 };
+template <int V>
+constexpr int kFwdBlocks = V == 1 ? 3 : 2;  // per SM
 template <typename T, int V, bool OUT, bool TMA>
-__global__ void __launch_bounds__(32 * kWarps, 2)
+__global__ void __launch_bounds__(32 * kWarps, kFwdBlocks<V>)
     linrec_fwd_kernel(const __grid_constant__ LinrecParams p, const __grid_constant__ LinrecMaps maps) {
   constexpr int R = kRows, CH = 32 * V;
   using S = Slots<T, V>;
@@ -638,9 +654,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
     if (ch < p.dim) read_gates(c, p, ch);
     arrived(0, turn);
     Vals<V> a[R], b[R];
-#pragma unroll
-    for (int j = 0; j < R; ++j)
-      step_of<T>(S::get(mine, j), S::get(mine + S::kArray, j), S::get(mine + 2 * S::kArray, j), c, a[j], b[j]);
+    steps_of<T>([&](int k, int j) { return S::get(mine + k * S::kArray, j); }, c, a, b);
     if (bits.start && p.init) {  // a sequence's first step starts from its initial state
 #pragma unroll
       for (int j = 0; j < R; ++j)
@@ -734,8 +748,9 @@ __global__ void __launch_bounds__(256) linrec_step_kernel(LinrecParams p) {
     load_vals<T, V>(rr, p.r, t * p.r_s + ch);
     load_vals<T, V>(ri, p.i, t * p.i_s + ch);
     if (p.z) load_vals<T, V>(rz, p.z, t * p.z_s + ch);
-    Vals<V> a, b;
-    step_of<T>(vals_of(rx), vals_of(rr), vals_of(ri), c, a, b);
+    const Vals<V> x2[2] = {vals_of(rx), {}}, r2[2] = {vals_of(rr), {}}, i2[2] = {vals_of(ri), {}};
+    Vals<V> a, b, none, none2;
+    step_of<T>(x2, r2, i2, c, a, b, none, none2);
     h = fma_of(a, h, b);
     vals_to(p.z ? mul_of(h, silu_of<T>(vals_of(rz))) : h, h0);
     store_vals<T, V>(p.out, t * p.dim + ch, h0);
@@ -767,20 +782,26 @@ __device__ __forceinline__ void grads_of(pair x, pair r, pair i, pair A2, pair c
   e = pfma(pmul(g, in), pr(-kLn2 * 0x1p24f), pmul(pmul(pmul(g, L2), h), pr(kLn2)));
   dr = pmul(e, pmul(er, R));
 }
+// Of two rows; g: of each one's state.
 template <typename T, int V>
-__device__ __forceinline__ void grads_of(const Vals<V>& x, const Vals<V>& r, const Vals<V>& i, const Gates<V>& c,
-                                         const Vals<V>& a, const Vals<V>& h, Vals<V>& g, Vals<V>& e, Vals<V>& dx,
-                                         Vals<V>& dr, Vals<V>& di) {
+__device__ __forceinline__ void grads_of(const Vals<V> (&x)[2], const Vals<V> (&r)[2], const Vals<V> (&i)[2],
+                                         const Gates<V>& c, const Vals<V> (&a)[2], const Vals<V> (&h)[2],
+                                         const Vals<V> (&g)[2], Vals<V> (&e)[2], Vals<V> (&dx)[2], Vals<V> (&dr)[2],
+                                         Vals<V> (&di)[2]) {
   if constexpr (V == 1) {
-    pair gg = pr(g.v[0]), pe, px, pq, pi;
-    grads_of<T>(pr(x.v[0]), pr(r.v[0]), pr(i.v[0]), pr(c.A2.v[0]), pr(c.cr.v[0]), pr(c.ci.v[0]), pr(a.v[0]),
-                pr(h.v[0]), gg, pe, px, pq, pi);
-    g.v[0] = un(gg).x, e.v[0] = un(pe).x, dx.v[0] = un(px).x, dr.v[0] = un(pq).x, di.v[0] = un(pi).x;
+    pair pg = two(g[0], g[1]), pe, px, pq, pi;
+    grads_of<T>(two(x[0], x[1]), two(r[0], r[1]), two(i[0], i[1]), pr(c.A2.v[0]), pr(c.cr.v[0]), pr(c.ci.v[0]),
+                two(a[0], a[1]), two(h[0], h[1]), pg, pe, px, pq, pi);
+    apart(pe, e[0], e[1]), apart(px, dx[0], dx[1]), apart(pq, dr[0], dr[1]), apart(pi, di[0], di[1]);
   } else {
 #pragma unroll
-    for (int k = 0; k < V / 2; ++k)
-      grads_of<T>(x.v[k], r.v[k], i.v[k], c.A2.v[k], c.cr.v[k], c.ci.v[k], a.v[k], h.v[k], g.v[k], e.v[k], dx.v[k],
-                  dr.v[k], di.v[k]);
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) {
+        pair pg = g[q].v[k];
+        grads_of<T>(x[q].v[k], r[q].v[k], i[q].v[k], c.A2.v[k], c.cr.v[k], c.ci.v[k], a[q].v[k], h[q].v[k], pg,
+                    e[q].v[k], dx[q].v[k], dr[q].v[k], di[q].v[k]);
+      }
   }
 }
 template <int V>
@@ -862,9 +883,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
     // rows of no sequence count for nothing
     auto row = [&](int k, int j) { return all || (bits.live >> j & 1) ? S::get(mine + k * S::kArray, j) : splat<V>(0.f); };
     Vals<V> a[R], b[R], dy[R], dq[R];  // dq: dout silu'(z), what dz takes times h
+    steps_of<T>(row, c, a, b);
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      step_of<T>(row(0, j), row(1, j), row(2, j), c, a[j], b[j]);
       dy[j] = row(3, j);
       if (p.z) {
         const Vals<V> z = row(4, j), q = sigmoid<T>(z);
@@ -939,21 +960,30 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
     Vals<V> C = get<V>(sh.runs.H[warp], lane);
     Vals<V> se = splat<V>(0.f), sr = se, si = se;
 #pragma unroll
-    for (int j = R - 1; j >= 0; --j) {
-      Vals<V> e, dx, dr, di;
-      C = bits.last >> j & 1 ? dy[j] : add_of(C, dy[j]);
-      grads_of<T>(row(0, j), row(1, j), row(2, j), c, a[j], b[j], C, e, dx, dr, di);
-      if (!(bits.live >> j & 1)) e = dx = dr = di = splat<V>(0.f);
-      se = add_of(se, e), sr = add_of(sr, dr), si = add_of(si, di);
-      if (j < n) {
-        const int64_t to = row_at + (uint64_t)(uint32_t)p.dim * (uint32_t)j;
-        store_of<T>(p.dx, to, dx);
-        store_of<T>(p.dr, to, dr);
-        store_of<T>(p.di, to, di);
-        if (p.dinit && (bits.start >> j & 1)) {
+    for (int j = R - 2; j >= 0; j -= 2) {
+      Vals<V> g[2], e[2], dx[2], dr[2], di[2];
+#pragma unroll
+      for (int q = 1; q >= 0; --q) {
+        g[q] = bits.last >> (j + q) & 1 ? dy[j + q] : add_of(C, dy[j + q]);
+        C = mul_of(a[j + q], g[q]);
+        if (p.dinit && ok && (bits.start >> (j + q) & 1)) {
           float f[V];
           vals_to(C, f);
-          store_state<V>(p.dinit, (int64_t)rows.n[warp * R + j] * p.dim + ch, f, false);
+          store_state<V>(p.dinit, (int64_t)rows.n[warp * R + j + q] * p.dim + ch, f, false);
+        }
+      }
+      const Vals<V> x[2] = {row(0, j), row(0, j + 1)}, r[2] = {row(1, j), row(1, j + 1)}, i[2] = {row(2, j), row(2, j + 1)};
+      const Vals<V> a2[2] = {a[j], a[j + 1]}, h2[2] = {b[j], b[j + 1]};
+      grads_of<T>(x, r, i, c, a2, h2, g, e, dx, dr, di);
+#pragma unroll
+      for (int q = 1; q >= 0; --q) {
+        if (!all && !(bits.live >> (j + q) & 1)) e[q] = dx[q] = dr[q] = di[q] = splat<V>(0.f);
+        se = add_of(se, e[q]), sr = add_of(sr, dr[q]), si = add_of(si, di[q]);
+        if (j + q < n) {
+          const int64_t to = row_at + (uint64_t)(uint32_t)p.dim * (uint32_t)(j + q);
+          store_of<T>(p.dx, to, dx[q]);
+          store_of<T>(p.dr, to, dr[q]);
+          store_of<T>(p.di, to, di[q]);
         }
       }
     }
@@ -1115,7 +1145,7 @@ cudaError_t launch_fwd_of(const LinrecParams& p, bool tma, cudaStream_t stream) 
   const int smem = (p.z && OUT ? 4 : 3) * Slots<T, V>::kArray;
   int sms = 0;
   if (sm_count(&sms) != KDA_OK) return cudaErrorUnknown;
-  const unsigned grid = std::min(p.units, 2u * sms);
+  const unsigned grid = std::min(p.units, (unsigned)(kFwdBlocks<V> * sms));
   cudaError_t e = cudaSuccess;
   if constexpr (V * sizeof(T) == 8) {
     if (tma) {
