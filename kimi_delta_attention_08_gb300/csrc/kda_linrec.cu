@@ -34,12 +34,13 @@ namespace {
 using namespace rows;
 
 constexpr int kWarps = 8;
-constexpr int kRows = 8, kTile = kWarps * kRows;  // rows per warp and tile
+constexpr int kRowsF = 16, kRowsB = 8;            // rows of a run: forward, backward
+constexpr int kTileF = kWarps * kRowsF, kTileB = kWarps * kRowsB;
 constexpr int kGroup = 16;                        // tiles of a group
 constexpr int kStepTokens = 8;                    // prompts up to this length: the step kernel
 constexpr uint64_t kWaitNs = 500000000ull;
 constexpr uint64_t kUnset = ~0ull;
-static_assert(kTile == KDA_LINREC_CHUNK, "one saved state per tile");
+static_assert(kTileB == KDA_LINREC_CHUNK && kTileF == 2 * kTileB, "one and two saved states per tile");
 
 struct LinrecParams {
   const void *x, *r, *i, *z, *dout;
@@ -145,7 +146,7 @@ __device__ __forceinline__ void copy_own(uint32_t slot, const void* p, bool ther
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(slot), "h"(v) : "memory");
   }
 }
-template <typename T, int V>
+template <typename T, int V, int kRows>
 struct Slots {
   static constexpr int kBytes = V * (int)sizeof(T), kRow = 32 * kBytes;  // of a lane, of a warp's row
   static constexpr int kRun = kRows * kRow, kArray = kWarps * kRun;      // of a run, of a tile, of one array
@@ -209,37 +210,39 @@ __device__ __forceinline__ void store_vals(void* p, int64_t at, const float (&f)
 }
 
 // Rows of a tile: every row's sequence, and a bit per row.
+template <int TILE>
 struct TileRows {
-  int n[kTile];
-  uint64_t start, last, live;    // first row of its sequence, last one, of a sequence at all
+  int n[TILE];
+  uint32_t start[TILE / 32], last[TILE / 32], live[TILE / 32];  // first row of its sequence, last one, of any
   int64_t bos, eos;              // of the first row's sequence, of the last row's
 };
-__device__ __forceinline__ void find_rows(TileRows& s, const LinrecParams& p, int64_t row0, int lane) {
-  static_assert(kTile == 64, "two rows per lane, a bit each");
-  uint64_t start = 0, last = 0, alive = 0;
+template <int TILE>
+__device__ __forceinline__ void find_rows(TileRows<TILE>& s, const LinrecParams& p, int64_t row0, int lane) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < TILE / 32; ++h) {
     const int64_t t = row0 + 32 * h + lane;
     int n = 0;
     int64_t bos = 0, eos = 0;
     const bool live = row_sequence(p, t, n, bos, eos);
     s.n[32 * h + lane] = n;
-    start |= (uint64_t)__ballot_sync(0xffffffffu, live && t == bos) << (32 * h);
-    last |= (uint64_t)__ballot_sync(0xffffffffu, live && t + 1 == eos) << (32 * h);
-    alive |= (uint64_t)__ballot_sync(0xffffffffu, live) << (32 * h);
+    const unsigned start = __ballot_sync(0xffffffffu, live && t == bos);
+    const unsigned last = __ballot_sync(0xffffffffu, live && t + 1 == eos);
+    const unsigned alive = __ballot_sync(0xffffffffu, live);
+    if (lane == 0) s.start[h] = start, s.last[h] = last, s.live[h] = alive;
     if (h == 0 && lane == 0) s.bos = bos;
-    if (h == 1 && lane == 31) s.eos = eos;
+    if (h == TILE / 32 - 1 && lane == 31) s.eos = eos;
   }
-  if (lane == 0) s.start = start, s.last = last, s.live = alive;
 }
 // A run's rows: bit j for row j.
 struct RowBits {
   unsigned start, last, live;
 };
-__device__ __forceinline__ RowBits run_rows(const TileRows& s, int warp) {
-  constexpr unsigned mask = (1u << kRows) - 1;
-  return {(unsigned)(s.start >> (warp * kRows)) & mask, (unsigned)(s.last >> (warp * kRows)) & mask,
-          (unsigned)(s.live >> (warp * kRows)) & mask};
+template <int TILE>
+__device__ __forceinline__ RowBits run_rows(const TileRows<TILE>& s, int warp) {
+  constexpr int R = TILE / kWarps;
+  constexpr unsigned mask = (1u << R) - 1;
+  const int at = warp * R / 32, by = warp * R % 32;
+  return {s.start[at] >> by & mask, s.last[at] >> by & mask, s.live[at] >> by & mask};
 }
 
 constexpr float kBiasScale16 = -kLog2e, kBiasScale32 = 1.f;
@@ -313,7 +316,7 @@ __device__ __forceinline__ void step_of(const Vals<V> (&x)[2], const Vals<V> (&r
   }
 }
 // `row(array, j)`: the values of x, r and i.
-template <typename T, int V, typename ROW>
+template <typename T, int V, int kRows, typename ROW>
 __device__ __forceinline__ void steps_of(ROW row, const Gates<V>& c, Vals<V> (&a)[kRows], Vals<V> (&b)[kRows]) {
 #pragma unroll
   for (int j = 0; j < kRows; j += 2) {
@@ -353,19 +356,19 @@ __device__ __forceinline__ Unit unit_of(const LinrecParams& p, unsigned ticket) 
 }
 // What a block's warps share.  This turn's unit and rows and the next one's alternate, so that
 // two barriers a turn are enough: the runs are there, and the states before them are.
-template <int V>
+template <int V, int TILE>
 struct BlockShared {
   Runs<V> runs;
-  TileRows rows[2];
+  TileRows<TILE> rows[2];
   Unit unit[2];
 };
 // The first turn's unit and rows.
-template <int V, bool FORWARD>
-__device__ __forceinline__ void start_block(const LinrecParams& p, BlockShared<V>& sh, int warp, int lane) {
+template <bool FORWARD, int V, int TILE>
+__device__ __forceinline__ void start_block(const LinrecParams& p, BlockShared<V, TILE>& sh, int warp, int lane) {
   if (threadIdx.x == 0) sh.unit[0] = unit_of(p, atomicAdd(p.ticket, 1u));
   __syncthreads();
   const int64_t s = sh.unit[0].tile;
-  if (warp == 0 && s >= 0) find_rows(sh.rows[0], p, (FORWARD ? s : p.tiles - 1 - s) * kTile, lane);
+  if (warp == 0 && s >= 0) find_rows(sh.rows[0], p, (FORWARD ? s : p.tiles - 1 - s) * TILE, lane);
   __syncthreads();
 }
 template <int V>
@@ -572,28 +575,28 @@ constexpr int kFwdBlocks = V == 1 ? 3 : 2;  // per SM
 template <typename T, int V, bool OUT, bool TMA>
 __global__ void __launch_bounds__(32 * kWarps, kFwdBlocks<V>)
     linrec_fwd_kernel(const __grid_constant__ LinrecParams p, const __grid_constant__ LinrecMaps maps) {
-  constexpr int R = kRows, CH = 32 * V;
-  using S = Slots<T, V>;
+  constexpr int R = kRowsF, CH = 32 * V;
+  using S = Slots<T, V, R>;
   extern __shared__ __align__(128) uint8_t slots[];  // x, r, i, z
-  __shared__ __align__(16) BlockShared<V> sh;
+  __shared__ __align__(16) BlockShared<V, kTileF> sh;
   __shared__ uint64_t full[2][kWarps];               // x, r, i are there; z is
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (TMA && threadIdx.x < 2 * kWarps) {
     ptx::mbar_init(&full[0][threadIdx.x], 1);
     ptx::fence_mbar_init();
   }
-  start_block<V, true>(p, sh, warp, lane);
+  start_block<true>(p, sh, warp, lane);
   uint8_t* const run = slots + warp * S::kRun;
   const uint8_t* const mine = run + lane * S::kBytes;
   auto place = [&](const Unit& u, int64_t& row0, int& ch) {  // the rows that exist
-    row0 = (int64_t)u.tile * kTile + warp * R;
+    row0 = (int64_t)u.tile * kTileF + warp * R;
     ch = u.block * CH + lane * V;
     return ch < p.dim && u.tile >= 0 ? (int)max((int64_t)0, min((int64_t)R, p.total - row0)) : 0;
   };
   auto copy = [&](const Unit& u) {
     if constexpr (TMA) {
       if (u.tile >= 0 && lane == 0) {
-        const int row0 = u.tile * kTile + warp * R, c0 = u.block * CH;
+        const int row0 = u.tile * kTileF + warp * R, c0 = u.block * CH;
         ptx::mbar_arrive_expect_tx(&full[0][warp], 3 * S::kRun);
         ptx::tma_load_2d(run, &maps.x, &full[0][warp], c0, row0);
         ptx::tma_load_2d(run + S::kArray, &maps.r, &full[0][warp], c0, row0);
@@ -617,7 +620,7 @@ __global__ void __launch_bounds__(32 * kWarps, kFwdBlocks<V>)
     if constexpr (TMA) {
       if (want && lane == 0) {
         ptx::mbar_arrive_expect_tx(&full[1][warp], S::kRun);
-        ptx::tma_load_2d(run + 3 * S::kArray, &maps.z, &full[1][warp], u.block * CH, u.tile * kTile + warp * R);
+        ptx::tma_load_2d(run + 3 * S::kArray, &maps.z, &full[1][warp], u.block * CH, u.tile * kTileF + warp * R);
       }
     } else {
       if (want) {
@@ -648,7 +651,7 @@ __global__ void __launch_bounds__(32 * kWarps, kFwdBlocks<V>)
     const bool ok = place(unit, row0, ch) > 0;
     unsigned ticket = 0;
     if (threadIdx.x == 32 * kWarps - 32) ticket = atomicAdd(p.ticket, 1u);
-    const TileRows& rows = sh.rows[turn & 1];
+    const auto& rows = sh.rows[turn & 1];
     const RowBits bits = run_rows(rows, warp);
     Gates<V> c = {};
     if (ch < p.dim) read_gates(c, p, ch);
@@ -677,8 +680,8 @@ __global__ void __launch_bounds__(32 * kWarps, kFwdBlocks<V>)
     put<V>(sh.runs.H[warp], lane, h);
     if (lane == 0) sh.runs.cut[warp] = bits.start != 0;
     if (threadIdx.x == 32 * kWarps - 32) sh.unit[(turn + 1) & 1] = unit_of(p, ticket);
-    const int64_t edge = rows.bos / kTile;
-    Join<V, true> join(p, s, edge, (rows.live & 1) && !(rows.start & 1) && s > 0, c0);
+    const int64_t edge = rows.bos / kTileF;
+    Join<V, true> join(p, s, edge, (rows.live[0] & 1) && !(rows.start[0] & 1) && s > 0, c0);
     __syncthreads();
     const Unit next = sh.unit[(turn + 1) & 1];
     copy(next);
@@ -687,10 +690,14 @@ __global__ void __launch_bounds__(32 * kWarps, kFwdBlocks<V>)
     __syncthreads();
     if (join.part == 0 && join.ok) {
       const float X = join.finish(sh.runs, edge, Pt, Ht);
-      if (p.states) p.states[s * p.dim + join.ch] = X;
+      if (p.states) {  // before the tile's first row, and before its second half
+        p.states[2 * s * p.dim + join.ch] = X;
+        if ((2 * s + 1) * KDA_LINREC_CHUNK < p.total)
+          p.states[(2 * s + 1) * p.dim + join.ch] = sh.runs.H[kWarps / 2][join.c];
+      }
     }
     if (warp == kWarps - 1 && next.tile >= 0)  // meanwhile: the next turn's rows
-      find_rows(sh.rows[(turn + 1) & 1], p, (int64_t)next.tile * kTile, lane);
+      find_rows(sh.rows[(turn + 1) & 1], p, (int64_t)next.tile * kTileF, lane);
     __syncthreads();
     if constexpr (OUT) {
       if (p.z) arrived(1, turn);
@@ -817,20 +824,20 @@ __device__ __forceinline__ void store_of(void* p, int64_t at, const Vals<V>& v) 
 
 template <typename T, int V>
 __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams p) {
-  constexpr int R = kRows, CH = 32 * V;
-  using S = Slots<T, V>;
+  constexpr int R = kRowsB, CH = 32 * V;
+  using S = Slots<T, V, R>;
   constexpr int kBuffer = 5 * S::kArray + S::kGates;  // x, r, i, dout, z, gates; two by turns
   extern __shared__ __align__(128) uint8_t slots[];
-  __shared__ __align__(16) BlockShared<V> sh;         // runs of the gradients, last run first
+  __shared__ __align__(16) BlockShared<V, kTileB> sh;         // runs of the gradients, last run first
   __shared__ __align__(16) float fw_H[kWarps][CH];    // of the states; the products are the same
   __shared__ __align__(8) unsigned char fw_cut[kWarps];
   __shared__ __align__(16) float sums[3][kWarps][CH];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  start_block<V, false>(p, sh, warp, lane);
+  start_block<false>(p, sh, warp, lane);
   const uint8_t* const mine0 = slots + warp * S::kRun + lane * S::kBytes;
   const uint32_t at0 = ptx::smem_u32(mine0), at_gates0 = ptx::smem_u32(slots + 5 * S::kArray + threadIdx.x * V * 4);
   auto place = [&](const Unit& u, int64_t& row0, int& ch) {  // the rows that exist
-    row0 = (p.tiles - 1 - u.tile) * kTile + warp * R;
+    row0 = (p.tiles - 1 - u.tile) * kTileB + warp * R;
     ch = u.block * CH + lane * V;
     return ch < p.dim ? (int)max((int64_t)0, min((int64_t)R, p.total - row0)) : 0;
   };
@@ -873,7 +880,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
     int ch;
     const int n = place(unit, row0, ch);
     const bool ok = n > 0;
-    const TileRows& rows = sh.rows[turn & 1];
+    const auto& rows = sh.rows[turn & 1];
     const RowBits bits = run_rows(rows, warp);
     const uint8_t* const mine = mine0 + (turn & 1) * kBuffer;
     ptx::cp_async_wait_all();
@@ -925,8 +932,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
     put<V>(sh.runs.H[warp], lane, h);
     if (lane == 0) sh.runs.cut[warp] = bits.last != 0, fw_cut[warp] = bits.start != 0;
     if (threadIdx.x == 32 * kWarps - 32) sh.unit[(turn + 1) & 1] = unit_of(p, ticket);
-    const int64_t edge = p.tiles - 1 - (rows.eos - 1) / kTile;
-    Join<V, false> join(p, s, edge, (rows.live >> (kTile - 1)) && !(rows.last >> (kTile - 1)) && s > 0, c0);
+    const int64_t edge = p.tiles - 1 - (rows.eos - 1) / kTileB;
+    Join<V, false> join(p, s, edge, (rows.live[1] >> 31) && !(rows.last[1] >> 31) && s > 0, c0);
     __syncthreads();
     float Pj, Hj, Pt, Ht;
     join.parts(sh.runs, Pj, Hj, Pt, Ht);
@@ -939,7 +946,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
                                         p.states[tile * p.dim + join.ch]);
     } else if (warp == kWarps - 1) {  // meanwhile: the next turn's rows
       const Unit next = sh.unit[(turn + 1) & 1];
-      if (next.tile >= 0) find_rows(sh.rows[(turn + 1) & 1], p, (p.tiles - 1 - next.tile) * kTile, lane);
+      if (next.tile >= 0) find_rows(sh.rows[(turn + 1) & 1], p, (p.tiles - 1 - next.tile) * kTileB, lane);
     }
     if (warp == kWarps - 2 && turn > 0) add_runs(last_tile, last_c0);
     __syncthreads();
@@ -1040,9 +1047,9 @@ __global__ void __launch_bounds__(256) linrec_setup_kernel(SetupParams p) {
 // ------------------------------------------------------------------- host --
 bool al_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-int64_t tiles_of(int64_t total) { return (total + kTile - 1) / kTile; }
-size_t join_bytes(int64_t total, int32_t dim) {  // what tiles publish
-  const size_t tiles = (size_t)tiles_of(total);
+int64_t tiles_of(int64_t total, int rows) { return (total + rows - 1) / rows; }
+size_t join_bytes(int64_t total, int32_t dim, int rows) {  // what tiles publish
+  const size_t tiles = (size_t)tiles_of(total, rows);
   return up256(tiles * dim * 8) + up256(tiles / kGroup * dim * 8) + up256(tiles / kGroup * dim * 4);
 }
 
@@ -1095,18 +1102,18 @@ void lanes_for(int& lanes, const void* p, size_t e) {  // contiguous rows
 }
 
 // Tiles and channel blocks of a pass, and its part of the workspace.
-bool plan_pass(LinrecParams& p, int lanes, uint8_t*& ws) {
-  p.tiles = tiles_of(p.total);
+bool plan_pass(LinrecParams& p, int lanes, int rows, uint8_t*& ws) {
+  p.tiles = tiles_of(p.total, rows);
   p.blocks = (p.dim + 32 * lanes - 1) / (32 * lanes);
   p.agg = reinterpret_cast<uint64_t*>(ws);
   p.group_agg = reinterpret_cast<uint64_t*>(ws + up256((size_t)p.tiles * p.dim * 8));
   p.ends = reinterpret_cast<unsigned*>(reinterpret_cast<uint8_t*>(p.group_agg) +
                                        up256((size_t)(p.tiles / kGroup) * p.dim * 8));
-  ws += join_bytes(p.total, p.dim);
-  const bool whole = !p.cu && p.T > 0 && p.T % kTile == 0;
+  ws += join_bytes(p.total, p.dim, rows);
+  const bool whole = !p.cu && p.T > 0 && p.T % rows == 0;
   p.units = (unsigned)(p.tiles * p.blocks);
   p.strips = whole ? (unsigned)(p.total / p.T) : 1u;
-  p.strip_tiles = whole ? (unsigned)(p.T / kTile) : (unsigned)p.tiles;
+  p.strip_tiles = whole ? (unsigned)(p.T / rows) : (unsigned)p.tiles;
   return p.tiles * p.blocks < (int64_t(1) << 31);
 }
 
@@ -1135,19 +1142,19 @@ cudaError_t launch_tiles(K kernel, bool (&done)[64], int smem, int blocks, const
 template <typename T>
 cudaError_t rows_map(CUtensorMap* m, const void* p, const LinrecParams& q, uint32_t stride, int channels) {
   const uint64_t dims[2] = {(uint64_t)q.dim, (uint64_t)q.total}, strides[1] = {(uint64_t)stride * sizeof(T)};
-  const uint32_t box[2] = {(uint32_t)channels, (uint32_t)kRows};
+  const uint32_t box[2] = {(uint32_t)channels, (uint32_t)kRowsF};
   return encode_tiled_map(m, sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p,
                           dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 template <typename T, int V, bool OUT>
 cudaError_t launch_fwd_of(const LinrecParams& p, bool tma, cudaStream_t stream) {
   LinrecMaps maps = {};
-  const int smem = (p.z && OUT ? 4 : 3) * Slots<T, V>::kArray;
+  const int smem = (p.z && OUT ? 4 : 3) * Slots<T, V, kRowsF>::kArray;
   int sms = 0;
   if (sm_count(&sms) != KDA_OK) return cudaErrorUnknown;
   const unsigned grid = std::min(p.units, (unsigned)(kFwdBlocks<V> * sms));
   cudaError_t e = cudaSuccess;
-  if constexpr (V * sizeof(T) == 8) {
+  if constexpr (V * sizeof(T) == 4) {
     if (tma) {
       static bool done[64];
       e = rows_map<T>(&maps.x, p.x, p, p.x_s, 32 * V);
@@ -1155,7 +1162,7 @@ cudaError_t launch_fwd_of(const LinrecParams& p, bool tma, cudaStream_t stream) 
       if (e == cudaSuccess) e = rows_map<T>(&maps.i, p.i, p, p.i_s, 32 * V);
       if (e == cudaSuccess) e = rows_map<T>(&maps.z, p.z, p, p.z_s, 32 * V);
       auto kernel = linrec_fwd_kernel<T, V, OUT, true>;
-      if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), 4 * Slots<T, V>::kArray, done);
+      if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), 4 * Slots<T, V, kRowsF>::kArray, done);
       if (e != cudaSuccess) return e;
       kernel<<<grid, 32 * kWarps, smem, stream>>>(p, maps);
       return cudaGetLastError();
@@ -1163,7 +1170,7 @@ cudaError_t launch_fwd_of(const LinrecParams& p, bool tma, cudaStream_t stream) 
   }
   static bool done[64];
   auto kernel = linrec_fwd_kernel<T, V, OUT, false>;
-  e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), 4 * Slots<T, V>::kArray, done);
+  e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), 4 * Slots<T, V, kRowsF>::kArray, done);
   if (e != cudaSuccess) return e;
   kernel<<<grid, 32 * kWarps, smem, stream>>>(p, maps);
   return cudaGetLastError();
@@ -1171,21 +1178,15 @@ cudaError_t launch_fwd_of(const LinrecParams& p, bool tma, cudaStream_t stream) 
 template <typename T, int V>
 cudaError_t launch_bwd_of(const LinrecParams& p, cudaStream_t stream) {
   static bool done[64];
-  return launch_tiles(linrec_bwd_kernel<T, V>, done, 2 * (5 * Slots<T, V>::kArray + Slots<T, V>::kGates), 2, p, stream);
+  return launch_tiles(linrec_bwd_kernel<T, V>, done, 2 * (5 * Slots<T, V, kRowsB>::kArray + Slots<T, V, kRowsB>::kGates), 2, p, stream);
 }
 
 // Channels per thread: 8 bytes of a row where its alignment allows, 4 in the backward, which
 // keeps more of each value in registers.
-constexpr int kFwd16 = 4, kFwd32 = 2, kBwd16 = 2, kBwd32 = 1;
-int lanes_of(int lanes, bool f32, bool bwd) {
-  return std::min(lanes, bwd ? (f32 ? kBwd32 : kBwd16) : f32 ? kFwd32 : kFwd16);
-}
+int lanes_of(int lanes, bool f32) { return f32 ? 1 : std::min(lanes, 2); }
 template <bool OUT>
 cudaError_t launch_fwd(const LinrecParams& p, bool f32, int lanes, bool tma, cudaStream_t stream) {
-  if (f32)
-    return lanes == 2 ? launch_fwd_of<float, 2, OUT>(p, tma, stream)
-                      : launch_fwd_of<float, 1, OUT>(p, tma, stream);
-  return lanes == 4   ? launch_fwd_of<bf16, 4, OUT>(p, tma, stream)
+  return f32          ? launch_fwd_of<float, 1, OUT>(p, tma, stream)
          : lanes == 2 ? launch_fwd_of<bf16, 2, OUT>(p, tma, stream)
                       : launch_fwd_of<bf16, 1, OUT>(p, tma, stream);
 }
@@ -1195,7 +1196,7 @@ size_t states_bytes(int64_t total, int32_t dim) {
 }
 size_t gates_bytes(int32_t dim) { return up256((size_t)dim * 3 * sizeof(float)); }
 size_t fwd_bytes(const LinrecParams& p) {
-  return KDA_STATUS_BYTES + gates_bytes(p.dim) + join_bytes(p.total, p.dim);
+  return KDA_STATUS_BYTES + gates_bytes(p.dim) + join_bytes(p.total, p.dim, kTileF);
 }
 
 }  // namespace
@@ -1226,11 +1227,11 @@ kda_status kda_linrec_bwd_get_workspace_size(const kda_linrec_problem* problem, 
   LinrecParams p = {};
   const kda_status st = check_sizes(problem, p);
   if (st != KDA_OK) return st;
-  const int64_t tiles = tiles_of(p.total);
-  *bytes = KDA_STATUS_BYTES + gates_bytes(p.dim) + join_bytes(p.total, p.dim) +
+  const int64_t tiles = tiles_of(p.total, kTileB);
+  *bytes = KDA_STATUS_BYTES + gates_bytes(p.dim) + join_bytes(p.total, p.dim, kTileB) +
            up256((size_t)tiles * 3 * p.dim * sizeof(float));
   if (!have_states)
-    *bytes += join_bytes(p.total, p.dim) + up256(states_bytes(p.total, p.dim));
+    *bytes += join_bytes(p.total, p.dim, kTileF) + up256(states_bytes(p.total, p.dim));
   return KDA_OK;
 }
 
@@ -1269,10 +1270,10 @@ kda_status kda_linrec_fwd(const kda_linrec_problem* problem, void* out, void* fi
   }
   uint8_t* ws = static_cast<uint8_t*>(workspace) + KDA_STATUS_BYTES;
   p.gates = reinterpret_cast<float*>(ws), ws += gates_bytes(p.dim);
-  lanes = lanes_of(lanes, f32, false);
-  if (!plan_pass(p, lanes, ws)) return KDA_ERR_INVALID_SHAPE;
+  lanes = lanes_of(lanes, f32);
+  if (!plan_pass(p, lanes, kTileF, ws)) return KDA_ERR_INVALID_SHAPE;
   p.ticket = p.status + 1;
-  cudaError_t e = launch_setup(p, f32, p.agg, join_bytes(p.total, p.dim), p.init, p.state_bf16,
+  cudaError_t e = launch_setup(p, f32, p.agg, join_bytes(p.total, p.dim, kTileF), p.init, p.state_bf16,
                                p.fin == p.init ? nullptr : p.fin, p.state_bf16, stream);
   if (e == cudaSuccess && p.total > 0) e = launch_fwd<true>(p, f32, lanes, tma, stream);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
@@ -1313,9 +1314,9 @@ kda_status kda_linrec_bwd(const kda_linrec_problem* problem, const void* dout, c
   uint8_t* const published_at = ws;
   LinrecParams f = p;
   f.stall = 0;
-  const int back = lanes_of(lanes, f32, true);
-  bool fits = plan_pass(p, back, ws);
-  if (!chunk_states) fits = fits && plan_pass(f, lanes_of(lanes, f32, false), ws);
+  const int back = lanes_of(lanes, f32);
+  bool fits = plan_pass(p, back, kTileB, ws);
+  if (!chunk_states) fits = fits && plan_pass(f, lanes_of(lanes, f32), kTileF, ws);
   if (!fits) return KDA_ERR_INVALID_SHAPE;
   const size_t published_bytes = (size_t)(ws - published_at);
   p.part = reinterpret_cast<float*>(ws);
@@ -1328,7 +1329,7 @@ kda_status kda_linrec_bwd(const kda_linrec_problem* problem, const void* dout, c
   cudaError_t err = launch_setup(p, f32, published_at, published_bytes, dfinal_state, p.state_bf16,
                                  dinitial_state, false, stream);
   if (err == cudaSuccess && p.total > 0) {
-    if (!chunk_states) err = launch_fwd<false>(f, f32, lanes_of(lanes, f32, false), tma, stream);
+    if (!chunk_states) err = launch_fwd<false>(f, f32, lanes_of(lanes, f32), tma, stream);
     if (err == cudaSuccess)
       err = f32     ? launch_bwd_of<float, 1>(p, stream)
             : back == 2 ? launch_bwd_of<bf16, 2>(p, stream)
