@@ -29,16 +29,10 @@ namespace {
 
 using namespace rows;
 
-constexpr int kTileM = 256, kTileK = 64;
-constexpr int kHalf = 128;                       // rows of A in each CTA
-constexpr uint32_t kOperandA = kHalf * kTileK * 2;  // its bytes in a stage
-// Tiles of N = 256 or 128 columns: half of them, of B, in each CTA.
-template <int N>
-struct Tile {
-  static constexpr int kHalfN = N / 2, kStages = N == 256 ? 6 : 8;
-  static constexpr uint32_t kOperandB = kHalfN * kTileK * 2, kStage = kOperandA + kOperandB;
-  static constexpr uint32_t kSmem = kStages * kStage + 1024;
-};
+constexpr int kTileM = 256, kTileN = 256, kTileK = 64, kStages = 6;
+constexpr int kHalf = 128;                       // rows of A, columns of B in each CTA
+constexpr uint32_t kOperand = kHalf * kTileK * 2, kStage = 2 * kOperand;  // bytes in a stage
+constexpr uint32_t kSmem = kStages * kStage + 1024;
 constexpr uint64_t kWaitNs = 500000000ull;
 constexpr int kEpilogueWarp = 4;                 // warps 4 .. 7
 
@@ -91,14 +85,12 @@ __device__ __forceinline__ void store8(bf16* p, const float* f) {
       make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
 }
 
-template <int PASS, int N>
+template <int PASS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     glu_kernel(const __grid_constant__ GluParams p) {
   constexpr bool A_MN = PASS == kWeights, B_MN = PASS == kInput || PASS == kWeights;
   constexpr bool DUAL = PASS == kForward || PASS == kRecompute;
   constexpr int SUMS = PASS == kInput ? 2 : 1;
-  using L = Tile<N>;
-  constexpr int kStages = L::kStages, kHalfN = L::kHalfN;
   extern __shared__ uint8_t raw[];
   uint8_t* const tiles = ptx::smem_align1024(raw);
   __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2];
@@ -114,7 +106,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     for (int b = 0; b < 2; ++b) ptx::mbar_init(&tfull[b], 1), ptx::mbar_init(&tempty[b], 8);
     ptx::fence_mbar_init();
   }
-  if (warp == 2) ptx::tmem_alloc_pair(&tmem_at, 2 * N);
+  if (warp == 2) ptx::tmem_alloc_pair(&tmem_at, 2 * kTileN);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::cluster_sync();
@@ -131,26 +123,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
       for (int kb = 0; kb < blocks && ok; ++kb) {
         ok = ptx::mbar_wait(&empty[stage], parity, kWaitNs);
         if (!ok) break;
-        if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * L::kStage);
+        if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kStage);
         const uint32_t bar = ptx::cluster_addr(&full[stage], 0);
-        uint8_t* const A = tiles + stage * L::kStage;
-        uint8_t* const B = A + kOperandA;
+        uint8_t* const A = tiles + stage * kStage;
+        uint8_t* const B = A + kOperand;
         const int part = SUMS == 2 && kb >= p.k_blocks, k0 = (kb - part * p.k_blocks) * kTileK;
         if constexpr (A_MN) {
           // tiles of the gate's gradient first, then of the other's
           const int half = p.m_tiles / 2, which = m >= half;
           const int at = (m - which * half) * kTileM + rank * kHalf;
           ptx::tma_load_2d_pair(A, &p.a[which], bar, at, k0);
-          ptx::tma_load_2d_pair(A + kOperandA / 2, &p.a[which], bar, at + 64, k0);
+          ptx::tma_load_2d_pair(A + kOperand / 2, &p.a[which], bar, at + 64, k0);
         } else {
           ptx::tma_load_2d_pair(A, &p.a[part], bar, k0, m * kTileM + (int)rank * kHalf);
         }
         if constexpr (B_MN) {
-          const int at = n * N + rank * kHalfN;
+          const int at = n * kTileN + rank * kHalf;
           ptx::tma_load_2d_pair(B, &p.b[part], bar, at, k0);
-          if constexpr (N == 256) ptx::tma_load_2d_pair(B + L::kOperandB / 2, &p.b[part], bar, at + 64, k0);
+          ptx::tma_load_2d_pair(B + kOperand / 2, &p.b[part], bar, at + 64, k0);
         } else {
-          ptx::tma_load_2d_pair(B, &p.b[rank], bar, k0, n * kHalfN);
+          ptx::tma_load_2d_pair(B, &p.b[rank], bar, k0, n * kHalf);
         }
         if (++stage == kStages) stage = 0, parity ^= 1;
       }
@@ -163,7 +155,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     if (!ok) failed = 1;
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // products of the pair
-    constexpr uint32_t idesc = ptx::idesc_bf16_f32(kTileM, N, A_MN, B_MN);
+    constexpr uint32_t idesc = ptx::idesc_bf16_f32(kTileM, kTileN, A_MN, B_MN);
     constexpr uint32_t a_step = A_MN ? 16 * 128 : 32, b_step = B_MN ? 16 * 128 : 32;
     uint32_t stage = 0, parity = 0, buf = 0, tparity = 1;
     bool ok = true;
@@ -174,11 +166,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
         ok = ptx::mbar_wait(&full[stage], parity, kWaitNs);
         if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t A = ptx::smem_u32(tiles + stage * L::kStage), B = A + kOperandA;
+        const uint32_t A = ptx::smem_u32(tiles + stage * kStage), B = A + kOperand;
 #pragma unroll
         for (int k = 0; k < kTileK / 16; ++k)
-          ptx::mma_bf16_ss_pair(tmem + buf * N, ptx::sw128_desc(A + k * a_step, kOperandA / 2, 1024),
-                                ptx::sw128_desc(B + k * b_step, kOperandA / 2, 1024), idesc, kb + k > 0);
+          ptx::mma_bf16_ss_pair(tmem + buf * kTileN, ptx::sw128_desc(A + k * a_step, kOperand / 2, 1024),
+                                ptx::sw128_desc(B + k * b_step, kOperand / 2, 1024), idesc, kb + k > 0);
         ptx::mma_commit_pair(&empty[stage]);
         if (++stage == kStages) stage = 0, parity ^= 1;
       }
@@ -210,16 +202,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
       }
       row += rank * kHalf + w * 32 + lane;
       const bool in = row < p.M;
-      const uint32_t acc = tmem + buf * N + ((uint32_t)(w * 32) << 16);
+      const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(w * 32) << 16);
 #pragma unroll 1
-      for (int c = 0; c < (DUAL ? kHalfN : N); c += 32) {
+      for (int c = 0; c < (DUAL ? kHalf : kTileN); c += 32) {
         uint32_t v[32];
         ptx::tmem_ld32(acc + c, v);
-        const int64_t col = (int64_t)n * (DUAL ? kHalfN : N) + c;
+        const int64_t col = (int64_t)n * (DUAL ? kHalf : kTileN) + c;
         const int64_t at = row * p.N + col;
         if constexpr (DUAL) {
           uint32_t q[32];
-          ptx::tmem_ld32(acc + kHalfN + c, q);
+          ptx::tmem_ld32(acc + kHalf + c, q);
           ptx::tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 32; j += 8) {
@@ -277,7 +269,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
   ptx::tc_fence_before();
   ptx::cluster_sync();
   ptx::tc_fence_after();
-  if (warp == 2) ptx::tmem_dealloc_pair(tmem, 2 * N);
+  if (warp == 2) ptx::tmem_dealloc_pair(tmem, 2 * kTileN);
 }
 
 // ------------------------------------------------------------- few rows --
@@ -444,30 +436,16 @@ cudaError_t map_of(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, in
                           CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int PASS, int N>
-cudaError_t launch_of(const GluParams& p, int sms, cudaStream_t stream) {
+template <int PASS>
+cudaError_t launch(const GluParams& p, cudaStream_t stream) {
   static bool done[64];
-  constexpr int smem = Tile<N>::kSmem;
-  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(glu_kernel<PASS, N>), smem, done);
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(glu_kernel<PASS>), kSmem, done);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles, pairs = tiles < sms / 2 ? tiles : sms / 2;
-  glu_kernel<PASS, N><<<(unsigned)(2 * pairs), 256, smem, stream>>>(p);
-  return cudaGetLastError();
-}
-// B's maps depend on the tiles' width: `maps(half of it)` makes them.  Narrow tiles take where
-// wide ones leave more of the last turn over the pairs unused than their lower rate costs.
-template <int PASS, typename MAPS>
-cudaError_t launch(GluParams& p, int64_t columns, MAPS maps, cudaStream_t stream) {
   int sms = 0;
   if (sm_count(&sms) != KDA_OK) return cudaErrorUnknown;
-  const int64_t pairs = sms / 2;
-  const int64_t wide = up(columns, 256), narrow = up(columns, 128);
-  const int64_t turns_wide = up(p.m_tiles * wide, pairs), turns_narrow = up(p.m_tiles * narrow, pairs);
-  const bool n128 = 10 * turns_wide > 6 * turns_narrow;
-  const cudaError_t e = maps(n128 ? 64 : 128);
-  if (e != cudaSuccess) return e;
-  p.n_tiles = (int32_t)(n128 ? narrow : wide);
-  return n128 ? launch_of<PASS, 128>(p, sms, stream) : launch_of<PASS, 256>(p, sms, stream);
+  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles, pairs = tiles < sms / 2 ? tiles : sms / 2;
+  glu_kernel<PASS><<<(unsigned)(2 * pairs), 256, kSmem, stream>>>(p);
+  return cudaGetLastError();
 }
 
 kda_status check_glu(const kda_glu_problem* q) {
@@ -476,8 +454,8 @@ kda_status check_glu(const kda_glu_problem* q) {
   if (q->rows < 0 || q->rows >= lim || q->dim < 8 || q->hidden < 8 || q->dim % 8 || q->hidden % 8 ||
       q->x_stride < q->dim || q->x_stride >= lim || q->x_stride % 8)
     return KDA_ERR_INVALID_SHAPE;
-  if (up(q->rows, kTileM) * up(q->hidden, 64) >= lim || up(q->rows, kTileM) * up(q->dim, 128) >= lim ||
-      2 * up(q->hidden, kTileM) * up(q->dim, 128) >= lim)
+  if (up(q->rows, kTileM) * up(q->hidden, kHalf) >= lim || up(q->rows, kTileM) * up(q->dim, kTileN) >= lim ||
+      2 * up(q->hidden, kTileM) * up(q->dim, kTileN) >= lim)
     return KDA_ERR_INVALID_SHAPE;
   if (q->dtype != KDA_ROW_BF16 || (q->fn != KDA_FN_SILU && q->fn != KDA_FN_SIGMOID && q->fn != KDA_FN_GELU))
     return KDA_ERR_INVALID_ARG;
@@ -491,17 +469,16 @@ template <int PASS>
 cudaError_t launch_dual(const kda_glu_problem* q, bf16* o0, bf16* o1, const void* dout, unsigned* status,
                         cudaStream_t stream) {
   GluParams p = {};
-  const cudaError_t e = map_of(&p.a[0], q->x, q->rows, q->dim, q->x_stride, kHalf);
+  cudaError_t e = map_of(&p.a[0], q->x, q->rows, q->dim, q->x_stride, kHalf);
+  if (e == cudaSuccess) e = map_of(&p.b[0], q->w_gate, q->hidden, q->dim, q->dim, kHalf);
+  if (e == cudaSuccess) e = map_of(&p.b[1], q->w_up, q->hidden, q->dim, q->dim, kHalf);
   if (e != cudaSuccess) return e;
   p.M = q->rows, p.N = q->hidden;
-  p.k_blocks = (int32_t)up(q->dim, kTileK), p.m_tiles = (int32_t)up(q->rows, kTileM);
+  p.k_blocks = (int32_t)up(q->dim, kTileK);
+  p.m_tiles = (int32_t)up(q->rows, kTileM), p.n_tiles = (int32_t)up(q->hidden, kHalf);
   p.fn = q->fn, p.stall = q->debug_stall, p.status = status;
   p.o0 = o0, p.o1 = o1, p.dout = static_cast<const bf16*>(dout);
-  auto maps = [&](int rows) {  // a tile's columns are as many of both projections
-    const cudaError_t e = map_of(&p.b[0], q->w_gate, q->hidden, q->dim, q->dim, rows);
-    return e == cudaSuccess ? map_of(&p.b[1], q->w_up, q->hidden, q->dim, q->dim, rows) : e;
-  };
-  return launch<PASS>(p, 2 * (int64_t)q->hidden, maps, stream);
+  return launch<PASS>(p, stream);
 }
 
 // Up to kStepRows rows.  As many CTAs share the summed axis as fit the GPU twice per SM, with four
@@ -604,21 +581,21 @@ kda_status kda_glu_bwd(const kda_glu_problem* problem, const void* dout, const v
   GluParams p = {};
   p.stall = q.debug_stall, p.status = status;
   // dx: both projections' products in one sum
-  auto none = [](int) { return cudaSuccess; };
   if (e == cudaSuccess) e = map_of(&p.a[0], dg, M, F, F, kHalf);
   if (e == cudaSuccess) e = map_of(&p.a[1], du, M, F, F, kHalf);
   if (e == cudaSuccess) e = map_of(&p.b[0], q.w_gate, F, D, D, kTileK);
   if (e == cudaSuccess) e = map_of(&p.b[1], q.w_up, F, D, D, kTileK);
   p.M = M, p.N = D, p.k_blocks = (int32_t)up(F, kTileK), p.m_tiles = (int32_t)up(M, kTileM);
+  p.n_tiles = (int32_t)up(D, kTileN);
   p.o0 = static_cast<bf16*>(dx);
-  if (e == cudaSuccess) e = launch<kInput>(p, D, none, stream);
+  if (e == cudaSuccess) e = launch<kInput>(p, stream);
   // the weights' gradients: the gate's rows, then the other's
   if (e == cudaSuccess) e = map_of(&p.a[0], dg, M, F, F, kTileK);
   if (e == cudaSuccess) e = map_of(&p.a[1], du, M, F, F, kTileK);
   if (e == cudaSuccess) e = map_of(&p.b[0], q.x, M, D, q.x_stride, kTileK);
   p.M = F, p.N = D, p.k_blocks = (int32_t)up(M, kTileK), p.m_tiles = (int32_t)(2 * up(F, kTileM));
   p.o0 = static_cast<bf16*>(dw_gate), p.o1 = static_cast<bf16*>(dw_up);
-  if (e == cudaSuccess) e = launch<kWeights>(p, D, none, stream);
+  if (e == cudaSuccess) e = launch<kWeights>(p, stream);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
