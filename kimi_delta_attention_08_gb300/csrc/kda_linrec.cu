@@ -22,6 +22,7 @@
 // were filled with ones before (no arithmetic result has these bits).  Waits give up after
 // half a second.
 #include <algorithm>
+#include <type_traits>
 
 #include "kda_internal.h"
 #include "kda_rows.cuh"
@@ -813,7 +814,14 @@ __device__ __forceinline__ void grads_of(const Vals<V> (&x)[2], const Vals<V> (&
 }
 template <int V>
 __device__ __forceinline__ Vals<V> add_of(const Vals<V>& a, const Vals<V>& b) {
-  return fma_of(a, splat<V>(1.f), b);
+  Vals<V> r;
+  if constexpr (V == 1) {
+    r.v[0] = a.v[0] + b.v[0];
+  } else {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) r.v[k] = padd(a.v[k], b.v[k]);
+  }
+  return r;
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_of(void* p, int64_t at, const Vals<V>& v) {
@@ -822,8 +830,8 @@ __device__ __forceinline__ void store_of(void* p, int64_t at, const Vals<V>& v) 
   store_vals<T, V>(p, at, f);
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams p) {
+template <typename T, int V, bool Z>
+__global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(const __grid_constant__ LinrecParams p) {
   constexpr int R = kRowsB, CH = 32 * V;
   using S = Slots<T, V, R>;
   constexpr int kBuffer = 5 * S::kArray + S::kGates;  // x, r, i, dout, z, gates; two by turns
@@ -851,7 +859,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
       S::copy(at + S::kArray, p.r, row0, p.r_s, ch, n);
       S::copy(at + 2 * S::kArray, p.i, row0, p.i_s, ch, n);
       S::copy(at + 3 * S::kArray, p.dout, row0, p.dim, ch, n);
-      if (p.z) S::copy(at + 4 * S::kArray, p.z, row0, p.z_s, ch, n);
+      if constexpr (Z) S::copy(at + 4 * S::kArray, p.z, row0, p.z_s, ch, n);
       S::copy_gates(at_gates0 + (turn & 1) * kBuffer, p.gates, p.dim, ch, ch < p.dim);
     }
     ptx::cp_async_commit();
@@ -886,48 +894,64 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
     ptx::cp_async_wait_all();
     Gates<V> c;
     S::gates(c, slots + 5 * S::kArray + threadIdx.x * V * 4 + (turn & 1) * kBuffer);
-    const bool all = bits.live == (1u << R) - 1;
-    // rows of no sequence count for nothing
-    auto row = [&](int k, int j) { return all || (bits.live >> j & 1) ? S::get(mine + k * S::kArray, j) : splat<V>(0.f); };
     Vals<V> a[R], b[R], dy[R], dq[R];  // dq: dout silu'(z), what dz takes times h
-    steps_of<T>(row, c, a, b);
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      dy[j] = row(3, j);
-      if (p.z) {
-        const Vals<V> z = row(4, j), q = sigmoid<T>(z);
-        // silu' = q + z q (1 - q)
-        dq[j] = mul_of(dy[j], fma_of(mul_of(z, q), fma_of(q, splat<V>(-1.f), splat<V>(1.f)), q));
-        dy[j] = mul_of(dy[j], mul_of(z, q));
-      }
-    }
+    Vals<V> h, P;
     auto initial = [&](int j) {
       float h0[V] = {};
       if (p.init && ok) load_state<V>(h0, p.init, (int64_t)rows.n[warp * R + j] * p.dim + ch, p.state_bf16);
       return vals_from(h0);
     };
-    // what the run does to a state
-    Vals<V> h = splat<V>(0.f), P = splat<V>(1.f);
+    // A run within one sequence asks nothing row by row (`inner`).
+    const bool within = __all_sync(0xffffffffu, n == R) && !bits.start && !bits.last && bits.live == (1u << R) - 1;
+    auto row = [&](auto inner, int k, int j) {  // rows of no sequence count for nothing
+      constexpr bool IN = decltype(inner)::value;
+      return IN || (bits.live >> j & 1) ? S::get(mine + k * S::kArray, j) : splat<V>(0.f);
+    };
+    // what the run does to a state, and to a gradient
+    auto compose = [&](auto inner) {
+      constexpr bool IN = decltype(inner)::value;
+      steps_of<T>([&](int k, int j) { return row(inner, k, j); }, c, a, b);
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      if (bits.start >> j & 1) h = initial(j);
-      h = fma_of(a[j], h, b[j]);
-      P = mul_of(P, a[j]);
-    }
-    put<V>(fw_H[warp], lane, h);
-    if (bits.last && p.dfin && ok) {  // the final state's gradient joins the last row's
-#pragma unroll
-      for (int j = 0; j < R; ++j)
-        if (bits.last >> j & 1) {
-          float d[V];
-          load_state<V>(d, p.dfin, (int64_t)rows.n[warp * R + j] * p.dim + ch, p.state_bf16);
-          dy[j] = add_of(dy[j], vals_from(d));
+      for (int j = 0; j < R; ++j) {
+        dy[j] = row(inner, 3, j);
+        if constexpr (Z) {
+          const Vals<V> z = row(inner, 4, j), q = sigmoid<T>(z), zq = mul_of(z, q);
+          // silu' = q + z q (1 - q)
+          dq[j] = mul_of(dy[j], fma_of(zq, fma_of(q, splat<V>(-1.f), splat<V>(1.f)), q));
+          dy[j] = mul_of(dy[j], zq);
         }
-    }
-    // and to a gradient
-    h = splat<V>(0.f);
+      }
+      if constexpr (IN) {
+        h = b[0], P = a[0];
 #pragma unroll
-    for (int j = R - 1; j >= 0; --j) h = mul_of(a[j], bits.last >> j & 1 ? dy[j] : add_of(h, dy[j]));
+        for (int j = 1; j < R; ++j) h = fma_of(a[j], h, b[j]), P = mul_of(P, a[j]);
+        put<V>(fw_H[warp], lane, h);
+        h = mul_of(a[R - 1], dy[R - 1]);
+#pragma unroll
+        for (int j = R - 2; j >= 0; --j) h = mul_of(a[j], add_of(h, dy[j]));
+      } else {
+        h = splat<V>(0.f), P = splat<V>(1.f);
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          if (bits.start >> j & 1) h = initial(j);
+          h = fma_of(a[j], h, b[j]);
+          P = mul_of(P, a[j]);
+        }
+        put<V>(fw_H[warp], lane, h);
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+          if (p.dfin && ok && (bits.last >> j & 1)) {  // the final state's gradient joins the last row's
+            float d[V];
+            load_state<V>(d, p.dfin, (int64_t)rows.n[warp * R + j] * p.dim + ch, p.state_bf16);
+            dy[j] = add_of(dy[j], vals_from(d));
+          }
+        h = splat<V>(0.f);
+#pragma unroll
+        for (int j = R - 1; j >= 0; --j) h = mul_of(a[j], bits.last >> j & 1 ? dy[j] : add_of(h, dy[j]));
+      }
+    };
+    if (within) compose(std::true_type{});
+    else compose(std::false_type{});
     put<V>(sh.runs.P[warp], lane, P);
     put<V>(sh.runs.H[warp], lane, h);
     if (lane == 0) sh.runs.cut[warp] = bits.last != 0, fw_cut[warp] = bits.start != 0;
@@ -951,49 +975,58 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(LinrecParams
     if (warp == kWarps - 2 && turn > 0) add_runs(last_tile, last_c0);
     __syncthreads();
     copy(sh.unit[(turn + 1) & 1], turn + 1);
-    // states again, b <- the one before each row; dz
-    const int64_t row_at = row0 * p.dim + ch;
-    h = get<V>(fw_H[warp], lane);
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      if (bits.start >> j & 1) h = initial(j);
-      const Vals<V> before = h;
-      h = fma_of(a[j], h, b[j]);
-      b[j] = before;
-      if (p.z && j < n)
-        store_of<T>(p.dz, row_at + (uint64_t)(uint32_t)p.dim * (uint32_t)j,
-                    bits.live >> j & 1 ? mul_of(dq[j], h) : splat<V>(0.f));
-    }
-    Vals<V> C = get<V>(sh.runs.H[warp], lane);
+    // states again, b <- the one before each row; dz; then the rows' gradients, last row first
     Vals<V> se = splat<V>(0.f), sr = se, si = se;
+    const int64_t row_at = row0 * p.dim + ch;
+    auto walk = [&](auto inner) {
+      constexpr bool IN = decltype(inner)::value;
+      auto at = [&](void* q, int j) {
+        return reinterpret_cast<char*>(static_cast<T*>(q) + row_at) + (uint64_t)(uint32_t)p.dim * (uint32_t)(j * sizeof(T));
+      };
+      h = get<V>(fw_H[warp], lane);
 #pragma unroll
-    for (int j = R - 2; j >= 0; j -= 2) {
-      Vals<V> g[2], e[2], dx[2], dr[2], di[2];
-#pragma unroll
-      for (int q = 1; q >= 0; --q) {
-        g[q] = bits.last >> (j + q) & 1 ? dy[j + q] : add_of(C, dy[j + q]);
-        C = mul_of(a[j + q], g[q]);
-        if (p.dinit && ok && (bits.start >> (j + q) & 1)) {
-          float f[V];
-          vals_to(C, f);
-          store_state<V>(p.dinit, (int64_t)rows.n[warp * R + j + q] * p.dim + ch, f, false);
+      for (int j = 0; j < R; ++j) {
+        if (!IN && (bits.start >> j & 1)) h = initial(j);
+        const Vals<V> before = h;
+        h = fma_of(a[j], h, b[j]);
+        b[j] = before;
+        if constexpr (Z) {
+          if (IN || j < n)
+            store_of<T>(at(p.dz, j), 0, IN || (bits.live >> j & 1) ? mul_of(dq[j], h) : splat<V>(0.f));
         }
       }
-      const Vals<V> x[2] = {row(0, j), row(0, j + 1)}, r[2] = {row(1, j), row(1, j + 1)}, i[2] = {row(2, j), row(2, j + 1)};
-      const Vals<V> a2[2] = {a[j], a[j + 1]}, h2[2] = {b[j], b[j + 1]};
-      grads_of<T>(x, r, i, c, a2, h2, g, e, dx, dr, di);
+      Vals<V> C = get<V>(sh.runs.H[warp], lane);
 #pragma unroll
-      for (int q = 1; q >= 0; --q) {
-        if (!all && !(bits.live >> (j + q) & 1)) e[q] = dx[q] = dr[q] = di[q] = splat<V>(0.f);
-        se = add_of(se, e[q]), sr = add_of(sr, dr[q]), si = add_of(si, di[q]);
-        if (j + q < n) {
-          const int64_t to = row_at + (uint64_t)(uint32_t)p.dim * (uint32_t)(j + q);
-          store_of<T>(p.dx, to, dx[q]);
-          store_of<T>(p.dr, to, dr[q]);
-          store_of<T>(p.di, to, di[q]);
+      for (int j = R - 2; j >= 0; j -= 2) {
+        Vals<V> g[2], e[2], dx[2], dr[2], di[2];
+#pragma unroll
+        for (int q = 1; q >= 0; --q) {
+          g[q] = !IN && (bits.last >> (j + q) & 1) ? dy[j + q] : add_of(C, dy[j + q]);
+          C = mul_of(a[j + q], g[q]);
+          if (!IN && p.dinit && ok && (bits.start >> (j + q) & 1)) {
+            float f[V];
+            vals_to(C, f);
+            store_state<V>(p.dinit, (int64_t)rows.n[warp * R + j + q] * p.dim + ch, f, false);
+          }
+        }
+        const Vals<V> x[2] = {row(inner, 0, j), row(inner, 0, j + 1)}, r[2] = {row(inner, 1, j), row(inner, 1, j + 1)};
+        const Vals<V> i[2] = {row(inner, 2, j), row(inner, 2, j + 1)};
+        const Vals<V> a2[2] = {a[j], a[j + 1]}, h2[2] = {b[j], b[j + 1]};
+        grads_of<T>(x, r, i, c, a2, h2, g, e, dx, dr, di);
+#pragma unroll
+        for (int q = 1; q >= 0; --q) {
+          if (!IN && !(bits.live >> (j + q) & 1)) e[q] = dx[q] = dr[q] = di[q] = splat<V>(0.f);
+          se = add_of(se, e[q]), sr = add_of(sr, dr[q]), si = add_of(si, di[q]);
+          if (IN || j + q < n) {
+            store_of<T>(at(p.dx, j + q), 0, dx[q]);
+            store_of<T>(at(p.dr, j + q), 0, dr[q]);
+            store_of<T>(at(p.di, j + q), 0, di[q]);
+          }
         }
       }
-    }
+    };
+    if (within) walk(std::true_type{});
+    else walk(std::false_type{});
     put<V>(sums[0][warp], lane, se);
     put<V>(sums[1][warp], lane, sr);
     put<V>(sums[2][warp], lane, si);
@@ -1177,8 +1210,11 @@ cudaError_t launch_fwd_of(const LinrecParams& p, bool tma, cudaStream_t stream) 
 }
 template <typename T, int V>
 cudaError_t launch_bwd_of(const LinrecParams& p, cudaStream_t stream) {
-  static bool done[64];
-  return launch_tiles(linrec_bwd_kernel<T, V>, done, 2 * (5 * Slots<T, V, kRowsB>::kArray + Slots<T, V, kRowsB>::kGates), 2, p, stream);
+  using S = Slots<T, V, kRowsB>;
+  constexpr int smem = 2 * (5 * S::kArray + S::kGates);
+  static bool done[2][64];
+  return p.z ? launch_tiles(linrec_bwd_kernel<T, V, true>, done[1], smem, 2, p, stream)
+             : launch_tiles(linrec_bwd_kernel<T, V, false>, done[0], smem, 2, p, stream);
 }
 
 // Channels per thread: 8 bytes of a row where its alignment allows, 4 in the backward, which
