@@ -84,8 +84,15 @@ def _opt(t, name, dtype, dev, shape):
 def _rows(t, name, dtype, dev, shape):
     """(pointer, row stride) of [B, T, ...] rows with contiguous channels."""
     try:
-        if len(shape) == 3 and t.dtype == dtype and t.device == dev and t.shape == shape and t.is_contiguous():
-            return t.data_ptr(), shape[2]
+        if len(shape) == 3 and t.dtype == dtype and t.device == dev and t.shape == shape:
+            if t.is_contiguous():
+                return t.data_ptr(), shape[2]
+            b, n, width = shape
+            sb, row, sc = t.stride()
+            if n == 1:
+                row = sb
+            if sc == 1 and row >= width and (b == 1 or sb == row * n) and b * n > 1 < width:
+                return t.data_ptr(), row  # a part of a wider projection
     except AttributeError:
         pass
     if _tensor(t, name).dtype != dtype:
