@@ -277,9 +277,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
 // takes 64 rows of both weights as the 128 rows of A, and all of x as B's columns, so the tensor
 // cores do no more work than the rows need; where the weights' rows alone do not fill the
 // GPU, a cluster splits the summed axis and adds up through its shared memory, in the order
-// of its CTAs.  Two CTAs fit an SM, each with 96 KB of weights and x in flight.
+// of its CTAs.  Two CTAs fit an SM, each with 108 KB of weights and x in flight.
 constexpr int kStepRows = 128, kStepTile = 64, kStepMaxSplit = 8;
-constexpr uint32_t kStepRing = 98304, kStepSmem = kStepRing + 1024;
+constexpr uint32_t kStepRing = 110592, kStepSmem = kStepRing + 1024;
 constexpr int kStepPitch = 132;                  // floats between two rows' sums
 
 struct StepParams {
@@ -301,11 +301,20 @@ __global__ void __launch_bounds__(256, 2) glu_step_kernel(const __grid_constant_
   const int per = (p.k_blocks + p.splits - 1) / p.splits;
   const int first = split * per, last = min(p.k_blocks, first + per);
   const uint32_t stage_bytes = 2 * kStepTile * 128 + p.cols * 128;
+  auto load = [&](int kb, int stage) {
+    uint8_t* const A = ring + stage * stage_bytes;
+    ptx::mbar_arrive_expect_tx(&full[stage], stage_bytes);
+    ptx::tma_load_2d(A, &p.w[0], &full[stage], kb * kTileK, f0);
+    ptx::tma_load_2d(A + kStepTile * 128, &p.w[1], &full[stage], kb * kTileK, f0);
+    ptx::tma_load_2d(A + 2 * kStepTile * 128, &p.x, &full[stage], kb * kTileK, 0);
+  };
+  const int ahead = p.stall ? 0 : min(p.stages, last - first);  // loads that need not wait for anything
   if (threadIdx.x == 0) {
     failed = 0;
     for (int s = 0; s < p.stages; ++s) ptx::mbar_init(&full[s], 1), ptx::mbar_init(&empty[s], 1);
     ptx::mbar_init(&done, 1);
     ptx::fence_mbar_init();
+    for (int s = 0; s < ahead; ++s) load(first + s, s);
   }
   if (warp == 2) {
     ptx::tmem_alloc(&tmem_at, 128);
@@ -317,15 +326,11 @@ __global__ void __launch_bounds__(256, 2) glu_step_kernel(const __grid_constant_
   const uint32_t tmem = tmem_at;
   if (warp == 0 && lane == 0) {
     bool ok = !p.stall;
-    uint32_t stage = 0, parity = 1;
-    for (int kb = first; kb < last && ok; ++kb) {
+    uint32_t stage = 0, parity = 0;
+    for (int kb = first + ahead; kb < last && ok; ++kb) {
       ok = ptx::mbar_wait(&empty[stage], parity, kWaitNs);
       if (!ok) break;
-      uint8_t* const A = ring + stage * stage_bytes;
-      ptx::mbar_arrive_expect_tx(&full[stage], stage_bytes);
-      ptx::tma_load_2d(A, &p.w[0], &full[stage], kb * kTileK, f0);
-      ptx::tma_load_2d(A + kStepTile * 128, &p.w[1], &full[stage], kb * kTileK, f0);
-      ptx::tma_load_2d(A + 2 * kStepTile * 128, &p.x, &full[stage], kb * kTileK, 0);
+      load(kb, stage);
       if (++stage == p.stages) stage = 0, parity ^= 1;
     }
     if (!ok) failed = 1;
