@@ -253,8 +253,10 @@ typedef struct {
   int32_t reserved;           /* 0                                                   */
 } kda_glu_problem;
 
-/* kda_glu_fwd -- out [rows, hidden], written, and (unless NULL) pre [rows, 2 hidden], g then
- * u of each row, rounded to bf16: kda_glu_bwd then computes them from there and not again.
+/* kda_glu_fwd -- out [rows, hidden], written, and (unless NULL) pre [rows, 2 hidden], 16 bits
+ * each: g, then u of each row, for kda_glu_bwd, which then does not compute them again.  What
+ * is kept has 9 bits of fraction and magnitudes up to 2^32 (a greater one becomes NaN); its
+ * encoding is the library's own.
  * workspace: NULL, or KDA_STATUS_BYTES (128-byte aligned) whose first word receives the
  * status; after KDA_ERR_DEVICE_TIMEOUT what the call wrote is not to be used. */
 KDA_API kda_status kda_glu_fwd(const kda_glu_problem* p, void* out, void* pre, void* workspace,
@@ -264,8 +266,8 @@ KDA_API kda_status kda_glu_fwd(const kda_glu_problem* p, void* out, void* pre, v
 KDA_API kda_status kda_glu_bwd_get_workspace_size(int64_t rows, int32_t hidden, size_t* bytes);
 
 /* kda_glu_bwd -- the gradients of <dout, out>: dx [rows, dim], dw_gate and dw_up
- * [hidden, dim].  pre: NULL (g and u are computed again, in fp32), or what the forward kept;
- * that saves a third of the products and adds the error of their rounding. */
+ * [hidden, dim].  pre: NULL (g and u are computed again, in fp32), or what the forward kept,
+ * which saves a third of the products and adds the error of its rounding. */
 KDA_API kda_status kda_glu_bwd(const kda_glu_problem* p, const void* dout, const void* pre, void* dx,
                                void* dw_gate, void* dw_up, void* workspace, size_t workspace_bytes,
                                cudaStream_t stream);

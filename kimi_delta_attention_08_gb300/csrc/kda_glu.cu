@@ -46,6 +46,7 @@ struct GluParams {
   int32_t m_tiles, n_tiles;
   int32_t fn, stall;
   bf16 *o0, *o1;
+  uint16_t* pre;           // NULL, or the kept pre-activations
   const bf16* dout;
   unsigned* status;
 };
@@ -70,6 +71,28 @@ __device__ __forceinline__ float act_of(float g, int fn, float& slope) {
   const float s = sigmoid<bf16>(g, t);
   slope = fn == KDA_FN_SILU ? fmaf(g, t, s) : t;
   return fn == KDA_FN_SILU ? g * s : s;
+}
+
+// Kept pre-activations: 16 bits each, 9 of fraction and 6 of exponent.  bf16's 7 bits of
+// fraction would leave dx and dW 3.1e-3 from their 64-bit values where computing g and u
+// again leaves 2.3e-3; these leave 2.4e-3.  Magnitudes up to 2^32; beyond that, and what is
+// not finite, becomes NaN, and below 2^-30 the fraction shortens.  The fp32 value times 2^-96
+// has its exponent in 6 bits, so what is kept is a part of its bits, rounded to even.
+__device__ __forceinline__ uint32_t keep_bits(float v) {
+  const uint32_t b = __float_as_uint(v * 0x1p-96f), m = b & 0x7FFFFFFFu;
+  const uint32_t r = (m + 0x1FFFu + (m >> 14 & 1u)) >> 14;
+  return (b >> 16 & 0x8000u) | (r < 0x7E00u ? r : 0x7E01u);
+}
+__device__ __forceinline__ float kept_value(uint32_t k) {
+  const uint32_t m = k & 0x7FFFu;
+  const float v = __uint_as_float((k & 0x8000u) << 16 | m << 14) * 0x1p96f;
+  return m < 0x7E00u ? v : __uint_as_float(0x7FFFFFFFu);
+}
+__device__ __forceinline__ void keep8(uint16_t* p, const float* f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = keep_bits(f[2 * k]) | keep_bits(f[2 * k + 1]) << 16;
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // A tile of the walk: groups of eight tiles down, so that the pairs at work share operands.
@@ -225,9 +248,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                 y[k] = act_of(g[k], p.fn) * h[k];
               }
               store8(p.o0 + at + j, y);
-              if (p.o1) {
-                store8(p.o1 + row * 2 * p.N + col + j, g);
-                store8(p.o1 + row * 2 * p.N + p.N + col + j, h);
+              if (p.pre) {
+                keep8(p.pre + row * 2 * p.N + col + j, g);
+                keep8(p.pre + row * 2 * p.N + p.N + col + j, h);
               }
             } else {
               const uint4 d = __ldg(reinterpret_cast<const uint4*>(p.dout + at + j));
@@ -286,7 +309,8 @@ struct StepParams {
   CUtensorMap w[2], x;
   int32_t rows, cols;        // of x that exist; of the product, a multiple of 16
   int32_t hidden, k_blocks, splits, stages, fn, stall;
-  bf16 *out, *pre;
+  bf16* out;
+  uint16_t* pre;
   unsigned* status;
 };
 
@@ -396,9 +420,9 @@ __global__ void __launch_bounds__(256, 2) glu_step_kernel(const __grid_constant_
       const int64_t at = (int64_t)r * p.hidden + col;
       *reinterpret_cast<uint32_t*>(p.out + at) = pack_bf16(act_of(g.x, p.fn) * u.x, act_of(g.y, p.fn) * u.y);
       if (p.pre) {
-        bf16* const to = p.pre + (int64_t)r * 2 * p.hidden + col;
-        *reinterpret_cast<uint32_t*>(to) = pack_bf16(g.x, g.y);
-        *reinterpret_cast<uint32_t*>(to + p.hidden) = pack_bf16(u.x, u.y);
+        uint16_t* const to = p.pre + (int64_t)r * 2 * p.hidden + col;
+        *reinterpret_cast<uint32_t*>(to) = keep_bits(g.x) | keep_bits(g.y) << 16;
+        *reinterpret_cast<uint32_t*>(to + p.hidden) = keep_bits(u.x) | keep_bits(u.y) << 16;
       }
     }
   }
@@ -406,7 +430,7 @@ __global__ void __launch_bounds__(256, 2) glu_step_kernel(const __grid_constant_
 }
 
 // dg and du from kept pre-activations, eight values a thread.
-__global__ void __launch_bounds__(256) glu_slope_kernel(const bf16* pre, const bf16* dout, bf16* dg, bf16* du,
+__global__ void __launch_bounds__(256) glu_slope_kernel(const uint16_t* pre, const bf16* dout, bf16* dg, bf16* du,
                                                         int64_t M, int64_t F, int fn) {
   const int64_t per = F / 8, n = M * per;
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
@@ -416,9 +440,10 @@ __global__ void __launch_bounds__(256) glu_slope_kernel(const bf16* pre, const b
     load_words(ru.w, pre + row * 2 * F + F + col);
     load_words(rd.w, dout + row * F + col);
     float g[8], u[8], d[8];
-    unpack(rg, g), unpack(ru, u), unpack(rd, d);
+    unpack(rd, d);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
+      g[k] = kept_value(rg.w[k / 2] >> (k % 2 * 16) & 0xFFFFu), u[k] = kept_value(ru.w[k / 2] >> (k % 2 * 16) & 0xFFFFu);
       float slope;
       const float f = act_of(g[k], fn, slope);
       g[k] = d[k] * u[k] * slope, u[k] = d[k] * f;
@@ -471,7 +496,7 @@ kda_status check_glu(const kda_glu_problem* q) {
 
 // The forward's tiles (also of the recomputing backward).
 template <int PASS>
-cudaError_t launch_dual(const kda_glu_problem* q, bf16* o0, bf16* o1, const void* dout, unsigned* status,
+cudaError_t launch_dual(const kda_glu_problem* q, bf16* o0, bf16* o1, uint16_t* pre, const void* dout, unsigned* status,
                         cudaStream_t stream) {
   GluParams p = {};
   cudaError_t e = map_of(&p.a[0], q->x, q->rows, q->dim, q->x_stride, kHalf);
@@ -482,13 +507,13 @@ cudaError_t launch_dual(const kda_glu_problem* q, bf16* o0, bf16* o1, const void
   p.k_blocks = (int32_t)up(q->dim, kTileK);
   p.m_tiles = (int32_t)up(q->rows, kTileM), p.n_tiles = (int32_t)up(q->hidden, kHalf);
   p.fn = q->fn, p.stall = q->debug_stall, p.status = status;
-  p.o0 = o0, p.o1 = o1, p.dout = static_cast<const bf16*>(dout);
+  p.o0 = o0, p.o1 = o1, p.pre = pre, p.dout = static_cast<const bf16*>(dout);
   return launch<PASS>(p, stream);
 }
 
 // Up to kStepRows rows.  As many CTAs share the summed axis as fit the GPU twice per SM, with four
 // steps of 64 at least for each.
-cudaError_t launch_step(const kda_glu_problem* q, bf16* out, bf16* pre, unsigned* status, cudaStream_t stream) {
+cudaError_t launch_step(const kda_glu_problem* q, bf16* out, uint16_t* pre, unsigned* status, cudaStream_t stream) {
   StepParams p = {};
   int sms = 0;
   if (sm_count(&sms) != KDA_OK) return cudaErrorUnknown;
@@ -533,9 +558,10 @@ kda_status kda_glu_fwd(const kda_glu_problem* problem, void* out, void* pre, voi
   unsigned* const status = static_cast<unsigned*>(workspace);
   if (status && cudaMemsetAsync(status, 0, 4, stream) != cudaSuccess) return KDA_ERR_CUDA;
   if (problem->rows == 0) return KDA_OK;
-  bf16 *const to = static_cast<bf16*>(out), *const kept = static_cast<bf16*>(pre);
+  bf16* const to = static_cast<bf16*>(out);
+  uint16_t* const kept = static_cast<uint16_t*>(pre);
   const cudaError_t e = problem->rows <= kStepRows ? launch_step(problem, to, kept, status, stream)
-                                                   : launch_dual<kForward>(problem, to, kept, nullptr, status, stream);
+                                                   : launch_dual<kForward>(problem, to, nullptr, kept, nullptr, status, stream);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -577,10 +603,10 @@ kda_status kda_glu_bwd(const kda_glu_problem* problem, const void* dout, const v
     if (pre) {
       const int64_t blocks = up(M * (F / 8), 256);
       glu_slope_kernel<<<(unsigned)(blocks < 152 * 32 ? blocks : 152 * 32), 256, 0, stream>>>(
-          static_cast<const bf16*>(pre), static_cast<const bf16*>(dout), dg, du, M, F, q.fn);
+          static_cast<const uint16_t*>(pre), static_cast<const bf16*>(dout), dg, du, M, F, q.fn);
       e = cudaGetLastError();
     } else {
-      e = launch_dual<kRecompute>(problem, dg, du, dout, status, stream);
+      e = launch_dual<kRecompute>(problem, dg, du, nullptr, dout, status, stream);
     }
   }
   GluParams p = {};

@@ -129,6 +129,30 @@ def test_far_arguments(kda_lib, fn):
         within(got[k], ref[k], k)
 
 
+def test_kept_values_of_every_size(kda_lib):
+    """Pre-activations from 2^-36 to 2^34 of both signs, zero and NaN, as they are kept: within
+    half a step, and not a number beyond 2^32."""
+    import kimi_delta_attention_08_gb300 as kda
+    from tests.glu_ref import kept_values
+    e = torch.arange(-36, 35)
+    w = torch.zeros(8 * len(e) + 16, 8)
+    w[:8 * len(e), 0] = torch.ldexp(torch.tensor([1.0, -1, 1.25, -1.5, 1.75, 1.9921875, -1.0078125, 1.5]).repeat(len(e)),
+                                    e.repeat_interleave(8))
+    x = torch.zeros(1, 200, 8, dtype=BF)
+    x[..., 0] = 1
+    x[0, 1, 0], x[0, 2, 0] = 0, float("nan")
+    w, x = w.to(BF).cuda(), x.cuda()
+    for rows in (5, 200):       # both kernels
+        out, pre = (torch.empty(1, rows, k * len(w), dtype=BF, device="cuda") for k in (1, 2))
+        kda.kda_glu_fwd(x[:, :rows].contiguous(), w, w, out, pre=pre)
+        got, want = kept_values(pre)[0, 0, :len(w)], w[:, 0].cpu().double()
+        small = want.abs() < 2.0 ** 32
+        assert got[~small].isnan().all()
+        # half a step: of the value, or of the smallest exponent's fraction
+        assert ((got - want).abs()[small] <= torch.clamp(want.abs()[small] * 2.0 ** -10, min=2.0 ** -40)).all()
+        assert (kept_values(pre)[0, 1] == 0).all() and kept_values(pre)[0, 2].isnan().all()
+
+
 def test_a_wait_that_runs_out_is_reported(kda_lib):
     """Nothing is loaded: the products and the epilogue give up, and the next call is right."""
     import kimi_delta_attention_08_gb300 as kda
