@@ -32,21 +32,22 @@ using namespace rows;
 constexpr int kTileM = 256, kTileN = 256, kTileK = 64, kStages = 6;
 constexpr int kHalf = 128;                       // rows of A, columns of B in each CTA
 constexpr uint32_t kOperand = kHalf * kTileK * 2, kStage = 2 * kOperand;  // bytes in a stage
-constexpr uint32_t kSmem = kStages * kStage + 1024;
+constexpr int kEpilogueWarp = 4, kEpilogueWarps = 8;  // warps 4 .. 11
+constexpr uint32_t kOut = 32 * 64;               // 32 rows by 32 columns of an output, on their way
+constexpr uint32_t kSmem = kStages * kStage + kEpilogueWarps * 2 * kOut + 1024;
 constexpr uint64_t kWaitNs = 500000000ull;
-constexpr int kEpilogueWarp = 4;                 // warps 4 .. 7
 
 // What a launch computes.
 enum GluPass : int { kForward = 0, kRecompute = 1, kInput = 2, kWeights = 3 };
 
 struct GluParams {
   CUtensorMap a[2], b[2];  // of the gate and the other projection, or one for both
+  CUtensorMap o[3];        // outputs: out, g and u; dg and du; dx; or dWg and dWu
   int64_t M, N;            // of the output (columns: of one projection)
   int32_t k_blocks;        // of each of `sums` products that one tile adds up
   int32_t m_tiles, n_tiles;
   int32_t fn, stall;
-  bf16 *o0, *o1;
-  uint16_t* pre;           // NULL, or the kept pre-activations
+  int32_t keep;            // whether g and u are outputs too
   const bf16* dout;
   unsigned* status;
 };
@@ -88,16 +89,11 @@ __device__ __forceinline__ float kept_value(uint32_t k) {
   const float v = __uint_as_float((k & 0x8000u) << 16 | m << 14) * 0x1p96f;
   return m < 0x7E00u ? v : __uint_as_float(0x7FFFFFFFu);
 }
-__device__ __forceinline__ void keep8(uint16_t* p, const float* f) {
-  uint32_t w[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) w[k] = keep_bits(f[2 * k]) | keep_bits(f[2 * k + 1]) << 16;
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
 
-// A tile of the walk: groups of eight tiles down, so that the pairs at work share operands.
+// A tile of the walk: groups of sixteen tiles down, so that the pairs at work share operands
+// and a group's rows of A stay in L2 while it meets all of B.
 __device__ __forceinline__ void tile_of(const GluParams& p, int t, int& m, int& n) {
-  constexpr int kDown = 8;
+  constexpr int kDown = 16;
   const int per = kDown * p.n_tiles, g = t / per, r = t % per;
   const int down = min(kDown, p.m_tiles - g * kDown);
   m = g * kDown + r % down, n = r / down;
@@ -109,7 +105,7 @@ __device__ __forceinline__ void store8(bf16* p, const float* f) {
 }
 
 template <int PASS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp + kEpilogueWarps), 1)
     glu_kernel(const __grid_constant__ GluParams p) {
   constexpr bool A_MN = PASS == kWeights, B_MN = PASS == kInput || PASS == kWeights;
   constexpr bool DUAL = PASS == kForward || PASS == kRecompute;
@@ -126,7 +122,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
   if (threadIdx.x == 0) {
     failed = 0;
     for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[s], 1), ptx::mbar_init(&empty[s], 1);
-    for (int b = 0; b < 2; ++b) ptx::mbar_init(&tfull[b], 1), ptx::mbar_init(&tempty[b], 8);
+    for (int b = 0; b < 2; ++b) ptx::mbar_init(&tfull[b], 1), ptx::mbar_init(&tempty[b], 2 * kEpilogueWarps);
     ptx::fence_mbar_init();
   }
   if (warp == 2) ptx::tmem_alloc_pair(&tmem_at, 2 * kTileN);
@@ -204,73 +200,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
     }
     if (!ok) failed = 1;
   } else if (warp >= kEpilogueWarp) {
-    const int w = warp - kEpilogueWarp;
+    // Two warps take the halves of the columns of 32 rows.  Values go 32 columns at a time through
+    // shared memory and out by TMA, whole sectors at once; a thread's own stores of 16 bytes a
+    // row took 4 % of the largest forward and a fifth of the smallest backward.
+    constexpr int kColumns = (DUAL ? kHalf : kTileN) / 2;
+    const int w = warp - kEpilogueWarp, quarter = w % 4, side = w / 4;
+    uint8_t* const out = tiles + kStages * kStage + w * 2 * kOut;
     const uint64_t limit = kWaitNs + (uint64_t)blocks * 2000;  // a whole tile's sum may be long
-    uint32_t buf = 0, parity = 0;
+    uint32_t buf = 0, parity = 0, turn = 0;
     bool ok = true;
+    // 32 columns of the warp's rows: `packed(k)` is the pair of columns 2 k and 2 k + 1
+    auto put = [&](const CUtensorMap* map, int64_t col, int64_t row0, int64_t rows, auto packed) {
+      uint8_t* const at = out + (turn++ & 1) * kOut;
+      if (lane == 0) ptx::tma_store_wait_read<1>();
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 4; ++k)  // 64-byte swizzle
+        *reinterpret_cast<uint4*>(at + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4)) =
+            make_uint4(packed(4 * k), packed(4 * k + 1), packed(4 * k + 2), packed(4 * k + 3));
+      ptx::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {  // a group for each turn, empty ones too: the wait above counts turns
+        if (row0 < rows && col < p.N) ptx::tma_store_2d(map, at, (int)col, (int)row0);
+        ptx::tma_store_commit();
+      }
+    };
     for (int t = first; t < total; t += step) {
       int m, n;
       tile_of(p, t, m, n);
+      int64_t row0 = (int64_t)m * kTileM;
+      int which = 0;
+      if constexpr (PASS == kWeights) {
+        const int half = p.m_tiles / 2;
+        which = m >= half;
+        row0 = (int64_t)(m - which * half) * kTileM;
+      }
+      row0 += rank * kHalf + quarter * 32;
+      const int64_t col0 = (int64_t)n * (DUAL ? kHalf : kTileN) + side * kColumns;
+      const uint32_t acc = tmem + buf * kTileN + side * kColumns + ((uint32_t)(quarter * 32) << 16);
+      uint4 d[4] = {};       // dout of 32 columns, asked for ahead
+      auto load = [&](int c) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (row0 + lane < p.M && col0 + c + 8 * k < p.N)
+            d[k] = __ldg(reinterpret_cast<const uint4*>(p.dout + (row0 + lane) * p.N + col0 + c + 8 * k));
+      };
+      if constexpr (PASS == kRecompute) load(0);
       ok = __all_sync(0xffffffffu, ptx::mbar_wait(&tfull[buf], parity, limit));
       if (!ok) break;
       ptx::tc_fence_after();
-      int64_t row;
-      bf16* o0 = p.o0;
-      if constexpr (PASS == kWeights) {
-        const int half = p.m_tiles / 2, which = m >= half;
-        row = (int64_t)(m - which * half) * kTileM;
-        o0 = which ? p.o1 : p.o0;
-      } else {
-        row = (int64_t)m * kTileM;
-      }
-      row += rank * kHalf + w * 32 + lane;
-      const bool in = row < p.M;
-      const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(w * 32) << 16);
 #pragma unroll 1
-      for (int c = 0; c < (DUAL ? kHalf : kTileN); c += 32) {
+      for (int c = 0; c < kColumns; c += 32) {
         uint32_t v[32];
         ptx::tmem_ld32(acc + c, v);
-        const int64_t col = (int64_t)n * (DUAL ? kHalf : kTileN) + c;
-        const int64_t at = row * p.N + col;
+        auto pack = [&](const uint32_t (&f)[32]) {
+          return [&](int k) { return pack_bf16(__uint_as_float(f[2 * k]), __uint_as_float(f[2 * k + 1])); };
+        };
         if constexpr (DUAL) {
           uint32_t q[32];
           ptx::tmem_ld32(acc + kHalf + c, q);
           ptx::tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            if (!in || col + j >= p.N) continue;
-            float y[8], h[8];
-            if constexpr (PASS == kForward) {
-              float g[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                g[k] = __uint_as_float(v[j + k]), h[k] = __uint_as_float(q[j + k]);
-                y[k] = act_of(g[k], p.fn) * h[k];
-              }
-              store8(p.o0 + at + j, y);
-              if (p.pre) {
-                keep8(p.pre + row * 2 * p.N + col + j, g);
-                keep8(p.pre + row * 2 * p.N + p.N + col + j, h);
-              }
-            } else {
-              const uint4 d = __ldg(reinterpret_cast<const uint4*>(p.dout + at + j));
-              const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float dy = k & 1 ? hi_bf16(dw[k / 2]) : lo_bf16(dw[k / 2]);
-                float slope;
-                h[k] = dy * act_of(__uint_as_float(v[j + k]), p.fn, slope);
-                y[k] = dy * __uint_as_float(q[j + k]) * slope;
-              }
-              store8(p.o0 + at + j, y);
-              store8(p.o1 + at + j, h);
+          if constexpr (PASS == kForward) {
+            if (p.keep) {
+              auto kept = [&](const uint32_t (&f)[32]) {
+                return [&](int k) { return keep_bits(__uint_as_float(f[2 * k])) | keep_bits(__uint_as_float(f[2 * k + 1])) << 16; };
+              };
+              put(&p.o[1], col0 + c, row0, p.M, kept(v));
+              put(&p.o[2], col0 + c, row0, p.M, kept(q));
             }
+            put(&p.o[0], col0 + c, row0, p.M, [&](int k) {
+              return pack_bf16(act_of(__uint_as_float(v[2 * k]), p.fn) * __uint_as_float(q[2 * k]),
+                               act_of(__uint_as_float(v[2 * k + 1]), p.fn) * __uint_as_float(q[2 * k + 1]));
+            });
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const uint32_t dw = (&d[k / 8].x)[k / 2 % 4];
+              const float dy = k & 1 ? hi_bf16(dw) : lo_bf16(dw);
+              float slope;
+              const float f = act_of(__uint_as_float(v[k]), p.fn, slope);
+              v[k] = __float_as_uint(dy * __uint_as_float(q[k]) * slope);
+              q[k] = __float_as_uint(dy * f);
+            }
+            if (c + 32 < kColumns) load(c + 32);
+            put(&p.o[0], col0 + c, row0, p.M, pack(v));
+            put(&p.o[1], col0 + c, row0, p.M, pack(q));
           }
         } else {
           ptx::tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; j += 8)
-            if (in && col + j < p.N) store8(o0 + at + j, reinterpret_cast<const float*>(v) + j);
+          put(&p.o[which], col0 + c, row0, p.M, pack(v));
         }
       }
       ptx::tc_fence_before();
@@ -279,6 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
       buf ^= 1;
       if (buf == 0) parity ^= 1;
     }
+    if (lane == 0) ptx::tma_store_wait();
     if (!ok && lane == 0) failed = 1;
   }
   __syncwarp();
@@ -458,6 +477,12 @@ bool al_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a 
 int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
+// A map of an output of 16-bit values, its boxes 32 columns by 32 rows, 64-byte swizzled.
+cudaError_t out_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t stride) {
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)stride * 2};
+  const uint32_t b[2] = {32, 32};
+  return encode_tiled_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, b, CU_TENSOR_MAP_SWIZZLE_64B);
+}
 // A map of bf16 [rows, cols] with boxes of 64 columns by `box` rows, 128-byte swizzled.
 cudaError_t map_of(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t stride, uint32_t box) {
   const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows}, strides[1] = {(uint64_t)stride * 2};
@@ -474,7 +499,7 @@ cudaError_t launch(const GluParams& p, cudaStream_t stream) {
   int sms = 0;
   if (sm_count(&sms) != KDA_OK) return cudaErrorUnknown;
   const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles, pairs = tiles < sms / 2 ? tiles : sms / 2;
-  glu_kernel<PASS><<<(unsigned)(2 * pairs), 256, kSmem, stream>>>(p);
+  glu_kernel<PASS><<<(unsigned)(2 * pairs), 32 * (kEpilogueWarp + kEpilogueWarps), kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -502,12 +527,18 @@ cudaError_t launch_dual(const kda_glu_problem* q, bf16* o0, bf16* o1, uint16_t* 
   cudaError_t e = map_of(&p.a[0], q->x, q->rows, q->dim, q->x_stride, kHalf);
   if (e == cudaSuccess) e = map_of(&p.b[0], q->w_gate, q->hidden, q->dim, q->dim, kHalf);
   if (e == cudaSuccess) e = map_of(&p.b[1], q->w_up, q->hidden, q->dim, q->dim, kHalf);
+  if (e == cudaSuccess) e = out_map(&p.o[0], o0, q->rows, q->hidden, q->hidden);
+  if (e == cudaSuccess && o1) e = out_map(&p.o[1], o1, q->rows, q->hidden, q->hidden);
+  if (e == cudaSuccess && pre) {
+    e = out_map(&p.o[1], pre, q->rows, q->hidden, 2 * (int64_t)q->hidden);
+    if (e == cudaSuccess) e = out_map(&p.o[2], pre + q->hidden, q->rows, q->hidden, 2 * (int64_t)q->hidden);
+  }
   if (e != cudaSuccess) return e;
   p.M = q->rows, p.N = q->hidden;
   p.k_blocks = (int32_t)up(q->dim, kTileK);
   p.m_tiles = (int32_t)up(q->rows, kTileM), p.n_tiles = (int32_t)up(q->hidden, kHalf);
   p.fn = q->fn, p.stall = q->debug_stall, p.status = status;
-  p.o0 = o0, p.o1 = o1, p.pre = pre, p.dout = static_cast<const bf16*>(dout);
+  p.keep = pre != nullptr, p.dout = static_cast<const bf16*>(dout);
   return launch<PASS>(p, stream);
 }
 
@@ -618,14 +649,15 @@ kda_status kda_glu_bwd(const kda_glu_problem* problem, const void* dout, const v
   if (e == cudaSuccess) e = map_of(&p.b[1], q.w_up, F, D, D, kTileK);
   p.M = M, p.N = D, p.k_blocks = (int32_t)up(F, kTileK), p.m_tiles = (int32_t)up(M, kTileM);
   p.n_tiles = (int32_t)up(D, kTileN);
-  p.o0 = static_cast<bf16*>(dx);
+  if (e == cudaSuccess) e = out_map(&p.o[0], dx, M, D, D);
   if (e == cudaSuccess) e = launch<kInput>(p, stream);
   // the weights' gradients: the gate's rows, then the other's
   if (e == cudaSuccess) e = map_of(&p.a[0], dg, M, F, F, kTileK);
   if (e == cudaSuccess) e = map_of(&p.a[1], du, M, F, F, kTileK);
   if (e == cudaSuccess) e = map_of(&p.b[0], q.x, M, D, q.x_stride, kTileK);
   p.M = F, p.N = D, p.k_blocks = (int32_t)up(M, kTileK), p.m_tiles = (int32_t)(2 * up(F, kTileM));
-  p.o0 = static_cast<bf16*>(dw_gate), p.o1 = static_cast<bf16*>(dw_up);
+  if (e == cudaSuccess) e = out_map(&p.o[0], dw_gate, F, D, D);
+  if (e == cudaSuccess) e = out_map(&p.o[1], dw_up, F, D, D);
   if (e == cudaSuccess) e = launch<kWeights>(p, stream);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
