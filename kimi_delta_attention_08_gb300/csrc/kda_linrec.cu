@@ -737,16 +737,38 @@ __global__ void __launch_bounds__(32 * kWarps, kFwdBlocks<V>)
   if constexpr (!TMA) ptx::cp_async_wait_all();
 }
 
-// Single tokens and prompts of a few: a thread takes the channels of one sequence.
+// V states at once, which lie on V times their size.
+template <int V>
+__device__ __forceinline__ void load_states(float (&h)[V], const void* p, int64_t at, bool b16) {
+  if constexpr (V == 1) {
+    load_state<1>(h, p, at, b16);
+  } else if (b16) {
+    Raw<bf16, V> r;
+    load_words<true>(r.w, static_cast<const bf16*>(p) + at);
+    unpack(r, h);
+  } else {
+    Raw<float, V> r;
+    load_words<true>(r.w, static_cast<const float*>(p) + at);
+    unpack(r, h);
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_states(void* p, int64_t at, const float (&h)[V], bool b16) {
+  if (b16) store_row<bf16, V, (V > 1)>(static_cast<bf16*>(p) + at, h, 1, 1);
+  else store_row<float, V, (V > 1)>(static_cast<float*>(p) + at, h, 1, 1);
+}
+
+// Single tokens and prompts of a few: a thread takes four channels of one sequence, or as
+// many as their alignment allows.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) linrec_step_kernel(LinrecParams p) {
-  const int per = (p.dim + V - 1) / V;
+  const unsigned per = (unsigned)p.dim / V;
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t n = at / per;
-  const int ch = (int)(at % per) * V;
+  const int64_t n = p.units ? (unsigned)at / per : at / per;  // (units: 32 bits are enough)
+  const int ch = (int)(at - n * per) * V;
   if (n >= p.N) return;
   float h0[V] = {};
-  if (p.init) load_state<V>(h0, p.init, n * p.dim + ch, p.state_bf16);
+  if (p.init) load_states<V>(h0, p.init, n * p.dim + ch, p.state_bf16);
   Gates<V> c;
   load_gates<T>(c, p, ch, true);
   Vals<V> h = vals_from(h0);
@@ -764,7 +786,7 @@ __global__ void __launch_bounds__(256) linrec_step_kernel(LinrecParams p) {
     store_vals<T, V>(p.out, t * p.dim + ch, h0);
   }
   vals_to(h, h0);
-  if (p.fin) store_state<V>(p.fin, n * p.dim + ch, h0, p.state_bf16);
+  if (p.fin) store_states<V>(p.fin, n * p.dim + ch, h0, p.state_bf16);
 }
 
 // --------------------------------------------------------------- backward --
@@ -1297,10 +1319,14 @@ kda_status kda_linrec_fwd(const kda_linrec_problem* problem, void* out, void* fi
   p.status = static_cast<unsigned*>(workspace);
   if (step) {
     if (workspace && cudaMemsetAsync(workspace, 0, 4, stream) != cudaSuccess) return KDA_ERR_CUDA;
-    const int V = std::min(lanes, f32 ? 1 : 2);
-    const int64_t blocks = ((int64_t)p.N * ((p.dim + V - 1) / V) + 255) / 256;
+    lanes_for(lanes, p.init, p.state_bf16 ? 2 : 4);
+    lanes_for(lanes, p.fin, p.state_bf16 ? 2 : 4);
+    const int V = lanes == 2 ? 1 : lanes;
+    const int64_t threads = (int64_t)p.N * (p.dim / V), blocks = (threads + 255) / 256;
     if (blocks >= (int64_t(1) << 31)) return KDA_ERR_INVALID_SHAPE;
-    auto kernel = f32 ? linrec_step_kernel<float, 1> : V == 2 ? linrec_step_kernel<bf16, 2> : linrec_step_kernel<bf16, 1>;
+    p.units = threads < (int64_t(1) << 31);
+    auto kernel = f32 ? (V == 4 ? linrec_step_kernel<float, 4> : linrec_step_kernel<float, 1>)
+                      : (V == 4 ? linrec_step_kernel<bf16, 4> : linrec_step_kernel<bf16, 1>);
     kernel<<<(unsigned)blocks, 256, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
   }

@@ -153,10 +153,11 @@ def test_kept_values_of_every_size(kda_lib):
         assert (kept_values(pre)[0, 1] == 0).all() and kept_values(pre)[0, 2].isnan().all()
 
 
-def test_a_wait_that_runs_out_is_reported(kda_lib):
+@pytest.mark.parametrize("rows", [5, 300])
+def test_a_wait_that_runs_out_is_reported(kda_lib, rows):
     """Nothing is loaded: the products and the epilogue give up, and the next call is right."""
     import kimi_delta_attention_08_gb300 as kda
-    x, wg, wu, dout = make(300, 128, 256)
+    x, wg, wu, dout = make(rows, 1024 if rows == 5 else 128, 256)
     out, ws = torch.empty_like(dout), torch.empty(256, dtype=torch.uint8, device="cuda")
     t0 = time.time()
     kda.kda_glu_fwd(x, wg, wu, out, ws, debug_stall=True)

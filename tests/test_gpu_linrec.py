@@ -123,6 +123,23 @@ def test_state_in_place(kda_lib, seq):
     assert torch.equal(o.nan_to_num(nan=7.0), out.nan_to_num(nan=7.0))
 
 
+@pytest.mark.parametrize("sty", [F, BF])
+@pytest.mark.parametrize("off", [1, 2, 4])
+@pytest.mark.parametrize("T", [1, 9])
+def test_states_anywhere(kda_lib, T, off, sty):
+    """States that begin at any element of a buffer, next to values that stay."""
+    import kimi_delta_attention_08_gb300 as kda
+    a, b, _, _, _ = make((3, T, None), 64, BF, 4, sty=sty)
+    buf = [torch.full((3 * 64 + 16,), 7.0, dtype=sty, device="cuda") for _ in range(2)]
+    init, fin = (v[off:off + 192].view(3, 64) for v in buf)
+    init.copy_(b["initial_state"])
+    out, want, wfin = (torch.empty_like(a["x"]), torch.empty_like(a["x"]), torch.empty_like(b["initial_state"]))
+    kda.kda_linrec_fwd(**a, out=want, **b, final_state=wfin)
+    kda.kda_linrec_fwd(**a, out=out, **{**b, "initial_state": init}, final_state=fin)
+    assert torch.equal(out, want) and torch.equal(fin, wfin)
+    assert (buf[1][:off] == 7).all() and (buf[1][off + 192:] == 7).all()
+
+
 def test_tokens_one_at_a_time(kda_lib):
     """Carried states: a prompt, then single tokens, against the whole sequence at once."""
     import kimi_delta_attention_08_gb300 as kda
