@@ -18,6 +18,13 @@
 // Accumulation is fp32.  dg and du are rounded to bf16 between the two steps of the backward,
 // since the tensor cores take bf16: their error, half a step of bf16 each and independent
 // over the summed axis, adds as much to dx and dW as the outputs' own rounding.
+//
+// 4,096 by 12,288: 32,768 rows forward 3.83 ms (1.72 PFLOP/s), 4,096 rows 468 us (1.76), 256 rows
+// 56 us: 96 tiles on 76 pairs, the first 76 at HBM's rate.  16,384 rows forward with kept
+// pre-activations and backward 6.44 ms (1.54), backward that computes them again 6.19 ms
+// (1.60).  The tensor pipe is active in 79 to 82 % of the cycles; operands arrive at 12 to 13
+// TB/s from L2, which half the products would still need 2.9 ms for at 32,768 rows.
+// One row 35 us, 32 rows 36.5 (5.8 TB/s of weights).
 #include <algorithm>
 
 #include "kda_internal.h"
@@ -315,7 +322,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
 }
 
 // ------------------------------------------------------------- few rows --
-// The forward of up to kStepRows rows reads the weights once and is bound by that.  A CTA
+// The forward of up to kStepRows rows reads the weights once and is bound by that (128 rows 43
+// us, 192 rows as 256 x 256 tiles 55).  A CTA
 // takes 64 rows of both weights as the 128 rows of A, and all of x as B's columns, so the tensor
 // cores do no more work than the rows need; where the weights' rows alone do not fill the
 // GPU, a cluster splits the summed axis and adds up through its shared memory, in the order
