@@ -53,6 +53,9 @@ struct GluParams {
   int64_t M, N;            // of the output (columns: of one projection)
   int32_t k_blocks;        // of each of `sums` products that one tile adds up
   int32_t m_tiles, n_tiles;
+  int32_t whole, splits;   // tiles from `whole` on are split over as many pairs
+  float* parts;            // [tiles that are split][splits] sums
+  unsigned* counts;        // [tiles that are split][2][kEpilogueWarps] parts that are there
   int32_t fn, stall;
   int32_t keep;            // whether g and u are outputs too
   const bf16* dout;
@@ -97,6 +100,18 @@ __device__ __forceinline__ float kept_value(uint32_t k) {
   return m < 0x7E00u ? v : __uint_as_float(0x7FFFFFFFu);
 }
 
+// A pair's unit of work: a tile, or in the backward's last turn, which leaves pairs without a tile, a
+// part of a tile's summed axis.
+struct Unit {
+  int tile, part, from, to;  // part: -1 for a whole tile
+};
+template <bool SPLITS>
+__device__ __forceinline__ Unit unit_of(const GluParams& p, int u, int blocks) {
+  if (!SPLITS || u < p.whole || p.splits == 1) return {u, -1, 0, blocks};
+  const int v = u - p.whole, t = v / p.splits, part = v - t * p.splits;
+  return {p.whole + t, part, (int)((int64_t)blocks * part / p.splits), (int)((int64_t)blocks * (part + 1) / p.splits)};
+}
+
 // A tile of the walk: groups of sixteen tiles down, so that the pairs at work share operands
 // and a group's rows of A stay in L2 while it meets all of B.
 __device__ __forceinline__ void tile_of(const GluParams& p, int t, int& m, int& n) {
@@ -124,7 +139,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
   __shared__ int failed;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = ptx::cluster_rank();
-  const int total = p.m_tiles * p.n_tiles, first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int total = p.whole + (p.m_tiles * p.n_tiles - p.whole) * p.splits;  // units
+  const int first = blockIdx.x / 2, step = gridDim.x / 2;
   const int blocks = SUMS * p.k_blocks;
   if (threadIdx.x == 0) {
     failed = 0;
@@ -144,9 +160,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
     uint32_t stage = 0, parity = 1;
     bool ok = !p.stall;
     for (int t = first; t < total && ok; t += step) {
+      const Unit u = unit_of<!DUAL>(p, t, blocks);
       int m, n;
-      tile_of(p, t, m, n);
-      for (int kb = 0; kb < blocks && ok; ++kb) {
+      tile_of(p, u.tile, m, n);
+      for (int kb = u.from; kb < u.to && ok; ++kb) {
         ok = ptx::mbar_wait(&empty[stage], parity, kWaitNs);
         if (!ok) break;
         if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kStage);
@@ -186,9 +203,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
     uint32_t stage = 0, parity = 0, buf = 0, tparity = 1;
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
+      const Unit u = unit_of<!DUAL>(p, t, blocks);
       ok = ptx::mbar_wait(&tempty[buf], tparity, kWaitNs);
       ptx::tc_fence_after();
-      for (int kb = 0; kb < blocks && ok; ++kb) {
+      for (int kb = u.from; kb < u.to && ok; ++kb) {
         ok = ptx::mbar_wait(&full[stage], parity, kWaitNs);
         if (!ok) break;
         ptx::tc_fence_after();
@@ -196,7 +214,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
 #pragma unroll
         for (int k = 0; k < kTileK / 16; ++k)
           ptx::mma_bf16_ss_pair(tmem + buf * kTileN, ptx::sw128_desc(A + k * a_step, kOperand / 2, 1024),
-                                ptx::sw128_desc(B + k * b_step, kOperand / 2, 1024), idesc, kb + k > 0);
+                                ptx::sw128_desc(B + k * b_step, kOperand / 2, 1024), idesc, kb > u.from || k > 0);
         ptx::mma_commit_pair(&empty[stage]);
         if (++stage == kStages) stage = 0, parity ^= 1;
       }
@@ -232,9 +250,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
         ptx::tma_store_commit();
       }
     };
+    auto release = [&]() {
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(ptx::cluster_addr(&tempty[buf], 0));
+      buf ^= 1;
+      if (buf == 0) parity ^= 1;
+    };
     for (int t = first; t < total; t += step) {
+      const Unit u = unit_of<!DUAL>(p, t, blocks);
       int m, n;
-      tile_of(p, t, m, n);
+      tile_of(p, u.tile, m, n);
       int64_t row0 = (int64_t)m * kTileM;
       int which = 0;
       if constexpr (PASS == kWeights) {
@@ -256,10 +282,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
       ok = __all_sync(0xffffffffu, ptx::mbar_wait(&tfull[buf], parity, limit));
       if (!ok) break;
       ptx::tc_fence_after();
+      // The parts of a split tile go to memory, and the warp whose part comes last adds them up, in
+      // the order of the parts: nobody waits, and the sums are the same in every run.
+      constexpr int kPart = kTileM * kTileN;
+      const float* sums = nullptr;
+      if constexpr (!DUAL) {
+        if (u.part >= 0) {
+          const int split = u.tile - p.whole;
+          float* const mine =
+              p.parts + (int64_t)split * p.splits * kPart + (rank * kEpilogueWarps + w) * 32 * kColumns + lane;
+          float* to = mine + (int64_t)u.part * kPart;
+#pragma unroll 1
+          for (int c = 0; c < kColumns; c += 32, to += 32 * 32) {
+            uint32_t v[32];
+            ptx::tmem_ld32(acc + c, v);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) to[k * 32] = __uint_as_float(v[k]);
+          }
+          release();
+          __threadfence();
+          __syncwarp();
+          unsigned before = 0;
+          if (lane == 0) before = atomicAdd(p.counts + (split * 2 + rank) * kEpilogueWarps + w, 1u);
+          if (__shfl_sync(0xffffffffu, before, 0) != p.splits - 1) continue;
+          __threadfence();
+          sums = mine;
+        }
+      }
 #pragma unroll 1
       for (int c = 0; c < kColumns; c += 32) {
         uint32_t v[32];
-        ptx::tmem_ld32(acc + c, v);
+        if (DUAL || !sums) ptx::tmem_ld32(acc + c, v);
         auto pack = [&](const uint32_t (&f)[32]) {
           return [&](int k) { return pack_bf16(__uint_as_float(f[2 * k]), __uint_as_float(f[2 * k + 1])); };
         };
@@ -294,15 +348,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
             put(&p.o[1], col0 + c, row0, p.M, pack(q));
           }
         } else {
-          ptx::tmem_wait_ld();
+          if (sums) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = 0u;
+            const float* from = sums + c * 32;
+            for (int q = 0; q < p.splits; ++q, from += kPart)
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + __ldcg(from + k * 32));
+          } else {
+            ptx::tmem_wait_ld();
+          }
           put(&p.o[which], col0 + c, row0, p.M, pack(v));
         }
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(ptx::cluster_addr(&tempty[buf], 0));
-      buf ^= 1;
-      if (buf == 0) parity ^= 1;
+      if (DUAL || !sums) release();
     }
     if (lane == 0) ptx::tma_store_wait();
     if (!ok && lane == 0) failed = 1;
@@ -499,14 +558,45 @@ cudaError_t map_of(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, in
                           CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// How the backward splits its last turn's tiles: as often as pairs are left over, where a part has
+// 16 steps of the summed axis at least and a tile 48.  A tile's parts cost a few us on their way
+// through memory, a step 0.33 us.  Backward without and with: 100 rows of 4,096 by 12,288 243 and
+// 168 us, 512 rows of 2,048 by 6,144 127 and 92, 16,384 rows of 1,000 by 2,728 521 and 453; parts of
+// four steps lose up to 12 us at 1,024 hidden.  The forward's tiles stay
+// whole: 256 rows, which read the weights at HBM's rate in either case, came to 53.1 us for 53.8,
+// 512 rows of 2,048 by 6,144 to 32.7 for 29.2.
+constexpr int64_t kPairs = 76;  // a GB300's: a workspace's size is asked for without a device
+constexpr int64_t kMaxSplits = 8;
+struct Split {
+  int64_t whole, splits, split;  // tiles in whole turns; parts of each of the others; those
+};
+Split split_of(int64_t tiles, int64_t blocks) {
+  Split s = {tiles / kPairs * kPairs, 1, tiles % kPairs};
+  if (s.split > 0 && blocks >= 48) s.splits = std::max<int64_t>(1, std::min({kMaxSplits, kPairs / s.split, blocks / 16}));
+  return s;
+}
+// Counters of the parts of dx's tiles, then of the weights'.
+constexpr size_t kCounters = kPairs * 2 * kEpilogueWarps * sizeof(unsigned);
+constexpr size_t kHeader = KDA_STATUS_BYTES + 2 * kCounters;
+static_assert(kCounters % 256 == 0, "what follows is aligned");
+// The backward's dg, du and parts; the last for any width of the rows.
+size_t bwd_operand(int64_t M, int64_t F) { return up256((size_t)M * F * 2); }
+size_t bwd_bytes(int64_t M, int64_t F) {
+  if (M == 0) return KDA_STATUS_BYTES;
+  return kHeader + 2 * bwd_operand(M, F) + (size_t)kPairs * kTileM * kTileN * sizeof(float);
+}
+
+// counts: zeros.
 template <int PASS>
-cudaError_t launch(const GluParams& p, cudaStream_t stream) {
+cudaError_t launch(GluParams& p, const Split& s, float* parts, unsigned* counts, cudaStream_t stream) {
   static bool done[64];
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(glu_kernel<PASS>), kSmem, done);
   if (e != cudaSuccess) return e;
   int sms = 0;
   if (sm_count(&sms) != KDA_OK) return cudaErrorUnknown;
-  const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles, pairs = tiles < sms / 2 ? tiles : sms / 2;
+  p.whole = (int32_t)s.whole, p.splits = (int32_t)s.splits;
+  p.parts = parts, p.counts = counts;
+  const int64_t units = s.whole + s.split * p.splits, pairs = units < sms / 2 ? units : sms / 2;
   glu_kernel<PASS><<<(unsigned)(2 * pairs), 32 * (kEpilogueWarp + kEpilogueWarps), kSmem, stream>>>(p);
   return cudaGetLastError();
 }
@@ -547,7 +637,7 @@ cudaError_t launch_dual(const kda_glu_problem* q, bf16* o0, bf16* o1, uint16_t* 
   p.m_tiles = (int32_t)up(q->rows, kTileM), p.n_tiles = (int32_t)up(q->hidden, kHalf);
   p.fn = q->fn, p.stall = q->debug_stall, p.status = status;
   p.keep = pre != nullptr, p.dout = static_cast<const bf16*>(dout);
-  return launch<PASS>(p, stream);
+  return launch<PASS>(p, {(int64_t)p.m_tiles * p.n_tiles, 1, 0}, nullptr, nullptr, stream);
 }
 
 // Up to kStepRows rows.  As many CTAs share the summed axis as fit the GPU twice per SM, with four
@@ -607,7 +697,7 @@ kda_status kda_glu_fwd(const kda_glu_problem* problem, void* out, void* pre, voi
 kda_status kda_glu_bwd_get_workspace_size(int64_t rows, int32_t hidden, size_t* bytes) {
   if (!bytes) return KDA_ERR_NULL_POINTER;
   if (rows < 0 || rows >= (int64_t(1) << 31) || hidden < 8 || hidden % 8) return KDA_ERR_INVALID_SHAPE;
-  *bytes = KDA_STATUS_BYTES + 2 * kda::up256((size_t)rows * hidden * 2);
+  *bytes = kda::bwd_bytes(rows, hidden);
   return KDA_OK;
 }
 
@@ -630,14 +720,16 @@ kda_status kda_glu_bwd(const kda_glu_problem* problem, const void* dout, const v
   if (st != KDA_OK) return st;
   unsigned* const status = static_cast<unsigned*>(workspace);
   const int64_t M = q.rows, D = q.dim, F = q.hidden;
-  cudaError_t e = cudaMemsetAsync(status, 0, 4, stream);
+  cudaError_t e = cudaMemsetAsync(status, 0, M ? kHeader : 4, stream);
   if (M == 0) {  // sums of nothing
     if (e == cudaSuccess) e = cudaMemsetAsync(dw_gate, 0, (size_t)F * D * 2, stream);
     if (e == cudaSuccess) e = cudaMemsetAsync(dw_up, 0, (size_t)F * D * 2, stream);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
   }
-  bf16* const dg = reinterpret_cast<bf16*>(static_cast<uint8_t*>(workspace) + KDA_STATUS_BYTES);
-  bf16* const du = dg + up256((size_t)M * F * 2) / 2;
+  unsigned* const counts = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(workspace) + KDA_STATUS_BYTES);
+  bf16* const dg = reinterpret_cast<bf16*>(static_cast<uint8_t*>(workspace) + kHeader);
+  bf16* const du = dg + bwd_operand(M, F) / 2;
+  float* const parts = reinterpret_cast<float*>(du + bwd_operand(M, F) / 2);
   if (e == cudaSuccess) {
     if (pre) {
       const int64_t blocks = up(M * (F / 8), 256);
@@ -658,7 +750,7 @@ kda_status kda_glu_bwd(const kda_glu_problem* problem, const void* dout, const v
   p.M = M, p.N = D, p.k_blocks = (int32_t)up(F, kTileK), p.m_tiles = (int32_t)up(M, kTileM);
   p.n_tiles = (int32_t)up(D, kTileN);
   if (e == cudaSuccess) e = out_map(&p.o[0], dx, M, D, D);
-  if (e == cudaSuccess) e = launch<kInput>(p, stream);
+  if (e == cudaSuccess) e = launch<kInput>(p, split_of((int64_t)p.m_tiles * p.n_tiles, 2 * p.k_blocks), parts, counts, stream);
   // the weights' gradients: the gate's rows, then the other's
   if (e == cudaSuccess) e = map_of(&p.a[0], dg, M, F, F, kTileK);
   if (e == cudaSuccess) e = map_of(&p.a[1], du, M, F, F, kTileK);
@@ -666,7 +758,7 @@ kda_status kda_glu_bwd(const kda_glu_problem* problem, const void* dout, const v
   p.M = F, p.N = D, p.k_blocks = (int32_t)up(M, kTileK), p.m_tiles = (int32_t)(2 * up(F, kTileM));
   if (e == cudaSuccess) e = out_map(&p.o[0], dw_gate, F, D, D);
   if (e == cudaSuccess) e = out_map(&p.o[1], dw_up, F, D, D);
-  if (e == cudaSuccess) e = launch<kWeights>(p, stream);
+  if (e == cudaSuccess) e = launch<kWeights>(p, split_of((int64_t)p.m_tiles * p.n_tiles, p.k_blocks), parts, counts + kCounters / sizeof(unsigned), stream);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

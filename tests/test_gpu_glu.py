@@ -59,6 +59,29 @@ def test_backward(kda_lib, size, fn, kept):
         within(g[k], ref[k], k)
 
 
+@pytest.mark.parametrize("size", [(97, 136, 6160), (300, 264, 2056), (3100, 264, 520), (3100, 1032, 2560)])
+def test_tiles_that_several_pairs_compute(kda_lib, size):
+    """Sizes at which dx's tiles (the first two), the weights' (the third) or the last turn of both are
+    split along the summed axis: in a workspace of anything, and twice in the same one, the same
+    gradients bit for bit."""
+    import kimi_delta_attention_08_gb300 as kda
+    x, wg, wu, dout = make(*size, seed=3)
+    ref = glu(x, wg, wu, "silu", dout)
+    ws = kda.make_glu_bwd_workspace(size[0], size[2])
+    ws.fill_(0xFF)
+    first = None
+    for _ in range(4):
+        g = kda.kda_glu_bwd(x, wg, wu, dout, ws)
+        assert kda.kda_get_device_status(ws) == 0
+        got = {k: v for k, v in g.items() if k != "workspace"}
+        if first is None:
+            first = got
+            for k, v in got.items():
+                within(v, ref[k], k)
+        for k, v in got.items():
+            assert torch.equal(v, first[k]), k
+
+
 def test_many_tiles_in_batches_and_slices(kda_lib):
     """More tiles than pairs of CTAs in every pass, two sequences, rows of a wider projection,
     both weights as parts of one matrix."""
