@@ -19,9 +19,12 @@
 // since the tensor cores take bf16: their error, half a step of bf16 each and independent
 // over the summed axis, adds as much to dx and dW as the outputs' own rounding.
 //
+// Where tiles of 128 columns would take a second turn and wider ones do not, they are 160 or 192 wide;
+// the backward splits the sums of its last turn's tiles over the pairs left.
+//
 // 4,096 by 12,288: 32,768 rows forward 3.83 ms (1.72 PFLOP/s), 4,096 rows 468 us (1.76), 256 rows
-// 56 us: 96 tiles on 76 pairs, the first 76 at HBM's rate.  16,384 rows forward with kept
-// pre-activations and backward 6.44 ms (1.54), backward that computes them again 6.19 ms
+// 44 us, 64 wide tiles on 76 pairs (4.6 TB/s of weights).  16,384 rows forward with kept
+// pre-activations and backward 6.24 ms (1.58), backward that computes them again 6.17 ms
 // (1.60).  The tensor pipe is active in 79 to 82 % of the cycles; operands arrive at 12 to 13
 // TB/s from L2, which half the products would still need 2.9 ms for at 32,768 rows.
 // One row 35 us, 32 rows 36.5 (5.8 TB/s of weights).
@@ -42,6 +45,11 @@ constexpr uint32_t kOperand = kHalf * kTileK * 2, kStage = 2 * kOperand;  // byt
 constexpr int kEpilogueWarp = 4, kEpilogueWarps = 8;  // warps 4 .. 11
 constexpr uint32_t kOut = 32 * 64;               // 32 rows by 32 columns of an output, on their way
 constexpr uint32_t kSmem = kStages * kStage + kEpilogueWarps * 2 * kOut + 1024;
+// Wide tiles, of which a pair has one: up to 192 columns of each projection, five stages of 40 KB,
+// whose memory the outputs take when the products are done.
+constexpr int kWide = 192, kWideStages = 5;
+constexpr uint32_t kWideStage = kOperand + kWide * kTileK * 2;
+static_assert(kWideStages * kWideStage + 1024 <= kSmem && kEpilogueWarps * 2 * kOut <= kWideStage, "");
 constexpr uint64_t kWaitNs = 500000000ull;
 
 // What a launch computes.
@@ -53,6 +61,7 @@ struct GluParams {
   int64_t M, N;            // of the output (columns: of one projection)
   int32_t k_blocks;        // of each of `sums` products that one tile adds up
   int32_t m_tiles, n_tiles;
+  int32_t width;           // columns of each projection in a wide tile
   int32_t whole, splits;   // tiles from `whole` on are split over as many pairs
   float* parts;            // [tiles that are split][splits] sums
   unsigned* counts;        // [tiles that are split][2][kEpilogueWarps] parts that are there
@@ -126,15 +135,17 @@ __device__ __forceinline__ void store8(bf16* p, const float* f) {
       make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
 }
 
-template <int PASS>
+template <int PASS, bool WIDE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp + kEpilogueWarps), 1)
     glu_kernel(const __grid_constant__ GluParams p) {
   constexpr bool A_MN = PASS == kWeights, B_MN = PASS == kInput || PASS == kWeights;
   constexpr bool DUAL = PASS == kForward || PASS == kRecompute;
   constexpr int SUMS = PASS == kInput ? 2 : 1;
+  constexpr int STAGES = WIDE ? kWideStages : kStages;
+  constexpr uint32_t STAGE = WIDE ? kWideStage : kStage;
   extern __shared__ uint8_t raw[];
   uint8_t* const tiles = ptx::smem_align1024(raw);
-  __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2];
+  __shared__ uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2];
   __shared__ uint32_t tmem_at;
   __shared__ int failed;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -144,7 +155,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
   const int blocks = SUMS * p.k_blocks;
   if (threadIdx.x == 0) {
     failed = 0;
-    for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[s], 1), ptx::mbar_init(&empty[s], 1);
+    for (int s = 0; s < STAGES; ++s) ptx::mbar_init(&full[s], 1), ptx::mbar_init(&empty[s], 1);
     for (int b = 0; b < 2; ++b) ptx::mbar_init(&tfull[b], 1), ptx::mbar_init(&tempty[b], 2 * kEpilogueWarps);
     ptx::fence_mbar_init();
   }
@@ -166,9 +177,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
       for (int kb = u.from; kb < u.to && ok; ++kb) {
         ok = ptx::mbar_wait(&empty[stage], parity, kWaitNs);
         if (!ok) break;
-        if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kStage);
+        if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], WIDE ? 2 * (kOperand + (uint32_t)p.width * kTileK * 2) : 2 * kStage);
         const uint32_t bar = ptx::cluster_addr(&full[stage], 0);
-        uint8_t* const A = tiles + stage * kStage;
+        uint8_t* const A = tiles + stage * STAGE;
         uint8_t* const B = A + kOperand;
         const int part = SUMS == 2 && kb >= p.k_blocks, k0 = (kb - part * p.k_blocks) * kTileK;
         if constexpr (A_MN) {
@@ -185,20 +196,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
           ptx::tma_load_2d_pair(B, &p.b[part], bar, at, k0);
           ptx::tma_load_2d_pair(B + kOperand / 2, &p.b[part], bar, at + 64, k0);
         } else {
-          ptx::tma_load_2d_pair(B, &p.b[rank], bar, k0, n * kHalf);
+          ptx::tma_load_2d_pair(B, &p.b[rank], bar, k0, n * (WIDE ? p.width : kHalf));
         }
-        if (++stage == kStages) stage = 0, parity ^= 1;
+        if (++stage == STAGES) stage = 0, parity ^= 1;
       }
     }
     // every stage is read before the pair may go
-    for (int s = 0; s < kStages && ok; ++s) {
+    for (int s = 0; s < STAGES && ok; ++s) {
       ok = ptx::mbar_wait(&empty[stage], parity, kWaitNs);
-      if (++stage == kStages) stage = 0, parity ^= 1;
+      if (++stage == STAGES) stage = 0, parity ^= 1;
     }
     if (!ok) failed = 1;
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // products of the pair
     constexpr uint32_t idesc = ptx::idesc_bf16_f32(kTileM, kTileN, A_MN, B_MN);
+    const uint32_t rest = WIDE ? ptx::idesc_bf16_f32(kTileM, 2 * (p.width - kHalf), A_MN, B_MN) : 0;
     constexpr uint32_t a_step = A_MN ? 16 * 128 : 32, b_step = B_MN ? 16 * 128 : 32;
     uint32_t stage = 0, parity = 0, buf = 0, tparity = 1;
     bool ok = true;
@@ -210,17 +222,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
         ok = ptx::mbar_wait(&full[stage], parity, kWaitNs);
         if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t A = ptx::smem_u32(tiles + stage * kStage), B = A + kOperand;
+        const uint32_t A = ptx::smem_u32(tiles + stage * STAGE), B = A + kOperand;
 #pragma unroll
-        for (int k = 0; k < kTileK / 16; ++k)
-          ptx::mma_bf16_ss_pair(tmem + buf * kTileN, ptx::sw128_desc(A + k * a_step, kOperand / 2, 1024),
-                                ptx::sw128_desc(B + k * b_step, kOperand / 2, 1024), idesc, kb > u.from || k > 0);
+        for (int k = 0; k < kTileK / 16; ++k) {
+          const uint64_t a_desc = ptx::sw128_desc(A + k * a_step, kOperand / 2, 1024);
+          ptx::mma_bf16_ss_pair(tmem + buf * kTileN, a_desc, ptx::sw128_desc(B + k * b_step, kOperand / 2, 1024), idesc,
+                                kb > u.from || k > 0);
+          if constexpr (WIDE)  // the columns from the 129th on of both
+            ptx::mma_bf16_ss_pair(tmem + kTileN, a_desc, ptx::sw128_desc(B + kOperand + k * b_step, kOperand / 2, 1024),
+                                  rest, kb > u.from || k > 0);
+        }
         ptx::mma_commit_pair(&empty[stage]);
-        if (++stage == kStages) stage = 0, parity ^= 1;
+        if (++stage == STAGES) stage = 0, parity ^= 1;
       }
       if (!ok) break;
       ptx::mma_commit_pair(&tfull[buf]);
-      buf ^= 1;
+      if (!WIDE) buf ^= 1;
       if (buf == 0) tparity ^= 1;
     }
     if (!ok) failed = 1;
@@ -230,7 +247,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
     // row took 4 % of the largest forward and a fifth of the smallest backward.
     constexpr int kColumns = (DUAL ? kHalf : kTileN) / 2;
     const int w = warp - kEpilogueWarp, quarter = w % 4, side = w / 4;
-    uint8_t* const out = tiles + kStages * kStage + w * 2 * kOut;
+    // a wide tile's in turn: 160 columns have an odd number of 32
+    const int first_c = side * (WIDE ? 32 : kColumns), step_c = WIDE ? 64 : 32;
+    const int end_c = WIDE ? p.width : first_c + kColumns;
+    uint8_t* const out = tiles + (WIDE ? 0 : kStages * kStage) + w * 2 * kOut;
     const uint64_t limit = kWaitNs + (uint64_t)blocks * 2000;  // a whole tile's sum may be long
     uint32_t buf = 0, parity = 0, turn = 0;
     bool ok = true;
@@ -254,7 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster(ptx::cluster_addr(&tempty[buf], 0));
-      buf ^= 1;
+      if (!WIDE) buf ^= 1;
       if (buf == 0) parity ^= 1;
     };
     for (int t = first; t < total; t += step) {
@@ -269,8 +289,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
         row0 = (int64_t)(m - which * half) * kTileM;
       }
       row0 += rank * kHalf + quarter * 32;
-      const int64_t col0 = (int64_t)n * (DUAL ? kHalf : kTileN) + side * kColumns;
-      const uint32_t acc = tmem + buf * kTileN + side * kColumns + ((uint32_t)(quarter * 32) << 16);
+      const int64_t col0 = (int64_t)n * (WIDE ? p.width : DUAL ? kHalf : kTileN);
+      const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(quarter * 32) << 16);
       uint4 d[4] = {};       // dout of 32 columns, asked for ahead
       auto load = [&](int c) {
 #pragma unroll
@@ -278,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
           if (row0 + lane < p.M && col0 + c + 8 * k < p.N)
             d[k] = __ldg(reinterpret_cast<const uint4*>(p.dout + (row0 + lane) * p.N + col0 + c + 8 * k));
       };
-      if constexpr (PASS == kRecompute) load(0);
+      if constexpr (PASS == kRecompute) load(first_c);
       ok = __all_sync(0xffffffffu, ptx::mbar_wait(&tfull[buf], parity, limit));
       if (!ok) break;
       ptx::tc_fence_after();
@@ -295,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
 #pragma unroll 1
           for (int c = 0; c < kColumns; c += 32, to += 32 * 32) {
             uint32_t v[32];
-            ptx::tmem_ld32(acc + c, v);
+            ptx::tmem_ld32(acc + side * kColumns + c, v);
             ptx::tmem_wait_ld();
 #pragma unroll
             for (int k = 0; k < 32; ++k) to[k * 32] = __uint_as_float(v[k]);
@@ -311,15 +331,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
         }
       }
 #pragma unroll 1
-      for (int c = 0; c < kColumns; c += 32) {
+      for (int c = first_c; c < end_c; c += step_c) {
         uint32_t v[32];
-        if (DUAL || !sums) ptx::tmem_ld32(acc + c, v);
+        if (DUAL || !sums) ptx::tmem_ld32(acc + (WIDE && c >= kHalf ? kHalf : 0) + c, v);
         auto pack = [&](const uint32_t (&f)[32]) {
           return [&](int k) { return pack_bf16(__uint_as_float(f[2 * k]), __uint_as_float(f[2 * k + 1])); };
         };
         if constexpr (DUAL) {
           uint32_t q[32];
-          ptx::tmem_ld32(acc + kHalf + c, q);
+          ptx::tmem_ld32(acc + (WIDE && c >= kHalf ? p.width : kHalf) + c, q);
           ptx::tmem_wait_ld();
           if constexpr (PASS == kForward) {
             if (p.keep) {
@@ -343,7 +363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
               v[k] = __float_as_uint(dy * __uint_as_float(q[k]) * slope);
               q[k] = __float_as_uint(dy * f);
             }
-            if (c + 32 < kColumns) load(c + 32);
+            if (c + step_c < end_c) load(c + step_c);
             put(&p.o[0], col0 + c, row0, p.M, pack(v));
             put(&p.o[1], col0 + c, row0, p.M, pack(q));
           }
@@ -351,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
           if (sums) {
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] = 0u;
-            const float* from = sums + c * 32;
+            const float* from = sums + (c - first_c) * 32;
             for (int q = 0; q < p.splits; ++q, from += kPart)
 #pragma unroll
               for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + __ldcg(from + k * 32));
@@ -382,7 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
 
 // ------------------------------------------------------------- few rows --
 // The forward of up to kStepRows rows reads the weights once and is bound by that (128 rows 43
-// us, 192 rows as 256 x 256 tiles 55).  A CTA
+// us, 192 rows as wide tiles 44).  A CTA
 // takes 64 rows of both weights as the 128 rows of A, and all of x as B's columns, so the tensor
 // cores do no more work than the rows need; where the weights' rows alone do not fill the
 // GPU, a cluster splits the summed axis and adds up through its shared memory, in the order
@@ -587,17 +607,17 @@ size_t bwd_bytes(int64_t M, int64_t F) {
 }
 
 // counts: zeros.
-template <int PASS>
+template <int PASS, bool WIDE = false>
 cudaError_t launch(GluParams& p, const Split& s, float* parts, unsigned* counts, cudaStream_t stream) {
   static bool done[64];
-  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(glu_kernel<PASS>), kSmem, done);
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(glu_kernel<PASS, WIDE>), kSmem, done);
   if (e != cudaSuccess) return e;
   int sms = 0;
   if (sm_count(&sms) != KDA_OK) return cudaErrorUnknown;
   p.whole = (int32_t)s.whole, p.splits = (int32_t)s.splits;
   p.parts = parts, p.counts = counts;
   const int64_t units = s.whole + s.split * p.splits, pairs = units < sms / 2 ? units : sms / 2;
-  glu_kernel<PASS><<<(unsigned)(2 * pairs), 32 * (kEpilogueWarp + kEpilogueWarps), kSmem, stream>>>(p);
+  glu_kernel<PASS, WIDE><<<(unsigned)(2 * pairs), 32 * (kEpilogueWarp + kEpilogueWarps), kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -617,14 +637,29 @@ kda_status check_glu(const kda_glu_problem* q) {
   return KDA_OK;
 }
 
+// Columns of each projection in a wide tile, or 0: where tiles of 128 need a second turn and wider ones
+// do not.  256 rows of 4,096 by 12,288 as 96 tiles 54.6 us, as 64 wide ones 44.0; 512 rows of 2,048 by
+// 6,144 30.0 and 24.5; 1,024 rows of 1,000 by 2,728 20.4 and 16.2.  Several turns of wide tiles, which
+// have one accumulator, would put each one's epilogue after its products.
+int wide_of(int64_t down, int64_t hidden) {
+  int sms = 0;
+  if (sm_count(&sms) != KDA_OK || down * up(hidden, kHalf) <= sms / 2) return 0;
+  for (int w : {160, kWide})
+    if (down * up(hidden, w) <= sms / 2) return w;
+  return 0;
+}
+
 // The forward's tiles (also of the recomputing backward).
 template <int PASS>
 cudaError_t launch_dual(const kda_glu_problem* q, bf16* o0, bf16* o1, uint16_t* pre, const void* dout, unsigned* status,
                         cudaStream_t stream) {
   GluParams p = {};
+  const int64_t down = up(q->rows, kTileM);
+  const int wide = wide_of(down, q->hidden);
+  p.width = wide ? wide : kHalf;
   cudaError_t e = map_of(&p.a[0], q->x, q->rows, q->dim, q->x_stride, kHalf);
-  if (e == cudaSuccess) e = map_of(&p.b[0], q->w_gate, q->hidden, q->dim, q->dim, kHalf);
-  if (e == cudaSuccess) e = map_of(&p.b[1], q->w_up, q->hidden, q->dim, q->dim, kHalf);
+  if (e == cudaSuccess) e = map_of(&p.b[0], q->w_gate, q->hidden, q->dim, q->dim, p.width);
+  if (e == cudaSuccess) e = map_of(&p.b[1], q->w_up, q->hidden, q->dim, q->dim, p.width);
   if (e == cudaSuccess) e = out_map(&p.o[0], o0, q->rows, q->hidden, q->hidden);
   if (e == cudaSuccess && o1) e = out_map(&p.o[1], o1, q->rows, q->hidden, q->hidden);
   if (e == cudaSuccess && pre) {
@@ -634,9 +669,10 @@ cudaError_t launch_dual(const kda_glu_problem* q, bf16* o0, bf16* o1, uint16_t* 
   if (e != cudaSuccess) return e;
   p.M = q->rows, p.N = q->hidden;
   p.k_blocks = (int32_t)up(q->dim, kTileK);
-  p.m_tiles = (int32_t)up(q->rows, kTileM), p.n_tiles = (int32_t)up(q->hidden, kHalf);
+  p.m_tiles = (int32_t)down, p.n_tiles = (int32_t)up(q->hidden, p.width);
   p.fn = q->fn, p.stall = q->debug_stall, p.status = status;
   p.keep = pre != nullptr, p.dout = static_cast<const bf16*>(dout);
+  if (wide) return launch<PASS, true>(p, {(int64_t)p.m_tiles * p.n_tiles, 1, 0}, nullptr, nullptr, stream);
   return launch<PASS>(p, {(int64_t)p.m_tiles * p.n_tiles, 1, 0}, nullptr, nullptr, stream);
 }
 

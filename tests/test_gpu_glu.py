@@ -82,6 +82,28 @@ def test_tiles_that_several_pairs_compute(kda_lib, size):
             assert torch.equal(v, first[k]), k
 
 
+@pytest.mark.parametrize("fn", ["silu", "gelu"])
+@pytest.mark.parametrize("size", [(200, 1000, 9800), (256, 136, 12288), (129, 72, 14592), (600, 264, 4008)])
+def test_wide_tiles(kda_lib, size, fn):
+    """Sizes whose tiles of 128 columns take a second turn: they are 160 (the first and the last) or
+    192 wide, with fewer and more steps than stages; kept values, and a backward that computes
+    them again."""
+    import kimi_delta_attention_08_gb300 as kda
+    x, wg, wu, dout = make(*size, seed=4)
+    out, pre = torch.full_like(dout, float("nan")), torch.full((1, size[0], 2 * size[2]), float("nan"), dtype=BF, device="cuda")
+    kda.kda_glu_fwd(x, wg, wu, out, pre=pre, activation=fn)
+    ref = glu(x, wg, wu, fn, dout)
+    within(out, ref["out"], "out")
+    within(pre, glu(x, wg, wu, fn)["pre"], "pre")
+    again = torch.full_like(dout, float("nan"))
+    kda.kda_glu_fwd(x, wg, wu, again, activation=fn)
+    assert torch.equal(again, out)
+    g = kda.kda_glu_bwd(x, wg, wu, dout, activation=fn)
+    assert kda.kda_get_device_status(g["workspace"]) == 0
+    for k in ("dx", "dw_gate", "dw_up"):
+        within(g[k], ref[k], k)
+
+
 def test_many_tiles_in_batches_and_slices(kda_lib):
     """More tiles than pairs of CTAs in every pass, two sequences, rows of a wider projection,
     both weights as parts of one matrix."""
