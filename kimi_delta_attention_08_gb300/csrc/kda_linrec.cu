@@ -21,10 +21,10 @@
 // filled with ones before (no arithmetic result has these bits).  Waits give up after half a
 // second.
 //
-// Device time: forward, 8 x 4,096 tokens of 4,096 channels, bf16, 265 us (4.1 TB/s of rows; fp32
-// 342, 6.3 TB/s); 74,080 packed tokens of 2,048 channels with a gate 443; 65,536 + 5 x 1,024
-// tokens of 1,024 channels 203; forward and backward of 4 x 4,096 tokens of 4,096 channels with a
-// gate 578.  Bound by the issue of instructions (41 a value forward, 126 backward, 0.48 a clock
+// Device time: forward, 8 x 4,096 tokens of 4,096 channels, bf16, 259 us (4.2 TB/s of rows; fp32
+// 342, 6.3 TB/s); 74,080 packed tokens of 2,048 channels with a gate 441; 65,536 + 5 x 1,024
+// tokens of 1,024 channels 201; forward and backward of 4 x 4,096 tokens of 4,096 channels with a
+// gate 567.  Bound by the issue of instructions (42 a value forward, 126 backward, 0.48 a clock
 // and scheduler with 16 warps per SM, which the registers of decays and inputs allow) and, where
 // few channels leave many tiles of one at work, by waits: 154 us for the long prompt without
 // them.  Runs of 8 rows by four channels take 262, 502 and 261 us for the three
@@ -270,7 +270,7 @@ __device__ __forceinline__ void load_gates(Gates<V>& c, const LinrecParams& p, i
 }
 
 // a and b = m I x of a pair of values.  m^2 and m come scaled by 2^24 and 2^12, so that what
-// the hardware takes for zero (below 2^-126) is zero in fp32 too, and I by 2^-12.  From
+// the hardware takes for zero (below 2^-126) is zero in fp32 too, and I (fp32 rows) by 2^-12.  From
 // L2 = -L log2 e: small steps, u = 2 L up to 1/4, take 1 - exp(-u) = u P(u), P of degree 3 with
 // P(0) = 1 fitted by reweighted least squares to an even relative error (2.9e-7, half of
 // that in m); 1 - a^2 would have none of its digits right for them.  From there on 1 - a^2
@@ -280,6 +280,14 @@ template <typename T>
 __device__ __forceinline__ pair gate_exp(pair v, pair c) {  // exp(-(v + bias))
   if constexpr (sizeof(T) < 4) return pex2(pfma(v, pr(-kLog2e), c));
   else return exp_minus<T>(padd(v, c));
+}
+// exp(v + bias) of bf16 rows, at most 2^30: E / (1 + E) is 1 from 2^24 on.  NaN stays.
+__device__ __forceinline__ pair plus_exp(pair v, pair c) {
+  const float2 n = un(pfma(v, pr(-kLog2e), c));
+  float2 e = make_float2(ptx::ex2_approx(-n.x), ptx::ex2_approx(-n.y));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(e.x) : "f"(0x1p30f));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(e.y) : "f"(0x1p30f));
+  return pr(e.x, e.y);
 }
 __device__ __forceinline__ pair rcp_of(pair v) {
   return pr(ptx::rcp_approx(un(v).x), ptx::rcp_approx(un(v).y));
@@ -301,10 +309,18 @@ __device__ __forceinline__ pair scaled_m2(pair L2, pair a) {
 template <typename T>
 __device__ __forceinline__ void step_of(pair x, pair r, pair i, pair A2, pair cr, pair ci, pair& a, pair& b) {
   const pair L2 = pmul(A2, rcp_of(padd(gate_exp<T>(r, cr), pr(1.f))));
-  const pair I = rcp_of(pfma(gate_exp<T>(i, ci), pr(4096.f), pr(4096.f)));
   a = pex2(padd(L2, pr(2.5e-8f)));
   const pair m2 = scaled_m2(L2, a);
-  b = pmul(pmul(pmul(m2, rsqrt_of(m2)), I), x);
+  if constexpr (sizeof(T) < 4) {
+    // m I = m^2 E / sqrt(m^2 (1 + E)^2), E = exp(i): one operation of the special-function unit for
+    // the root and the reciprocal (8 x 4,096 tokens of 4,096 channels 265 to 259 us; fp32 rows, whose
+    // exponential costs more on this side, 342 to 347)
+    const pair E = plus_exp(i, ci), d = pfma(E, pr(4096.f), pr(4096.f));
+    b = pmul(pmul(pmul(m2, rsqrt_of(pmul(pmul(m2, d), d))), E), x);
+  } else {
+    const pair I = rcp_of(pfma(gate_exp<T>(i, ci), pr(4096.f), pr(4096.f)));
+    b = pmul(pmul(pmul(m2, rsqrt_of(m2)), I), x);
+  }
 }
 // Two rows' steps: single channels pair up across them.
 __device__ __forceinline__ pair two(const Vals<1>& u, const Vals<1>& v) { return pr(u.v[0], v.v[0]); }

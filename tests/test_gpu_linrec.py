@@ -294,6 +294,33 @@ def test_rates_of_zero_and_infinity(kda_lib):
         assert g[k].isfinite().all(), k
 
 
+@pytest.mark.parametrize("ty", [BF, F])
+@pytest.mark.parametrize("T", [3, 200])
+def test_infinite_gates(kda_lib, ty, T):
+    """Gates of plus and minus infinity are 1 and 0 exactly; an input gate that is NaN makes NaN from
+    its row on."""
+    import kimi_delta_attention_08_gb300 as kda
+    g = torch.Generator().manual_seed(6)
+    inf = float("inf")
+    pick = lambda *s: torch.tensor([-inf, inf])[torch.randint(2, s, generator=g)].to(ty).cuda()  # noqa: E731
+    D = 64
+    x, r, i = torch.randn(1, T, D, generator=g).to(ty).cuda(), pick(1, T, D), pick(1, T, D)
+    A = torch.linspace(-3, 2, D).cuda()
+    out = torch.empty_like(x)
+    kda.kda_linrec_fwd(x, r, i, A, out)
+    L = torch.exp(A.double().cpu()) * (r.double().cpu() > 0)
+    a, b = torch.exp(-L), torch.sqrt(1 - torch.exp(-2 * L)) * (i.double().cpu() > 0) * x.double().cpu()
+    h, want, mag, m = torch.zeros(D, dtype=torch.float64), [], [], torch.zeros(D, dtype=torch.float64)
+    for t in range(T):
+        h, m = a[0, t] * h + b[0, t], a[0, t] * m + b[0, t].abs()
+        want.append(h), mag.append(m)
+    # 2^-21 of a factor at most: as many steps for each token as in the other tests
+    R.close(out, torch.stack(want)[None], torch.stack(mag)[None], 8 * T + 64, "out")
+    i[0, T // 2] = float("nan")
+    kda.kda_linrec_fwd(x, r, i, A, out)
+    assert out[0, T // 2:].isnan().all() and out[0, :T // 2].isfinite().all()
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_what_is_not_finite_stays_in_its_sequence_and_channel(kda_lib, bad):
     import kimi_delta_attention_08_gb300 as kda
