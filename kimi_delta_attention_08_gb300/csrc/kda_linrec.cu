@@ -21,10 +21,10 @@
 // filled with ones before (no arithmetic result has these bits).  Waits give up after half a
 // second.
 //
-// Device time: forward, 8 x 4,096 tokens of 4,096 channels, bf16, 259 us (4.2 TB/s of rows; fp32
-// 342, 6.3 TB/s); 74,080 packed tokens of 2,048 channels with a gate 441; 65,536 + 5 x 1,024
-// tokens of 1,024 channels 201; forward and backward of 4 x 4,096 tokens of 4,096 channels with a
-// gate 567.  Bound by the issue of instructions (42 a value forward, 126 backward, 0.48 a clock
+// Device time: forward, 8 x 4,096 tokens of 4,096 channels, bf16, 258 us (4.2 TB/s of rows; fp32
+// 342, 6.3 TB/s); 74,080 packed tokens of 2,048 channels with a gate 433; 65,536 + 5 x 1,024
+// tokens of 1,024 channels 202; forward and backward of 4 x 4,096 tokens of 4,096 channels with a
+// gate 561.  Bound by the issue of instructions (42 a value forward, 126 backward, 0.48 a clock
 // and scheduler with 16 warps per SM, which the registers of decays and inputs allow) and, where
 // few channels leave many tiles of one at work, by waits: 154 us for the long prompt without
 // them.  Runs of 8 rows by four channels take 262, 502 and 261 us for the three
@@ -96,16 +96,36 @@ __device__ __forceinline__ unsigned published(float v) {
   return b == ~0u ? 0x7FFFFFFFu : b;
 }
 
-// The sequence of row t and its bounds; false where t belongs to none.
-__device__ __forceinline__ bool row_sequence(const LinrecParams& p, int64_t t, int& n, int64_t& bos,
+// The last sequence that starts at row t or before, searched for by a warp, 32 places at a time.
+__device__ __noinline__ int sequence_at(const int64_t* cu, int N, int64_t t, int lane) {
+  int lo = 0, hi = N;
+  while (hi - lo > 1) {
+    const unsigned each = ((unsigned)(hi - lo) + 31) / 32, at = lo + lane * each;
+    const unsigned below = __ballot_sync(0xffffffffu, at < (unsigned)hi && (lane == 0 || __ldg(cu + at) <= t));
+    lo += (31 - __clz(below)) * each;
+    hi = (int)min((unsigned)hi, lo + each);
+  }
+  return lo;
+}
+// The sequence of row t, a lane's of 32 that follow one another, and its bounds; false where t belongs
+// to none.  Of many sequences the first row's is found by all lanes together; the others' are among the
+// next 32 but for empty ones (2,000 single tokens of 4,096 channels 81 us without, 58 with it; not
+// `TOGETHER` in the kernels for rows off 16 bytes, whose registers would not take it).
+template <bool TOGETHER>
+__device__ __forceinline__ bool row_sequence(const LinrecParams& p, int64_t t, int lane, int& n, int64_t& bos,
                                              int64_t& eos) {
-  if (t >= p.total) return false;
   if (!p.cu) {
+    if (t >= p.total) return false;
     n = (int)((uint32_t)t / (uint32_t)p.T);
     bos = (int64_t)n * p.T, eos = bos + p.T;
     return true;
   }
   int lo = 0, hi = p.N;
+  if (TOGETHER && hi > 64) {
+    lo = sequence_at(p.cu, hi, t - lane, lane);
+    if (hi - lo > 33 && __ldg(p.cu + lo + 33) > t) hi = lo + 33;
+  }
+  if (t >= p.total) return false;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
     if (__ldg(p.cu + mid) <= t) lo = mid;
@@ -225,14 +245,15 @@ struct TileRows {
   uint32_t start[TILE / 32], last[TILE / 32], live[TILE / 32];  // first row of its sequence, last one, of any
   int64_t bos, eos;              // of the first row's sequence, of the last row's
 };
-template <int TILE>
-__device__ __forceinline__ void find_rows(TileRows<TILE>& s, const LinrecParams& p, int64_t row0, int lane) {
+template <bool TOGETHER, int TILE>
+__device__ __forceinline__ void find_rows(TileRows<TILE>& s, const LinrecParams& p, int64_t row0, int lane,
+                                          int first = 0, int step = 1) {  // of a tile's 32 rows each
 #pragma unroll
-  for (int h = 0; h < TILE / 32; ++h) {
+  for (int h = first; h < TILE / 32; h += step) {
     const int64_t t = row0 + 32 * h + lane;
     int n = 0;
     int64_t bos = 0, eos = 0;
-    const bool live = row_sequence(p, t, n, bos, eos);
+    const bool live = row_sequence<TOGETHER>(p, t, lane, n, bos, eos);
     s.n[32 * h + lane] = n;
     const unsigned start = __ballot_sync(0xffffffffu, live && t == bos);
     const unsigned last = __ballot_sync(0xffffffffu, live && t + 1 == eos);
@@ -389,12 +410,12 @@ struct BlockShared {
   Unit unit[2];
 };
 // The first turn's unit and rows.
-template <bool FORWARD, int V, int TILE>
+template <bool FORWARD, bool TOGETHER, int V, int TILE>
 __device__ __forceinline__ void start_block(const LinrecParams& p, BlockShared<V, TILE>& sh, int warp, int lane) {
   if (threadIdx.x == 0) sh.unit[0] = unit_of(p, atomicAdd(p.ticket, 1u));
   __syncthreads();
   const int64_t s = sh.unit[0].tile;
-  if (warp == 0 && s >= 0) find_rows(sh.rows[0], p, (FORWARD ? s : p.tiles - 1 - s) * TILE, lane);
+  if (s >= 0) find_rows<TOGETHER>(sh.rows[0], p, (FORWARD ? s : p.tiles - 1 - s) * TILE, lane, warp, kWarps);
   __syncthreads();
 }
 template <int V>
@@ -611,7 +632,7 @@ __global__ void __launch_bounds__(32 * kWarps, kFwdBlocks<V>)
     ptx::mbar_init(&full[0][threadIdx.x], 1);
     ptx::fence_mbar_init();
   }
-  start_block<true>(p, sh, warp, lane);
+  start_block<true, TMA || V == 2>(p, sh, warp, lane);
   uint8_t* const run = slots + warp * S::kRun;
   const uint8_t* const mine = run + lane * S::kBytes;
   auto place = [&](const Unit& u, int64_t& row0, int& ch) {  // the rows that exist
@@ -685,13 +706,18 @@ __global__ void __launch_bounds__(32 * kWarps, kFwdBlocks<V>)
     Vals<V> a[R], b[R];
     steps_of<T>([&](int k, int j) { return S::get(mine + k * S::kArray, j); }, c, a, b);
     if (bits.start && p.init) {  // a sequence's first step starts from its initial state
+      constexpr int kAhead = 4;  // loads on their way at once (256 single tokens 18.7 to 16.9 us)
 #pragma unroll
-      for (int j = 0; j < R; ++j)
-        if (ok && (bits.start >> j & 1)) {
-          float h0[V];
-          load_state<V>(h0, p.init, (int64_t)rows.n[warp * R + j] * p.dim + ch, p.state_bf16);
-          b[j] = fma_of(a[j], vals_from(h0), b[j]);
-        }
+      for (int j = 0; j < R; j += kAhead) {
+        float h0[kAhead][V] = {};
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (ok && (bits.start >> (j + k) & 1))
+            load_state<V>(h0[k], p.init, (int64_t)rows.n[warp * R + j + k] * p.dim + ch, p.state_bf16);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (bits.start >> (j + k) & 1) b[j + k] = fma_of(a[j + k], vals_from(h0[k]), b[j + k]);
+      }
     }
     // what the run does to a state
     Vals<V> P = a[0], h = b[0];
@@ -723,7 +749,7 @@ __global__ void __launch_bounds__(32 * kWarps, kFwdBlocks<V>)
       }
     }
     if (warp == kWarps - 1 && next.tile >= 0)  // meanwhile: the next turn's rows
-      find_rows(sh.rows[(turn + 1) & 1], p, (int64_t)next.tile * kTileF, lane);
+      find_rows<TMA || V == 2>(sh.rows[(turn + 1) & 1], p, (int64_t)next.tile * kTileF, lane);
     __syncthreads();
     if constexpr (OUT) {
       if (p.z) arrived(1, turn);
@@ -888,7 +914,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(const __grid
   __shared__ __align__(8) unsigned char fw_cut[kWarps];
   __shared__ __align__(16) float sums[3][kWarps][CH];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  start_block<false>(p, sh, warp, lane);
+  start_block<false, true>(p, sh, warp, lane);
   const uint8_t* const mine0 = slots + warp * S::kRun + lane * S::kBytes;
   const uint32_t at0 = ptx::smem_u32(mine0), at_gates0 = ptx::smem_u32(slots + 5 * S::kArray + threadIdx.x * V * 4);
   auto place = [&](const Unit& u, int64_t& row0, int& ch) {  // the rows that exist
@@ -1017,7 +1043,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(const __grid
                                         p.states[tile * p.dim + join.ch]);
     } else if (warp == kWarps - 1) {  // meanwhile: the next turn's rows
       const Unit next = sh.unit[(turn + 1) & 1];
-      if (next.tile >= 0) find_rows(sh.rows[(turn + 1) & 1], p, (p.tiles - 1 - next.tile) * kTileB, lane);
+      if (next.tile >= 0) find_rows<true>(sh.rows[(turn + 1) & 1], p, (p.tiles - 1 - next.tile) * kTileB, lane);
     }
     if (warp == kWarps - 2 && turn > 0) add_runs(last_tile, last_c0);
     __syncthreads();
@@ -1103,10 +1129,9 @@ struct SetupParams {
 __global__ void __launch_bounds__(256) linrec_setup_kernel(SetupParams p) {
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
   for (int64_t k = at; k < p.count; k += step) p.words[k] = kUnset;
-  if (blockIdx.x == 0 && threadIdx.x < 32) {
-    if (p.cu) check_seqlens(p.cu, p.N, p.total, p.status, kDevStatusBadSeqlens);
-    else if (threadIdx.x == 0) p.status[0] = 0u;
-    if (threadIdx.x >= 1) p.status[threadIdx.x] = 0u;
+  if (blockIdx.x == 0) {
+    const bool bad = __syncthreads_or(p.cu && bad_seqlens(p.cu, p.N, p.total, threadIdx.x, 256));
+    if (threadIdx.x < 32) p.status[threadIdx.x] = threadIdx.x == 0 && bad ? kDevStatusBadSeqlens : 0u;
   }
   for (int64_t d = at; d < p.dim; d += step) {
     p.gates[d] = scan::rate_of(p.A_log[d]);

@@ -351,14 +351,17 @@ __device__ __forceinline__ int find_sequence(const int64_t* cu, int N, int64_t t
 
 // Writes the status word of a workspace from a full check of cu_seqlens: one warp.
 // cu[0] = 0, non-decreasing, cu[N] <= total.
-__device__ __forceinline__ void check_seqlens(const int64_t* cu, int N, int64_t total,
-                                              unsigned* status, unsigned bad_bit) {
+__device__ __forceinline__ bool bad_seqlens(const int64_t* cu, int N, int64_t total, int first, int step) {
   bool bad = false;
-  for (int i = threadIdx.x & 31; i <= N; i += 32) {
+  for (int i = first; i <= N; i += step) {
     const int64_t c = cu[i];
     bad |= c < 0 || c > total || (i == 0 && c != 0) || (i < N && cu[i + 1] < c);
   }
-  bad = __any_sync(0xffffffffu, bad);
+  return bad;
+}
+__device__ __forceinline__ void check_seqlens(const int64_t* cu, int N, int64_t total,
+                                              unsigned* status, unsigned bad_bit) {
+  const bool bad = __any_sync(0xffffffffu, bad_seqlens(cu, N, total, threadIdx.x & 31, 32));
   if ((threadIdx.x & 31) == 0) *status = bad ? bad_bit : 0u;
 }
 

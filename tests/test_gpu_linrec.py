@@ -343,6 +343,44 @@ def test_what_is_not_finite_stays_in_its_sequence_and_channel(kda_lib, bad):
     assert torch.equal(fin[:, only], wfin[:, only]) and torch.equal(g["dA_log"][only], wg["dA_log"][only])
 
 
+def many(kind):
+    """More sequences than are searched one by one: single tokens; short and empty ones; runs of empty
+    ones longer than what a warp looks at, between some long ones; rows behind the last."""
+    g = torch.Generator().manual_seed(8)
+    if kind == "tokens":
+        n = [1] * 300
+    elif kind == "short":
+        n = torch.randint(0, 6, (400,), generator=g).tolist()
+    else:
+        n = ([0] * 40 + [3] + [0] * 70 + [130, 1, 0, 2]) * 4
+    cu = [0]
+    for v in n:
+        cu.append(cu[-1] + v)
+    return 1, cu[-1] + (9 if kind == "empty" else 0), cu
+
+
+@pytest.mark.parametrize("ty,dim", [(BF, 64), (BF, 37), (F, 40)])
+@pytest.mark.parametrize("kind", ["tokens", "short", "empty"])
+def test_many_sequences(kda_lib, kind, ty, dim):
+    import kimi_delta_attention_08_gb300 as kda
+    check_fwd(kda, many(kind), dim, ty)
+    check_bwd(kda, many(kind), dim, ty)
+
+
+def test_many_bad_sequences_are_reported(kda_lib):
+    """Bounds out of order, beyond the rows or below zero, among many: a status, nothing out of range."""
+    import kimi_delta_attention_08_gb300 as kda
+    g = torch.Generator().manual_seed(9)
+    for cu in ([0] + torch.randint(-50, 400, (200,), generator=g).tolist(), [0] * 100 + [500] * 100, list(range(150, -1, -1))):
+        a, b, dout, _, cud = make((1, 200, cu), 64, BF, 2)
+        ws = kda.make_linrec_workspace(1, 200, 64, len(cu) - 1)
+        fin = torch.empty(len(cu) - 1, 64, device="cuda")
+        kda.kda_linrec_fwd(**a, out=torch.empty_like(dout), **b, final_state=fin, cu_seqlens=cud, workspace=ws)
+        assert kda.kda_get_device_status(ws) == 9
+        g2 = kda.kda_linrec_bwd(**a, dout=dout, **b, cu_seqlens=cud)
+        assert kda.kda_get_device_status(g2["workspace"]) == 9
+
+
 def test_bad_sequences_are_reported(kda_lib):
     import kimi_delta_attention_08_gb300 as kda
     for cu in ([0, 50, 40, 200], [3, 50, 200], [0, 50, 300], [0, -5, 200]):
