@@ -21,10 +21,10 @@
 // filled with ones before (no arithmetic result has these bits).  Waits give up after half a
 // second.
 //
-// Device time: forward, 8 x 4,096 tokens of 4,096 channels, bf16, 258 us (4.2 TB/s of rows; fp32
-// 342, 6.3 TB/s); 74,080 packed tokens of 2,048 channels with a gate 433; 65,536 + 5 x 1,024
-// tokens of 1,024 channels 202; forward and backward of 4 x 4,096 tokens of 4,096 channels with a
-// gate 561.  Bound by the issue of instructions (42 a value forward, 126 backward, 0.48 a clock
+// Device time: forward, 8 x 4,096 tokens of 4,096 channels, bf16, 257 us (4.2 TB/s of rows; fp32
+// 342, 6.3 TB/s); 74,080 packed tokens of 2,048 channels with a gate 431; 65,536 + 5 x 1,024
+// tokens of 1,024 channels 201; forward and backward of 4 x 4,096 tokens of 4,096 channels with a
+// gate 559.  Bound by the issue of instructions (42 a value forward, 126 backward, 0.48 a clock
 // and scheduler with 16 warps per SM, which the registers of decays and inputs allow) and, where
 // few channels leave many tiles of one at work, by waits: 154 us for the long prompt without
 // them.  Runs of 8 rows by four channels take 262, 502 and 261 us for the three
@@ -412,6 +412,7 @@ struct BlockShared {
 // The first turn's unit and rows.
 template <bool FORWARD, bool TOGETHER, int V, int TILE>
 __device__ __forceinline__ void start_block(const LinrecParams& p, BlockShared<V, TILE>& sh, int warp, int lane) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the launch before, see launch_behind
   if (threadIdx.x == 0) sh.unit[0] = unit_of(p, atomicAdd(p.ticket, 1u));
   __syncthreads();
   const int64_t s = sh.unit[0].tile;
@@ -1127,6 +1128,7 @@ struct SetupParams {
   int32_t src_bf16, dst_bf16;
 };
 __global__ void __launch_bounds__(256) linrec_setup_kernel(SetupParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
   for (int64_t k = at; k < p.count; k += step) p.words[k] = kUnset;
   if (blockIdx.x == 0) {
@@ -1235,14 +1237,26 @@ cudaError_t launch_setup(const LinrecParams& p, bool f32, void* words, size_t by
   return cudaGetLastError();
 }
 
+// A launch whose blocks may start while the one before it, always one of ours, still runs: they wait
+// for its end before they read anything of it (512 tokens of 1,024 channels 9.4 to 8.8 us, 2,048 of 4,096
+// 28.9 to 27.9).
+template <typename... A>
+cudaError_t launch_behind(void (*kernel)(A...), unsigned grid, int smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid), c.blockDim = dim3(32 * kWarps), c.dynamicSmemBytes = smem, c.stream = stream;
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &a, c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
 template <typename K>
 cudaError_t launch_tiles(K kernel, bool (&done)[64], int smem, int blocks, const LinrecParams& p, cudaStream_t stream) {
   int sms = 0;
   if (sm_count(&sms) != KDA_OK) return cudaErrorUnknown;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), smem, done);
   if (e != cudaSuccess) return e;
-  kernel<<<std::min(p.units, (unsigned)(blocks * sms)), 32 * kWarps, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_behind(kernel, std::min(p.units, (unsigned)(blocks * sms)), smem, stream, p);
 }
 template <typename T>
 cudaError_t rows_map(CUtensorMap* m, const void* p, const LinrecParams& q, uint32_t stride, int channels) {
@@ -1269,16 +1283,14 @@ cudaError_t launch_fwd_of(const LinrecParams& p, bool tma, cudaStream_t stream) 
       auto kernel = linrec_fwd_kernel<T, V, OUT, true>;
       if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), 4 * Slots<T, V, kRowsF>::kArray, done);
       if (e != cudaSuccess) return e;
-      kernel<<<grid, 32 * kWarps, smem, stream>>>(p, maps);
-      return cudaGetLastError();
+      return launch_behind(kernel, grid, smem, stream, p, maps);
     }
   }
   static bool done[64];
   auto kernel = linrec_fwd_kernel<T, V, OUT, false>;
   e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), 4 * Slots<T, V, kRowsF>::kArray, done);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, 32 * kWarps, smem, stream>>>(p, maps);
-  return cudaGetLastError();
+  return launch_behind(kernel, grid, smem, stream, p, maps);
 }
 template <typename T, int V>
 cudaError_t launch_bwd_of(const LinrecParams& p, cudaStream_t stream) {
