@@ -67,6 +67,7 @@ struct GluParams {
   unsigned* counts;        // [tiles that are split][2][kEpilogueWarps] parts that are there
   int32_t fn, stall;
   int32_t keep;            // whether g and u are outputs too
+  int32_t ahead;           // whether the weights' gradients may start before dx ends
   const bf16* dout;
   unsigned* status;
 };
@@ -165,6 +166,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_at;
+  // The backward's launches are in their places before the one ahead ends: dx waits for dg and du, and
+  // the weights' gradients, which do not need dx, for dx, before their first tile or (`ahead`) their end.
+  if (PASS == kInput || (PASS == kWeights && !p.ahead)) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (PASS == kInput || PASS == kRecompute) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0 && lane == 0) {
     // loads: this CTA's half of both operands
@@ -398,6 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
   ptx::cluster_sync();
   ptx::tc_fence_after();
   if (warp == 2) ptx::tmem_dealloc_pair(tmem, 2 * kTileN);
+  if constexpr (PASS == kWeights) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------- few rows --
@@ -586,24 +592,25 @@ cudaError_t map_of(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, in
 // whole: 256 rows, which read the weights at HBM's rate in either case, came to 53.1 us for 53.8,
 // 512 rows of 2,048 by 6,144 to 32.7 for 29.2.
 constexpr int64_t kPairs = 76;  // a GB300's: a workspace's size is asked for without a device
-constexpr int64_t kMaxSplits = 8;
+constexpr int64_t kMaxSplits = 8, kSplitBlocks = 48;
 struct Split {
   int64_t whole, splits, split;  // tiles in whole turns; parts of each of the others; those
 };
 Split split_of(int64_t tiles, int64_t blocks) {
   Split s = {tiles / kPairs * kPairs, 1, tiles % kPairs};
-  if (s.split > 0 && blocks >= 48) s.splits = std::max<int64_t>(1, std::min({kMaxSplits, kPairs / s.split, blocks / 16}));
+  if (s.split > 0 && blocks >= kSplitBlocks) s.splits = std::max<int64_t>(1, std::min({kMaxSplits, kPairs / s.split, blocks / 16}));
   return s;
 }
 // Counters of the parts of dx's tiles, then of the weights'.
 constexpr size_t kCounters = kPairs * 2 * kEpilogueWarps * sizeof(unsigned);
 constexpr size_t kHeader = KDA_STATUS_BYTES + 2 * kCounters;
 static_assert(kCounters % 256 == 0, "what follows is aligned");
-// The backward's dg, du and parts; the last for any width of the rows.
+// The backward's dg, du and parts of dx's tiles and of the weights', for any width of the rows.
 size_t bwd_operand(int64_t M, int64_t F) { return up256((size_t)M * F * 2); }
+size_t parts_bytes(int64_t blocks) { return blocks < kSplitBlocks ? 0 : (size_t)kPairs * kTileM * kTileN * sizeof(float); }
 size_t bwd_bytes(int64_t M, int64_t F) {
   if (M == 0) return KDA_STATUS_BYTES;
-  return kHeader + 2 * bwd_operand(M, F) + (size_t)kPairs * kTileM * kTileN * sizeof(float);
+  return kHeader + 2 * bwd_operand(M, F) + parts_bytes(2 * up(F, kTileK)) + parts_bytes(up(M, kTileK));
 }
 
 // counts: zeros.
@@ -617,8 +624,14 @@ cudaError_t launch(GluParams& p, const Split& s, float* parts, unsigned* counts,
   p.whole = (int32_t)s.whole, p.splits = (int32_t)s.splits;
   p.parts = parts, p.counts = counts;
   const int64_t units = s.whole + s.split * p.splits, pairs = units < sms / 2 ? units : sms / 2;
-  glu_kernel<PASS, WIDE><<<(unsigned)(2 * pairs), 32 * (kEpilogueWarp + kEpilogueWarps), kSmem, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)(2 * pairs)), c.blockDim = dim3(32 * (kEpilogueWarp + kEpilogueWarps));
+  c.dynamicSmemBytes = kSmem, c.stream = stream;
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &a, c.numAttrs = PASS == kInput || PASS == kWeights;  // see glu_kernel
+  return cudaLaunchKernelEx(&c, glu_kernel<PASS, WIDE>, p);
 }
 
 kda_status check_glu(const kda_glu_problem* q) {
@@ -787,14 +800,21 @@ kda_status kda_glu_bwd(const kda_glu_problem* problem, const void* dout, const v
   p.n_tiles = (int32_t)up(D, kTileN);
   if (e == cudaSuccess) e = out_map(&p.o[0], dx, M, D, D);
   if (e == cudaSuccess) e = launch<kInput>(p, split_of((int64_t)p.m_tiles * p.n_tiles, 2 * p.k_blocks), parts, counts, stream);
-  // the weights' gradients: the gate's rows, then the other's
+  // The weights' gradients start where dx leaves pairs without work, if it has two turns of tiles at
+  // most: 4,097 rows of 1,000 by 2,728 138 us without, 132 with it, of 256 by 1,024 50 and 36.  Behind
+  // a longer dx the pairs would come out of step and share less of what L2 holds: 4,097 rows of 4,096 by
+  // 12,288 1,524 us without, 1,597 with it.
+  p.ahead = (int64_t)p.m_tiles * p.n_tiles <= 2 * kPairs;
+  // the gate's rows, then the other's
   if (e == cudaSuccess) e = map_of(&p.a[0], dg, M, F, F, kTileK);
   if (e == cudaSuccess) e = map_of(&p.a[1], du, M, F, F, kTileK);
   if (e == cudaSuccess) e = map_of(&p.b[0], q.x, M, D, q.x_stride, kTileK);
   p.M = F, p.N = D, p.k_blocks = (int32_t)up(M, kTileK), p.m_tiles = (int32_t)(2 * up(F, kTileM));
   if (e == cudaSuccess) e = out_map(&p.o[0], dw_gate, F, D, D);
   if (e == cudaSuccess) e = out_map(&p.o[1], dw_up, F, D, D);
-  if (e == cudaSuccess) e = launch<kWeights>(p, split_of((int64_t)p.m_tiles * p.n_tiles, p.k_blocks), parts, counts + kCounters / sizeof(unsigned), stream);
+  if (e == cudaSuccess) e = launch<kWeights>(p, split_of((int64_t)p.m_tiles * p.n_tiles, p.k_blocks),
+                                               parts + parts_bytes(2 * up(F, kTileK)) / sizeof(float),
+                                               counts + kCounters / sizeof(unsigned), stream);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
