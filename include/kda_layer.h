@@ -262,7 +262,8 @@ typedef struct {
 KDA_API kda_status kda_glu_fwd(const kda_glu_problem* p, void* out, void* pre, void* workspace,
                                size_t workspace_bytes, cudaStream_t stream);
 
-/* Bytes of workspace of kda_glu_bwd (status word, and the gradients of g and u in bf16). */
+/* Bytes of workspace of kda_glu_bwd: status word, the gradients of g and u in bf16, and up to 40 MB
+ * for sums of tiles that several SMs share. */
 KDA_API kda_status kda_glu_bwd_get_workspace_size(int64_t rows, int32_t hidden, size_t* bytes);
 
 /* kda_glu_bwd -- the gradients of <dout, out>: dx [rows, dim], dw_gate and dw_up

@@ -24,7 +24,7 @@
 // Device time: forward, 8 x 4,096 tokens of 4,096 channels, bf16, 257 us (4.2 TB/s of rows; fp32
 // 342, 6.3 TB/s); 74,080 packed tokens of 2,048 channels with a gate 431; 65,536 + 5 x 1,024
 // tokens of 1,024 channels 201; forward and backward of 4 x 4,096 tokens of 4,096 channels with a
-// gate 559.  Bound by the issue of instructions (42 a value forward, 126 backward, 0.48 a clock
+// gate 559.  Bound by the issue of instructions (41 a value forward, 124 backward, 0.5 a clock
 // and scheduler with 16 warps per SM, which the registers of decays and inputs allow) and, where
 // few channels leave many tiles of one at work, by waits: 154 us for the long prompt without
 // them.  Runs of 8 rows by four channels take 262, 502 and 261 us for the three
