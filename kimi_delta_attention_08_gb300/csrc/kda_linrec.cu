@@ -843,26 +843,28 @@ __global__ void __launch_bounds__(256) linrec_step_kernel(LinrecParams p) {
 
 // --------------------------------------------------------------- backward --
 // The gradients of a pair of values: g of the state, a its decay, h the state before.  On
-// return g holds a g, what goes on to the row before.  Exponentials stop at 2^120, so that
-// 1 - sigmoid(v) = exp(-v) sigmoid(v) keeps its digits on both sides.
+// return g holds a g, what goes on to the row before.  1 - sigmoid(v) = exp(-v) sigmoid(v) keeps its
+// digits on both sides; in that product an infinite exponential, whose sigmoid is 0, becomes a finite
+// one (2^115: times 4096 still is).  The sigmoids take the exponentials as they are, so that a
+// gate that is no number makes gradients that are none, and one far out the forward's decay.
 __device__ __forceinline__ pair at_most(pair v, float top) {
   return pr(fminf(un(v).x, top), fminf(un(v).y, top));
 }
 template <typename T>
 __device__ __forceinline__ void grads_of(pair x, pair r, pair i, pair A2, pair cr, pair ci, pair a, pair h,
                                          pair& g, pair& e, pair& dx, pair& dr, pair& di) {
-  const pair er = at_most(gate_exp<T>(r, cr), 0x1p120f), ei = at_most(gate_exp<T>(i, ci), 0x1p108f);
+  const pair er = gate_exp<T>(r, cr), ei = gate_exp<T>(i, ci);
   const pair R = rcp_of(padd(er, pr(1.f)));
   const pair I = rcp_of(pfma(ei, pr(4096.f), pr(4096.f)));  // by 2^-12, as m is by 2^12
   const pair L2 = pmul(A2, R);
   const pair m2 = scaled_m2(L2, a), rsm = rsqrt_of(m2);     // 2^-12 / m
   dx = pmul(pmul(g, pmul(m2, rsm)), I);
-  di = pmul(pmul(dx, x), pmul(pmul(ei, pr(4096.f)), I));
+  di = pmul(pmul(dx, x), pmul(pmul(at_most(ei, 0x1p115f), pr(4096.f)), I));
   g = pmul(g, a);
   // g L2 and L2 / m before what could leave the range for an infinite rate
   const pair in = pmul(pmul(a, pmul(pmul(L2, rsm), I)), x);  // by 2^-24
   e = pfma(pmul(g, in), pr(-kLn2 * 0x1p24f), pmul(pmul(pmul(g, L2), h), pr(kLn2)));
-  dr = pmul(e, pmul(er, R));
+  dr = pmul(e, pmul(at_most(er, FLT_MAX), R));
 }
 // Of two rows; g: of each one's state.
 template <typename T, int V>
