@@ -213,7 +213,7 @@ KDA_API kda_status kda_linrec_bwd_get_workspace_size(const kda_linrec_problem* p
  * final_state may be initial_state itself.  chunk_states: NULL, or the buffer of saved
  * states (16-byte aligned), written.  workspace: may be NULL for prompts of up to 8 tokens
  * without cu_seqlens and chunk_states.  After KDA_ERR_DEVICE_TIMEOUT in its status word
- * what the call wrote is not to be used. */
+ * what the call wrote is not to be used: what waited in vain for the rows before it is NaN. */
 KDA_API kda_status kda_linrec_fwd(const kda_linrec_problem* p, void* out, void* final_state,
                                   void* chunk_states, size_t chunk_states_bytes, void* workspace,
                                   size_t workspace_bytes, cudaStream_t stream);
