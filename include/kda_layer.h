@@ -258,7 +258,9 @@ typedef struct {
  * is kept has 9 bits of fraction and magnitudes up to 2^32 (a greater one becomes NaN); its
  * encoding is the library's own.
  * workspace: NULL, or KDA_STATUS_BYTES (128-byte aligned) whose first word receives the
- * status; after KDA_ERR_DEVICE_TIMEOUT what the call wrote is not to be used. */
+ * status; after KDA_ERR_DEVICE_TIMEOUT what the call wrote is not to be used.  Without a
+ * workspace a wait that ran out shows in the results alone: those of the products that it cut
+ * short are NaN, in out and in pre. */
 KDA_API kda_status kda_glu_fwd(const kda_glu_problem* p, void* out, void* pre, void* workspace,
                                size_t workspace_bytes, cudaStream_t stream);
 

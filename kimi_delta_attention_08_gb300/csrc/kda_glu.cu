@@ -69,6 +69,8 @@ struct GluParams {
   int32_t keep;            // whether g and u are outputs too
   int32_t ahead;           // whether the weights' gradients may start before dx ends
   const bf16* dout;
+  bf16* out;               // the forward's results again, for a wait that runs out
+  uint16_t* pre;
   unsigned* status;
 };
 
@@ -99,10 +101,11 @@ __device__ __forceinline__ float act_of(float g, int fn, float& slope) {
 // again leaves 2.3e-3; these leave 2.4e-3.  Magnitudes up to 2^32; beyond that, and what is
 // not finite, becomes NaN, and below 2^-30 the fraction shortens.  The fp32 value times 2^-96
 // has its exponent in 6 bits, so what is kept is a part of its bits, rounded to even.
+constexpr uint32_t kKeptNan = 0x7E01u;
 __device__ __forceinline__ uint32_t keep_bits(float v) {
   const uint32_t b = __float_as_uint(v * 0x1p-96f), m = b & 0x7FFFFFFFu;
   const uint32_t r = (m + 0x1FFFu + (m >> 14 & 1u)) >> 14;
-  return (b >> 16 & 0x8000u) | (r < 0x7E00u ? r : 0x7E01u);
+  return (b >> 16 & 0x8000u) | (r < 0x7E00u ? r : kKeptNan);
 }
 __device__ __forceinline__ float kept_value(uint32_t k) {
   const uint32_t m = k & 0x7FFFu;
@@ -398,6 +401,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
     const uint64_t t0 = ptx::global_timer_ns();
     while (ptx::global_timer_ns() - t0 < 2000000) {
     }
+    if constexpr (PASS == kForward) {  // and, as the caller may read no status, this CTA's results become NaN
+      const int64_t width = WIDE ? p.width : kHalf;
+      for (int t = first; t < total; t += step) {
+        int m, n;
+        tile_of(p, t, m, n);
+        const int64_t row0 = (int64_t)m * kTileM + rank * kHalf, col0 = n * width;
+        for (int64_t e = threadIdx.x; e < kHalf * width; e += blockDim.x) {
+          const int64_t row = row0 + e / width, col = col0 + e % width;
+          if (row >= p.M || col >= p.N) continue;
+          p.out[row * p.N + col] = __float2bfloat16_rn(__uint_as_float(0x7FFFFFFFu));
+          if (p.keep) p.pre[row * 2 * p.N + col] = p.pre[(row * 2 + 1) * p.N + col] = (uint16_t)kKeptNan;
+        }
+      }
+    }
   }
   ptx::tc_fence_before();
   ptx::cluster_sync();
@@ -504,12 +521,14 @@ __global__ void __launch_bounds__(256, 2) glu_step_kernel(const __grid_constant_
   ptx::tc_fence_after();
   if (warp >= 4) {
     const int f = (warp - 4) * 32 + lane;
+    const bool bad = failed;  // no number then, as the caller may read no status
     for (int c = 0; c < p.cols; c += 16) {
       uint32_t v[16];
       ptx::tmem_ld16(tmem + ((uint32_t)((warp - 4) * 32) << 16) + c, v);
       ptx::tmem_wait_ld();
 #pragma unroll
-      for (int k = 0; k < 16; ++k) sums[(c + k) * kStepPitch + f] = first < last ? __uint_as_float(v[k]) : 0.f;
+      for (int k = 0; k < 16; ++k)
+        sums[(c + k) * kStepPitch + f] = __uint_as_float(bad ? 0x7FFFFFFFu : first < last ? v[k] : 0u);
     }
   }
   ptx::tc_fence_before();
@@ -685,6 +704,7 @@ cudaError_t launch_dual(const kda_glu_problem* q, bf16* o0, bf16* o1, uint16_t* 
   p.m_tiles = (int32_t)down, p.n_tiles = (int32_t)up(q->hidden, p.width);
   p.fn = q->fn, p.stall = q->debug_stall, p.status = status;
   p.keep = pre != nullptr, p.dout = static_cast<const bf16*>(dout);
+  p.out = o0, p.pre = pre;
   if (wide) return launch<PASS, true>(p, {(int64_t)p.m_tiles * p.n_tiles, 1, 0}, nullptr, nullptr, stream);
   return launch<PASS>(p, {(int64_t)p.m_tiles * p.n_tiles, 1, 0}, nullptr, nullptr, stream);
 }

@@ -613,8 +613,8 @@ def kda_glu_fwd(x, w_gate, w_up, out, workspace=None, *, pre=None, activation="s
     multiple of 8 (both may be parts of one matrix); out: [B, T, F] bf16, written; activation:
     "silu", "sigmoid" or "gelu" (the tanh form).  pre: None, or [B, T, 2 F] of x's dtype, a buffer
     that receives both projections for kda_glu_bwd (16 bits each, in the library's own
-    encoding).  workspace: uint8, 256 bytes or more, whose
-    first word receives the status, or None."""
+    encoding).  workspace: uint8, 256 bytes or more, whose first word receives the status, or
+    None: a wait that ran out then shows as NaN in the results alone."""
     q, F = _glu_problem(x, w_gate, w_up, activation, debug_stall)
     B, T, dev = x.shape[0], x.shape[1], x.device
     op = _need(out, "out", x.dtype, dev, (B, T, F))

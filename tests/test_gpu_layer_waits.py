@@ -1,8 +1,10 @@
 """What a wait that ran out leaves where nobody reads a status word: no number, not a plausible
-value.  (The test's hook makes the wait run out: a result that is never handed on.)"""
+value.  (The test's hook makes the wait run out: a result that is never handed on, tiles that are
+never loaded.)"""
 import pytest
 import torch
 
+from tests import test_gpu_glu as G
 from tests import test_gpu_linrec as L
 
 pytestmark = pytest.mark.gpu
@@ -31,3 +33,23 @@ def test_recurrence(kda_lib, T, ty, dim):
     kda.kda_linrec_fwd(**a, out=want, **b)
     kda.kda_linrec_fwd(**a, out=got, **b)
     assert want.isfinite().all() and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("size", [(5, 1024, 256), (128, 256, 128), (300, 128, 256), (200, 1000, 9800), (1100, 264, 4104)])
+@pytest.mark.parametrize("keep", [False, True])
+def test_feed_forward(kda_lib, size, keep):
+    """Few rows, tiles of both widths, more tiles than pairs."""
+    import kimi_delta_attention_08_gb300 as kda
+    from tests.glu_ref import glu, kept_values, within
+    x, wg, wu, dout = G.make(*size)
+    out = torch.zeros_like(dout)
+    pre = torch.zeros(1, size[0], 2 * size[2], dtype=BF, device="cuda") if keep else None
+    kda.kda_glu_fwd(x, wg, wu, out, pre=pre, debug_stall=True)
+    assert out.isnan().all()
+    if keep:
+        assert kept_values(pre).isnan().all()
+    kda.kda_glu_fwd(x, wg, wu, out, pre=pre)
+    ref = glu(x, wg, wu, "silu")
+    within(out, ref["out"], "out")
+    if keep:
+        within(pre, ref["pre"], "pre")
