@@ -76,7 +76,9 @@ struct GluParams {
 
 constexpr float kGelu = 1.5957691216057308f, kGeluCube = 0.044715f;  // sqrt(8 / pi)
 
-// f(g) and f'(g).  gelu is its tanh form, g sigmoid(sqrt(8 / pi) (g + 0.044715 g^3)).
+// f(g) and f'(g).  gelu is its tanh form, g sigmoid(sqrt(8 / pi) (g + 0.044715 g^3)).  Its slope takes
+// the square up to 2^96 only, from where on it meets a sigmoid of 0 or 1 and a slope of 0 in any
+// case: infinity times that 0 would be no number.
 __device__ __forceinline__ float act_of(float g, int fn) {
   if (fn == KDA_FN_GELU) return g * sigmoid<bf16>(kGelu * g * fmaf(kGeluCube * g, g, 1.f));
   const float s = sigmoid<bf16>(g);
@@ -84,7 +86,7 @@ __device__ __forceinline__ float act_of(float g, int fn) {
 }
 __device__ __forceinline__ float act_of(float g, int fn, float& slope) {
   if (fn == KDA_FN_GELU) {
-    const float c = kGeluCube * g * g;
+    const float c = fminf(kGeluCube * g * g, 0x1p96f);
     float t;
     const float s = sigmoid<bf16>(kGelu * g * (1.f + c), t);
     slope = fmaf(g * t, kGelu * fmaf(3.f, c, 1.f), s);

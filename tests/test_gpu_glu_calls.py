@@ -1,0 +1,37 @@
+"""Calls of the gated feed-forward product at the ends of their range."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+NAMES = ("dx", "dw_gate", "dw_up")
+
+
+@pytest.mark.parametrize("rows", [5, 300])
+@pytest.mark.parametrize("fn", ["silu", "gelu", "sigmoid"])
+def test_arguments_beyond_the_range_of_their_powers(kda_lib, rows, fn):
+    """Pre-activations of 2^66 and 2^120 of both signs, whose cubes (and squares) fp32 does not hold:
+    f is g or 0 (sigmoid: 1 or 0) and its slope 1 or 0 (0).  Powers of two, so that everything is exact."""
+    import kimi_delta_attention_08_gb300 as kda
+    w = torch.zeros(8, 8)
+    w[:, 0] = torch.tensor([2.0 ** 66, -2.0 ** 66, 2.0 ** 44, -2.0 ** 44, 2.0 ** 120, -2.0 ** 120, 2.0 ** 20, -2.0 ** 20])
+    x = torch.zeros(1, rows, 8)
+    x[..., 0], x[..., 1] = 1, 0.5
+    up = torch.zeros(8, 8)
+    up[:, 1] = 4                             # u = 2
+    dout = torch.full((1, rows, 8), 2.0 ** -60)
+    dev = lambda v: v.to(BF).cuda()          # noqa: E731
+    out = torch.empty(1, rows, 8, dtype=BF, device="cuda")
+    kda.kda_glu_fwd(dev(x), dev(w), dev(up), out, activation=fn)
+    g = w[:, 0].double()
+    f, df = (torch.where(g > 0, g, 0), (g > 0).double()) if fn != "sigmoid" else ((g > 0).double(), 0 * g)
+    assert torch.equal(out.cpu().double(), (2 * f).expand(1, rows, 8))
+    got = kda.kda_glu_bwd(dev(x), dev(w), dev(up), dev(dout), activation=fn)
+    dg, du = 2.0 ** -60 * 2 * df, 2.0 ** -60 * f
+    dx = torch.zeros(8, dtype=torch.float64)
+    dx[0], dx[1] = (dg * g).sum(), (du * 4).sum()
+    want = {"dx": dx.expand(1, rows, 8), "dw_gate": rows * torch.outer(dg, x[0, 0].double()),
+            "dw_up": rows * torch.outer(du, x[0, 0].double())}
+    for k in NAMES:  # dx's sums have other terms that a rounding to bf16 drops: half a step of it
+        assert ((got[k].cpu().double() - want[k]).abs() <= 2.0 ** -8 * want[k].abs()).all(), k
