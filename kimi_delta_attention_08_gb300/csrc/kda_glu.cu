@@ -68,6 +68,7 @@ struct GluParams {
   int32_t fn, stall;
   int32_t keep;            // whether g and u are outputs too
   int32_t ahead;           // whether the weights' gradients may start before dx ends
+  unsigned* ready;         // set by dx when dg and du are there
   const bf16* dout;
   bf16* out;               // the forward's results again, for a wait that runs out
   uint16_t* pre;
@@ -173,8 +174,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (kEpilogueWarp 
   const uint32_t tmem = tmem_at;
   // The backward's launches are in their places before the one ahead ends: dx waits for dg and du, and
   // the weights' gradients, which do not need dx, for dx, before their first tile or (`ahead`) their end.
+  // What a launch wrote is promised to those that wait for it, so `ahead` takes dg and du from dx, which
+  // did: dx says so by a word that it releases before it lets the next launch start, and the threads that
+  // load acquire it; where it is not there they wait for the whole of dx.
   if (PASS == kInput || (PASS == kWeights && !p.ahead)) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (PASS == kInput) {
+    if (blockIdx.x == 0) {
+      if (threadIdx.x == 0) ptx::st_release(p.ready, 1u);
+      __syncthreads();
+    }
+  }
   if constexpr (PASS == kInput || PASS == kRecompute) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (PASS == kWeights) {
+    if (p.ahead && warp == 0 && lane == 0) {
+      if (ptx::ld_acquire(p.ready) == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+      ptx::fence_proxy_async_all();  // the loads are the asynchronous proxy's
+    }
+  }
 
   if (warp == 0 && lane == 0) {
     // loads: this CTA's half of both operands
@@ -812,7 +828,7 @@ kda_status kda_glu_bwd(const kda_glu_problem* problem, const void* dout, const v
     }
   }
   GluParams p = {};
-  p.stall = q.debug_stall, p.status = status;
+  p.stall = q.debug_stall, p.status = status, p.ready = status + 1;
   // dx: both projections' products in one sum
   if (e == cudaSuccess) e = map_of(&p.a[0], dg, M, F, F, kHalf);
   if (e == cudaSuccess) e = map_of(&p.a[1], du, M, F, F, kHalf);

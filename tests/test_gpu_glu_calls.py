@@ -1,6 +1,10 @@
-"""Calls of the gated feed-forward product at the ends of their range."""
+"""Calls of the gated feed-forward product: arguments at the ends of their range, workspaces that held
+another call's values."""
 import pytest
 import torch
+
+from tests.glu_ref import glu, within
+from tests.test_gpu_glu import make
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +39,30 @@ def test_arguments_beyond_the_range_of_their_powers(kda_lib, rows, fn):
             "dw_up": rows * torch.outer(du, x[0, 0].double())}
     for k in NAMES:  # dx's sums have other terms that a rounding to bf16 drops: half a step of it
         assert ((got[k].cpu().double() - want[k]).abs() <= 2.0 ** -8 * want[k].abs()).all(), k
+
+
+@pytest.mark.parametrize("size", [(97, 136, 6160), (300, 264, 2056), (513, 64, 2056), (1100, 264, 1032)])
+@pytest.mark.parametrize("kept", [False, True])
+def test_calls_in_turn_in_one_workspace(kda_lib, size, kept):
+    """Sizes at which the weights' gradients start before dx ends: of calls in turn, each reads its own
+    gradients of g and u, not those that the call before left in the workspace."""
+    import kimi_delta_attention_08_gb300 as kda
+    ws = kda.make_glu_bwd_workspace(size[0], size[2])
+    sets, want = [make(*size, seed=k) for k in (1, 2)], []
+    pres = [None, None]
+    if kept:
+        pres = [torch.empty(1, size[0], 2 * size[2], dtype=BF, device="cuda") for _ in sets]
+        for (x, wg, wu, dout), pre in zip(sets, pres):
+            kda.kda_glu_fwd(x, wg, wu, torch.empty_like(dout), pre=pre)
+    for (x, wg, wu, dout), pre in zip(sets, pres):
+        g = kda.kda_glu_bwd(x, wg, wu, dout, pre=pre)  # in memory of its own
+        ref = glu(x, wg, wu, "silu", dout, pre)
+        for k in NAMES:
+            within(g[k], ref[k], k)
+        want.append(g)
+    torch.cuda.synchronize()
+    got = [kda.kda_glu_bwd(*sets[n % 2], ws, pre=pres[n % 2]) for n in range(40)]
+    for n, g in enumerate(got):
+        for k in NAMES:
+            assert torch.equal(g[k], want[n % 2][k]), (n, k)
+    assert kda.kda_get_device_status(ws) == 0
