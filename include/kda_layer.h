@@ -256,7 +256,7 @@ typedef struct {
 /* kda_glu_fwd -- out [rows, hidden], written, and (unless NULL) pre [rows, 2 hidden], 16 bits
  * each: g, then u of each row, for kda_glu_bwd, which then does not compute them again.  What
  * is kept has 9 bits of fraction and magnitudes up to 2^32 (a greater one becomes NaN); its
- * encoding is the library's own.
+ * encoding is the library's own, neither bf16 nor fp16: only kda_glu_bwd may read it.
  * workspace: NULL, or KDA_STATUS_BYTES (128-byte aligned) whose first word receives the
  * status; after KDA_ERR_DEVICE_TIMEOUT what the call wrote is not to be used.  Without a
  * workspace a wait that ran out shows in the results alone: those of the products that it cut

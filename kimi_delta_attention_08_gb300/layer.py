@@ -580,6 +580,15 @@ def kda_linrec_bwd(x, r, i, A_log, dout, z=None, r_bias=None, i_bias=None, initi
 
 
 # ----------------------------------------------- gated feed-forward product --
+def _pre(pre, dev, shape):
+    """The pointer of kept pre-activations.  Their 16 bits are no type of torch's: int16 is refused by,
+    or plainly wrong in, whatever would take them for numbers; bfloat16 is accepted as a buffer of
+    the same size."""
+    if pre is not None and _tensor(pre, "pre").dtype == torch.int16:
+        return _need(pre, "pre", torch.int16, dev, shape)
+    return _opt(pre, "pre", torch.bfloat16, dev, shape)
+
+
 def _glu_problem(x, w_gate, w_up, activation, debug_stall):
     """The C problem of a call, and the hidden width."""
     try:
@@ -611,14 +620,15 @@ def kda_glu_fwd(x, w_gate, w_up, out, workspace=None, *, pre=None, activation="s
 
     x: rows [B, T, D] bf16, D and the rows' stride multiples of 8; w_gate, w_up: [F, D] bf16, F a
     multiple of 8 (both may be parts of one matrix); out: [B, T, F] bf16, written; activation:
-    "silu", "sigmoid" or "gelu" (the tanh form).  pre: None, or [B, T, 2 F] of x's dtype, a buffer
-    that receives both projections for kda_glu_bwd (16 bits each, in the library's own
-    encoding).  workspace: uint8, 256 bytes or more, whose first word receives the status, or
+    "silu", "sigmoid" or "gelu" (the tanh form).  pre: None, or [B, T, 2 F] int16, a buffer that
+    receives both projections for kda_glu_bwd, 16 bits each in the library's own encoding; a
+    bfloat16 buffer is taken too, but what it then holds is no bfloat16: nothing but
+    kda_glu_bwd may read or convert it.  workspace: uint8, 256 bytes or more, whose first word receives the status, or
     None: a wait that ran out then shows as NaN in the results alone."""
     q, F = _glu_problem(x, w_gate, w_up, activation, debug_stall)
     B, T, dev = x.shape[0], x.shape[1], x.device
     op = _need(out, "out", x.dtype, dev, (B, T, F))
-    pp = _opt(pre, "pre", x.dtype, dev, (B, T, 2 * F))
+    pp = _pre(pre, dev, (B, T, 2 * F))
     wp, wb = (None, 0) if workspace is None else _workspace(workspace, None, dev, stream)[1:]
     _call("kda_glu_fwd", dev, stream, ctypes.byref(q), op, pp, wp, wb)
 
@@ -632,13 +642,13 @@ def make_glu_bwd_workspace(rows, hidden, device=None):
 def kda_glu_bwd(x, w_gate, w_up, dout, workspace=None, *, pre=None, activation="silu", stream=None,
                 debug_stall=False):
     """Enqueue the backward of kda_glu_fwd (include/kda_layer.h, kda_glu_bwd).  dout: [B, T, F]
-    bf16.  pre: what the forward kept; without it both projections are computed again.
+    bf16.  pre: the buffer that the forward filled, bit for bit; without it both projections are computed again.
     Returns a dict: dx [B, T, D], dw_gate, dw_up [F, D] in bf16, and the workspace."""
     q, F = _glu_problem(x, w_gate, w_up, activation, debug_stall)
     B, T, D = x.shape
     dev, ty = x.device, x.dtype
     dop = _need(dout, "dout", ty, dev, (B, T, F))
-    pp = _opt(pre, "pre", ty, dev, (B, T, 2 * F))
+    pp = _pre(pre, dev, (B, T, 2 * F))
     with _pool(stream, dev):
         ws, wp, wb = _workspace(workspace, lambda: _size("kda_glu_bwd_get_workspace_size", B * T, F), dev,
                                 stream)

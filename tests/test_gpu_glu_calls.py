@@ -1,9 +1,9 @@
 """Calls of the gated feed-forward product: arguments at the ends of their range, workspaces that held
-another call's values."""
+another call's values, kept pre-activations as integers."""
 import pytest
 import torch
 
-from tests.glu_ref import glu, within
+from tests.glu_ref import glu, kept_values, within
 from tests.test_gpu_glu import make
 
 pytestmark = pytest.mark.gpu
@@ -66,3 +66,20 @@ def test_calls_in_turn_in_one_workspace(kda_lib, size, kept):
         for k in NAMES:
             assert torch.equal(g[k], want[n % 2][k]), (n, k)
     assert kda.kda_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("size", [(5, 72, 136), (300, 264, 2056)])
+def test_kept_values_as_integers(kda_lib, size):
+    """The buffer of kept pre-activations as int16, which no operation takes for numbers: the same bits."""
+    import kimi_delta_attention_08_gb300 as kda
+    x, wg, wu, dout = make(*size)
+    out, shape = torch.empty_like(dout), (1, size[0], 2 * size[2])
+    pre, same = torch.empty(shape, dtype=torch.int16, device="cuda"), torch.empty(shape, dtype=BF, device="cuda")
+    kda.kda_glu_fwd(x, wg, wu, out, pre=pre)
+    kda.kda_glu_fwd(x, wg, wu, out, pre=same)
+    assert torch.equal(pre, same.view(torch.int16))
+    within(pre, glu(x, wg, wu, "silu")["pre"], "pre")
+    a, b = (kda.kda_glu_bwd(x, wg, wu, dout, pre=p) for p in (pre, same))
+    for k in NAMES:
+        assert torch.equal(a[k], b[k]), k
+    assert kept_values(pre).isfinite().all()
