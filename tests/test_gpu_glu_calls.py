@@ -1,10 +1,13 @@
 """Calls of the gated feed-forward product: arguments at the ends of their range, workspaces that held
-another call's values, kept pre-activations as integers."""
+another call's values, kept pre-activations as integers, no writes beyond the results."""
+import ctypes
+
 import pytest
 import torch
 
 from tests.glu_ref import glu, kept_values, within
 from tests.test_gpu_glu import make
+from tests.test_gpu_linrec_batches import guarded
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +86,27 @@ def test_kept_values_as_integers(kda_lib, size):
     for k in NAMES:
         assert torch.equal(a[k], b[k]), k
     assert kept_values(pre).isfinite().all()
+
+
+@pytest.mark.parametrize("size", [(5, 72, 136), (130, 136, 264), (200, 1000, 9800), (300, 264, 2056)])
+def test_nothing_beyond_the_results_is_written(kda_lib, size):
+    """Few rows, tiles of both widths, split tiles; forward, and backward through the C entry point."""
+    import kimi_delta_attention_08_gb300 as kda
+    from kimi_delta_attention_08_gb300 import layer
+    M, D, Fh = size
+    x, wg, wu, dout = make(*size)
+    (out, ok0), (pre, ok1) = guarded((1, M, Fh), BF), guarded((1, M, 2 * Fh), BF)
+    kda.kda_glu_fwd(x, wg, wu, out)
+    within(out, glu(x, wg, wu, "silu")["out"], "out")
+    kda.kda_glu_fwd(x, wg, wu, out, pre=pre)
+    assert ok0() and ok1()
+    q, _ = layer._glu_problem(x, wg, wu, "silu", False)
+    ws = kda.make_glu_bwd_workspace(M, Fh)
+    for kept in (None, pre):
+        grads = [guarded((1, M, D), BF), guarded((Fh, D), BF), guarded((Fh, D), BF)]
+        layer._call("kda_glu_bwd", x.device, None, ctypes.byref(q), dout.data_ptr(),
+                    None if kept is None else kept.data_ptr(), *[v.data_ptr() for v, _ in grads],
+                    ws.data_ptr(), ws.numel())
+        want = kda.kda_glu_bwd(x, wg, wu, dout, pre=kept)
+        for nm, (v, ok) in zip(NAMES, grads):
+            assert ok() and torch.equal(v, want[nm]), nm
