@@ -9,7 +9,8 @@
 // L / m, not 1 / m, is what e needs: it goes to zero with L where 1 / m has no bound.
 //
 // Each row is read once and written once.  A block takes a tile of 128 rows (backward: 64) by
-// 64 channels; its warps take consecutive runs of 16 (8) rows, a lane two channels.  A run is
+// 64 channels; its warps take consecutive runs of 16 (8) rows, a lane two channels (fp32 rows, and
+// bf16 ones off 4 bytes: 32 channels, a lane one).  A run is
 // scanned in registers from zero along with the product of its decays; runs, tiles and
 // groups of tiles are joined as affine steps, in shared memory and through the workspace;
 // then each run is walked again from the state before it.  So a prompt of any length fills
@@ -164,9 +165,8 @@ struct Gates {
 // that no other thread touches, so that nothing but its own copies is waited for.
 template <int BYTES>
 __device__ __forceinline__ void copy_own(uint32_t slot, const void* p, bool there) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot), "l"(p), "r"(there ? 16 : 0) : "memory");
-  else if constexpr (BYTES == 8)
+  static_assert(BYTES == 2 || BYTES == 4 || BYTES == 8, "one or two channels");
+  if constexpr (BYTES == 8)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(slot), "l"(p), "r"(there ? 8 : 0) : "memory");
   else if constexpr (BYTES == 4)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(slot), "l"(p), "r"(there ? 4 : 0) : "memory");
@@ -198,12 +198,9 @@ struct Slots {
   static __device__ __forceinline__ Vals<V> get(const uint8_t* at, int j) {
     Raw<T, V> r;
     const uint8_t* const q = at + j * kRow;
+    static_assert(kBytes == 2 || kBytes == 4, "one channel, or two of bf16");
     if constexpr (kBytes == 2) r.w[0] = (uint32_t)*reinterpret_cast<const unsigned short*>(q);
-    else if constexpr (kBytes == 4) r.w[0] = *reinterpret_cast<const uint32_t*>(q);
-    else {
-      const uint2 v = *reinterpret_cast<const uint2*>(q);
-      r.w[0] = v.x, r.w[1] = v.y;
-    }
+    else r.w[0] = *reinterpret_cast<const uint32_t*>(q);
     float f[V];
     if constexpr (V == 1 && sizeof(T) == 4) f[0] = __uint_as_float(r.w[0]);
     else unpack(r, f);
@@ -537,11 +534,11 @@ struct Join {
     }
   }
   // The runs are there: together they are published; the part's tiles are composed.
-  __device__ __forceinline__ void parts(Runs<V>& sh, float& P, float& H, float& Pt, float& Ht) {
+  __device__ __forceinline__ void parts(Runs<V>& sh, float& Pt, float& Ht) {
     Pt = 1.f, Ht = 0.f;      // of the tiles
     if (part == kParts - 1 && ok) {
       const uint64_t cuts = *reinterpret_cast<const uint64_t*>(sh.cut);
-      P = 1.f, H = 0.f;
+      float P = 1.f, H = 0.f;
 #pragma unroll
       for (int q = 0; q < kWarps; ++q) {
         const int r = FORWARD ? q : kWarps - 1 - q;
@@ -738,8 +735,8 @@ __global__ void __launch_bounds__(32 * kWarps, kFwdBlocks<V>)
     __syncthreads();
     const Unit next = sh.unit[(turn + 1) & 1];
     copy(next);
-    float Pj, Hj, Pt, Ht;
-    join.parts(sh.runs, Pj, Hj, Pt, Ht);
+    float Pt, Ht;
+    join.parts(sh.runs, Pt, Ht);
     __syncthreads();
     if (join.part == 0 && join.ok) {
       const float X = join.finish(sh.runs, edge, Pt, Ht);
@@ -1035,8 +1032,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) linrec_bwd_kernel(const __grid
     const int64_t edge = p.tiles - 1 - (rows.eos - 1) / kTileB;
     Join<V, false> join(p, s, edge, (rows.live[1] >> 31) && !(rows.last[1] >> 31) && s > 0, c0);
     __syncthreads();
-    float Pj, Hj, Pt, Ht;
-    join.parts(sh.runs, Pj, Hj, Pt, Ht);
+    float Pt, Ht;
+    join.parts(sh.runs, Pt, Ht);
     __syncthreads();
     if (join.part == 0) {
       if (join.ok) join.finish(sh.runs, edge, Pt, Ht);

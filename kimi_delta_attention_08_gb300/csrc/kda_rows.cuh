@@ -349,7 +349,7 @@ __device__ __forceinline__ int find_sequence(const int64_t* cu, int N, int64_t t
   return lo;
 }
 
-// Writes the status word of a workspace from a full check of cu_seqlens: one warp.
+// Whether cu_seqlens is inconsistent at a thread's entries, first, first + step, ...: not
 // cu[0] = 0, non-decreasing, cu[N] <= total.
 __device__ __forceinline__ bool bad_seqlens(const int64_t* cu, int N, int64_t total, int first, int step) {
   bool bad = false;
@@ -359,6 +359,7 @@ __device__ __forceinline__ bool bad_seqlens(const int64_t* cu, int N, int64_t to
   }
   return bad;
 }
+// Writes the status word of a workspace from a full check of cu_seqlens: one warp.
 __device__ __forceinline__ void check_seqlens(const int64_t* cu, int N, int64_t total,
                                               unsigned* status, unsigned bad_bit) {
   const bool bad = __any_sync(0xffffffffu, bad_seqlens(cu, N, total, threadIdx.x & 31, 32));
