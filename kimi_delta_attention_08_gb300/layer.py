@@ -580,13 +580,16 @@ def kda_linrec_bwd(x, r, i, A_log, dout, z=None, r_bias=None, i_bias=None, initi
 
 
 # ----------------------------------------------- gated feed-forward product --
-def _pre(pre, dev, shape):
+def _pre(pre, dev, stream, shape):
     """The pointer of kept pre-activations.  Their 16 bits are no type of torch's: int16 is refused by,
     or plainly wrong in, whatever would take them for numbers; bfloat16 is accepted as a buffer of
     the same size."""
-    if pre is not None and _tensor(pre, "pre").dtype == torch.int16:
-        return _need(pre, "pre", torch.int16, dev, shape)
-    return _opt(pre, "pre", torch.bfloat16, dev, shape)
+    if pre is None:
+        return None
+    ty = torch.int16 if _tensor(pre, "pre").dtype == torch.int16 else torch.bfloat16
+    at = _need(pre, "pre", ty, dev, shape)
+    _in_use(pre, stream)
+    return at
 
 
 def _glu_problem(x, w_gate, w_up, activation, debug_stall):
@@ -628,7 +631,7 @@ def kda_glu_fwd(x, w_gate, w_up, out, workspace=None, *, pre=None, activation="s
     q, F = _glu_problem(x, w_gate, w_up, activation, debug_stall)
     B, T, dev = x.shape[0], x.shape[1], x.device
     op = _need(out, "out", x.dtype, dev, (B, T, F))
-    pp = _pre(pre, dev, (B, T, 2 * F))
+    pp = _pre(pre, dev, stream, (B, T, 2 * F))
     wp, wb = (None, 0) if workspace is None else _workspace(workspace, None, dev, stream)[1:]
     _call("kda_glu_fwd", dev, stream, ctypes.byref(q), op, pp, wp, wb)
 
@@ -648,7 +651,7 @@ def kda_glu_bwd(x, w_gate, w_up, dout, workspace=None, *, pre=None, activation="
     B, T, D = x.shape
     dev, ty = x.device, x.dtype
     dop = _need(dout, "dout", ty, dev, (B, T, F))
-    pp = _pre(pre, dev, (B, T, 2 * F))
+    pp = _pre(pre, dev, stream, (B, T, 2 * F))
     with _pool(stream, dev):
         ws, wp, wb = _workspace(workspace, lambda: _size("kda_glu_bwd_get_workspace_size", B * T, F), dev,
                                 stream)
