@@ -22,10 +22,10 @@
 // Where tiles of 128 columns would take a second turn and wider ones do not, they are 160 or 192 wide;
 // the backward splits the sums of its last turn's tiles over the pairs left.
 //
-// 4,096 by 12,288: 32,768 rows forward 3.83 ms (1.72 PFLOP/s), 4,096 rows 468 us (1.76), 256 rows
-// 44 us, 64 wide tiles on 76 pairs (4.6 TB/s of weights).  16,384 rows forward with kept
-// pre-activations and backward 6.24 ms (1.58), backward that computes them again 6.17 ms
-// (1.60).  The tensor pipe is active in 79 to 82 % of the cycles; operands arrive at 12 to 13
+// 4,096 by 12,288: 32,768 rows forward 3.83 to 4.04 ms (1.63 to 1.72 PFLOP/s; the longer runs meet the
+// power limit), 4,096 rows 468 us (1.76), 256 rows 44 us, 64 wide tiles on 76 pairs (4.6 TB/s of
+// weights).  16,384 rows forward with kept pre-activations and backward 6.24 to 6.66 ms (1.49 to 1.58),
+// backward that computes them again 6.17 to 6.36 ms (1.56 to 1.60).  The tensor pipe is active in 79 to 82 % of the cycles; operands arrive at 12 to 13
 // TB/s from L2, which half the products would still need 2.9 ms for at 32,768 rows.
 // One row 35 us, 32 rows 36.5 (5.8 TB/s of weights).
 #include <algorithm>

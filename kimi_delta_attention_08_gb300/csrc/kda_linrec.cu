@@ -25,11 +25,15 @@
 // Device time: forward, 8 x 4,096 tokens of 4,096 channels, bf16, 257 us (4.2 TB/s of rows; fp32
 // 342, 6.3 TB/s); 74,080 packed tokens of 2,048 channels with a gate 431; 65,536 + 5 x 1,024
 // tokens of 1,024 channels 201; forward and backward of 4 x 4,096 tokens of 4,096 channels with a
-// gate 559.  Bound by the issue of instructions (41 a value forward, 124 backward, 0.5 a clock
-// and scheduler with 16 warps per SM, which the registers of decays and inputs allow) and, where
-// few channels leave many tiles of one at work, by waits: 154 us for the long prompt without
-// them.  Runs of 8 rows by four channels take 262, 502 and 261 us for the three
-// forwards, decays and inputs in shared memory with three blocks per SM 287, 450 and 266.
+// gate 556.  Bound by latency: no unit is near its peak (of 2 x 4,096 tokens, forward and
+// backward: 0.52 and 0.50 instructions a clock and scheduler, which could issue one, FMA pipe 21 %,
+// special-function unit 25 and 24 %, DRAM 42 and 28 %).  Decays and inputs in registers leave 16 warps
+// per SM, too few to cover the three barriers at which a tile's runs meet: more warps wait
+// there (1.8 and 1.6 for each instruction that issues) than for anything else.  Where few channels
+// leave many tiles of one at work they also wait for each other: 154 us for the long prompt
+// without that.  41 instructions a value forward, 124 backward.  Runs of 8 rows by four channels
+// take 262, 502 and 261 us for the three forwards, decays and inputs in shared memory with three
+// blocks per SM 287, 450 and 266.
 #include <algorithm>
 #include <type_traits>
 
